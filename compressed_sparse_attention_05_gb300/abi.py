@@ -46,6 +46,15 @@ class Window(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("pos0", C.c_void_p)]
 
 
+class Bounded(C.Structure):
+    _fields_ = [("entry_pos", C.c_void_p), ("weight", C.c_void_p), ("shift", C.c_void_p)]
+
+
+class ScoreMods(C.Structure):
+    _fields_ = [("logit_cap", C.c_float), ("slopes", C.c_void_p), ("doc_start", C.c_void_p),
+                ("prefix_len", C.c_void_p)]
+
+
 class LayerArgs(C.Structure):
     _fields_ = [
         ("mode", C.c_int32), ("hierarchical", C.c_int32), ("dims", Dims), ("cache", Cache),
@@ -96,6 +105,17 @@ SIGNATURES = {
                                           _I32, _P]),
     "csa2_sparse_attn": (C.c_int, [C.POINTER(Dims), C.POINTER(Cache), C.POINTER(Window), _P, _P, _P, _P,
                                    _F, _P, _P, _P]),
+    "csa2_dense_attn_workspace_size": (_SZ, [C.POINTER(Dims), _I32]),
+    "csa2_dense_attn": (C.c_int, [C.POINTER(Dims), C.POINTER(Cache), C.POINTER(Bounded), C.POINTER(Window),
+                                  C.POINTER(ScoreMods), _P, _P, _F, _I32, _P, _P, _P, _SZ, _P]),
+    "csa2_entry_weights_workspace_size": (_SZ, [C.POINTER(Dims), _I32]),
+    "csa2_entry_weights": (C.c_int, [C.POINTER(Dims), C.POINTER(Cache), C.POINTER(Bounded), C.POINTER(ScoreMods),
+                                     _P, _P, _P, _F, _F, _P, _P, _I32, _P, _SZ, _P]),
+    "csa2_evict_workspace_size": (_SZ, [C.POINTER(Dims), _I32]),
+    "csa2_evict": (C.c_int, [C.POINTER(Dims), C.POINTER(Cache), C.POINTER(Bounded), _P, _I32, _I32, _I32, _I32,
+                             _P, _SZ, _P]),
+    "csa2_compress_pack_bounded": (C.c_int, [_P, _I32, _I32, _I32, _P, _P, _F, _F, _P, _P, C.POINTER(Dims),
+                                             C.POINTER(Cache), C.POINTER(Bounded), _P, _SZ, _P]),
     "csa2_layer_workspace_size": (_SZ, [C.POINTER(LayerArgs)]),
     "csa2_layer": (C.c_int, [C.POINTER(LayerArgs), _P, _SZ, _P]),
 }
@@ -285,6 +305,60 @@ def csa2_sparse_attn(dims: Dims, cache: Cache, window: Window, Q, q_pos, idx, cn
                      lse=None, stream=None):
     _check(lib().csa2_sparse_attn(C.byref(dims), C.byref(cache), C.byref(window), ptr(Q), ptr(q_pos),
                                   ptr(idx), ptr(cnt), softmax_scale, ptr(O), ptr(lse), stream_handle(stream)))
+
+
+def _ref(struct):
+    return C.byref(struct) if struct is not None else None
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size() if t is not None else 0
+
+
+def csa2_dense_attn_workspace_size(dims: Dims, max_entries: int) -> int:
+    return lib().csa2_dense_attn_workspace_size(C.byref(dims), max_entries)
+
+
+def csa2_dense_attn(dims: Dims, cache: Cache, window: Optional[Window], Q, q_pos, softmax_scale, max_entries, O,
+                    lse=None, ws=None, mods: Optional[ScoreMods] = None, bounded: Optional[Bounded] = None,
+                    stream=None):
+    """Attention over every visible entry of the cache and the window; O [B][Tq][Hq][d] bf16."""
+    _check(lib().csa2_dense_attn(C.byref(dims), C.byref(cache), _ref(bounded), _ref(window), _ref(mods), ptr(Q),
+                                 ptr(q_pos), softmax_scale, max_entries, ptr(O), ptr(lse), ptr(ws), _nbytes(ws),
+                                 stream_handle(stream)))
+
+
+def csa2_entry_weights_workspace_size(dims: Dims, max_entries: int) -> int:
+    return lib().csa2_entry_weights_workspace_size(C.byref(dims), max_entries)
+
+
+def csa2_entry_weights(dims: Dims, cache: Cache, Q, q_pos, lse, softmax_scale, decay, weight_in, weight_out,
+                       max_entries, ws=None, mods: Optional[ScoreMods] = None, bounded: Optional[Bounded] = None,
+                       stream=None):
+    """weight_out = decay * weight_in + the softmax weight of every entry, summed over tokens and heads."""
+    _check(lib().csa2_entry_weights(C.byref(dims), C.byref(cache), _ref(bounded), _ref(mods), ptr(Q), ptr(q_pos),
+                                    ptr(lse), softmax_scale, decay, ptr(weight_in), ptr(weight_out), max_entries,
+                                    ptr(ws), _nbytes(ws), stream_handle(stream)))
+
+
+def csa2_evict_workspace_size(dims: Dims, max_entries: int) -> int:
+    return lib().csa2_evict_workspace_size(C.byref(dims), max_entries)
+
+
+def csa2_evict(dims: Dims, cache: Cache, bounded: Bounded, n_entries, keep, n_sink, n_recent, max_entries, ws,
+               stream=None):
+    """Cuts every sequence of more than `keep` entries to `keep`; n_entries is the cache's own count tensor."""
+    _check(lib().csa2_evict(C.byref(dims), C.byref(cache), C.byref(bounded), ptr(n_entries), keep, n_sink, n_recent,
+                            max_entries, ptr(ws), _nbytes(ws), stream_handle(stream)))
+
+
+def csa2_compress_pack_bounded(hidden, W, gamma, eps, rope_base, W_idx, first_entry, dims: Dims, cache: Cache,
+                               bounded: Bounded, ws, stream=None):
+    """csa2_compress_pack into a bounded cache (positions from first_entry + shift, weights from 0)."""
+    B, T, H = hidden.shape
+    _check(lib().csa2_compress_pack_bounded(ptr(hidden), B, T, H, ptr(W), ptr(gamma), eps, rope_base, ptr(W_idx),
+                                            ptr(first_entry), C.byref(dims), C.byref(cache), C.byref(bounded),
+                                            ptr(ws), _nbytes(ws), stream_handle(stream)))
 
 
 def csa2_layer_workspace_size(args: LayerArgs) -> int:

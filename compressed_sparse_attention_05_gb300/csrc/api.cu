@@ -336,12 +336,10 @@ size_t csa2_compress_layers_workspace_size(int32_t B, int32_t T, int32_t H, int3
   return compress_partials_bytes(B, T, H, L * (d + Di), 0, nullptr);
 }
 
-int csa2_compress_pack(const uint16_t* hidden, int32_t B, int32_t T, int32_t H, const uint16_t* W,
-                       const float* gamma, float eps, float rope_base, const uint16_t* W_idx,
-                       const int32_t* first_entry, const csa2_dims* dm, const csa2_cache* c, void* ws,
-                       size_t ws_bytes, void* stream) {
-  NvtxRange nvtx_("csa2_compress_pack");
-  g_err[0] = 0;
+static int compress_pack_impl(const uint16_t* hidden, int32_t B, int32_t T, int32_t H, const uint16_t* W,
+                              const float* gamma, float eps, float rope_base, const uint16_t* W_idx,
+                              const int32_t* first_entry, const csa2_dims* dm, const csa2_cache* c,
+                              const BoundedSpec& bounded, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_dims(dm, false, false);
   if (rc) return rc;
   if (dm->d != 64 && dm->d != 512) return fail(CSA2_ERR_UNSUPPORTED, "d must be 64 or 512 (got %d)", dm->d);
@@ -371,9 +369,31 @@ int csa2_compress_pack(const uint16_t* hidden, int32_t B, int32_t T, int32_t H, 
   LAUNCH(launch_norm_rope_pack(src, B, G, dm->d, dm->r, gamma, eps, rope_base, first_entry, nullptr,
                                c->page_table, dm->max_pages, c->n_pages, c->kv_codes, c->kv_scales,
                                W_idx ? part + dm->d : nullptr, N, Di, dm->idx_dtype, W_idx ? c->idx_k : nullptr, s,
-                               dm->kv_format == CSA2_KV_FP8),
+                               dm->kv_format == CSA2_KV_FP8, bounded),
          "compress_epilogue");
   return CSA2_OK;
+}
+
+int csa2_compress_pack(const uint16_t* hidden, int32_t B, int32_t T, int32_t H, const uint16_t* W,
+                       const float* gamma, float eps, float rope_base, const uint16_t* W_idx,
+                       const int32_t* first_entry, const csa2_dims* dm, const csa2_cache* c, void* ws,
+                       size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("csa2_compress_pack");
+  g_err[0] = 0;
+  return compress_pack_impl(hidden, B, T, H, W, gamma, eps, rope_base, W_idx, first_entry, dm, c, BoundedSpec{}, ws,
+                            ws_bytes, stream);
+}
+
+int csa2_compress_pack_bounded(const uint16_t* hidden, int32_t B, int32_t T, int32_t H, const uint16_t* W,
+                               const float* gamma, float eps, float rope_base, const uint16_t* W_idx,
+                               const int32_t* first_entry, const csa2_dims* dm, const csa2_cache* c,
+                               const csa2_bounded* bounded, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("csa2_compress_pack_bounded");
+  g_err[0] = 0;
+  REQUIRE(bounded, "bounded must not be NULL");
+  REQUIRE_IPTR(bounded->entry_pos); REQUIRE_IPTR(bounded->weight); REQUIRE_IPTR(bounded->shift);
+  return compress_pack_impl(hidden, B, T, H, W, gamma, eps, rope_base, W_idx, first_entry, dm, c,
+                            BoundedSpec{bounded->shift, bounded->entry_pos, bounded->weight}, ws, ws_bytes, stream);
 }
 
 int csa2_compress_layers(const uint16_t* hidden, int32_t B, int32_t T, int32_t H, int32_t L,
@@ -713,6 +733,157 @@ int csa2_sparse_attn(const csa2_dims* dm, const csa2_cache* c, const csa2_window
   NvtxRange nvtx_("csa2_sparse_attn");
   g_err[0] = 0;
   return attn_impl(dm, c, win, Q, q_pos, idx, cnt, softmax_scale, O, lse, static_cast<cudaStream_t>(stream));
+}
+
+// ---- a bounded cache: attention over all of it, weights, eviction -----------------
+// Checks and arguments that csa2_dense_attn and csa2_entry_weights share.
+static int dense_args(const csa2_dims* dm, const csa2_cache* c, const csa2_bounded* bounded,
+                      const csa2_score_mods* mods, const uint16_t* Q, const int32_t* q_pos, float softmax_scale,
+                      int32_t max_entries, DenseArgs* out) {
+  REQUIRE(dm, "dims must not be NULL");
+  REQUIRE(dm->B >= 0 && dm->Tq >= 0, "B and Tq must be >= 0");
+  REQUIRE(dm->max_pages >= 1, "max_pages must be >= 1");
+  if (dm->d != 64 && dm->d != 512) return fail(CSA2_ERR_UNSUPPORTED, "d must be 64 or 512 (got %d)", dm->d);
+  if (dm->kv_format != CSA2_KV_MXFP4)
+    return fail(CSA2_ERR_UNSUPPORTED, "the whole-cache kernels read the MXFP4 main KV only (kv_format %d)", dm->kv_format);
+  REQUIRE(dm->Hq >= 1 && dm->Hq <= 128, "Hq must be in 1..128 (got %d)", dm->Hq);
+  REQUIRE(dm->W >= 0 && dm->W <= 1024, "W must be in 0..1024 (got %d)", dm->W);
+  REQUIRE(dm->swa_cap >= 0, "swa_cap must be >= 0");
+  REQUIRE(max_entries >= 0, "max_entries must be >= 0");
+  REQUIRE((int64_t)dm->Tq * dm->Hq < (1ll << 30) && dm->B <= 65535, "too many query tokens or sequences");
+  REQUIRE(softmax_scale == softmax_scale && softmax_scale - softmax_scale == 0.f, "softmax_scale must be finite");
+  if (mods) {
+    REQUIRE(mods->logit_cap >= 0.f && mods->logit_cap - mods->logit_cap == 0.f, "logit_cap must be finite and >= 0");
+    if (mods->slopes) REQUIRE_IPTR(mods->slopes);
+    if (mods->doc_start) REQUIRE_IPTR(mods->doc_start);
+    if (mods->prefix_len) REQUIRE_IPTR(mods->prefix_len);
+  }
+  if (bounded && bounded->entry_pos) REQUIRE_IPTR(bounded->entry_pos);
+  if (bounded && bounded->shift) REQUIRE_IPTR(bounded->shift);
+  if ((int64_t)dm->B * dm->Tq == 0) return CSA2_OK;
+  const int rc = check_cache(c, true, false);
+  if (rc) return rc;
+  REQUIRE(c->n_pages < (1ll << 31) / kPage, "cache.n_pages is too large");
+  REQUIRE_PTR(Q); REQUIRE_IPTR(q_pos);
+  DenseArgs a = {};
+  a.Q = Q; a.kv_codes = c->kv_codes; a.kv_scales = c->kv_scales; a.page_table = c->page_table;
+  a.n_entries = c->n_entries; a.q_pos = q_pos; a.n_pages = c->n_pages; a.max_pages = dm->max_pages;
+  a.B = dm->B; a.Tq = dm->Tq; a.Hq = dm->Hq; a.d = dm->d; a.max_entries = max_entries; a.scale = softmax_scale;
+  if (mods) {
+    a.cap = mods->logit_cap; a.slopes = mods->slopes; a.doc_start = mods->doc_start; a.prefix_len = mods->prefix_len;
+  }
+  if (bounded) {
+    a.entry_pos = bounded->entry_pos;
+    a.shift = bounded->shift;
+  }
+  *out = a;
+  return CSA2_OK;
+}
+
+size_t csa2_dense_attn_workspace_size(const csa2_dims* dm, int32_t max_entries) {
+  if (!dm || max_entries < 0 || dm->B <= 0 || dm->Tq <= 0) return 0;
+  return 0;
+}
+
+int csa2_dense_attn(const csa2_dims* dm, const csa2_cache* c, const csa2_bounded* bounded, const csa2_window* win,
+                    const csa2_score_mods* mods, const uint16_t* Q, const int32_t* q_pos, float softmax_scale,
+                    int32_t max_entries, uint16_t* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("csa2_dense_attn");
+  g_err[0] = 0;
+  DenseArgs a;
+  int rc = dense_args(dm, c, bounded, mods, Q, q_pos, softmax_scale, max_entries, &a);
+  if (rc) return rc;
+  if ((int64_t)dm->B * dm->Tq == 0) return CSA2_OK;
+  REQUIRE_PTR(O);
+  if (lse) REQUIRE_IPTR(lse);
+  if (dm->swa_cap > 0 && dm->W > 0) {
+    REQUIRE(win, "window must not be NULL");
+    REQUIRE_PTR(win->codes); REQUIRE_IPTR(win->scales); REQUIRE_IPTR(win->pos0);
+    REQUIRE((int64_t)dm->B * dm->swa_cap < (1ll << 31), "the window buffers are too large");
+    a.W = dm->W; a.swa_cap = dm->swa_cap;
+    a.swa_codes = win->codes; a.swa_scales = win->scales; a.swa_pos0 = win->pos0;
+  }
+  a.O = O; a.lse = lse;
+  const size_t need = csa2_dense_attn_workspace_size(dm, max_entries);
+  if (need && (!ws || ws_bytes < need)) return fail(CSA2_ERR_WORKSPACE, "dense_attn needs %zu workspace bytes (got %zu)", need, ws_bytes);
+  if (need) REQUIRE(aligned16(ws), "ws must be 16-byte aligned");
+  LAUNCH(launch_dense_attn_plain(a, static_cast<cudaStream_t>(stream)), "dense_attn");
+  return CSA2_OK;
+}
+
+size_t csa2_entry_weights_workspace_size(const csa2_dims* dm, int32_t max_entries) {
+  if (!dm || max_entries < 0 || dm->B <= 0 || dm->Tq <= 0) return 0;
+  return 0;
+}
+
+int csa2_entry_weights(const csa2_dims* dm, const csa2_cache* c, const csa2_bounded* bounded,
+                       const csa2_score_mods* mods, const uint16_t* Q, const int32_t* q_pos, const float* lse,
+                       float softmax_scale, float decay, const float* weight_in, float* weight_out,
+                       int32_t max_entries, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("csa2_entry_weights");
+  g_err[0] = 0;
+  DenseArgs a;
+  int rc = dense_args(dm, c, bounded, mods, Q, q_pos, softmax_scale, max_entries, &a);
+  if (rc) return rc;
+  REQUIRE(decay >= 0.f && decay <= 1.f, "decay must be in 0..1 (got %g)", (double)decay);
+  if ((int64_t)dm->B * dm->Tq == 0 || max_entries == 0) return CSA2_OK;
+  REQUIRE_IPTR(lse); REQUIRE_IPTR(weight_out);
+  if (weight_in) REQUIRE_IPTR(weight_in);
+  a.lse_in = lse; a.decay = decay; a.weight_in = weight_in; a.weight_out = weight_out;
+  const size_t need = csa2_entry_weights_workspace_size(dm, max_entries);
+  if (need && (!ws || ws_bytes < need)) return fail(CSA2_ERR_WORKSPACE, "entry_weights needs %zu workspace bytes (got %zu)", need, ws_bytes);
+  if (need) REQUIRE(aligned16(ws), "ws must be 16-byte aligned");
+  LAUNCH(launch_entry_weights_plain(a, static_cast<cudaStream_t>(stream)), "entry_weights");
+  return CSA2_OK;
+}
+
+size_t csa2_evict_workspace_size(const csa2_dims* dm, int32_t max_entries) {
+  if (!dm || max_entries < 0 || dm->B <= 0) return 0;
+  return evict_workspace_bytes(dm->B, max_entries);
+}
+
+int csa2_evict(const csa2_dims* dm, const csa2_cache* c, const csa2_bounded* bounded, int32_t* n_entries,
+               int32_t keep, int32_t n_sink, int32_t n_recent, int32_t max_entries, void* ws, size_t ws_bytes,
+               void* stream) {
+  NvtxRange nvtx_("csa2_evict");
+  g_err[0] = 0;
+  REQUIRE(dm, "dims must not be NULL");
+  REQUIRE(dm->B >= 0 && dm->B <= 65535, "B must be in 0..65535 (got %d)", dm->B);
+  REQUIRE(dm->max_pages >= 1, "max_pages must be >= 1");
+  REQUIRE(dm->kv_format == CSA2_KV_MXFP4 || dm->kv_format == CSA2_KV_FP8, "kv_format must be CSA2_KV_MXFP4 or CSA2_KV_FP8");
+  const bool fp8 = dm->kv_format == CSA2_KV_FP8;
+  if ((dm->d != 64 && dm->d != 512) || (fp8 && dm->d != 512))
+    return fail(CSA2_ERR_UNSUPPORTED, "d must be 64 or 512, and 512 for the FP8 main KV (got %d)", dm->d);
+  REQUIRE(keep >= 1, "keep must be >= 1 (got %d)", keep);
+  REQUIRE(n_sink >= 0 && n_recent >= 0 && (int64_t)n_sink + n_recent <= keep,
+          "n_sink + n_recent must be in 0..keep (got %d + %d, keep %d)", n_sink, n_recent, keep);
+  REQUIRE(max_entries >= 0, "max_entries must be >= 0");
+  if (dm->B == 0) return CSA2_OK;
+  REQUIRE(c, "cache must not be NULL");
+  int rc = check_cache(c, true, false);
+  if (rc) return rc;
+  REQUIRE(n_entries == c->n_entries, "n_entries must be the array that cache.n_entries points to");
+  REQUIRE(bounded, "bounded must not be NULL");
+  REQUIRE_IPTR(bounded->entry_pos); REQUIRE_IPTR(bounded->weight); REQUIRE_IPTR(bounded->shift);
+  if (c->idx_k) {
+    REQUIRE_PTR(c->idx_k);
+    REQUIRE(dm->Di == 32 || dm->Di == 64 || dm->Di == 128, "Di must be 32, 64 or 128 (got %d)", dm->Di);
+    REQUIRE(dm->idx_dtype == CSA2_BF16 || dm->idx_dtype == CSA2_F32, "idx_dtype must be CSA2_BF16 or CSA2_F32");
+  }
+  if (max_entries <= keep) return CSA2_OK;   // no sequence can be over its budget
+  const size_t need = evict_workspace_bytes(dm->B, max_entries);
+  if (!ws || ws_bytes < need) return fail(CSA2_ERR_WORKSPACE, "evict needs %zu workspace bytes (got %zu)", need, ws_bytes);
+  REQUIRE(aligned16(ws), "ws must be 16-byte aligned");
+  EvictArgs a = {};
+  a.kv_codes = c->kv_codes; a.kv_scales = c->kv_scales; a.idx_k = static_cast<uint8_t*>(c->idx_k);
+  a.page_table = c->page_table; a.n_entries = n_entries; a.entry_pos = bounded->entry_pos;
+  a.weight = bounded->weight; a.shift = bounded->shift; a.n_pages = c->n_pages; a.B = dm->B;
+  a.max_pages = dm->max_pages; a.max_entries = max_entries; a.keep = keep; a.n_sink = n_sink; a.n_recent = n_recent;
+  a.code_bytes = fp8 ? dm->d : dm->d / 2;
+  a.scale_bytes = fp8 ? 4 : dm->d / 16;
+  a.idx_bytes = dm->Di * (dm->idx_dtype == CSA2_F32 ? 4 : 2);
+  LAUNCH(launch_evict(a, ws, static_cast<cudaStream_t>(stream)), "evict");
+  return CSA2_OK;
 }
 
 size_t csa2_layer_workspace_size(const csa2_layer_args* a) {

@@ -63,6 +63,13 @@ cudaError_t launch_pack_fp8_window(const float* x, int B, int Tq, int d, const i
                                    const int32_t* pos0, int swa_cap, uint8_t* codes,
                                    float* scales, cudaStream_t s);
 
+// A bounded cache's state as the packing epilogue needs it: entry e is rotated at
+// position 4(e + shift[b]) + 3, which is stored in entry_pos, and starts with weight 0.
+struct BoundedSpec {
+  const int32_t* shift;
+  int32_t* entry_pos;
+  float* weight;
+};
 // Row source of the norm/rope/pack epilogue: either a plain fp32 latent
 // [B][n_max][d] or n_split fp32 partial sums [n_split][M][ld] (compression).
 struct LatentSource {
@@ -98,7 +105,9 @@ cudaError_t launch_norm_rope_pack(LatentSource src, int B, int n_max, int d, int
                                   const float* idx_src, int64_t idx_row_stride, int Di,
                                   int idx_dtype, void* idx_k, cudaStream_t s,
                                   // 1: FP8 main-KV rows (E4M3 codes [d], fp32 scale per entry)
-                                  int kv_fp8 = 0);
+                                  int kv_fp8 = 0,
+                                  // a bounded cache's state (csa2_compress_pack_bounded)
+                                  BoundedSpec bounded = {});
 // Window rows rebuilt from replayed tokens: row i of sequence b (latent = the
 // split sum of src row b * n_tok + i) gets RMSNorm, RoPE at raw position
 // tok_pos0[b] + i and the FP8 pack, into window row tok_pos0[b] + i - win_pos0[b].
@@ -218,5 +227,52 @@ cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t s);
 // ---- attention_tc.cu: tcgen05 kernel for d = 512 (every Hq and K + W the ABI admits)
 bool sparse_attn_tc_supported(const AttnArgs& a);
 cudaError_t launch_sparse_attn_tc(const AttnArgs& a, cudaStream_t s);
+
+// ---- attention and attention weights over the whole cache -----------------------
+struct DenseArgs {
+  const uint16_t* Q;          // [B][Tq][Hq][d] bf16
+  const uint8_t* kv_codes;
+  const uint8_t* kv_scales;
+  const int32_t* page_table;  // [B][max_pages]
+  const int32_t* n_entries;   // [B]
+  const int32_t* q_pos;       // [B][Tq]
+  const uint8_t* swa_codes;   // [B][swa_cap][d]
+  const float* swa_scales;    // [B][swa_cap]
+  const int32_t* swa_pos0;    // [B]
+  const float* slopes;        // [Hq] or null
+  const int32_t* doc_start;   // [B][Tq] or null
+  const int32_t* prefix_len;  // [B] or null
+  const int32_t* entry_pos;   // [n_pages][64] or null
+  const int32_t* shift;       // [B] or null
+  int64_t n_pages;
+  int max_pages, B, Tq, Hq, d, W, swa_cap, max_entries;
+  float scale, cap;
+  uint16_t* O;                // attention: [B][Tq][Hq][d] bf16
+  float* lse;                 // attention: [B][Tq][Hq] or null
+  const float* lse_in;        // weights: [B][Tq][Hq]
+  const float* weight_in;     // weights: [n_pages][64] or null
+  float* weight_out;          // weights: [n_pages][64]
+  float decay;
+};
+// ---- dense_attn.cu: plain kernels for d = 64 (and any shape the others do not take)
+cudaError_t launch_dense_attn_plain(const DenseArgs& a, cudaStream_t s);
+cudaError_t launch_entry_weights_plain(const DenseArgs& a, cudaStream_t s);
+
+// ---- evict.cu ---------------------------------------------------------------------
+struct EvictArgs {
+  uint8_t* kv_codes;
+  uint8_t* kv_scales;
+  uint8_t* idx_k;             // or null
+  const int32_t* page_table;
+  int32_t* n_entries;
+  int32_t* entry_pos;
+  float* weight;
+  int32_t* shift;
+  int64_t n_pages;
+  int B, max_pages, max_entries, keep, n_sink, n_recent;
+  int code_bytes, scale_bytes, idx_bytes;   // per entry
+};
+size_t evict_workspace_bytes(int B, int max_entries);
+cudaError_t launch_evict(const EvictArgs& a, void* ws, cudaStream_t s);
 
 }  // namespace csa2

@@ -191,7 +191,7 @@ __device__ __forceinline__ void norm_rope_pack_entry(const LatentSource& src, in
                                                      uint8_t* __restrict__ kv_scales, const float* idx_src,
                                                      int64_t idx_row_stride, int Di, int idx_dtype, void* idx_k,
                                                      int kv_fp8, const RopeTurns& rope, float* row, int lane,
-                                                     uint32_t* status) {
+                                                     uint32_t* status, const BoundedSpec& bd = {}) {
   const int b = (int)(m / n_max), i = (int)(m % n_max);
   if (n_rows && i >= n_rows[b]) return;
   const int e = first_entry[b] + i;
@@ -201,7 +201,11 @@ __device__ __forceinline__ void norm_rope_pack_entry(const LatentSource& src, in
   const bool has = lane < d / 16;
   float v[16];
   load_latent(src, m, has, lane, v);
-  norm_rope_row(v, has, d, r, gamma, eps, 4ull * (uint64_t)e + 3ull, rope, row, lane);
+  // an entry of a bounded cache keeps the position it would have had without evictions
+  const uint64_t pos = 4ull * ((uint64_t)e + (bd.shift ? (uint64_t)max(0, bd.shift[b]) : 0ull)) + 3ull;
+  if (lane == 0 && bd.entry_pos) bd.entry_pos[slot] = (int32_t)pos;
+  if (lane == 0 && bd.weight) bd.weight[slot] = 0.f;
+  norm_rope_row(v, has, d, r, gamma, eps, pos, rope, row, lane);
   if (kv_fp8) {   // the FP8 main-KV format: R5's row rule, one fp32 scale per entry
     __syncwarp();
     fp8_row(row, d, kv_codes + slot * d, reinterpret_cast<float*>(kv_scales) + slot, lane);
@@ -231,7 +235,7 @@ k_norm_rope_pack(LatentSource src, int B, int n_max, int d, int r, const float* 
                  int max_pages, int64_t n_pages, uint8_t* __restrict__ kv_codes,
                  uint8_t* __restrict__ kv_scales, const float* idx_src, int64_t idx_row_stride,
                  int Di, int idx_dtype, void* idx_k, int kv_fp8, const __grid_constant__ RopeTurns rope,
-                 uint32_t* status) {
+                 uint32_t* status, BoundedSpec bd) {
   __shared__ __align__(16) float row_buf[kNrpWarps][512];
   pdl_trigger();
   pdl_wait();
@@ -240,7 +244,7 @@ k_norm_rope_pack(LatentSource src, int B, int n_max, int d, int r, const float* 
   if (m >= (int64_t)B * n_max) return;
   norm_rope_pack_entry(src, m, n_max, d, r, gamma, eps, first_entry, n_rows, page_table, max_pages, n_pages, kv_codes,
                        kv_scales, idx_src, idx_row_stride, Di, idx_dtype, idx_k, kv_fp8, rope, row_buf[warp], lane,
-                       status);
+                       status, bd);
 }
 
 // The same for several layers at once (grid.y = layer): every layer's latent
@@ -352,14 +356,14 @@ cudaError_t launch_norm_rope_pack(LatentSource src, int B, int n_max, int d, int
                                   const int32_t* page_table, int max_pages, int64_t n_pages,
                                   uint8_t* kv_codes, uint8_t* kv_scales, const float* idx_src,
                                   int64_t idx_row_stride, int Di, int idx_dtype, void* idx_k,
-                                  cudaStream_t s, int kv_fp8) {
+                                  cudaStream_t s, int kv_fp8, BoundedSpec bounded) {
   const int64_t rows = (int64_t)B * n_max;
   if (rows == 0) return cudaSuccess;
   if (r < 0 || r / 2 > 256 || (kv_fp8 && d != 512)) return cudaErrorInvalidValue;
   const RopeTurns rope = rope_turns(r, rope_base);
   return launch_step(k_norm_rope_pack, dim3(grid_for(rows, kNrpWarps)), dim3(kNrpWarps * 32), 0, s,
       src, B, n_max, d, r, gamma, eps, first_entry, n_rows, page_table, max_pages,
-      n_pages, kv_codes, kv_scales, idx_src, idx_row_stride, Di, idx_dtype, idx_k, kv_fp8, rope, status_word());
+      n_pages, kv_codes, kv_scales, idx_src, idx_row_stride, Di, idx_dtype, idx_k, kv_fp8, rope, status_word(), bounded);
 }
 
 cudaError_t launch_norm_rope_pack_layers(LatentSource src, int B, int n_max, int d, int r, const float* gamma,

@@ -98,6 +98,31 @@
  *      replayed token's own latent RoPE_t(RMSNorm(W_swa h_t)) at its raw
  *      position t, packed as R5; the rebuilt window starts at the first
  *      replayed token.
+ *   R14 attention over the whole cache (csa2_dense_attn): R11's attention with
+ *      every visible entry in the place of a selection, and O in bf16.  Logits
+ *      l = cap * tanh(softmax_scale * q . k / cap) (cap = 0: no cap), minus
+ *      slopes[h] * |t - p| with p the raw position of the key (an entry's: of
+ *      its last token).  A key is visible to the token at raw position t if
+ *        - entry j: j + shift completes by then, 4 (j + shift) + 3 <= t, where
+ *          shift is the number of entries evicted so far (R16); tokens of the
+ *          prefix (t < prefix_len) see every entry with 4 (j + shift) + 3 <
+ *          prefix_len instead;
+ *        - window row: raw position in max(0, t-W+1) .. t, held by the buffer
+ *          (the window stays causal in the prefix too);
+ *        - and, with a document mask, all of its tokens lie at or after
+ *          doc_start.
+ *      A token that sees nothing gets O = 0 and lse = -inf.  Products run on
+ *      fp16 tensor-core operands with R11's powers of two, P rounded to fp16,
+ *      everything else in fp32; O is rounded once.
+ *   R15 accumulated weight: weight_out[j] = decay * weight_in[j] + the sum over
+ *      the call's query tokens and heads of exp(l - lse), l as in R14, lse as
+ *      csa2_dense_attn wrote it; rows whose lse is infinite add nothing.
+ *   R16 eviction: of n > keep entries those stay whose position is among the
+ *      first n_sink of the sequence or the newest n_recent, then the ones of
+ *      highest weight (equal weights -> lower index; -0 equals +0), keep in
+ *      all.  Survivors below index keep stay where they are; those above, in
+ *      index order, fill the holes below keep, in index order.  So an entry's
+ *      index no longer gives its position: entry_pos does.
  * ---------------------------------------------------------------------------
  */
 #ifndef CSA2_H
@@ -361,6 +386,89 @@ int csa2_sparse_attn(const csa2_dims* dims, const csa2_cache* cache, const csa2_
                      const uint16_t* Q, const int32_t* q_pos, const int32_t* idx,
                      const int32_t* cnt, float softmax_scale, float* O, float* lse,
                      void* stream);
+
+/* ---- a bounded cache: attention over all of it, weights, eviction ------------
+ * A cache that never grows past a budget needs no selection: every entry it
+ * holds is attended to, the weight each entry receives is added up, and when
+ * the cache is full the entries of least weight leave.
+ *
+ * State of such a cache, beside csa2_cache (weight and entry_pos lie like the
+ * pages, one value per slot; shift has one per sequence).  A cache that no
+ * entry was evicted from may go without (NULL, or NULL members): entry j's
+ * position is then 4 (j + shift) + 3 and shift is 0. */
+typedef struct csa2_bounded {
+  int32_t* entry_pos;        /* [n_pages][64] raw position of the entry's last token */
+  float* weight;             /* [n_pages][64] accumulated weight (R15)          */
+  int32_t* shift;            /* [B] entries evicted so far                      */
+} csa2_bounded;
+
+/* Changes to the logits and to what is visible (R14); NULL or zeros: none. */
+typedef struct csa2_score_mods {
+  float logit_cap;           /* > 0: l = cap * tanh(l / cap)                    */
+  const float* slopes;       /* fp32 [Hq]: l -= slopes[h] * |t - p|             */
+  const int32_t* doc_start;  /* [B][Tq] raw position where the token's document starts */
+  const int32_t* prefix_len; /* [B] tokens at positions below it see each other */
+} csa2_score_mods;
+
+/* Attention over every visible entry and the window (R14).  Q bf16
+ * [B][Tq][Hq][d], q_pos int32 [B][Tq] raw positions (after an eviction too), O
+ * bf16 [B][Tq][Hq][d], lse fp32 [B][Tq][Hq] or NULL.  max_entries bounds every
+ * n_entries[b] (more: CSA2_STATUS_BAD_COUNT, and only max_entries are read).
+ * dims: B, Tq, d, Hq, W, max_pages, swa_cap are used; d = 512 or 64, MXFP4 main
+ * KV only.  A page-table entry out of range hides its entries and raises
+ * CSA2_STATUS_BAD_PAGE.  bounded: entry_pos and shift are read (NULL: see
+ * above).  Needs csa2_dense_attn_workspace_size() bytes of workspace, which
+ * calls that can overlap must not share. */
+size_t csa2_dense_attn_workspace_size(const csa2_dims* dims, int32_t max_entries);
+int csa2_dense_attn(const csa2_dims* dims, const csa2_cache* cache, const csa2_bounded* bounded,
+                    const csa2_window* win, const csa2_score_mods* mods, const uint16_t* Q,
+                    const int32_t* q_pos, float softmax_scale, int32_t max_entries, uint16_t* O,
+                    float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* The weight that every entry received from the call's query tokens (R15):
+ * Q, q_pos, softmax_scale and mods as given to csa2_dense_attn, lse as it wrote
+ * them.  weight_in fp32 [n_pages][64] (NULL: zeros), weight_out fp32
+ * [n_pages][64] (may be weight_in): written for the n_entries[b] entries of
+ * every sequence, whether a token of the call saw them or not; other slots are
+ * left as they were.  Sequences must not share pages.  decay in 0..1.  Sums run
+ * in a fixed order.  Needs csa2_entry_weights_workspace_size() bytes of
+ * workspace, which calls that can overlap must not share. */
+size_t csa2_entry_weights_workspace_size(const csa2_dims* dims, int32_t max_entries);
+int csa2_entry_weights(const csa2_dims* dims, const csa2_cache* cache, const csa2_bounded* bounded,
+                       const csa2_score_mods* mods, const uint16_t* Q, const int32_t* q_pos,
+                       const float* lse, float softmax_scale, float decay, const float* weight_in,
+                       float* weight_out, int32_t max_entries, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* Cuts every sequence of more than `keep` entries to `keep` (R16): moves codes,
+ * scales, indexer keys (unless cache->idx_k is NULL), weights and positions
+ * inside the sequence's own pages, sets n_entries[b] = keep and adds the number
+ * evicted to shift[b].  n_entries is the array that cache->n_entries points to,
+ * writable.  Slots at index >= keep keep their bytes; pages that lie wholly
+ * there are free for reuse once the call is done.  keep >= 1, n_sink + n_recent <= keep.  A
+ * sequence whose n_entries is negative, above max_entries or past its page
+ * table, or whose shift is negative, stays as it is and raises
+ * CSA2_STATUS_BAD_COUNT.  Sequences must not share pages.  NaN weights are not
+ * supported.  dims: B, d, Di, idx_dtype, max_pages, kv_format are used.
+ *
+ * After an eviction csa2_index_topk, csa2_sparse_attn and the other calls that
+ * know nothing of shift take q_pos[b][i] - 4 shift[b] in the place of q_pos
+ * (their visible count is then min(n_entries, floor((t+1)/4) - shift)) and
+ * win->pos0[b] - 4 shift[b] in the place of pos0, with keep >= W / 4. */
+size_t csa2_evict_workspace_size(const csa2_dims* dims, int32_t max_entries);
+int csa2_evict(const csa2_dims* dims, const csa2_cache* cache, const csa2_bounded* bounded,
+               int32_t* n_entries, int32_t keep, int32_t n_sink, int32_t n_recent,
+               int32_t max_entries, void* ws, size_t ws_bytes, void* stream);
+
+/* csa2_compress_pack into a bounded cache: entry first_entry[b] + i (an index)
+ * is rotated at position 4 (first_entry[b] + shift[b] + i) + 3, which entry_pos
+ * receives, and starts with weight 0.  Workspace as for csa2_compress_pack. */
+int csa2_compress_pack_bounded(const uint16_t* hidden, int32_t B, int32_t T, int32_t H,
+                               const uint16_t* W, const float* gamma, float eps, float rope_base,
+                               const uint16_t* W_idx, const int32_t* first_entry,
+                               const csa2_dims* dims, const csa2_cache* cache,
+                               const csa2_bounded* bounded, void* ws, size_t ws_bytes,
+                               void* stream);
 
 /* ---- one layer step in any mode -------------------------------------------
  * FULL    : [compress new tokens if hidden != NULL] [pack window rows of the

@@ -18,6 +18,8 @@ citing the passage it follows:
              and an independent dense masked form
   replay     SWA Bounded Replay: window rows rebuilt from the replayed
              tokens' hidden states, and the window cut at the replay start
+  bounded    attention over a whole bounded cache (score cap, distance bias,
+             document and prefix masks), accumulated weights, eviction
   layer      the layer schedule (Full / Reindex / Reuse) for sampled tokens
 
 Pins (tests/test_oracle_*.py, run with ``-m "not gpu"``) tie every function
