@@ -781,8 +781,8 @@ static int dense_args(const csa2_dims* dm, const csa2_cache* c, const csa2_bound
 }
 
 size_t csa2_dense_attn_workspace_size(const csa2_dims* dm, int32_t max_entries) {
-  if (!dm || max_entries < 0 || dm->B <= 0 || dm->Tq <= 0) return 0;
-  return 0;
+  if (!dm || max_entries < 0 || dm->B <= 0 || dm->Tq <= 0 || dm->Hq <= 0 || !dense_tc_supported(dm)) return 0;
+  return dense_attn_workspace_bytes(dm, max_entries);
 }
 
 int csa2_dense_attn(const csa2_dims* dm, const csa2_cache* c, const csa2_bounded* bounded, const csa2_window* win,
@@ -807,13 +807,14 @@ int csa2_dense_attn(const csa2_dims* dm, const csa2_cache* c, const csa2_bounded
   const size_t need = csa2_dense_attn_workspace_size(dm, max_entries);
   if (need && (!ws || ws_bytes < need)) return fail(CSA2_ERR_WORKSPACE, "dense_attn needs %zu workspace bytes (got %zu)", need, ws_bytes);
   if (need) REQUIRE(aligned16(ws), "ws must be 16-byte aligned");
-  LAUNCH(launch_dense_attn_plain(a, static_cast<cudaStream_t>(stream)), "dense_attn");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LAUNCH(dense_tc_supported(dm) ? launch_dense_attn_tc(dm, a, ws, s) : launch_dense_attn_plain(a, s), "dense_attn");
   return CSA2_OK;
 }
 
 size_t csa2_entry_weights_workspace_size(const csa2_dims* dm, int32_t max_entries) {
-  if (!dm || max_entries < 0 || dm->B <= 0 || dm->Tq <= 0) return 0;
-  return 0;
+  if (!dm || max_entries < 0 || dm->B <= 0 || dm->Tq <= 0 || dm->Hq <= 0 || !dense_tc_supported(dm)) return 0;
+  return entry_weights_workspace_bytes(dm, max_entries);
 }
 
 int csa2_entry_weights(const csa2_dims* dm, const csa2_cache* c, const csa2_bounded* bounded,
@@ -833,7 +834,9 @@ int csa2_entry_weights(const csa2_dims* dm, const csa2_cache* c, const csa2_boun
   const size_t need = csa2_entry_weights_workspace_size(dm, max_entries);
   if (need && (!ws || ws_bytes < need)) return fail(CSA2_ERR_WORKSPACE, "entry_weights needs %zu workspace bytes (got %zu)", need, ws_bytes);
   if (need) REQUIRE(aligned16(ws), "ws must be 16-byte aligned");
-  LAUNCH(launch_entry_weights_plain(a, static_cast<cudaStream_t>(stream)), "entry_weights");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LAUNCH(dense_tc_supported(dm) ? launch_entry_weights_tc(dm, a, ws, s) : launch_entry_weights_plain(a, s),
+         "entry_weights");
   return CSA2_OK;
 }
 

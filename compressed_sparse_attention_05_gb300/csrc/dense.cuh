@@ -22,8 +22,8 @@ __device__ __forceinline__ bool dense_count_bad(const DenseArgs& a, int b) {
   return n < 0 || n > min((int64_t)a.max_entries, (int64_t)a.max_pages * kPage) || (a.shift && a.shift[b] < 0);
 }
 
-// Raw position of entry j's last token before the `shift` entries evicted from the
-// cache are known one by one: entry j of an untouched cache, or of its newest part.
+// Entries evicted from sequence b so far: without entry_pos, entry j's last token is at
+// raw position 4 (j + shift) + 3.
 __device__ __forceinline__ int64_t dense_shift(const DenseArgs& a, int b) {
   const int s = a.shift ? a.shift[b] : 0;
   return s > 0 ? s : 0;
@@ -54,10 +54,10 @@ __device__ __forceinline__ DenseRow dense_row(const DenseArgs& a, int b, int i, 
   return r;
 }
 
-// First entry index that a document mask can let through (entries of an untouched
-// cache are in position order: entry j's first token is at 4j).
-__device__ __forceinline__ int dense_first(const DenseArgs& a, int doc) {
-  return a.entry_pos ? 0 : (int)(((int64_t)doc + 3) >> 2);
+// First entry index that a document mask can let through (without entry_pos the
+// entries are in position order: entry j's first token is at 4 (j + shift)).
+__device__ __forceinline__ int dense_first(const DenseArgs& a, int doc, int64_t shift) {
+  return a.entry_pos ? 0 : (int)max((int64_t)0, (((int64_t)doc + 3) >> 2) - shift);
 }
 
 }  // namespace csa2

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
     __syncthreads();
     attend(w0 + lane < r.w_n, dense_distance(r.t, (int64_t)r.w_lo + w0 + lane));
   }
-  for (int e0 = dense_first(a, r.doc) / kTile * kTile; e0 < r.nv; e0 += kTile) {
+  for (int e0 = dense_first(a, r.doc, shift) / kTile * kTile; e0 < r.nv; e0 += kTile) {
     __syncthreads();
     load_entries(a, b, e0, n_ent, shift, tile, kLd, pos, slots, status);
     const int64_t p = pos[lane];

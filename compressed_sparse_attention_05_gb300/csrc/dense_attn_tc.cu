@@ -1,0 +1,1286 @@
+// Attention over every visible entry of the compressed cache (reading R14) and the
+// entries' attention weights (reading R15) on the fifth-generation tensor cores,
+// d = 512.
+//
+//   l_rj = cap tanh(tau q_r . k_j / cap) - slope_h |t_r - p_j|
+//   O_r  = sum_j exp(l_rj - m) k_j / sum_j exp(l_rj - m),  lse_r = m + log(sum)
+//   w_j  = decay w_j + sum_r exp(l_rj - lse_r)
+//
+// One shared KV head, so the (token, head) pairs of a sequence are the rows of one
+// matrix whatever the number of heads: a tile is 64 consecutive rows (one token of
+// 64 heads, half a token of 128, several tokens of fewer heads), each row with its
+// own masks.  A tile's keys come in chunks of 128, nearest first (window rows, then
+// entries from the newest to the oldest), so that a distance bias only lowers later
+// chunks and the reference maxima hardly move.  Per chunk
+//   S^T [128 keys x 64 rows]  = K [128 x 512] . Q^T        (32 MMAs, k = 16 channels)
+//   O^T [512 dims x 64 rows] += V^T [512 x 128] . P^T      (4 M-tiles x 8 MMAs, k = 16 keys)
+//
+// Two copies of the dequantised chunk keep the two products apart: the score
+// product reads K as an A operand in tensor memory (a ring of three 128-channel
+// quarters), the value product reads V from shared memory.  So S of the next chunk
+// runs while the softmax of this one does, and the shared-memory copy is only
+// rewritten quarter by quarter behind the value product.  S from tensor memory also
+// leaves shared memory, the narrowest path of this shape (N = 64), to the value
+// product.
+//
+// Work is split over the SMs by chunks, not by tiles: every CTA computes the chunk
+// count of all tiles (lengths live on the device), takes an equal contiguous share,
+// and walks the tiles in it.  A tile that falls to several CTAs leaves partial
+// (m, l, O) in the workspace and k_dense_merge joins them in order.
+//
+// Roles (768 threads): warps 0-15 dequantise (thread = one key x 128 channels),
+// warps 16-19 do the softmax (thread = one key x 64 rows), warp 20 issues the MMAs,
+// warp 21 requests pages into L2 ahead.  Operand ranges as in attention_tc.cu (R11's
+// powers of two for Q rows and window rows); P is rounded to fp16, the normaliser
+// sums the unrounded fp32 P, everything else is fp32.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "dense.cuh"
+#include "operands.cuh"
+#include "tc.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kD = 512;
+constexpr int kRows = 64;                 // rows of a tile (N of both products)
+constexpr int kChunk = 128;               // keys of a chunk
+constexpr int kDeqWarps = 16, kSoftWarps = 4;
+constexpr int kDeqThreads = kDeqWarps * 32;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kThreads = 768;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
+constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
+// registers per thread after the split: 4 x 80 + 120 + 40 = 6 x 80 per warpgroup set
+constexpr int kRegsLaunch = 80, kRegsSoft = 120, kRegsMisc = 40;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0;             // O^T: four M-tiles of 64 columns
+constexpr uint32_t kColS = 256;           // S^T: 64 columns
+constexpr uint32_t kColK = 320;           // K ring: three quarters of 64 columns (128 channels of fp16)
+constexpr int kRing = 3;
+constexpr float kRescaleLog2 = 8.f;       // a reference maximum moves only beyond this growth
+constexpr float kUnset = 3e38f;           // -m_ref of a row without keys: any finite logit outgrows it, -inf stays -inf
+constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, then m and l
+
+// Operand tiles (no-swizzle canonical layout, core matrices of 8 rows x 16 bytes):
+//   Q [row][dim]: (r/8)*8192 + (d/8)*128 + (r%8)*16 + (d%8)*2
+//   V [key][dim]: (k/8)*8192 + (d/8)*128 + (k%8)*16 + (d%8)*2
+//   P [key][row]: (k/8)*1024 + (r/8)*128 + (k%8)*16 + (r%8)*2
+struct Segment {            // what the roles need to know of the current tile
+  int b, nw, c_hi, units;   // window chunks; entry chunks end at c_hi; units = max(1, chunks)
+  int n_chunks;
+  int e_lo, e_hi;           // entries any row of the tile sees
+  int w_lo, w_hi;           // window rows any row sees (raw positions, inclusive)
+  int all_lo, all_hi;       // entries every row sees
+  int one_t, t;             // all rows belong to the token at raw position t
+  int pos0;
+};
+template <bool kWeights>
+struct Smem {
+  uint16_t q[kRows * kD];
+  uint16_t v[kWeights ? 8 : kChunk * kD];
+  uint16_t p[kWeights ? 8 : 2 * kChunk * kRows];
+  float mult[kRows];        // logit multiplier: softmax scale * log2(e) * 2^e_r
+  float nref[kRows];        // attention: -m_ref (kUnset before the row's first key); weights: -lse * log2(e)
+  float slope2[kRows];      // slope * log2(e)
+  // a row sees entry j if j < hi[0] and its first token is >= lo[0], and the window row
+  // at position p if p - 1 < hi[1] (the row's own position) and p >= lo[1]
+  int hi[2][kRows], lo[2][kRows];
+  union {
+    float red[kSoftWarps][kRows];   // per-warp maxima / sums of a row over the keys; [0] also: see below
+    int qexp[kSoftWarps][kRows];    // [1]: largest exponent field of each row of Q, before the products
+    int64_t scan[kThreads / 32];    // before the first tile
+  };
+  uint64_t kq_full[kRing], kq_free[kRing], s_full, s_free, v_full[4], pv_done[4], p_full, p_free[2];
+  Segment seg;
+  int64_t found_start;
+  int found_tile;
+  uint32_t tmem;
+  int abort;
+  int progress;             // chunks whose softmax has begun (paces the L2 requests)
+};
+// red[0][r] holds the factor of a row's rescaling and, at the end of a tile, its sum l:
+// each is computed by the one thread that reads the column, from the column.
+static_assert(sizeof(Smem<false>) <= 232448, "shared memory of the attention kernel");
+
+struct Plan {
+  int tiles_per_seq;        // of the whole call
+  int tile0, tiles;         // tiles [tile0, tile0 + tiles) of every sequence are this launch's
+  int n_ctas;
+  float* parts;             // attention: partial results, kPartFloats per slot, two slots per CTA
+  int32_t* cont;            // attention: [n_ctas] tile that the CTA's share starts in the middle of, or -1
+  float* sums;              // weights: [B * tiles][sum_stride] when a sequence has several tiles, else null
+  int2* ranges;             // weights: [B * tiles] entry chunks written to sums
+  int64_t sum_stride;
+};
+
+__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void deq_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kDeqThreads) : "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
+__device__ __forceinline__ bool soft_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "n"(kSoftThreads)
+      : "memory");
+  return r != 0;
+}
+
+// Bounded wait of a whole warp; on time-out the CTA's abort flag is raised.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool ok = false;
+  for (uint32_t i = 0; i < (1u << 21); ++i) {   // <= 2^21 suspensions of <= 1 us
+    if (tc::mbar_try_wait_sleep(bar, parity, 1000)) {
+      ok = true;
+      break;
+    }
+    if ((i & 63) == 63 && *abort) break;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) *abort = 1;
+  return ok;
+}
+
+// tcgen05.mma with the A operand in tensor memory (K-major, two fp16 per column).
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::
+          "r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// tanh: an odd polynomial below 0.55 (least-squares fit of (tanh x / x - 1) / x^2 in
+// x^2, relative error 1.2 x 2^-24), 1 - 2 / (e^2x + 1) above (relative error < 2^-21).
+__device__ __forceinline__ float fast_tanh(float x) {
+  const float a = fabsf(x), z = x * x;
+  float r = -0.0066150883f;
+  r = fmaf(r, z, 0.021312291f);
+  r = fmaf(r, z, -0.053909965f);
+  r = fmaf(r, z, 0.13333116f);
+  r = fmaf(r, z, -0.33333331f);
+  r = fmaf(x * z, r, x);
+  const float e = ex2(fminf(a, 10.f) * (2.f * kLog2e));   // tanh(10) rounds to 1
+  const float big = copysignf(1.f - 2.f * rcp_approx(e + 1.f), x);
+  return a < 0.55f ? r : big;
+}
+
+// ---- tiles and their chunks ----------------------------------------------------------
+struct Range {
+  int e_lo, e_hi, w_lo, w_hi;
+};
+__device__ __forceinline__ int range_chunks(const Range& r, bool weights) {
+  const int ne = r.e_hi > r.e_lo ? (r.e_hi + kChunk - 1) / kChunk - r.e_lo / kChunk : 0;
+  const int nw = !weights && r.w_hi >= r.w_lo ? (int)(((int64_t)r.w_hi - r.w_lo) / kChunk) + 1 : 0;
+  return ne + nw;
+}
+// Chunks of a tile (tile = index among this launch's tiles), at least 1.
+template <bool kWeights>
+__device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {
+  const int b = tile / pl.tiles;
+  const int r0 = (pl.tile0 + tile % pl.tiles) * kRows;
+  const int64_t rows = (int64_t)a.Tq * a.Hq;
+  if (r0 >= rows) return 1;
+  const int n_ent = dense_entries(a, b);
+  Range g{INT_MAX, 0, INT_MAX, INT_MIN};
+  if (kWeights && !pl.sums) {
+    g.e_lo = 0;
+    g.e_hi = n_ent;
+  } else {
+    const int64_t shift = dense_shift(a, b);
+    const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
+    const int i1 = (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
+    for (int i = r0 / a.Hq; i <= i1; ++i) {
+      const DenseRow r = dense_row(a, b, i, n_ent, shift, pos0);
+      const int lo = dense_first(a, r.doc, shift);
+      if (r.nv > lo) {
+        g.e_lo = min(g.e_lo, lo);
+        g.e_hi = max(g.e_hi, r.nv);
+      }
+      if (r.w_n > 0) {
+        g.w_lo = min(g.w_lo, r.w_lo);
+        g.w_hi = max(g.w_hi, r.w_lo + r.w_n - 1);
+      }
+    }
+  }
+  return max(1, range_chunks(g, kWeights));
+}
+
+// Inclusive block-wide prefix sum (all 768 threads), and the total.
+__device__ int64_t block_scan(int64_t v, int64_t* sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+  for (int k = 0; k < kThreads / 32; ++k) {
+    const int64_t s = sums[k];
+    if (k < warp) before += s;
+    all += s;
+  }
+  *total = all;
+  return before + v;
+}
+
+// ---- dequantisation --------------------------------------------------------------------
+// A thread's part of an entry: 128 channels (64 bytes of codes, 8 scales).
+struct Packed {
+  uint4 c[4];
+  uint2 s;
+};
+// 16 channel pairs (32 channels) of MXFP4: piece i of the thread's 128 channels.
+__device__ __forceinline__ void dequant32(const Packed& k, int i, uint32_t (&o)[16]) {
+  const uint32_t w = (i & 2) ? k.s.y : k.s.x;
+  const uint32_t s = e4m3x2_f16x2((w >> (16 * (i & 1))) & 0xFFFFu);
+  const uint32_t g0 = prmt(s, s, 0x1010u), g1 = prmt(s, s, 0x3232u);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t c = word_of(k.c[i], j);
+    const uint32_t g = j < 2 ? g0 : g1;
+    o[4 * j] = hmul2(e2m1x2_f16x2(c & 0xFFu), g);   // exact: <= 6 significant bits
+    o[4 * j + 1] = hmul2(e2m1x2_f16x2((c >> 8) & 0xFFu), g);
+    o[4 * j + 2] = hmul2(e2m1x2_f16x2((c >> 16) & 0xFFu), g);
+    o[4 * j + 3] = hmul2(e2m1x2_f16x2(c >> 24), g);
+  }
+}
+
+template <bool kWeights>
+struct Ctx {
+  const DenseArgs& a;
+  const Plan& pl;
+  Smem<kWeights>& sm;
+  uint32_t tm;
+  int64_t u0, u1;          // this CTA's units
+  int tile;                // first tile and its first unit
+  int64_t tstart;
+  uint32_t* status;
+};
+
+// One key of a chunk as its dequantising thread needs it.
+struct KeyRef {
+  const uint8_t* codes;    // this thread's first code byte (null: no key, zeros)
+  const uint8_t* scales;
+  float wsc;               // window row: scale * 2^-f
+};
+
+template <bool kWeights>
+__device__ __forceinline__ KeyRef key_ref(const Ctx<kWeights>& cx, int k, int key, int qd, bool report) {
+  const Segment& sg = cx.sm.seg;
+  KeyRef r{nullptr, nullptr, 0.f};
+  if (k < sg.nw) {
+    const int64_t p = (int64_t)sg.w_lo + (int64_t)k * kChunk + key;
+    if (p > sg.w_hi) return r;
+    bool seen = sg.one_t != 0;      // one token: the tile's rows all see its whole window
+    if (!seen)
+      for (int i = 0; i < kRows; ++i) seen |= p >= cx.sm.lo[1][i] && p <= cx.sm.hi[1][i];
+    if (!seen) return r;
+    const int64_t w = (int64_t)sg.b * cx.a.swa_cap + (p - sg.pos0);
+    const float s = __ldg(cx.a.swa_scales + w);
+    r.wsc = s * pow2i(-window_exp(s));
+    r.codes = cx.a.swa_codes + w * kD + 128 * qd;
+    return r;
+  }
+  const int j = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key;
+  if (j < sg.e_lo || j >= sg.e_hi) return r;
+  const int page = __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j >> 6));
+  if (page < 0 || page >= cx.a.n_pages) {
+    if (report) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
+    return r;
+  }
+  const int64_t slot = (int64_t)page * kPage + (j & (kPage - 1));
+  r.codes = cx.a.kv_codes + slot * (kD / 2) + 64 * qd;
+  r.scales = cx.a.kv_scales + slot * (kD / 16) + 8 * qd;
+  return r;
+}
+
+template <bool kWeights>
+__device__ __forceinline__ void load_packed(const Ctx<kWeights>& cx, int k, int key, int qd, Packed& o) {
+  // no key: zero codes and scales (the channels are then +0); window rows are read where they are used
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.c[i] = make_uint4(0, 0, 0, 0);
+  o.s = make_uint2(0, 0);
+  if (k < cx.sm.seg.nw) return;
+  const KeyRef r = key_ref<kWeights>(cx, k, key, qd, qd == 0);
+  if (!r.codes) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.c[i] = __ldg(reinterpret_cast<const uint4*>(r.codes) + i);
+  o.s = __ldg(reinterpret_cast<const uint2*>(r.scales));
+}
+
+// Piece i (32 channels) of the thread's key, from the packed registers or the window row.
+template <bool kWeights>
+__device__ __forceinline__ void piece(const Packed& pk, const KeyRef& w, bool window, int i, uint32_t (&o)[16]) {
+  if (window) {   // uniform over the warp
+    uint4 c0 = make_uint4(0, 0, 0, 0), c1 = c0;
+    if (w.codes) {
+      c0 = __ldg(reinterpret_cast<const uint4*>(w.codes) + 2 * i);
+      c1 = __ldg(reinterpret_cast<const uint4*>(w.codes) + 2 * i + 1);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t x = word_of(j < 4 ? c0 : c1, j & 3);
+      o[2 * j] = win2_f16x2(x & 0xFFFFu, w.wsc);
+      o[2 * j + 1] = win2_f16x2(x >> 16, w.wsc);
+    }
+  } else {
+    dequant32(pk, i, o);
+  }
+}
+
+// ---- roles ------------------------------------------------------------------------------
+
+// This CTA's part of the current tile.
+struct Span {
+  int k0, n;        // chunks k0 .. k0 + n - 1
+  bool first, last; // holds the tile's first / last unit
+};
+__device__ __forceinline__ Span span_of(const Segment& sg, int64_t u, int64_t u1, int64_t tstart) {
+  Span s;
+  const int64_t end = min(u1, tstart + sg.units);
+  s.k0 = (int)(u - tstart);
+  s.n = min((int)(end - u), max(0, sg.n_chunks - s.k0));
+  s.first = u == tstart;
+  s.last = end == tstart + sg.units;
+  return s;
+}
+
+template <bool kWeights>
+__device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
+  Smem<kWeights>& sm = cx.sm;
+  const DenseArgs& a = cx.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int key = 32 * (warp & 3) + lane, qd = warp >> 2;
+  const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
+  volatile int* abort = &sm.abort;
+  uint32_t c = 0;                       // chunks so far
+  int tile = cx.tile;
+  int64_t u = cx.u0, tstart = cx.tstart;
+  while (u < cx.u1) {
+    block_sync();                       // the previous tile is done
+    // ---- Q rows -> fp16 B operand, row r scaled by 2^-e_r (exact)
+    const int b = tile / cx.pl.tiles;
+    const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
+    const int64_t rows = (int64_t)a.Tq * a.Hq;
+    if (tid < kRows) sm.qexp[1][tid] = 0;
+    uint4 qv[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int h = 8 * r + (tid & 7), c8 = tid >> 3;
+      qv[r] = r0 + h < rows ? __ldg(reinterpret_cast<const uint4*>(a.Q + ((int64_t)b * rows + r0 + h) * kD + c8 * 8))
+                            : make_uint4(0, 0, 0, 0);
+    }
+    deq_sync();
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      uint32_t e = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = word_of(qv[r], j);
+        e = max(e, max((w >> 7) & 0xFFu, (w >> 23) & 0xFFu));
+      }
+      e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
+      e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
+      if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * r + lane], (int)e);
+    }
+    deq_sync();
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int h = 8 * r + (tid & 7), c8 = tid >> 3;
+      const float qs = pow2i(-q_head_exp(sm.qexp[1][h]));
+      uint32_t ov[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = word_of(qv[r], j);
+        ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
+      }
+      *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + (h >> 3) * 8192 + c8 * 128 + (h & 7) * 16) =
+          make_uint4(ov[0], ov[1], ov[2], ov[3]);
+    }
+    if (tid < kRows) sm.mult[tid] = a.scale * kLog2e * pow2i(q_head_exp(sm.qexp[1][tid]));
+    tc::fence_async_smem();
+    block_sync();                       // Q, row constants and the tile's chunks are there
+    const Span sp = span_of(sm.seg, u, cx.u1, tstart);
+    const int units = sm.seg.units, nw = sm.seg.nw;
+
+    // K of a chunk: quarter qd of every key into the ring
+    auto put_k = [&](int i, const Packed& pk) -> bool {
+      const int k = sp.k0 + i;
+      const bool window = k < nw;
+      KeyRef w{nullptr, nullptr, 0.f};
+      if (window) w = key_ref<kWeights>(cx, k, key, qd, false);
+      const uint32_t seq = 4u * (c + i) + qd, slot = seq % kRing, use = seq / kRing;
+      if (use > 0 && !warp_wait(&sm.kq_free[slot], (use - 1) & 1, abort)) return false;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t o[16];
+        piece<kWeights>(pk, w, window, x, o);
+        __syncwarp();
+        tmem_st16u(cx.tm + kColK + 64 * slot + 16 * x + lane_q, o);
+      }
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.kq_full[slot]);
+      return true;
+    };
+    // V of a chunk: the same channels into the shared-memory tile
+    auto put_v = [&](int i, const Packed& pk) -> bool {
+      const int k = sp.k0 + i;
+      const bool window = k < nw;
+      KeyRef w{nullptr, nullptr, 0.f};
+      if (window) w = key_ref<kWeights>(cx, k, key, qd, false);
+      if (c + i > 0 && !warp_wait(&sm.pv_done[qd], (c + i - 1) & 1, abort)) return false;
+      unsigned char* dst = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 8192 + 16 * qd * 128 + (key & 7) * 16;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t o[16];
+        piece<kWeights>(pk, w, window, x, o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(dst + (4 * x + j) * 128) =
+              make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.v_full[qd]);
+      return true;
+    };
+    if (sp.n > 0) {
+      Packed cur, nxt;
+      load_packed<kWeights>(cx, sp.k0, key, qd, cur);
+      bool ok = put_k(0, cur);
+      if (kWeights) {
+        for (int i = 1; ok && i < sp.n; ++i) {
+          load_packed<kWeights>(cx, sp.k0 + i, key, qd, cur);
+          ok = put_k(i, cur);
+        }
+      } else {
+        if (sp.n > 1) load_packed<kWeights>(cx, sp.k0 + 1, key, qd, nxt);
+        for (int i = 0; ok && i < sp.n; ++i) {
+          if (i + 1 < sp.n) ok = put_k(i + 1, nxt);
+          if (ok) ok = put_v(i, cur);
+          cur = nxt;
+          if (i + 2 < sp.n) load_packed<kWeights>(cx, sp.k0 + i + 2, key, qd, nxt);
+        }
+      }
+    }
+    block_sync();                       // the tile's products are complete, l is known
+    tc::tc_fence_after();
+    if (*abort) break;
+    if (!kWeights) {
+      // ---- O^T from tensor memory: M-tile qd, this warp's lanes (dims), all rows
+      const int dim = 128 * qd + key;
+      const bool whole = sp.first && sp.last;
+      float* part = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kRows; c0 += 16) {
+        float o[16];
+        if (sp.n > 0) {
+          tc::tmem_ld16(cx.tm + kColO + 64 * qd + c0 + lane_q, o);
+          tc::tmem_wait_ld();
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int r = c0 + j;
+          const float x = sp.n > 0 ? o[j] : 0.f;
+          if (!whole)
+            part[r * kD + dim] = x;
+          else if (r0 + r < rows) {
+            const float l = sm.red[0][r];
+            a.O[((int64_t)b * rows + r0 + r) * kD + dim] =
+                (uint16_t)(f32x2_bf16x2(l > 0.f ? x * (1.f / l) : 0.f, 0.f) & 0xFFFFu);
+          }
+        }
+      }
+      tc::tc_fence_before();
+    }
+    c += sp.n;
+    u = min(cx.u1, tstart + units);
+    tstart += units;
+    ++tile;
+  }
+}
+
+// Logits (log2 domain, as the value product carries them) of this thread's key for
+// columns c0 .. c0+15, or -inf where the row does not see the key.
+struct KeyView {
+  bool general;        // masks, cap, bias or a rescaled window row
+  int ka, kb;          // compared with r_hi and r_lo
+  int win;             // 1: window row
+  float kf, ff;        // window row: 2^f and f
+  int64_t p;
+  float dist;          // |t - p| when the tile holds one token
+};
+template <bool kWeights>
+__device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyView& kv, uint32_t lane_q, int c0,
+                                            float (&x)[16]) {
+  const Smem<kWeights>& sm = cx.sm;
+  tc::tmem_ld16(cx.tm + kColS + c0 + lane_q, x);
+  tc::tmem_wait_ld();
+#pragma unroll
+  for (int j4 = 0; j4 < 4; ++j4) {
+    const float4 m = *reinterpret_cast<const float4*>(&sm.mult[c0 + 4 * j4]);
+    x[4 * j4] *= m.x; x[4 * j4 + 1] *= m.y; x[4 * j4 + 2] *= m.z; x[4 * j4 + 3] *= m.w;
+  }
+  if (!kv.general) return;
+  const float cap2 = cx.a.cap * kLog2e;
+  if (kv.kf != 1.f) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] *= kv.kf;
+  }
+  if (cx.a.cap > 0.f) {
+    const float inv = 1.f / cap2;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = cap2 * fast_tanh(x[j] * inv);
+  }
+  if (cx.a.slopes) {
+    if (sm.seg.one_t) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = fmaf(-sm.slope2[c0 + j], kv.dist, x[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int64_t d = (int64_t)sm.hi[1][c0 + j] - kv.p;
+        x[j] = fmaf(-sm.slope2[c0 + j], (float)(d < 0 ? -d : d), x[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const bool seen = kv.ka < sm.hi[kv.win][c0 + j] && kv.kb >= sm.lo[kv.win][c0 + j];
+    x[j] = seen ? x[j] + kv.ff : -INFINITY;
+  }
+}
+
+template <bool kWeights>
+__device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
+  Smem<kWeights>& sm = cx.sm;
+  const DenseArgs& a = cx.a;
+  const int st = threadIdx.x - kDeqThreads, warp = st >> 5, lane = st & 31;
+  const int key = st;                   // thread = key of the chunk = tensor-memory lane
+  const uint32_t lane_q = (uint32_t)(32 * warp) << 16;
+  volatile int* abort = &sm.abort;
+  uint32_t c = 0;
+  int tile = cx.tile;
+  int64_t u = cx.u0, tstart = cx.tstart;
+  const int64_t rows = (int64_t)a.Tq * a.Hq;
+  while (u < cx.u1) {
+    block_sync();
+    // ---- rows of the tile
+    const int b = tile / cx.pl.tiles;
+    const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
+    const int n_ent = dense_entries(a, b);
+    const int64_t shift = dense_shift(a, b);
+    if (st == 0) {
+      sm.seg.b = b;
+      sm.seg.pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
+      sm.seg.e_lo = INT_MAX; sm.seg.e_hi = 0; sm.seg.w_lo = INT_MAX; sm.seg.w_hi = INT_MIN;
+      sm.seg.all_lo = 0; sm.seg.all_hi = INT_MAX;
+      sm.seg.one_t = r0 / a.Hq == (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
+      if (tile % cx.pl.tiles == 0 && tstart == u && dense_count_bad(a, b)) raise_status(cx.status, CSA2_STATUS_BAD_COUNT);
+    }
+    soft_sync();
+    if (st < kRows) {
+      const bool live = r0 + st < rows;
+      DenseRow r{INT_MIN, 0, 0, 0, 0};
+      float slope = 0.f, nref = kUnset;
+      if (live) {
+        const int i = (r0 + st) / a.Hq, h = (r0 + st) % a.Hq;
+        r = dense_row(a, b, i, n_ent, shift, sm.seg.pos0);
+        const int lo = dense_first(a, r.doc, shift);
+        if (r.nv > lo) {
+          atomicMin(&sm.seg.e_lo, lo);
+          atomicMax(&sm.seg.e_hi, r.nv);
+        }
+        if (r.w_n > 0) {
+          atomicMin(&sm.seg.w_lo, r.w_lo);
+          atomicMax(&sm.seg.w_hi, r.w_lo + r.w_n - 1);
+        }
+        atomicMax(&sm.seg.all_lo, a.entry_pos && r.doc > 0 ? INT_MAX : lo);   // by position: no chunk is free of masks
+        atomicMin(&sm.seg.all_hi, r.nv);
+        if (a.slopes) slope = a.slopes[h];
+        if (kWeights) {
+          const float lse = a.lse_in[(int64_t)b * rows + r0 + st];
+          nref = isinf(lse) ? -INFINITY : -lse * kLog2e;   // a row that saw nothing adds nothing
+        }
+        if (st == 0) sm.seg.t = r.t;
+      } else if (kWeights) {
+        nref = -INFINITY;
+      }
+      sm.hi[0][st] = r.nv;
+      sm.lo[0][st] = r.doc;
+      sm.hi[1][st] = r.t;
+      sm.lo[1][st] = r.w_n > 0 ? r.w_lo : INT_MAX;
+      sm.slope2[st] = slope * kLog2e;
+      sm.nref[st] = nref;
+    }
+    soft_sync();
+    if (st == 0) {
+      Range g{sm.seg.e_lo, sm.seg.e_hi, sm.seg.w_lo, sm.seg.w_hi};
+      if (kWeights && !cx.pl.sums) {
+        g.e_lo = sm.seg.e_lo = 0;
+        g.e_hi = sm.seg.e_hi = n_ent;
+      }
+      sm.seg.n_chunks = range_chunks(g, kWeights);
+      sm.seg.units = max(1, sm.seg.n_chunks);
+      sm.seg.c_hi = (g.e_hi + kChunk - 1) / kChunk;
+      sm.seg.nw = !kWeights && g.w_hi >= g.w_lo ? (int)(((int64_t)g.w_hi - g.w_lo) / kChunk) + 1 : 0;
+    }
+    block_sync();
+    const Span sp = span_of(sm.seg, u, cx.u1, tstart);
+    const int units = sm.seg.units, nw = sm.seg.nw;
+    float lsum[kWeights ? 1 : kRows];
+#pragma unroll
+    for (int j = 0; j < (kWeights ? 1 : kRows); ++j) lsum[j] = 0.f;
+
+    for (int i = 0; i < sp.n; ++i) {
+      const int k = sp.k0 + i;
+      const uint32_t cc = c + i;
+      if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)cc;
+      // ---- this thread's key
+      KeyView kv;
+      kv.win = k < nw;
+      kv.kf = 1.f;
+      kv.ff = 0.f;
+      kv.p = 0;
+      int64_t slot = -1;
+      if (kv.win) {
+        kv.p = (int64_t)sm.seg.w_lo + (int64_t)k * kChunk + key;
+        kv.ka = kv.p > sm.seg.w_hi ? INT_MAX : (int)kv.p - 1;
+        kv.kb = (int)kv.p;
+        kv.general = true;
+        if (kv.p <= sm.seg.w_hi) {
+          const int f = window_exp(__ldg(a.swa_scales + (int64_t)b * a.swa_cap + (kv.p - sm.seg.pos0)));
+          if (f != 0) {
+            kv.kf = pow2i(f);
+            kv.ff = (float)f;
+          }
+        }
+      } else {
+        const int e0 = (sm.seg.c_hi - 1 - (k - nw)) * kChunk, j = e0 + key;
+        bool have = j >= sm.seg.e_lo && j < sm.seg.e_hi;
+        int page = -1;
+        if (have) page = __ldg(a.page_table + (int64_t)b * a.max_pages + (j >> 6));
+        have = have && page >= 0 && page < a.n_pages;
+        if (have) slot = (int64_t)page * kPage + (j & (kPage - 1));
+        kv.p = a.entry_pos && have ? (int64_t)__ldg(a.entry_pos + slot) : 4 * ((int64_t)j + shift) + 3;
+        kv.ka = have ? j : INT_MAX;
+        kv.kb = (int)min(max(kv.p - 3, (int64_t)INT_MIN), (int64_t)INT_MAX);
+        // uniform over the CTA's threads but for entries behind a bad page, whose warp masks them
+        kv.general = a.cap > 0.f || a.slopes || e0 < sm.seg.all_lo || e0 + kChunk > sm.seg.all_hi ||
+                     __any_sync(0xffffffffu, !have);
+      }
+      const int64_t far = (int64_t)sm.seg.t - kv.p;
+      kv.dist = (float)(far < 0 ? -far : far);
+
+      const bool ok = warp_wait(&sm.s_full, cc & 1, abort);
+      tc::tc_fence_after();
+      if (kWeights) {
+        if (!ok) break;
+        float sum = 0.f;
+#pragma unroll
+        for (int c0 = 0; c0 < kRows; c0 += 16) {
+          float x[16];
+          load_logits<kWeights>(cx, kv, lane_q, c0, x);
+#pragma unroll
+          for (int j4 = 0; j4 < 4; ++j4) {
+            const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
+            sum += (ex2(x[4 * j4] + z.x) + ex2(x[4 * j4 + 1] + z.y)) + (ex2(x[4 * j4 + 2] + z.z) + ex2(x[4 * j4 + 3] + z.w));
+          }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.s_free);
+        const int e0 = (sm.seg.c_hi - 1 - (k - nw)) * kChunk, j = e0 + key;
+        if (cx.pl.sums)
+          cx.pl.sums[(int64_t)tile * cx.pl.sum_stride + j] = slot >= 0 ? sum : 0.f;
+        else if (slot >= 0)
+          a.weight_out[slot] = (a.weight_in ? a.decay * a.weight_in[slot] : 0.f) + sum;
+        continue;
+      }
+      // ---- does a logit outgrow its row's reference?
+      bool above = false;
+      if (ok) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int c0 = 0; c0 < kRows; c0 += 16) {
+          float x[16];
+          load_logits<kWeights>(cx, kv, lane_q, c0, x);
+#pragma unroll
+          for (int j4 = 0; j4 < 4; ++j4) {
+            const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
+            top = fmaxf(top, fmaxf(fmaxf(x[4 * j4] + z.x, x[4 * j4 + 1] + z.y), fmaxf(x[4 * j4 + 2] + z.z, x[4 * j4 + 3] + z.w)));
+          }
+        }
+        above = top > kRescaleLog2;
+      }
+      const bool seen_abort = !ok || *abort != 0;
+      if (soft_or(above || seen_abort)) {
+        if (soft_or(seen_abort)) break;   // (a wait that fails below is met by the next vote)
+#pragma unroll 1
+        for (int c0 = 0; c0 < kRows; c0 += 16) {
+          float x[16];
+          load_logits<kWeights>(cx, kv, lane_q, c0, x);
+          const float mx = reduce16<true>(x, lane);
+          if (lane < 16) sm.red[warp][c0 + lane] = mx;
+        }
+        soft_sync();
+        bool need = false;
+        if (st < kRows) {
+          const float m = fmaxf(fmaxf(sm.red[0][st], sm.red[1][st]), fmaxf(sm.red[2][st], sm.red[3][st]));
+          const float no = sm.nref[st];
+          float al = 1.f;
+          if (m + no > kRescaleLog2) {
+            if (no != kUnset) {
+              al = ex2(-no - m);
+              need = true;
+            }
+            sm.nref[st] = -m;
+          }
+          sm.red[0][st] = al;
+        }
+        if (soft_or(need)) {
+          // O^T *= alpha (column = row of the tile): the value products so far must be done
+          if (cc > 0) warp_wait(&sm.pv_done[3], (cc - 1) & 1, abort);
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < 4 * kRows; c0 += 16) {
+            float o[16];
+            tc::tmem_ld16(cx.tm + kColO + c0 + lane_q, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] *= sm.red[0][(c0 & (kRows - 1)) + j];
+            tc::tmem_st16(cx.tm + kColO + c0 + lane_q, o);
+          }
+          tc::tmem_wait_st();
+#pragma unroll
+          for (int j = 0; j < (kWeights ? 1 : kRows); ++j) lsum[j] *= sm.red[0][j];
+        }
+      }
+      // ---- P = exp2(l - m_ref), rounded to fp16 for the value product
+      if (cc >= 2) warp_wait(&sm.p_free[cc & 1], ((cc >> 1) - 1) & 1, abort);
+      const float pf = pow2i(-(int)kv.ff);   // the normaliser adds p = 2^-f (2^f p)
+      unsigned char* pd = reinterpret_cast<unsigned char*>(sm.p) + (cc & 1) * (kChunk * kRows * 2) + (key >> 3) * 1024 +
+                          (key & 7) * 16;
+#pragma unroll
+      for (int c0 = 0; c0 < (kWeights ? 0 : kRows); c0 += 16) {
+        float x[16];
+        load_logits<kWeights>(cx, kv, lane_q, c0, x);
+        uint32_t pk[8];
+#pragma unroll
+        for (int j4 = 0; j4 < 4; ++j4) {
+          const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
+          const float p0 = ex2(x[4 * j4] + z.x), p1 = ex2(x[4 * j4 + 1] + z.y);
+          const float p2 = ex2(x[4 * j4 + 2] + z.z), p3 = ex2(x[4 * j4 + 3] + z.w);
+          lsum[c0 + 4 * j4] = fmaf(p0, pf, lsum[c0 + 4 * j4]);
+          lsum[c0 + 4 * j4 + 1] = fmaf(p1, pf, lsum[c0 + 4 * j4 + 1]);
+          lsum[c0 + 4 * j4 + 2] = fmaf(p2, pf, lsum[c0 + 4 * j4 + 2]);
+          lsum[c0 + 4 * j4 + 3] = fmaf(p3, pf, lsum[c0 + 4 * j4 + 3]);
+          pk[2 * j4] = f32x2_f16x2(p0, p1);
+          pk[2 * j4 + 1] = f32x2_f16x2(p2, p3);
+        }
+        *reinterpret_cast<uint4*>(pd + (c0 / 8) * 128) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<uint4*>(pd + (c0 / 8 + 1) * 128) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+      }
+      tc::fence_async_smem();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&sm.s_free);
+        tc::mbar_arrive(&sm.p_full);
+      }
+    }
+    if (!kWeights) {
+      // all products of the tile, and the row sums over its keys
+      if (sp.n > 0) warp_wait(&sm.pv_done[3], (c + sp.n - 1) & 1, abort);
+#pragma unroll
+      for (int c0 = 0; c0 < (kWeights ? 0 : kRows); c0 += 16) {
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = lsum[c0 + j];
+        const float s = reduce16<false>(x, lane);
+        if (lane < 16) sm.red[warp][c0 + lane] = s;
+      }
+      soft_sync();
+      if (st < kRows) {
+        const float l = (sm.red[0][st] + sm.red[1][st]) + (sm.red[2][st] + sm.red[3][st]);
+        const float m = sm.nref[st] == kUnset ? -INFINITY : -sm.nref[st];
+        sm.red[0][st] = l;
+        if (sp.first && sp.last) {
+          if (a.lse && r0 + st < rows)
+            a.lse[(int64_t)b * rows + r0 + st] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        } else {
+          float* ml = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats + kRows * kD;
+          ml[st] = m;
+          ml[kRows + st] = l;
+        }
+      }
+    }
+    block_sync();
+    if (*abort) break;
+    c += sp.n;
+    u = min(cx.u1, tstart + units);
+    tstart += units;
+    ++tile;
+  }
+}
+
+template <bool kWeights>
+__device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx, bool issuer) {
+  Smem<kWeights>& sm = cx.sm;
+  volatile int* abort = &sm.abort;
+  constexpr uint32_t kIdS = tc::idesc_f16(128, kRows, 0, 0, 0);   // K-major A (tensor memory) and B
+  constexpr uint32_t kIdO = tc::idesc_f16(128, kRows, 0, 1, 1);   // MN-major A and B
+  const uint64_t dq = tc::smem_desc(tc::smem_addr(sm.q), 128, 8192);
+  const uint64_t dv = tc::smem_desc(tc::smem_addr(sm.v), 8192, 128);
+  const uint64_t dp = tc::smem_desc(tc::smem_addr(sm.p), 1024, 128);
+  uint32_t c = 0;
+  int64_t u = cx.u0, tstart = cx.tstart;
+  while (u < cx.u1) {
+    block_sync();
+    block_sync();
+    const Span sp = span_of(sm.seg, u, cx.u1, tstart);
+    const int units = sm.seg.units;
+    if (issuer) {
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        for (uint32_t i = 0; i < (1u << 24); ++i) {
+          if (tc::mbar_try_wait(bar, parity)) return true;
+          if ((i & 255) == 255 && *abort) return false;
+        }
+        *abort = 1;
+        return false;
+      };
+      auto scores = [&](int i) -> bool {
+        const uint32_t cc = c + i;
+        if (cc > 0 && !wait(&sm.s_free, (cc - 1) & 1)) return false;
+        for (uint32_t q = 0; q < 4; ++q) {
+          const uint32_t seq = 4 * cc + q, slot = seq % kRing, use = seq / kRing;
+          if (!wait(&sm.kq_full[slot], use & 1)) return false;
+          tc::tc_fence_after();
+#pragma unroll
+          for (uint32_t ks = 0; ks < 8; ++ks)
+            mma_f16_ta(cx.tm + kColS, cx.tm + kColK + 64 * slot + 8 * ks, dq + (uint64_t)((8 * q + ks) * 16), kIdS,
+                       (q | ks) != 0);
+          tc::mma_commit(&sm.kq_free[slot]);
+        }
+        tc::mma_commit(&sm.s_full);
+        return true;
+      };
+      bool ok = sp.n > 0 && scores(0);
+      for (int i = 0; ok && i < sp.n; ++i) {
+        if (i + 1 < sp.n && !scores(i + 1)) break;
+        if (kWeights) continue;
+        const uint32_t cc = c + i;
+        if (!wait(&sm.p_full, cc & 1)) break;
+        for (int mt = 0; ok && mt < 4; ++mt) {
+          if (!wait(&sm.v_full[mt], cc & 1)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_f16(cx.tm + kColO + 64 * mt, dv + (uint64_t)(mt * 128 + kk * 1024),
+                        dp + (uint64_t)((cc & 1) * (kChunk * kRows * 2 / 16) + kk * 128), kIdO,
+                        (i > 0 || kk > 0) ? 1u : 0u);
+          tc::mma_commit(&sm.pv_done[mt]);
+        }
+        if (ok) tc::mma_commit(&sm.p_free[cc & 1]);
+      }
+    }
+    __syncwarp();
+    block_sync();
+    if (*abort) break;
+    c += sp.n;
+    u = min(cx.u1, tstart + units);
+    tstart += units;
+  }
+}
+
+// Warp 21: the packed pages of the chunks ahead into L2.  Warps 22 and 23: barriers only.
+template <bool kWeights>
+__device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx, bool active) {
+  Smem<kWeights>& sm = cx.sm;
+  const DenseArgs& a = cx.a;
+  volatile int* abort = &sm.abort;
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31;
+  uint32_t c = 0;
+  int64_t u = cx.u0, tstart = cx.tstart;
+  while (u < cx.u1) {
+    block_sync();
+    block_sync();
+    const Span sp = span_of(sm.seg, u, cx.u1, tstart);
+    const int units = sm.seg.units;
+    if (active) {
+      auto request = [&](int i) {
+        const int k = sp.k0 + i;
+        if (i >= sp.n || k < sm.seg.nw || lane >= 4) return;
+        const int lp = (sm.seg.c_hi - 1 - (k - sm.seg.nw)) * (kChunk / kPage) + (lane & 1);
+        if (lp >= a.max_pages || (int64_t)lp * kPage >= sm.seg.e_hi) return;
+        const int page = __ldg(a.page_table + (int64_t)sm.seg.b * a.max_pages + lp);
+        if (page < 0 || page >= a.n_pages) return;
+        const uint32_t bytes = (lane & 2) ? kPage * (kD / 16) : kPage * (kD / 2);
+        const uint8_t* src = ((lane & 2) ? a.kv_scales : a.kv_codes) + (int64_t)page * bytes;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+      };
+      for (int i = 2; i < kAhead; ++i) request(i);
+      for (int i = 0; i + kAhead < sp.n; ++i) {
+        request(i + kAhead);
+        // not a wait on s_full: this warp may fall behind by more than a phase
+        for (uint32_t k = 0; k < (1u << 22); ++k) {
+          if (*reinterpret_cast<volatile int*>(&sm.progress) >= (int)c + i + 1 || *abort) break;
+          __nanosleep(100);
+        }
+        if (*abort) break;
+      }
+    }
+    __syncwarp();
+    block_sync();
+    if (*abort) break;
+    c += sp.n;
+    u = min(cx.u1, tstart + units);
+    tstart += units;
+  }
+}
+
+template <bool kWeights>
+__global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, uint32_t* status) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem<kWeights>& sm = *reinterpret_cast<Smem<kWeights>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(&sm.kq_full[i], 4);
+      tc::mbar_init(&sm.kq_free[i], 1);
+    }
+    tc::mbar_init(&sm.s_full, 1);
+    tc::mbar_init(&sm.s_free, kSoftWarps);
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sm.v_full[i], 4);
+      tc::mbar_init(&sm.pv_done[i], 1);
+    }
+    tc::mbar_init(&sm.p_full, kSoftWarps);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.p_free[i], 1);
+    sm.abort = 0;
+    sm.progress = 0;
+    tc::mbar_fence_init();
+  }
+  if (warp == kDeqWarps + kSoftWarps) tc::tmem_alloc(&sm.tmem, kTmemCols);
+  pdl_wait();
+
+  // ---- this CTA's share of the chunks of all tiles
+  const int tiles = a.B * pl.tiles;
+  int64_t mine = 0, total = 0;
+  for (int t = tid; t < tiles; t += kThreads) mine += tile_units<kWeights>(a, pl, t);
+  const int64_t own = mine;
+  int64_t inc = block_scan(mine, sm.scan, &total);
+  const int64_t ctas = min((int64_t)gridDim.x, total);
+  const int64_t g = blockIdx.x;
+  const int64_t u0 = g < ctas ? total * g / ctas : 0, u1 = g < ctas ? total * (g + 1) / ctas : 0;
+  if (u1 > u0) {
+    int64_t base = 0;
+    for (int t0 = 0; t0 < tiles; t0 += kThreads) {
+      int64_t v = own, all = total;
+      if (tiles > kThreads) {          // (with one batch the first scan holds the answer)
+        v = t0 + tid < tiles ? tile_units<kWeights>(a, pl, t0 + tid) : 0;
+        inc = block_scan(v, sm.scan, &all);
+      }
+      const int64_t start = base + inc - v;
+      if (t0 + tid < tiles && u0 >= start && u0 < start + v) {
+        sm.found_tile = t0 + tid;
+        sm.found_start = start;
+      }
+      base += all;
+      if (u0 < base) break;            // uniform
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tm = sm.tmem;
+  Ctx<kWeights> cx{a, pl, sm, tm, u0, u1, sm.found_tile, sm.found_start, status};
+  if (u1 <= u0) cx.tile = 0;
+  if (!kWeights && tid == 0) pl.cont[g] = (u1 > u0 && cx.tstart < u0) ? cx.tile : -1;
+
+  // ---- roles, each with its own walk over the tiles (every walk meets the same barriers)
+  if (warp < kDeqWarps) {
+    role_dequant<kWeights>(cx);
+  } else if (warp < kDeqWarps + kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    role_softmax<kWeights>(cx);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
+    if (warp == kDeqWarps + kSoftWarps)
+      role_mma<kWeights>(cx, (tid & 31) == 0);
+    else
+      role_prefetch<kWeights>(cx, warp == kDeqWarps + kSoftWarps + 1);
+  }
+  tc::tc_fence_before();
+  block_sync();
+  if (warp == kDeqWarps + kSoftWarps) tc::tmem_dealloc(tm, kTmemCols);
+  if (tid == 0 && sm.abort) raise_status(status, CSA2_STATUS_TIMEOUT);
+}
+
+// Joins the partial results of tiles that several CTAs shared.  blockIdx.x = n-th such
+// tile, blockIdx.y = row; 4 groups of 128 threads (4 channels each) take the partials
+// in turn, and their sums are added in group order.
+constexpr int kMergeGroups = 4;
+__global__ void __launch_bounds__(128 * kMergeGroups) k_dense_merge(DenseArgs a, Plan pl) {
+  __shared__ int s_first, s_count;
+  __shared__ int s_cont[kMaxCtas];
+  __shared__ float s_fac[kMaxCtas + 1];
+  __shared__ float4 s_sum[kMergeGroups][128];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, r = blockIdx.y;
+  for (int g = tid; g < pl.n_ctas; g += blockDim.x) s_cont[g] = pl.cont[g];
+  if (tid == 0) s_first = -1;
+  __syncthreads();
+  if (tid < 32) {   // the n-th CTA that is the first to continue a tile
+    int n = (int)blockIdx.x;
+    for (int g0 = 0; g0 < pl.n_ctas; g0 += 32) {
+      const int g = g0 + tid;
+      const bool head = g > 0 && g < pl.n_ctas && s_cont[g] >= 0 && s_cont[g - 1] != s_cont[g];
+      const uint32_t m = __ballot_sync(0xffffffffu, head);
+      const int k = __popc(m);
+      if (n < k) {
+        if (head && __popc(m & ((1u << tid) - 1)) == n) s_first = g;
+        break;
+      }
+      n -= k;
+    }
+  }
+  __syncthreads();
+  const int first = s_first;
+  if (first < 0) return;
+  const int tile = s_cont[first];
+  const int b = tile / pl.tiles;
+  const int64_t rows = (int64_t)a.Tq * a.Hq;
+  const int64_t row = (int64_t)(pl.tile0 + tile % pl.tiles) * kRows + r;
+  if (row >= rows) return;
+  // partial 0: the CTA before (its last share), then every CTA that continues the tile
+  if (tid < 32) {
+    int count = 0;
+    for (int g0 = first; g0 < pl.n_ctas; g0 += 32) {
+      const bool in = g0 + tid < pl.n_ctas && s_cont[g0 + tid] == tile;
+      const int k = __popc(__ballot_sync(0xffffffffu, in));
+      count += k;
+      if (k < 32) break;
+    }
+    if (tid == 0) s_count = count + 1;
+    __syncwarp();
+    float M = -INFINITY, L = 0.f;
+    for (int q = tid; q <= count; q += 32) {
+      const float* ml = pl.parts + (int64_t)(q == 0 ? 2 * (first - 1) + 1 : 2 * (first - 1 + q)) * kPartFloats + kRows * kD;
+      M = fmaxf(M, ml[r]);
+    }
+    M = warp_max(M);
+    for (int q = tid; q <= count; q += 32) {
+      const float* ml = pl.parts + (int64_t)(q == 0 ? 2 * (first - 1) + 1 : 2 * (first - 1 + q)) * kPartFloats + kRows * kD;
+      const float f = ml[r] == -INFINITY ? 0.f : ex2(ml[r] - M);
+      s_fac[q] = f;
+      L += f * ml[kRows + r];
+    }
+    L = warp_sum(L);
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    for (int q = tid; q <= count; q += 32) s_fac[q] *= inv;
+    if (a.lse && tid == 0) a.lse[(int64_t)b * rows + row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  }
+  __syncthreads();
+  const int n = s_count, grp = tid >> 7, c4 = tid & 127;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int q = grp; q < n; q += kMergeGroups) {
+    const float* part = pl.parts + (int64_t)(q == 0 ? 2 * (first - 1) + 1 : 2 * (first - 1 + q)) * kPartFloats;
+    const float4 v = *reinterpret_cast<const float4*>(part + r * kD + 4 * c4);
+    const float f = s_fac[q];
+    acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y); acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+  }
+  s_sum[grp][c4] = acc;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int k = 1; k < kMergeGroups; ++k) {
+      const float4 v = s_sum[k][c4];
+      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(a.O + ((int64_t)b * rows + row) * kD + 4 * c4) =
+        make_uint2(f32x2_bf16x2(acc.x, acc.y), f32x2_bf16x2(acc.z, acc.w));
+  }
+}
+
+// weight_out[j] = (first slab: decay * weight_in[j], later ones: weight_out[j]) + the
+// sums of the slab's tiles, in tile order.
+__global__ void __launch_bounds__(256) k_weights_sum(DenseArgs a, Plan pl, int first_slab, uint32_t* status) {
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.y;
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  if (j >= dense_entries(a, b)) return;
+  const int64_t slot = entry_slot(a.page_table, a.max_pages, a.n_pages, b, j, first_slab ? status : nullptr);
+  if (slot < 0) return;
+  float w = first_slab ? (a.weight_in ? a.decay * a.weight_in[slot] : 0.f) : a.weight_out[slot];
+  for (int t = 0; t < pl.tiles; ++t) {
+    const int64_t tile = (int64_t)b * pl.tiles + t;
+    const int2 rg = pl.ranges[tile];
+    if (j >= rg.x && j < rg.y) w += pl.sums[tile * pl.sum_stride + j];
+  }
+  a.weight_out[slot] = w;
+}
+// The entries whose sums a tile writes (whole chunks).
+__global__ void __launch_bounds__(128) k_weights_ranges(DenseArgs a, Plan pl) {
+  pdl_trigger();
+  pdl_wait();
+  const int tile = blockIdx.x * 128 + threadIdx.x;
+  if (tile >= a.B * pl.tiles) return;
+  const int b = tile / pl.tiles;
+  const int r0 = (pl.tile0 + tile % pl.tiles) * kRows;
+  const int64_t rows = (int64_t)a.Tq * a.Hq;
+  int lo = INT_MAX, hi = 0;
+  if (r0 < rows) {
+    const int n_ent = dense_entries(a, b);
+    const int64_t shift = dense_shift(a, b);
+    const int i1 = (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
+    for (int i = r0 / a.Hq; i <= i1; ++i) {
+      const DenseRow r = dense_row(a, b, i, n_ent, shift, 0);
+      const int f = dense_first(a, r.doc, shift);
+      if (r.nv > f) {
+        lo = min(lo, f);
+        hi = max(hi, r.nv);
+      }
+    }
+  }
+  pl.ranges[tile] = hi > lo ? make_int2(lo / kChunk * kChunk, (hi + kChunk - 1) / kChunk * kChunk) : make_int2(0, 0);
+}
+
+int tiles_of(const csa2_dims* dm) { return (int)(((int64_t)dm->Tq * dm->Hq + kRows - 1) / kRows); }
+
+// Chunks that a sequence's tile can have.
+int64_t max_chunks(int max_entries, int W, int64_t tq) {
+  return ((int64_t)max_entries + kChunk - 1) / kChunk + ((int64_t)W + tq + kChunk - 1) / kChunk + 2;
+}
+
+cudaError_t device_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e;
+}
+
+// The register split adds up to what the block is launched with; a build whose
+// kernel has fewer registers per thread must not run it (its wait would not end).
+template <bool kWeights>
+cudaError_t prepare_kernel() {
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, k_dense_tc<kWeights>);
+  if (e != cudaSuccess) return e;
+  static_assert(4 * kRegsLaunch + kRegsSoft + kRegsMisc <= 6 * kRegsLaunch, "register split");
+  if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(k_dense_tc<kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(Smem<kWeights>));
+}
+
+// Sums of the weights' tiles: at most this many bytes per slab of tiles.
+constexpr size_t kSumBytes = (size_t)256 << 20;
+
+int slab_tiles(const csa2_dims* dm, int max_entries, int64_t* stride) {
+  *stride = ((int64_t)max_entries + kChunk - 1) / kChunk * kChunk;
+  const int64_t per = std::max<int64_t>(1, dm->B) * *stride * 4;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(tiles_of(dm), (int64_t)kSumBytes / std::max<int64_t>(1, per)));
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+bool dense_tc_supported(const csa2_dims* dm) { return dm->d == kD; }
+
+size_t dense_attn_workspace_bytes(const csa2_dims* dm, int max_entries) {
+  // two slots per CTA, and never more CTAs than chunks
+  const int64_t units = (int64_t)dm->B * tiles_of(dm) * max_chunks(max_entries, dm->W, dm->swa_cap);
+  const int64_t ctas = std::min<int64_t>(kMaxCtas, std::max<int64_t>(1, units));
+  return up((size_t)kMaxCtas * 4) + (size_t)ctas * 2 * kPartFloats * sizeof(float);
+}
+
+cudaError_t launch_dense_attn_tc(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s) {
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e == cudaSuccess) e = prepare_kernel<false>();
+  if (e != cudaSuccess) return e;
+  Plan pl = {};
+  pl.tiles_per_seq = pl.tiles = tiles_of(dm);
+  const int64_t tiles = (int64_t)a.B * pl.tiles;
+  if (tiles >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  const int64_t units = tiles * max_chunks(a.max_entries, a.W, a.swa_cap);
+  pl.n_ctas = (int)std::min<int64_t>(std::min(sms, kMaxCtas), std::max<int64_t>(1, units));
+  pl.cont = static_cast<int32_t*>(ws);
+  pl.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + up((size_t)kMaxCtas * 4));
+  e = launch_step(k_dense_tc<false>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<false>), s, a, pl, status_word());
+  if (e != cudaSuccess || pl.n_ctas == 1) return e;
+  const unsigned shared = (unsigned)std::min<int64_t>(tiles, pl.n_ctas - 1);
+  return launch_step(k_dense_merge, dim3(shared, kRows), dim3(128 * kMergeGroups), 0, s, a, pl);
+}
+
+size_t entry_weights_workspace_bytes(const csa2_dims* dm, int max_entries) {
+  if (tiles_of(dm) <= 1) return 0;
+  int64_t stride;
+  const int tiles = slab_tiles(dm, max_entries, &stride);
+  return up((size_t)dm->B * tiles * sizeof(int2)) + (size_t)dm->B * tiles * stride * sizeof(float);
+}
+
+cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s) {
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e == cudaSuccess) e = prepare_kernel<true>();
+  if (e != cudaSuccess) return e;
+  const int all = tiles_of(dm);
+  Plan pl = {};
+  pl.tiles_per_seq = all;
+  if ((int64_t)a.B * all >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  const int slab = all <= 1 ? 1 : slab_tiles(dm, a.max_entries, &pl.sum_stride);
+  for (int t0 = 0; t0 < all; t0 += slab) {
+    pl.tile0 = t0;
+    pl.tiles = std::min(slab, all - t0);
+    const int64_t units = (int64_t)a.B * pl.tiles * max_chunks(a.max_entries, 0, 0);
+    pl.n_ctas = (int)std::min<int64_t>(std::min(sms, kMaxCtas), std::max<int64_t>(1, units));
+    if (all > 1) {
+      pl.ranges = static_cast<int2*>(ws);
+      pl.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + up((size_t)a.B * slab * sizeof(int2)));
+      e = launch_step(k_weights_ranges, dim3((unsigned)(((int64_t)a.B * pl.tiles + 127) / 128)), dim3(128), 0, s, a, pl);
+      if (e != cudaSuccess) return e;
+    }
+    e = launch_step(k_dense_tc<true>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<true>), s, a, pl, status_word());
+    if (e != cudaSuccess) return e;
+    if (all > 1) {
+      e = launch_step(k_weights_sum, dim3((unsigned)((a.max_entries + 255) / 256), (unsigned)a.B), dim3(256), 0, s, a, pl,
+                      (int)(t0 == 0), status_word());
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace csa2

@@ -254,9 +254,16 @@ struct DenseArgs {
   float* weight_out;          // weights: [n_pages][64]
   float decay;
 };
-// ---- dense_attn.cu: plain kernels for d = 64 (and any shape the others do not take)
+// ---- dense_attn.cu: plain kernels (d = 64)
 cudaError_t launch_dense_attn_plain(const DenseArgs& a, cudaStream_t s);
 cudaError_t launch_entry_weights_plain(const DenseArgs& a, cudaStream_t s);
+
+// ---- dense_attn_tc.cu: tcgen05 kernels for d = 512
+bool dense_tc_supported(const csa2_dims* dm);
+size_t dense_attn_workspace_bytes(const csa2_dims* dm, int max_entries);
+cudaError_t launch_dense_attn_tc(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s);
+size_t entry_weights_workspace_bytes(const csa2_dims* dm, int max_entries);
+cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s);
 
 // ---- evict.cu ---------------------------------------------------------------------
 struct EvictArgs {

@@ -49,6 +49,7 @@ CASES = {
     "prefix": dict(B=2, Tq=64, Hq=8, lens=(40,), q_pos=[list(range(100, 164))] * 2, prefix=[130, 3], W=16),
     "prefix_slopes": dict(Tq=8, Hq=64, lens=(64,), q_pos=[list(range(200, 208))], prefix=[256], slopes=[0.02]),
     "shifted": dict(B=2, Tq=3, lens=(200, 333), shift=[50, 7]),
+    "shifted_docs": dict(Tq=2, Hq=40, lens=(300,), shift=[50], docs=[[333, 800]], W=8),
     "scrambled": dict(B=2, Tq=3, Hq=40, lens=(200, 333), shift=[50, 1], scrambled=True, slopes=[0.01, 0.2]),
     "scrambled_docs": dict(Tq=2, Hq=64, lens=(260,), shift=[30], scrambled=True, docs=[[300, 801]], W=8),
     "tokens_far_apart": dict(Tq=4, Hq=8, lens=(600,), q_pos=[[40, 700, 1500, 2403]], W=16),
