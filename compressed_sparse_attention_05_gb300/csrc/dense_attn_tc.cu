@@ -92,7 +92,7 @@ struct Smem {
     int qexp[kSoftWarps][kRows];    // [1]: largest exponent field of each row of Q, before the products
     int64_t scan[kThreads / 32];    // before the first tile
   };
-  uint64_t kq_full[kRing], kq_free[kRing], s_full, s_free, v_full[4], pv_done[4], p_full, p_free[2];
+  uint64_t kq_full[4], kq_free[4], s_full, s_free, v_full[4], pv_done[4], p_full, p_free[2];
   Segment seg;
   int64_t found_start;
   int found_tile;
@@ -428,8 +428,12 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
       const bool window = k < nw;
       KeyRef w{nullptr, nullptr, 0.f};
       if (window) w = key_ref<kWeights>(cx, k, key, qd, false);
-      const uint32_t seq = 4u * (c + i) + qd, slot = seq % kRing, use = seq / kRing;
-      if (use > 0 && !warp_wait(&sm.kq_free[slot], (use - 1) & 1, abort)) return false;
+      // quarter qd of chunk cc is number 4 cc + qd in the ring; its slot last held the quarter
+      // three before.  The barriers belong to quarters, not slots, so that every group of warps
+      // waits for consecutive phases of one barrier.
+      const uint32_t cc = c + i, slot = (4u * cc + qd) % kRing;
+      const uint32_t pq = (qd + 1) & 3, pc = qd == 3 ? cc : cc - 1;
+      if ((cc > 0 || qd == 3) && !warp_wait(&sm.kq_free[pq], pc & 1, abort)) return false;
       tc::tc_fence_after();
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -441,7 +445,7 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
       tc::tmem_wait_st();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.kq_full[slot]);
+      if (lane == 0) tc::mbar_arrive(&sm.kq_full[qd]);
       return true;
     };
     // V of a chunk: the same channels into the shared-memory tile
@@ -875,14 +879,14 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx, bool issuer) {
         const uint32_t cc = c + i;
         if (cc > 0 && !wait(&sm.s_free, (cc - 1) & 1)) return false;
         for (uint32_t q = 0; q < 4; ++q) {
-          const uint32_t seq = 4 * cc + q, slot = seq % kRing, use = seq / kRing;
-          if (!wait(&sm.kq_full[slot], use & 1)) return false;
+          const uint32_t slot = (4 * cc + q) % kRing;
+          if (!wait(&sm.kq_full[q], cc & 1)) return false;
           tc::tc_fence_after();
 #pragma unroll
           for (uint32_t ks = 0; ks < 8; ++ks)
             mma_f16_ta(cx.tm + kColS, cx.tm + kColK + 64 * slot + 8 * ks, dq + (uint64_t)((8 * q + ks) * 16), kIdS,
                        (q | ks) != 0);
-          tc::mma_commit(&sm.kq_free[slot]);
+          tc::mma_commit(&sm.kq_free[q]);
         }
         tc::mma_commit(&sm.s_full);
         return true;
@@ -972,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   const int tid = threadIdx.x, warp = tid >> 5;
   pdl_trigger();
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sm.kq_full[i], 4);
       tc::mbar_init(&sm.kq_free[i], 1);
     }
