@@ -15,22 +15,22 @@
 //   S^T [128 keys x 64 rows]  = K [128 x 512] . Q^T        (32 MMAs, k = 16 channels)
 //   O^T [512 dims x 64 rows] += V^T [512 x 128] . P^T      (4 M-tiles x 8 MMAs, k = 16 keys)
 //
-// Two copies of the dequantised chunk keep the two products apart: the score
-// product reads K as an A operand in tensor memory (a ring of three 128-channel
-// quarters), the value product reads V from shared memory.  So S of the next chunk
-// runs while the softmax of this one does, and the shared-memory copy is only
-// rewritten quarter by quarter behind the value product.  S from tensor memory also
-// leaves shared memory, the narrowest path of this shape (N = 64), to the value
-// product.
+// Shared memory holds one dequantised chunk (128 KB) beside Q (64 KB) and P, so with
+// both products reading it the softmax would stand between them.  Every second chunk
+// therefore has its K as an A operand in tensor memory as well (two 128-channel
+// quarters at a time): its scores need no room in shared memory and run while the
+// softmax of the chunk before does.  (An MMA of this shape takes 58 cycles with A in
+// shared memory K-major, 52 MN-major, 87 with A in tensor memory, whatever N up to 64,
+// so all chunks that way would cost 26% more, every second one 13%.)
 //
 // Work is split over the SMs by chunks, not by tiles: every CTA computes the chunk
 // count of all tiles (lengths live on the device), takes an equal contiguous share,
 // and walks the tiles in it.  A tile that falls to several CTAs leaves partial
 // (m, l, O) in the workspace and k_dense_merge joins them in order.
 //
-// Roles (768 threads): warps 0-15 dequantise (thread = one key x 128 channels),
-// warps 16-19 do the softmax (thread = one key x 64 rows), warp 20 issues the MMAs,
-// warp 21 requests pages into L2 ahead.  Operand ranges as in attention_tc.cu (R11's
+// Roles (640 threads): warps 0-7 dequantise (thread = one key x 256 channels), warps
+// 8-15 do the softmax (thread = one key x 32 rows), warp 16 issues the MMAs, warp 17
+// requests pages into L2 ahead.  Operand ranges as in attention_tc.cu (R11's
 // powers of two for Q rows and window rows); P is rounded to fp16, the normaliser
 // sums the unrounded fp32 P, everything else is fp32.
 #include <cuda_fp16.h>
@@ -47,18 +47,17 @@ namespace {
 constexpr int kD = 512;
 constexpr int kRows = 64;                 // rows of a tile (N of both products)
 constexpr int kChunk = 128;               // keys of a chunk
-constexpr int kDeqWarps = 16, kSoftWarps = 4;
+constexpr int kDeqWarps = 8, kSoftWarps = 8;
 constexpr int kDeqThreads = kDeqWarps * 32;
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kThreads = 768;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
+constexpr int kThreads = 640;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
 constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
-// registers per thread after the split: 4 x 80 + 120 + 40 = 6 x 80 per warpgroup set
-constexpr int kRegsLaunch = 80, kRegsSoft = 120, kRegsMisc = 40;
+// registers per thread after the split of the five warpgroups: 2 x 88 + 2 x 128 + 48 = 5 x 96
+constexpr int kRegsLaunch = 96, kRegsDeq = 88, kRegsSoft = 128, kRegsMisc = 48;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;             // O^T: four M-tiles of 64 columns
-constexpr uint32_t kColS = 256;           // S^T: 64 columns
-constexpr uint32_t kColK = 320;           // K ring: three quarters of 64 columns (128 channels of fp16)
-constexpr int kRing = 3;
+constexpr uint32_t kColS = 256;           // S^T: two buffers of 64 columns
+constexpr uint32_t kColK = 384;           // K of odd chunks: two quarters of 64 columns (128 channels of fp16 each)
 constexpr float kRescaleLog2 = 8.f;       // a reference maximum moves only beyond this growth
 constexpr float kUnset = 3e38f;           // -m_ref of a row without keys: any finite logit outgrows it, -inf stays -inf
 constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, then m and l
@@ -68,8 +67,8 @@ constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, then m and l
 //   V [key][dim]: (k/8)*8192 + (d/8)*128 + (k%8)*16 + (d%8)*2
 //   P [key][row]: (k/8)*1024 + (r/8)*128 + (k%8)*16 + (r%8)*2
 struct Segment {            // what the roles need to know of the current tile
-  int b, nw, c_hi, units;   // window chunks; entry chunks end at c_hi; units = max(1, chunks)
-  int n_chunks;
+  int b, nw, c_hi;          // window chunks; entry chunks end at c_hi
+  int n_chunks;             // (a tile without chunks still counts as one unit of work)
   int e_lo, e_hi;           // entries any row of the tile sees
   int w_lo, w_hi;           // window rows any row sees (raw positions, inclusive)
   int all_lo, all_hi;       // entries every row sees
@@ -79,7 +78,7 @@ struct Segment {            // what the roles need to know of the current tile
 template <bool kWeights>
 struct Smem {
   uint16_t q[kRows * kD];
-  uint16_t v[kWeights ? 8 : kChunk * kD];
+  uint16_t v[kChunk * kD];
   uint16_t p[kWeights ? 8 : 2 * kChunk * kRows];
   float mult[kRows];        // logit multiplier: softmax scale * log2(e) * 2^e_r
   float nref[kRows];        // attention: -m_ref (kUnset before the row's first key); weights: -lse * log2(e)
@@ -88,14 +87,18 @@ struct Smem {
   // at position p if p - 1 < hi[1] (the row's own position) and p >= lo[1]
   int hi[2][kRows], lo[2][kRows];
   union {
-    float red[kSoftWarps][kRows];   // per-warp maxima / sums of a row over the keys; [0] also: see below
-    int qexp[kSoftWarps][kRows];    // [1]: largest exponent field of each row of Q, before the products
-    int64_t scan[kThreads / 32];    // before the first tile
+    float red[4][kRows];            // per-lane-quarter maxima / sums of a row over the keys; [0] also: see below
+    int qexp[4][kRows];             // [1]: largest exponent field of each row of Q, before the products
+    struct {                        // before the first tile
+      int64_t scan[kThreads / 32];
+      int64_t found_start;
+      int found_tile;
+    };
   };
-  uint64_t kq_full[4], kq_free[4], s_full, s_free, v_full[4], pv_done[4], p_full, p_free[2];
+  uint64_t kq_full[4], kq_free[4];  // quarters of an odd chunk's K in tensor memory
+  uint64_t v_full[4], pv_done[4];   // quarters of the shared-memory tile (weights: free again after the scores)
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
   Segment seg;
-  int64_t found_start;
-  int found_tile;
   uint32_t tmem;
   int abort;
   int progress;             // chunks whose softmax has begun (paces the L2 requests)
@@ -105,7 +108,6 @@ struct Smem {
 static_assert(sizeof(Smem<false>) <= 232448, "shared memory of the attention kernel");
 
 struct Plan {
-  int tiles_per_seq;        // of the whole call
   int tile0, tiles;         // tiles [tile0, tile0 + tiles) of every sequence are this launch's
   int n_ctas;
   float* parts;             // attention: partial results, kPartFloats per slot, two slots per CTA
@@ -118,14 +120,30 @@ struct Plan {
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory"); }
 __device__ __forceinline__ void deq_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kDeqThreads) : "memory"); }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
-__device__ __forceinline__ bool soft_or(bool v) {
+// The 128 threads of one half of the softmax warps (32 rows).
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(3 + half) : "memory"); }
+__device__ __forceinline__ bool half_or(int half, bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((uint32_t)v), "n"(kSoftThreads)
+      : "r"((uint32_t)v), "r"(3 + half)
       : "memory");
   return r != 0;
+}
+// 32 lanes x 32 columns: thread i of the warp gets lane (base + i).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Bounded wait of a whole warp; on time-out the CTA's abort flag is raised.
@@ -255,12 +273,10 @@ __device__ __forceinline__ void dequant32(const Packed& k, int i, uint32_t (&o)[
   const uint32_t g0 = prmt(s, s, 0x1010u), g1 = prmt(s, s, 0x3232u);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t c = word_of(k.c[i], j);
     const uint32_t g = j < 2 ? g0 : g1;
-    o[4 * j] = hmul2(e2m1x2_f16x2(c & 0xFFu), g);   // exact: <= 6 significant bits
-    o[4 * j + 1] = hmul2(e2m1x2_f16x2((c >> 8) & 0xFFu), g);
-    o[4 * j + 2] = hmul2(e2m1x2_f16x2((c >> 16) & 0xFFu), g);
-    o[4 * j + 3] = hmul2(e2m1x2_f16x2(c >> 24), g);
+    e2m1x8_f16x8(word_of(k.c[i], j), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[4 * j + x] = hmul2(o[4 * j + x], g);   // exact: <= 6 significant bits
   }
 }
 
@@ -270,71 +286,74 @@ struct Ctx {
   const Plan& pl;
   Smem<kWeights>& sm;
   uint32_t tm;
-  int64_t u0, u1;          // this CTA's units
+  int u0, u1;              // this CTA's units (a launch has fewer than 2^31)
   int tile;                // first tile and its first unit
-  int64_t tstart;
+  int tstart;
   uint32_t* status;
 };
 
-// One key of a chunk as its dequantising thread needs it.
+// A window row as its dequantising thread needs it (null: no key, zeros).
 struct KeyRef {
-  const uint8_t* codes;    // this thread's first code byte (null: no key, zeros)
-  const uint8_t* scales;
-  float wsc;               // window row: scale * 2^-f
+  const uint8_t* codes;    // the row's first code byte
+  float wsc;               // scale * 2^-f
 };
 
 template <bool kWeights>
-__device__ __forceinline__ KeyRef key_ref(const Ctx<kWeights>& cx, int k, int key, int qd, bool report) {
+__device__ __forceinline__ KeyRef window_ref(const Ctx<kWeights>& cx, int k, int key) {
   const Segment& sg = cx.sm.seg;
-  KeyRef r{nullptr, nullptr, 0.f};
-  if (k < sg.nw) {
-    const int64_t p = (int64_t)sg.w_lo + (int64_t)k * kChunk + key;
-    if (p > sg.w_hi) return r;
-    bool seen = sg.one_t != 0;      // one token: the tile's rows all see its whole window
-    if (!seen)
-      for (int i = 0; i < kRows; ++i) seen |= p >= cx.sm.lo[1][i] && p <= cx.sm.hi[1][i];
-    if (!seen) return r;
-    const int64_t w = (int64_t)sg.b * cx.a.swa_cap + (p - sg.pos0);
-    const float s = __ldg(cx.a.swa_scales + w);
-    r.wsc = s * pow2i(-window_exp(s));
-    r.codes = cx.a.swa_codes + w * kD + 128 * qd;
-    return r;
-  }
-  const int j = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key;
-  if (j < sg.e_lo || j >= sg.e_hi) return r;
-  const int page = __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j >> 6));
-  if (page < 0 || page >= cx.a.n_pages) {
-    if (report) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
-    return r;
-  }
-  const int64_t slot = (int64_t)page * kPage + (j & (kPage - 1));
-  r.codes = cx.a.kv_codes + slot * (kD / 2) + 64 * qd;
-  r.scales = cx.a.kv_scales + slot * (kD / 16) + 8 * qd;
+  KeyRef r{nullptr, 0.f};
+  const int64_t p = (int64_t)sg.w_lo + (int64_t)k * kChunk + key;
+  if (p > sg.w_hi) return r;
+  bool seen = sg.one_t != 0;      // one token: the tile's rows all see its whole window
+  if (!seen)
+    for (int i = 0; i < kRows; ++i) seen |= p >= cx.sm.lo[1][i] && p <= cx.sm.hi[1][i];
+  if (!seen) return r;
+  const int64_t w = (int64_t)sg.b * cx.a.swa_cap + (p - sg.pos0);
+  const float s = __ldg(cx.a.swa_scales + w);
+  r.wsc = s * pow2i(-window_exp(s));
+  r.codes = cx.a.swa_codes + w * kD;
   return r;
 }
 
+// Page-table entry of this thread's key in entry chunk k (-1: a window chunk, or no such entry).
 template <bool kWeights>
-__device__ __forceinline__ void load_packed(const Ctx<kWeights>& cx, int k, int key, int qd, Packed& o) {
-  // no key: zero codes and scales (the channels are then +0); window rows are read where they are used
+__device__ __forceinline__ int page_of(const Ctx<kWeights>& cx, int k, int key, bool exists) {
+  const Segment& sg = cx.sm.seg;
+  if (!exists || k < sg.nw) return -1;
+  const int j = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key;
+  if (j < sg.e_lo || j >= sg.e_hi) return -1;
+  return __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j >> 6));
+}
+
+// Quarter q of a key's packed bytes.  No key, or one behind a bad page: zero codes and
+// scales (the channels are then +0); window rows are read where they are used.
+template <bool kWeights>
+__device__ __forceinline__ void load_packed(const Ctx<kWeights>& cx, int k, int key, int q, int page, Packed& o) {
+  const Segment& sg = cx.sm.seg;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o.c[i] = make_uint4(0, 0, 0, 0);
   o.s = make_uint2(0, 0);
-  if (k < cx.sm.seg.nw) return;
-  const KeyRef r = key_ref<kWeights>(cx, k, key, qd, qd == 0);
-  if (!r.codes) return;
+  if (k < sg.nw) return;
+  const int j = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key;
+  if (j < sg.e_lo || j >= sg.e_hi) return;
+  if (page < 0 || page >= cx.a.n_pages) {
+    if (q == 0) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
+    return;
+  }
+  const int64_t slot = (int64_t)page * kPage + (j & (kPage - 1));
+  const uint4* codes = reinterpret_cast<const uint4*>(cx.a.kv_codes + slot * (kD / 2) + 64 * q);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o.c[i] = __ldg(reinterpret_cast<const uint4*>(r.codes) + i);
-  o.s = __ldg(reinterpret_cast<const uint2*>(r.scales));
+  for (int i = 0; i < 4; ++i) o.c[i] = __ldg(codes + i);
+  o.s = __ldg(reinterpret_cast<const uint2*>(cx.a.kv_scales + slot * (kD / 16) + 8 * q));
 }
 
-// Piece i (32 channels) of the thread's key, from the packed registers or the window row.
-template <bool kWeights>
-__device__ __forceinline__ void piece(const Packed& pk, const KeyRef& w, bool window, int i, uint32_t (&o)[16]) {
+// Channels 128 q + 32 p .. +31 of a key, from its packed registers or the window row.
+__device__ __forceinline__ void piece(const Packed& pk, const KeyRef& w, bool window, int q, int p, uint32_t (&o)[16]) {
   if (window) {   // uniform over the warp
     uint4 c0 = make_uint4(0, 0, 0, 0), c1 = c0;
     if (w.codes) {
-      c0 = __ldg(reinterpret_cast<const uint4*>(w.codes) + 2 * i);
-      c1 = __ldg(reinterpret_cast<const uint4*>(w.codes) + 2 * i + 1);
+      c0 = __ldg(reinterpret_cast<const uint4*>(w.codes + 128 * q) + 2 * p);
+      c1 = __ldg(reinterpret_cast<const uint4*>(w.codes + 128 * q) + 2 * p + 1);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -343,7 +362,7 @@ __device__ __forceinline__ void piece(const Packed& pk, const KeyRef& w, bool wi
       o[2 * j + 1] = win2_f16x2(x >> 16, w.wsc);
     }
   } else {
-    dequant32(pk, i, o);
+    dequant32(pk, p, o);
   }
 }
 
@@ -354,14 +373,57 @@ struct Span {
   int k0, n;        // chunks k0 .. k0 + n - 1
   bool first, last; // holds the tile's first / last unit
 };
-__device__ __forceinline__ Span span_of(const Segment& sg, int64_t u, int64_t u1, int64_t tstart) {
+__device__ __forceinline__ Span span_of(const Segment& sg, int u, int u1, int tstart) {
   Span s;
-  const int64_t end = min(u1, tstart + sg.units);
-  s.k0 = (int)(u - tstart);
-  s.n = min((int)(end - u), max(0, sg.n_chunks - s.k0));
+  const int units = max(1, sg.n_chunks);
+  const int end = min(u1, tstart + units);
+  s.k0 = u - tstart;
+  s.n = min(end - u, max(0, sg.n_chunks - s.k0));
   s.first = u == tstart;
-  s.last = end == tstart + sg.units;
+  s.last = end == tstart + units;
   return s;
+}
+
+// Counters that run through all tiles of a CTA: chunks, and those at even and odd places
+// of their tile (the two S and P buffers).  Phase k of a barrier is its k-th use.
+struct Count {
+  uint32_t all = 0, even = 0, odd = 0;
+  __device__ __forceinline__ void add(int n) {
+    all += n;
+    even += (n + 1) / 2;
+    odd += n / 2;
+  }
+  __device__ __forceinline__ uint32_t phase(int i) const { return ((i & 1) ? odd : even) + i / 2; }
+};
+
+// O^T of the finished tile from tensor memory: M-tile mt, this warp's lanes (dims), all rows.
+template <bool kWeights>
+__device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp, int tile, int mt, int lq, int lane) {
+  const DenseArgs& a = cx.a;
+  const int b = tile / cx.pl.tiles;
+  const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
+  const int64_t rows = (int64_t)a.Tq * a.Hq;
+  const int dim = 128 * mt + 32 * lq + lane;
+  const bool whole = sp.first && sp.last;
+  float* part = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kRows; c0 += 16) {
+    float o[16];
+    tc::tmem_ld16(cx.tm + kColO + 64 * mt + c0 + ((uint32_t)(32 * lq) << 16), o);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int r = c0 + j;
+      const float x = sp.n > 0 ? o[j] : 0.f;   // (a tile without keys has no products)
+      if (!whole)
+        part[r * kD + dim] = x;
+      else if (r0 + r < rows) {
+        const float l = cx.sm.red[0][r];
+        a.O[((int64_t)b * rows + r0 + r) * kD + dim] = (uint16_t)(f32x2_bf16x2(l > 0.f ? x * (1.f / l) : 0.f, 0.f) & 0xFFFFu);
+      }
+    }
+  }
+  tc::tc_fence_before();
 }
 
 template <bool kWeights>
@@ -369,211 +431,209 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int key = 32 * (warp & 3) + lane, qd = warp >> 2;
-  const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
+  const int lq = warp & 3, half = warp >> 2;     // lane quarter; quarters 2 half and 2 half + 1 of the channels
+  const int key = 32 * lq + lane;
+  const uint32_t lane_q = (uint32_t)(32 * lq) << 16;
   volatile int* abort = &sm.abort;
-  uint32_t c = 0;                       // chunks so far
+  Count c;
   int tile = cx.tile;
-  int64_t u = cx.u0, tstart = cx.tstart;
+  int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
     block_sync();                       // the previous tile is done
-    // ---- Q rows -> fp16 B operand, row r scaled by 2^-e_r (exact)
+    // ---- Q rows -> fp16 B operand, row r scaled by 2^-e_r (exact); read twice (the second time from L2)
     const int b = tile / cx.pl.tiles;
     const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
     const int64_t rows = (int64_t)a.Tq * a.Hq;
     if (tid < kRows) sm.qexp[1][tid] = 0;
-    uint4 qv[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int h = 8 * r + (tid & 7), c8 = tid >> 3;
-      qv[r] = r0 + h < rows ? __ldg(reinterpret_cast<const uint4*>(a.Q + ((int64_t)b * rows + r0 + h) * kD + c8 * 8))
-                            : make_uint4(0, 0, 0, 0);
-    }
     deq_sync();
+    // thread: row 8 g + tid % 8, channels 8 c8 .. +7 for c8 = tid / 8 and tid / 8 + 32
+    auto q_load = [&](int g, int c8) -> uint4 {
+      const int h = 8 * g + (tid & 7);
+      return r0 + h < rows ? __ldg(reinterpret_cast<const uint4*>(a.Q + ((int64_t)b * rows + r0 + h) * kD + c8 * 8))
+                           : make_uint4(0, 0, 0, 0);
+    };
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int g = 0; g < 8; ++g) {
       uint32_t e = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = word_of(qv[r], j);
-        e = max(e, max((w >> 7) & 0xFFu, (w >> 23) & 0xFFu));
+      for (int x = 0; x < 2; ++x) {
+        const uint4 v = q_load(g, (tid >> 3) + 32 * x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = word_of(v, j);
+          e = max(e, max((w >> 7) & 0xFFu, (w >> 23) & 0xFFu));
+        }
       }
       e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
       e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
-      if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * r + lane], (int)e);
+      if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * g + lane], (int)e);
     }
     deq_sync();
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int h = 8 * r + (tid & 7), c8 = tid >> 3;
-      const float qs = pow2i(-q_head_exp(sm.qexp[1][h]));
-      uint32_t ov[4];
+    for (int g = 0; g < 8; ++g) {
+      const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * g + (tid & 7)]));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = word_of(qv[r], j);
-        ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
+      for (int x = 0; x < 2; ++x) {
+        const int c8 = (tid >> 3) + 32 * x;
+        const uint4 v = q_load(g, c8);
+        uint32_t ov[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = word_of(v, j);
+          ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + g * 8192 + c8 * 128 + (tid & 7) * 16) =
+            make_uint4(ov[0], ov[1], ov[2], ov[3]);
       }
-      *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + (h >> 3) * 8192 + c8 * 128 + (h & 7) * 16) =
-          make_uint4(ov[0], ov[1], ov[2], ov[3]);
     }
     if (tid < kRows) sm.mult[tid] = a.scale * kLog2e * pow2i(q_head_exp(sm.qexp[1][tid]));
     tc::fence_async_smem();
     block_sync();                       // Q, row constants and the tile's chunks are there
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = sm.seg.units, nw = sm.seg.nw;
+    const int units = max(1, sm.seg.n_chunks), nw = sm.seg.nw;
 
-    // K of a chunk: quarter qd of every key into the ring
-    auto put_k = [&](int i, const Packed& pk) -> bool {
-      const int k = sp.k0 + i;
-      const bool window = k < nw;
-      KeyRef w{nullptr, nullptr, 0.f};
-      if (window) w = key_ref<kWeights>(cx, k, key, qd, false);
-      // quarter qd of chunk cc is number 4 cc + qd in the ring; its slot last held the quarter
-      // three before.  The barriers belong to quarters, not slots, so that every group of warps
-      // waits for consecutive phases of one barrier.
-      const uint32_t cc = c + i, slot = (4u * cc + qd) % kRing;
-      const uint32_t pq = (qd + 1) & 3, pc = qd == 3 ? cc : cc - 1;
-      if ((cc > 0 || qd == 3) && !warp_wait(&sm.kq_free[pq], pc & 1, abort)) return false;
-      tc::tc_fence_after();
+    // Packed bytes of this thread's two quarters: of the chunk at hand until its last use, then
+    // of the next one (its page is known by then; the pages' bytes are in L2).
+    Packed pk[2];
+    int page = page_of<kWeights>(cx, sp.k0, key, sp.n > 0);
+    auto load = [&](int i, int x) { load_packed<kWeights>(cx, sp.k0 + i, key, 2 * half + x, page, pk[x]); };
+    // K of an odd chunk: quarters into tensor memory.  Quarter q's slot q % 2 last held quarter
+    // q - 2 of this chunk, or q + 2 of the odd chunk before; the barriers belong to quarters, so
+    // that a warp waits for consecutive phases of each.
+    auto put_k = [&](int i) -> bool {
+      const uint32_t ph = c.phase(i);
+      KeyRef w{nullptr, 0.f};
+      const bool window = sp.k0 + i < nw;
+      if (window) w = window_ref<kWeights>(cx, sp.k0 + i, key);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t o[16];
-        piece<kWeights>(pk, w, window, x, o);
+      for (int x = 0; x < 2; ++x) {
+        const int q = 2 * half + x;
+        if (half == 1) {
+          if (!warp_wait(&sm.kq_free[q - 2], ph & 1, abort)) return false;
+        } else if (ph > 0) {
+          if (!warp_wait(&sm.kq_free[q + 2], (ph - 1) & 1, abort)) return false;
+        }
+        tc::tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint32_t o[16];
+          piece(pk[x], w, window, q, p, o);
+          __syncwarp();
+          tmem_st16u(cx.tm + kColK + 64 * x + 16 * p + lane_q, o);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
         __syncwarp();
-        tmem_st16u(cx.tm + kColK + 64 * slot + 16 * x + lane_q, o);
+        if (lane == 0) tc::mbar_arrive(&sm.kq_full[q]);
       }
-      tc::tmem_wait_st();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.kq_full[qd]);
       return true;
     };
-    // V of a chunk: the same channels into the shared-memory tile
-    auto put_v = [&](int i, const Packed& pk) -> bool {
-      const int k = sp.k0 + i;
-      const bool window = k < nw;
-      KeyRef w{nullptr, nullptr, 0.f};
-      if (window) w = key_ref<kWeights>(cx, k, key, qd, false);
-      if (c + i > 0 && !warp_wait(&sm.pv_done[qd], (c + i - 1) & 1, abort)) return false;
-      unsigned char* dst = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 8192 + 16 * qd * 128 + (key & 7) * 16;
+    // A chunk into the shared-memory tile, quarter by quarter behind the products that read it;
+    // each quarter's registers then take the next chunk's.
+    auto put_v = [&](int i) -> bool {
+      KeyRef w{nullptr, 0.f};
+      const bool window = sp.k0 + i < nw;
+      if (window) w = window_ref<kWeights>(cx, sp.k0 + i, key);
+      const bool more = i + 1 < sp.n;
+      page = page_of<kWeights>(cx, sp.k0 + i + 1, key, more);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t o[16];
-        piece<kWeights>(pk, w, window, x, o);
+      for (int x = 0; x < 2; ++x) {
+        const int q = 2 * half + x;
+        const uint32_t cc = c.all + i;
+        if (cc > 0 && !warp_wait(&sm.pv_done[q], (cc - 1) & 1, abort)) return false;
+        unsigned char* dst = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 8192 + 16 * q * 128 + (key & 7) * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(dst + (4 * x + j) * 128) =
-              make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        for (int p = 0; p < 4; ++p) {
+          uint32_t o[16];
+          piece(pk[x], w, window, q, p, o);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + (4 * p + j) * 128) =
+                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.v_full[q]);
+        if (more) load(i + 1, x);
       }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.v_full[qd]);
       return true;
     };
     if (sp.n > 0) {
-      Packed cur, nxt;
-      load_packed<kWeights>(cx, sp.k0, key, qd, cur);
-      bool ok = put_k(0, cur);
-      if (kWeights) {
-        for (int i = 1; ok && i < sp.n; ++i) {
-          load_packed<kWeights>(cx, sp.k0 + i, key, qd, cur);
-          ok = put_k(i, cur);
-        }
-      } else {
-        if (sp.n > 1) load_packed<kWeights>(cx, sp.k0 + 1, key, qd, nxt);
-        for (int i = 0; ok && i < sp.n; ++i) {
-          if (i + 1 < sp.n) ok = put_k(i + 1, nxt);
-          if (ok) ok = put_v(i, cur);
-          cur = nxt;
-          if (i + 2 < sp.n) load_packed<kWeights>(cx, sp.k0 + i + 2, key, qd, nxt);
-        }
+      load(0, 0);
+      load(0, 1);
+      for (int i = 0; i < sp.n; ++i) {
+        if (!kWeights && (i & 1) && !put_k(i)) break;
+        if (!put_v(i)) break;
       }
     }
     block_sync();                       // the tile's products are complete, l is known
     tc::tc_fence_after();
     if (*abort) break;
-    if (!kWeights) {
-      // ---- O^T from tensor memory: M-tile qd, this warp's lanes (dims), all rows
-      const int dim = 128 * qd + key;
-      const bool whole = sp.first && sp.last;
-      float* part = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats;
-#pragma unroll 1
-      for (int c0 = 0; c0 < kRows; c0 += 16) {
-        float o[16];
-        if (sp.n > 0) {
-          tc::tmem_ld16(cx.tm + kColO + 64 * qd + c0 + lane_q, o);
-          tc::tmem_wait_ld();
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int r = c0 + j;
-          const float x = sp.n > 0 ? o[j] : 0.f;
-          if (!whole)
-            part[r * kD + dim] = x;
-          else if (r0 + r < rows) {
-            const float l = sm.red[0][r];
-            a.O[((int64_t)b * rows + r0 + r) * kD + dim] =
-                (uint16_t)(f32x2_bf16x2(l > 0.f ? x * (1.f / l) : 0.f, 0.f) & 0xFFFFu);
-          }
-        }
-      }
-      tc::tc_fence_before();
-    }
-    c += sp.n;
+    if (!kWeights) drain_o<kWeights>(cx, sp, tile, half, lq, lane);
+    c.add(sp.n);
     u = min(cx.u1, tstart + units);
     tstart += units;
     ++tile;
   }
 }
 
-// Logits (log2 domain, as the value product carries them) of this thread's key for
-// columns c0 .. c0+15, or -inf where the row does not see the key.
+// One key of a chunk as its softmax thread sees it.
 struct KeyView {
   bool general;        // masks, cap, bias or a rescaled window row
-  int ka, kb;          // compared with r_hi and r_lo
+  int ka, kb;          // compared with hi and lo
   int win;             // 1: window row
   float kf, ff;        // window row: 2^f and f
   int64_t p;
   float dist;          // |t - p| when the tile holds one token
 };
+
+// Columns c0 .. c0+31 of this thread's key: the logits in the log2 domain as the value
+// product carries them (-inf where the row does not see the key), plus nref.
 template <bool kWeights>
-__device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyView& kv, uint32_t lane_q, int c0,
-                                            float (&x)[16]) {
+__device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyView& kv, uint32_t taddr, int c0, bool ref,
+                                            float (&x)[32]) {
   const Smem<kWeights>& sm = cx.sm;
-  tc::tmem_ld16(cx.tm + kColS + c0 + lane_q, x);
+  tmem_ld32(taddr, x);
   tc::tmem_wait_ld();
+  if (!kv.general) {
 #pragma unroll
-  for (int j4 = 0; j4 < 4; ++j4) {
-    const float4 m = *reinterpret_cast<const float4*>(&sm.mult[c0 + 4 * j4]);
-    x[4 * j4] *= m.x; x[4 * j4 + 1] *= m.y; x[4 * j4 + 2] *= m.z; x[4 * j4 + 3] *= m.w;
+    for (int j4 = 0; j4 < 8; ++j4) {
+      const float4 m = *reinterpret_cast<const float4*>(&sm.mult[c0 + 4 * j4]);
+      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ref) z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
+      x[4 * j4] = fmaf(x[4 * j4], m.x, z.x);
+      x[4 * j4 + 1] = fmaf(x[4 * j4 + 1], m.y, z.y);
+      x[4 * j4 + 2] = fmaf(x[4 * j4 + 2], m.z, z.z);
+      x[4 * j4 + 3] = fmaf(x[4 * j4 + 3], m.w, z.w);
+    }
+    return;
   }
-  if (!kv.general) return;
-  const float cap2 = cx.a.cap * kLog2e;
-  if (kv.kf != 1.f) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] *= kv.kf;
+  for (int j4 = 0; j4 < 8; ++j4) {
+    const float4 m = *reinterpret_cast<const float4*>(&sm.mult[c0 + 4 * j4]);
+    x[4 * j4] *= m.x * kv.kf; x[4 * j4 + 1] *= m.y * kv.kf; x[4 * j4 + 2] *= m.z * kv.kf; x[4 * j4 + 3] *= m.w * kv.kf;
   }
   if (cx.a.cap > 0.f) {
-    const float inv = 1.f / cap2;
+    const float cap2 = cx.a.cap * kLog2e, inv = 1.f / cap2;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = cap2 * fast_tanh(x[j] * inv);
+    for (int j = 0; j < 32; ++j) x[j] = cap2 * fast_tanh(x[j] * inv);
   }
   if (cx.a.slopes) {
     if (sm.seg.one_t) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = fmaf(-sm.slope2[c0 + j], kv.dist, x[j]);
+      for (int j = 0; j < 32; ++j) x[j] = fmaf(-sm.slope2[c0 + j], kv.dist, x[j]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 32; ++j) {
         const int64_t d = (int64_t)sm.hi[1][c0 + j] - kv.p;
         x[j] = fmaf(-sm.slope2[c0 + j], (float)(d < 0 ? -d : d), x[j]);
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 32; ++j) {
     const bool seen = kv.ka < sm.hi[kv.win][c0 + j] && kv.kb >= sm.lo[kv.win][c0 + j];
-    x[j] = seen ? x[j] + kv.ff : -INFINITY;
+    x[j] = seen ? x[j] + kv.ff + (ref ? sm.nref[c0 + j] : 0.f) : -INFINITY;
   }
 }
 
@@ -582,12 +642,13 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   const int st = threadIdx.x - kDeqThreads, warp = st >> 5, lane = st & 31;
-  const int key = st;                   // thread = key of the chunk = tensor-memory lane
-  const uint32_t lane_q = (uint32_t)(32 * warp) << 16;
+  const int lq = warp & 3, half = warp >> 2;   // lane quarter; attention: rows 32 half .. +31, weights: chunks of that parity
+  const int key = 32 * lq + lane;              // thread = key of the chunk = tensor-memory lane
+  const uint32_t lane_q = (uint32_t)(32 * lq) << 16;
   volatile int* abort = &sm.abort;
-  uint32_t c = 0;
+  Count c;
   int tile = cx.tile;
-  int64_t u = cx.u0, tstart = cx.tstart;
+  int u = cx.u0, tstart = cx.tstart;
   const int64_t rows = (int64_t)a.Tq * a.Hq;
   while (u < cx.u1) {
     block_sync();
@@ -647,28 +708,27 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         g.e_hi = sm.seg.e_hi = n_ent;
       }
       sm.seg.n_chunks = range_chunks(g, kWeights);
-      sm.seg.units = max(1, sm.seg.n_chunks);
       sm.seg.c_hi = (g.e_hi + kChunk - 1) / kChunk;
       sm.seg.nw = !kWeights && g.w_hi >= g.w_lo ? (int)(((int64_t)g.w_hi - g.w_lo) / kChunk) + 1 : 0;
     }
     block_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = sm.seg.units, nw = sm.seg.nw;
-    float lsum[kWeights ? 1 : kRows];
-#pragma unroll
-    for (int j = 0; j < (kWeights ? 1 : kRows); ++j) lsum[j] = 0.f;
+    const int units = max(1, sm.seg.n_chunks), nw = sm.seg.nw;
+    const int e_lo = sm.seg.e_lo, e_hi = sm.seg.e_hi, c_hi = sm.seg.c_hi;
 
-    for (int i = 0; i < sp.n; ++i) {
-      const int k = sp.k0 + i;
-      const uint32_t cc = c + i;
-      if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)cc;
-      // ---- this thread's key
+    // The key of a chunk; its page (and position) are read one chunk ahead.
+    auto entry_of = [&](int i) -> int { return (c_hi - 1 - (sp.k0 + i - nw)) * kChunk + key; };
+    auto page_ahead = [&](int i) -> int { return page_of<kWeights>(cx, sp.k0 + i, key, i < sp.n); };
+    constexpr int kStep = kWeights ? 2 : 1;
+    const int first = kWeights ? half : 0;
+    int page = page_ahead(first);
+    auto view = [&](int i, int64_t* slot) -> KeyView {
       KeyView kv;
+      const int k = sp.k0 + i;
       kv.win = k < nw;
       kv.kf = 1.f;
       kv.ff = 0.f;
-      kv.p = 0;
-      int64_t slot = -1;
+      *slot = -1;
       if (kv.win) {
         kv.p = (int64_t)sm.seg.w_lo + (int64_t)k * kChunk + key;
         kv.ka = kv.p > sm.seg.w_hi ? INT_MAX : (int)kv.p - 1;
@@ -682,149 +742,155 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
           }
         }
       } else {
-        const int e0 = (sm.seg.c_hi - 1 - (k - nw)) * kChunk, j = e0 + key;
-        bool have = j >= sm.seg.e_lo && j < sm.seg.e_hi;
-        int page = -1;
-        if (have) page = __ldg(a.page_table + (int64_t)b * a.max_pages + (j >> 6));
-        have = have && page >= 0 && page < a.n_pages;
-        if (have) slot = (int64_t)page * kPage + (j & (kPage - 1));
-        kv.p = a.entry_pos && have ? (int64_t)__ldg(a.entry_pos + slot) : 4 * ((int64_t)j + shift) + 3;
+        const int j = entry_of(i), e0 = j - key;
+        const bool have = j >= e_lo && j < e_hi && page >= 0 && page < a.n_pages;
+        if (have) *slot = (int64_t)page * kPage + (j & (kPage - 1));
+        kv.p = a.entry_pos && have ? (int64_t)__ldg(a.entry_pos + *slot) : 4 * ((int64_t)j + shift) + 3;
         kv.ka = have ? j : INT_MAX;
         kv.kb = (int)min(max(kv.p - 3, (int64_t)INT_MIN), (int64_t)INT_MAX);
-        // uniform over the CTA's threads but for entries behind a bad page, whose warp masks them
         kv.general = a.cap > 0.f || a.slopes || e0 < sm.seg.all_lo || e0 + kChunk > sm.seg.all_hi ||
                      __any_sync(0xffffffffu, !have);
       }
+      page = page_ahead(i + kStep);
       const int64_t far = (int64_t)sm.seg.t - kv.p;
       kv.dist = (float)(far < 0 ? -far : far);
+      return kv;
+    };
 
-      const bool ok = warp_wait(&sm.s_full, cc & 1, abort);
-      tc::tc_fence_after();
-      if (kWeights) {
-        if (!ok) break;
+    if (kWeights) {
+      for (int i = first; i < sp.n; i += 2) {
+        if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + i);
+        int64_t slot;
+        const KeyView kv = view(i, &slot);
+        const float before = slot >= 0 && !cx.pl.sums && a.weight_in ? a.weight_in[slot] : 0.f;
+        if (!warp_wait(&sm.s_full[i & 1], c.phase(i) & 1, abort)) break;
+        tc::tc_fence_after();
         float sum = 0.f;
 #pragma unroll
-        for (int c0 = 0; c0 < kRows; c0 += 16) {
-          float x[16];
-          load_logits<kWeights>(cx, kv, lane_q, c0, x);
+        for (int c0 = 0; c0 < kRows; c0 += 32) {
+          float x[32];
+          load_logits<kWeights>(cx, kv, cx.tm + kColS + 64 * (i & 1) + c0 + lane_q, c0, true, x);
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j4 = 0; j4 < 4; ++j4) {
-            const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
-            sum += (ex2(x[4 * j4] + z.x) + ex2(x[4 * j4 + 1] + z.y)) + (ex2(x[4 * j4 + 2] + z.z) + ex2(x[4 * j4 + 3] + z.w));
-          }
+          for (int j = 0; j < 32; ++j) s4[j & 3] += ex2(x[j]);
+          sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
         }
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.s_free);
-        const int e0 = (sm.seg.c_hi - 1 - (k - nw)) * kChunk, j = e0 + key;
+        if (lane == 0) tc::mbar_arrive(&sm.s_free[i & 1]);
         if (cx.pl.sums)
-          cx.pl.sums[(int64_t)tile * cx.pl.sum_stride + j] = slot >= 0 ? sum : 0.f;
+          cx.pl.sums[(int64_t)tile * cx.pl.sum_stride + entry_of(i)] = slot >= 0 ? sum : 0.f;
         else if (slot >= 0)
-          a.weight_out[slot] = (a.weight_in ? a.decay * a.weight_in[slot] : 0.f) + sum;
-        continue;
+          a.weight_out[slot] = (a.weight_in ? a.decay * before : 0.f) + sum;
       }
-      // ---- does a logit outgrow its row's reference?
-      bool above = false;
-      if (ok) {
+      if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + sp.n);
+    } else {
+      float lsum[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) lsum[j] = 0.f;
+      const int c0 = 32 * half;
+      for (int i = 0; i < sp.n; ++i) {
+        const int e = i & 1;
+        const uint32_t ph = c.phase(i), ts = cx.tm + kColS + 64 * e + c0 + lane_q;
+        if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + i);
+        int64_t slot;
+        const KeyView kv = view(i, &slot);
+        const bool ok = warp_wait(&sm.s_full[e], ph & 1, abort);
+        tc::tc_fence_after();
+        // ---- logits over the reference, and whether one outgrows it
+        float x[32];
         float top = -INFINITY;
+        if (ok) {
+          load_logits<kWeights>(cx, kv, ts, c0, true, x);
 #pragma unroll
-        for (int c0 = 0; c0 < kRows; c0 += 16) {
-          float x[16];
-          load_logits<kWeights>(cx, kv, lane_q, c0, x);
+          for (int j = 0; j < 32; ++j) top = fmaxf(top, x[j]);
+        }
+        const bool seen_abort = !ok || *abort != 0;
+        if (half_or(half, top > kRescaleLog2 || seen_abort)) {
+          if (half_or(half, seen_abort)) break;   // (a wait that fails below is met by the next vote)
+          load_logits<kWeights>(cx, kv, ts, c0, false, x);
+          // maxima of the half's 32 rows over the 128 keys
 #pragma unroll
-          for (int j4 = 0; j4 < 4; ++j4) {
-            const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
-            top = fmaxf(top, fmaxf(fmaxf(x[4 * j4] + z.x, x[4 * j4 + 1] + z.y), fmaxf(x[4 * j4 + 2] + z.z, x[4 * j4 + 3] + z.w)));
+          for (int q = 0; q < 2; ++q) {
+            float y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = x[16 * q + j];
+            const float mx = reduce16<true>(y, lane);
+            if (lane < 16) sm.red[lq][c0 + 16 * q + lane] = mx;
           }
-        }
-        above = top > kRescaleLog2;
-      }
-      const bool seen_abort = !ok || *abort != 0;
-      if (soft_or(above || seen_abort)) {
-        if (soft_or(seen_abort)) break;   // (a wait that fails below is met by the next vote)
-#pragma unroll 1
-        for (int c0 = 0; c0 < kRows; c0 += 16) {
-          float x[16];
-          load_logits<kWeights>(cx, kv, lane_q, c0, x);
-          const float mx = reduce16<true>(x, lane);
-          if (lane < 16) sm.red[warp][c0 + lane] = mx;
-        }
-        soft_sync();
-        bool need = false;
-        if (st < kRows) {
-          const float m = fmaxf(fmaxf(sm.red[0][st], sm.red[1][st]), fmaxf(sm.red[2][st], sm.red[3][st]));
-          const float no = sm.nref[st];
-          float al = 1.f;
-          if (m + no > kRescaleLog2) {
-            if (no != kUnset) {
-              al = ex2(-no - m);
-              need = true;
+          half_sync(half);
+          bool need = false;
+          if (lq == 0) {
+            const int r = c0 + lane;
+            const float m = fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]), fmaxf(sm.red[2][r], sm.red[3][r]));
+            const float no = sm.nref[r];
+            float al = 1.f;
+            if (m + no > kRescaleLog2) {
+              if (no != kUnset) {
+                al = ex2(-no - m);
+                need = true;
+              }
+              sm.nref[r] = -m;
             }
-            sm.nref[st] = -m;
+            sm.red[0][r] = al;
           }
-          sm.red[0][st] = al;
-        }
-        if (soft_or(need)) {
-          // O^T *= alpha (column = row of the tile): the value products so far must be done
-          if (cc > 0) warp_wait(&sm.pv_done[3], (cc - 1) & 1, abort);
-          tc::tc_fence_after();
+          if (half_or(half, need)) {
+            // O^T *= alpha (column = row of the tile): the value products so far must be done
+            if (c.all + i > 0) warp_wait(&sm.pv_done[3], (c.all + i - 1) & 1, abort);
+            tc::tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < 4 * kRows; c0 += 16) {
-            float o[16];
-            tc::tmem_ld16(cx.tm + kColO + c0 + lane_q, o);
-            tc::tmem_wait_ld();
+            for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll 1
+              for (int q = 0; q < 32; q += 16) {
+                const uint32_t ta = cx.tm + kColO + 64 * mt + c0 + q + lane_q;
+                float o[16];
+                tc::tmem_ld16(ta, o);
+                tc::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] *= sm.red[0][(c0 & (kRows - 1)) + j];
-            tc::tmem_st16(cx.tm + kColO + c0 + lane_q, o);
+                for (int j = 0; j < 16; ++j) o[j] *= sm.red[0][c0 + q + j];
+                tc::tmem_st16(ta, o);
+              }
+            }
+            tc::tmem_wait_st();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) lsum[j] *= sm.red[0][c0 + j];
           }
-          tc::tmem_wait_st();
-#pragma unroll
-          for (int j = 0; j < (kWeights ? 1 : kRows); ++j) lsum[j] *= sm.red[0][j];
+          load_logits<kWeights>(cx, kv, ts, c0, true, x);
+          half_sync(half);                     // red is read; the next vote may come
         }
-      }
-      // ---- P = exp2(l - m_ref), rounded to fp16 for the value product
-      if (cc >= 2) warp_wait(&sm.p_free[cc & 1], ((cc >> 1) - 1) & 1, abort);
-      const float pf = pow2i(-(int)kv.ff);   // the normaliser adds p = 2^-f (2^f p)
-      unsigned char* pd = reinterpret_cast<unsigned char*>(sm.p) + (cc & 1) * (kChunk * kRows * 2) + (key >> 3) * 1024 +
-                          (key & 7) * 16;
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.s_free[e]);
+        // ---- P = exp2(l - m_ref), rounded to fp16 for the value product
+        const float pf = pow2i(-(int)kv.ff);   // the normaliser adds p = 2^-f (2^f p)
+        uint32_t pk[16];
 #pragma unroll
-      for (int c0 = 0; c0 < (kWeights ? 0 : kRows); c0 += 16) {
-        float x[16];
-        load_logits<kWeights>(cx, kv, lane_q, c0, x);
-        uint32_t pk[8];
-#pragma unroll
-        for (int j4 = 0; j4 < 4; ++j4) {
-          const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
-          const float p0 = ex2(x[4 * j4] + z.x), p1 = ex2(x[4 * j4 + 1] + z.y);
-          const float p2 = ex2(x[4 * j4 + 2] + z.z), p3 = ex2(x[4 * j4 + 3] + z.w);
-          lsum[c0 + 4 * j4] = fmaf(p0, pf, lsum[c0 + 4 * j4]);
-          lsum[c0 + 4 * j4 + 1] = fmaf(p1, pf, lsum[c0 + 4 * j4 + 1]);
-          lsum[c0 + 4 * j4 + 2] = fmaf(p2, pf, lsum[c0 + 4 * j4 + 2]);
-          lsum[c0 + 4 * j4 + 3] = fmaf(p3, pf, lsum[c0 + 4 * j4 + 3]);
-          pk[2 * j4] = f32x2_f16x2(p0, p1);
-          pk[2 * j4 + 1] = f32x2_f16x2(p2, p3);
+        for (int j = 0; j < 32; j += 2) {
+          const float p0 = ex2(x[j]), p1 = ex2(x[j + 1]);
+          lsum[j] = fmaf(p0, pf, lsum[j]);
+          lsum[j + 1] = fmaf(p1, pf, lsum[j + 1]);
+          pk[j / 2] = f32x2_f16x2(p0, p1);
         }
-        *reinterpret_cast<uint4*>(pd + (c0 / 8) * 128) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4*>(pd + (c0 / 8 + 1) * 128) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        if (ph > 0) warp_wait(&sm.p_free[e], (ph - 1) & 1, abort);
+        unsigned char* pd = reinterpret_cast<unsigned char*>(sm.p) + e * (kChunk * kRows * 2) + (key >> 3) * 1024 +
+                            (c0 / 8) * 128 + (key & 7) * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(pd + j * 128) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.p_full[e]);
       }
-      tc::fence_async_smem();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(&sm.s_free);
-        tc::mbar_arrive(&sm.p_full);
-      }
-    }
-    if (!kWeights) {
+      if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + sp.n);
       // all products of the tile, and the row sums over its keys
-      if (sp.n > 0) warp_wait(&sm.pv_done[3], (c + sp.n - 1) & 1, abort);
+      if (sp.n > 0) warp_wait(&sm.pv_done[3], (c.all + sp.n - 1) & 1, abort);
 #pragma unroll
-      for (int c0 = 0; c0 < (kWeights ? 0 : kRows); c0 += 16) {
-        float x[16];
+      for (int q = 0; q < 2; ++q) {
+        float y[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = lsum[c0 + j];
-        const float s = reduce16<false>(x, lane);
-        if (lane < 16) sm.red[warp][c0 + lane] = s;
+        for (int j = 0; j < 16; ++j) y[j] = lsum[16 * q + j];
+        const float s = reduce16<false>(y, lane);
+        if (lane < 16) sm.red[lq][c0 + 16 * q + lane] = s;
       }
       soft_sync();
       if (st < kRows) {
@@ -842,30 +908,37 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       }
     }
     block_sync();
+    tc::tc_fence_after();
     if (*abort) break;
-    c += sp.n;
+    if (!kWeights) drain_o<kWeights>(cx, sp, tile, 2 + half, lq, lane);
+    c.add(sp.n);
     u = min(cx.u1, tstart + units);
     tstart += units;
     ++tile;
   }
 }
 
+// Order of the products of a tile's chunks A (even) and B (odd), A' the next even one:
+//   S(A) | S(B) from tensor memory | PV(A) | PV(B) | S(A') ...
+// softmax(A) runs under S(B), softmax(B) under PV(A); B takes A's shared-memory tile quarter
+// by quarter behind PV(A), A' takes B's behind PV(B).
 template <bool kWeights>
 __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx, bool issuer) {
   Smem<kWeights>& sm = cx.sm;
   volatile int* abort = &sm.abort;
-  constexpr uint32_t kIdS = tc::idesc_f16(128, kRows, 0, 0, 0);   // K-major A (tensor memory) and B
+  constexpr uint32_t kIdS = tc::idesc_f16(128, kRows, 0, 0, 0);   // K-major A and B
   constexpr uint32_t kIdO = tc::idesc_f16(128, kRows, 0, 1, 1);   // MN-major A and B
   const uint64_t dq = tc::smem_desc(tc::smem_addr(sm.q), 128, 8192);
+  const uint64_t dk = tc::smem_desc(tc::smem_addr(sm.v), 128, 8192);
   const uint64_t dv = tc::smem_desc(tc::smem_addr(sm.v), 8192, 128);
   const uint64_t dp = tc::smem_desc(tc::smem_addr(sm.p), 1024, 128);
-  uint32_t c = 0;
-  int64_t u = cx.u0, tstart = cx.tstart;
+  Count c;
+  int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
     block_sync();
     block_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = sm.seg.units;
+    const int units = max(1, sm.seg.n_chunks);
     if (issuer) {
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         for (uint32_t i = 0; i < (1u << 24); ++i) {
@@ -876,67 +949,85 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx, bool issuer) {
         return false;
       };
       auto scores = [&](int i) -> bool {
-        const uint32_t cc = c + i;
-        if (cc > 0 && !wait(&sm.s_free, (cc - 1) & 1)) return false;
+        const int e = i & 1;
+        const uint32_t ph = c.phase(i);
+        const uint32_t d = cx.tm + kColS + 64 * e;
+        if (ph > 0 && !wait(&sm.s_free[e], (ph - 1) & 1)) return false;
+#pragma unroll 1
         for (uint32_t q = 0; q < 4; ++q) {
-          const uint32_t slot = (4 * cc + q) % kRing;
-          if (!wait(&sm.kq_full[q], cc & 1)) return false;
-          tc::tc_fence_after();
+          if (kWeights || e == 0) {
+            if (!wait(&sm.v_full[q], (c.all + i) & 1)) return false;
+            tc::tc_fence_after();
 #pragma unroll
-          for (uint32_t ks = 0; ks < 8; ++ks)
-            mma_f16_ta(cx.tm + kColS, cx.tm + kColK + 64 * slot + 8 * ks, dq + (uint64_t)((8 * q + ks) * 16), kIdS,
-                       (q | ks) != 0);
-          tc::mma_commit(&sm.kq_free[q]);
+            for (uint32_t ks = 0; ks < 8; ++ks)
+              tc::mma_f16(d, dk + (uint64_t)((8 * q + ks) * 16), dq + (uint64_t)((8 * q + ks) * 16), kIdS, (q | ks) != 0);
+            if (kWeights) tc::mma_commit(&sm.pv_done[q]);
+          } else {
+            if (!wait(&sm.kq_full[q], ph & 1)) return false;
+            tc::tc_fence_after();
+#pragma unroll
+            for (uint32_t ks = 0; ks < 8; ++ks)
+              mma_f16_ta(d, cx.tm + kColK + 64 * (q & 1) + 8 * ks, dq + (uint64_t)((8 * q + ks) * 16), kIdS, (q | ks) != 0);
+            tc::mma_commit(&sm.kq_free[q]);
+          }
         }
-        tc::mma_commit(&sm.s_full);
+        tc::mma_commit(&sm.s_full[e]);
         return true;
       };
-      bool ok = sp.n > 0 && scores(0);
-      for (int i = 0; ok && i < sp.n; ++i) {
-        if (i + 1 < sp.n && !scores(i + 1)) break;
-        if (kWeights) continue;
-        const uint32_t cc = c + i;
-        if (!wait(&sm.p_full, cc & 1)) break;
-        for (int mt = 0; ok && mt < 4; ++mt) {
-          if (!wait(&sm.v_full[mt], cc & 1)) {
-            ok = false;
-            break;
-          }
+      auto values = [&](int i) -> bool {
+        const int e = i & 1;
+        if (!wait(&sm.p_full[e], c.phase(i) & 1)) return false;
+#pragma unroll 1
+        for (int mt = 0; mt < 4; ++mt) {
+          if (!wait(&sm.v_full[mt], (c.all + i) & 1)) return false;
           tc::tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             tc::mma_f16(cx.tm + kColO + 64 * mt, dv + (uint64_t)(mt * 128 + kk * 1024),
-                        dp + (uint64_t)((cc & 1) * (kChunk * kRows * 2 / 16) + kk * 128), kIdO,
-                        (i > 0 || kk > 0) ? 1u : 0u);
+                        dp + (uint64_t)(e * (kChunk * kRows * 2 / 16) + kk * 128), kIdO, (i > 0 || kk > 0) ? 1u : 0u);
           tc::mma_commit(&sm.pv_done[mt]);
         }
-        if (ok) tc::mma_commit(&sm.p_free[cc & 1]);
+        tc::mma_commit(&sm.p_free[e]);
+        return true;
+      };
+      if (kWeights) {
+        for (int i = 0; i < sp.n; ++i)
+          if (!scores(i)) break;
+      } else {
+        bool ok = true;
+        for (int i = 0; ok && i < sp.n; i += 2) {   // S(A) S(B) PV(A) PV(B)
+          const int end = min(i + 2, sp.n);
+#pragma unroll 1
+          for (int j = i; ok && j < end; ++j) ok = scores(j);
+#pragma unroll 1
+          for (int j = i; ok && j < end; ++j) ok = values(j);
+        }
       }
     }
     __syncwarp();
     block_sync();
     if (*abort) break;
-    c += sp.n;
+    c.add(sp.n);
     u = min(cx.u1, tstart + units);
     tstart += units;
   }
 }
 
-// Warp 21: the packed pages of the chunks ahead into L2.  Warps 22 and 23: barriers only.
+// The warp after the MMA warp: the packed pages of the chunks ahead into L2.  The last two: barriers only.
 template <bool kWeights>
 __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx, bool active) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   volatile int* abort = &sm.abort;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 5;
   const int lane = threadIdx.x & 31;
   uint32_t c = 0;
-  int64_t u = cx.u0, tstart = cx.tstart;
+  int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
     block_sync();
     block_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = sm.seg.units;
+    const int units = max(1, sm.seg.n_chunks);
     if (active) {
       auto request = [&](int i) {
         const int k = sp.k0 + i;
@@ -979,15 +1070,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sm.kq_full[i], 4);
       tc::mbar_init(&sm.kq_free[i], 1);
-    }
-    tc::mbar_init(&sm.s_full, 1);
-    tc::mbar_init(&sm.s_free, kSoftWarps);
-    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sm.v_full[i], 4);
       tc::mbar_init(&sm.pv_done[i], 1);
     }
-    tc::mbar_init(&sm.p_full, kSoftWarps);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.p_free[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.s_full[i], 1);
+      tc::mbar_init(&sm.s_free[i], kWeights ? kSoftWarps / 2 : kSoftWarps);
+      tc::mbar_init(&sm.p_full[i], kSoftWarps);
+      tc::mbar_init(&sm.p_free[i], 1);
+    }
     sm.abort = 0;
     sm.progress = 0;
     tc::mbar_fence_init();
@@ -1025,12 +1116,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tm = sm.tmem;
-  Ctx<kWeights> cx{a, pl, sm, tm, u0, u1, sm.found_tile, sm.found_start, status};
+  Ctx<kWeights> cx{a, pl, sm, tm, (int)u0, (int)u1, sm.found_tile, (int)sm.found_start, status};
   if (u1 <= u0) cx.tile = 0;
   if (!kWeights && tid == 0) pl.cont[g] = (u1 > u0 && cx.tstart < u0) ? cx.tile : -1;
 
   // ---- roles, each with its own walk over the tiles (every walk meets the same barriers)
   if (warp < kDeqWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDeq));
     role_dequant<kWeights>(cx);
   } else if (warp < kDeqWarps + kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
@@ -1201,7 +1293,7 @@ cudaError_t prepare_kernel() {
   cudaFuncAttributes at;
   cudaError_t e = cudaFuncGetAttributes(&at, k_dense_tc<kWeights>);
   if (e != cudaSuccess) return e;
-  static_assert(4 * kRegsLaunch + kRegsSoft + kRegsMisc <= 6 * kRegsLaunch, "register split");
+  static_assert(2 * kRegsDeq + 2 * kRegsSoft + kRegsMisc <= 5 * kRegsLaunch, "register split");
   if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(k_dense_tc<kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)sizeof(Smem<kWeights>));
@@ -1214,6 +1306,11 @@ int slab_tiles(const csa2_dims* dm, int max_entries, int64_t* stride) {
   *stride = ((int64_t)max_entries + kChunk - 1) / kChunk * kChunk;
   const int64_t per = std::max<int64_t>(1, dm->B) * *stride * 4;
   return (int)std::max<int64_t>(1, std::min<int64_t>(tiles_of(dm), (int64_t)kSumBytes / std::max<int64_t>(1, per)));
+}
+
+// Tiles of every sequence that one launch takes: its units of work stay below 2^31.
+int launch_tiles(int64_t units_per_tile, int tiles) {
+  return (int)std::min<int64_t>(tiles, ((int64_t)INT_MAX) / std::max<int64_t>(1, units_per_tile));
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -1235,17 +1332,24 @@ cudaError_t launch_dense_attn_tc(const csa2_dims* dm, const DenseArgs& a, void* 
   if (e == cudaSuccess) e = prepare_kernel<false>();
   if (e != cudaSuccess) return e;
   Plan pl = {};
-  pl.tiles_per_seq = pl.tiles = tiles_of(dm);
-  const int64_t tiles = (int64_t)a.B * pl.tiles;
-  if (tiles >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-  const int64_t units = tiles * max_chunks(a.max_entries, a.W, a.swa_cap);
-  pl.n_ctas = (int)std::min<int64_t>(std::min(sms, kMaxCtas), std::max<int64_t>(1, units));
+  const int all = tiles_of(dm);
   pl.cont = static_cast<int32_t*>(ws);
   pl.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + up((size_t)kMaxCtas * 4));
-  e = launch_step(k_dense_tc<false>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<false>), s, a, pl, status_word());
-  if (e != cudaSuccess || pl.n_ctas == 1) return e;
-  const unsigned shared = (unsigned)std::min<int64_t>(tiles, pl.n_ctas - 1);
-  return launch_step(k_dense_merge, dim3(shared, kRows), dim3(128 * kMergeGroups), 0, s, a, pl);
+  const int64_t per_tile = (int64_t)a.B * max_chunks(a.max_entries, a.W, a.swa_cap);   // units of a tile of every sequence
+  const int slab = launch_tiles(per_tile, all);
+  if (slab == 0) return cudaErrorInvalidConfiguration;
+  for (int t0 = 0; t0 < all; t0 += slab) {
+    pl.tile0 = t0;
+    pl.tiles = std::min(slab, all - t0);
+    pl.n_ctas = (int)std::min<int64_t>(std::min(sms, kMaxCtas), per_tile * pl.tiles);
+    e = launch_step(k_dense_tc<false>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<false>), s, a, pl, status_word());
+    if (e != cudaSuccess) return e;
+    if (pl.n_ctas == 1) continue;
+    const unsigned shared = (unsigned)std::min<int64_t>((int64_t)a.B * pl.tiles, pl.n_ctas - 1);
+    e = launch_step(k_dense_merge, dim3(shared, kRows), dim3(128 * kMergeGroups), 0, s, a, pl);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 size_t entry_weights_workspace_bytes(const csa2_dims* dm, int max_entries) {
@@ -1262,14 +1366,13 @@ cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, voi
   if (e != cudaSuccess) return e;
   const int all = tiles_of(dm);
   Plan pl = {};
-  pl.tiles_per_seq = all;
-  if ((int64_t)a.B * all >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-  const int slab = all <= 1 ? 1 : slab_tiles(dm, a.max_entries, &pl.sum_stride);
+  const int64_t per_tile = (int64_t)a.B * max_chunks(a.max_entries, 0, 0);
+  const int slab = std::min(launch_tiles(per_tile, all), all <= 1 ? 1 : slab_tiles(dm, a.max_entries, &pl.sum_stride));
+  if (slab == 0) return cudaErrorInvalidConfiguration;
   for (int t0 = 0; t0 < all; t0 += slab) {
     pl.tile0 = t0;
     pl.tiles = std::min(slab, all - t0);
-    const int64_t units = (int64_t)a.B * pl.tiles * max_chunks(a.max_entries, 0, 0);
-    pl.n_ctas = (int)std::min<int64_t>(std::min(sms, kMaxCtas), std::max<int64_t>(1, units));
+    pl.n_ctas = (int)std::min<int64_t>(std::min(sms, kMaxCtas), per_tile * pl.tiles);
     if (all > 1) {
       pl.ranges = static_cast<int2*>(ws);
       pl.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + up((size_t)a.B * slab * sizeof(int2)));
