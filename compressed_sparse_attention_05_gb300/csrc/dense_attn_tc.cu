@@ -28,9 +28,9 @@
 // and walks the tiles in it.  A tile that falls to several CTAs leaves partial
 // (m, l, O) in the workspace and k_dense_merge joins them in order.
 //
-// Roles (640 threads): warps 0-7 dequantise (thread = one key x 256 channels), warps
-// 8-15 do the softmax (thread = one key x 32 rows), warp 16 issues the MMAs, warp 17
-// requests pages into L2 ahead.  Operand ranges as in attention_tc.cu (R11's
+// Roles (896 threads): warps 0-15 dequantise (a warp: 32 keys x 128 channels), warps 16-23
+// do the softmax (thread = one key x 32 rows), warp 24 issues the MMAs, warp 25 requests
+// pages into L2 ahead.  Operand ranges as in attention_tc.cu (R11's
 // powers of two for Q rows and window rows); P is rounded to fp16, the normaliser
 // sums the unrounded fp32 P, everything else is fp32.
 #include <cuda_fp16.h>
@@ -47,13 +47,13 @@ namespace {
 constexpr int kD = 512;
 constexpr int kRows = 64;                 // rows of a tile (N of both products)
 constexpr int kChunk = 128;               // keys of a chunk
-constexpr int kDeqWarps = 8, kSoftWarps = 8;
+constexpr int kDeqWarps = 16, kSoftWarps = 8;
 constexpr int kDeqThreads = kDeqWarps * 32;
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kThreads = 640;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
+constexpr int kThreads = 896;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
 constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
-// registers per thread after the split of the five warpgroups: 2 x 88 + 2 x 128 + 48 = 5 x 96
-constexpr int kRegsLaunch = 96, kRegsDeq = 88, kRegsSoft = 128, kRegsMisc = 48;
+// registers per thread after the split of the seven warpgroups: 4 x 64 + 2 x 104 + 40 = 7 x 72
+constexpr int kRegsLaunch = 72, kRegsDeq = 64, kRegsSoft = 104, kRegsMisc = 40;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;             // O^T: four M-tiles of 64 columns
 constexpr uint32_t kColS = 256;           // S^T: two buffers of 64 columns
@@ -90,9 +90,8 @@ struct Smem {
     float red[4][kRows];            // per-lane-quarter maxima / sums of a row over the keys; [0] also: see below
     int qexp[4][kRows];             // [1]: largest exponent field of each row of Q, before the products
     struct {                        // before the first tile
-      int64_t scan[kThreads / 32];
-      int64_t found_start;
-      int found_tile;
+      int scan[kThreads / 32];
+      int found_start, found_tile;
     };
   };
   uint64_t kq_full[4], kq_free[4];  // quarters of an odd chunk's K in tensor memory
@@ -131,6 +130,12 @@ __device__ __forceinline__ bool half_or(int half, bool v) {
       : "memory");
   return r != 0;
 }
+// Maximum over the warp.
+__device__ __forceinline__ float warp_max_f32(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 // 32 lanes x 32 columns: thread i of the warp gets lane (base + i).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -149,6 +154,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 // Bounded wait of a whole warp; on time-out the CTA's abort flag is raised.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   bool ok = false;
+#pragma unroll 1
   for (uint32_t i = 0; i < (1u << 21); ++i) {   // <= 2^21 suspensions of <= 1 us
     if (tc::mbar_try_wait_sleep(bar, parity, 1000)) {
       ok = true;
@@ -161,13 +167,38 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return ok;
 }
 
-// tcgen05.mma with the A operand in tensor memory (K-major, two fp16 per column).
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// Shared-memory descriptors as their low words (address and leading offset; an operand's
+// steps only move the address); the high word (stride offset, version) is a constant.  The
+// issuing thread has few registers and a spilled descriptor costs it more than an MMA takes.
+__device__ __forceinline__ uint32_t desc_lo(const void* p, uint32_t lbo) {
+  return ((tc::smem_addr(p) & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14); }
+
+// D[tmem] (+)= A . B^T, kind::f16, fp32 accumulation; A in shared memory or (K-major, two fp16
+// per column) in tensor memory.  The whole warp runs the issuing code, so that its operands are
+// uniform registers from the start, and one elected lane issues.
+template <uint32_t kAHi, uint32_t kBHi, uint32_t kIdesc>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %3, 0;\n"
+      " mov.b64 da, {%1, %4};\n mov.b64 db, {%2, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %6, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(accumulate), "n"(kAHi), "n"(kBHi), "n"(kIdesc)
+      : "memory");
+}
+template <uint32_t kBHi, uint32_t kIdesc>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 db;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %3, 0;\n"
+      " mov.b64 db, {%2, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %5, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(accumulate), "n"(kBHi), "n"(kIdesc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -223,6 +254,7 @@ __device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {
     const int64_t shift = dense_shift(a, b);
     const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
     const int i1 = (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
+#pragma unroll 1
     for (int i = r0 / a.Hq; i <= i1; ++i) {
       const DenseRow r = dense_row(a, b, i, n_ent, shift, pos0);
       const int lo = dense_first(a, r.doc, shift);
@@ -239,45 +271,64 @@ __device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {
   return max(1, range_chunks(g, kWeights));
 }
 
-// Inclusive block-wide prefix sum (all 768 threads), and the total.
-__device__ int64_t block_scan(int64_t v, int64_t* sums, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive block-wide prefix sum (all threads), and the total.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += x;
   }
+  return v;
+}
+__device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v, lane);
   __syncthreads();
   if (lane == 31) sums[warp] = v;
   __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int k = 0; k < kThreads / 32; ++k) {
-    const int64_t s = sums[k];
-    if (k < warp) before += s;
-    all += s;
-  }
-  *total = all;
-  return before + v;
+  const int w = warp_scan(lane < kThreads / 32 ? sums[lane] : 0, lane);   // every warp: the warps' prefix sums
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return v + (warp ? before : 0);
 }
 
 // ---- dequantisation --------------------------------------------------------------------
-// A thread's part of an entry: 128 channels (64 bytes of codes, 8 scales).
+// A warp's quarter (128 channels) of its 32 keys, packed.  Lane l = 8 part + kk holds piece
+// `part` (32 channels, 16 bytes) of keys 8 it + kk, it = 0 .. 3: a load instruction then
+// touches 8 cache lines instead of 32 (a lane per key kept the cache's tag stage busy for
+// half of the chunk).
 struct Packed {
-  uint4 c[4];
-  uint2 s;
+  uint4 c[4];       // by it
+  uint32_t sv[4];   // their scale pairs, as loaded: no instruction may wait for a load before the registers' use
+  uint2 sk;         // the quarter's 8 scales of key `lane` (for the copy in tensor memory)
 };
-// 16 channel pairs (32 channels) of MXFP4: piece i of the thread's 128 channels.
-__device__ __forceinline__ void dequant32(const Packed& k, int i, uint32_t (&o)[16]) {
-  const uint32_t w = (i & 2) ? k.s.y : k.s.x;
-  const uint32_t s = e4m3x2_f16x2((w >> (16 * (i & 1))) & 0xFFFFu);
+// 16 channel pairs (32 channels) of MXFP4 with their two scales.
+__device__ __forceinline__ void dequant32(const uint4& c, uint32_t scales, uint32_t (&o)[16]) {
+  const uint32_t s = e4m3x2_f16x2(scales & 0xFFFFu);
   const uint32_t g0 = prmt(s, s, 0x1010u), g1 = prmt(s, s, 0x3232u);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t g = j < 2 ? g0 : g1;
-    e2m1x8_f16x8(word_of(k.c[i], j), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    e2m1x8_f16x8(word_of(c, j), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
 #pragma unroll
     for (int x = 0; x < 4; ++x) o[4 * j + x] = hmul2(o[4 * j + x], g);   // exact: <= 6 significant bits
   }
+}
+// From "piece lane / 8 of key 8 it + lane % 8" to "piece p of key lane": a 4 x 4 transpose
+// between the register index and bits 3 and 4 of the lane.
+__device__ __forceinline__ void exchange(uint4& a, uint4& b, bool upper, int mask) {
+  uint4 s = upper ? a : b;
+  s.x = __shfl_xor_sync(0xffffffffu, s.x, mask);
+  s.y = __shfl_xor_sync(0xffffffffu, s.y, mask);
+  s.z = __shfl_xor_sync(0xffffffffu, s.z, mask);
+  s.w = __shfl_xor_sync(0xffffffffu, s.w, mask);
+  if (upper) a = s; else b = s;
+}
+__device__ __forceinline__ void key_per_lane(uint4 (&t)[4], int lane) {
+  exchange(t[0], t[1], (lane & 8) != 0, 8);
+  exchange(t[2], t[3], (lane & 8) != 0, 8);
+  exchange(t[0], t[2], (lane & 16) != 0, 16);
+  exchange(t[1], t[3], (lane & 16) != 0, 16);
 }
 
 template <bool kWeights>
@@ -306,6 +357,7 @@ __device__ __forceinline__ KeyRef window_ref(const Ctx<kWeights>& cx, int k, int
   if (p > sg.w_hi) return r;
   bool seen = sg.one_t != 0;      // one token: the tile's rows all see its whole window
   if (!seen)
+#pragma unroll 1
     for (int i = 0; i < kRows; ++i) seen |= p >= cx.sm.lo[1][i] && p <= cx.sm.hi[1][i];
   if (!seen) return r;
   const int64_t w = (int64_t)sg.b * cx.a.swa_cap + (p - sg.pos0);
@@ -325,44 +377,62 @@ __device__ __forceinline__ int page_of(const Ctx<kWeights>& cx, int k, int key, 
   return __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j >> 6));
 }
 
-// Quarter q of a key's packed bytes.  No key, or one behind a bad page: zero codes and
-// scales (the channels are then +0); window rows are read where they are used.
+// The same for a warp's 32 keys from key0 on, which lie on one page.
 template <bool kWeights>
-__device__ __forceinline__ void load_packed(const Ctx<kWeights>& cx, int k, int key, int q, int page, Packed& o) {
+__device__ __forceinline__ int page_of_warp(const Ctx<kWeights>& cx, int k, int key0, bool exists) {
   const Segment& sg = cx.sm.seg;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o.c[i] = make_uint4(0, 0, 0, 0);
-  o.s = make_uint2(0, 0);
-  if (k < sg.nw) return;
-  const int j = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key;
-  if (j < sg.e_lo || j >= sg.e_hi) return;
-  if (page < 0 || page >= cx.a.n_pages) {
-    if (q == 0) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
-    return;
-  }
-  const int64_t slot = (int64_t)page * kPage + (j & (kPage - 1));
-  const uint4* codes = reinterpret_cast<const uint4*>(cx.a.kv_codes + slot * (kD / 2) + 64 * q);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o.c[i] = __ldg(codes + i);
-  o.s = __ldg(reinterpret_cast<const uint2*>(cx.a.kv_scales + slot * (kD / 16) + 8 * q));
+  if (!exists || k < sg.nw) return -1;
+  const int j0 = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key0;
+  if (j0 + 32 <= sg.e_lo || j0 >= sg.e_hi) return -1;
+  return __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j0 >> 6));
 }
 
-// Channels 128 q + 32 p .. +31 of a key, from its packed registers or the window row.
-__device__ __forceinline__ void piece(const Packed& pk, const KeyRef& w, bool window, int q, int p, uint32_t (&o)[16]) {
-  if (window) {   // uniform over the warp
-    uint4 c0 = make_uint4(0, 0, 0, 0), c1 = c0;
-    if (w.codes) {
-      c0 = __ldg(reinterpret_cast<const uint4*>(w.codes + 128 * q) + 2 * p);
-      c1 = __ldg(reinterpret_cast<const uint4*>(w.codes + 128 * q) + 2 * p + 1);
-    }
+// Quarter q of the packed bytes of the warp's keys (key0 .. key0 + 31 of entry chunk k, all on
+// one page).  No key, or one behind a bad page: zero codes and scales (the channels are then
+// +0); window rows are read where they are used.
+template <bool kWeights>
+__device__ __forceinline__ void load_packed(const Ctx<kWeights>& cx, int k, int key0, int q, int page, int lane, Packed& o) {
+  const Segment& sg = cx.sm.seg;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t x = word_of(j < 4 ? c0 : c1, j & 3);
-      o[2 * j] = win2_f16x2(x & 0xFFFFu, w.wsc);
-      o[2 * j + 1] = win2_f16x2(x >> 16, w.wsc);
+  for (int i = 0; i < 4; ++i) {
+    o.c[i] = make_uint4(0, 0, 0, 0);
+    o.sv[i] = 0;
+  }
+  o.sk = make_uint2(0, 0);
+  if (k < sg.nw) return;
+  const int j0 = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key0;
+  if (j0 + 32 <= sg.e_lo || j0 >= sg.e_hi) return;
+  if (page < 0 || page >= cx.a.n_pages) {
+    if (q == 0 && lane == 0) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
+    return;
+  }
+  const int64_t slot0 = (int64_t)page * kPage + (j0 & (kPage - 1));
+  const int kk = lane & 7, part = lane >> 3;
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int j = j0 + 8 * it + kk;
+    if (j >= sg.e_lo && j < sg.e_hi) {
+      const int64_t slot = slot0 + 8 * it + kk;
+      o.c[it] = __ldg(reinterpret_cast<const uint4*>(cx.a.kv_codes + slot * (kD / 2) + 64 * q + 16 * part));
+      o.sv[it] = __ldg(reinterpret_cast<const uint16_t*>(cx.a.kv_scales + slot * (kD / 16) + 8 * q + 2 * part));
     }
-  } else {
-    dequant32(pk, p, o);
+  }
+  if (!kWeights && j0 + lane >= sg.e_lo && j0 + lane < sg.e_hi)
+    o.sk = __ldg(reinterpret_cast<const uint2*>(cx.a.kv_scales + (slot0 + lane) * (kD / 16) + 8 * q));
+}
+
+// Channels 128 q + 32 p .. +31 of a window row.
+__device__ __forceinline__ void window_piece(const KeyRef& w, int q, int p, uint32_t (&o)[16]) {
+  uint4 c0 = make_uint4(0, 0, 0, 0), c1 = c0;
+  if (w.codes) {
+    c0 = __ldg(reinterpret_cast<const uint4*>(w.codes + 128 * q) + 2 * p);
+    c1 = __ldg(reinterpret_cast<const uint4*>(w.codes + 128 * q) + 2 * p + 1);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t x = word_of(j < 4 ? c0 : c1, j & 3);
+    o[2 * j] = win2_f16x2(x & 0xFFFFu, w.wsc);
+    o[2 * j + 1] = win2_f16x2(x >> 16, w.wsc);
   }
 }
 
@@ -411,16 +481,19 @@ __device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp,
     float o[16];
     tc::tmem_ld16(cx.tm + kColO + 64 * mt + c0 + ((uint32_t)(32 * lq) << 16), o);
     tc::tmem_wait_ld();
+    if (sp.n == 0) {   // (a tile without keys has no products)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int r = c0 + j;
-      const float x = sp.n > 0 ? o[j] : 0.f;   // (a tile without keys has no products)
-      if (!whole)
-        part[r * kD + dim] = x;
-      else if (r0 + r < rows) {
-        const float l = cx.sm.red[0][r];
-        a.O[((int64_t)b * rows + r0 + r) * kD + dim] = (uint16_t)(f32x2_bf16x2(l > 0.f ? x * (1.f / l) : 0.f, 0.f) & 0xFFFFu);
-      }
+      for (int j = 0; j < 16; ++j) o[j] = 0.f;
+    }
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) part[(c0 + j) * kD + dim] = o[j];
+    } else {
+      uint16_t* out = a.O + ((int64_t)b * rows + r0 + c0) * kD + dim;
+      const int live = (int)min(rows - r0 - c0, (int64_t)16);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < live) out[j * kD] = (uint16_t)(f32x2_bf16x2(o[j] * cx.sm.red[0][c0 + j], 0.f) & 0xFFFFu);
     }
   }
   tc::tc_fence_before();
@@ -431,8 +504,7 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int lq = warp & 3, half = warp >> 2;     // lane quarter; quarters 2 half and 2 half + 1 of the channels
-  const int key = 32 * lq + lane;
+  const int lq = warp & 3, q = warp >> 2;        // lane quarter (keys 32 lq ..); quarter of the channels
   const uint32_t lane_q = (uint32_t)(32 * lq) << 16;
   volatile int* abort = &sm.abort;
   Count c;
@@ -446,45 +518,39 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
     const int64_t rows = (int64_t)a.Tq * a.Hq;
     if (tid < kRows) sm.qexp[1][tid] = 0;
     deq_sync();
-    // thread: row 8 g + tid % 8, channels 8 c8 .. +7 for c8 = tid / 8 and tid / 8 + 32
-    auto q_load = [&](int g, int c8) -> uint4 {
+    // thread: row 8 g + tid % 8, channels 8 c8 .. +7
+    const int c8 = tid >> 3;
+    auto q_load = [&](int g) -> uint4 {
       const int h = 8 * g + (tid & 7);
       return r0 + h < rows ? __ldg(reinterpret_cast<const uint4*>(a.Q + ((int64_t)b * rows + r0 + h) * kD + c8 * 8))
                            : make_uint4(0, 0, 0, 0);
     };
-#pragma unroll
+#pragma unroll 2
     for (int g = 0; g < 8; ++g) {
+      const uint4 v = q_load(g);
       uint32_t e = 0;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint4 v = q_load(g, (tid >> 3) + 32 * x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = word_of(v, j);
-          e = max(e, max((w >> 7) & 0xFFu, (w >> 23) & 0xFFu));
-        }
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = word_of(v, j);
+        e = max(e, max((w >> 7) & 0xFFu, (w >> 23) & 0xFFu));
       }
       e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
       e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
       if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * g + lane], (int)e);
     }
     deq_sync();
-#pragma unroll
+#pragma unroll 2
     for (int g = 0; g < 8; ++g) {
       const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * g + (tid & 7)]));
+      const uint4 v = q_load(g);
+      uint32_t ov[4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int c8 = (tid >> 3) + 32 * x;
-        const uint4 v = q_load(g, c8);
-        uint32_t ov[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = word_of(v, j);
-          ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
-        }
-        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + g * 8192 + c8 * 128 + (tid & 7) * 16) =
-            make_uint4(ov[0], ov[1], ov[2], ov[3]);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = word_of(v, j);
+        ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
       }
+      *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + g * 8192 + c8 * 128 + (tid & 7) * 16) =
+          make_uint4(ov[0], ov[1], ov[2], ov[3]);
     }
     if (tid < kRows) sm.mult[tid] = a.scale * kLog2e * pow2i(q_head_exp(sm.qexp[1][tid]));
     tc::fence_async_smem();
@@ -492,75 +558,88 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks), nw = sm.seg.nw;
 
-    // Packed bytes of this thread's two quarters: of the chunk at hand until its last use, then
-    // of the next one (its page is known by then; the pages' bytes are in L2).
-    Packed pk[2];
-    int page = page_of<kWeights>(cx, sp.k0, key, sp.n > 0);
-    auto load = [&](int i, int x) { load_packed<kWeights>(cx, sp.k0 + i, key, 2 * half + x, page, pk[x]); };
-    // K of an odd chunk: quarters into tensor memory.  Quarter q's slot q % 2 last held quarter
+    // Packed bytes of the warp's quarter: of the chunk at hand until their last use, then of the
+    // next one (its page is known by then; the pages' bytes are in L2).
+    Packed pk;
+    int page = page_of_warp<kWeights>(cx, sp.k0, 32 * lq, sp.n > 0);
+    auto load = [&](int i) { load_packed<kWeights>(cx, sp.k0 + i, 32 * lq, q, page, lane, pk); };
+    // K of an odd chunk: its quarters in tensor memory.  Quarter q's slot q % 2 last held quarter
     // q - 2 of this chunk, or q + 2 of the odd chunk before; the barriers belong to quarters, so
-    // that a warp waits for consecutive phases of each.
+    // that a warp waits for consecutive phases of one.
     auto put_k = [&](int i) -> bool {
       const uint32_t ph = c.phase(i);
-      KeyRef w{nullptr, 0.f};
-      const bool window = sp.k0 + i < nw;
-      if (window) w = window_ref<kWeights>(cx, sp.k0 + i, key);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int q = 2 * half + x;
-        if (half == 1) {
-          if (!warp_wait(&sm.kq_free[q - 2], ph & 1, abort)) return false;
-        } else if (ph > 0) {
-          if (!warp_wait(&sm.kq_free[q + 2], (ph - 1) & 1, abort)) return false;
-        }
-        tc::tc_fence_after();
+      const bool window = sp.k0 + i < nw;      // uniform
+      uint4 t[4] = {pk.c[0], pk.c[1], pk.c[2], pk.c[3]};
+      key_per_lane(t, lane);
+      if (q >= 2) {
+        if (!warp_wait(&sm.kq_free[q - 2], ph & 1, abort)) return false;
+      } else if (ph > 0) {
+        if (!warp_wait(&sm.kq_free[q + 2], (ph - 1) & 1, abort)) return false;
+      }
+      tc::tc_fence_after();
+      const uint32_t ta = cx.tm + kColK + 64 * (q & 1) + lane_q;
+      if (!window) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           uint32_t o[16];
-          piece(pk[x], w, window, q, p, o);
-          __syncwarp();
-          tmem_st16u(cx.tm + kColK + 64 * x + 16 * p + lane_q, o);
+          dequant32(t[p], (p & 2 ? pk.sk.y : pk.sk.x) >> (16 * (p & 1)), o);
+          tmem_st16u(ta + 16 * p, o);
         }
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.kq_full[q]);
+      } else {
+        const KeyRef w = window_ref<kWeights>(cx, sp.k0 + i, 32 * lq + lane);
+#pragma unroll 1
+        for (int p = 0; p < 4; ++p) {
+          uint32_t o[16];
+          window_piece(w, q, p, o);
+          __syncwarp();
+          tmem_st16u(ta + 16 * p, o);
+        }
       }
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.kq_full[q]);
       return true;
     };
-    // A chunk into the shared-memory tile, quarter by quarter behind the products that read it;
-    // each quarter's registers then take the next chunk's.
+    // A chunk's quarter into the shared-memory tile, behind the products that read it there; the
+    // registers then take the next chunk's.  Keys 32 lq + 8 it + lane % 8, piece lane / 8.
+    unsigned char* dst = reinterpret_cast<unsigned char*>(sm.v) + 4 * lq * 8192 + (16 * q + 4 * (lane >> 3)) * 128 +
+                         (lane & 7) * 16;
     auto put_v = [&](int i) -> bool {
-      KeyRef w{nullptr, 0.f};
       const bool window = sp.k0 + i < nw;
-      if (window) w = window_ref<kWeights>(cx, sp.k0 + i, key);
       const bool more = i + 1 < sp.n;
-      page = page_of<kWeights>(cx, sp.k0 + i + 1, key, more);
+      page = page_of_warp<kWeights>(cx, sp.k0 + i + 1, 32 * lq, more);
+      const uint32_t cc = c.all + i;
+      if (cc > 0 && !warp_wait(&sm.pv_done[q], (cc - 1) & 1, abort)) return false;
+      auto store = [&](int it, const uint32_t (&o)[16]) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int q = 2 * half + x;
-        const uint32_t cc = c.all + i;
-        if (cc > 0 && !warp_wait(&sm.pv_done[q], (cc - 1) & 1, abort)) return false;
-        unsigned char* dst = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 8192 + 16 * q * 128 + (key & 7) * 16;
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(dst + it * 8192 + j * 128) =
+              make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      };
+      if (!window) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int it = 0; it < 4; ++it) {
           uint32_t o[16];
-          piece(pk[x], w, window, q, p, o);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(dst + (4 * p + j) * 128) =
-                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          dequant32(pk.c[it], pk.sv[it], o);
+          store(it, o);
         }
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.v_full[q]);
-        if (more) load(i + 1, x);
+      } else {
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it) {
+          uint32_t o[16];
+          window_piece(window_ref<kWeights>(cx, sp.k0 + i, 32 * lq + 8 * it + (lane & 7)), q, lane >> 3, o);
+          store(it, o);
+        }
       }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.v_full[q]);
+      if (more) load(i + 1);
       return true;
     };
     if (sp.n > 0) {
-      load(0, 0);
-      load(0, 1);
+      load(0);
       for (int i = 0; i < sp.n; ++i) {
         if (!kWeights && (i & 1) && !put_k(i)) break;
         if (!put_v(i)) break;
@@ -569,7 +648,7 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
     block_sync();                       // the tile's products are complete, l is known
     tc::tc_fence_after();
     if (*abort) break;
-    if (!kWeights) drain_o<kWeights>(cx, sp, tile, half, lq, lane);
+    if (!kWeights) drain_o<kWeights>(cx, sp, tile, q, lq, lane);
     c.add(sp.n);
     u = min(cx.u1, tstart + units);
     tstart += units;
@@ -583,35 +662,31 @@ struct KeyView {
   int ka, kb;          // compared with hi and lo
   int win;             // 1: window row
   float kf, ff;        // window row: 2^f and f
-  int64_t p;
+  int p;
   float dist;          // |t - p| when the tile holds one token
 };
 
+// |t - p| in fp32 (exact below 2^24).
+__device__ __forceinline__ float distance(int t, int p) {
+  return (float)(t > p ? (uint32_t)t - (uint32_t)p : (uint32_t)p - (uint32_t)t);
+}
+
 // Columns c0 .. c0+31 of this thread's key: the logits in the log2 domain as the value
-// product carries them (-inf where the row does not see the key), plus nref.
+// product carries them, -inf where the row does not see the key.
 template <bool kWeights>
-__device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyView& kv, uint32_t taddr, int c0, bool ref,
-                                            float (&x)[32]) {
+__device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyView& kv, uint32_t taddr, int c0, float (&x)[32]) {
   const Smem<kWeights>& sm = cx.sm;
   tmem_ld32(taddr, x);
   tc::tmem_wait_ld();
-  if (!kv.general) {
-#pragma unroll
-    for (int j4 = 0; j4 < 8; ++j4) {
-      const float4 m = *reinterpret_cast<const float4*>(&sm.mult[c0 + 4 * j4]);
-      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (ref) z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
-      x[4 * j4] = fmaf(x[4 * j4], m.x, z.x);
-      x[4 * j4 + 1] = fmaf(x[4 * j4 + 1], m.y, z.y);
-      x[4 * j4 + 2] = fmaf(x[4 * j4 + 2], m.z, z.z);
-      x[4 * j4 + 3] = fmaf(x[4 * j4 + 3], m.w, z.w);
-    }
-    return;
-  }
 #pragma unroll
   for (int j4 = 0; j4 < 8; ++j4) {
     const float4 m = *reinterpret_cast<const float4*>(&sm.mult[c0 + 4 * j4]);
-    x[4 * j4] *= m.x * kv.kf; x[4 * j4 + 1] *= m.y * kv.kf; x[4 * j4 + 2] *= m.z * kv.kf; x[4 * j4 + 3] *= m.w * kv.kf;
+    x[4 * j4] *= m.x; x[4 * j4 + 1] *= m.y; x[4 * j4 + 2] *= m.z; x[4 * j4 + 3] *= m.w;
+  }
+  if (!kv.general) return;
+  if (kv.kf != 1.f) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] *= kv.kf;
   }
   if (cx.a.cap > 0.f) {
     const float cap2 = cx.a.cap * kLog2e, inv = 1.f / cap2;
@@ -624,16 +699,13 @@ __device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyVi
       for (int j = 0; j < 32; ++j) x[j] = fmaf(-sm.slope2[c0 + j], kv.dist, x[j]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const int64_t d = (int64_t)sm.hi[1][c0 + j] - kv.p;
-        x[j] = fmaf(-sm.slope2[c0 + j], (float)(d < 0 ? -d : d), x[j]);
-      }
+      for (int j = 0; j < 32; ++j) x[j] = fmaf(-sm.slope2[c0 + j], distance(sm.hi[1][c0 + j], kv.p), x[j]);
     }
   }
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     const bool seen = kv.ka < sm.hi[kv.win][c0 + j] && kv.kb >= sm.lo[kv.win][c0 + j];
-    x[j] = seen ? x[j] + kv.ff + (ref ? sm.nref[c0 + j] : 0.f) : -INFINITY;
+    x[j] = seen ? x[j] + kv.ff : -INFINITY;
   }
 }
 
@@ -730,11 +802,13 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       kv.ff = 0.f;
       *slot = -1;
       if (kv.win) {
-        kv.p = (int64_t)sm.seg.w_lo + (int64_t)k * kChunk + key;
-        kv.ka = kv.p > sm.seg.w_hi ? INT_MAX : (int)kv.p - 1;
-        kv.kb = (int)kv.p;
+        const int64_t p = (int64_t)sm.seg.w_lo + (int64_t)k * kChunk + key;
+        const bool have = p <= sm.seg.w_hi;
+        kv.p = have ? (int)p : 0;
+        kv.ka = have ? kv.p - 1 : INT_MAX;
+        kv.kb = kv.p;
         kv.general = true;
-        if (kv.p <= sm.seg.w_hi) {
+        if (have) {
           const int f = window_exp(__ldg(a.swa_scales + (int64_t)b * a.swa_cap + (kv.p - sm.seg.pos0)));
           if (f != 0) {
             kv.kf = pow2i(f);
@@ -745,15 +819,14 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         const int j = entry_of(i), e0 = j - key;
         const bool have = j >= e_lo && j < e_hi && page >= 0 && page < a.n_pages;
         if (have) *slot = (int64_t)page * kPage + (j & (kPage - 1));
-        kv.p = a.entry_pos && have ? (int64_t)__ldg(a.entry_pos + *slot) : 4 * ((int64_t)j + shift) + 3;
+        kv.p = a.entry_pos && have ? __ldg(a.entry_pos + *slot) : (int)min(4 * ((int64_t)j + shift) + 3, (int64_t)INT_MAX);
         kv.ka = have ? j : INT_MAX;
-        kv.kb = (int)min(max(kv.p - 3, (int64_t)INT_MIN), (int64_t)INT_MAX);
+        kv.kb = max(kv.p, INT_MIN + 3) - 3;
         kv.general = a.cap > 0.f || a.slopes || e0 < sm.seg.all_lo || e0 + kChunk > sm.seg.all_hi ||
                      __any_sync(0xffffffffu, !have);
       }
       page = page_ahead(i + kStep);
-      const int64_t far = (int64_t)sm.seg.t - kv.p;
-      kv.dist = (float)(far < 0 ? -far : far);
+      kv.dist = distance(sm.seg.t, kv.p);
       return kv;
     };
 
@@ -766,13 +839,19 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         if (!warp_wait(&sm.s_full[i & 1], c.phase(i) & 1, abort)) break;
         tc::tc_fence_after();
         float sum = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < kRows; c0 += 32) {
           float x[32];
-          load_logits<kWeights>(cx, kv, cx.tm + kColS + 64 * (i & 1) + c0 + lane_q, c0, true, x);
+          load_logits<kWeights>(cx, kv, cx.tm + kColS + 64 * (i & 1) + c0 + lane_q, c0, x);
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s4[j & 3] += ex2(x[j]);
+          for (int j4 = 0; j4 < 8; ++j4) {
+            const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
+            s4[0] += ex2(x[4 * j4] + z.x);
+            s4[1] += ex2(x[4 * j4 + 1] + z.y);
+            s4[2] += ex2(x[4 * j4 + 2] + z.z);
+            s4[3] += ex2(x[4 * j4 + 3] + z.w);
+          }
           sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
         }
         tc::tc_fence_before();
@@ -800,24 +879,23 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         // ---- logits over the reference, and whether one outgrows it
         float x[32];
         float top = -INFINITY;
-        if (ok) {
-          load_logits<kWeights>(cx, kv, ts, c0, true, x);
+        load_logits<kWeights>(cx, kv, ts, c0, x);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) top = fmaxf(top, x[j]);
+        for (int j4 = 0; j4 < 8; ++j4) {
+          const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
+          top = fmaxf(top, fmaxf(fmaxf(x[4 * j4] + z.x, x[4 * j4 + 1] + z.y), fmaxf(x[4 * j4 + 2] + z.z, x[4 * j4 + 3] + z.w)));
         }
         const bool seen_abort = !ok || *abort != 0;
         if (half_or(half, top > kRescaleLog2 || seen_abort)) {
           if (half_or(half, seen_abort)) break;   // (a wait that fails below is met by the next vote)
-          load_logits<kWeights>(cx, kv, ts, c0, false, x);
           // maxima of the half's 32 rows over the 128 keys
+          float mine = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float y[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = x[16 * q + j];
-            const float mx = reduce16<true>(y, lane);
-            if (lane < 16) sm.red[lq][c0 + 16 * q + lane] = mx;
+          for (int j = 0; j < 32; ++j) {
+            const float mx = warp_max_f32(x[j]);
+            if (lane == j) mine = mx;
           }
+          sm.red[lq][c0 + lane] = mine;
           half_sync(half);
           bool need = false;
           if (lq == 0) {
@@ -855,7 +933,6 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) lsum[j] *= sm.red[0][c0 + j];
           }
-          load_logits<kWeights>(cx, kv, ts, c0, true, x);
           half_sync(half);                     // red is read; the next vote may come
         }
         tc::tc_fence_before();
@@ -865,11 +942,16 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         const float pf = pow2i(-(int)kv.ff);   // the normaliser adds p = 2^-f (2^f p)
         uint32_t pk[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float p0 = ex2(x[j]), p1 = ex2(x[j + 1]);
-          lsum[j] = fmaf(p0, pf, lsum[j]);
-          lsum[j + 1] = fmaf(p1, pf, lsum[j + 1]);
-          pk[j / 2] = f32x2_f16x2(p0, p1);
+        for (int j4 = 0; j4 < 8; ++j4) {
+          const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
+          const float p0 = ex2(x[4 * j4] + z.x), p1 = ex2(x[4 * j4 + 1] + z.y);
+          const float p2 = ex2(x[4 * j4 + 2] + z.z), p3 = ex2(x[4 * j4 + 3] + z.w);
+          lsum[4 * j4] = fmaf(p0, pf, lsum[4 * j4]);
+          lsum[4 * j4 + 1] = fmaf(p1, pf, lsum[4 * j4 + 1]);
+          lsum[4 * j4 + 2] = fmaf(p2, pf, lsum[4 * j4 + 2]);
+          lsum[4 * j4 + 3] = fmaf(p3, pf, lsum[4 * j4 + 3]);
+          pk[2 * j4] = f32x2_f16x2(p0, p1);
+          pk[2 * j4 + 1] = f32x2_f16x2(p2, p3);
         }
         if (ph > 0) warp_wait(&sm.p_free[e], (ph - 1) & 1, abort);
         unsigned char* pd = reinterpret_cast<unsigned char*>(sm.p) + e * (kChunk * kRows * 2) + (key >> 3) * 1024 +
@@ -896,7 +978,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       if (st < kRows) {
         const float l = (sm.red[0][st] + sm.red[1][st]) + (sm.red[2][st] + sm.red[3][st]);
         const float m = sm.nref[st] == kUnset ? -INFINITY : -sm.nref[st];
-        sm.red[0][st] = l;
+        sm.red[0][st] = l > 0.f ? 1.f / l : 0.f;   // the factor of O
         if (sp.first && sp.last) {
           if (a.lse && r0 + st < rows)
             a.lse[(int64_t)b * rows + r0 + st] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
@@ -908,9 +990,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       }
     }
     block_sync();
-    tc::tc_fence_after();
     if (*abort) break;
-    if (!kWeights) drain_o<kWeights>(cx, sp, tile, 2 + half, lq, lane);
     c.add(sp.n);
     u = min(cx.u1, tstart + units);
     tstart += units;
@@ -923,15 +1003,13 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
 // softmax(A) runs under S(B), softmax(B) under PV(A); B takes A's shared-memory tile quarter
 // by quarter behind PV(A), A' takes B's behind PV(B).
 template <bool kWeights>
-__device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx, bool issuer) {
+__device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   volatile int* abort = &sm.abort;
   constexpr uint32_t kIdS = tc::idesc_f16(128, kRows, 0, 0, 0);   // K-major A and B
   constexpr uint32_t kIdO = tc::idesc_f16(128, kRows, 0, 1, 1);   // MN-major A and B
-  const uint64_t dq = tc::smem_desc(tc::smem_addr(sm.q), 128, 8192);
-  const uint64_t dk = tc::smem_desc(tc::smem_addr(sm.v), 128, 8192);
-  const uint64_t dv = tc::smem_desc(tc::smem_addr(sm.v), 8192, 128);
-  const uint64_t dp = tc::smem_desc(tc::smem_addr(sm.p), 1024, 128);
+  constexpr uint32_t kHiS = desc_hi(8192), kHiO = desc_hi(128);
+  const uint32_t dq = desc_lo(sm.q, 128), dk = desc_lo(sm.v, 128), dv = desc_lo(sm.v, 8192), dp = desc_lo(sm.p, 1024);
   Count c;
   int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
@@ -939,11 +1017,13 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx, bool issuer) {
     block_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks);
-    if (issuer) {
+    {
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        // the warp votes, so that its control flow stays uniform
+#pragma unroll 1
         for (uint32_t i = 0; i < (1u << 24); ++i) {
-          if (tc::mbar_try_wait(bar, parity)) return true;
-          if ((i & 255) == 255 && *abort) return false;
+          if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+          if ((i & 255) == 255 && __any_sync(0xffffffffu, *abort != 0)) return false;
         }
         *abort = 1;
         return false;
@@ -960,34 +1040,34 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx, bool issuer) {
             tc::tc_fence_after();
 #pragma unroll
             for (uint32_t ks = 0; ks < 8; ++ks)
-              tc::mma_f16(d, dk + (uint64_t)((8 * q + ks) * 16), dq + (uint64_t)((8 * q + ks) * 16), kIdS, (q | ks) != 0);
-            if (kWeights) tc::mma_commit(&sm.pv_done[q]);
+              mma_ss<kHiS, kHiS, kIdS>(d, dk + (8 * q + ks) * 16, dq + (8 * q + ks) * 16, q | ks);
+            if (kWeights) mma_commit_elected(&sm.pv_done[q]);
           } else {
             if (!wait(&sm.kq_full[q], ph & 1)) return false;
             tc::tc_fence_after();
 #pragma unroll
             for (uint32_t ks = 0; ks < 8; ++ks)
-              mma_f16_ta(d, cx.tm + kColK + 64 * (q & 1) + 8 * ks, dq + (uint64_t)((8 * q + ks) * 16), kIdS, (q | ks) != 0);
-            tc::mma_commit(&sm.kq_free[q]);
+              mma_ts<kHiS, kIdS>(d, cx.tm + kColK + 64 * (q & 1) + 8 * ks, dq + (8 * q + ks) * 16, q | ks);
+            mma_commit_elected(&sm.kq_free[q]);
           }
         }
-        tc::mma_commit(&sm.s_full[e]);
+        mma_commit_elected(&sm.s_full[e]);
         return true;
       };
       auto values = [&](int i) -> bool {
         const int e = i & 1;
         if (!wait(&sm.p_full[e], c.phase(i) & 1)) return false;
 #pragma unroll 1
-        for (int mt = 0; mt < 4; ++mt) {
+        for (uint32_t mt = 0; mt < 4; ++mt) {
           if (!wait(&sm.v_full[mt], (c.all + i) & 1)) return false;
           tc::tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma_f16(cx.tm + kColO + 64 * mt, dv + (uint64_t)(mt * 128 + kk * 1024),
-                        dp + (uint64_t)(e * (kChunk * kRows * 2 / 16) + kk * 128), kIdO, (i > 0 || kk > 0) ? 1u : 0u);
-          tc::mma_commit(&sm.pv_done[mt]);
+          for (uint32_t kk = 0; kk < 8; ++kk)
+            mma_ss<kHiO, kHiO, kIdO>(cx.tm + kColO + 64 * mt, dv + mt * 128 + kk * 1024,
+                                     dp + e * (kChunk * kRows * 2 / 16) + kk * 128, (uint32_t)i | kk);
+          mma_commit_elected(&sm.pv_done[mt]);
         }
-        tc::mma_commit(&sm.p_free[e]);
+        mma_commit_elected(&sm.p_free[e]);
         return true;
       };
       if (kWeights) {
@@ -1040,10 +1120,13 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx, bool acti
         const uint8_t* src = ((lane & 2) ? a.kv_scales : a.kv_codes) + (int64_t)page * bytes;
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
       };
+#pragma unroll 1
       for (int i = 2; i < kAhead; ++i) request(i);
+#pragma unroll 1
       for (int i = 0; i + kAhead < sp.n; ++i) {
         request(i + kAhead);
         // not a wait on s_full: this warp may fall behind by more than a phase
+#pragma unroll 1
         for (uint32_t k = 0; k < (1u << 22); ++k) {
           if (*reinterpret_cast<volatile int*>(&sm.progress) >= (int)c + i + 1 || *abort) break;
           __nanosleep(100);
@@ -1086,24 +1169,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   if (warp == kDeqWarps + kSoftWarps) tc::tmem_alloc(&sm.tmem, kTmemCols);
   pdl_wait();
 
-  // ---- this CTA's share of the chunks of all tiles
+  // ---- this CTA's share of the chunks of all tiles (their number is below 2^31)
   const int tiles = a.B * pl.tiles;
-  int64_t mine = 0, total = 0;
+  int mine = 0, total = 0;
+#pragma unroll 1
   for (int t = tid; t < tiles; t += kThreads) mine += tile_units<kWeights>(a, pl, t);
-  const int64_t own = mine;
-  int64_t inc = block_scan(mine, sm.scan, &total);
-  const int64_t ctas = min((int64_t)gridDim.x, total);
-  const int64_t g = blockIdx.x;
-  const int64_t u0 = g < ctas ? total * g / ctas : 0, u1 = g < ctas ? total * (g + 1) / ctas : 0;
+  int inc = block_scan(mine, sm.scan, &total);
+  const int ctas = min((int)gridDim.x, total), g = blockIdx.x;
+  const int u0 = g < ctas ? (int)((int64_t)total * g / ctas) : 0;
+  const int u1 = g < ctas ? (int)((int64_t)total * (g + 1) / ctas) : 0;
   if (u1 > u0) {
-    int64_t base = 0;
+    int base = 0, v = mine, all = total;
+#pragma unroll 1
     for (int t0 = 0; t0 < tiles; t0 += kThreads) {
-      int64_t v = own, all = total;
       if (tiles > kThreads) {          // (with one batch the first scan holds the answer)
         v = t0 + tid < tiles ? tile_units<kWeights>(a, pl, t0 + tid) : 0;
         inc = block_scan(v, sm.scan, &all);
       }
-      const int64_t start = base + inc - v;
+      const int start = base + inc - v;
       if (t0 + tid < tiles && u0 >= start && u0 < start + v) {
         sm.found_tile = t0 + tid;
         sm.found_start = start;
@@ -1116,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tm = sm.tmem;
-  Ctx<kWeights> cx{a, pl, sm, tm, (int)u0, (int)u1, sm.found_tile, (int)sm.found_start, status};
+  Ctx<kWeights> cx{a, pl, sm, tm, u0, u1, sm.found_tile, sm.found_start, status};
   if (u1 <= u0) cx.tile = 0;
   if (!kWeights && tid == 0) pl.cont[g] = (u1 > u0 && cx.tstart < u0) ? cx.tile : -1;
 
@@ -1130,7 +1213,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
     if (warp == kDeqWarps + kSoftWarps)
-      role_mma<kWeights>(cx, (tid & 31) == 0);
+      role_mma<kWeights>(cx);
     else
       role_prefetch<kWeights>(cx, warp == kDeqWarps + kSoftWarps + 1);
   }
@@ -1260,6 +1343,7 @@ __global__ void __launch_bounds__(128) k_weights_ranges(DenseArgs a, Plan pl) {
     const int n_ent = dense_entries(a, b);
     const int64_t shift = dense_shift(a, b);
     const int i1 = (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
+#pragma unroll 1
     for (int i = r0 / a.Hq; i <= i1; ++i) {
       const DenseRow r = dense_row(a, b, i, n_ent, shift, 0);
       const int f = dense_first(a, r.doc, shift);
@@ -1293,7 +1377,7 @@ cudaError_t prepare_kernel() {
   cudaFuncAttributes at;
   cudaError_t e = cudaFuncGetAttributes(&at, k_dense_tc<kWeights>);
   if (e != cudaSuccess) return e;
-  static_assert(2 * kRegsDeq + 2 * kRegsSoft + kRegsMisc <= 5 * kRegsLaunch, "register split");
+  static_assert(4 * kRegsDeq + 2 * kRegsSoft + kRegsMisc <= 7 * kRegsLaunch, "register split");
   if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(k_dense_tc<kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)sizeof(Smem<kWeights>));
