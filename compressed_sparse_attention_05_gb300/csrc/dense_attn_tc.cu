@@ -15,22 +15,26 @@
 //   S^T [128 keys x 64 rows]  = K [128 x 512] . Q^T        (32 MMAs, k = 16 channels)
 //   O^T [512 dims x 64 rows] += V^T [512 x 128] . P^T      (4 M-tiles x 8 MMAs, k = 16 keys)
 //
-// Shared memory holds one dequantised chunk (128 KB) beside Q (64 KB) and P, so with
-// both products reading it the softmax would stand between them.  Every second chunk
-// therefore has its K as an A operand in tensor memory as well (two 128-channel
-// quarters at a time): its scores need no room in shared memory and run while the
-// softmax of the chunk before does.  (An MMA of this shape takes 58 cycles with A in
-// shared memory K-major, 52 MN-major, 87 with A in tensor memory, whatever N up to 64,
-// so all chunks that way would cost 26% more, every second one 13%.)
+// The score product reads K as an A operand in tensor memory, where three 128-channel
+// quarters of the dequantised chunk fit at a time; the value product reads V from shared
+// memory.  (Shared memory holds one dequantised chunk (128 KB) beside Q (64 KB) and P, so
+// with both products reading it the softmax would stand between them.  And at N = 64 an MMA
+// with both operands in shared memory reads 6 KB in 48 cycles, all that the memory gives,
+// while the dequantising warps' stores and every barrier wait: with the scores of every
+// second chunk from shared memory the same batch took 281 us.)  An MMA with A in tensor
+// memory takes 87 cycles, so the tensor pipe's floor is 32 x 87 + 32 x 52 = 4,450 cycles per
+// 128 keys x 64 rows.  S(c+1) is issued before PV(c), so that the softmax of a chunk has a
+// whole chunk's products to hide behind.
 //
 // Work is split over the SMs by chunks, not by tiles: every CTA computes the chunk
 // count of all tiles (lengths live on the device), takes an equal contiguous share,
 // and walks the tiles in it.  A tile that falls to several CTAs leaves partial
 // (m, l, O) in the workspace and k_dense_merge joins them in order.
 //
-// Roles (896 threads): warps 0-15 dequantise (a warp: 32 keys x 128 channels), warps 16-23
-// do the softmax (thread = one key x 32 rows), warp 24 issues the MMAs, warp 25 requests
-// pages into L2 ahead.  Operand ranges as in attention_tc.cu (R11's
+// Roles (896 threads): warps 0-7 dequantise V into shared memory (a warp: 32 keys x 256
+// channels), warps 8-15 K into tensor memory (the same split), warps 16-23 do the softmax
+// (thread = one key x 32 rows), warp 24 issues the MMAs, warp 25 requests pages into L2
+// ahead.  Operand ranges as in attention_tc.cu (R11's
 // powers of two for Q rows and window rows); P is rounded to fp16, the normaliser
 // sums the unrounded fp32 P, everything else is fp32.
 #include <cuda_fp16.h>
@@ -40,6 +44,7 @@
 #include "dense.cuh"
 #include "operands.cuh"
 #include "tc.cuh"
+#include "tma.cuh"
 
 namespace csa2 {
 namespace {
@@ -47,25 +52,40 @@ namespace {
 constexpr int kD = 512;
 constexpr int kRows = 64;                 // rows of a tile (N of both products)
 constexpr int kChunk = 128;               // keys of a chunk
-constexpr int kDeqWarps = 16, kSoftWarps = 8;
-constexpr int kDeqThreads = kDeqWarps * 32;
+constexpr int kValWarps = 8, kKeyWarps = 8, kSoftWarps = 8;
+constexpr int kValThreads = kValWarps * 32;
+constexpr int kSoftFirst = (kValWarps + kKeyWarps) * 32;   // first softmax thread
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = 896;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
+constexpr int kMmaWarp = kValWarps + kKeyWarps + kSoftWarps;
 constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
-// registers per thread after the split of the seven warpgroups: 4 x 64 + 2 x 104 + 40 = 7 x 72
-constexpr int kRegsLaunch = 72, kRegsDeq = 64, kRegsSoft = 104, kRegsMisc = 40;
+// registers per thread after the split of the seven warpgroups: 4 x 56 + 2 x 120 + 40 = 7 x 72
+constexpr int kRegsLaunch = 72, kRegsFill = 56, kRegsSoft = 120, kRegsMisc = 40;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0;             // O^T: four M-tiles of 64 columns
-constexpr uint32_t kColS = 256;           // S^T: two buffers of 64 columns
-constexpr uint32_t kColK = 384;           // K of odd chunks: two quarters of 64 columns (128 channels of fp16 each)
+// Tensor memory.  Attention: O^T (four M-tiles of 64 columns), S^T, and a ring of three
+// quarters of K (64 columns each: 128 channels of fp16).  Weights: two S^T, a ring of four.
+constexpr uint32_t kColO = 0;
+template <bool kWeights> struct Cols;
+template <> struct Cols<false> { static constexpr uint32_t S = 256, K = 320; static constexpr int ring = 3, s_bufs = 1; };
+template <> struct Cols<true> { static constexpr uint32_t S = 0, K = 128; static constexpr int ring = 4, s_bufs = 2; };
 constexpr float kRescaleLog2 = 8.f;       // a reference maximum moves only beyond this growth
 constexpr float kUnset = 3e38f;           // -m_ref of a row without keys: any finite logit outgrows it, -inf stays -inf
 constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, then m and l
 
+constexpr int kQuarter = 128;                         // channels of a quarter
+constexpr int kVSlots = 3;                            // quarters of V in shared memory
+constexpr int kStageBytes = kChunk * kQuarter / 2;    // packed codes of a chunk's quarter
+template <bool kWeights> struct Stages;               // staging slots of the K and V streams
+template <> struct Stages<false> { static constexpr int K = 2, V = 2; };
+template <> struct Stages<true> { static constexpr int K = 8, V = 1; };
+
 // Operand tiles (no-swizzle canonical layout, core matrices of 8 rows x 16 bytes):
-//   Q [row][dim]: (r/8)*8192 + (d/8)*128 + (r%8)*16 + (d%8)*2
-//   V [key][dim]: (k/8)*8192 + (d/8)*128 + (k%8)*16 + (d%8)*2
-//   P [key][row]: (k/8)*1024 + (r/8)*128 + (k%8)*16 + (r%8)*2
+//   Q [row][dim]:         (r/8)*8192 + (d/8)*128 + (r%8)*16 + (d%8)*2
+//   V slot [key][dim]:    (k/8)*2048 + (d/8)*128 + (k%8)*16 + (d%8)*2   (128 channels)
+//   P [key][row]:         (k/8)*1024 + (r/8)*128 + (k%8)*16 + (r%8)*2
+// Staging slots hold the codes of one quarter of 128 keys as tensor-map copies with the
+// 64-byte swizzle write them: 16-byte piece p of key k at 64 k + 16 (p ^ (k/2)%4), so that
+// the 8 lanes of a phase (lane = key) read all banks.
 struct Segment {            // what the roles need to know of the current tile
   int b, nw, c_hi;          // window chunks; entry chunks end at c_hi
   int n_chunks;             // (a tile without chunks still counts as one unit of work)
@@ -77,15 +97,17 @@ struct Segment {            // what the roles need to know of the current tile
 };
 template <bool kWeights>
 struct Smem {
+  unsigned char kst[Stages<kWeights>::K][kStageBytes];   // (1024-aligned)
+  unsigned char vst[kWeights ? 1 : Stages<kWeights>::V][kWeights ? 16 : kStageBytes];
   uint16_t q[kRows * kD];
-  uint16_t v[kChunk * kD];
+  uint16_t v[kWeights ? 8 : kVSlots * kChunk * kQuarter];
   uint16_t p[kWeights ? 8 : 2 * kChunk * kRows];
   float mult[kRows];        // logit multiplier: softmax scale * log2(e) * 2^e_r
   float nref[kRows];        // attention: -m_ref (kUnset before the row's first key); weights: -lse * log2(e)
   float slope2[kRows];      // slope * log2(e)
-  // a row sees entry j if j < hi[0] and its first token is >= lo[0], and the window row
-  // at position p if p - 1 < hi[1] (the row's own position) and p >= lo[1]
-  int hi[2][kRows], lo[2][kRows];
+  // a row sees entry j if j < nv and its first token is >= doc, and the window row at
+  // position p if 0 <= t - p < W and p >= doc
+  int nv[kRows], doc[kRows], t[kRows];
   union {
     float red[4][kRows];            // per-lane-quarter maxima / sums of a row over the keys; [0] also: see below
     int qexp[4][kRows];             // [1]: largest exponent field of each row of Q, before the products
@@ -94,8 +116,10 @@ struct Smem {
       int found_start, found_tile;
     };
   };
-  uint64_t kq_full[4], kq_free[4];  // quarters of an odd chunk's K in tensor memory
-  uint64_t v_full[4], pv_done[4];   // quarters of the shared-memory tile (weights: free again after the scores)
+  uint64_t kst_full[Stages<kWeights>::K], kst_free[Stages<kWeights>::K];   // staging slots
+  uint64_t vst_full[Stages<kWeights>::V], vst_free[Stages<kWeights>::V];
+  uint64_t kq_full[4], kq_free[4];  // quarters of a chunk's K in tensor memory
+  uint64_t v_full[4], v_free[4];    // quarters of a chunk's V in shared memory
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
   Segment seg;
   uint32_t tmem;
@@ -104,7 +128,7 @@ struct Smem {
 };
 // red[0][r] holds the factor of a row's rescaling and, at the end of a tile, its sum l:
 // each is computed by the one thread that reads the column, from the column.
-static_assert(sizeof(Smem<false>) <= 232448, "shared memory of the attention kernel");
+static_assert(sizeof(Smem<false>) <= 232448 && sizeof(Smem<true>) <= 232448, "shared memory");
 
 struct Plan {
   int tile0, tiles;         // tiles [tile0, tile0 + tiles) of every sequence are this launch's
@@ -117,7 +141,7 @@ struct Plan {
 };
 
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory"); }
-__device__ __forceinline__ void deq_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kDeqThreads) : "memory"); }
+__device__ __forceinline__ void val_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kValThreads) : "memory"); }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
 // The 128 threads of one half of the softmax warps (32 rows).
 __device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(3 + half) : "memory"); }
@@ -177,36 +201,49 @@ __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4)
 
 // D[tmem] (+)= A . B^T, kind::f16, fp32 accumulation; A in shared memory or (K-major, two fp16
 // per column) in tensor memory.  The whole warp runs the issuing code, so that its operands are
-// uniform registers from the start, and one elected lane issues.
+// uniform registers from the start, and the elected lane (leader != 0) issues.
 template <uint32_t kAHi, uint32_t kBHi, uint32_t kIdesc>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %3, 0;\n"
+      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %3, 0;\n"
       " mov.b64 da, {%1, %4};\n mov.b64 db, {%2, %5};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %6, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(accumulate), "n"(kAHi), "n"(kBHi), "n"(kIdesc)
+      "r"(a), "r"(b), "r"(accumulate), "n"(kAHi), "n"(kBHi), "n"(kIdesc), "r"(leader)
       : "memory");
 }
 template <uint32_t kBHi, uint32_t kIdesc>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 db;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %3, 0;\n"
+      "{\n .reg .pred p, e;\n .reg .b64 db;\n setp.ne.b32 e, %6, 0;\n setp.ne.b32 p, %3, 0;\n"
       " mov.b64 db, {%2, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %5, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(accumulate), "n"(kBHi), "n"(kIdesc)
+      "r"(a), "r"(b), "r"(accumulate), "n"(kBHi), "n"(kIdesc), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit_elected(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit_by(uint32_t leader, uint64_t* bar) {
   asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_addr(bar))
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_addr(bar)),
+      "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+// Whether the phase of the given parity is complete (never suspends).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::
-          "r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -214,19 +251,23 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// tanh: an odd polynomial below 0.55 (least-squares fit of (tanh x / x - 1) / x^2 in
-// x^2, relative error 1.2 x 2^-24), 1 - 2 / (e^2x + 1) above (relative error < 2^-21).
-__device__ __forceinline__ float fast_tanh(float x) {
-  const float a = fabsf(x), z = x * x;
+// tanh below 0.55: an odd polynomial (least-squares fit of (tanh x / x - 1) / x^2 in x^2,
+// relative error 1.2 x 2^-24).
+__device__ __forceinline__ float small_tanh(float x) {
+  const float z = x * x;
   float r = -0.0066150883f;
   r = fmaf(r, z, 0.021312291f);
   r = fmaf(r, z, -0.053909965f);
   r = fmaf(r, z, 0.13333116f);
   r = fmaf(r, z, -0.33333331f);
-  r = fmaf(x * z, r, x);
+  return fmaf(x * z, r, x);
+}
+// Any x: above 0.55, 1 - 2 / (e^2x + 1) (relative error < 2^-21).
+__device__ __forceinline__ float fast_tanh(float x) {
+  const float a = fabsf(x);
   const float e = ex2(fminf(a, 10.f) * (2.f * kLog2e));   // tanh(10) rounds to 1
   const float big = copysignf(1.f - 2.f * rcp_approx(e + 1.f), x);
-  return a < 0.55f ? r : big;
+  return a < 0.55f ? small_tanh(x) : big;
 }
 
 // ---- tiles and their chunks ----------------------------------------------------------
@@ -293,42 +334,14 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
 }
 
 // ---- dequantisation --------------------------------------------------------------------
-// A warp's quarter (128 channels) of its 32 keys, packed.  Lane l = 8 part + kk holds piece
-// `part` (32 channels, 16 bytes) of keys 8 it + kk, it = 0 .. 3: a load instruction then
-// touches 8 cache lines instead of 32 (a lane per key kept the cache's tag stage busy for
-// half of the chunk).
-struct Packed {
-  uint4 c[4];       // by it
-  uint32_t sv[4];   // their scale pairs, as loaded: no instruction may wait for a load before the registers' use
-  uint2 sk;         // the quarter's 8 scales of key `lane` (for the copy in tensor memory)
-};
-// 16 channel pairs (32 channels) of MXFP4 with their two scales.
-__device__ __forceinline__ void dequant32(const uint4& c, uint32_t scales, uint32_t (&o)[16]) {
+// Half h (16 channels) of a piece with its two E4M3 scales: 8 fp16 pairs.
+__device__ __forceinline__ void dequant16(const uint4& c, uint32_t scales, int h, uint32_t (&o)[8]) {
   const uint32_t s = e4m3x2_f16x2(scales & 0xFFFFu);
-  const uint32_t g0 = prmt(s, s, 0x1010u), g1 = prmt(s, s, 0x3232u);
+  const uint32_t g = prmt(s, s, h ? 0x3232u : 0x1010u);
+  e2m1x8_f16x8(h ? c.z : c.x, o[0], o[1], o[2], o[3]);
+  e2m1x8_f16x8(h ? c.w : c.y, o[4], o[5], o[6], o[7]);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t g = j < 2 ? g0 : g1;
-    e2m1x8_f16x8(word_of(c, j), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[4 * j + x] = hmul2(o[4 * j + x], g);   // exact: <= 6 significant bits
-  }
-}
-// From "piece lane / 8 of key 8 it + lane % 8" to "piece p of key lane": a 4 x 4 transpose
-// between the register index and bits 3 and 4 of the lane.
-__device__ __forceinline__ void exchange(uint4& a, uint4& b, bool upper, int mask) {
-  uint4 s = upper ? a : b;
-  s.x = __shfl_xor_sync(0xffffffffu, s.x, mask);
-  s.y = __shfl_xor_sync(0xffffffffu, s.y, mask);
-  s.z = __shfl_xor_sync(0xffffffffu, s.z, mask);
-  s.w = __shfl_xor_sync(0xffffffffu, s.w, mask);
-  if (upper) a = s; else b = s;
-}
-__device__ __forceinline__ void key_per_lane(uint4 (&t)[4], int lane) {
-  exchange(t[0], t[1], (lane & 8) != 0, 8);
-  exchange(t[2], t[3], (lane & 8) != 0, 8);
-  exchange(t[0], t[2], (lane & 16) != 0, 16);
-  exchange(t[1], t[3], (lane & 16) != 0, 16);
+  for (int x = 0; x < 8; ++x) o[x] = hmul2(o[x], g);   // exact: <= 6 significant bits
 }
 
 template <bool kWeights>
@@ -341,6 +354,7 @@ struct Ctx {
   int tile;                // first tile and its first unit
   int tstart;
   uint32_t* status;
+  const CUtensorMap* map;  // codes: [n_pages * 64][256] bytes in boxes of 64 x 64
 };
 
 // A window row as its dequantising thread needs it (null: no key, zeros).
@@ -358,7 +372,7 @@ __device__ __forceinline__ KeyRef window_ref(const Ctx<kWeights>& cx, int k, int
   bool seen = sg.one_t != 0;      // one token: the tile's rows all see its whole window
   if (!seen)
 #pragma unroll 1
-    for (int i = 0; i < kRows; ++i) seen |= p >= cx.sm.lo[1][i] && p <= cx.sm.hi[1][i];
+    for (int i = 0; i < kRows; ++i) seen |= (uint32_t)(cx.sm.t[i] - (int)p) < (uint32_t)cx.a.W && p >= cx.sm.doc[i];
   if (!seen) return r;
   const int64_t w = (int64_t)sg.b * cx.a.swa_cap + (p - sg.pos0);
   const float s = __ldg(cx.a.swa_scales + w);
@@ -367,70 +381,21 @@ __device__ __forceinline__ KeyRef window_ref(const Ctx<kWeights>& cx, int k, int
   return r;
 }
 
-// Page-table entry of this thread's key in entry chunk k (-1: a window chunk, or no such entry).
+// Page-table entry of entry j, or -1 if no row of the tile sees it.
 template <bool kWeights>
-__device__ __forceinline__ int page_of(const Ctx<kWeights>& cx, int k, int key, bool exists) {
+__device__ __forceinline__ int page_of(const Ctx<kWeights>& cx, int j, bool exists) {
   const Segment& sg = cx.sm.seg;
-  if (!exists || k < sg.nw) return -1;
-  const int j = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key;
-  if (j < sg.e_lo || j >= sg.e_hi) return -1;
+  if (!exists || j < sg.e_lo || j >= sg.e_hi) return -1;
   return __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j >> 6));
 }
 
-// The same for a warp's 32 keys from key0 on, which lie on one page.
-template <bool kWeights>
-__device__ __forceinline__ int page_of_warp(const Ctx<kWeights>& cx, int k, int key0, bool exists) {
-  const Segment& sg = cx.sm.seg;
-  if (!exists || k < sg.nw) return -1;
-  const int j0 = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key0;
-  if (j0 + 32 <= sg.e_lo || j0 >= sg.e_hi) return -1;
-  return __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j0 >> 6));
-}
-
-// Quarter q of the packed bytes of the warp's keys (key0 .. key0 + 31 of entry chunk k, all on
-// one page).  No key, or one behind a bad page: zero codes and scales (the channels are then
-// +0); window rows are read where they are used.
-template <bool kWeights>
-__device__ __forceinline__ void load_packed(const Ctx<kWeights>& cx, int k, int key0, int q, int page, int lane, Packed& o) {
-  const Segment& sg = cx.sm.seg;
+// Channels 16 p .. +15 of a window row.
+__device__ __forceinline__ void window_piece(const KeyRef& w, int p, uint32_t (&o)[8]) {
+  uint4 c = make_uint4(0, 0, 0, 0);
+  if (w.codes) c = __ldg(reinterpret_cast<const uint4*>(w.codes) + p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o.c[i] = make_uint4(0, 0, 0, 0);
-    o.sv[i] = 0;
-  }
-  o.sk = make_uint2(0, 0);
-  if (k < sg.nw) return;
-  const int j0 = (sg.c_hi - 1 - (k - sg.nw)) * kChunk + key0;
-  if (j0 + 32 <= sg.e_lo || j0 >= sg.e_hi) return;
-  if (page < 0 || page >= cx.a.n_pages) {
-    if (q == 0 && lane == 0) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
-    return;
-  }
-  const int64_t slot0 = (int64_t)page * kPage + (j0 & (kPage - 1));
-  const int kk = lane & 7, part = lane >> 3;
-#pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int j = j0 + 8 * it + kk;
-    if (j >= sg.e_lo && j < sg.e_hi) {
-      const int64_t slot = slot0 + 8 * it + kk;
-      o.c[it] = __ldg(reinterpret_cast<const uint4*>(cx.a.kv_codes + slot * (kD / 2) + 64 * q + 16 * part));
-      o.sv[it] = __ldg(reinterpret_cast<const uint16_t*>(cx.a.kv_scales + slot * (kD / 16) + 8 * q + 2 * part));
-    }
-  }
-  if (!kWeights && j0 + lane >= sg.e_lo && j0 + lane < sg.e_hi)
-    o.sk = __ldg(reinterpret_cast<const uint2*>(cx.a.kv_scales + (slot0 + lane) * (kD / 16) + 8 * q));
-}
-
-// Channels 128 q + 32 p .. +31 of a window row.
-__device__ __forceinline__ void window_piece(const KeyRef& w, int q, int p, uint32_t (&o)[16]) {
-  uint4 c0 = make_uint4(0, 0, 0, 0), c1 = c0;
-  if (w.codes) {
-    c0 = __ldg(reinterpret_cast<const uint4*>(w.codes + 128 * q) + 2 * p);
-    c1 = __ldg(reinterpret_cast<const uint4*>(w.codes + 128 * q) + 2 * p + 1);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t x = word_of(j < 4 ? c0 : c1, j & 3);
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t x = word_of(c, j);
     o[2 * j] = win2_f16x2(x & 0xFFFFu, w.wsc);
     o[2 * j + 1] = win2_f16x2(x >> 16, w.wsc);
   }
@@ -455,7 +420,7 @@ __device__ __forceinline__ Span span_of(const Segment& sg, int u, int u1, int ts
 }
 
 // Counters that run through all tiles of a CTA: chunks, and those at even and odd places
-// of their tile (the two S and P buffers).  Phase k of a barrier is its k-th use.
+// of their tile (double buffers).  Phase k of a barrier is its k-th use.
 struct Count {
   uint32_t all = 0, even = 0, odd = 0;
   __device__ __forceinline__ void add(int n) {
@@ -499,15 +464,121 @@ __device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp,
   tc::tc_fence_before();
 }
 
+// Dequantises every chunk of a tile, quarter by quarter: eight warps, lane = key, four of them
+// take quarters 0 and 2, four take 1 and 3.  kV: into the shared-memory slots that the value
+// product reads; else K, into the tensor-memory slots that the score product reads.
+// Quarter number n = 4 chunk + q goes where number n - ring was; barriers belong to quarters
+// (and staging slots to one group of warps), so that a warp waits for consecutive phases.
+template <bool kWeights, bool kV>
+__device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, const Span& sp, const Count& c, uint32_t entries, int warp,
+                                          int lane) {
+  Smem<kWeights>& sm = cx.sm;
+  const DenseArgs& a = cx.a;
+  constexpr int kRing = kV ? kVSlots : Cols<kWeights>::ring, kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
+  const int lq = warp & 3, odd = warp >> 2, key = 32 * lq + lane;
+  volatile int* abort = &sm.abort;
+  const int nw = sm.seg.nw, c_hi = sm.seg.c_hi;
+  const int i0 = min(max(nw - sp.k0, 0), sp.n);   // first entry chunk of the span
+  auto entry_of = [&](int i) -> int { return (c_hi - 1 - (sp.k0 + i - nw)) * kChunk + key; };
+  // scales of the key's two quarters, a chunk ahead (its page another chunk ahead); no key, or one
+  // behind a bad page: zero, so that whatever codes the staging slot holds become zeros
+  uint2 sc[2], sn[2];
+  int page = page_of<kWeights>(cx, entry_of(i0), i0 < sp.n);
+  auto load_scales = [&](int i, uint2 (&o)[2]) {
+    o[0] = o[1] = make_uint2(0, 0);
+    if (i >= sp.n) return;
+    const int j = entry_of(i);
+    if (j >= sm.seg.e_lo && j < sm.seg.e_hi) {
+      if (page >= 0 && page < a.n_pages) {
+        const uint2* p = reinterpret_cast<const uint2*>(
+            a.kv_scales + ((int64_t)page * kPage + (j & (kPage - 1))) * (kD / 16) + 8 * odd);
+        o[0] = __ldg(p);
+        o[1] = __ldg(p + 2);
+      } else if (!kV && odd == 0) {
+        raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
+      }
+    }
+    page = page_of<kWeights>(cx, entry_of(i + 1), i + 1 < sp.n);
+  };
+  load_scales(i0, sn);
+  const uint32_t dst_k = cx.tm + Cols<kWeights>::K + ((uint32_t)(32 * lq) << 16);
+  unsigned char* dst_v = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 2048 + (key & 7) * 16;
+#pragma unroll 1
+  for (int n = 0; n < 2 * sp.n; ++n) {
+    const int i = n >> 1, k = sp.k0 + i, q = odd + 2 * (n & 1);
+    const uint32_t cc = c.all + i, number = 4 * cc + q;
+    const bool window = k < nw;             // uniform
+    if (!window && (n & 1) == 0) {
+      sc[0] = sn[0];
+      sc[1] = sn[1];
+      load_scales(i + 1, sn);
+    }
+    uint4 t[4];
+    if (!window) {
+      const uint32_t st = 4 * (entries + (i - i0)) + q, slot = st % kStage, use = st / kStage;
+      if (!warp_wait(kV ? &sm.vst_full[slot] : &sm.kst_full[slot], use & 1, abort)) break;
+      const unsigned char* src = (kV ? sm.vst[slot] : sm.kst[slot]) + 64 * key;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) t[p] = *reinterpret_cast<const uint4*>(src + 16 * (p ^ ((key >> 1) & 3)));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(kV ? &sm.vst_free[slot] : &sm.kst_free[slot]);
+    }
+    if (number >= (uint32_t)kRing &&
+        !warp_wait(kV ? &sm.v_free[(q - kRing) & 3] : &sm.kq_free[(q - kRing) & 3], ((number - kRing) >> 2) & 1, abort))
+      break;
+    if (!kV) tc::tc_fence_after();
+    const uint32_t slot = number % kRing;
+    auto put = [&](int p, const uint32_t (&o)[8]) {   // channels 16 p .. +15 of the quarter
+      if (kV) {
+        unsigned char* d = dst_v + slot * (kChunk * kQuarter * 2) + 2 * p * 128;
+        *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(d + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+      } else {
+        tmem_st8u(dst_k + 64 * slot + 8 * p, o);
+      }
+    };
+    if (!window) {
+      const uint2 s = (n & 1) ? sc[1] : sc[0];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        uint32_t o[8];
+        dequant16(t[p >> 1], (p & 4 ? s.y : s.x) >> (16 * ((p >> 1) & 1)), p & 1, o);
+        put(p, o);
+      }
+    } else {
+      const KeyRef w = window_ref<kWeights>(cx, k, key);
+#pragma unroll 1
+      for (int p = 0; p < 8; ++p) {
+        uint32_t o[8];
+        window_piece(w, 8 * q + p, o);
+        __syncwarp();
+        put(p, o);
+      }
+    }
+    if (kV) {
+      tc::fence_async_smem();
+    } else {
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(kV ? &sm.v_full[q] : &sm.kq_full[q]);
+  }
+}
+// Entry chunks of a span (the others are window chunks).
+__device__ __forceinline__ int entry_chunks(const Segment& sg, const Span& sp) {
+  return sp.n - min(max(sg.nw - sp.k0, 0), sp.n);
+}
+
+// Warps 0-7: Q, then V, then half of O.
 template <bool kWeights>
-__device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
+__device__ __forceinline__ void role_values(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int lq = warp & 3, q = warp >> 2;        // lane quarter (keys 32 lq ..); quarter of the channels
-  const uint32_t lane_q = (uint32_t)(32 * lq) << 16;
   volatile int* abort = &sm.abort;
   Count c;
+  uint32_t entries = 0;
   int tile = cx.tile;
   int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
@@ -517,16 +588,15 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
     const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
     const int64_t rows = (int64_t)a.Tq * a.Hq;
     if (tid < kRows) sm.qexp[1][tid] = 0;
-    deq_sync();
-    // thread: row 8 g + tid % 8, channels 8 c8 .. +7
-    const int c8 = tid >> 3;
+    val_sync();
+    // step g: row 8 (g / 2) + tid % 8, channels 8 c8 .. +7 with c8 = tid / 8 + 32 (g % 2)
     auto q_load = [&](int g) -> uint4 {
-      const int h = 8 * g + (tid & 7);
+      const int h = 8 * (g >> 1) + (tid & 7), c8 = (tid >> 3) + 32 * (g & 1);
       return r0 + h < rows ? __ldg(reinterpret_cast<const uint4*>(a.Q + ((int64_t)b * rows + r0 + h) * kD + c8 * 8))
                            : make_uint4(0, 0, 0, 0);
     };
-#pragma unroll 2
-    for (int g = 0; g < 8; ++g) {
+#pragma unroll 4
+    for (int g = 0; g < 16; ++g) {
       const uint4 v = q_load(g);
       uint32_t e = 0;
 #pragma unroll
@@ -536,12 +606,12 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
       }
       e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
       e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
-      if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * g + lane], (int)e);
+      if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * (g >> 1) + lane], (int)e);
     }
-    deq_sync();
-#pragma unroll 2
-    for (int g = 0; g < 8; ++g) {
-      const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * g + (tid & 7)]));
+    val_sync();
+#pragma unroll 4
+    for (int g = 0; g < 16; ++g) {
+      const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * (g >> 1) + (tid & 7)]));
       const uint4 v = q_load(g);
       uint32_t ov[4];
 #pragma unroll
@@ -549,126 +619,129 @@ __device__ __forceinline__ void role_dequant(const Ctx<kWeights>& cx) {
         const uint32_t w = word_of(v, j);
         ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
       }
-      *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + g * 8192 + c8 * 128 + (tid & 7) * 16) =
-          make_uint4(ov[0], ov[1], ov[2], ov[3]);
+      *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + (g >> 1) * 8192 +
+                                ((tid >> 3) + 32 * (g & 1)) * 128 + (tid & 7) * 16) = make_uint4(ov[0], ov[1], ov[2], ov[3]);
     }
     if (tid < kRows) sm.mult[tid] = a.scale * kLog2e * pow2i(q_head_exp(sm.qexp[1][tid]));
     tc::fence_async_smem();
     block_sync();                       // Q, row constants and the tile's chunks are there
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = max(1, sm.seg.n_chunks), nw = sm.seg.nw;
-
-    // Packed bytes of the warp's quarter: of the chunk at hand until their last use, then of the
-    // next one (its page is known by then; the pages' bytes are in L2).
-    Packed pk;
-    int page = page_of_warp<kWeights>(cx, sp.k0, 32 * lq, sp.n > 0);
-    auto load = [&](int i) { load_packed<kWeights>(cx, sp.k0 + i, 32 * lq, q, page, lane, pk); };
-    // K of an odd chunk: its quarters in tensor memory.  Quarter q's slot q % 2 last held quarter
-    // q - 2 of this chunk, or q + 2 of the odd chunk before; the barriers belong to quarters, so
-    // that a warp waits for consecutive phases of one.
-    auto put_k = [&](int i) -> bool {
-      const uint32_t ph = c.phase(i);
-      const bool window = sp.k0 + i < nw;      // uniform
-      uint4 t[4] = {pk.c[0], pk.c[1], pk.c[2], pk.c[3]};
-      key_per_lane(t, lane);
-      if (q >= 2) {
-        if (!warp_wait(&sm.kq_free[q - 2], ph & 1, abort)) return false;
-      } else if (ph > 0) {
-        if (!warp_wait(&sm.kq_free[q + 2], (ph - 1) & 1, abort)) return false;
-      }
-      tc::tc_fence_after();
-      const uint32_t ta = cx.tm + kColK + 64 * (q & 1) + lane_q;
-      if (!window) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint32_t o[16];
-          dequant32(t[p], (p & 2 ? pk.sk.y : pk.sk.x) >> (16 * (p & 1)), o);
-          tmem_st16u(ta + 16 * p, o);
-        }
-      } else {
-        const KeyRef w = window_ref<kWeights>(cx, sp.k0 + i, 32 * lq + lane);
-#pragma unroll 1
-        for (int p = 0; p < 4; ++p) {
-          uint32_t o[16];
-          window_piece(w, q, p, o);
-          __syncwarp();
-          tmem_st16u(ta + 16 * p, o);
-        }
-      }
-      tc::tmem_wait_st();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.kq_full[q]);
-      return true;
-    };
-    // A chunk's quarter into the shared-memory tile, behind the products that read it there; the
-    // registers then take the next chunk's.  Keys 32 lq + 8 it + lane % 8, piece lane / 8.
-    unsigned char* dst = reinterpret_cast<unsigned char*>(sm.v) + 4 * lq * 8192 + (16 * q + 4 * (lane >> 3)) * 128 +
-                         (lane & 7) * 16;
-    auto put_v = [&](int i) -> bool {
-      const bool window = sp.k0 + i < nw;
-      const bool more = i + 1 < sp.n;
-      page = page_of_warp<kWeights>(cx, sp.k0 + i + 1, 32 * lq, more);
-      const uint32_t cc = c.all + i;
-      if (cc > 0 && !warp_wait(&sm.pv_done[q], (cc - 1) & 1, abort)) return false;
-      auto store = [&](int it, const uint32_t (&o)[16]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(dst + it * 8192 + j * 128) =
-              make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-      };
-      if (!window) {
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          uint32_t o[16];
-          dequant32(pk.c[it], pk.sv[it], o);
-          store(it, o);
-        }
-      } else {
-#pragma unroll 1
-        for (int it = 0; it < 4; ++it) {
-          uint32_t o[16];
-          window_piece(window_ref<kWeights>(cx, sp.k0 + i, 32 * lq + 8 * it + (lane & 7)), q, lane >> 3, o);
-          store(it, o);
-        }
-      }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.v_full[q]);
-      if (more) load(i + 1);
-      return true;
-    };
-    if (sp.n > 0) {
-      load(0);
-      for (int i = 0; i < sp.n; ++i) {
-        if (!kWeights && (i & 1) && !put_k(i)) break;
-        if (!put_v(i)) break;
-      }
-    }
+    const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
+    if (!kWeights) fill_tile<kWeights, true>(cx, sp, c, entries, warp, lane);
     block_sync();                       // the tile's products are complete, l is known
     tc::tc_fence_after();
     if (*abort) break;
-    if (!kWeights) drain_o<kWeights>(cx, sp, tile, q, lq, lane);
+    if (!kWeights) drain_o<kWeights>(cx, sp, tile, warp >> 2, warp & 3, lane);
     c.add(sp.n);
+    entries += more;
     u = min(cx.u1, tstart + units);
     tstart += units;
     ++tile;
   }
 }
 
+// Warps 8-15: K, then the other half of O.
+template <bool kWeights>
+__device__ __forceinline__ void role_keys(const Ctx<kWeights>& cx) {
+  Smem<kWeights>& sm = cx.sm;
+  const int warp = (threadIdx.x >> 5) - kValWarps, lane = threadIdx.x & 31;
+  volatile int* abort = &sm.abort;
+  Count c;
+  uint32_t entries = 0;
+  int tile = cx.tile;
+  int u = cx.u0, tstart = cx.tstart;
+  while (u < cx.u1) {
+    block_sync();
+    block_sync();
+    const Span sp = span_of(sm.seg, u, cx.u1, tstart);
+    const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
+    fill_tile<kWeights, false>(cx, sp, c, entries, warp, lane);
+    block_sync();
+    tc::tc_fence_after();
+    if (*abort) break;
+    if (!kWeights) drain_o<kWeights>(cx, sp, tile, 2 + (warp >> 2), warp & 3, lane);
+    c.add(sp.n);
+    entries += more;
+    u = min(cx.u1, tstart + units);
+    tstart += units;
+    ++tile;
+  }
+}
+
+// One warp each for K and V: the codes of every entry chunk's quarters into the staging slots,
+// two tensor-map copies (one per page) a quarter.
+template <bool kWeights, bool kV>
+__device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
+  Smem<kWeights>& sm = cx.sm;
+  const DenseArgs& a = cx.a;
+  constexpr int kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort = &sm.abort;
+  uint32_t entries = 0, issued = 0;     // quarters given to the copy engine
+  int u = cx.u0, tstart = cx.tstart;
+  while (u < cx.u1) {
+    block_sync();
+    block_sync();
+    const Span sp = span_of(sm.seg, u, cx.u1, tstart);
+    const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
+    if (!(kV && kWeights)) {
+      const int nw = sm.seg.nw, i0 = sp.n - more;
+      // lane h (0, 1): page h of a chunk, a chunk ahead
+      auto page_at = [&](int i) -> int {
+        const int lp = (sm.seg.c_hi - 1 - (sp.k0 + i - nw)) * (kChunk / kPage) + (lane & 1);
+        if (i >= sp.n || (lp + 1) * kPage <= sm.seg.e_lo || lp * kPage >= sm.seg.e_hi) return -1;
+        const int p = __ldg(a.page_table + (int64_t)sm.seg.b * a.max_pages + lp);
+        return p < a.n_pages ? p : -1;
+      };
+      int next = page_at(i0);
+#pragma unroll 1
+      for (int n = 0; n < 4 * more; ++n) {
+        const int i = i0 + (n >> 2), q = n & 3;
+        const uint32_t st = 4 * entries + n, slot = st % kStage, use = st / kStage;
+        const int page = next;
+        if (q == 3) next = page_at(i + 1);
+        if (use > 0 && !warp_wait(kV ? &sm.vst_free[slot] : &sm.kst_free[slot], (use - 1) & 1, abort)) break;
+        const uint32_t have = __ballot_sync(0xffffffffu, lane < 2 && page >= 0);
+        uint64_t* full = kV ? &sm.vst_full[slot] : &sm.kst_full[slot];
+        if (lane == 0) tc::mbar_arrive_expect_tx(full, __popc(have) * (kStageBytes / 2));
+        __syncwarp();
+        if (lane < 2 && page >= 0)
+          tma::load_2d((kV ? sm.vst[slot] : sm.kst[slot]) + lane * (kStageBytes / 2), cx.map, 64 * q, page * kPage, full);
+        issued = st + 1;
+      }
+    }
+    block_sync();
+    if (*abort) break;
+    entries += more;
+    u = min(cx.u1, tstart + units);
+    tstart += units;
+  }
+  // an abandoned tile may leave copies in flight: they land before the block ends
+  if (*abort)
+    for (uint32_t st = issued > (uint32_t)kStage ? issued - kStage : 0; st < issued; ++st)
+      for (uint32_t n = 0; n < (1u << 22); ++n)
+        if (tc::mbar_try_wait(kV ? &sm.vst_full[st % kStage] : &sm.kst_full[st % kStage], (st / kStage) & 1)) break;
+}
+
 // One key of a chunk as its softmax thread sees it.
 struct KeyView {
-  bool general;        // masks, cap, bias or a rescaled window row
-  int ka, kb;          // compared with hi and lo
+  bool masked;         // some row may not see the key, or its window row is rescaled (uniform over the warp)
+  bool seen;           // what every row of a one-token tile sees
   int win;             // 1: window row
+  int j, p;            // entry index; raw position (an entry's: of its last token)
   float kf, ff;        // window row: 2^f and f
-  int p;
-  float dist;          // |t - p| when the tile holds one token
+  float dist;          // |t - p| in a one-token tile
 };
 
 // |t - p| in fp32 (exact below 2^24).
 __device__ __forceinline__ float distance(int t, int p) {
   return (float)(t > p ? (uint32_t)t - (uint32_t)p : (uint32_t)p - (uint32_t)t);
+}
+template <bool kWeights>
+__device__ __forceinline__ bool row_sees(const Ctx<kWeights>& cx, const KeyView& kv, int r) {
+  const Smem<kWeights>& sm = cx.sm;
+  if (kv.win) return (uint32_t)(sm.t[r] - kv.p) < (uint32_t)cx.a.W && kv.p >= sm.doc[r];
+  return kv.j < sm.nv[r] && kv.p - 3 >= sm.doc[r];
 }
 
 // Columns c0 .. c0+31 of this thread's key: the logits in the log2 domain as the value
@@ -683,29 +756,44 @@ __device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyVi
     const float4 m = *reinterpret_cast<const float4*>(&sm.mult[c0 + 4 * j4]);
     x[4 * j4] *= m.x; x[4 * j4 + 1] *= m.y; x[4 * j4 + 2] *= m.z; x[4 * j4 + 3] *= m.w;
   }
-  if (!kv.general) return;
   if (kv.kf != 1.f) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) x[j] *= kv.kf;
   }
   if (cx.a.cap > 0.f) {
     const float cap2 = cx.a.cap * kLog2e, inv = 1.f / cap2;
+    float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = cap2 * fast_tanh(x[j] * inv);
+    for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(x[j]));
+    if (__all_sync(0xffffffffu, top * inv < 0.55f)) {
+      // the usual case: every logit of the warp is well below the cap
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = cap2 * small_tanh(x[j] * inv);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = cap2 * fast_tanh(x[j] * inv);
+    }
   }
   if (cx.a.slopes) {
     if (sm.seg.one_t) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = fmaf(-sm.slope2[c0 + j], kv.dist, x[j]);
+      for (int j4 = 0; j4 < 8; ++j4) {
+        const float4 m = *reinterpret_cast<const float4*>(&sm.slope2[c0 + 4 * j4]);
+        x[4 * j4] = fmaf(-m.x, kv.dist, x[4 * j4]); x[4 * j4 + 1] = fmaf(-m.y, kv.dist, x[4 * j4 + 1]);
+        x[4 * j4 + 2] = fmaf(-m.z, kv.dist, x[4 * j4 + 2]); x[4 * j4 + 3] = fmaf(-m.w, kv.dist, x[4 * j4 + 3]);
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = fmaf(-sm.slope2[c0 + j], distance(sm.hi[1][c0 + j], kv.p), x[j]);
+      for (int j = 0; j < 32; ++j) x[j] = fmaf(-sm.slope2[c0 + j], distance(sm.t[c0 + j], kv.p), x[j]);
     }
   }
+  if (!kv.masked) return;
+  if (sm.seg.one_t) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const bool seen = kv.ka < sm.hi[kv.win][c0 + j] && kv.kb >= sm.lo[kv.win][c0 + j];
-    x[j] = seen ? x[j] + kv.ff : -INFINITY;
+    for (int j = 0; j < 32; ++j) x[j] = kv.seen ? x[j] + kv.ff : -INFINITY;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = kv.seen && row_sees<kWeights>(cx, kv, c0 + j) ? x[j] + kv.ff : -INFINITY;
   }
 }
 
@@ -713,7 +801,7 @@ template <bool kWeights>
 __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
-  const int st = threadIdx.x - kDeqThreads, warp = st >> 5, lane = st & 31;
+  const int st = threadIdx.x - kSoftFirst, warp = st >> 5, lane = st & 31;
   const int lq = warp & 3, half = warp >> 2;   // lane quarter; attention: rows 32 half .. +31, weights: chunks of that parity
   const int key = 32 * lq + lane;              // thread = key of the chunk = tensor-memory lane
   const uint32_t lane_q = (uint32_t)(32 * lq) << 16;
@@ -765,10 +853,9 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       } else if (kWeights) {
         nref = -INFINITY;
       }
-      sm.hi[0][st] = r.nv;
-      sm.lo[0][st] = r.doc;
-      sm.hi[1][st] = r.t;
-      sm.lo[1][st] = r.w_n > 0 ? r.w_lo : INT_MAX;
+      sm.nv[st] = r.nv;
+      sm.doc[st] = r.doc;
+      sm.t[st] = r.t;
       sm.slope2[st] = slope * kLog2e;
       sm.nref[st] = nref;
     }
@@ -788,11 +875,11 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
     const int units = max(1, sm.seg.n_chunks), nw = sm.seg.nw;
     const int e_lo = sm.seg.e_lo, e_hi = sm.seg.e_hi, c_hi = sm.seg.c_hi;
 
-    // The key of a chunk; its page (and position) are read one chunk ahead.
+    // The key of a chunk; its page is read one chunk ahead.
     auto entry_of = [&](int i) -> int { return (c_hi - 1 - (sp.k0 + i - nw)) * kChunk + key; };
-    auto page_ahead = [&](int i) -> int { return page_of<kWeights>(cx, sp.k0 + i, key, i < sp.n); };
     constexpr int kStep = kWeights ? 2 : 1;
     const int first = kWeights ? half : 0;
+    auto page_ahead = [&](int i) -> int { return page_of<kWeights>(cx, entry_of(i), i < sp.n && sp.k0 + i >= nw); };
     int page = page_ahead(first);
     auto view = [&](int i, int64_t* slot) -> KeyView {
       KeyView kv;
@@ -800,15 +887,14 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       kv.win = k < nw;
       kv.kf = 1.f;
       kv.ff = 0.f;
+      kv.j = 0;
       *slot = -1;
       if (kv.win) {
         const int64_t p = (int64_t)sm.seg.w_lo + (int64_t)k * kChunk + key;
-        const bool have = p <= sm.seg.w_hi;
-        kv.p = have ? (int)p : 0;
-        kv.ka = have ? kv.p - 1 : INT_MAX;
-        kv.kb = kv.p;
-        kv.general = true;
-        if (have) {
+        kv.seen = p <= sm.seg.w_hi;
+        kv.p = kv.seen ? (int)p : 0;
+        kv.masked = true;
+        if (kv.seen) {
           const int f = window_exp(__ldg(a.swa_scales + (int64_t)b * a.swa_cap + (kv.p - sm.seg.pos0)));
           if (f != 0) {
             kv.kf = pow2i(f);
@@ -816,17 +902,17 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
           }
         }
       } else {
-        const int j = entry_of(i), e0 = j - key;
-        const bool have = j >= e_lo && j < e_hi && page >= 0 && page < a.n_pages;
-        if (have) *slot = (int64_t)page * kPage + (j & (kPage - 1));
-        kv.p = a.entry_pos && have ? __ldg(a.entry_pos + *slot) : (int)min(4 * ((int64_t)j + shift) + 3, (int64_t)INT_MAX);
-        kv.ka = have ? j : INT_MAX;
-        kv.kb = max(kv.p, INT_MIN + 3) - 3;
-        kv.general = a.cap > 0.f || a.slopes || e0 < sm.seg.all_lo || e0 + kChunk > sm.seg.all_hi ||
-                     __any_sync(0xffffffffu, !have);
+        const int e0 = entry_of(i) - key;
+        kv.j = entry_of(i);
+        kv.seen = kv.j >= e_lo && kv.j < e_hi && page >= 0 && page < a.n_pages;
+        if (kv.seen) *slot = (int64_t)page * kPage + (kv.j & (kPage - 1));
+        kv.p = a.entry_pos && kv.seen ? max(__ldg(a.entry_pos + *slot), INT_MIN + 3)
+                                      : (int)min(4 * ((int64_t)kv.j + shift) + 3, (int64_t)INT_MAX);
+        kv.masked = e0 < sm.seg.all_lo || e0 + kChunk > sm.seg.all_hi || __any_sync(0xffffffffu, !kv.seen);
       }
       page = page_ahead(i + kStep);
       kv.dist = distance(sm.seg.t, kv.p);
+      if (sm.seg.one_t) kv.seen = kv.seen && row_sees<kWeights>(cx, kv, 0);
       return kv;
     };
 
@@ -842,7 +928,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
 #pragma unroll 1
         for (int c0 = 0; c0 < kRows; c0 += 32) {
           float x[32];
-          load_logits<kWeights>(cx, kv, cx.tm + kColS + 64 * (i & 1) + c0 + lane_q, c0, x);
+          load_logits<kWeights>(cx, kv, cx.tm + Cols<true>::S + 64 * (i & 1) + c0 + lane_q, c0, x);
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j4 = 0; j4 < 8; ++j4) {
@@ -870,11 +956,11 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       const int c0 = 32 * half;
       for (int i = 0; i < sp.n; ++i) {
         const int e = i & 1;
-        const uint32_t ph = c.phase(i), ts = cx.tm + kColS + 64 * e + c0 + lane_q;
+        const uint32_t ph = c.phase(i), ts = cx.tm + Cols<false>::S + c0 + lane_q;
         if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + i);
         int64_t slot;
         const KeyView kv = view(i, &slot);
-        const bool ok = warp_wait(&sm.s_full[e], ph & 1, abort);
+        const bool ok = warp_wait(&sm.s_full[0], (c.all + i) & 1, abort);
         tc::tc_fence_after();
         // ---- logits over the reference, and whether one outgrows it
         float x[32];
@@ -914,7 +1000,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
           }
           if (half_or(half, need)) {
             // O^T *= alpha (column = row of the tile): the value products so far must be done
-            if (c.all + i > 0) warp_wait(&sm.pv_done[3], (c.all + i - 1) & 1, abort);
+            if (c.all + i > 0) warp_wait(&sm.v_free[3], (c.all + i - 1) & 1, abort);
             tc::tc_fence_after();
 #pragma unroll 1
             for (int mt = 0; mt < 4; ++mt) {
@@ -937,7 +1023,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         }
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.s_free[e]);
+        if (lane == 0) tc::mbar_arrive(&sm.s_free[0]);
         // ---- P = exp2(l - m_ref), rounded to fp16 for the value product
         const float pf = pow2i(-(int)kv.ff);   // the normaliser adds p = 2^-f (2^f p)
         uint32_t pk[16];
@@ -965,7 +1051,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       }
       if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + sp.n);
       // all products of the tile, and the row sums over its keys
-      if (sp.n > 0) warp_wait(&sm.pv_done[3], (c.all + sp.n - 1) & 1, abort);
+      if (sp.n > 0) warp_wait(&sm.v_free[3], (c.all + sp.n - 1) & 1, abort);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float y[16];
@@ -998,18 +1084,18 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
   }
 }
 
-// Order of the products of a tile's chunks A (even) and B (odd), A' the next even one:
-//   S(A) | S(B) from tensor memory | PV(A) | PV(B) | S(A') ...
-// softmax(A) runs under S(B), softmax(B) under PV(A); B takes A's shared-memory tile quarter
-// by quarter behind PV(A), A' takes B's behind PV(B).
+// Order of the products: S(0) | S(1) PV(0) | S(2) PV(1) | ...
 template <bool kWeights>
 __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   volatile int* abort = &sm.abort;
-  constexpr uint32_t kIdS = tc::idesc_f16(128, kRows, 0, 0, 0);   // K-major A and B
+  constexpr uint32_t kIdS = tc::idesc_f16(128, kRows, 0, 0, 0);   // K-major A (tensor memory) and B
   constexpr uint32_t kIdO = tc::idesc_f16(128, kRows, 0, 1, 1);   // MN-major A and B
   constexpr uint32_t kHiS = desc_hi(8192), kHiO = desc_hi(128);
-  const uint32_t dq = desc_lo(sm.q, 128), dk = desc_lo(sm.v, 128), dv = desc_lo(sm.v, 8192), dp = desc_lo(sm.p, 1024);
+  constexpr int kRing = Cols<kWeights>::ring;
+  const uint32_t dq = desc_lo(sm.q, 128), dv = desc_lo(sm.v, 2048), dp = desc_lo(sm.p, 1024);
+  const uint32_t leader = elect_lane();
+  const int lane = threadIdx.x & 31;
   Count c;
   int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
@@ -1017,70 +1103,51 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
     block_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks);
-    {
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        // the warp votes, so that its control flow stays uniform
+    // Round i does S(i + 1), then PV(i), in steps
+    //   0 S buffer free   1-4 a quarter of K there: its products   5 P there   6-9 a quarter of V there: its products
+    // Lane n looks at the barrier of step n, so that one look (a trip through the busy shared
+    // memory pipe) tells of all the round's steps.
+    bool ok = true;
 #pragma unroll 1
-        for (uint32_t i = 0; i < (1u << 24); ++i) {
-          if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
-          if ((i & 255) == 255 && __any_sync(0xffffffffu, *abort != 0)) return false;
+    for (int i = -1; ok && i < sp.n; ++i) {
+      const bool more = i + 1 < sp.n;
+      const uint32_t cs = c.all + i + 1, cv = c.all + i;      // running numbers of the two chunks
+      const int es = kWeights ? (i + 1) & 1 : 0, ev = i & 1;
+      const uint32_t ps = kWeights ? c.phase(i + 1) : cs, pv = c.phase(max(i, 0));
+      const int first = !more ? 5 : ps > 0 ? 0 : 1, last = kWeights || i < 0 ? 4 : 9;
+      const uint32_t bar = tc::smem_addr(lane == 0 ? &sm.s_free[es] : lane <= 4 ? &sm.kq_full[lane - 1]
+                                                  : lane == 5 ? &sm.p_full[ev] : &sm.v_full[(lane - 6) & 3]);
+      const uint32_t parity = (lane == 0 ? ps - 1 : lane <= 4 ? cs : lane == 5 ? pv : cv) & 1;
+      uint32_t ready = 0;
+#pragma unroll 1
+      for (int step = first; step <= last; ++step) {
+        uint32_t n = 0;
+#pragma unroll 1
+        while (!(ready >> step & 1)) {
+          ready = __ballot_sync(0xffffffffu, mbar_test(bar, parity));
+          if ((++n & 255) == 0 && (n >> 24 || __any_sync(0xffffffffu, *abort != 0))) break;
         }
-        *abort = 1;
-        return false;
-      };
-      auto scores = [&](int i) -> bool {
-        const int e = i & 1;
-        const uint32_t ph = c.phase(i);
-        const uint32_t d = cx.tm + kColS + 64 * e;
-        if (ph > 0 && !wait(&sm.s_free[e], (ph - 1) & 1)) return false;
-#pragma unroll 1
-        for (uint32_t q = 0; q < 4; ++q) {
-          if (kWeights || e == 0) {
-            if (!wait(&sm.v_full[q], (c.all + i) & 1)) return false;
-            tc::tc_fence_after();
-#pragma unroll
-            for (uint32_t ks = 0; ks < 8; ++ks)
-              mma_ss<kHiS, kHiS, kIdS>(d, dk + (8 * q + ks) * 16, dq + (8 * q + ks) * 16, q | ks);
-            if (kWeights) mma_commit_elected(&sm.pv_done[q]);
-          } else {
-            if (!wait(&sm.kq_full[q], ph & 1)) return false;
-            tc::tc_fence_after();
-#pragma unroll
-            for (uint32_t ks = 0; ks < 8; ++ks)
-              mma_ts<kHiS, kIdS>(d, cx.tm + kColK + 64 * (q & 1) + 8 * ks, dq + (8 * q + ks) * 16, q | ks);
-            mma_commit_elected(&sm.kq_free[q]);
-          }
+        ok = ready >> step & 1;
+        if (!ok) {
+          *abort = 1;
+          break;
         }
-        mma_commit_elected(&sm.s_full[e]);
-        return true;
-      };
-      auto values = [&](int i) -> bool {
-        const int e = i & 1;
-        if (!wait(&sm.p_full[e], c.phase(i) & 1)) return false;
-#pragma unroll 1
-        for (uint32_t mt = 0; mt < 4; ++mt) {
-          if (!wait(&sm.v_full[mt], (c.all + i) & 1)) return false;
-          tc::tc_fence_after();
+        tc::tc_fence_after();
+        if (step >= 1 && step <= 4) {
+          const uint32_t q = step - 1, ka = cx.tm + Cols<kWeights>::K + 64 * ((4 * cs + q) % kRing);
+          const uint32_t d = cx.tm + Cols<kWeights>::S + 64 * es;
+#pragma unroll
+          for (uint32_t ks = 0; ks < 8; ++ks) mma_ts<kHiS, kIdS>(leader, d, ka + 8 * ks, dq + (8 * q + ks) * 16, q | ks);
+          mma_commit_by(leader, &sm.kq_free[q]);
+          if (step == 4) mma_commit_by(leader, &sm.s_full[es]);
+        } else if (!kWeights && step >= 6) {
+          const uint32_t mt = step - 6, va = dv + ((4 * cv + mt) % kVSlots) * (kChunk * kQuarter * 2 / 16);
 #pragma unroll
           for (uint32_t kk = 0; kk < 8; ++kk)
-            mma_ss<kHiO, kHiO, kIdO>(cx.tm + kColO + 64 * mt, dv + mt * 128 + kk * 1024,
-                                     dp + e * (kChunk * kRows * 2 / 16) + kk * 128, (uint32_t)i | kk);
-          mma_commit_elected(&sm.pv_done[mt]);
-        }
-        mma_commit_elected(&sm.p_free[e]);
-        return true;
-      };
-      if (kWeights) {
-        for (int i = 0; i < sp.n; ++i)
-          if (!scores(i)) break;
-      } else {
-        bool ok = true;
-        for (int i = 0; ok && i < sp.n; i += 2) {   // S(A) S(B) PV(A) PV(B)
-          const int end = min(i + 2, sp.n);
-#pragma unroll 1
-          for (int j = i; ok && j < end; ++j) ok = scores(j);
-#pragma unroll 1
-          for (int j = i; ok && j < end; ++j) ok = values(j);
+            mma_ss<kHiO, kHiO, kIdO>(leader, cx.tm + kColO + 64 * mt, va + kk * 256,
+                                     dp + ev * (kChunk * kRows * 2 / 16) + kk * 128, (uint32_t)i | kk);
+          mma_commit_by(leader, &sm.v_free[mt]);
+          if (step == 9) mma_commit_by(leader, &sm.p_free[ev]);
         }
       }
     }
@@ -1093,9 +1160,9 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
   }
 }
 
-// The warp after the MMA warp: the packed pages of the chunks ahead into L2.  The last two: barriers only.
+// The last warp: the packed pages of the chunks ahead into L2.
 template <bool kWeights>
-__device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx, bool active) {
+__device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   volatile int* abort = &sm.abort;
@@ -1108,7 +1175,7 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx, bool acti
     block_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks);
-    if (active) {
+    {
       auto request = [&](int i) {
         const int k = sp.k0 + i;
         if (i >= sp.n || k < sm.seg.nw || lane >= 4) return;
@@ -1144,7 +1211,7 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx, bool acti
 }
 
 template <bool kWeights>
-__global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, uint32_t* status) {
+__global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, const __grid_constant__ CUtensorMap map, uint32_t* status) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem<kWeights>& sm = *reinterpret_cast<Smem<kWeights>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -1154,7 +1221,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
       tc::mbar_init(&sm.kq_full[i], 4);
       tc::mbar_init(&sm.kq_free[i], 1);
       tc::mbar_init(&sm.v_full[i], 4);
-      tc::mbar_init(&sm.pv_done[i], 1);
+      tc::mbar_init(&sm.v_free[i], 1);
+    }
+    for (int i = 0; i < Stages<kWeights>::K; ++i) {
+      tc::mbar_init(&sm.kst_full[i], 1);
+      tc::mbar_init(&sm.kst_free[i], 4);
+    }
+    for (int i = 0; i < Stages<kWeights>::V; ++i) {
+      tc::mbar_init(&sm.vst_full[i], 1);
+      tc::mbar_init(&sm.vst_free[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
@@ -1166,7 +1241,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
     sm.progress = 0;
     tc::mbar_fence_init();
   }
-  if (warp == kDeqWarps + kSoftWarps) tc::tmem_alloc(&sm.tmem, kTmemCols);
+  if (warp == kMmaWarp) tc::tmem_alloc(&sm.tmem, kTmemCols);
   pdl_wait();
 
   // ---- this CTA's share of the chunks of all tiles (their number is below 2^31)
@@ -1199,27 +1274,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tm = sm.tmem;
-  Ctx<kWeights> cx{a, pl, sm, tm, u0, u1, sm.found_tile, sm.found_start, status};
+  Ctx<kWeights> cx{a, pl, sm, tm, u0, u1, sm.found_tile, sm.found_start, status, &map};
   if (u1 <= u0) cx.tile = 0;
   if (!kWeights && tid == 0) pl.cont[g] = (u1 > u0 && cx.tstart < u0) ? cx.tile : -1;
 
   // ---- roles, each with its own walk over the tiles (every walk meets the same barriers)
-  if (warp < kDeqWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDeq));
-    role_dequant<kWeights>(cx);
-  } else if (warp < kDeqWarps + kSoftWarps) {
+  if (warp < kValWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill));
+    role_values<kWeights>(cx);
+  } else if (warp < kValWarps + kKeyWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill));
+    role_keys<kWeights>(cx);
+  } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     role_softmax<kWeights>(cx);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
-    if (warp == kDeqWarps + kSoftWarps)
+    if (warp == kMmaWarp)
       role_mma<kWeights>(cx);
+    else if (warp == kMmaWarp + 1)
+      role_stage<kWeights, false>(cx);
+    else if (warp == kMmaWarp + 2)
+      role_stage<kWeights, true>(cx);
     else
-      role_prefetch<kWeights>(cx, warp == kDeqWarps + kSoftWarps + 1);
+      role_prefetch<kWeights>(cx);
   }
   tc::tc_fence_before();
   block_sync();
-  if (warp == kDeqWarps + kSoftWarps) tc::tmem_dealloc(tm, kTmemCols);
+  if (warp == kMmaWarp) tc::tmem_dealloc(tm, kTmemCols);
   if (tid == 0 && sm.abort) raise_status(status, CSA2_STATUS_TIMEOUT);
 }
 
@@ -1377,7 +1459,7 @@ cudaError_t prepare_kernel() {
   cudaFuncAttributes at;
   cudaError_t e = cudaFuncGetAttributes(&at, k_dense_tc<kWeights>);
   if (e != cudaSuccess) return e;
-  static_assert(4 * kRegsDeq + 2 * kRegsSoft + kRegsMisc <= 7 * kRegsLaunch, "register split");
+  static_assert(4 * kRegsFill + 2 * kRegsSoft + kRegsMisc <= 7 * kRegsLaunch, "register split");
   if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(k_dense_tc<kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)sizeof(Smem<kWeights>));
@@ -1410,11 +1492,25 @@ size_t dense_attn_workspace_bytes(const csa2_dims* dm, int max_entries) {
   return up((size_t)kMaxCtas * 4) + (size_t)ctas * 2 * kPartFloats * sizeof(float);
 }
 
+// The packed codes as rows of 256 bytes; a box is one quarter of a page's 64 entries.
+static bool codes_map(const DenseArgs& a, CUtensorMap* map) {
+  const cuuint64_t dims[2] = {(cuuint64_t)(kD / 2), (cuuint64_t)a.n_pages * kPage};
+  const cuuint64_t strides[1] = {(cuuint64_t)(kD / 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)(kQuarter / 2), (cuuint32_t)kPage};
+  const cuuint32_t estr[2] = {1, 1};
+  return tensor_map_encoder() &&
+         tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.kv_codes), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_dense_attn_tc(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = device_sms(&sms);
   if (e == cudaSuccess) e = prepare_kernel<false>();
   if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!codes_map(a, &map)) return cudaErrorInvalidValue;
   Plan pl = {};
   const int all = tiles_of(dm);
   pl.cont = static_cast<int32_t*>(ws);
@@ -1426,7 +1522,7 @@ cudaError_t launch_dense_attn_tc(const csa2_dims* dm, const DenseArgs& a, void* 
     pl.tile0 = t0;
     pl.tiles = std::min(slab, all - t0);
     pl.n_ctas = (int)std::min<int64_t>(std::min(sms, kMaxCtas), per_tile * pl.tiles);
-    e = launch_step(k_dense_tc<false>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<false>), s, a, pl, status_word());
+    e = launch_step(k_dense_tc<false>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<false>), s, a, pl, map, status_word());
     if (e != cudaSuccess) return e;
     if (pl.n_ctas == 1) continue;
     const unsigned shared = (unsigned)std::min<int64_t>((int64_t)a.B * pl.tiles, pl.n_ctas - 1);
@@ -1449,6 +1545,8 @@ cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, voi
   if (e == cudaSuccess) e = prepare_kernel<true>();
   if (e != cudaSuccess) return e;
   const int all = tiles_of(dm);
+  CUtensorMap map;
+  if (!codes_map(a, &map)) return cudaErrorInvalidValue;
   Plan pl = {};
   const int64_t per_tile = (int64_t)a.B * max_chunks(a.max_entries, 0, 0);
   const int slab = std::min(launch_tiles(per_tile, all), all <= 1 ? 1 : slab_tiles(dm, a.max_entries, &pl.sum_stride));
@@ -1463,7 +1561,7 @@ cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, voi
       e = launch_step(k_weights_ranges, dim3((unsigned)(((int64_t)a.B * pl.tiles + 127) / 128)), dim3(128), 0, s, a, pl);
       if (e != cudaSuccess) return e;
     }
-    e = launch_step(k_dense_tc<true>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<true>), s, a, pl, status_word());
+    e = launch_step(k_dense_tc<true>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<true>), s, a, pl, map, status_word());
     if (e != cudaSuccess) return e;
     if (all > 1) {
       e = launch_step(k_weights_sum, dim3((unsigned)((a.max_entries + 255) / 256), (unsigned)a.B), dim3(256), 0, s, a, pl,
