@@ -53,14 +53,13 @@ constexpr int kD = 512;
 constexpr int kRows = 64;                 // rows of a tile (N of both products)
 constexpr int kChunk = 128;               // keys of a chunk
 constexpr int kValWarps = 8, kKeyWarps = 8, kSoftWarps = 8;
-constexpr int kValThreads = kValWarps * 32;
 constexpr int kSoftFirst = (kValWarps + kKeyWarps) * 32;   // first softmax thread
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = 896;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
 constexpr int kMmaWarp = kValWarps + kKeyWarps + kSoftWarps;
 constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
-// registers per thread after the split of the seven warpgroups: 4 x 56 + 2 x 120 + 40 = 7 x 72
-constexpr int kRegsLaunch = 72, kRegsFill = 56, kRegsSoft = 120, kRegsMisc = 40;
+// registers per thread after the split of the seven warpgroups: 4 x 64 + 2 x 104 + 40 = 7 x 72
+constexpr int kRegsLaunch = 72, kRegsFill = 64, kRegsSoft = 104, kRegsMisc = 40;
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory.  Attention: O^T (four M-tiles of 64 columns), S^T, and a ring of three
 // quarters of K (64 columns each: 128 channels of fp16).  Weights: two S^T, a ring of four.
@@ -141,7 +140,11 @@ struct Plan {
 };
 
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory"); }
-__device__ __forceinline__ void val_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kValThreads) : "memory"); }
+constexpr int kFillThreads = (kValWarps + kKeyWarps) * 32;
+__device__ __forceinline__ void fill_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kFillThreads) : "memory"); }
+// The softmax warps announce a tile's chunks (seg) to the last warpgroup.
+__device__ __forceinline__ void seg_arrive() { asm volatile("bar.arrive 5, %0;" ::"n"(kSoftThreads + 128) : "memory"); }
+__device__ __forceinline__ void seg_sync() { asm volatile("bar.sync 5, %0;" ::"n"(kSoftThreads + 128) : "memory"); }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
 // The 128 threads of one half of the softmax warps (32 rows).
 __device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(3 + half) : "memory"); }
@@ -470,58 +473,59 @@ __device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp,
 // Quarter number n = 4 chunk + q goes where number n - ring was; barriers belong to quarters
 // (and staging slots to one group of warps), so that a warp waits for consecutive phases.
 template <bool kWeights, bool kV>
-__device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, const Span& sp, const Count& c, uint32_t entries, int warp,
+__device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n_chunks, uint32_t chunks, uint32_t entries, int warp,
                                           int lane) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   constexpr int kRing = kV ? kVSlots : Cols<kWeights>::ring, kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
+  constexpr bool kEarly = kStage <= 2;   // one slot for each four warps: it is wanted back at once
   const int lq = warp & 3, odd = warp >> 2, key = 32 * lq + lane;
   volatile int* abort = &sm.abort;
-  const int nw = sm.seg.nw, c_hi = sm.seg.c_hi;
-  const int i0 = min(max(nw - sp.k0, 0), sp.n);   // first entry chunk of the span
-  auto entry_of = [&](int i) -> int { return (c_hi - 1 - (sp.k0 + i - nw)) * kChunk + key; };
-  // scales of the key's two quarters, a chunk ahead (its page another chunk ahead); no key, or one
-  // behind a bad page: zero, so that whatever codes the staging slot holds become zeros
-  uint2 sc[2], sn[2];
-  int page = page_of<kWeights>(cx, entry_of(i0), i0 < sp.n);
-  auto load_scales = [&](int i, uint2 (&o)[2]) {
-    o[0] = o[1] = make_uint2(0, 0);
-    if (i >= sp.n) return;
-    const int j = entry_of(i);
-    if (j >= sm.seg.e_lo && j < sm.seg.e_hi) {
-      if (page >= 0 && page < a.n_pages) {
-        const uint2* p = reinterpret_cast<const uint2*>(
-            a.kv_scales + ((int64_t)page * kPage + (j & (kPage - 1))) * (kD / 16) + 8 * odd);
-        o[0] = __ldg(p);
-        o[1] = __ldg(p + 2);
-      } else if (!kV && odd == 0) {
-        raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
-      }
+  const int i0 = min(max(sm.seg.nw - k0, 0), n_chunks);   // first entry chunk of the span
+  const int j0 = (sm.seg.c_hi - 1 - (k0 - sm.seg.nw)) * kChunk + key;   // the key's entry in chunk 0 (128 less a chunk)
+  // The scales of a step's quarter, a step ahead (the key's page a chunk ahead); no key, or one behind
+  // a bad page: zero, so that whatever codes the staging slot holds become zeros.
+  int page = page_of<kWeights>(cx, j0 - i0 * kChunk, i0 < n_chunks), page1 = -1;
+  auto scales_of = [&](int n) -> uint2 {
+    const int i = n >> 1, j = j0 - i * kChunk;
+    if (i < i0 || i >= n_chunks) return make_uint2(0, 0);
+    if ((n & 1) == 0) {
+      if (i > i0) page = page1;
+      page1 = page_of<kWeights>(cx, j - kChunk, i + 1 < n_chunks);
     }
-    page = page_of<kWeights>(cx, entry_of(i + 1), i + 1 < sp.n);
+    if (j < sm.seg.e_lo || j >= sm.seg.e_hi) return make_uint2(0, 0);
+    if (page < 0 || page >= a.n_pages) {
+      if (!kV && odd == 0) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
+      return make_uint2(0, 0);
+    }
+    return __ldg(reinterpret_cast<const uint2*>(a.kv_scales + ((int64_t)page * kPage + (j & (kPage - 1))) * (kD / 16) + 8 * odd) +
+                 2 * (n & 1));
   };
-  load_scales(i0, sn);
+  uint2 next = scales_of(2 * i0);
   const uint32_t dst_k = cx.tm + Cols<kWeights>::K + ((uint32_t)(32 * lq) << 16);
   unsigned char* dst_v = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 2048 + (key & 7) * 16;
 #pragma unroll 1
-  for (int n = 0; n < 2 * sp.n; ++n) {
-    const int i = n >> 1, k = sp.k0 + i, q = odd + 2 * (n & 1);
-    const uint32_t cc = c.all + i, number = 4 * cc + q;
-    const bool window = k < nw;             // uniform
-    if (!window && (n & 1) == 0) {
-      sc[0] = sn[0];
-      sc[1] = sn[1];
-      load_scales(i + 1, sn);
-    }
+  for (int n = 0; n < 2 * n_chunks; ++n) {
+    const int i = n >> 1, q = odd + 2 * (n & 1);
+    const uint32_t number = 4 * (chunks + i) + q;
+    const bool window = i < i0;             // uniform
+    const uint2 s = next;
+    if (n >= 2 * i0) next = scales_of(n + 1);
+    const uint32_t st = 4 * (entries + (i - i0)) + q;   // running number among the staged quarters
     uint4 t[4];
     if (!window) {
-      const uint32_t st = 4 * (entries + (i - i0)) + q, slot = st % kStage, use = st / kStage;
+      const uint32_t slot = st % kStage, use = st / kStage;
       if (!warp_wait(kV ? &sm.vst_full[slot] : &sm.kst_full[slot], use & 1, abort)) break;
       const unsigned char* src = (kV ? sm.vst[slot] : sm.kst[slot]) + 64 * key;
 #pragma unroll
       for (int p = 0; p < 4; ++p) t[p] = *reinterpret_cast<const uint4*>(src + 16 * (p ^ ((key >> 1) & 3)));
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(kV ? &sm.vst_free[slot] : &sm.kst_free[slot]);
+      // The slot may be written again once the loads have arrived, not when they are issued: the vote
+      // reads a word of each (lane 0 always votes yes).  With many slots that can wait for the quarter's end.
+      if (kEarly) {
+        const uint32_t any = t[0].x ^ t[1].x ^ t[2].x ^ t[3].x;
+        if (__ballot_sync(0xffffffffu, lane == 0 || any == 0x5A5A5A5Au) & (lane == 0))
+          tc::mbar_arrive(kV ? &sm.vst_free[slot] : &sm.kst_free[slot]);
+      }
     }
     if (number >= (uint32_t)kRing &&
         !warp_wait(kV ? &sm.v_free[(q - kRing) & 3] : &sm.kq_free[(q - kRing) & 3], ((number - kRing) >> 2) & 1, abort))
@@ -538,7 +542,6 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, const Span& s
       }
     };
     if (!window) {
-      const uint2 s = (n & 1) ? sc[1] : sc[0];
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
         uint32_t o[8];
@@ -546,7 +549,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, const Span& s
         put(p, o);
       }
     } else {
-      const KeyRef w = window_ref<kWeights>(cx, k, key);
+      const KeyRef w = window_ref<kWeights>(cx, k0 + i, key);
 #pragma unroll 1
       for (int p = 0; p < 8; ++p) {
         uint32_t o[8];
@@ -562,7 +565,10 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, const Span& s
       tc::tc_fence_before();
     }
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(kV ? &sm.v_full[q] : &sm.kq_full[q]);
+    if (lane == 0) {
+      tc::mbar_arrive(kV ? &sm.v_full[q] : &sm.kq_full[q]);
+      if (!kEarly && !window) tc::mbar_arrive(kV ? &sm.vst_free[st % kStage] : &sm.kst_free[st % kStage]);
+    }
   }
 }
 // Entry chunks of a span (the others are window chunks).
@@ -570,97 +576,72 @@ __device__ __forceinline__ int entry_chunks(const Segment& sg, const Span& sp) {
   return sp.n - min(max(sg.nw - sp.k0, 0), sp.n);
 }
 
-// Warps 0-7: Q, then V, then half of O.
+// Warps 0-7 fill V, warps 8-15 K; before that they bring in the tile's Q, after it they write O.
 template <bool kWeights>
-__device__ __forceinline__ void role_values(const Ctx<kWeights>& cx) {
+__device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool values = tid < kValWarps * 32;
+  const int warp = (tid >> 5) - (values ? 0 : kValWarps);
   volatile int* abort = &sm.abort;
-  Count c;
-  uint32_t entries = 0;
+  uint32_t chunks = 0, entries = 0;
   int tile = cx.tile;
   int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
-    block_sync();                       // the previous tile is done
-    // ---- Q rows -> fp16 B operand, row r scaled by 2^-e_r (exact); read twice (the second time from L2)
+    // ---- Q rows -> fp16 B operand, row r scaled by 2^-e_r (exact)
     const int b = tile / cx.pl.tiles;
     const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
     const int64_t rows = (int64_t)a.Tq * a.Hq;
-    if (tid < kRows) sm.qexp[1][tid] = 0;
-    val_sync();
-    // step g: row 8 (g / 2) + tid % 8, channels 8 c8 .. +7 with c8 = tid / 8 + 32 (g % 2)
-    auto q_load = [&](int g) -> uint4 {
-      const int h = 8 * (g >> 1) + (tid & 7), c8 = (tid >> 3) + 32 * (g & 1);
-      return r0 + h < rows ? __ldg(reinterpret_cast<const uint4*>(a.Q + ((int64_t)b * rows + r0 + h) * kD + c8 * 8))
-                           : make_uint4(0, 0, 0, 0);
-    };
-#pragma unroll 4
-    for (int g = 0; g < 16; ++g) {
-      const uint4 v = q_load(g);
-      uint32_t e = 0;
+    {
+      uint4 qv[8];                      // row 8 g + tid % 8, channels 8 (tid / 8) .. +7
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = word_of(v, j);
-        e = max(e, max((w >> 7) & 0xFFu, (w >> 23) & 0xFFu));
+      for (int g = 0; g < 8; ++g) {
+        const int h = 8 * g + (tid & 7);
+        qv[g] = r0 + h < rows ? __ldg(reinterpret_cast<const uint4*>(a.Q + ((int64_t)b * rows + r0 + h) * kD + (tid >> 3) * 8))
+                              : make_uint4(0, 0, 0, 0);
       }
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
-      if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * (g >> 1) + lane], (int)e);
-    }
-    val_sync();
-#pragma unroll 4
-    for (int g = 0; g < 16; ++g) {
-      const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * (g >> 1) + (tid & 7)]));
-      const uint4 v = q_load(g);
-      uint32_t ov[4];
+      if (tid < kRows) sm.qexp[1][tid] = 0;
+      fill_sync();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = word_of(v, j);
-        ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
+      for (int g = 0; g < 8; ++g) {
+        uint32_t e = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e = max(e, max(word_of(qv[g], j) & 0x7F80u, (word_of(qv[g], j) >> 16) & 0x7F80u));
+        e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
+        e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
+        if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * g + lane], (int)(e >> 7));
       }
-      *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + (g >> 1) * 8192 +
-                                ((tid >> 3) + 32 * (g & 1)) * 128 + (tid & 7) * 16) = make_uint4(ov[0], ov[1], ov[2], ov[3]);
+      fill_sync();
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * g + (tid & 7)]));
+        uint32_t ov[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = word_of(qv[g], j);
+          ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + g * 8192 + (tid >> 3) * 128 + (tid & 7) * 16) =
+            make_uint4(ov[0], ov[1], ov[2], ov[3]);
+      }
     }
     if (tid < kRows) sm.mult[tid] = a.scale * kLog2e * pow2i(q_head_exp(sm.qexp[1][tid]));
     tc::fence_async_smem();
-    block_sync();                       // Q, row constants and the tile's chunks are there
+    tc::tc_fence_before();
+    block_sync();                       // Q, row constants and the tile's chunks are there, O of the last tile is not
+    tc::tc_fence_after();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
-    if (!kWeights) fill_tile<kWeights, true>(cx, sp, c, entries, warp, lane);
+    if (!values)
+      fill_tile<kWeights, false>(cx, sp.k0, sp.n, chunks, entries, warp, lane);
+    else if (!kWeights)
+      fill_tile<kWeights, true>(cx, sp.k0, sp.n, chunks, entries, warp, lane);
     block_sync();                       // the tile's products are complete, l is known
     tc::tc_fence_after();
     if (*abort) break;
-    if (!kWeights) drain_o<kWeights>(cx, sp, tile, warp >> 2, warp & 3, lane);
-    c.add(sp.n);
-    entries += more;
-    u = min(cx.u1, tstart + units);
-    tstart += units;
-    ++tile;
-  }
-}
-
-// Warps 8-15: K, then the other half of O.
-template <bool kWeights>
-__device__ __forceinline__ void role_keys(const Ctx<kWeights>& cx) {
-  Smem<kWeights>& sm = cx.sm;
-  const int warp = (threadIdx.x >> 5) - kValWarps, lane = threadIdx.x & 31;
-  volatile int* abort = &sm.abort;
-  Count c;
-  uint32_t entries = 0;
-  int tile = cx.tile;
-  int u = cx.u0, tstart = cx.tstart;
-  while (u < cx.u1) {
-    block_sync();
-    block_sync();
-    const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
-    fill_tile<kWeights, false>(cx, sp, c, entries, warp, lane);
-    block_sync();
-    tc::tc_fence_after();
-    if (*abort) break;
-    if (!kWeights) drain_o<kWeights>(cx, sp, tile, 2 + (warp >> 2), warp & 3, lane);
-    c.add(sp.n);
+    if (!kWeights) drain_o<kWeights>(cx, sp, tile, (values ? 0 : 2) + (warp >> 2), warp & 3, lane);
+    chunks += sp.n;
     entries += more;
     u = min(cx.u1, tstart + units);
     tstart += units;
@@ -680,36 +661,39 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
   uint32_t entries = 0, issued = 0;     // quarters given to the copy engine
   int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
-    block_sync();
-    block_sync();
+    seg_sync();                         // the tile's chunks are known (the copies need no more than that)
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
-    if (!(kV && kWeights)) {
-      const int nw = sm.seg.nw, i0 = sp.n - more;
-      // lane h (0, 1): page h of a chunk, a chunk ahead
-      auto page_at = [&](int i) -> int {
-        const int lp = (sm.seg.c_hi - 1 - (sp.k0 + i - nw)) * (kChunk / kPage) + (lane & 1);
-        if (i >= sp.n || (lp + 1) * kPage <= sm.seg.e_lo || lp * kPage >= sm.seg.e_hi) return -1;
-        const int p = __ldg(a.page_table + (int64_t)sm.seg.b * a.max_pages + lp);
-        return p < a.n_pages ? p : -1;
-      };
-      int next = page_at(i0);
+    const int nw = sm.seg.nw, i0 = sp.n - more, steps = kV && kWeights ? 0 : 4 * more;
+    // lane h (0, 1): page h of a chunk, a chunk ahead
+    auto page_at = [&](int i) -> int {
+      const int lp = (sm.seg.c_hi - 1 - (sp.k0 + i - nw)) * (kChunk / kPage) + (lane & 1);
+      if (i >= sp.n || (lp + 1) * kPage <= sm.seg.e_lo || lp * kPage >= sm.seg.e_hi) return -1;
+      const int p = __ldg(a.page_table + (int64_t)sm.seg.b * a.max_pages + lp);
+      return p < a.n_pages ? p : -1;
+    };
+    int next = page_at(i0);
+    bool synced = false;
 #pragma unroll 1
-      for (int n = 0; n < 4 * more; ++n) {
-        const int i = i0 + (n >> 2), q = n & 3;
-        const uint32_t st = 4 * entries + n, slot = st % kStage, use = st / kStage;
-        const int page = next;
-        if (q == 3) next = page_at(i + 1);
-        if (use > 0 && !warp_wait(kV ? &sm.vst_free[slot] : &sm.kst_free[slot], (use - 1) & 1, abort)) break;
-        const uint32_t have = __ballot_sync(0xffffffffu, lane < 2 && page >= 0);
-        uint64_t* full = kV ? &sm.vst_full[slot] : &sm.kst_full[slot];
-        if (lane == 0) tc::mbar_arrive_expect_tx(full, __popc(have) * (kStageBytes / 2));
-        __syncwarp();
-        if (lane < 2 && page >= 0)
-          tma::load_2d((kV ? sm.vst[slot] : sm.kst[slot]) + lane * (kStageBytes / 2), cx.map, 64 * q, page * kPage, full);
-        issued = st + 1;
+    for (int n = 0; n < steps; ++n) {
+      if (n == kStage) {                // the slots are full: only now wait for the other roles
+        block_sync();
+        synced = true;
       }
+      const int i = i0 + (n >> 2), q = n & 3;
+      const uint32_t st = 4 * entries + n, slot = st % kStage, use = st / kStage;
+      const int page = next;
+      if (q == 3) next = page_at(i + 1);
+      if (use > 0 && !warp_wait(kV ? &sm.vst_free[slot] : &sm.kst_free[slot], (use - 1) & 1, abort)) break;
+      const uint32_t have = __ballot_sync(0xffffffffu, lane < 2 && page >= 0);
+      uint64_t* full = kV ? &sm.vst_full[slot] : &sm.kst_full[slot];
+      if (lane == 0) tc::mbar_arrive_expect_tx(full, __popc(have) * (kStageBytes / 2));
+      __syncwarp();
+      if (lane < 2 && page >= 0)
+        tma::load_2d((kV ? sm.vst[slot] : sm.kst[slot]) + lane * (kStageBytes / 2), cx.map, 64 * q, page * kPage, full);
+      issued = st + 1;
     }
+    if (!synced) block_sync();
     block_sync();
     if (*abort) break;
     entries += more;
@@ -811,7 +795,6 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
   int u = cx.u0, tstart = cx.tstart;
   const int64_t rows = (int64_t)a.Tq * a.Hq;
   while (u < cx.u1) {
-    block_sync();
     // ---- rows of the tile
     const int b = tile / cx.pl.tiles;
     const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
@@ -870,6 +853,8 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       sm.seg.c_hi = (g.e_hi + kChunk - 1) / kChunk;
       sm.seg.nw = !kWeights && g.w_hi >= g.w_lo ? (int)(((int64_t)g.w_hi - g.w_lo) / kChunk) + 1 : 0;
     }
+    soft_sync();
+    seg_arrive();
     block_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks), nw = sm.seg.nw;
@@ -1050,7 +1035,9 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         if (lane == 0) tc::mbar_arrive(&sm.p_full[e]);
       }
       if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + sp.n);
-      // all products of the tile, and the row sums over its keys
+      // all products of the tile (the last but one first: a parity alone does not tell its phase from
+      // the one before it), and the row sums over its keys
+      if (sp.n > 1) warp_wait(&sm.v_free[3], (c.all + sp.n - 2) & 1, abort);
       if (sp.n > 0) warp_wait(&sm.v_free[3], (c.all + sp.n - 1) & 1, abort);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -1099,8 +1086,9 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
   Count c;
   int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
+    seg_sync();
     block_sync();
-    block_sync();
+    tc::tc_fence_after();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks);
     // Round i does S(i + 1), then PV(i), in steps
@@ -1169,13 +1157,24 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx) {
   constexpr int kAhead = 5;
   const int lane = threadIdx.x & 31;
   uint32_t c = 0;
+  int tile = cx.tile;
   int u = cx.u0, tstart = cx.tstart;
   while (u < cx.u1) {
-    block_sync();
-    block_sync();
+    seg_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks);
     {
+      // the next tile's Q rows (contiguous)
+      const int64_t rows = (int64_t)a.Tq * a.Hq;
+      const int tn = tile + 1;
+      if (tstart + units < cx.u1 && lane < 4) {
+        const int64_t r0 = (int64_t)(cx.pl.tile0 + tn % cx.pl.tiles) * kRows + 16 * lane;
+        const int64_t live = min(rows - r0, (int64_t)16);
+        if (live > 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.Q + ((int64_t)(tn / cx.pl.tiles) * rows + r0) * kD),
+                       "r"((uint32_t)(live * kD * 2))
+                       : "memory");
+      }
       auto request = [&](int i) {
         const int k = sp.k0 + i;
         if (i >= sp.n || k < sm.seg.nw || lane >= 4) return;
@@ -1188,7 +1187,8 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx) {
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
       };
 #pragma unroll 1
-      for (int i = 2; i < kAhead; ++i) request(i);
+      for (int i = 1; i < kAhead; ++i) request(i);
+      block_sync();
 #pragma unroll 1
       for (int i = 0; i + kAhead < sp.n; ++i) {
         request(i + kAhead);
@@ -1207,6 +1207,7 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx) {
     c += sp.n;
     u = min(cx.u1, tstart + units);
     tstart += units;
+    ++tile;
   }
 }
 
@@ -1279,12 +1280,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   if (!kWeights && tid == 0) pl.cont[g] = (u1 > u0 && cx.tstart < u0) ? cx.tile : -1;
 
   // ---- roles, each with its own walk over the tiles (every walk meets the same barriers)
-  if (warp < kValWarps) {
+  if (warp < kValWarps + kKeyWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill));
-    role_values<kWeights>(cx);
-  } else if (warp < kValWarps + kKeyWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill));
-    role_keys<kWeights>(cx);
+    role_fill<kWeights>(cx);
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     role_softmax<kWeights>(cx);

@@ -67,6 +67,20 @@ SMALL = {"d64_" + k: dict(CASES[k], d=64) for k in ("empty_window_only", "nothin
 ALL = {**CASES, **SMALL}
 
 
+@pytest.mark.parametrize("name", ["one_long", "many_chunks"])
+def test_repeated_calls_give_the_same_bits(name):
+    """No result depends on which copy, product or warp was first."""
+    c = Case(seed=5, **CASES[name])
+    O, lse = (t.clone() for t in c.attend())
+    w = c.weigh(lse, None, torch.zeros(c.n_pages * 64, device="cuda")).clone()
+    for _ in range(30):
+        c.attend()
+        again = c.weigh(lse, None, torch.zeros(c.n_pages * 64, device="cuda"))
+        assert torch.equal(c.O.view(torch.int16), O.view(torch.int16)) and torch.equal(c.lse, lse)
+        assert torch.equal(again, w)
+    assert status() == 0
+
+
 @pytest.mark.parametrize("name", ALL)
 def test_attention_matches_oracle(name):
     c = Case(seed=len(name) * 7 + 1, **ALL[name])
