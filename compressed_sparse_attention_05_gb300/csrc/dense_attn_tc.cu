@@ -75,7 +75,7 @@ constexpr int kQuarter = 128;                         // channels of a quarter
 constexpr int kVSlots = 3;                            // quarters of V in shared memory
 constexpr int kStageBytes = kChunk * kQuarter / 2;    // packed codes of a chunk's quarter
 template <bool kWeights> struct Stages;               // staging slots of the K and V streams
-template <> struct Stages<false> { static constexpr int K = 2, V = 2; };
+template <> struct Stages<false> { static constexpr int K = 3, V = 3; };
 template <> struct Stages<true> { static constexpr int K = 8, V = 1; };
 
 // Operand tiles (no-swizzle canonical layout, core matrices of 8 rows x 16 bytes):
@@ -94,13 +94,18 @@ struct Segment {            // what the roles need to know of the current tile
   int one_t, t;             // all rows belong to the token at raw position t
   int pos0;
 };
+// A slot's four reading warps, and so its barrier, change from use to use when the number of slots is
+// odd; a warp has to wait for consecutive phases, so that the "full" barriers of less than four slots
+// belong to the quarters (a quarter is free again before the same one of the next chunk is staged).
+template <int kSlots> constexpr int kMax4 = kSlots < 4 ? 4 : kSlots;
+
 template <bool kWeights>
 struct Smem {
   unsigned char kst[Stages<kWeights>::K][kStageBytes];   // (1024-aligned)
   unsigned char vst[kWeights ? 1 : Stages<kWeights>::V][kWeights ? 16 : kStageBytes];
   uint16_t q[kRows * kD];
   uint16_t v[kWeights ? 8 : kVSlots * kChunk * kQuarter];
-  uint16_t p[kWeights ? 8 : 2 * kChunk * kRows];
+  uint16_t p[kWeights ? 8 : kChunk * kRows];
   float mult[kRows];        // logit multiplier: softmax scale * log2(e) * 2^e_r
   float nref[kRows];        // attention: -m_ref (kUnset before the row's first key); weights: -lse * log2(e)
   float slope2[kRows];      // slope * log2(e)
@@ -115,11 +120,11 @@ struct Smem {
       int found_start, found_tile;
     };
   };
-  uint64_t kst_full[Stages<kWeights>::K], kst_free[Stages<kWeights>::K];   // staging slots
-  uint64_t vst_full[Stages<kWeights>::V], vst_free[Stages<kWeights>::V];
+  uint64_t kst_full[kMax4<Stages<kWeights>::K>], kst_free[Stages<kWeights>::K];   // staging slots (full: see Full)
+  uint64_t vst_full[kMax4<Stages<kWeights>::V>], vst_free[Stages<kWeights>::V];
   uint64_t kq_full[4], kq_free[4];  // quarters of a chunk's K in tensor memory
   uint64_t v_full[4], v_free[4];    // quarters of a chunk's V in shared memory
-  uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
+  uint64_t s_full[2], s_free[2], p_full, p_free;
   Segment seg;
   uint32_t tmem;
   int abort;
@@ -478,7 +483,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   constexpr int kRing = kV ? kVSlots : Cols<kWeights>::ring, kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
-  constexpr bool kEarly = kStage <= 2;   // one slot for each four warps: it is wanted back at once
+  constexpr bool kEarly = kStage < 4;   // few slots: they are wanted back at once
   const int lq = warp & 3, odd = warp >> 2, key = 32 * lq + lane;
   volatile int* abort = &sm.abort;
   const int i0 = min(max(sm.seg.nw - k0, 0), n_chunks);   // first entry chunk of the span
@@ -514,8 +519,8 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
     const uint32_t st = 4 * (entries + (i - i0)) + q;   // running number among the staged quarters
     uint4 t[4];
     if (!window) {
-      const uint32_t slot = st % kStage, use = st / kStage;
-      if (!warp_wait(kV ? &sm.vst_full[slot] : &sm.kst_full[slot], use & 1, abort)) break;
+      const uint32_t slot = st % kStage, full = st % kMax4<kStage>;
+      if (!warp_wait(kV ? &sm.vst_full[full] : &sm.kst_full[full], (st / kMax4<kStage>) & 1, abort)) break;
       const unsigned char* src = (kV ? sm.vst[slot] : sm.kst[slot]) + 64 * key;
 #pragma unroll
       for (int p = 0; p < 4; ++p) t[p] = *reinterpret_cast<const uint4*>(src + 16 * (p ^ ((key >> 1) & 3)));
@@ -665,14 +670,15 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
     const int nw = sm.seg.nw, i0 = sp.n - more, steps = kV && kWeights ? 0 : 4 * more;
-    // lane h (0, 1): page h of a chunk, a chunk ahead
-    auto page_at = [&](int i) -> int {
+    // lane l: page l % 2 of chunk i + l / 2, for 16 chunks; the next 16 are on their way
+    auto pages_at = [&](int i) -> int {
+      i += lane >> 1;
       const int lp = (sm.seg.c_hi - 1 - (sp.k0 + i - nw)) * (kChunk / kPage) + (lane & 1);
       if (i >= sp.n || (lp + 1) * kPage <= sm.seg.e_lo || lp * kPage >= sm.seg.e_hi) return -1;
       const int p = __ldg(a.page_table + (int64_t)sm.seg.b * a.max_pages + lp);
       return p < a.n_pages ? p : -1;
     };
-    int next = page_at(i0);
+    int pages = -1, ahead = pages_at(i0);
     bool synced = false;
 #pragma unroll 1
     for (int n = 0; n < steps; ++n) {
@@ -682,11 +688,14 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
       }
       const int i = i0 + (n >> 2), q = n & 3;
       const uint32_t st = 4 * entries + n, slot = st % kStage, use = st / kStage;
-      const int page = next;
-      if (q == 3) next = page_at(i + 1);
+      if ((n & 63) == 0) {
+        pages = ahead;
+        ahead = pages_at(i + 16);
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, 2 * ((n >> 2) & 15) + (lane & 1));
       if (use > 0 && !warp_wait(kV ? &sm.vst_free[slot] : &sm.kst_free[slot], (use - 1) & 1, abort)) break;
       const uint32_t have = __ballot_sync(0xffffffffu, lane < 2 && page >= 0);
-      uint64_t* full = kV ? &sm.vst_full[slot] : &sm.kst_full[slot];
+      uint64_t* full = kV ? &sm.vst_full[st % kMax4<kStage>] : &sm.kst_full[st % kMax4<kStage>];
       if (lane == 0) tc::mbar_arrive_expect_tx(full, __popc(have) * (kStageBytes / 2));
       __syncwarp();
       if (lane < 2 && page >= 0)
@@ -704,7 +713,9 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
   if (*abort)
     for (uint32_t st = issued > (uint32_t)kStage ? issued - kStage : 0; st < issued; ++st)
       for (uint32_t n = 0; n < (1u << 22); ++n)
-        if (tc::mbar_try_wait(kV ? &sm.vst_full[st % kStage] : &sm.kst_full[st % kStage], (st / kStage) & 1)) break;
+        if (tc::mbar_try_wait(kV ? &sm.vst_full[st % kMax4<kStage>] : &sm.kst_full[st % kMax4<kStage>],
+                              (st / kMax4<kStage>) & 1))
+          break;
 }
 
 // One key of a chunk as its softmax thread sees it.
@@ -731,10 +742,16 @@ __device__ __forceinline__ bool row_sees(const Ctx<kWeights>& cx, const KeyView&
 // Columns c0 .. c0+31 of this thread's key: the logits in the log2 domain as the value
 // product carries them, -inf where the row does not see the key.
 template <bool kWeights>
-__device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyView& kv, uint32_t taddr, int c0, float (&x)[32]) {
+__device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyView& kv, uint32_t taddr, int c0, uint64_t* done,
+                                            float (&x)[32]) {
   const Smem<kWeights>& sm = cx.sm;
   tmem_ld32(taddr, x);
   tc::tmem_wait_ld();
+  if (done) {   // the buffer's last columns
+    tc::tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(done);
+  }
 #pragma unroll
   for (int j4 = 0; j4 < 8; ++j4) {
     const float4 m = *reinterpret_cast<const float4*>(&sm.mult[c0 + 4 * j4]);
@@ -913,7 +930,8 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
 #pragma unroll 1
         for (int c0 = 0; c0 < kRows; c0 += 32) {
           float x[32];
-          load_logits<kWeights>(cx, kv, cx.tm + Cols<true>::S + 64 * (i & 1) + c0 + lane_q, c0, x);
+          load_logits<kWeights>(cx, kv, cx.tm + Cols<true>::S + 64 * (i & 1) + c0 + lane_q, c0,
+                                c0 ? &sm.s_free[i & 1] : nullptr, x);
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j4 = 0; j4 < 8; ++j4) {
@@ -925,9 +943,6 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
           }
           sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.s_free[i & 1]);
         if (cx.pl.sums)
           cx.pl.sums[(int64_t)tile * cx.pl.sum_stride + entry_of(i)] = slot >= 0 ? sum : 0.f;
         else if (slot >= 0)
@@ -940,17 +955,16 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       for (int j = 0; j < 32; ++j) lsum[j] = 0.f;
       const int c0 = 32 * half;
       for (int i = 0; i < sp.n; ++i) {
-        const int e = i & 1;
-        const uint32_t ph = c.phase(i), ts = cx.tm + Cols<false>::S + c0 + lane_q;
+        const uint32_t ph = c.all + i, ts = cx.tm + Cols<false>::S + c0 + lane_q;
         if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + i);
         int64_t slot;
         const KeyView kv = view(i, &slot);
-        const bool ok = warp_wait(&sm.s_full[0], (c.all + i) & 1, abort);
+        const bool ok = warp_wait(&sm.s_full[0], ph & 1, abort);
         tc::tc_fence_after();
         // ---- logits over the reference, and whether one outgrows it
         float x[32];
         float top = -INFINITY;
-        load_logits<kWeights>(cx, kv, ts, c0, x);
+        load_logits<kWeights>(cx, kv, ts, c0, &sm.s_free[0], x);
 #pragma unroll
         for (int j4 = 0; j4 < 8; ++j4) {
           const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
@@ -985,7 +999,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
           }
           if (half_or(half, need)) {
             // O^T *= alpha (column = row of the tile): the value products so far must be done
-            if (c.all + i > 0) warp_wait(&sm.v_free[3], (c.all + i - 1) & 1, abort);
+            if (ph > 0) warp_wait(&sm.p_free, (ph - 1) & 1, abort);
             tc::tc_fence_after();
 #pragma unroll 1
             for (int mt = 0; mt < 4; ++mt) {
@@ -1001,14 +1015,12 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
               }
             }
             tc::tmem_wait_st();
+            tc::tc_fence_before();
 #pragma unroll
             for (int j = 0; j < 32; ++j) lsum[j] *= sm.red[0][c0 + j];
           }
           half_sync(half);                     // red is read; the next vote may come
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.s_free[0]);
         // ---- P = exp2(l - m_ref), rounded to fp16 for the value product
         const float pf = pow2i(-(int)kv.ff);   // the normaliser adds p = 2^-f (2^f p)
         uint32_t pk[16];
@@ -1024,21 +1036,18 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
           pk[2 * j4] = f32x2_f16x2(p0, p1);
           pk[2 * j4 + 1] = f32x2_f16x2(p2, p3);
         }
-        if (ph > 0) warp_wait(&sm.p_free[e], (ph - 1) & 1, abort);
-        unsigned char* pd = reinterpret_cast<unsigned char*>(sm.p) + e * (kChunk * kRows * 2) + (key >> 3) * 1024 +
-                            (c0 / 8) * 128 + (key & 7) * 16;
+        if (ph > 0) warp_wait(&sm.p_free, (ph - 1) & 1, abort);
+        unsigned char* pd = reinterpret_cast<unsigned char*>(sm.p) + (key >> 3) * 1024 + (c0 / 8) * 128 + (key & 7) * 16;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<uint4*>(pd + j * 128) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
         tc::fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.p_full[e]);
+        if (lane == 0) tc::mbar_arrive(&sm.p_full);
       }
       if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + sp.n);
-      // all products of the tile (the last but one first: a parity alone does not tell its phase from
-      // the one before it), and the row sums over its keys
-      if (sp.n > 1) warp_wait(&sm.v_free[3], (c.all + sp.n - 2) & 1, abort);
-      if (sp.n > 0) warp_wait(&sm.v_free[3], (c.all + sp.n - 1) & 1, abort);
+      // all products of the tile, and the row sums over its keys
+      if (sp.n > 0) warp_wait(&sm.p_free, (c.all + sp.n - 1) & 1, abort);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float y[16];
@@ -1100,12 +1109,12 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
     for (int i = -1; ok && i < sp.n; ++i) {
       const bool more = i + 1 < sp.n;
       const uint32_t cs = c.all + i + 1, cv = c.all + i;      // running numbers of the two chunks
-      const int es = kWeights ? (i + 1) & 1 : 0, ev = i & 1;
-      const uint32_t ps = kWeights ? c.phase(i + 1) : cs, pv = c.phase(max(i, 0));
+      const int es = kWeights ? (i + 1) & 1 : 0;
+      const uint32_t ps = kWeights ? c.phase(i + 1) : cs;
       const int first = !more ? 5 : ps > 0 ? 0 : 1, last = kWeights || i < 0 ? 4 : 9;
       const uint32_t bar = tc::smem_addr(lane == 0 ? &sm.s_free[es] : lane <= 4 ? &sm.kq_full[lane - 1]
-                                                  : lane == 5 ? &sm.p_full[ev] : &sm.v_full[(lane - 6) & 3]);
-      const uint32_t parity = (lane == 0 ? ps - 1 : lane <= 4 ? cs : lane == 5 ? pv : cv) & 1;
+                                                  : lane == 5 ? &sm.p_full : &sm.v_full[(lane - 6) & 3]);
+      const uint32_t parity = (lane == 0 ? ps - 1 : lane <= 4 ? cs : cv) & 1;
       uint32_t ready = 0;
 #pragma unroll 1
       for (int step = first; step <= last; ++step) {
@@ -1133,9 +1142,9 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
 #pragma unroll
           for (uint32_t kk = 0; kk < 8; ++kk)
             mma_ss<kHiO, kHiO, kIdO>(leader, cx.tm + kColO + 64 * mt, va + kk * 256,
-                                     dp + ev * (kChunk * kRows * 2 / 16) + kk * 128, (uint32_t)i | kk);
+                                     dp + kk * 128, (uint32_t)i | kk);
           mma_commit_by(leader, &sm.v_free[mt]);
-          if (step == 9) mma_commit_by(leader, &sm.p_free[ev]);
+          if (step == 9) mma_commit_by(leader, &sm.p_free);
         }
       }
     }
@@ -1224,20 +1233,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
       tc::mbar_init(&sm.v_full[i], 4);
       tc::mbar_init(&sm.v_free[i], 1);
     }
-    for (int i = 0; i < Stages<kWeights>::K; ++i) {
-      tc::mbar_init(&sm.kst_full[i], 1);
-      tc::mbar_init(&sm.kst_free[i], 4);
-    }
-    for (int i = 0; i < Stages<kWeights>::V; ++i) {
-      tc::mbar_init(&sm.vst_full[i], 1);
-      tc::mbar_init(&sm.vst_free[i], 4);
-    }
+    for (int i = 0; i < kMax4<Stages<kWeights>::K>; ++i) tc::mbar_init(&sm.kst_full[i], 1);
+    for (int i = 0; i < Stages<kWeights>::K; ++i) tc::mbar_init(&sm.kst_free[i], 4);
+    for (int i = 0; i < kMax4<Stages<kWeights>::V>; ++i) tc::mbar_init(&sm.vst_full[i], 1);
+    for (int i = 0; i < Stages<kWeights>::V; ++i) tc::mbar_init(&sm.vst_free[i], 4);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
       tc::mbar_init(&sm.s_free[i], kWeights ? kSoftWarps / 2 : kSoftWarps);
-      tc::mbar_init(&sm.p_full[i], kSoftWarps);
-      tc::mbar_init(&sm.p_free[i], 1);
     }
+    tc::mbar_init(&sm.p_full, kSoftWarps);
+    tc::mbar_init(&sm.p_free, 1);
     sm.abort = 0;
     sm.progress = 0;
     tc::mbar_fence_init();
