@@ -58,8 +58,8 @@ constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = 896;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
 constexpr int kMmaWarp = kValWarps + kKeyWarps + kSoftWarps;
 constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
-// registers per thread after the split of the seven warpgroups: 4 x 64 + 2 x 104 + 40 = 7 x 72
-constexpr int kRegsLaunch = 72, kRegsFill = 64, kRegsSoft = 104, kRegsMisc = 40;
+// registers per thread after the split of the seven warpgroups: 4 x 56 + 2 x 120 + 40 = 7 x 72
+constexpr int kRegsLaunch = 72, kRegsFill = 56, kRegsSoft = 120, kRegsMisc = 40;
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory.  Attention: O^T (four M-tiles of 64 columns), S^T, and a ring of three
 // quarters of K (64 columns each: 128 channels of fp16).  Weights: two S^T, a ring of four.
@@ -94,11 +94,6 @@ struct Segment {            // what the roles need to know of the current tile
   int one_t, t;             // all rows belong to the token at raw position t
   int pos0;
 };
-// A slot's four reading warps, and so its barrier, change from use to use when the number of slots is
-// odd; a warp has to wait for consecutive phases, so that the "full" barriers of less than four slots
-// belong to the quarters (a quarter is free again before the same one of the next chunk is staged).
-template <int kSlots> constexpr int kMax4 = kSlots < 4 ? 4 : kSlots;
-
 template <bool kWeights>
 struct Smem {
   unsigned char kst[Stages<kWeights>::K][kStageBytes];   // (1024-aligned)
@@ -120,8 +115,8 @@ struct Smem {
       int found_start, found_tile;
     };
   };
-  uint64_t kst_full[kMax4<Stages<kWeights>::K>], kst_free[Stages<kWeights>::K];   // staging slots (full: see Full)
-  uint64_t vst_full[kMax4<Stages<kWeights>::V>], vst_free[Stages<kWeights>::V];
+  uint64_t kst_full[Stages<kWeights>::K], kst_free[Stages<kWeights>::K];   // staging slots
+  uint64_t vst_full[Stages<kWeights>::V], vst_free[Stages<kWeights>::V];
   uint64_t kq_full[4], kq_free[4];  // quarters of a chunk's K in tensor memory
   uint64_t v_full[4], v_free[4];    // quarters of a chunk's V in shared memory
   uint64_t s_full[2], s_free[2], p_full, p_free;
@@ -472,97 +467,41 @@ __device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp,
   tc::tc_fence_before();
 }
 
-// Dequantises every chunk of a tile, quarter by quarter: eight warps, lane = key, four of them
-// take quarters 0 and 2, four take 1 and 3.  kV: into the shared-memory slots that the value
-// product reads; else K, into the tensor-memory slots that the score product reads.
-// Quarter number n = 4 chunk + q goes where number n - ring was; barriers belong to quarters
-// (and staging slots to one group of warps), so that a warp waits for consecutive phases.
+// Dequantises the chunks of a tile, quarter by quarter: eight warps share a quarter, lane = key,
+// half of its channels to four of them (a quarter to four warps took so long, 1,900 cycles, that the
+// tensor pipe stood waiting for the last one of every chunk).  kV: into the shared-memory slots that
+// the value product reads; else K, into the tensor-memory slots that the score product reads.  With
+// the weights, which have no V, sixteen warps do K: quarters 0 and 2 (first = 0), 1 and 3 (first = 1).
+// Quarter number n = 4 chunk + q goes where number n - ring was; barriers belong to quarters (and
+// staging slots to the same eight warps), so that a warp waits for consecutive phases.
 template <bool kWeights, bool kV>
-__device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n_chunks, uint32_t chunks, uint32_t entries, int warp,
-                                          int lane) {
+__device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n_chunks, uint32_t chunks, uint32_t entries, int first,
+                                          int warp, int lane) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   constexpr int kRing = kV ? kVSlots : Cols<kWeights>::ring, kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
-  constexpr bool kEarly = kStage < 4;   // few slots: they are wanted back at once
-  const int lq = warp & 3, odd = warp >> 2, key = 32 * lq + lane;
+  constexpr bool kEarly = kStage < 4;        // few slots: they are wanted back at once
+  const int lq = warp & 3, half = warp >> 2, key = 32 * lq + lane;
   volatile int* abort = &sm.abort;
-  const int i0 = min(max(sm.seg.nw - k0, 0), n_chunks);   // first entry chunk of the span
-  const int j0 = (sm.seg.c_hi - 1 - (k0 - sm.seg.nw)) * kChunk + key;   // the key's entry in chunk 0 (128 less a chunk)
-  // The scales of a step's quarter, a step ahead (the key's page a chunk ahead); no key, or one behind
-  // a bad page: zero, so that whatever codes the staging slot holds become zeros.
-  int page = page_of<kWeights>(cx, j0 - i0 * kChunk, i0 < n_chunks), page1 = -1;
-  auto scales_of = [&](int n) -> uint2 {
-    const int i = n >> 1, j = j0 - i * kChunk;
-    if (i < i0 || i >= n_chunks) return make_uint2(0, 0);
-    if ((n & 1) == 0) {
-      if (i > i0) page = page1;
-      page1 = page_of<kWeights>(cx, j - kChunk, i + 1 < n_chunks);
+  const uint32_t dst_k = cx.tm + Cols<kWeights>::K + 32 * half + ((uint32_t)(32 * lq) << 16);
+  unsigned char* dst_v = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 2048 + (key & 7) * 16 + half * 1024;
+  auto put = [&](uint32_t slot, int p, const uint32_t (&o)[8]) {   // channels 16 p .. +15 of the half
+    if (kV) {
+      unsigned char* d = dst_v + slot * (kChunk * kQuarter * 2) + 2 * p * 128;
+      *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(d + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+    } else {
+      tmem_st8u(dst_k + 64 * slot + 8 * p, o);
     }
-    if (j < sm.seg.e_lo || j >= sm.seg.e_hi) return make_uint2(0, 0);
-    if (page < 0 || page >= a.n_pages) {
-      if (!kV && odd == 0) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
-      return make_uint2(0, 0);
-    }
-    return __ldg(reinterpret_cast<const uint2*>(a.kv_scales + ((int64_t)page * kPage + (j & (kPage - 1))) * (kD / 16) + 8 * odd) +
-                 2 * (n & 1));
   };
-  uint2 next = scales_of(2 * i0);
-  const uint32_t dst_k = cx.tm + Cols<kWeights>::K + ((uint32_t)(32 * lq) << 16);
-  unsigned char* dst_v = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 2048 + (key & 7) * 16;
-#pragma unroll 1
-  for (int n = 0; n < 2 * n_chunks; ++n) {
-    const int i = n >> 1, q = odd + 2 * (n & 1);
-    const uint32_t number = 4 * (chunks + i) + q;
-    const bool window = i < i0;             // uniform
-    const uint2 s = next;
-    if (n >= 2 * i0) next = scales_of(n + 1);
-    const uint32_t st = 4 * (entries + (i - i0)) + q;   // running number among the staged quarters
-    uint4 t[4];
-    if (!window) {
-      const uint32_t slot = st % kStage, full = st % kMax4<kStage>;
-      if (!warp_wait(kV ? &sm.vst_full[full] : &sm.kst_full[full], (st / kMax4<kStage>) & 1, abort)) break;
-      const unsigned char* src = (kV ? sm.vst[slot] : sm.kst[slot]) + 64 * key;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) t[p] = *reinterpret_cast<const uint4*>(src + 16 * (p ^ ((key >> 1) & 3)));
-      // The slot may be written again once the loads have arrived, not when they are issued: the vote
-      // reads a word of each (lane 0 always votes yes).  With many slots that can wait for the quarter's end.
-      if (kEarly) {
-        const uint32_t any = t[0].x ^ t[1].x ^ t[2].x ^ t[3].x;
-        if (__ballot_sync(0xffffffffu, lane == 0 || any == 0x5A5A5A5Au) & (lane == 0))
-          tc::mbar_arrive(kV ? &sm.vst_free[slot] : &sm.kst_free[slot]);
-      }
-    }
+  auto ring_free = [&](uint32_t number, int q) {   // the quarter that was in the slot has been read
     if (number >= (uint32_t)kRing &&
         !warp_wait(kV ? &sm.v_free[(q - kRing) & 3] : &sm.kq_free[(q - kRing) & 3], ((number - kRing) >> 2) & 1, abort))
-      break;
+      return false;
     if (!kV) tc::tc_fence_after();
-    const uint32_t slot = number % kRing;
-    auto put = [&](int p, const uint32_t (&o)[8]) {   // channels 16 p .. +15 of the quarter
-      if (kV) {
-        unsigned char* d = dst_v + slot * (kChunk * kQuarter * 2) + 2 * p * 128;
-        *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(d + 128) = make_uint4(o[4], o[5], o[6], o[7]);
-      } else {
-        tmem_st8u(dst_k + 64 * slot + 8 * p, o);
-      }
-    };
-    if (!window) {
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        uint32_t o[8];
-        dequant16(t[p >> 1], (p & 4 ? s.y : s.x) >> (16 * ((p >> 1) & 1)), p & 1, o);
-        put(p, o);
-      }
-    } else {
-      const KeyRef w = window_ref<kWeights>(cx, k0 + i, key);
-#pragma unroll 1
-      for (int p = 0; p < 8; ++p) {
-        uint32_t o[8];
-        window_piece(w, 8 * q + p, o);
-        __syncwarp();
-        put(p, o);
-      }
-    }
+    return true;
+  };
+  auto ring_full = [&](int q, uint64_t* staged) {
     if (kV) {
       tc::fence_async_smem();
     } else {
@@ -572,7 +511,91 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
     __syncwarp();
     if (lane == 0) {
       tc::mbar_arrive(kV ? &sm.v_full[q] : &sm.kq_full[q]);
-      if (!kEarly && !window) tc::mbar_arrive(kV ? &sm.vst_free[st % kStage] : &sm.kst_free[st % kStage]);
+      if (staged) tc::mbar_arrive(staged);
+    }
+  };
+  const int i0 = min(max(sm.seg.nw - k0, 0), n_chunks);   // first entry chunk of the span
+  uint32_t chunk4 = 4 * chunks;
+  if (!kWeights) {
+#pragma unroll 1
+    for (int n = 0; n < 4 * i0; ++n) {
+      const int q = n & 3;
+      if (!ring_free(chunk4 + n, q)) return;
+      const KeyRef w = window_ref<kWeights>(cx, k0 + (n >> 2), key);
+#pragma unroll 1
+      for (int p = 0; p < 4; ++p) {
+        uint32_t o[8];
+        window_piece(w, 8 * q + 4 * half + p, o);
+        __syncwarp();
+        put((chunk4 + n) % kRing, p, o);
+      }
+      ring_full(q, nullptr);
+    }
+    chunk4 += 4 * i0;
+  }
+  if (i0 >= n_chunks) return;
+  // A step's four scales are read a step ahead, the key's page a chunk ahead of that.  The offset is
+  // the key's place in the pool (32 bits: 2^32 entries would be 1 TB of codes); none if there is no
+  // such key, or behind a bad page: then the scales are zero, and whatever the staging slot holds
+  // becomes zeros.
+  constexpr uint32_t kNone = 0xFFFFFFFFu;
+  const int e_lo = sm.seg.e_lo, e_hi = sm.seg.e_hi;
+  const int32_t* table = a.page_table + (int64_t)sm.seg.b * a.max_pages;
+  int j = (sm.seg.c_hi - 1 - (k0 + i0 - sm.seg.nw)) * kChunk + key;   // the key's entry
+  auto page_at = [&](int j) { return j >= e_lo && j < e_hi ? __ldg(table + (j >> 6)) : -1; };
+  auto place = [&](int j, int page) -> uint32_t {
+    if (page >= 0 && page < a.n_pages) return (uint32_t)page * kPage + (j & (kPage - 1));
+    if (!kV && first + half == 0 && j >= e_lo && j < e_hi) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
+    return kNone;
+  };
+  const uint8_t* scales = a.kv_scales + 4 * half + 8 * first;
+  auto scales_of = [&](uint32_t at, int q) -> uint32_t {
+    return at == kNone ? 0 : __ldg(reinterpret_cast<const uint32_t*>(scales + (size_t)at * (kD / 16) + 8 * q));
+  };
+  int left = n_chunks - i0;               // chunks from this one on
+  uint32_t at = place(j, page_at(j)), at1 = kNone;
+  uint32_t next = scales_of(at, 0);
+  int page1 = left > 1 ? page_at(j - kChunk) : -1;
+  uint32_t st4 = 4 * entries + first;
+#pragma unroll 1
+  for (int q2 = 0;;) {                    // q2: this quarter less `first`
+    constexpr int kStep = kWeights ? 2 : 1;
+    const int q = q2 + first;
+    if (q2 == 0) {
+      at1 = left > 1 ? place(j - kChunk, page1) : kNone;
+      page1 = left > 2 ? page_at(j - 2 * kChunk) : -1;
+    }
+    const uint32_t s = next;
+    next = q2 + kStep < 4 ? scales_of(at, q2 + kStep) : scales_of(at1, 0);
+    const uint32_t st = st4 + q2, slot = st % kStage;   // running number among the staged quarters
+    if (!warp_wait(kV ? &sm.vst_full[slot] : &sm.kst_full[slot], (st / kStage) & 1, abort)) return;
+    const unsigned char* src = (kV ? sm.vst[slot] : sm.kst[slot]) + 64 * key;
+    uint4 t[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) t[p] = *reinterpret_cast<const uint4*>(src + 16 * ((2 * half + p) ^ ((key >> 1) & 3)));
+    // The slot may be written again once the loads have arrived, not when they are issued: the vote
+    // reads a word of each (lane 0 always votes yes).  With many slots that can wait for the quarter's end.
+    if (kEarly) {
+      if (__ballot_sync(0xffffffffu, lane == 0 || (t[0].x ^ t[1].x) == 0x5A5A5A5Au) & (lane == 0))
+        tc::mbar_arrive(kV ? &sm.vst_free[slot] : &sm.kst_free[slot]);
+    }
+    const uint32_t number = chunk4 + q;
+    if (!ring_free(number, q)) return;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      uint32_t o[8];
+      dequant16(t[p >> 1], s >> (16 * (p >> 1)), p & 1, o);
+      put(number % kRing, p, o);
+    }
+    ring_full(q, kEarly ? nullptr : kV ? &sm.vst_free[slot] : &sm.kst_free[slot]);
+    q2 += kStep;
+    if (q2 >= 4) {
+      if (--left == 0) break;
+      q2 = 0;
+      j -= kChunk;
+      at = at1;
+      chunk4 += 4;
+      st4 += 4;
     }
   }
 }
@@ -599,36 +622,48 @@ __device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
     const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
     const int64_t rows = (int64_t)a.Tq * a.Hq;
     {
-      uint4 qv[8];                      // row 8 g + tid % 8, channels 8 (tid / 8) .. +7
+      // row 8 g + tid % 8, channels 8 (tid / 8) .. +7; four rows at a time, and once more for the conversion
+      // (from L2: eight of them in registers would have the other roles' code spill)
+      const uint16_t* src = a.Q + ((int64_t)b * rows + r0 + (tid & 7)) * kD + (tid >> 3) * 8;
+      const int live = (int)min(rows - r0 - (tid & 7), (int64_t)kRows);
+      auto load4 = [&](int g0, uint4 (&qv)[4]) {
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const int h = 8 * g + (tid & 7);
-        qv[g] = r0 + h < rows ? __ldg(reinterpret_cast<const uint4*>(a.Q + ((int64_t)b * rows + r0 + h) * kD + (tid >> 3) * 8))
-                              : make_uint4(0, 0, 0, 0);
-      }
+        for (int g = 0; g < 4; ++g)
+          qv[g] = 8 * (g0 + g) < live ? __ldg(reinterpret_cast<const uint4*>(src + 8 * (g0 + g) * kD)) : make_uint4(0, 0, 0, 0);
+      };
+      uint4 qv[4];
+      load4(0, qv);
       if (tid < kRows) sm.qexp[1][tid] = 0;
       fill_sync();
+#pragma unroll 1
+      for (int g0 = 0; g0 < 8; g0 += 4) {
+        if (g0) load4(g0, qv);
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        uint32_t e = 0;
+        for (int g = 0; g < 4; ++g) {
+          uint32_t e = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) e = max(e, max(word_of(qv[g], j) & 0x7F80u, (word_of(qv[g], j) >> 16) & 0x7F80u));
-        e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
-        e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
-        if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * g + lane], (int)(e >> 7));
+          for (int j = 0; j < 4; ++j) e = max(e, max(word_of(qv[g], j) & 0x7F80u, (word_of(qv[g], j) >> 16) & 0x7F80u));
+          e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
+          e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
+          if (lane < 8 && e) atomicMax(&sm.qexp[1][8 * (g0 + g) + lane], (int)(e >> 7));
+        }
       }
       fill_sync();
+#pragma unroll 1
+      for (int g0 = 4; g0 >= 0; g0 -= 4) {
+        if (g0 == 0) load4(0, qv);
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * g + (tid & 7)]));
-        uint32_t ov[4];
+        for (int g = 0; g < 4; ++g) {
+          const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * (g0 + g) + (tid & 7)]));
+          uint32_t ov[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = word_of(qv[g], j);
-          ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = word_of(qv[g], j);
+            ov[j] = f32x2_f16x2(__uint_as_float(w << 16) * qs, __uint_as_float(w & 0xFFFF0000u) * qs);
+          }
+          *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + (g0 + g) * 8192 + (tid >> 3) * 128 + (tid & 7) * 16) =
+              make_uint4(ov[0], ov[1], ov[2], ov[3]);
         }
-        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.q) + g * 8192 + (tid >> 3) * 128 + (tid & 7) * 16) =
-            make_uint4(ov[0], ov[1], ov[2], ov[3]);
       }
     }
     if (tid < kRows) sm.mult[tid] = a.scale * kLog2e * pow2i(q_head_exp(sm.qexp[1][tid]));
@@ -638,10 +673,10 @@ __device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
     tc::tc_fence_after();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
-    if (!values)
-      fill_tile<kWeights, false>(cx, sp.k0, sp.n, chunks, entries, warp, lane);
-    else if (!kWeights)
-      fill_tile<kWeights, true>(cx, sp.k0, sp.n, chunks, entries, warp, lane);
+    if (kWeights || !values)
+      fill_tile<kWeights, false>(cx, sp.k0, sp.n, chunks, entries, values, warp, lane);
+    else
+      fill_tile<kWeights, true>(cx, sp.k0, sp.n, chunks, entries, 0, warp, lane);
     block_sync();                       // the tile's products are complete, l is known
     tc::tc_fence_after();
     if (*abort) break;
@@ -695,7 +730,7 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
       const int page = __shfl_sync(0xffffffffu, pages, 2 * ((n >> 2) & 15) + (lane & 1));
       if (use > 0 && !warp_wait(kV ? &sm.vst_free[slot] : &sm.kst_free[slot], (use - 1) & 1, abort)) break;
       const uint32_t have = __ballot_sync(0xffffffffu, lane < 2 && page >= 0);
-      uint64_t* full = kV ? &sm.vst_full[st % kMax4<kStage>] : &sm.kst_full[st % kMax4<kStage>];
+      uint64_t* full = kV ? &sm.vst_full[slot] : &sm.kst_full[slot];
       if (lane == 0) tc::mbar_arrive_expect_tx(full, __popc(have) * (kStageBytes / 2));
       __syncwarp();
       if (lane < 2 && page >= 0)
@@ -713,9 +748,7 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
   if (*abort)
     for (uint32_t st = issued > (uint32_t)kStage ? issued - kStage : 0; st < issued; ++st)
       for (uint32_t n = 0; n < (1u << 22); ++n)
-        if (tc::mbar_try_wait(kV ? &sm.vst_full[st % kMax4<kStage>] : &sm.kst_full[st % kMax4<kStage>],
-                              (st / kMax4<kStage>) & 1))
-          break;
+        if (tc::mbar_try_wait(kV ? &sm.vst_full[st % kStage] : &sm.kst_full[st % kStage], (st / kStage) & 1)) break;
 }
 
 // One key of a chunk as its softmax thread sees it.
@@ -874,19 +907,19 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
     seg_arrive();
     block_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = max(1, sm.seg.n_chunks), nw = sm.seg.nw;
-    const int e_lo = sm.seg.e_lo, e_hi = sm.seg.e_hi, c_hi = sm.seg.c_hi;
+    const Segment& sg = sm.seg;   // (read where needed: registers are what this role is short of)
 
+    const int shift32 = (int)min(shift, (int64_t)1 << 29);
     // The key of a chunk; its page is read one chunk ahead.
-    auto entry_of = [&](int i) -> int { return (c_hi - 1 - (sp.k0 + i - nw)) * kChunk + key; };
+    auto entry_of = [&](int i) -> int { return (sg.c_hi - 1 - (sp.k0 + i - sg.nw)) * kChunk + key; };
     constexpr int kStep = kWeights ? 2 : 1;
     const int first = kWeights ? half : 0;
-    auto page_ahead = [&](int i) -> int { return page_of<kWeights>(cx, entry_of(i), i < sp.n && sp.k0 + i >= nw); };
+    auto page_ahead = [&](int i) -> int { return page_of<kWeights>(cx, entry_of(i), i < sp.n && sp.k0 + i >= sg.nw); };
     int page = page_ahead(first);
     auto view = [&](int i, int64_t* slot) -> KeyView {
       KeyView kv;
       const int k = sp.k0 + i;
-      kv.win = k < nw;
+      kv.win = k < sg.nw;
       kv.kf = 1.f;
       kv.ff = 0.f;
       kv.j = 0;
@@ -906,10 +939,10 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       } else {
         const int e0 = entry_of(i) - key;
         kv.j = entry_of(i);
-        kv.seen = kv.j >= e_lo && kv.j < e_hi && page >= 0 && page < a.n_pages;
+        kv.seen = kv.j >= sg.e_lo && kv.j < sg.e_hi && page >= 0 && page < a.n_pages;
         if (kv.seen) *slot = (int64_t)page * kPage + (kv.j & (kPage - 1));
         kv.p = a.entry_pos && kv.seen ? max(__ldg(a.entry_pos + *slot), INT_MIN + 3)
-                                      : (int)min(4 * ((int64_t)kv.j + shift) + 3, (int64_t)INT_MAX);
+                                      : kv.j + shift32 < (1 << 29) ? 4 * (kv.j + shift32) + 3 : INT_MAX;
         kv.masked = e0 < sm.seg.all_lo || e0 + kChunk > sm.seg.all_hi || __any_sync(0xffffffffu, !kv.seen);
       }
       page = page_ahead(i + kStep);
@@ -1071,6 +1104,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         }
       }
     }
+    const int units = max(1, sm.seg.n_chunks);
     block_sync();
     if (*abort) break;
     c.add(sp.n);
@@ -1228,15 +1262,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      tc::mbar_init(&sm.kq_full[i], 4);
+      tc::mbar_init(&sm.kq_full[i], 8);
       tc::mbar_init(&sm.kq_free[i], 1);
-      tc::mbar_init(&sm.v_full[i], 4);
+      tc::mbar_init(&sm.v_full[i], 8);
       tc::mbar_init(&sm.v_free[i], 1);
     }
-    for (int i = 0; i < kMax4<Stages<kWeights>::K>; ++i) tc::mbar_init(&sm.kst_full[i], 1);
-    for (int i = 0; i < Stages<kWeights>::K; ++i) tc::mbar_init(&sm.kst_free[i], 4);
-    for (int i = 0; i < kMax4<Stages<kWeights>::V>; ++i) tc::mbar_init(&sm.vst_full[i], 1);
-    for (int i = 0; i < Stages<kWeights>::V; ++i) tc::mbar_init(&sm.vst_free[i], 4);
+    for (int i = 0; i < Stages<kWeights>::K; ++i) {
+      tc::mbar_init(&sm.kst_full[i], 1);
+      tc::mbar_init(&sm.kst_free[i], 8);
+    }
+    for (int i = 0; i < Stages<kWeights>::V; ++i) {
+      tc::mbar_init(&sm.vst_full[i], 1);
+      tc::mbar_init(&sm.vst_free[i], 8);
+    }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
       tc::mbar_init(&sm.s_free[i], kWeights ? kSoftWarps / 2 : kSoftWarps);
