@@ -480,7 +480,6 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   constexpr int kRing = kV ? kVSlots : Cols<kWeights>::ring, kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
-  constexpr bool kEarly = kStage < 4;        // few slots: they are wanted back at once
   const int lq = warp & 3, half = warp >> 2, key = 32 * lq + lane;
   volatile int* abort = &sm.abort;
   const uint32_t dst_k = cx.tm + Cols<kWeights>::K + 32 * half + ((uint32_t)(32 * lq) << 16);
@@ -494,14 +493,9 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
       tmem_st8u(dst_k + 64 * slot + 8 * p, o);
     }
   };
-  auto ring_free = [&](uint32_t number, int q) {   // the quarter that was in the slot has been read
-    if (number >= (uint32_t)kRing &&
-        !warp_wait(kV ? &sm.v_free[(q - kRing) & 3] : &sm.kq_free[(q - kRing) & 3], ((number - kRing) >> 2) & 1, abort))
-      return false;
-    if (!kV) tc::tc_fence_after();
-    return true;
-  };
-  auto ring_full = [&](int q, uint64_t* staged) {
+  // The barrier of the quarter that was in the slot before (a slot's first use: a phase that is over).
+  auto ring_bar = [&](int q) { return kV ? &sm.v_free[(q - kRing) & 3] : &sm.kq_free[(q - kRing) & 3]; };
+  auto ring_full = [&](int q) {
     if (kV) {
       tc::fence_async_smem();
     } else {
@@ -509,10 +503,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
       tc::tc_fence_before();
     }
     __syncwarp();
-    if (lane == 0) {
-      tc::mbar_arrive(kV ? &sm.v_full[q] : &sm.kq_full[q]);
-      if (staged) tc::mbar_arrive(staged);
-    }
+    if (lane == 0) tc::mbar_arrive(kV ? &sm.v_full[q] : &sm.kq_full[q]);
   };
   const int i0 = min(max(sm.seg.nw - k0, 0), n_chunks);   // first entry chunk of the span
   uint32_t chunk4 = 4 * chunks;
@@ -520,7 +511,8 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
 #pragma unroll 1
     for (int n = 0; n < 4 * i0; ++n) {
       const int q = n & 3;
-      if (!ring_free(chunk4 + n, q)) return;
+      if (!warp_wait(ring_bar(q), ((chunk4 + n - kRing) >> 2) & 1, abort)) return;
+      if (!kV) tc::tc_fence_after();
       const KeyRef w = window_ref<kWeights>(cx, k0 + (n >> 2), key);
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
@@ -529,7 +521,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
         __syncwarp();
         put((chunk4 + n) % kRing, p, o);
       }
-      ring_full(q, nullptr);
+      ring_full(q);
     }
     chunk4 += 4 * i0;
   }
@@ -556,10 +548,26 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   uint32_t at = place(j, page_at(j)), at1 = kNone;
   uint32_t next = scales_of(at, 0);
   int page1 = left > 1 ? page_at(j - kChunk) : -1;
-  uint32_t st4 = 4 * entries + first;
+  constexpr int kStep = kWeights ? 2 : 1;
+  uint32_t st = 4 * entries + first;      // running number among the staged quarters
+  auto staged_bar = [&](uint32_t st) { return kV ? &sm.vst_full[st % kStage] : &sm.kst_full[st % kStage]; };
+  uint4 t[2];
+  auto load_staged = [&] {
+    const unsigned char* src = (kV ? sm.vst[st % kStage] : sm.kst[st % kStage]) + 64 * key;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) t[p] = *reinterpret_cast<const uint4*>(src + 16 * ((2 * half + p) ^ ((key >> 1) & 3)));
+  };
+  // The slot may be written again once the loads have arrived, not when they are issued: the vote reads
+  // a word of each (lane 0 always votes yes).
+  auto free_staged = [&] {
+    if (__ballot_sync(0xffffffffu, lane == 0 || (t[0].x ^ t[1].x) == 0x5A5A5A5Au) & (lane == 0))
+      tc::mbar_arrive(kV ? &sm.vst_free[st % kStage] : &sm.kst_free[st % kStage]);
+  };
+  if (!warp_wait(staged_bar(st), (st / kStage) & 1, abort)) return;
+  load_staged();
+  free_staged();
 #pragma unroll 1
   for (int q2 = 0;;) {                    // q2: this quarter less `first`
-    constexpr int kStep = kWeights ? 2 : 1;
     const int q = q2 + first;
     if (q2 == 0) {
       at1 = left > 1 ? place(j - kChunk, page1) : kNone;
@@ -567,27 +575,28 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
     }
     const uint32_t s = next;
     next = q2 + kStep < 4 ? scales_of(at, q2 + kStep) : scales_of(at1, 0);
-    const uint32_t st = st4 + q2, slot = st % kStage;   // running number among the staged quarters
-    if (!warp_wait(kV ? &sm.vst_full[slot] : &sm.kst_full[slot], (st / kStage) & 1, abort)) return;
-    const unsigned char* src = (kV ? sm.vst[slot] : sm.kst[slot]) + 64 * key;
-    uint4 t[2];
-#pragma unroll
-    for (int p = 0; p < 2; ++p) t[p] = *reinterpret_cast<const uint4*>(src + 16 * ((2 * half + p) ^ ((key >> 1) & 3)));
-    // The slot may be written again once the loads have arrived, not when they are issued: the vote
-    // reads a word of each (lane 0 always votes yes).  With many slots that can wait for the quarter's end.
-    if (kEarly) {
-      if (__ballot_sync(0xffffffffu, lane == 0 || (t[0].x ^ t[1].x) == 0x5A5A5A5Au) & (lane == 0))
-        tc::mbar_arrive(kV ? &sm.vst_free[slot] : &sm.kst_free[slot]);
-    }
-    const uint32_t number = chunk4 + q;
-    if (!ring_free(number, q)) return;
+    const bool more = left > 1 || q2 + kStep < 4;
+    st += kStep;                          // the next step's
+    // One look at two barriers (a look is a trip through the busy shared-memory pipe, 180 cycles): lane
+    // 0 at this step's ring slot, lane 1 at the next step's codes.
+    const uint32_t number = chunk4 + q, parity = ((number - kRing) >> 2) & 1;
+    const bool there = mbar_test(tc::smem_addr(lane == 1 ? staged_bar(st) : ring_bar(q)), lane == 1 ? (st / kStage) & 1 : parity);
+    const uint32_t look = __ballot_sync(0xffffffffu, there);
+    __syncwarp();
+    if (!(look & 1) && !warp_wait(ring_bar(q), parity, abort)) return;
+    if (!kV) tc::tc_fence_after();
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       uint32_t o[8];
       dequant16(t[p >> 1], s >> (16 * (p >> 1)), p & 1, o);
       put(number % kRing, p, o);
     }
-    ring_full(q, kEarly ? nullptr : kV ? &sm.vst_free[slot] : &sm.kst_free[slot]);
+    if (more) {
+      if (!(look & 2) && !warp_wait(staged_bar(st), (st / kStage) & 1, abort)) return;
+      load_staged();
+    }
+    ring_full(q);
+    if (more) free_staged();
     q2 += kStep;
     if (q2 >= 4) {
       if (--left == 0) break;
@@ -595,7 +604,6 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
       j -= kChunk;
       at = at1;
       chunk4 += 4;
-      st4 += 4;
     }
   }
 }
