@@ -178,12 +178,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait of a whole warp; on time-out the CTA's abort flag is raised.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   bool ok = false;
 #pragma unroll 1
   for (uint32_t i = 0; i < (1u << 21); ++i) {   // <= 2^21 suspensions of <= 1 us
-    if (tc::mbar_try_wait_sleep(bar, parity, 1000)) {
+    if (mbar_try_wait_at(bar, parity)) {
       ok = true;
       break;
     }
@@ -192,6 +201,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) *abort = 1;
   return ok;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return warp_wait(tc::smem_addr(bar), parity, abort);
 }
 
 // Shared-memory descriptors as their low words (address and leading offset; an operand's
@@ -228,6 +240,17 @@ __device__ __forceinline__ void mma_commit_by(uint32_t leader, uint64_t* bar) {
       " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_addr(bar)),
       "r"(leader)
       : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 // Whether the phase of the given parity is complete (never suspends).
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -482,19 +505,22 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   constexpr int kRing = kV ? kVSlots : Cols<kWeights>::ring, kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
   const int lq = warp & 3, half = warp >> 2, key = 32 * lq + lane;
   volatile int* abort = &sm.abort;
-  const uint32_t dst_k = cx.tm + Cols<kWeights>::K + 32 * half + ((uint32_t)(32 * lq) << 16);
-  unsigned char* dst_v = reinterpret_cast<unsigned char*>(sm.v) + (key >> 3) * 2048 + (key & 7) * 16 + half * 1024;
-  auto put = [&](uint32_t slot, int p, const uint32_t (&o)[8]) {   // channels 16 p .. +15 of the half
+  constexpr uint32_t kSlot = kV ? kChunk * kQuarter * 2 : 64;   // a ring slot: bytes, or tensor-memory columns
+  const uint32_t dst0 = kV ? tc::smem_addr(sm.v) + (key >> 3) * 2048 + (key & 7) * 16 + half * 1024
+                           : cx.tm + Cols<kWeights>::K + 32 * half + ((uint32_t)(32 * lq) << 16);
+  auto put = [&](uint32_t dst, int p, const uint32_t (&o)[8]) {   // channels 16 p .. +15 of the half
     if (kV) {
-      unsigned char* d = dst_v + slot * (kChunk * kQuarter * 2) + 2 * p * 128;
-      *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(d + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+      sts16(dst + 256 * p, o[0], o[1], o[2], o[3]);
+      sts16(dst + 256 * p + 128, o[4], o[5], o[6], o[7]);
     } else {
-      tmem_st8u(dst_k + 64 * slot + 8 * p, o);
+      tmem_st8u(dst + 8 * p, o);
     }
   };
-  // The barrier of the quarter that was in the slot before (a slot's first use: a phase that is over).
-  auto ring_bar = [&](int q) { return kV ? &sm.v_free[(q - kRing) & 3] : &sm.kq_free[(q - kRing) & 3]; };
+  // Barriers of quarter q's data, and of the quarter that was in its slot before (a slot's first use: a
+  // phase that is over); cp: the chunk's running number.
+  const uint32_t full_bar = tc::smem_addr(kV ? sm.v_full : sm.kq_full), free_bar = tc::smem_addr(kV ? sm.v_free : sm.kq_free);
+  auto ring_bar = [&](int q) { return free_bar + 8 * ((q - kRing) & 3); };
+  auto ring_parity = [&](uint32_t cp, int q) { return (kRing == 3 && q == 3 ? cp : cp + 1) & 1; };
   auto ring_full = [&](int q) {
     if (kV) {
       tc::fence_async_smem();
@@ -503,15 +529,15 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
       tc::tc_fence_before();
     }
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(kV ? &sm.v_full[q] : &sm.kq_full[q]);
+    if (lane == 0) arrive_at(full_bar + 8 * q);
   };
   const int i0 = min(max(sm.seg.nw - k0, 0), n_chunks);   // first entry chunk of the span
-  uint32_t chunk4 = 4 * chunks;
+  uint32_t ring = (4 * chunks + first) % kRing;   // slot of the step's quarter
   if (!kWeights) {
 #pragma unroll 1
     for (int n = 0; n < 4 * i0; ++n) {
       const int q = n & 3;
-      if (!warp_wait(ring_bar(q), ((chunk4 + n - kRing) >> 2) & 1, abort)) return;
+      if (!warp_wait(ring_bar(q), ring_parity(chunks, q), abort)) return;
       if (!kV) tc::tc_fence_after();
       const KeyRef w = window_ref<kWeights>(cx, k0 + (n >> 2), key);
 #pragma unroll 1
@@ -519,11 +545,12 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
         uint32_t o[8];
         window_piece(w, 8 * q + 4 * half + p, o);
         __syncwarp();
-        put((chunk4 + n) % kRing, p, o);
+        put(dst0 + ring * kSlot, p, o);
       }
       ring_full(q);
+      ring = ring + 1 == kRing ? 0 : ring + 1;
+      chunks += q == 3;
     }
-    chunk4 += 4 * i0;
   }
   if (i0 >= n_chunks) return;
   // A step's four scales are read a step ahead, the key's page a chunk ahead of that.  The offset is
@@ -549,21 +576,21 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   uint32_t next = scales_of(at, 0);
   int page1 = left > 1 ? page_at(j - kChunk) : -1;
   constexpr int kStep = kWeights ? 2 : 1;
-  uint32_t st = 4 * entries + first;      // running number among the staged quarters
-  auto staged_bar = [&](uint32_t st) { return kV ? &sm.vst_full[st % kStage] : &sm.kst_full[st % kStage]; };
+  // the staging slot of the step's codes and its phase
+  uint32_t slot = (4 * entries + first) % kStage, phase = ((4 * entries + first) / kStage) & 1;
+  const uint32_t st_full = tc::smem_addr(kV ? sm.vst_full : sm.kst_full), st_free = tc::smem_addr(kV ? sm.vst_free : sm.kst_free);
+  const uint32_t codes = tc::smem_addr(kV ? sm.vst[0] : sm.kst[0]) + 64 * key + 16 * ((2 * half) ^ ((key >> 1) & 3));
   uint4 t[2];
   auto load_staged = [&] {
-    const unsigned char* src = (kV ? sm.vst[st % kStage] : sm.kst[st % kStage]) + 64 * key;
-#pragma unroll
-    for (int p = 0; p < 2; ++p) t[p] = *reinterpret_cast<const uint4*>(src + 16 * ((2 * half + p) ^ ((key >> 1) & 3)));
+    t[0] = lds16(codes + slot * kStageBytes);
+    t[1] = lds16((codes + slot * kStageBytes) ^ 16);
   };
   // The slot may be written again once the loads have arrived, not when they are issued: the vote reads
   // a word of each (lane 0 always votes yes).
   auto free_staged = [&] {
-    if (__ballot_sync(0xffffffffu, lane == 0 || (t[0].x ^ t[1].x) == 0x5A5A5A5Au) & (lane == 0))
-      tc::mbar_arrive(kV ? &sm.vst_free[st % kStage] : &sm.kst_free[st % kStage]);
+    if (__ballot_sync(0xffffffffu, lane == 0 || (t[0].x ^ t[1].x) == 0x5A5A5A5Au) & (lane == 0)) arrive_at(st_free + 8 * slot);
   };
-  if (!warp_wait(staged_bar(st), (st / kStage) & 1, abort)) return;
+  if (!warp_wait(st_full + 8 * slot, phase, abort)) return;
   load_staged();
   free_staged();
 #pragma unroll 1
@@ -576,34 +603,41 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
     const uint32_t s = next;
     next = q2 + kStep < 4 ? scales_of(at, q2 + kStep) : scales_of(at1, 0);
     const bool more = left > 1 || q2 + kStep < 4;
-    st += kStep;                          // the next step's
+    slot += kStep;                        // the next step's
+    if (slot >= kStage) {
+      slot -= kStage;
+      phase ^= 1;
+    }
     // One look at two barriers (a look is a trip through the busy shared-memory pipe, 180 cycles): lane
     // 0 at this step's ring slot, lane 1 at the next step's codes.
-    const uint32_t number = chunk4 + q, parity = ((number - kRing) >> 2) & 1;
-    const bool there = mbar_test(tc::smem_addr(lane == 1 ? staged_bar(st) : ring_bar(q)), lane == 1 ? (st / kStage) & 1 : parity);
-    const uint32_t look = __ballot_sync(0xffffffffu, there);
+    const uint32_t parity = ring_parity(chunks, q);
+    const uint32_t look = __ballot_sync(
+        0xffffffffu, mbar_test(lane == 1 ? st_full + 8 * slot : ring_bar(q), lane == 1 ? phase : parity));
     __syncwarp();
     if (!(look & 1) && !warp_wait(ring_bar(q), parity, abort)) return;
     if (!kV) tc::tc_fence_after();
+    const uint32_t dst = dst0 + ring * kSlot;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       uint32_t o[8];
       dequant16(t[p >> 1], s >> (16 * (p >> 1)), p & 1, o);
-      put(number % kRing, p, o);
+      put(dst, p, o);
     }
     if (more) {
-      if (!(look & 2) && !warp_wait(staged_bar(st), (st / kStage) & 1, abort)) return;
+      if (!(look & 2) && !warp_wait(st_full + 8 * slot, phase, abort)) return;
       load_staged();
     }
     ring_full(q);
     if (more) free_staged();
+    ring += kStep;
+    if (ring >= kRing) ring -= kRing;
     q2 += kStep;
     if (q2 >= 4) {
       if (--left == 0) break;
       q2 = 0;
       j -= kChunk;
       at = at1;
-      chunk4 += 4;
+      ++chunks;
     }
   }
 }
