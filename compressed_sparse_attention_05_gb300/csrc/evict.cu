@@ -11,10 +11,14 @@
 //
 // k_evict_select: a cluster of up to 8 CTAs per sequence.  Every CTA holds its
 // share of the order-preserving weight keys in shared memory (one read of the
-// weights); three radix passes (11, 11, 10 bits) over cluster-wide histograms
-// (distributed shared memory) find the keep-th largest key and how many of its
-// equals stay; a prefix count over the cluster then numbers holes and movers in
-// index order.  k_evict_move copies the rows, one warp per row, over all SMs.
+// weights; a share that does not fit lies in the workspace); three radix passes
+// (11, 11, 10 bits), each over its own cluster-wide histogram (distributed shared
+// memory), find the keep-th largest key and how many of its equals stay; counts
+// by ballots, in index order, number holes and movers over the cluster.  A call on
+// a cache of a few thousand entries is a chain of dependent trips (page, weight,
+// five cluster barriers, lists, pages again, rows), so every step has all its
+// loads in flight at once.  k_evict_move copies the rows, one warp per row and
+// four rows of a warp in flight, over all SMs.
 #include <algorithm>
 
 #include "common.cuh"
@@ -23,10 +27,11 @@
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxCached = 48 * 1024;    // keys of one CTA held in shared memory (192 KB)
+constexpr int kMaxCached = 48 * 1024;    // keys of one CTA held in shared memory (192 KB beside 24 KB of histograms)
 constexpr int kMinPerCta = 2048;         // entries that make another CTA of the cluster worth its barriers
 
 // Order-preserving key of a weight (larger key = larger weight; zeros are equal;
@@ -57,42 +62,43 @@ struct EvictWs {
   int32_t* n_moves;   // [B]
   int32_t* holes;     // [B][cap]
   int32_t* movers;    // [B][cap]
+  uint32_t* keys;     // [B][cap], or null while every share fits in shared memory
   int64_t cap;
 };
 
-// Sum over the block of v, and the exclusive prefix of this thread (thread order).
-__device__ __forceinline__ uint64_t block_prefix(uint64_t v, uint64_t* warp_sums, uint64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t inc = v;
+// Exclusive prefix (thread order) of v over the block, and the sum.
+__device__ __forceinline__ uint32_t warp_inclusive(uint32_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
+    const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
   }
+  return v;
+}
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t inc = warp_inclusive(v, lane);
   __syncthreads();
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  uint64_t before = 0, all = 0;
-#pragma unroll
-  for (int k = 0; k < kThreads / 32; ++k) {
-    const uint64_t s = warp_sums[k];
-    if (k < warp) before += s;
-    all += s;
-  }
-  *total = all;
-  return before + inc - v;
+  const uint32_t all = warp_inclusive(warp_sums[lane], lane);   // (32 warps)
+  *total = __shfl_sync(0xffffffffu, all, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
+  return (warp ? before : 0) + inc - v;
 }
+static_assert(kWarps == 32, "a warp scans the warps' sums");
 
 __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs ws, int n_cl, int cached,
                                                            uint32_t* status) {
-  extern __shared__ uint32_t keys[];     // [cached] this CTA's keys (when its share fits)
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint64_t warp_sums[kThreads / 32];
-  __shared__ uint32_t pub[4];            // read by the cluster's other CTAs
-  __shared__ uint32_t found[2];
+  extern __shared__ uint32_t smem_keys[];   // [cached] this CTA's keys (when its share fits)
+  __shared__ uint32_t hist[3][kBins];    // read by the cluster's other CTAs, as are pub
+  __shared__ uint32_t warp_sums[kWarps];
+  __shared__ uint32_t pub[3];
+  __shared__ uint32_t found[3];
   pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
   pdl_wait();
-  const int tid = threadIdx.x;
   const int b = (int)blockIdx.x / n_cl;
   const int rank = n_cl > 1 ? (int)cl_rank() : 0;
   const int n = a.n_entries[b];
@@ -106,98 +112,124 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
     }
     return;
   }
-  // this CTA's entries [lo, hi), each thread's run of them [t0, t1)
-  const int lo = (int)((int64_t)n * rank / n_cl), hi = (int)((int64_t)n * (rank + 1) / n_cl);
-  const bool in_smem = hi - lo <= cached;
+  // this CTA's entries [lo, lo + count)
+  const int lo = (int)((int64_t)n * rank / n_cl), count = (int)((int64_t)n * (rank + 1) / n_cl) - lo;
+  uint32_t* keys = count <= cached ? smem_keys : ws.keys + (int64_t)b * ws.cap + lo;
   const int64_t first_recent = 4 * ((int64_t)n + shift - a.n_recent) + 3;
-  auto fetch = [&](int j, bool report) -> uint32_t {
-    const int64_t slot = entry_slot(a.page_table, a.max_pages, a.n_pages, b, j, report ? status : nullptr);
-    if (slot < 0) return 0u;
-    const int64_t p = a.entry_pos[slot];
-    return (p < 4ll * a.n_sink || p >= first_recent) ? 0xFFFFFFFFu : weight_key(a.weight[slot]);
-  };
-  if (in_smem) {
-    for (int j = lo + tid; j < hi; j += kThreads) keys[j - lo] = fetch(j, true);
+  __syncthreads();
+  // ---- keys, four loads of each kind in flight, and the first digit's histogram
+  constexpr int kAhead = 4;
+  for (int j0 = tid; j0 < count; j0 += kAhead * kThreads) {
+    int64_t slot[kAhead];
+    int pos[kAhead];
+    float w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * kThreads;
+      slot[i] = j < count ? entry_slot(a.page_table, a.max_pages, a.n_pages, b, lo + j, status) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      pos[i] = slot[i] >= 0 ? a.entry_pos[slot[i]] : 0;
+      w[i] = slot[i] >= 0 ? a.weight[slot[i]] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * kThreads;
+      if (j >= count) break;
+      const uint32_t k = slot[i] < 0 ? 0u
+                         : pos[i] < 4ll * a.n_sink || pos[i] >= first_recent ? 0xFFFFFFFFu
+                                                                              : weight_key(w[i]);
+      keys[j] = k;
+      atomicAdd(&hist[0][k >> 21], 1u);
+    }
   }
-  auto key_of = [&](int j) -> uint32_t { return in_smem ? keys[j - lo] : fetch(j, false); };
 
   // ---- the keep-th largest key, digit by digit from the top
   uint32_t prefix = 0, mask = 0;
   uint32_t need = (uint32_t)a.keep;      // entries still to be taken among those that match the prefix
-  const int shifts[3] = {21, 10, 0}, widths[3] = {11, 11, 10};
+#pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int sh = shifts[pass], nb = 1 << widths[pass];
-    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    for (int j = lo + tid; j < hi; j += kThreads) {
-      const uint32_t k = key_of(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> sh) & (nb - 1)], 1u);
-    }
+    const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, nb = pass == 2 ? 1024 : 2048;
+    if (pass > 0)
+      for (int j = tid; j < count; j += kThreads) {
+        const uint32_t k = keys[j];
+        if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> sh) & (nb - 1)], 1u);
+      }
     __syncthreads();
     if (n_cl > 1) cl_sync();
-    // bins from the top: thread t holds bins nb-1-4t .. nb-4-4t
-    uint32_t c[4] = {0, 0, 0, 0};
-    uint32_t mine = 0;
+    // bins from the top: thread t holds bins nb-1-2t and nb-2-2t
+    uint32_t c[2] = {0, 0};
+    const int top = nb - 1 - 2 * tid;
+    if (top >= 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int bin = nb - 1 - (4 * tid + i);
-      if (bin >= 0) {
-        if (n_cl > 1)
-          for (int q = 0; q < n_cl; ++q) c[i] += cl_load(&hist[bin], q);
-        else
-          c[i] = hist[bin];
-      }
-      mine += c[i];
-    }
-    uint64_t total;
-    const uint64_t before = block_prefix(mine, warp_sums, &total);
-    if (before < need && before + mine >= need) {
-      uint32_t above = (uint32_t)before;
-      for (int i = 0; i < 4; ++i) {
-        if (above + c[i] >= need) {
-          found[0] = (uint32_t)(nb - 1 - (4 * tid + i));
-          found[1] = need - above;
-          break;
+      for (int i = 0; i < 2; ++i) {
+        c[i] = n_cl > 1 ? 0 : hist[pass][top - i];
+        if (n_cl > 1) {
+#pragma unroll
+          for (int q = 0; q < kMaxCluster; ++q) c[i] += q < n_cl ? cl_load(&hist[pass][top - i], q) : 0;
         }
-        above += c[i];
       }
     }
-    if (n_cl > 1) cl_sync(); else __syncthreads();   // also: every rank has read this pass's histograms
+    const uint32_t mine = c[0] + c[1];
+    uint32_t total;
+    const uint32_t before = block_prefix(mine, warp_sums, &total);
+    if (before < need && before + mine >= need) {
+      const int i = before + c[0] >= need ? 0 : 1;
+      found[0] = (uint32_t)(top - i);
+      found[1] = need - before - (i ? c[0] : 0);
+      found[2] = c[i];
+    }
+    __syncthreads();
     prefix |= found[0] << sh;
     mask |= (uint32_t)(nb - 1) << sh;
     need = found[1];
-    __syncthreads();
   }
   const uint32_t thr = prefix;           // keys above stay; of its equals the `need` lowest indices
+  const bool all_equals = found[2] == need;
 
-  // ---- equals before each thread's run, over the cluster
-  const int run = (hi - lo + kThreads - 1) / kThreads;
-  const int t0 = min(hi, lo + tid * run), t1 = min(hi, t0 + run);
-  uint32_t eq = 0;
-  for (int j = t0; j < t1; ++j) eq += key_of(j) == thr;
-  uint64_t total;
-  uint32_t eq_before = (uint32_t)block_prefix(eq, warp_sums, &total);
-  if (tid == 0) pub[0] = (uint32_t)total;
-  if (n_cl > 1) {
-    cl_sync();
-    for (int q = 0; q < rank; ++q) eq_before += cl_load(&pub[0], q);
+  // ---- each warp a run of the share, 32 entries at a time, in index order
+  const int run = (count + kThreads - 1) / kThreads * 32;
+  const int w0 = min(count, warp * run), w1 = min(count, w0 + run);
+  uint32_t eq_before = 0;                // equals at lower indices than the warp's run
+  uint32_t total;
+  if (!all_equals) {
+    uint32_t eq = 0;
+    for (int j0 = w0; j0 < w1; j0 += 32) eq += __popc(__ballot_sync(0xffffffffu, j0 + lane < w1 && keys[j0 + lane] == thr));
+    eq_before = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? eq : 0, warp_sums, &total), 0);
+    if (tid == 0) pub[0] = total;
+    if (n_cl > 1) {
+      cl_sync();
+      for (int q = 0; q < rank; ++q) eq_before += cl_load(&pub[0], q);
+    }
   }
+  // Lane's entry j0 + lane of the run: whether it stays; e counts the equals so far.
+  const uint32_t below = (1u << lane) - 1;
+  auto stays = [&](int j0, uint32_t& e) -> bool {
+    const bool in = j0 + lane < w1;
+    const uint32_t k = in ? keys[j0 + lane] : 0;
+    if (all_equals) return in && k >= thr;
+    const uint32_t m = __ballot_sync(0xffffffffu, in && k == thr);
+    const bool kept = in && (k > thr || (k == thr && e + __popc(m & below) < need));
+    e += __popc(m);
+    return kept;
+  };
   // ---- holes (evicted, below keep) and movers (kept, at or above keep)
   uint32_t holes = 0, movers = 0, e = eq_before;
-  for (int j = t0; j < t1; ++j) {
-    const uint32_t k = key_of(j);
-    const bool kept = k > thr || (k == thr && e < need);
-    e += k == thr;
-    holes += !kept && j < a.keep;
-    movers += kept && j >= a.keep;
+  for (int j0 = w0; j0 < w1; j0 += 32) {
+    const bool kept = stays(j0, e);
+    const int j = lo + j0 + lane;
+    holes += __popc(__ballot_sync(0xffffffffu, !kept && j0 + lane < w1 && j < a.keep));
+    movers += __popc(__ballot_sync(0xffffffffu, kept && j >= a.keep));
   }
-  uint64_t both = block_prefix(((uint64_t)holes << 32) | movers, warp_sums, &total);
-  if (tid == 0) {
-    pub[1] = (uint32_t)(total >> 32);
-    pub[2] = (uint32_t)total;
-  }
-  uint32_t h = (uint32_t)(both >> 32), m = (uint32_t)both, all_holes = (uint32_t)(total >> 32);
+  uint32_t all_holes, all_movers;
+  uint32_t h = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? holes : 0, warp_sums, &all_holes), 0);
+  uint32_t m = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? movers : 0, warp_sums, &all_movers), 0);
   if (n_cl > 1) {
+    if (tid == 0) {
+      pub[1] = all_holes;
+      pub[2] = all_movers;
+    }
     cl_sync();
     all_holes = 0;
     for (int q = 0; q < n_cl; ++q) {
@@ -208,66 +240,114 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
       }
       all_holes += hq;
     }
+    // no CTA leaves while another still reads its shared memory, and every CTA has read the count
+    // before it changes (waited for at the end)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   e = eq_before;
   int32_t* hl = ws.holes + (int64_t)b * ws.cap;
   int32_t* ml = ws.movers + (int64_t)b * ws.cap;
-  for (int j = t0; j < t1; ++j) {
-    const uint32_t k = key_of(j);
-    const bool kept = k > thr || (k == thr && e < need);
-    e += k == thr;
-    if (!kept && j < a.keep) hl[h++] = j;
-    if (kept && j >= a.keep) ml[m++] = j;
+  for (int j0 = w0; j0 < w1; j0 += 32) {
+    const bool kept = stays(j0, e);
+    const int j = lo + j0 + lane;
+    const bool hole = !kept && j0 + lane < w1 && j < a.keep, mover = kept && j >= a.keep;
+    const uint32_t hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
+    if (hole) hl[h + __popc(hm & below)] = j;
+    if (mover) ml[m + __popc(mm & below)] = j;
+    h += __popc(hm);
+    m += __popc(mm);
   }
-  if (n_cl > 1) cl_sync();               // no CTA leaves while another still reads its shared memory,
-  if (rank == 0 && tid == 0) {           // and every CTA has read the count before it changes
+  if (n_cl > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else __syncthreads();
+  if (rank == 0 && tid == 0) {
     ws.n_moves[b] = (int32_t)all_holes;
     a.n_entries[b] = a.keep;
     a.shift[b] = (int32_t)(shift + n - a.keep);
   }
 }
 
-// Copies `bytes` (a multiple of 4) of a row with a warp, 16 bytes at a time where both
-// rows start on 16 bytes.
-__device__ __forceinline__ void copy_row(uint8_t* base, int64_t to, int64_t from, int bytes, int lane) {
-  if (bytes % 16 == 0) {
-    const uint4* s = reinterpret_cast<const uint4*>(base + from * bytes);
-    uint4* d = reinterpret_cast<uint4*>(base + to * bytes);
-    for (int i = lane; i < bytes / 16; i += 32) d[i] = s[i];
-  } else {
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(base + from * bytes);
-    uint32_t* d = reinterpret_cast<uint32_t*>(base + to * bytes);
-    for (int i = lane; i < bytes / 4; i += 32) d[i] = s[i];
-  }
+// A row's bytes as a lane sees them: 16-byte pieces of the arrays whose rows are a multiple of 16
+// bytes, 4-byte words of the others (4 bytes of scales) and of the weight and position.  The
+// largest rows have 512 bytes of codes and 512 of keys: two pieces and one word for a lane.
+struct Field {
+  uint8_t* base;       // the piece of row 0 (null: none)
+  int bytes;           // row stride
+};
+__device__ __forceinline__ Field piece16(const EvictArgs& a, int i) {
+  const int nc = a.code_bytes / 16, ni = a.idx_k ? a.idx_bytes / 16 : 0, ns = a.scale_bytes / 16;
+  if (i < nc) return {a.kv_codes + 16 * i, a.code_bytes};
+  i -= nc;
+  if (i < ni) return {a.idx_k + 16 * i, a.idx_bytes};
+  i -= ni;
+  if (i < ns) return {a.kv_scales + 16 * i, a.scale_bytes};
+  return {nullptr, 0};
+}
+__device__ __forceinline__ Field piece4(const EvictArgs& a, int i) {
+  if (i == 0) return {reinterpret_cast<uint8_t*>(a.weight), 4};
+  if (i == 1) return {reinterpret_cast<uint8_t*>(a.entry_pos), 4};
+  if (i == 2 && a.scale_bytes == 4) return {a.kv_scales, 4};
+  return {nullptr, 0};
 }
 
+constexpr int kRowsAhead = 4;
 __global__ void __launch_bounds__(256) k_evict_move(EvictArgs a, EvictWs ws, uint32_t* status) {
   pdl_trigger();
-  pdl_wait();
   const int b = (int)blockIdx.y, lane = threadIdx.x & 31;
+  const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const Field f0 = piece16(a, lane), f1 = piece16(a, lane + 32), g0 = piece4(a, lane);
+  pdl_wait();
   const int n = ws.n_moves[b];
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
-    const int to = ws.holes[(int64_t)b * ws.cap + i], from = ws.movers[(int64_t)b * ws.cap + i];
-    const int64_t d = entry_slot(a.page_table, a.max_pages, a.n_pages, b, to, status);
-    const int64_t s = entry_slot(a.page_table, a.max_pages, a.n_pages, b, from, status);
-    if (d < 0 || s < 0) continue;
-    copy_row(a.kv_codes, d, s, a.code_bytes, lane);
-    copy_row(a.kv_scales, d, s, a.scale_bytes, lane);
-    if (a.idx_k) copy_row(a.idx_k, d, s, a.idx_bytes, lane);
-    if (lane == 0) {
-      a.weight[d] = a.weight[s];
-      a.entry_pos[d] = a.entry_pos[s];
+  // 32 of the warp's rows (w, w + warps, ...) at a time: lane l looks up row l of them
+  for (int i0 = 0; (int64_t)i0 * warps + w < n; i0 += 32) {
+    const int64_t at = (int64_t)(i0 + lane) * warps + w;
+    int64_t d = -1, s = -1;
+    if (at < n) {
+      d = entry_slot(a.page_table, a.max_pages, a.n_pages, b, ws.holes[(int64_t)b * ws.cap + at], status);
+      s = entry_slot(a.page_table, a.max_pages, a.n_pages, b, ws.movers[(int64_t)b * ws.cap + at], status);
+      if (s < 0) d = -1;
+    }
+    const int here = (int)min((int64_t)32, (n - w + (int64_t)warps - 1) / warps - i0);
+    for (int r = 0; r < here; r += kRowsAhead) {
+      int64_t to[kRowsAhead], from[kRowsAhead];
+      uint4 v0[kRowsAhead], v1[kRowsAhead];
+      uint32_t v2[kRowsAhead];
+#pragma unroll
+      for (int k = 0; k < kRowsAhead; ++k) {
+        to[k] = __shfl_sync(0xffffffffu, d, r + k);
+        from[k] = __shfl_sync(0xffffffffu, s, r + k);
+        if (r + k >= here) to[k] = -1;
+        if (to[k] < 0) continue;
+        if (f0.base) v0[k] = *reinterpret_cast<const uint4*>(f0.base + from[k] * f0.bytes);
+        if (f1.base) v1[k] = *reinterpret_cast<const uint4*>(f1.base + from[k] * f1.bytes);
+        if (g0.base) v2[k] = *reinterpret_cast<const uint32_t*>(g0.base + from[k] * g0.bytes);
+      }
+#pragma unroll
+      for (int k = 0; k < kRowsAhead; ++k) {
+        if (to[k] < 0) continue;
+        if (f0.base) *reinterpret_cast<uint4*>(f0.base + to[k] * f0.bytes) = v0[k];
+        if (f1.base) *reinterpret_cast<uint4*>(f1.base + to[k] * f1.bytes) = v1[k];
+        if (g0.base) *reinterpret_cast<uint32_t*>(g0.base + to[k] * g0.bytes) = v2[k];
+      }
     }
   }
 }
 
 int64_t list_cap(int max_entries) { return ((int64_t)max_entries + 3) / 4 * 4; }
+int cluster_size(int max_entries) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxCluster, ((int64_t)max_entries + kMinPerCta - 1) / kMinPerCta));
+}
+// Entries that a CTA's share can have.
+int64_t share_cap(int max_entries) {
+  const int n = cluster_size(max_entries);
+  return ((int64_t)max_entries + n - 1) / n + 1;
+}
 
 }  // namespace
 
 size_t evict_workspace_bytes(int B, int max_entries) {
   if (B <= 0 || max_entries <= 0) return 0;
-  return (((size_t)B + 63) / 64 * 64 + 2 * (size_t)B * (size_t)list_cap(max_entries)) * sizeof(int32_t);
+  const size_t lists = share_cap(max_entries) > kMaxCached ? 3 : 2;   // holes, movers, and keys that do not fit
+  return (((size_t)B + 63) / 64 * 64 + lists * (size_t)B * (size_t)list_cap(max_entries)) * sizeof(int32_t);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, void* wsp, cudaStream_t s) {
@@ -281,8 +361,9 @@ cudaError_t launch_evict(const EvictArgs& a, void* wsp, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int n_cl = std::max(1, std::min(kMaxCluster, (a.max_entries + kMinPerCta - 1) / kMinPerCta));
-  const int cached = std::min(kMaxCached, (a.max_entries + n_cl - 1) / n_cl + 1);
+  const int n_cl = cluster_size(a.max_entries);
+  const int cached = (int)std::min<int64_t>(kMaxCached, share_cap(a.max_entries));
+  ws.keys = share_cap(a.max_entries) > kMaxCached ? reinterpret_cast<uint32_t*>(ws.movers + (int64_t)a.B * ws.cap) : nullptr;
   const size_t smem = (size_t)cached * sizeof(uint32_t);
   e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)(kMaxCached * sizeof(uint32_t)));
