@@ -32,6 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCached = 48 * 1024;    // keys of one CTA held in shared memory (192 KB beside 24 KB of histograms)
+constexpr uint32_t kNone = 0xFFFFFFFFu;    // no such entry (a pool of 2^32 entries would be 1 TB of codes)
 constexpr int kMinPerCta = 2048;         // entries that make another CTA of the cluster worth its barriers
 
 // Order-preserving key of a weight (larger key = larger weight; zeros are equal;
@@ -66,7 +67,6 @@ struct EvictWs {
   int64_t cap;
 };
 
-// Exclusive prefix (thread order) of v over the block, and the sum.
 __device__ __forceinline__ uint32_t warp_inclusive(uint32_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -75,16 +75,20 @@ __device__ __forceinline__ uint32_t warp_inclusive(uint32_t v, int lane) {
   }
   return v;
 }
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
+// v0 and v1 of each warp (uniform): the sums over the warps before it, and over all.
+__device__ __forceinline__ void warps_prefix(uint32_t v0, uint32_t v1, uint32_t (*sums)[2], uint32_t (&before)[2],
+                                             uint32_t (&all)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t inc = warp_inclusive(v, lane);
   __syncthreads();
-  if (lane == 31) warp_sums[warp] = inc;
+  if (lane < 2) sums[warp][lane] = lane ? v1 : v0;
   __syncthreads();
-  const uint32_t all = warp_inclusive(warp_sums[lane], lane);   // (32 warps)
-  *total = __shfl_sync(0xffffffffu, all, 31);
-  const uint32_t before = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
-  return (warp ? before : 0) + inc - v;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t inc = warp_inclusive(sums[lane][k], lane);
+    all[k] = __shfl_sync(0xffffffffu, inc, 31);
+    before[k] = __shfl_sync(0xffffffffu, inc, max(warp - 1, 0));
+    if (warp == 0) before[k] = 0;
+  }
 }
 static_assert(kWarps == 32, "a warp scans the warps' sums");
 
@@ -92,7 +96,8 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
                                                            uint32_t* status) {
   extern __shared__ uint32_t smem_keys[];   // [cached] this CTA's keys (when its share fits)
   __shared__ uint32_t hist[3][kBins];    // read by the cluster's other CTAs, as are pub
-  __shared__ uint32_t warp_sums[kWarps];
+  __shared__ uint32_t group[3][kWarps];  // sums of 64 bins
+  __shared__ uint32_t sums[kWarps][2];
   __shared__ uint32_t pub[3];
   __shared__ uint32_t found[3];
   pdl_trigger();
@@ -117,27 +122,28 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
   uint32_t* keys = count <= cached ? smem_keys : ws.keys + (int64_t)b * ws.cap + lo;
   const int64_t first_recent = 4 * ((int64_t)n + shift - a.n_recent) + 3;
   __syncthreads();
-  // ---- keys, four loads of each kind in flight, and the first digit's histogram
-  constexpr int kAhead = 4;
+  // ---- keys, eight loads of each kind in flight, and the first digit's histogram
+  constexpr int kAhead = 8;
+
   for (int j0 = tid; j0 < count; j0 += kAhead * kThreads) {
-    int64_t slot[kAhead];
+    uint32_t slot[kAhead];
     int pos[kAhead];
     float w[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int j = j0 + i * kThreads;
-      slot[i] = j < count ? entry_slot(a.page_table, a.max_pages, a.n_pages, b, lo + j, status) : -1;
+      slot[i] = j < count ? (uint32_t)entry_slot(a.page_table, a.max_pages, a.n_pages, b, lo + j, status) : kNone;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      pos[i] = slot[i] >= 0 ? a.entry_pos[slot[i]] : 0;
-      w[i] = slot[i] >= 0 ? a.weight[slot[i]] : 0.f;
+      pos[i] = slot[i] != kNone ? a.entry_pos[slot[i]] : 0;
+      w[i] = slot[i] != kNone ? a.weight[slot[i]] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int j = j0 + i * kThreads;
       if (j >= count) break;
-      const uint32_t k = slot[i] < 0 ? 0u
+      const uint32_t k = slot[i] == kNone ? 0u
                          : pos[i] < 4ll * a.n_sink || pos[i] >= first_recent ? 0xFFFFFFFFu
                                                                               : weight_key(w[i]);
       keys[j] = k;
@@ -157,28 +163,39 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
         if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> sh) & (nb - 1)], 1u);
       }
     __syncthreads();
-    if (n_cl > 1) cl_sync();
-    // bins from the top: thread t holds bins nb-1-2t and nb-2-2t
-    uint32_t c[2] = {0, 0};
-    const int top = nb - 1 - 2 * tid;
-    if (top >= 0) {
+    // The keep-th key's bin in two looks: first the sums of 64 bins (warp w: bins 64 w ..), over the
+    // cluster, then the 64 bins of the one group; a look is one round of remote loads, all in flight.
+    // (Every CTA reading all 2,048 bins of all eight took 3.5 us a pass.)
+    const uint32_t g = __reduce_add_sync(0xffffffffu, hist[pass][64 * warp + lane] + hist[pass][64 * warp + 32 + lane]);
+    if (lane == 0) group[pass][warp] = g;
+    if (n_cl > 1) cl_sync(); else __syncthreads();
+    if (warp == 0) {
+      auto over_cluster = [&](const uint32_t* p) {
+        if (n_cl == 1) return *p;
+        uint32_t v[kMaxCluster], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        c[i] = n_cl > 1 ? 0 : hist[pass][top - i];
-        if (n_cl > 1) {
+        for (int q = 0; q < kMaxCluster; ++q) v[q] = q < n_cl ? cl_load(p, q) : 0;
 #pragma unroll
-          for (int q = 0; q < kMaxCluster; ++q) c[i] += q < n_cl ? cl_load(&hist[pass][top - i], q) : 0;
-        }
+        for (int q = 0; q < kMaxCluster; ++q) sum += v[q];
+        return sum;
+      };
+      // lane l: the l-th group from the top, then its l-th pair of bins from the top
+      uint32_t c = over_cluster(&group[pass][31 - lane]);
+      uint32_t inc = warp_inclusive(c, lane);
+      const int gl = __ffs(__ballot_sync(0xffffffffu, inc >= need)) - 1;
+      uint32_t left = need - (__shfl_sync(0xffffffffu, inc, gl) - __shfl_sync(0xffffffffu, c, gl));
+      const int top = 64 * (31 - gl) + 63 - 2 * lane;
+      const uint32_t c0 = over_cluster(&hist[pass][top]), c1 = over_cluster(&hist[pass][top - 1]);
+      c = c0 + c1;
+      inc = warp_inclusive(c, lane);
+      const int bl = __ffs(__ballot_sync(0xffffffffu, inc >= left)) - 1;
+      if (lane == bl) {
+        left -= inc - c;
+        const bool second = left > c0;
+        found[0] = (uint32_t)(top - second);
+        found[1] = left - (second ? c0 : 0);
+        found[2] = second ? c1 : c0;
       }
-    }
-    const uint32_t mine = c[0] + c[1];
-    uint32_t total;
-    const uint32_t before = block_prefix(mine, warp_sums, &total);
-    if (before < need && before + mine >= need) {
-      const int i = before + c[0] >= need ? 0 : 1;
-      found[0] = (uint32_t)(top - i);
-      found[1] = need - before - (i ? c[0] : 0);
-      found[2] = c[i];
     }
     __syncthreads();
     prefix |= found[0] << sh;
@@ -192,15 +209,22 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
   const int run = (count + kThreads - 1) / kThreads * 32;
   const int w0 = min(count, warp * run), w1 = min(count, w0 + run);
   uint32_t eq_before = 0;                // equals at lower indices than the warp's run
-  uint32_t total;
+  uint32_t before[2], all[2];
+  // Lane q: rank q's published number; the sums over the ranks before this one, and over all.
+  auto ranks_prefix = [&](const uint32_t* p, uint32_t* sum) -> uint32_t {
+    const uint32_t v = lane < n_cl ? cl_load(p, lane) : 0;
+    *sum = __reduce_add_sync(0xffffffffu, v);
+    return __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
+  };
   if (!all_equals) {
-    uint32_t eq = 0;
+    uint32_t eq = 0, sum;
     for (int j0 = w0; j0 < w1; j0 += 32) eq += __popc(__ballot_sync(0xffffffffu, j0 + lane < w1 && keys[j0 + lane] == thr));
-    eq_before = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? eq : 0, warp_sums, &total), 0);
-    if (tid == 0) pub[0] = total;
+    warps_prefix(eq, 0, sums, before, all);
+    eq_before = before[0];
     if (n_cl > 1) {
+      if (tid == 0) pub[0] = all[0];
       cl_sync();
-      for (int q = 0; q < rank; ++q) eq_before += cl_load(&pub[0], q);
+      eq_before += ranks_prefix(&pub[0], &sum);
     }
   }
   // Lane's entry j0 + lane of the run: whether it stays; e counts the equals so far.
@@ -222,24 +246,17 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
     holes += __popc(__ballot_sync(0xffffffffu, !kept && j0 + lane < w1 && j < a.keep));
     movers += __popc(__ballot_sync(0xffffffffu, kept && j >= a.keep));
   }
-  uint32_t all_holes, all_movers;
-  uint32_t h = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? holes : 0, warp_sums, &all_holes), 0);
-  uint32_t m = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? movers : 0, warp_sums, &all_movers), 0);
+  warps_prefix(holes, movers, sums, before, all);
+  uint32_t h = before[0], m = before[1], all_holes = all[0];
   if (n_cl > 1) {
     if (tid == 0) {
-      pub[1] = all_holes;
-      pub[2] = all_movers;
+      pub[1] = all[0];
+      pub[2] = all[1];
     }
     cl_sync();
-    all_holes = 0;
-    for (int q = 0; q < n_cl; ++q) {
-      const uint32_t hq = cl_load(&pub[1], q), mq = cl_load(&pub[2], q);
-      if (q < rank) {
-        h += hq;
-        m += mq;
-      }
-      all_holes += hq;
-    }
+    uint32_t sum;
+    h += ranks_prefix(&pub[1], &all_holes);
+    m += ranks_prefix(&pub[2], &sum);
     // no CTA leaves while another still reads its shared memory, and every CTA has read the count
     // before it changes (waited for at the end)
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -271,15 +288,15 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
 // largest rows have 512 bytes of codes and 512 of keys: two pieces and one word for a lane.
 struct Field {
   uint8_t* base;       // the piece of row 0 (null: none)
-  int bytes;           // row stride
+  uint32_t bytes;      // row stride
 };
 __device__ __forceinline__ Field piece16(const EvictArgs& a, int i) {
   const int nc = a.code_bytes / 16, ni = a.idx_k ? a.idx_bytes / 16 : 0, ns = a.scale_bytes / 16;
-  if (i < nc) return {a.kv_codes + 16 * i, a.code_bytes};
+  if (i < nc) return {a.kv_codes + 16 * i, (uint32_t)a.code_bytes};
   i -= nc;
-  if (i < ni) return {a.idx_k + 16 * i, a.idx_bytes};
+  if (i < ni) return {a.idx_k + 16 * i, (uint32_t)a.idx_bytes};
   i -= ni;
-  if (i < ns) return {a.kv_scales + 16 * i, a.scale_bytes};
+  if (i < ns) return {a.kv_scales + 16 * i, (uint32_t)a.scale_bytes};
   return {nullptr, 0};
 }
 __device__ __forceinline__ Field piece4(const EvictArgs& a, int i) {
@@ -289,8 +306,8 @@ __device__ __forceinline__ Field piece4(const EvictArgs& a, int i) {
   return {nullptr, 0};
 }
 
-constexpr int kRowsAhead = 4;
-__global__ void __launch_bounds__(256) k_evict_move(EvictArgs a, EvictWs ws, uint32_t* status) {
+constexpr int kRowsAhead = 4, kMoveBlocks = 4;   // rows of a warp in flight; blocks of an SM
+__global__ void __launch_bounds__(256, kMoveBlocks) k_evict_move(EvictArgs a, EvictWs ws, uint32_t* status) {
   pdl_trigger();
   const int b = (int)blockIdx.y, lane = threadIdx.x & 31;
   const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -300,33 +317,33 @@ __global__ void __launch_bounds__(256) k_evict_move(EvictArgs a, EvictWs ws, uin
   // 32 of the warp's rows (w, w + warps, ...) at a time: lane l looks up row l of them
   for (int i0 = 0; (int64_t)i0 * warps + w < n; i0 += 32) {
     const int64_t at = (int64_t)(i0 + lane) * warps + w;
-    int64_t d = -1, s = -1;
+    uint32_t d = kNone, s = kNone;
     if (at < n) {
-      d = entry_slot(a.page_table, a.max_pages, a.n_pages, b, ws.holes[(int64_t)b * ws.cap + at], status);
-      s = entry_slot(a.page_table, a.max_pages, a.n_pages, b, ws.movers[(int64_t)b * ws.cap + at], status);
-      if (s < 0) d = -1;
+      d = (uint32_t)entry_slot(a.page_table, a.max_pages, a.n_pages, b, ws.holes[(int64_t)b * ws.cap + at], status);
+      s = (uint32_t)entry_slot(a.page_table, a.max_pages, a.n_pages, b, ws.movers[(int64_t)b * ws.cap + at], status);
+      if (s == kNone) d = kNone;
     }
     const int here = (int)min((int64_t)32, (n - w + (int64_t)warps - 1) / warps - i0);
     for (int r = 0; r < here; r += kRowsAhead) {
-      int64_t to[kRowsAhead], from[kRowsAhead];
+      uint32_t to[kRowsAhead], from[kRowsAhead];
       uint4 v0[kRowsAhead], v1[kRowsAhead];
       uint32_t v2[kRowsAhead];
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) {
         to[k] = __shfl_sync(0xffffffffu, d, r + k);
         from[k] = __shfl_sync(0xffffffffu, s, r + k);
-        if (r + k >= here) to[k] = -1;
-        if (to[k] < 0) continue;
-        if (f0.base) v0[k] = *reinterpret_cast<const uint4*>(f0.base + from[k] * f0.bytes);
-        if (f1.base) v1[k] = *reinterpret_cast<const uint4*>(f1.base + from[k] * f1.bytes);
-        if (g0.base) v2[k] = *reinterpret_cast<const uint32_t*>(g0.base + from[k] * g0.bytes);
+        if (r + k >= here) to[k] = kNone;
+        if (to[k] == kNone) continue;
+        if (f0.base) v0[k] = *reinterpret_cast<const uint4*>(f0.base + (size_t)from[k] * f0.bytes);
+        if (f1.base) v1[k] = *reinterpret_cast<const uint4*>(f1.base + (size_t)from[k] * f1.bytes);
+        if (g0.base) v2[k] = *reinterpret_cast<const uint32_t*>(g0.base + (size_t)from[k] * g0.bytes);
       }
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) {
-        if (to[k] < 0) continue;
-        if (f0.base) *reinterpret_cast<uint4*>(f0.base + to[k] * f0.bytes) = v0[k];
-        if (f1.base) *reinterpret_cast<uint4*>(f1.base + to[k] * f1.bytes) = v1[k];
-        if (g0.base) *reinterpret_cast<uint32_t*>(g0.base + to[k] * g0.bytes) = v2[k];
+        if (to[k] == kNone) continue;
+        if (f0.base) *reinterpret_cast<uint4*>(f0.base + (size_t)to[k] * f0.bytes) = v0[k];
+        if (f1.base) *reinterpret_cast<uint4*>(f1.base + (size_t)to[k] * f1.bytes) = v1[k];
+        if (g0.base) *reinterpret_cast<uint32_t*>(g0.base + (size_t)to[k] * g0.bytes) = v2[k];
       }
     }
   }
@@ -385,7 +402,7 @@ cudaError_t launch_evict(const EvictArgs& a, void* wsp, cudaStream_t s) {
   e = counted(cudaLaunchKernelEx(&cfg, k_evict_select, a, ws, n_cl, cached, status_word()));
   if (e != cudaSuccess) return e;
   const int64_t most = std::min<int64_t>(a.keep, (int64_t)a.max_entries - a.keep);
-  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((most + 7) / 8, ((int64_t)sms * 8 + a.B - 1) / a.B));
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((most + 7) / 8, ((int64_t)sms * kMoveBlocks + a.B - 1) / a.B));
   return launch_step(k_evict_move, dim3((unsigned)blocks, (unsigned)a.B), dim3(256), 0, s, a, ws, status_word());
 }
 
