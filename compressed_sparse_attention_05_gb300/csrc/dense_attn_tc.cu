@@ -92,6 +92,7 @@ struct Segment {            // what the roles need to know of the current tile
   int w_lo, w_hi;           // window rows any row sees (raw positions, inclusive)
   int all_lo, all_hi;       // entries every row sees
   int one_t, t;             // all rows belong to the token at raw position t
+  int next_t;               // first row of the tile's second token
   int pos0;
 };
 template <bool kWeights>
@@ -396,9 +397,10 @@ __device__ __forceinline__ KeyRef window_ref(const Ctx<kWeights>& cx, int k, int
   const int64_t p = (int64_t)sg.w_lo + (int64_t)k * kChunk + key;
   if (p > sg.w_hi) return r;
   bool seen = sg.one_t != 0;      // one token: the tile's rows all see its whole window
-  if (!seen)
+  if (!seen)                      // else: the first row of each token, and the tile's first
 #pragma unroll 1
-    for (int i = 0; i < kRows; ++i) seen |= (uint32_t)(cx.sm.t[i] - (int)p) < (uint32_t)cx.a.W && p >= cx.sm.doc[i];
+    for (int i = 0; i < kRows; i = i ? i + cx.a.Hq : sg.next_t)
+      seen |= (uint32_t)(cx.sm.t[i] - (int)p) < (uint32_t)cx.a.W && p >= cx.sm.doc[i];
   if (!seen) return r;
   const int64_t w = (int64_t)sg.b * cx.a.swa_cap + (p - sg.pos0);
   const float s = __ldg(cx.a.swa_scales + w);
@@ -415,15 +417,13 @@ __device__ __forceinline__ int page_of(const Ctx<kWeights>& cx, int j, bool exis
   return __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j >> 6));
 }
 
-// Channels 16 p .. +15 of a window row.
-__device__ __forceinline__ void window_piece(const KeyRef& w, int p, uint32_t (&o)[8]) {
-  uint4 c = make_uint4(0, 0, 0, 0);
-  if (w.codes) c = __ldg(reinterpret_cast<const uint4*>(w.codes) + p);
+// 16 channels of a window row.
+__device__ __forceinline__ void window_piece(const uint4& c, float wsc, uint32_t (&o)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t x = word_of(c, j);
-    o[2 * j] = win2_f16x2(x & 0xFFFFu, w.wsc);
-    o[2 * j + 1] = win2_f16x2(x >> 16, w.wsc);
+    o[2 * j] = win2_f16x2(x & 0xFFFFu, wsc);
+    o[2 * j + 1] = win2_f16x2(x >> 16, wsc);
   }
 }
 
@@ -534,17 +534,21 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   const int i0 = min(max(sm.seg.nw - k0, 0), n_chunks);   // first entry chunk of the span
   uint32_t ring = (4 * chunks + first) % kRing;   // slot of the step's quarter
   if (!kWeights) {
+    KeyRef w{nullptr, 0.f};
 #pragma unroll 1
     for (int n = 0; n < 4 * i0; ++n) {
       const int q = n & 3;
+      if (q == 0) w = window_ref<kWeights>(cx, k0 + (n >> 2), key);
+      uint4 c[4];                         // in flight over the wait
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        c[p] = w.codes ? __ldg(reinterpret_cast<const uint4*>(w.codes) + 8 * q + 4 * half + p) : make_uint4(0, 0, 0, 0);
       if (!warp_wait(ring_bar(q), ring_parity(chunks, q), abort)) return;
       if (!kV) tc::tc_fence_after();
-      const KeyRef w = window_ref<kWeights>(cx, k0 + (n >> 2), key);
-#pragma unroll 1
+#pragma unroll
       for (int p = 0; p < 4; ++p) {
         uint32_t o[8];
-        window_piece(w, 8 * q + 4 * half + p, o);
-        __syncwarp();
+        window_piece(c[p], w.wsc, o);
         put(dst0 + ring * kSlot, p, o);
       }
       ring_full(q);
@@ -897,6 +901,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       sm.seg.pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
       sm.seg.e_lo = INT_MAX; sm.seg.e_hi = 0; sm.seg.w_lo = INT_MAX; sm.seg.w_hi = INT_MIN;
       sm.seg.all_lo = 0; sm.seg.all_hi = INT_MAX;
+      sm.seg.next_t = a.Hq - r0 % a.Hq;
       sm.seg.one_t = r0 / a.Hq == (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
       if (tile % cx.pl.tiles == 0 && tstart == u && dense_count_bad(a, b)) raise_status(cx.status, CSA2_STATUS_BAD_COUNT);
     }
