@@ -28,7 +28,7 @@
 //
 // Work is split over the SMs by chunks, not by tiles: every CTA computes the chunk
 // count of all tiles (lengths live on the device), takes an equal contiguous share,
-// and walks the tiles in it.  A tile that falls to several CTAs leaves partial
+// and walks the tiles in it.  A tile counts kTileUnits chunks more than it has.  A tile that falls to several CTAs leaves partial
 // (m, l, O) in the workspace and k_dense_merge joins them in order.
 //
 // Roles (896 threads): warps 0-7 dequantise V into shared memory (a warp: 32 keys x 256
@@ -87,7 +87,7 @@ template <> struct Stages<true> { static constexpr int K = 8, V = 1; };
 // the 8 lanes of a phase (lane = key) read all banks.
 struct Segment {            // what the roles need to know of the current tile
   int b, nw, c_hi;          // window chunks; entry chunks end at c_hi
-  int n_chunks;             // (a tile without chunks still counts as one unit of work)
+  int n_chunks;
   int e_lo, e_hi;           // entries any row of the tile sees
   int w_lo, w_hi;           // window rows any row sees (raw positions, inclusive)
   int all_lo, all_hi;       // entries every row sees
@@ -113,7 +113,7 @@ struct Smem {
     int qexp[4][kRows];             // [1]: largest exponent field of each row of Q, before the products
     struct {                        // before the first tile
       int scan[kThreads / 32];
-      int found_start, found_tile;
+      int found_start, found_tile, found_end;
     };
   };
   uint64_t kst_full[Stages<kWeights>::K], kst_free[Stages<kWeights>::K];   // staging slots
@@ -306,13 +306,17 @@ __device__ __forceinline__ int range_chunks(const Range& r, bool weights) {
   const int nw = !weights && r.w_hi >= r.w_lo ? (int)(((int64_t)r.w_hi - r.w_lo) / kChunk) + 1 : 0;
   return ne + nw;
 }
-// Chunks of a tile (tile = index among this launch's tiles), at least 1.
+// Units of work of a tile (tile = index among this launch's tiles): its chunks, and what beginning and
+// ending a tile takes (15 us, a chunk 4 us; without it an SM with 50 tiles of two chunks was still at work
+// when the SMs with tiles of 17 chunks had long finished).  A share never begins or ends in the first
+// kTileUnits units: such a bound moves to the tile's start.
+constexpr int kTileUnits = 4;
 template <bool kWeights>
 __device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {
   const int b = tile / pl.tiles;
   const int r0 = (pl.tile0 + tile % pl.tiles) * kRows;
   const int64_t rows = (int64_t)a.Tq * a.Hq;
-  if (r0 >= rows) return 1;
+  if (r0 >= rows) return kTileUnits;
   const int n_ent = dense_entries(a, b);
   Range g{INT_MAX, 0, INT_MAX, INT_MIN};
   if (kWeights && !pl.sums) {
@@ -336,7 +340,7 @@ __device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {
       }
     }
   }
-  return max(1, range_chunks(g, kWeights));
+  return kTileUnits + range_chunks(g, kWeights);
 }
 
 // Inclusive block-wide prefix sum (all threads), and the total.
@@ -436,10 +440,10 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Segment& sg, int u, int u1, int tstart) {
   Span s;
-  const int units = max(1, sg.n_chunks);
+  const int units = sg.n_chunks + kTileUnits;
   const int end = min(u1, tstart + units);
-  s.k0 = u - tstart;
-  s.n = min(end - u, max(0, sg.n_chunks - s.k0));
+  s.k0 = max(0, u - tstart - kTileUnits);
+  s.n = end - tstart - kTileUnits - s.k0;
   s.first = u == tstart;
   s.last = end == tstart + units;
   return s;
@@ -718,7 +722,7 @@ __device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
     block_sync();                       // Q, row constants and the tile's chunks are there, O of the last tile is not
     tc::tc_fence_after();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
+    const int units = sm.seg.n_chunks + kTileUnits, more = entry_chunks(sm.seg, sp);
     if (kWeights || !values)
       fill_tile<kWeights, false>(cx, sp.k0, sp.n, chunks, entries, values, warp, lane);
     else
@@ -749,7 +753,7 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
   while (u < cx.u1) {
     seg_sync();                         // the tile's chunks are known (the copies need no more than that)
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = max(1, sm.seg.n_chunks), more = entry_chunks(sm.seg, sp);
+    const int units = sm.seg.n_chunks + kTileUnits, more = entry_chunks(sm.seg, sp);
     const int nw = sm.seg.nw, i0 = sp.n - more, steps = kV && kWeights ? 0 : 4 * more;
     // lane l: page l % 2 of chunk i + l / 2, for 16 chunks; the next 16 are on their way
     auto pages_at = [&](int i) -> int {
@@ -1151,7 +1155,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         }
       }
     }
-    const int units = max(1, sm.seg.n_chunks);
+    const int units = sm.seg.n_chunks + kTileUnits;
     block_sync();
     if (*abort) break;
     c.add(sp.n);
@@ -1180,7 +1184,7 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
     block_sync();
     tc::tc_fence_after();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = max(1, sm.seg.n_chunks);
+    const int units = sm.seg.n_chunks + kTileUnits;
     // Round i does S(i + 1), then PV(i), in steps
     //   0 S buffer free   1-4 a quarter of K there: its products   5 P there   6-9 a quarter of V there: its products
     // Lane n looks at the barrier of step n, so that one look (a trip through the busy shared
@@ -1252,7 +1256,7 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx) {
   while (u < cx.u1) {
     seg_sync();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
-    const int units = max(1, sm.seg.n_chunks);
+    const int units = sm.seg.n_chunks + kTileUnits;
     {
       // the next tile's Q rows (contiguous)
       const int64_t rows = (int64_t)a.Tq * a.Hq;
@@ -1342,8 +1346,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   for (int t = tid; t < tiles; t += kThreads) mine += tile_units<kWeights>(a, pl, t);
   int inc = block_scan(mine, sm.scan, &total);
   const int ctas = min((int)gridDim.x, total), g = blockIdx.x;
-  const int u0 = g < ctas ? (int)((int64_t)total * g / ctas) : 0;
-  const int u1 = g < ctas ? (int)((int64_t)total * (g + 1) / ctas) : 0;
+  int u0 = g < ctas ? (int)((int64_t)total * g / ctas) : 0;
+  int u1 = g < ctas ? (int)((int64_t)total * (g + 1) / ctas) : 0;
+  if (tid == 0) sm.found_end = u1;
+  __syncthreads();
   if (u1 > u0) {
     int base = 0, v = mine, all = total;
 #pragma unroll 1
@@ -1357,14 +1363,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
         sm.found_tile = t0 + tid;
         sm.found_start = start;
       }
+      if (t0 + tid < tiles && u1 >= start && u1 < start + v && u1 - start <= kTileUnits) sm.found_end = start;
       base += all;
-      if (u0 < base) break;            // uniform
+      if (u1 < base) break;            // uniform
     }
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tm = sm.tmem;
+  if (u1 > u0) {
+    if (u0 - sm.found_start <= kTileUnits) u0 = sm.found_start;
+    u1 = sm.found_end;
+  }
   Ctx<kWeights> cx{a, pl, sm, tm, u0, u1, sm.found_tile, sm.found_start, status, &map};
   if (u1 <= u0) cx.tile = 0;
   if (!kWeights && tid == 0) pl.cont[g] = (u1 > u0 && cx.tstart < u0) ? cx.tile : -1;
@@ -1528,9 +1539,9 @@ __global__ void __launch_bounds__(128) k_weights_ranges(DenseArgs a, Plan pl) {
 
 int tiles_of(const csa2_dims* dm) { return (int)(((int64_t)dm->Tq * dm->Hq + kRows - 1) / kRows); }
 
-// Chunks that a sequence's tile can have.
+// Units that a sequence's tile can have.
 int64_t max_chunks(int max_entries, int W, int64_t tq) {
-  return ((int64_t)max_entries + kChunk - 1) / kChunk + ((int64_t)W + tq + kChunk - 1) / kChunk + 2;
+  return ((int64_t)max_entries + kChunk - 1) / kChunk + ((int64_t)W + tq + kChunk - 1) / kChunk + 2 + kTileUnits;
 }
 
 cudaError_t device_sms(int* sms) {
