@@ -19,6 +19,8 @@ namespace {
 
 constexpr int kTile = 32;
 constexpr int kWarps = 8;
+constexpr int D = 64, kLd = D + 1;   // tile row, padded
+constexpr size_t kSmem = ((size_t)kTile * kLd + (size_t)kWarps * D) * sizeof(float);
 
 __device__ __forceinline__ float e2m1_to_f32(uint32_t c) { return bf16_bits_to_f32(e2m1_to_bf16_bits(c)); }
 
@@ -35,7 +37,7 @@ __device__ __forceinline__ float dense_logit(const DenseArgs& a, float dot, floa
 
 // Dequantises entries e0 .. e0+31 of sequence b into the tile; pos[k] receives the
 // raw position of each entry's last token, or INT64_MIN for none (a bad page too).
-__device__ void load_entries(const DenseArgs& a, int b, int e0, int n_ent, int64_t shift, float* tile, int ld,
+__device__ void load_entries(const DenseArgs& a, int b, int e0, int n_ent, int64_t shift, float* tile,
                              int64_t* pos, int64_t* slots, uint32_t* status) {
   const int tid = threadIdx.x;
   if (tid < kTile) {
@@ -46,26 +48,25 @@ __device__ void load_entries(const DenseArgs& a, int b, int e0, int n_ent, int64
     pos[tid] = slot < 0 ? INT64_MIN : a.entry_pos ? (int64_t)a.entry_pos[slot] : 4 * ((int64_t)j + shift) + 3;
   }
   __syncthreads();
-  const int per = a.d / 2;   // code bytes of an entry
+  constexpr int per = D / 2;   // code bytes of an entry
   for (int u = tid; u < kTile * per; u += blockDim.x) {
     const int k = u / per, c = u % per;
     const int64_t slot = slots[k];
     float x0 = 0.f, x1 = 0.f;
     if (slot >= 0) {
       const uint32_t byte = a.kv_codes[slot * per + c];
-      const float s = e4m3_to_f32(a.kv_scales[slot * (a.d / 16) + c / 8]);
+      const float s = e4m3_to_f32(a.kv_scales[slot * (D / 16) + c / 8]);
       x0 = e2m1_to_f32(byte & 15u) * s;
       x1 = e2m1_to_f32(byte >> 4) * s;
     }
-    tile[k * ld + 2 * c] = x0;
-    tile[k * ld + 2 * c + 1] = x1;
+    tile[k * kLd + 2 * c] = x0;
+    tile[k * kLd + 2 * c + 1] = x1;
   }
   __syncthreads();
 }
 
-template <int D>
 __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, uint32_t* status) {
-  constexpr int kLd = D + 1, kPer = D / 32;
+  constexpr int kPer = D / 32;
   extern __shared__ float smem[];
   float* tile = smem;                       // [32][D + 1]
   float* qs = tile + kTile * kLd;           // [8][D]
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
   }
   for (int e0 = dense_first(a, r.doc, shift) / kTile * kTile; e0 < r.nv; e0 += kTile) {
     __syncthreads();
-    load_entries(a, b, e0, n_ent, shift, tile, kLd, pos, slots, status);
+    load_entries(a, b, e0, n_ent, shift, tile, pos, slots, status);
     const int64_t p = pos[lane];
     attend(e0 + lane < r.nv && p != INT64_MIN && p - 3 >= r.doc, dense_distance(r.t, p));
   }
@@ -140,9 +141,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
 
 // One CTA per 32 entries of a sequence; its warps share out the (token, head) rows
 // and their sums are added in warp order.
-template <int D>
 __global__ void __launch_bounds__(kWarps * 32) k_entry_weights_plain(DenseArgs a, uint32_t* status) {
-  constexpr int kLd = D + 1;
   extern __shared__ float smem[];
   float* tile = smem;
   float* qs = tile + kTile * kLd;
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_entry_weights_plain(DenseArgs a
   const int64_t shift = dense_shift(a, b);
   for (int64_t e0 = (int64_t)blockIdx.x * kTile; e0 < n_ent; e0 += (int64_t)gridDim.x * kTile) {
     __syncthreads();
-    load_entries(a, b, (int)e0, n_ent, shift, tile, kLd, pos, slots, status);
+    load_entries(a, b, (int)e0, n_ent, shift, tile, pos, slots, status);
     const int64_t p = pos[lane];
     float w = 0.f;
     for (int i = 0; i < a.Tq; ++i) {
@@ -185,11 +184,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_entry_weights_plain(DenseArgs a
   }
 }
 
-template <int D>
-size_t plain_smem() {
-  return ((size_t)kTile * (D + 1) + (size_t)kWarps * D) * sizeof(float);
-}
-
 }  // namespace
 
 cudaError_t launch_dense_attn_plain(const DenseArgs& a, cudaStream_t s) {
@@ -197,24 +191,13 @@ cudaError_t launch_dense_attn_plain(const DenseArgs& a, cudaStream_t s) {
   if (rows == 0) return cudaSuccess;
   if (rows >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)rows, (unsigned)((a.Hq + kWarps - 1) / kWarps));
-  if (a.d == 64) return launch_step(k_dense_attn_plain<64>, grid, dim3(kWarps * 32), plain_smem<64>(), s, a, status_word());
-  const size_t smem = plain_smem<512>();
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_dense_attn_plain<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return launch_step(k_dense_attn_plain<512>, grid, dim3(kWarps * 32), smem, s, a, status_word());
+  return launch_step(k_dense_attn_plain, grid, dim3(kWarps * 32), kSmem, s, a, status_word());
 }
 
 cudaError_t launch_entry_weights_plain(const DenseArgs& a, cudaStream_t s) {
   if (a.B == 0 || a.max_entries == 0) return cudaSuccess;
   const dim3 grid((unsigned)((a.max_entries + kTile - 1) / kTile), (unsigned)a.B);
-  if (a.d == 64)
-    return launch_step(k_entry_weights_plain<64>, grid, dim3(kWarps * 32), plain_smem<64>(), s, a, status_word());
-  const size_t smem = plain_smem<512>();
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_entry_weights_plain<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return launch_step(k_entry_weights_plain<512>, grid, dim3(kWarps * 32), smem, s, a, status_word());
+  return launch_step(k_entry_weights_plain, grid, dim3(kWarps * 32), kSmem, s, a, status_word());
 }
 
 }  // namespace csa2

@@ -17,26 +17,35 @@
 //
 // The score product reads K as an A operand in tensor memory, where three 128-channel
 // quarters of the dequantised chunk fit at a time; the value product reads V from shared
-// memory.  (Shared memory holds one dequantised chunk (128 KB) beside Q (64 KB) and P, so
-// with both products reading it the softmax would stand between them.  And at N = 64 an MMA
-// with both operands in shared memory reads 6 KB in 48 cycles, all that the memory gives,
-// while the dequantising warps' stores and every barrier wait: with the scores of every
-// second chunk from shared memory the same batch took 281 us.)  An MMA with A in tensor
-// memory takes 87 cycles, so the tensor pipe's floor is 32 x 87 + 32 x 52 = 4,450 cycles per
-// 128 keys x 64 rows.  S(c+1) is issued before PV(c), so that the softmax of a chunk has a
-// whole chunk's products to hide behind.
+// memory, in three quarters too.  (Shared memory holds one dequantised chunk (128 KB) beside
+// Q (64 KB) and P, so with both products reading it the softmax would stand between them.  And
+// at N = 64 an MMA with both operands in shared memory reads 6 KB in 48 cycles, all that the
+// memory gives, while the dequantising warps' stores and every barrier wait: with the scores
+// of every second chunk from shared memory a batch of 32 x 32,768 entries took 281 us.)  An
+// MMA with A in tensor memory takes 87 cycles, so the tensor pipe's floor is 32 x 87 + 32 x 52
+// = 4,450 cycles per 128 keys x 64 rows.  S(c+1) is issued before PV(c), so that the softmax of
+// a chunk has a whole chunk's products to hide behind.
+//
+// What bounds it: a chunk takes 4.0 us (7,000 cycles), the products 4,100 of them; the rest are
+// waits for the last quarters of K and V.  A fill warp's step (64 channels of 32 keys) takes
+// 1,400 cycles, of which 400 are conversion and stores; the others are trips through a shared
+// memory that the products keep busy (a barrier looked at: 180) and instruction issue (24 busy
+// warps).  A batch of 32 x 32,768 entries takes 221 us (623 TFLOP/s, 1.4 TB/s of packed
+// entries), the weights of the same batch 108 us, of which the products are 82.
 //
 // Work is split over the SMs by chunks, not by tiles: every CTA computes the chunk
 // count of all tiles (lengths live on the device), takes an equal contiguous share,
 // and walks the tiles in it.  A tile counts kTileUnits chunks more than it has.  A tile that falls to several CTAs leaves partial
 // (m, l, O) in the workspace and k_dense_merge joins them in order.
 //
-// Roles (896 threads): warps 0-7 dequantise V into shared memory (a warp: 32 keys x 256
-// channels), warps 8-15 K into tensor memory (the same split), warps 16-23 do the softmax
-// (thread = one key x 32 rows), warp 24 issues the MMAs, warp 25 requests pages into L2
-// ahead.  Operand ranges as in attention_tc.cu (R11's
-// powers of two for Q rows and window rows); P is rounded to fp16, the normaliser
-// sums the unrounded fp32 P, everything else is fp32.
+// Roles (896 threads): warps 0-7 dequantise V into shared memory, warps 8-15 K into tensor
+// memory (with the weights all sixteen do K); before a tile's products the same warps bring in
+// Q, after them they write O.  Warps 16-23 do the softmax (thread = one key x 32 rows), warp 24
+// issues the MMAs, warps 25 and 26 copy the packed codes of K and V into staging slots (tensor
+// map copies: read by the dequantising warps themselves, lane = key, they throttled the L1),
+// warp 27 requests pages into L2 ahead.  Operand ranges as in attention_tc.cu (R11's powers of
+// two for Q rows and window rows); P is rounded to fp16, the normaliser sums the unrounded fp32
+// P, everything else is fp32.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -55,7 +64,7 @@ constexpr int kChunk = 128;               // keys of a chunk
 constexpr int kValWarps = 8, kKeyWarps = 8, kSoftWarps = 8;
 constexpr int kSoftFirst = (kValWarps + kKeyWarps) * 32;   // first softmax thread
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kThreads = 896;             // + MMA warp, L2 warp, two idle warps (whole warpgroups)
+constexpr int kThreads = 896;             // + MMA warp, two staging warps, L2 warp
 constexpr int kMmaWarp = kValWarps + kKeyWarps + kSoftWarps;
 constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
 // registers per thread after the split of the seven warpgroups: 4 x 56 + 2 x 120 + 40 = 7 x 72
@@ -65,8 +74,8 @@ constexpr uint32_t kTmemCols = 512;
 // quarters of K (64 columns each: 128 channels of fp16).  Weights: two S^T, a ring of four.
 constexpr uint32_t kColO = 0;
 template <bool kWeights> struct Cols;
-template <> struct Cols<false> { static constexpr uint32_t S = 256, K = 320; static constexpr int ring = 3, s_bufs = 1; };
-template <> struct Cols<true> { static constexpr uint32_t S = 0, K = 128; static constexpr int ring = 4, s_bufs = 2; };
+template <> struct Cols<false> { static constexpr uint32_t S = 256, K = 320; static constexpr int ring = 3; };
+template <> struct Cols<true> { static constexpr uint32_t S = 0, K = 128; static constexpr int ring = 4; };
 constexpr float kRescaleLog2 = 8.f;       // a reference maximum moves only beyond this growth
 constexpr float kUnset = 3e38f;           // -m_ref of a row without keys: any finite logit outgrows it, -inf stays -inf
 constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, then m and l
@@ -495,7 +504,7 @@ __device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp,
 }
 
 // Dequantises the chunks of a tile, quarter by quarter: eight warps share a quarter, lane = key,
-// half of its channels to four of them (a quarter to four warps took so long, 1,900 cycles, that the
+// half of its channels to four of them (a quarter to four warps took so long, 1,450 cycles, that the
 // tensor pipe stood waiting for the last one of every chunk).  kV: into the shared-memory slots that
 // the value product reads; else K, into the tensor-memory slots that the score product reads.  With
 // the weights, which have no V, sixteen warps do K: quarters 0 and 2 (first = 0), 1 and 3 (first = 1).
