@@ -67,8 +67,10 @@ constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = 896;             // + MMA warp, two staging warps, L2 warp
 constexpr int kMmaWarp = kValWarps + kKeyWarps + kSoftWarps;
 constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
-// registers per thread after the split of the seven warpgroups: 4 x 56 + 2 x 120 + 40 = 7 x 72
-constexpr int kRegsLaunch = 72, kRegsFill = 56, kRegsSoft = 120, kRegsMisc = 40;
+// registers per thread after the split of the seven warpgroups: 4 x 56 + 2 x 120 + 40 = 4 x 64 + 2 x 104 + 40 = 7 x 72
+constexpr int kRegsLaunch = 72, kRegsMisc = 40;
+template <bool kWeights> constexpr int kRegsFill = kWeights ? 64 : 56;
+template <bool kWeights> constexpr int kRegsSoft = kWeights ? 104 : 120;
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory.  Attention: O^T (four M-tiles of 64 columns), S^T, and a ring of three
 // quarters of K (64 columns each: 128 channels of fp16).  Weights: two S^T, a ring of four.
@@ -503,25 +505,29 @@ __device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp,
   tc::tc_fence_before();
 }
 
-// Dequantises the chunks of a tile, quarter by quarter: eight warps share a quarter, lane = key,
-// half of its channels to four of them (a quarter to four warps took so long, 1,450 cycles, that the
-// tensor pipe stood waiting for the last one of every chunk).  kV: into the shared-memory slots that
-// the value product reads; else K, into the tensor-memory slots that the score product reads.  With
-// the weights, which have no V, sixteen warps do K: quarters 0 and 2 (first = 0), 1 and 3 (first = 1).
+// Dequantises the chunks of a tile, quarter by quarter, lane = key.  kV: into the shared-memory
+// slots that the value product reads; else K, into the tensor-memory slots that the score product
+// reads.  Attention: the operand's eight warps share every quarter, half of its channels to four of
+// them (a quarter to four warps took so long, 1,900 cycles, that the tensor pipe stood waiting for
+// the last one of every chunk: 228 us instead of 221 for 32 x 32,768 entries).  Weights: no V, so
+// that sixteen warps do K, four a quarter (a ring of four: 93 us, shared quarters 108).
 // Quarter number n = 4 chunk + q goes where number n - ring was; barriers belong to quarters (and
-// staging slots to the same eight warps), so that a warp waits for consecutive phases.
+// staging slots to the same warps), so that a warp waits for consecutive phases.
+template <bool kWeights> constexpr int kSplit = kWeights ? 1 : 2;   // warps that share a quarter's keys
 template <bool kWeights, bool kV>
-__device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n_chunks, uint32_t chunks, uint32_t entries, int first,
-                                          int warp, int lane) {
+__device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n_chunks, uint32_t chunks, uint32_t entries, int group,
+                                          int lq, int lane) {
   Smem<kWeights>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   constexpr int kRing = kV ? kVSlots : Cols<kWeights>::ring, kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
-  const int lq = warp & 3, half = warp >> 2, key = 32 * lq + lane;
+  constexpr int kStep = kWeights ? 4 : 1;    // quarters from one step to the next
+  constexpr int kPieces = 8 / kSplit<kWeights>;   // of 16 channels, in a step
+  const int key = 32 * lq + lane, first = kWeights ? group : 0, half = kWeights ? 0 : group;
   volatile int* abort = &sm.abort;
   constexpr uint32_t kSlot = kV ? kChunk * kQuarter * 2 : 64;   // a ring slot: bytes, or tensor-memory columns
   const uint32_t dst0 = kV ? tc::smem_addr(sm.v) + (key >> 3) * 2048 + (key & 7) * 16 + half * 1024
                            : cx.tm + Cols<kWeights>::K + 32 * half + ((uint32_t)(32 * lq) << 16);
-  auto put = [&](uint32_t dst, int p, const uint32_t (&o)[8]) {   // channels 16 p .. +15 of the half
+  auto put = [&](uint32_t dst, int p, const uint32_t (&o)[8]) {   // the step's channels 16 p .. +15
     if (kV) {
       sts16(dst + 256 * p, o[0], o[1], o[2], o[3]);
       sts16(dst + 256 * p + 128, o[4], o[5], o[6], o[7]);
@@ -570,7 +576,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
     }
   }
   if (i0 >= n_chunks) return;
-  // A step's four scales are read a step ahead, the key's page a chunk ahead of that.  The offset is
+  // A step's scales are read a step ahead, the key's page a chunk ahead of that.  The offset is
   // the key's place in the pool (32 bits: 2^32 entries would be 1 TB of codes); none if there is no
   // such key, or behind a bad page: then the scales are zero, and whatever the staging slot holds
   // becomes zeros.
@@ -581,31 +587,35 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   auto page_at = [&](int j) { return j >= e_lo && j < e_hi ? __ldg(table + (j >> 6)) : -1; };
   auto place = [&](int j, int page) -> uint32_t {
     if (page >= 0 && page < a.n_pages) return (uint32_t)page * kPage + (j & (kPage - 1));
-    if (!kV && first + half == 0 && j >= e_lo && j < e_hi) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
+    if (!kV && group == 0 && j >= e_lo && j < e_hi) raise_status(cx.status, CSA2_STATUS_BAD_PAGE);
     return kNone;
   };
-  const uint8_t* scales = a.kv_scales + 4 * half + 8 * first;
-  auto scales_of = [&](uint32_t at, int q) -> uint32_t {
-    return at == kNone ? 0 : __ldg(reinterpret_cast<const uint32_t*>(scales + (size_t)at * (kD / 16) + 8 * q));
+  const uint8_t* scales = a.kv_scales + 8 * first + 4 * half;
+  auto scales_of = [&](uint32_t at, int q) -> uint2 {
+    if (at == kNone) return make_uint2(0, 0);
+    const uint8_t* s = scales + (size_t)at * (kD / 16) + 8 * q;
+    return kPieces == 8 ? __ldg(reinterpret_cast<const uint2*>(s)) : make_uint2(__ldg(reinterpret_cast<const uint32_t*>(s)), 0);
   };
   int left = n_chunks - i0;               // chunks from this one on
   uint32_t at = place(j, page_at(j)), at1 = kNone;
-  uint32_t next = scales_of(at, 0);
+  uint2 next = scales_of(at, 0);
   int page1 = left > 1 ? page_at(j - kChunk) : -1;
-  constexpr int kStep = kWeights ? 2 : 1;
   // the staging slot of the step's codes and its phase
   uint32_t slot = (4 * entries + first) % kStage, phase = ((4 * entries + first) / kStage) & 1;
   const uint32_t st_full = tc::smem_addr(kV ? sm.vst_full : sm.kst_full), st_free = tc::smem_addr(kV ? sm.vst_free : sm.kst_free);
   const uint32_t codes = tc::smem_addr(kV ? sm.vst[0] : sm.kst[0]) + 64 * key + 16 * ((2 * half) ^ ((key >> 1) & 3));
-  uint4 t[2];
+  uint4 t[kPieces / 2];
   auto load_staged = [&] {
-    t[0] = lds16(codes + slot * kStageBytes);
-    t[1] = lds16((codes + slot * kStageBytes) ^ 16);
+#pragma unroll
+    for (int p = 0; p < kPieces / 2; ++p) t[p] = lds16((codes + slot * kStageBytes) ^ (16 * p));
   };
   // The slot may be written again once the loads have arrived, not when they are issued: the vote reads
   // a word of each (lane 0 always votes yes).
   auto free_staged = [&] {
-    if (__ballot_sync(0xffffffffu, lane == 0 || (t[0].x ^ t[1].x) == 0x5A5A5A5Au) & (lane == 0)) arrive_at(st_free + 8 * slot);
+    uint32_t any = 0;
+#pragma unroll
+    for (int p = 0; p < kPieces / 2; ++p) any ^= t[p].x;
+    if (__ballot_sync(0xffffffffu, lane == 0 || any == 0x5A5A5A5Au) & (lane == 0)) arrive_at(st_free + 8 * slot);
   };
   if (!warp_wait(st_full + 8 * slot, phase, abort)) return;
   load_staged();
@@ -617,7 +627,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
       at1 = left > 1 ? place(j - kChunk, page1) : kNone;
       page1 = left > 2 ? page_at(j - 2 * kChunk) : -1;
     }
-    const uint32_t s = next;
+    const uint2 s = next;
     next = q2 + kStep < 4 ? scales_of(at, q2 + kStep) : scales_of(at1, 0);
     const bool more = left > 1 || q2 + kStep < 4;
     slot += kStep;                        // the next step's
@@ -635,9 +645,9 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
     if (!kV) tc::tc_fence_after();
     const uint32_t dst = dst0 + ring * kSlot;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < kPieces; ++p) {
       uint32_t o[8];
-      dequant16(t[p >> 1], s >> (16 * (p >> 1)), p & 1, o);
+      dequant16(t[p >> 1], (p & 4 ? s.y : s.x) >> (16 * ((p >> 1) & 1)), p & 1, o);
       put(dst, p, o);
     }
     if (more) {
@@ -733,9 +743,9 @@ __device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = sm.seg.n_chunks + kTileUnits, more = entry_chunks(sm.seg, sp);
     if (kWeights || !values)
-      fill_tile<kWeights, false>(cx, sp.k0, sp.n, chunks, entries, values, warp, lane);
+      fill_tile<kWeights, false>(cx, sp.k0, sp.n, chunks, entries, (warp >> 2) + (kWeights && values ? 2 : 0), warp & 3, lane);
     else
-      fill_tile<kWeights, true>(cx, sp.k0, sp.n, chunks, entries, 0, warp, lane);
+      fill_tile<kWeights, true>(cx, sp.k0, sp.n, chunks, entries, warp >> 2, warp & 3, lane);
     block_sync();                       // the tile's products are complete, l is known
     tc::tc_fence_after();
     if (*abort) break;
@@ -1322,18 +1332,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      tc::mbar_init(&sm.kq_full[i], 8);
+      tc::mbar_init(&sm.kq_full[i], 4 * kSplit<kWeights>);
       tc::mbar_init(&sm.kq_free[i], 1);
-      tc::mbar_init(&sm.v_full[i], 8);
+      tc::mbar_init(&sm.v_full[i], 4 * kSplit<kWeights>);
       tc::mbar_init(&sm.v_free[i], 1);
     }
     for (int i = 0; i < Stages<kWeights>::K; ++i) {
       tc::mbar_init(&sm.kst_full[i], 1);
-      tc::mbar_init(&sm.kst_free[i], 8);
+      tc::mbar_init(&sm.kst_free[i], 4 * kSplit<kWeights>);
     }
     for (int i = 0; i < Stages<kWeights>::V; ++i) {
       tc::mbar_init(&sm.vst_full[i], 1);
-      tc::mbar_init(&sm.vst_free[i], 8);
+      tc::mbar_init(&sm.vst_free[i], 4 * kSplit<kWeights>);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
@@ -1391,10 +1401,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
 
   // ---- roles, each with its own walk over the tiles (every walk meets the same barriers)
   if (warp < kValWarps + kKeyWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill<kWeights>));
     role_fill<kWeights>(cx);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft<kWeights>));
     role_softmax<kWeights>(cx);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
@@ -1567,7 +1577,7 @@ cudaError_t prepare_kernel() {
   cudaFuncAttributes at;
   cudaError_t e = cudaFuncGetAttributes(&at, k_dense_tc<kWeights>);
   if (e != cudaSuccess) return e;
-  static_assert(4 * kRegsFill + 2 * kRegsSoft + kRegsMisc <= 7 * kRegsLaunch, "register split");
+  static_assert(4 * kRegsFill<kWeights> + 2 * kRegsSoft<kWeights> + kRegsMisc <= 7 * kRegsLaunch, "register split");
   if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(k_dense_tc<kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)sizeof(Smem<kWeights>));
