@@ -26,12 +26,14 @@
 // = 4,450 cycles per 128 keys x 64 rows.  S(c+1) is issued before PV(c), so that the softmax of
 // a chunk has a whole chunk's products to hide behind.
 //
-// What bounds it: a chunk takes 4.0 us (7,000 cycles), the products 4,100 of them; the rest are
+// What bounds it: a chunk takes 3.6 us (6,400 cycles), the products 4,100 of them; the rest are
 // waits for the last quarters of K and V.  A fill warp's step (64 channels of 32 keys) takes
 // 1,400 cycles, of which 400 are conversion and stores; the others are trips through a shared
-// memory that the products keep busy (a barrier looked at: 180) and instruction issue (24 busy
-// warps).  A batch of 32 x 32,768 entries takes 221 us (623 TFLOP/s, 1.4 TB/s of packed
-// entries), the weights of the same batch 108 us, of which the products are 82.
+// memory that the products keep busy (a barrier looked at: 180) and instruction issue (half of
+// all slots are taken, by 24 warps; no pipe is over 40%).  The products of a chunk interleaved with
+// the next scores, so that the last quarters have more time, changed nothing.  A batch of
+// 32 x 32,768 entries takes 217 us (635 TFLOP/s, 1.4 TB/s of packed entries), the weights of
+// the same batch 93 us, of which the products are 82.
 //
 // Work is split over the SMs by chunks, not by tiles: every CTA computes the chunk
 // count of all tiles (lengths live on the device), takes an equal contiguous share,
@@ -576,7 +578,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
     }
   }
   if (i0 >= n_chunks) return;
-  // A step's scales are read a step ahead, the key's page a chunk ahead of that.  The offset is
+  // A step's scales are read two steps ahead, the key's page a chunk ahead of that.  The offset is
   // the key's place in the pool (32 bits: 2^32 entries would be 1 TB of codes); none if there is no
   // such key, or behind a bad page: then the scales are zero, and whatever the staging slot holds
   // becomes zeros.
@@ -596,10 +598,24 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
     const uint8_t* s = scales + (size_t)at * (kD / 16) + 8 * q;
     return kPieces == 8 ? __ldg(reinterpret_cast<const uint2*>(s)) : make_uint2(__ldg(reinterpret_cast<const uint32_t*>(s)), 0);
   };
-  int left = n_chunks - i0;               // chunks from this one on
-  uint32_t at = place(j, page_at(j)), at1 = kNone;
-  uint2 next = scales_of(at, 0);
+  int left = n_chunks - i0;               // chunks of which scales are still to be read
+  uint32_t at = place(j, page_at(j));
   int page1 = left > 1 ? page_at(j - kChunk) : -1;
+  int qs = 0;
+  auto next_scales = [&]() -> uint2 {     // of the steps in order
+    const uint2 v = scales_of(at, qs);
+    qs += kStep;
+    if (qs >= 4) {
+      qs = 0;
+      j -= kChunk;
+      --left;
+      at = left > 0 ? place(j, page1) : kNone;
+      page1 = left > 1 ? page_at(j - kChunk) : -1;
+    }
+    return v;
+  };
+  int steps = (n_chunks - i0) * (4 / kStep);
+  uint2 s = next_scales(), next = next_scales();
   // the staging slot of the step's codes and its phase
   uint32_t slot = (4 * entries + first) % kStage, phase = ((4 * entries + first) / kStage) & 1;
   const uint32_t st_full = tc::smem_addr(kV ? sm.vst_full : sm.kst_full), st_free = tc::smem_addr(kV ? sm.vst_free : sm.kst_free);
@@ -621,15 +637,8 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   load_staged();
   free_staged();
 #pragma unroll 1
-  for (int q2 = 0;;) {                    // q2: this quarter less `first`
-    const int q = q2 + first;
-    if (q2 == 0) {
-      at1 = left > 1 ? place(j - kChunk, page1) : kNone;
-      page1 = left > 2 ? page_at(j - 2 * kChunk) : -1;
-    }
-    const uint2 s = next;
-    next = q2 + kStep < 4 ? scales_of(at, q2 + kStep) : scales_of(at1, 0);
-    const bool more = left > 1 || q2 + kStep < 4;
+  for (int q = first;;) {
+    const bool more = --steps > 0;
     slot += kStep;                        // the next step's
     if (slot >= kStage) {
       slot -= kStage;
@@ -654,16 +663,16 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
       if (!(look & 2) && !warp_wait(st_full + 8 * slot, phase, abort)) return;
       load_staged();
     }
+    s = next;
+    next = next_scales();
     ring_full(q);
     if (more) free_staged();
     ring += kStep;
     if (ring >= kRing) ring -= kRing;
-    q2 += kStep;
-    if (q2 >= 4) {
-      if (--left == 0) break;
-      q2 = 0;
-      j -= kChunk;
-      at = at1;
+    if (!more) break;
+    q += kStep;
+    if (q >= 4) {
+      q -= 4;
       ++chunks;
     }
   }
