@@ -940,7 +940,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
     soft_sync();
     if (st < kRows) {
       const bool live = r0 + st < rows;
-      DenseRow r{INT_MIN, 0, 0, 0, 0};
+      DenseRow r{INT_MIN, 0, INT_MAX, 0, 0};   // no row: it sees nothing, wherever t - p wraps to
       float slope = 0.f, nref = kUnset;
       if (live) {
         const int i = (r0 + st) / a.Hq, h = (r0 + st) % a.Hq;

@@ -448,7 +448,8 @@ int csa2_entry_weights(const csa2_dims* dims, const csa2_cache* cache, const csa
  * there are free for reuse once the call is done.  keep >= 1, n_sink + n_recent <= keep.  A
  * sequence whose n_entries is negative, above max_entries or past its page
  * table, or whose shift is negative, stays as it is and raises
- * CSA2_STATUS_BAD_COUNT.  Sequences must not share pages.  NaN weights are not
+ * CSA2_STATUS_BAD_COUNT (with max_entries <= keep the call returns at once and
+ * looks at no count).  Sequences must not share pages.  NaN weights are not
  * supported.  dims: B, d, Di, idx_dtype, max_pages, kv_format are used.
  *
  * After an eviction csa2_index_topk, csa2_sparse_attn and the other calls that

@@ -123,3 +123,10 @@ def test_compress_pack_bounded_refusals(lib):
     assert call(BOUNDED, H=100) == 1 and "multiple of 64" in err()
     assert call(BOUNDED, T=3) == 0                                      # no whole group: nothing to do
     assert call(BOUNDED, nbytes=abi.csa2_compress_workspace_size(2, 64, 128, 512, 128) - 1) == 4
+
+
+def test_pools_past_32_bit_entry_numbers_are_refused(lib):
+    big = cache(n_pages=(1 << 31) // 64)
+    for rc in (attn(lib, c=big), weights(lib, c=big), evict(lib, c=big)):
+        assert rc == 1 and "n_pages" in err()
+    assert evict(lib, c=cache(n_pages=(1 << 31) // 64 - 1), keep=100) == 0

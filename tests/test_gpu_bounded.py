@@ -181,3 +181,17 @@ def test_runs_give_the_same_bits(kw):
         assert torch.equal(c.O.view(torch.int16), O.view(torch.int16)) and torch.equal(c.lse, lse)
         assert torch.equal(w, first)
     assert status() == 0
+
+
+@pytest.mark.parametrize("entries", [0, 70])
+def test_rows_that_no_token_sees_near_the_largest_position(entries):
+    """A tile with fewer rows than it has room for, positions up to 2^31 - 2: window rows between the tokens'
+    windows hold NaN and must not be taken for visible ones."""
+    top = 2 ** 31 - 2
+    c = Case(seed=8, Tq=2, Hq=8, lens=(entries,), W=8, q_pos=[[top - 18, top]], docs=[[0, top]])
+    hidden = [int(p - c.pos0[0]) for p in range(top - 17, top)]
+    c.t["wscales"][0, hidden] = float("nan")
+    c.t["wcodes"][0, hidden] = 0x7F
+    c.attend()
+    assert status() == 0
+    c.check_attention()
