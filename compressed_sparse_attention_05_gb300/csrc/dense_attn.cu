@@ -13,6 +13,7 @@
 // one head; lane k computes the dot product of key k, and the 32 weights are then
 // broadcast one by one while every lane adds its d/32 channels.
 #include "dense.cuh"
+#include "operands.cuh"
 
 namespace csa2 {
 namespace {
@@ -22,6 +23,8 @@ constexpr int kWarps = 8;
 constexpr int D = 64, kLd = D + 1;   // tile row, padded
 constexpr size_t kSmem = ((size_t)kTile * kLd + (size_t)kWarps * D) * sizeof(float);
 
+// An E4M3 code, its NaN included.
+__device__ __forceinline__ float fp8_to_f32(uint8_t c) { return (c & 0x7F) == 0x7F ? NAN : e4m3_to_f32(c); }
 __device__ __forceinline__ float e2m1_to_f32(uint32_t c) { return bf16_bits_to_f32(e2m1_to_bf16_bits(c)); }
 
 // |t - p| in fp32 (exact below 2^24)
@@ -55,7 +58,7 @@ __device__ void load_entries(const DenseArgs& a, int b, int e0, int n_ent, int64
     float x0 = 0.f, x1 = 0.f;
     if (slot >= 0) {
       const uint32_t byte = a.kv_codes[slot * per + c];
-      const float s = e4m3_to_f32(a.kv_scales[slot * (D / 16) + c / 8]);
+      const float s = fp8_to_f32(a.kv_scales[slot * (D / 16) + c / 8]);
       x0 = e2m1_to_f32(byte & 15u) * s;
       x1 = e2m1_to_f32(byte >> 4) * s;
     }
@@ -107,6 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
     for (int c = 0; c < kPer; ++c) o[c] *= al;
     for (int k = 0; k < kTile; ++k) {
       const float pk = __shfl_sync(0xffffffffu, p, k);
+      if (pk == 0.f) continue;   // uniform; a hidden key may hold NaN
 #pragma unroll
       for (int c = 0; c < kPer; ++c) o[c] += pk * tile[k * kLd + 32 * c + lane];
     }
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
       float x = 0.f;
       if (w0 + k < r.w_n) {
         const int64_t wr = (int64_t)b * a.swa_cap + ((int64_t)r.w_lo + w0 + k - pos0);
-        x = bf16_bits_to_f32(f32_to_bf16_bits(e4m3_to_f32(a.swa_codes[wr * D + c]) * a.swa_scales[wr]));
+        x = bf16_bits_to_f32(f32_to_bf16_bits(fp8_to_f32(a.swa_codes[wr * D + c]) * a.swa_scales[wr]));
       }
       tile[k * kLd + c] = x;
     }
@@ -132,11 +136,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
     attend(e0 + lane < r.nv && p != INT64_MIN && p - 3 >= r.doc, dense_distance(r.t, p));
   }
   if (!live) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int c = 0; c < kPer; ++c)
-    a.O[(row * a.Hq + h) * D + 32 * c + lane] = (uint16_t)f32_to_bf16_bits(o[c] * inv);
-  if (a.lse && lane == 0) a.lse[row * a.Hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    a.O[(row * a.Hq + h) * D + 32 * c + lane] = (uint16_t)(f32x2_bf16x2(o[c] * inv, 0.f) & 0xFFFFu);
+  if (a.lse && lane == 0) a.lse[row * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 // One CTA per 32 entries of a sequence; its warps share out the (token, head) rows

@@ -378,9 +378,18 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
 }
 
 // ---- dequantisation --------------------------------------------------------------------
-// Half h (16 channels) of a piece with its two E4M3 scales: 8 fp16 pairs.
+// min(a, b); the other one where one is NaN.  V takes a NaN as some finite value: a row that sees its key
+// gets the NaN through K and the weight, and a row that does not must not get 0 x NaN.
+__device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Half h (16 channels) of a piece with its two E4M3 scales (at most 448): 8 fp16 pairs.
+template <bool kV>
 __device__ __forceinline__ void dequant16(const uint4& c, uint32_t scales, int h, uint32_t (&o)[8]) {
-  const uint32_t s = e4m3x2_f16x2(scales & 0xFFFFu);
+  uint32_t s = e4m3x2_f16x2(scales & 0xFFFFu);
+  if (kV) s = min_f16x2(s, 0x5F005F00u);
   const uint32_t g = prmt(s, s, h ? 0x3232u : 0x1010u);
   e2m1x8_f16x8(h ? c.z : c.x, o[0], o[1], o[2], o[3]);
   e2m1x8_f16x8(h ? c.w : c.y, o[4], o[5], o[6], o[7]);
@@ -435,12 +444,18 @@ __device__ __forceinline__ int page_of(const Ctx<kWeights>& cx, int j, bool exis
 }
 
 // 16 channels of a window row.
+template <bool kV>
 __device__ __forceinline__ void window_piece(const uint4& c, float wsc, uint32_t (&o)[8]) {
+  if (kV && !isfinite(wsc)) wsc = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t x = word_of(c, j);
     o[2 * j] = win2_f16x2(x & 0xFFFFu, wsc);
     o[2 * j + 1] = win2_f16x2(x >> 16, wsc);
+    if (kV) {
+      o[2 * j] = min_f16x2(o[2 * j], 0x7BFF7BFFu);
+      o[2 * j + 1] = min_f16x2(o[2 * j + 1], 0x7BFF7BFFu);
+    }
   }
 }
 
@@ -569,7 +584,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         uint32_t o[8];
-        window_piece(c[p], w.wsc, o);
+        window_piece<kV>(c[p], w.wsc, o);
         put(dst0 + ring * kSlot, p, o);
       }
       ring_full(q);
@@ -656,7 +671,7 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
       uint32_t o[8];
-      dequant16(t[p >> 1], (p & 4 ? s.y : s.x) >> (16 * ((p >> 1) & 1)), p & 1, o);
+      dequant16<kV>(t[p >> 1], (p & 4 ? s.y : s.x) >> (16 * ((p >> 1) & 1)), p & 1, o);
       put(dst, p, o);
     }
     if (more) {
@@ -1172,10 +1187,10 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       if (st < kRows) {
         const float l = (sm.red[0][st] + sm.red[1][st]) + (sm.red[2][st] + sm.red[3][st]);
         const float m = sm.nref[st] == kUnset ? -INFINITY : -sm.nref[st];
-        sm.red[0][st] = l > 0.f ? 1.f / l : 0.f;   // the factor of O
+        sm.red[0][st] = l == 0.f ? 0.f : 1.f / l;   // the factor of O
         if (sp.first && sp.last) {
           if (a.lse && r0 + st < rows)
-            a.lse[(int64_t)b * rows + r0 + st] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            a.lse[(int64_t)b * rows + r0 + st] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         } else {
           float* ml = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats + kRows * kD;
           ml[st] = m;
@@ -1493,9 +1508,9 @@ __global__ void __launch_bounds__(128 * kMergeGroups) k_dense_merge(DenseArgs a,
       L += f * ml[kRows + r];
     }
     L = warp_sum(L);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     for (int q = tid; q <= count; q += 32) s_fac[q] *= inv;
-    if (a.lse && tid == 0) a.lse[(int64_t)b * rows + row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    if (a.lse && tid == 0) a.lse[(int64_t)b * rows + row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
   __syncthreads();
   const int n = s_count, grp = tid >> 7, c4 = tid & 127;

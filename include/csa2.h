@@ -111,7 +111,8 @@
  *          (the window stays causal in the prefix too);
  *        - and, with a document mask, all of its tokens lie at or after
  *          doc_start.
- *      A token that sees nothing gets O = 0 and lse = -inf.  Products run on
+ *      A token that sees nothing gets O = 0 and lse = -inf; a NaN in a key
+ *      reaches the tokens that see the key, and no other.  Products run on
  *      fp16 tensor-core operands with R11's powers of two, P rounded to fp16,
  *      everything else in fp32; O is rounded once.
  *   R15 accumulated weight: weight_out[j] = decay * weight_in[j] + the sum over

@@ -195,3 +195,30 @@ def test_rows_that_no_token_sees_near_the_largest_position(entries):
     c.attend()
     assert status() == 0
     c.check_attention()
+
+
+@pytest.mark.parametrize("d", [512, 64])
+@pytest.mark.parametrize("bad", ["entry", "window_scale", "window_code"])
+def test_nan_keys_reach_only_the_tokens_that_see_them(d, bad):
+    """Two tokens of one tile: a key with a NaN that the first sees and the second does not."""
+    if d == 64 and bad != "entry":
+        pytest.skip("the plain kernel reads only the window rows that its token sees")
+    c = Case(seed=9, Tq=2, Hq=8, d=d, lens=(300,), W=16, q_pos=[[1170, 1199]], docs=[[0, 1180]])
+    if bad == "entry":
+        c.t["scales"][int(c.slots[0][200]), 1] = 0x7F
+        c.t["scales"][int(c.slots[0][201]), 2] = 0xFF
+    elif bad == "window_scale":
+        c.t["wscales"][0, 1165 - int(c.pos0[0])] = float("nan")
+        c.t["wscales"][0, 1166 - int(c.pos0[0])] = float("inf")
+    else:
+        c.t["wcodes"][0, 1165 - int(c.pos0[0]), 5] = 0x7F
+        c.t["wcodes"][0, 1165 - int(c.pos0[0]), 400] = 0xFF
+    c.attend()
+    assert status() == 0
+    assert c.lse[0, 0].isnan().all() and c.O[0, 0].isnan().any()   # the first token's result says so
+    c.check_attention([(0, 1)])
+    out = torch.zeros(c.n_pages * 64, device="cuda")
+    c.weigh(torch.where(c.lse.isfinite(), c.lse, float("inf")), None, out)
+    assert status() == 0
+    visible = torch.from_numpy(c.slots[0][295:]).cuda()   # of the second token's document: finite
+    assert out[visible].isfinite().all() and (out[visible] > 0).all()
