@@ -61,7 +61,13 @@ namespace csa2 {
 namespace {
 
 constexpr int kD = 512;
-constexpr int kRows = 64;                 // rows of a tile (N of both products)
+// What a kernel does: 0 attention; else the weights, with tiles of that many rows (64 or 128).  Attention's
+// O^T takes tensor memory for 64 rows only.  An MMA with A in tensor memory takes 87 cycles for 64 rows as
+// for 128, so the weights take 128 where a sequence has more than 64: 2 x 257 tokens x 64 heads over 16,384
+// entries in 646 us instead of 861.
+template <int kMode> constexpr bool kWeights = kMode != 0;
+template <int kMode> constexpr int kRowsOf = kMode ? kMode : 64;
+constexpr int kRows = 64;                 // rows of an attention tile (N of both products)
 constexpr int kChunk = 128;               // keys of a chunk
 constexpr int kValWarps = 8, kKeyWarps = 8, kSoftWarps = 8;
 constexpr int kSoftFirst = (kValWarps + kKeyWarps) * 32;   // first softmax thread
@@ -71,15 +77,14 @@ constexpr int kMmaWarp = kValWarps + kKeyWarps + kSoftWarps;
 constexpr int kMaxCtas = 256;             // bound of the grid (workspace slots)
 // registers per thread after the split of the seven warpgroups: 4 x 56 + 2 x 120 + 40 = 4 x 64 + 2 x 104 + 40 = 7 x 72
 constexpr int kRegsLaunch = 72, kRegsMisc = 40;
-template <bool kWeights> constexpr int kRegsFill = kWeights ? 64 : 56;
-template <bool kWeights> constexpr int kRegsSoft = kWeights ? 104 : 120;
+template <int kMode> constexpr int kRegsFill = kMode ? 64 : 56;
+template <int kMode> constexpr int kRegsSoft = kMode ? 104 : 120;
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory.  Attention: O^T (four M-tiles of 64 columns), S^T, and a ring of three
 // quarters of K (64 columns each: 128 channels of fp16).  Weights: two S^T, a ring of four.
 constexpr uint32_t kColO = 0;
-template <bool kWeights> struct Cols;
-template <> struct Cols<false> { static constexpr uint32_t S = 256, K = 320; static constexpr int ring = 3; };
-template <> struct Cols<true> { static constexpr uint32_t S = 0, K = 128; static constexpr int ring = 4; };
+template <int kMode> struct Cols { static constexpr uint32_t S = 0, K = 2 * kMode; static constexpr int ring = 4; };
+template <> struct Cols<0> { static constexpr uint32_t S = 256, K = 320; static constexpr int ring = 3; };
 constexpr float kRescaleLog2 = 8.f;       // a reference maximum moves only beyond this growth
 constexpr float kUnset = 3e38f;           // -m_ref of a row without keys: any finite logit outgrows it, -inf stays -inf
 constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, then m and l
@@ -87,9 +92,8 @@ constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, then m and l
 constexpr int kQuarter = 128;                         // channels of a quarter
 constexpr int kVSlots = 3;                            // quarters of V in shared memory
 constexpr int kStageBytes = kChunk * kQuarter / 2;    // packed codes of a chunk's quarter
-template <bool kWeights> struct Stages;               // staging slots of the K and V streams
-template <> struct Stages<false> { static constexpr int K = 3, V = 3; };
-template <> struct Stages<true> { static constexpr int K = 8, V = 1; };
+template <int kMode> struct Stages { static constexpr int K = 8, V = 1; };   // staging slots of the K and V streams
+template <> struct Stages<0> { static constexpr int K = 3, V = 3; };
 
 // Operand tiles (no-swizzle canonical layout, core matrices of 8 rows x 16 bytes):
 //   Q [row][dim]:         (r/8)*8192 + (d/8)*128 + (r%8)*16 + (d%8)*2
@@ -104,33 +108,34 @@ struct Segment {            // what the roles need to know of the current tile
   int e_lo, e_hi;           // entries any row of the tile sees
   int w_lo, w_hi;           // window rows any row sees (raw positions, inclusive)
   int all_lo, all_hi;       // entries every row sees
-  int one_t, t;             // all rows belong to the token at raw position t
+  int one_t;                // all rows belong to one token
+  int one_tok;              // bit k: rows 32 k .. +31 do
   int next_t;               // first row of the tile's second token
   int pos0;
 };
-template <bool kWeights>
+template <int kMode>
 struct Smem {
-  unsigned char kst[Stages<kWeights>::K][kStageBytes];   // (1024-aligned)
-  unsigned char vst[kWeights ? 1 : Stages<kWeights>::V][kWeights ? 16 : kStageBytes];
-  uint16_t q[kRows * kD];
-  uint16_t v[kWeights ? 8 : kVSlots * kChunk * kQuarter];
-  uint16_t p[kWeights ? 8 : kChunk * kRows];
-  float mult[kRows];        // logit multiplier: softmax scale * log2(e) * 2^e_r
-  float nref[kRows];        // attention: -m_ref (kUnset before the row's first key); weights: -lse * log2(e)
-  float slope2[kRows];      // slope * log2(e)
+  unsigned char kst[Stages<kMode>::K][kStageBytes];   // (1024-aligned)
+  unsigned char vst[kWeights<kMode> ? 1 : Stages<kMode>::V][kWeights<kMode> ? 16 : kStageBytes];
+  uint16_t q[kRowsOf<kMode> * kD];
+  uint16_t v[kWeights<kMode> ? 8 : kVSlots * kChunk * kQuarter];
+  uint16_t p[kWeights<kMode> ? 8 : kChunk * kRowsOf<kMode>];
+  float mult[kRowsOf<kMode>];        // logit multiplier: softmax scale * log2(e) * 2^e_r
+  float nref[kRowsOf<kMode>];        // attention: -m_ref (kUnset before the row's first key); weights: -lse * log2(e)
+  float slope2[kRowsOf<kMode>];      // slope * log2(e)
   // a row sees entry j if j < nv and its first token is >= doc, and the window row at
   // position p if 0 <= t - p < W and p >= doc
-  int nv[kRows], doc[kRows], t[kRows];
+  int nv[kRowsOf<kMode>], doc[kRowsOf<kMode>], t[kRowsOf<kMode>];
   union {
-    float red[4][kRows];            // per-lane-quarter maxima / sums of a row over the keys; [0] also: see below
-    int qexp[4][kRows];             // [1]: largest exponent field of each row of Q, before the products
+    float red[4][kRowsOf<kMode>];            // per-lane-quarter maxima / sums of a row over the keys; [0] also: see below
+    int qexp[4][kRowsOf<kMode>];             // [1]: largest exponent field of each row of Q, before the products
     struct {                        // before the first tile
       int scan[kThreads / 32];
       int found_start, found_tile, found_end;
     };
   };
-  uint64_t kst_full[Stages<kWeights>::K], kst_free[Stages<kWeights>::K];   // staging slots
-  uint64_t vst_full[Stages<kWeights>::V], vst_free[Stages<kWeights>::V];
+  uint64_t kst_full[Stages<kMode>::K], kst_free[Stages<kMode>::K];   // staging slots
+  uint64_t vst_full[Stages<kMode>::V], vst_free[Stages<kMode>::V];
   uint64_t kq_full[4], kq_free[4];  // quarters of a chunk's K in tensor memory
   uint64_t v_full[4], v_free[4];    // quarters of a chunk's V in shared memory
   uint64_t s_full[2], s_free[2], p_full, p_free;
@@ -141,9 +146,10 @@ struct Smem {
 };
 // red[0][r] holds the factor of a row's rescaling and, at the end of a tile, its sum l:
 // each is computed by the one thread that reads the column, from the column.
-static_assert(sizeof(Smem<false>) <= 232448 && sizeof(Smem<true>) <= 232448, "shared memory");
+static_assert(sizeof(Smem<0>) <= 232448 && sizeof(Smem<64>) <= 232448 && sizeof(Smem<128>) <= 232448, "shared memory");
 
 struct Plan {
+  int rows;                 // rows of a tile
   int tile0, tiles;         // tiles [tile0, tile0 + tiles) of every sequence are this launch's
   int n_ctas;
   float* parts;             // attention: partial results, kPartFloats per slot, two slots per CTA
@@ -324,21 +330,21 @@ __device__ __forceinline__ int range_chunks(const Range& r, bool weights) {
 // when the SMs with tiles of 17 chunks had long finished).  A share never begins or ends in the first
 // kTileUnits units: such a bound moves to the tile's start.
 constexpr int kTileUnits = 4;
-template <bool kWeights>
+template <int kMode>
 __device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {
   const int b = tile / pl.tiles;
-  const int r0 = (pl.tile0 + tile % pl.tiles) * kRows;
+  const int r0 = (pl.tile0 + tile % pl.tiles) * kRowsOf<kMode>;
   const int64_t rows = (int64_t)a.Tq * a.Hq;
   if (r0 >= rows) return kTileUnits;
   const int n_ent = dense_entries(a, b);
   Range g{INT_MAX, 0, INT_MAX, INT_MIN};
-  if (kWeights && !pl.sums) {
+  if (kWeights<kMode> && !pl.sums) {
     g.e_lo = 0;
     g.e_hi = n_ent;
   } else {
     const int64_t shift = dense_shift(a, b);
     const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
-    const int i1 = (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
+    const int i1 = (int)(min((int64_t)r0 + kRowsOf<kMode>, rows) - 1) / a.Hq;
 #pragma unroll 1
     for (int i = r0 / a.Hq; i <= i1; ++i) {
       const DenseRow r = dense_row(a, b, i, n_ent, shift, pos0);
@@ -353,7 +359,7 @@ __device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {
       }
     }
   }
-  return kTileUnits + range_chunks(g, kWeights);
+  return kTileUnits + range_chunks(g, kWeights<kMode>);
 }
 
 // Inclusive block-wide prefix sum (all threads), and the total.
@@ -397,11 +403,11 @@ __device__ __forceinline__ void dequant16(const uint4& c, uint32_t scales, int h
   for (int x = 0; x < 8; ++x) o[x] = hmul2(o[x], g);   // exact: <= 6 significant bits
 }
 
-template <bool kWeights>
+template <int kMode>
 struct Ctx {
   const DenseArgs& a;
   const Plan& pl;
-  Smem<kWeights>& sm;
+  Smem<kMode>& sm;
   uint32_t tm;
   int u0, u1;              // this CTA's units (a launch has fewer than 2^31)
   int tile;                // first tile and its first unit
@@ -416,8 +422,8 @@ struct KeyRef {
   float wsc;               // scale * 2^-f
 };
 
-template <bool kWeights>
-__device__ __forceinline__ KeyRef window_ref(const Ctx<kWeights>& cx, int k, int key) {
+template <int kMode>
+__device__ __forceinline__ KeyRef window_ref(const Ctx<kMode>& cx, int k, int key) {
   const Segment& sg = cx.sm.seg;
   KeyRef r{nullptr, 0.f};
   const int64_t p = (int64_t)sg.w_lo + (int64_t)k * kChunk + key;
@@ -425,7 +431,7 @@ __device__ __forceinline__ KeyRef window_ref(const Ctx<kWeights>& cx, int k, int
   bool seen = sg.one_t != 0;      // one token: the tile's rows all see its whole window
   if (!seen)                      // else: the first row of each token, and the tile's first
 #pragma unroll 1
-    for (int i = 0; i < kRows; i = i ? i + cx.a.Hq : sg.next_t)
+    for (int i = 0; i < kRowsOf<kMode>; i = i ? i + cx.a.Hq : sg.next_t)
       seen |= (uint32_t)(cx.sm.t[i] - (int)p) < (uint32_t)cx.a.W && p >= cx.sm.doc[i];
   if (!seen) return r;
   const int64_t w = (int64_t)sg.b * cx.a.swa_cap + (p - sg.pos0);
@@ -436,8 +442,8 @@ __device__ __forceinline__ KeyRef window_ref(const Ctx<kWeights>& cx, int k, int
 }
 
 // Page-table entry of entry j, or -1 if no row of the tile sees it.
-template <bool kWeights>
-__device__ __forceinline__ int page_of(const Ctx<kWeights>& cx, int j, bool exists) {
+template <int kMode>
+__device__ __forceinline__ int page_of(const Ctx<kMode>& cx, int j, bool exists) {
   const Segment& sg = cx.sm.seg;
   if (!exists || j < sg.e_lo || j >= sg.e_hi) return -1;
   return __ldg(cx.a.page_table + (int64_t)sg.b * cx.a.max_pages + (j >> 6));
@@ -490,17 +496,17 @@ struct Count {
 };
 
 // O^T of the finished tile from tensor memory: M-tile mt, this warp's lanes (dims), all rows.
-template <bool kWeights>
-__device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp, int tile, int mt, int lq, int lane) {
+template <int kMode>
+__device__ __forceinline__ void drain_o(const Ctx<kMode>& cx, const Span& sp, int tile, int mt, int lq, int lane) {
   const DenseArgs& a = cx.a;
   const int b = tile / cx.pl.tiles;
-  const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
+  const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRowsOf<kMode>;
   const int64_t rows = (int64_t)a.Tq * a.Hq;
   const int dim = 128 * mt + 32 * lq + lane;
   const bool whole = sp.first && sp.last;
   float* part = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats;
 #pragma unroll 1
-  for (int c0 = 0; c0 < kRows; c0 += 16) {
+  for (int c0 = 0; c0 < kRowsOf<kMode>; c0 += 16) {
     float o[16];
     tc::tmem_ld16(cx.tm + kColO + 64 * mt + c0 + ((uint32_t)(32 * lq) << 16), o);
     tc::tmem_wait_ld();
@@ -530,20 +536,20 @@ __device__ __forceinline__ void drain_o(const Ctx<kWeights>& cx, const Span& sp,
 // that sixteen warps do K, four a quarter (a ring of four: 93 us, shared quarters 108).
 // Quarter number n = 4 chunk + q goes where number n - ring was; barriers belong to quarters (and
 // staging slots to the same warps), so that a warp waits for consecutive phases.
-template <bool kWeights> constexpr int kSplit = kWeights ? 1 : 2;   // warps that share a quarter's keys
-template <bool kWeights, bool kV>
-__device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n_chunks, uint32_t chunks, uint32_t entries, int group,
+template <int kMode> constexpr int kSplit = kMode ? 1 : 2;   // warps that share a quarter's keys
+template <int kMode, bool kV>
+__device__ __forceinline__ void fill_tile(const Ctx<kMode>& cx, int k0, int n_chunks, uint32_t chunks, uint32_t entries, int group,
                                           int lq, int lane) {
-  Smem<kWeights>& sm = cx.sm;
+  Smem<kMode>& sm = cx.sm;
   const DenseArgs& a = cx.a;
-  constexpr int kRing = kV ? kVSlots : Cols<kWeights>::ring, kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
-  constexpr int kStep = kWeights ? 4 : 1;    // quarters from one step to the next
-  constexpr int kPieces = 8 / kSplit<kWeights>;   // of 16 channels, in a step
-  const int key = 32 * lq + lane, first = kWeights ? group : 0, half = kWeights ? 0 : group;
+  constexpr int kRing = kV ? kVSlots : Cols<kMode>::ring, kStage = kV ? Stages<kMode>::V : Stages<kMode>::K;
+  constexpr int kStep = kWeights<kMode> ? 4 : 1;    // quarters from one step to the next
+  constexpr int kPieces = 8 / kSplit<kMode>;   // of 16 channels, in a step
+  const int key = 32 * lq + lane, first = kWeights<kMode> ? group : 0, half = kWeights<kMode> ? 0 : group;
   volatile int* abort = &sm.abort;
   constexpr uint32_t kSlot = kV ? kChunk * kQuarter * 2 : 64;   // a ring slot: bytes, or tensor-memory columns
   const uint32_t dst0 = kV ? tc::smem_addr(sm.v) + (key >> 3) * 2048 + (key & 7) * 16 + half * 1024
-                           : cx.tm + Cols<kWeights>::K + 32 * half + ((uint32_t)(32 * lq) << 16);
+                           : cx.tm + Cols<kMode>::K + 32 * half + ((uint32_t)(32 * lq) << 16);
   auto put = [&](uint32_t dst, int p, const uint32_t (&o)[8]) {   // the step's channels 16 p .. +15
     if (kV) {
       sts16(dst + 256 * p, o[0], o[1], o[2], o[3]);
@@ -569,12 +575,12 @@ __device__ __forceinline__ void fill_tile(const Ctx<kWeights>& cx, int k0, int n
   };
   const int i0 = min(max(sm.seg.nw - k0, 0), n_chunks);   // first entry chunk of the span
   uint32_t ring = (4 * chunks + first) % kRing;   // slot of the step's quarter
-  if (!kWeights) {
+  if (!kWeights<kMode>) {
     KeyRef w{nullptr, 0.f};
 #pragma unroll 1
     for (int n = 0; n < 4 * i0; ++n) {
       const int q = n & 3;
-      if (q == 0) w = window_ref<kWeights>(cx, k0 + (n >> 2), key);
+      if (q == 0) w = window_ref<kMode>(cx, k0 + (n >> 2), key);
       uint4 c[4];                         // in flight over the wait
 #pragma unroll
       for (int p = 0; p < 4; ++p)
@@ -698,9 +704,9 @@ __device__ __forceinline__ int entry_chunks(const Segment& sg, const Span& sp) {
 }
 
 // Warps 0-7 fill V, warps 8-15 K; before that they bring in the tile's Q, after it they write O.
-template <bool kWeights>
-__device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
-  Smem<kWeights>& sm = cx.sm;
+template <int kMode>
+__device__ __forceinline__ void role_fill(const Ctx<kMode>& cx) {
+  Smem<kMode>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   const int tid = threadIdx.x, lane = tid & 31;
   const bool values = tid < kValWarps * 32;
@@ -712,24 +718,25 @@ __device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
   while (u < cx.u1) {
     // ---- Q rows -> fp16 B operand, row r scaled by 2^-e_r (exact)
     const int b = tile / cx.pl.tiles;
-    const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
+    const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRowsOf<kMode>;
     const int64_t rows = (int64_t)a.Tq * a.Hq;
     {
       // row 8 g + tid % 8, channels 8 (tid / 8) .. +7; four rows at a time, and once more for the conversion
       // (from L2: eight of them in registers would have the other roles' code spill)
       const uint16_t* src = a.Q + ((int64_t)b * rows + r0 + (tid & 7)) * kD + (tid >> 3) * 8;
-      const int live = (int)min(rows - r0 - (tid & 7), (int64_t)kRows);
+      const int live = (int)min(rows - r0 - (tid & 7), (int64_t)kRowsOf<kMode>);
       auto load4 = [&](int g0, uint4 (&qv)[4]) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           qv[g] = 8 * (g0 + g) < live ? __ldg(reinterpret_cast<const uint4*>(src + 8 * (g0 + g) * kD)) : make_uint4(0, 0, 0, 0);
       };
+      constexpr int kLast = kRowsOf<kMode> / 8 - 4;
       uint4 qv[4];
       load4(0, qv);
-      if (tid < kRows) sm.qexp[1][tid] = 0;
+      if (tid < kRowsOf<kMode>) sm.qexp[1][tid] = 0;
       fill_sync();
 #pragma unroll 1
-      for (int g0 = 0; g0 < 8; g0 += 4) {
+      for (int g0 = 0; g0 < kLast + 4; g0 += 4) {
         if (g0) load4(g0, qv);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -743,8 +750,8 @@ __device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
       }
       fill_sync();
 #pragma unroll 1
-      for (int g0 = 4; g0 >= 0; g0 -= 4) {
-        if (g0 == 0) load4(0, qv);
+      for (int g0 = kLast; g0 >= 0; g0 -= 4) {
+        if (g0 != kLast) load4(g0, qv);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const float qs = pow2i(-q_head_exp(sm.qexp[1][8 * (g0 + g) + (tid & 7)]));
@@ -759,21 +766,21 @@ __device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
         }
       }
     }
-    if (tid < kRows) sm.mult[tid] = a.scale * kLog2e * pow2i(q_head_exp(sm.qexp[1][tid]));
+    if (tid < kRowsOf<kMode>) sm.mult[tid] = a.scale * kLog2e * pow2i(q_head_exp(sm.qexp[1][tid]));
     tc::fence_async_smem();
     tc::tc_fence_before();
     block_sync();                       // Q, row constants and the tile's chunks are there, O of the last tile is not
     tc::tc_fence_after();
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = sm.seg.n_chunks + kTileUnits, more = entry_chunks(sm.seg, sp);
-    if (kWeights || !values)
-      fill_tile<kWeights, false>(cx, sp.k0, sp.n, chunks, entries, (warp >> 2) + (kWeights && values ? 2 : 0), warp & 3, lane);
+    if (kWeights<kMode> || !values)
+      fill_tile<kMode, false>(cx, sp.k0, sp.n, chunks, entries, (warp >> 2) + (kWeights<kMode> && values ? 2 : 0), warp & 3, lane);
     else
-      fill_tile<kWeights, true>(cx, sp.k0, sp.n, chunks, entries, warp >> 2, warp & 3, lane);
+      fill_tile<kMode, true>(cx, sp.k0, sp.n, chunks, entries, warp >> 2, warp & 3, lane);
     block_sync();                       // the tile's products are complete, l is known
     tc::tc_fence_after();
     if (*abort) break;
-    if (!kWeights) drain_o<kWeights>(cx, sp, tile, (values ? 0 : 2) + (warp >> 2), warp & 3, lane);
+    if (!kWeights<kMode>) drain_o<kMode>(cx, sp, tile, (values ? 0 : 2) + (warp >> 2), warp & 3, lane);
     chunks += sp.n;
     entries += more;
     u = min(cx.u1, tstart + units);
@@ -784,11 +791,11 @@ __device__ __forceinline__ void role_fill(const Ctx<kWeights>& cx) {
 
 // One warp each for K and V: the codes of every entry chunk's quarters into the staging slots,
 // two tensor-map copies (one per page) a quarter.
-template <bool kWeights, bool kV>
-__device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
-  Smem<kWeights>& sm = cx.sm;
+template <int kMode, bool kV>
+__device__ __forceinline__ void role_stage(const Ctx<kMode>& cx) {
+  Smem<kMode>& sm = cx.sm;
   const DenseArgs& a = cx.a;
-  constexpr int kStage = kV ? Stages<kWeights>::V : Stages<kWeights>::K;
+  constexpr int kStage = kV ? Stages<kMode>::V : Stages<kMode>::K;
   const int lane = threadIdx.x & 31;
   volatile int* abort = &sm.abort;
   uint32_t entries = 0, issued = 0;     // quarters given to the copy engine
@@ -797,7 +804,7 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
     seg_sync();                         // the tile's chunks are known (the copies need no more than that)
     const Span sp = span_of(sm.seg, u, cx.u1, tstart);
     const int units = sm.seg.n_chunks + kTileUnits, more = entry_chunks(sm.seg, sp);
-    const int nw = sm.seg.nw, i0 = sp.n - more, steps = kV && kWeights ? 0 : 4 * more;
+    const int nw = sm.seg.nw, i0 = sp.n - more, steps = kV && kWeights<kMode> ? 0 : 4 * more;
     // lane l: page l % 2 of chunk i + l / 2, for 16 chunks; the next 16 are on their way
     auto pages_at = [&](int i) -> int {
       i += lane >> 1;
@@ -847,30 +854,29 @@ __device__ __forceinline__ void role_stage(const Ctx<kWeights>& cx) {
 // One key of a chunk as its softmax thread sees it.
 struct KeyView {
   bool masked;         // some row may not see the key, or its window row is rescaled (uniform over the warp)
-  bool seen;           // what every row of a one-token tile sees
+  bool seen;           // a key that some row may see
   int win;             // 1: window row
   int j, p;            // entry index; raw position (an entry's: of its last token)
   float kf, ff;        // window row: 2^f and f
-  float dist;          // |t - p| in a one-token tile
 };
 
 // |t - p| in fp32 (exact below 2^24).
 __device__ __forceinline__ float distance(int t, int p) {
   return (float)(t > p ? (uint32_t)t - (uint32_t)p : (uint32_t)p - (uint32_t)t);
 }
-template <bool kWeights>
-__device__ __forceinline__ bool row_sees(const Ctx<kWeights>& cx, const KeyView& kv, int r) {
-  const Smem<kWeights>& sm = cx.sm;
+template <int kMode>
+__device__ __forceinline__ bool row_sees(const Ctx<kMode>& cx, const KeyView& kv, int r) {
+  const Smem<kMode>& sm = cx.sm;
   if (kv.win) return (uint32_t)(sm.t[r] - kv.p) < (uint32_t)cx.a.W && kv.p >= sm.doc[r];
   return kv.j < sm.nv[r] && kv.p - 3 >= sm.doc[r];
 }
 
 // Columns c0 .. c0+31 of this thread's key: the logits in the log2 domain as the value
 // product carries them, -inf where the row does not see the key.
-template <bool kWeights>
-__device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyView& kv, uint32_t taddr, int c0, uint64_t* done,
+template <int kMode>
+__device__ __forceinline__ void load_logits(const Ctx<kMode>& cx, const KeyView& kv, uint32_t taddr, int c0, uint64_t* done,
                                             float (&x)[32]) {
-  const Smem<kWeights>& sm = cx.sm;
+  const Smem<kMode>& sm = cx.sm;
   tmem_ld32(taddr, x);
   tc::tmem_wait_ld();
   if (done) {   // the buffer's last columns
@@ -901,13 +907,15 @@ __device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyVi
       for (int j = 0; j < 32; ++j) x[j] = cap2 * fast_tanh(x[j] * inv);
     }
   }
+  auto one = [&] { return (sm.seg.one_tok >> (c0 / 32) & 1) != 0; };   // the columns belong to one token
   if (cx.a.slopes) {
-    if (sm.seg.one_t) {
+    if (one()) {
+      const float dist = distance(sm.t[c0], kv.p);
 #pragma unroll
       for (int j4 = 0; j4 < 8; ++j4) {
         const float4 m = *reinterpret_cast<const float4*>(&sm.slope2[c0 + 4 * j4]);
-        x[4 * j4] = fmaf(-m.x, kv.dist, x[4 * j4]); x[4 * j4 + 1] = fmaf(-m.y, kv.dist, x[4 * j4 + 1]);
-        x[4 * j4 + 2] = fmaf(-m.z, kv.dist, x[4 * j4 + 2]); x[4 * j4 + 3] = fmaf(-m.w, kv.dist, x[4 * j4 + 3]);
+        x[4 * j4] = fmaf(-m.x, dist, x[4 * j4]); x[4 * j4 + 1] = fmaf(-m.y, dist, x[4 * j4 + 1]);
+        x[4 * j4 + 2] = fmaf(-m.z, dist, x[4 * j4 + 2]); x[4 * j4 + 3] = fmaf(-m.w, dist, x[4 * j4 + 3]);
       }
     } else {
 #pragma unroll
@@ -915,18 +923,19 @@ __device__ __forceinline__ void load_logits(const Ctx<kWeights>& cx, const KeyVi
     }
   }
   if (!kv.masked) return;
-  if (sm.seg.one_t) {
+  if (one()) {
+    const bool seen = kv.seen && row_sees<kMode>(cx, kv, c0);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = kv.seen ? x[j] + kv.ff : -INFINITY;
+    for (int j = 0; j < 32; ++j) x[j] = seen ? x[j] + kv.ff : -INFINITY;
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = kv.seen && row_sees<kWeights>(cx, kv, c0 + j) ? x[j] + kv.ff : -INFINITY;
+    for (int j = 0; j < 32; ++j) x[j] = kv.seen && row_sees<kMode>(cx, kv, c0 + j) ? x[j] + kv.ff : -INFINITY;
   }
 }
 
-template <bool kWeights>
-__device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
-  Smem<kWeights>& sm = cx.sm;
+template <int kMode>
+__device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
+  Smem<kMode>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   const int st = threadIdx.x - kSoftFirst, warp = st >> 5, lane = st & 31;
   const int lq = warp & 3, half = warp >> 2;   // lane quarter; attention: rows 32 half .. +31, weights: chunks of that parity
@@ -940,7 +949,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
   while (u < cx.u1) {
     // ---- rows of the tile
     const int b = tile / cx.pl.tiles;
-    const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRows;
+    const int r0 = (cx.pl.tile0 + tile % cx.pl.tiles) * kRowsOf<kMode>;
     const int n_ent = dense_entries(a, b);
     const int64_t shift = dense_shift(a, b);
     if (st == 0) {
@@ -949,11 +958,14 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       sm.seg.e_lo = INT_MAX; sm.seg.e_hi = 0; sm.seg.w_lo = INT_MAX; sm.seg.w_hi = INT_MIN;
       sm.seg.all_lo = 0; sm.seg.all_hi = INT_MAX;
       sm.seg.next_t = a.Hq - r0 % a.Hq;
-      sm.seg.one_t = r0 / a.Hq == (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
+      sm.seg.one_tok = 0;
+      for (int k = 0; k < kRowsOf<kMode> / 32; ++k)
+        sm.seg.one_tok |= (r0 + 32 * k) / a.Hq == (r0 + 32 * k + 31) / a.Hq ? 1 << k : 0;
+      sm.seg.one_t = r0 / a.Hq == (int)(min((int64_t)r0 + kRowsOf<kMode>, rows) - 1) / a.Hq;
       if (tile % cx.pl.tiles == 0 && tstart == u && dense_count_bad(a, b)) raise_status(cx.status, CSA2_STATUS_BAD_COUNT);
     }
     soft_sync();
-    if (st < kRows) {
+    if (st < kRowsOf<kMode>) {
       const bool live = r0 + st < rows;
       DenseRow r{INT_MIN, 0, INT_MAX, 0, 0};   // no row: it sees nothing, wherever t - p wraps to
       float slope = 0.f, nref = kUnset;
@@ -972,12 +984,11 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         atomicMax(&sm.seg.all_lo, a.entry_pos && r.doc > 0 ? INT_MAX : lo);   // by position: no chunk is free of masks
         atomicMin(&sm.seg.all_hi, r.nv);
         if (a.slopes) slope = a.slopes[h];
-        if (kWeights) {
+        if (kWeights<kMode>) {
           const float lse = a.lse_in[(int64_t)b * rows + r0 + st];
           nref = isinf(lse) ? -INFINITY : -lse * kLog2e;   // a row that saw nothing adds nothing
         }
-        if (st == 0) sm.seg.t = r.t;
-      } else if (kWeights) {
+      } else if (kWeights<kMode>) {
         nref = -INFINITY;
       }
       sm.nv[st] = r.nv;
@@ -989,13 +1000,13 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
     soft_sync();
     if (st == 0) {
       Range g{sm.seg.e_lo, sm.seg.e_hi, sm.seg.w_lo, sm.seg.w_hi};
-      if (kWeights && !cx.pl.sums) {
+      if (kWeights<kMode> && !cx.pl.sums) {
         g.e_lo = sm.seg.e_lo = 0;
         g.e_hi = sm.seg.e_hi = n_ent;
       }
-      sm.seg.n_chunks = range_chunks(g, kWeights);
+      sm.seg.n_chunks = range_chunks(g, kWeights<kMode>);
       sm.seg.c_hi = (g.e_hi + kChunk - 1) / kChunk;
-      sm.seg.nw = !kWeights && g.w_hi >= g.w_lo ? (int)(((int64_t)g.w_hi - g.w_lo) / kChunk) + 1 : 0;
+      sm.seg.nw = !kWeights<kMode> && g.w_hi >= g.w_lo ? (int)(((int64_t)g.w_hi - g.w_lo) / kChunk) + 1 : 0;
     }
     soft_sync();
     seg_arrive();
@@ -1006,9 +1017,9 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
     const int shift32 = (int)min(shift, (int64_t)1 << 29);
     // The key of a chunk; its page is read one chunk ahead.
     auto entry_of = [&](int i) -> int { return (sg.c_hi - 1 - (sp.k0 + i - sg.nw)) * kChunk + key; };
-    constexpr int kStep = kWeights ? 2 : 1;
-    const int first = kWeights ? half : 0;
-    auto page_ahead = [&](int i) -> int { return page_of<kWeights>(cx, entry_of(i), i < sp.n && sp.k0 + i >= sg.nw); };
+    constexpr int kStep = kWeights<kMode> ? 2 : 1;
+    const int first = kWeights<kMode> ? half : 0;
+    auto page_ahead = [&](int i) -> int { return page_of<kMode>(cx, entry_of(i), i < sp.n && sp.k0 + i >= sg.nw); };
     int page = page_ahead(first);
     auto view = [&](int i, int64_t* slot) -> KeyView {
       KeyView kv;
@@ -1040,12 +1051,10 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         kv.masked = e0 < sm.seg.all_lo || e0 + kChunk > sm.seg.all_hi || __any_sync(0xffffffffu, !kv.seen);
       }
       page = page_ahead(i + kStep);
-      kv.dist = distance(sm.seg.t, kv.p);
-      if (sm.seg.one_t) kv.seen = kv.seen && row_sees<kWeights>(cx, kv, 0);
       return kv;
     };
 
-    if (kWeights) {
+    if (kWeights<kMode>) {
       for (int i = first; i < sp.n; i += 2) {
         if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + i);
         int64_t slot;
@@ -1055,10 +1064,10 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         tc::tc_fence_after();
         float sum = 0.f;
 #pragma unroll 1
-        for (int c0 = 0; c0 < kRows; c0 += 32) {
+        for (int c0 = 0; c0 < kRowsOf<kMode>; c0 += 32) {
           float x[32];
-          load_logits<kWeights>(cx, kv, cx.tm + Cols<true>::S + 64 * (i & 1) + c0 + lane_q, c0,
-                                c0 ? &sm.s_free[i & 1] : nullptr, x);
+          load_logits<kMode>(cx, kv, cx.tm + Cols<kMode>::S + kRowsOf<kMode> * (i & 1) + c0 + lane_q, c0,
+                                c0 + 32 == kRowsOf<kMode> ? &sm.s_free[i & 1] : nullptr, x);
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j4 = 0; j4 < 8; ++j4) {
@@ -1082,7 +1091,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
       for (int j = 0; j < 32; ++j) lsum[j] = 0.f;
       const int c0 = 32 * half;
       for (int i = 0; i < sp.n; ++i) {
-        const uint32_t ph = c.all + i, ts = cx.tm + Cols<false>::S + c0 + lane_q;
+        const uint32_t ph = c.all + i, ts = cx.tm + Cols<0>::S + c0 + lane_q;
         if (st == 0) *reinterpret_cast<volatile int*>(&sm.progress) = (int)(c.all + i);
         int64_t slot;
         const KeyView kv = view(i, &slot);
@@ -1091,7 +1100,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         // ---- logits over the reference, and whether one outgrows it
         float x[32];
         float top = -INFINITY;
-        load_logits<kWeights>(cx, kv, ts, c0, &sm.s_free[0], x);
+        load_logits<kMode>(cx, kv, ts, c0, &sm.s_free[0], x);
 #pragma unroll
         for (int j4 = 0; j4 < 8; ++j4) {
           const float4 z = *reinterpret_cast<const float4*>(&sm.nref[c0 + 4 * j4]);
@@ -1184,7 +1193,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
         if (lane < 16) sm.red[lq][c0 + 16 * q + lane] = s;
       }
       soft_sync();
-      if (st < kRows) {
+      if (st < kRowsOf<kMode>) {
         const float l = (sm.red[0][st] + sm.red[1][st]) + (sm.red[2][st] + sm.red[3][st]);
         const float m = sm.nref[st] == kUnset ? -INFINITY : -sm.nref[st];
         sm.red[0][st] = l == 0.f ? 0.f : 1.f / l;   // the factor of O
@@ -1192,9 +1201,9 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
           if (a.lse && r0 + st < rows)
             a.lse[(int64_t)b * rows + r0 + st] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         } else {
-          float* ml = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats + kRows * kD;
+          float* ml = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats + kRowsOf<kMode> * kD;
           ml[st] = m;
-          ml[kRows + st] = l;
+          ml[kRowsOf<kMode> + st] = l;
         }
       }
     }
@@ -1209,14 +1218,14 @@ __device__ __forceinline__ void role_softmax(const Ctx<kWeights>& cx) {
 }
 
 // Order of the products: S(0) | S(1) PV(0) | S(2) PV(1) | ...
-template <bool kWeights>
-__device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
-  Smem<kWeights>& sm = cx.sm;
+template <int kMode>
+__device__ __forceinline__ void role_mma(const Ctx<kMode>& cx) {
+  Smem<kMode>& sm = cx.sm;
   volatile int* abort = &sm.abort;
-  constexpr uint32_t kIdS = tc::idesc_f16(128, kRows, 0, 0, 0);   // K-major A (tensor memory) and B
-  constexpr uint32_t kIdO = tc::idesc_f16(128, kRows, 0, 1, 1);   // MN-major A and B
+  constexpr uint32_t kIdS = tc::idesc_f16(128, kRowsOf<kMode>, 0, 0, 0);   // K-major A (tensor memory) and B
+  constexpr uint32_t kIdO = tc::idesc_f16(128, kRowsOf<kMode>, 0, 1, 1);   // MN-major A and B
   constexpr uint32_t kHiS = desc_hi(8192), kHiO = desc_hi(128);
-  constexpr int kRing = Cols<kWeights>::ring;
+  constexpr int kRing = Cols<kMode>::ring;
   const uint32_t dq = desc_lo(sm.q, 128), dv = desc_lo(sm.v, 2048), dp = desc_lo(sm.p, 1024);
   const uint32_t leader = elect_lane();
   const int lane = threadIdx.x & 31;
@@ -1237,9 +1246,9 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
     for (int i = -1; ok && i < sp.n; ++i) {
       const bool more = i + 1 < sp.n;
       const uint32_t cs = c.all + i + 1, cv = c.all + i;      // running numbers of the two chunks
-      const int es = kWeights ? (i + 1) & 1 : 0;
-      const uint32_t ps = kWeights ? c.phase(i + 1) : cs;
-      const int first = !more ? 5 : ps > 0 ? 0 : 1, last = kWeights || i < 0 ? 4 : 9;
+      const int es = kWeights<kMode> ? (i + 1) & 1 : 0;
+      const uint32_t ps = kWeights<kMode> ? c.phase(i + 1) : cs;
+      const int first = !more ? 5 : ps > 0 ? 0 : 1, last = kWeights<kMode> || i < 0 ? 4 : 9;
       const uint32_t bar = tc::smem_addr(lane == 0 ? &sm.s_free[es] : lane <= 4 ? &sm.kq_full[lane - 1]
                                                   : lane == 5 ? &sm.p_full : &sm.v_full[(lane - 6) & 3]);
       const uint32_t parity = (lane == 0 ? ps - 1 : lane <= 4 ? cs : cv) & 1;
@@ -1259,13 +1268,13 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
         }
         tc::tc_fence_after();
         if (step >= 1 && step <= 4) {
-          const uint32_t q = step - 1, ka = cx.tm + Cols<kWeights>::K + 64 * ((4 * cs + q) % kRing);
-          const uint32_t d = cx.tm + Cols<kWeights>::S + 64 * es;
+          const uint32_t q = step - 1, ka = cx.tm + Cols<kMode>::K + 64 * ((4 * cs + q) % kRing);
+          const uint32_t d = cx.tm + Cols<kMode>::S + kRowsOf<kMode> * es;
 #pragma unroll
           for (uint32_t ks = 0; ks < 8; ++ks) mma_ts<kHiS, kIdS>(leader, d, ka + 8 * ks, dq + (8 * q + ks) * 16, q | ks);
           mma_commit_by(leader, &sm.kq_free[q]);
           if (step == 4) mma_commit_by(leader, &sm.s_full[es]);
-        } else if (!kWeights && step >= 6) {
+        } else if (!kWeights<kMode> && step >= 6) {
           const uint32_t mt = step - 6, va = dv + ((4 * cv + mt) % kVSlots) * (kChunk * kQuarter * 2 / 16);
 #pragma unroll
           for (uint32_t kk = 0; kk < 8; ++kk)
@@ -1286,9 +1295,9 @@ __device__ __forceinline__ void role_mma(const Ctx<kWeights>& cx) {
 }
 
 // The last warp: the packed pages of the chunks ahead into L2.
-template <bool kWeights>
-__device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx) {
-  Smem<kWeights>& sm = cx.sm;
+template <int kMode>
+__device__ __forceinline__ void role_prefetch(const Ctx<kMode>& cx) {
+  Smem<kMode>& sm = cx.sm;
   const DenseArgs& a = cx.a;
   volatile int* abort = &sm.abort;
   constexpr int kAhead = 5;
@@ -1304,8 +1313,8 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx) {
       // the next tile's Q rows (contiguous)
       const int64_t rows = (int64_t)a.Tq * a.Hq;
       const int tn = tile + 1;
-      if (tstart + units < cx.u1 && lane < 4) {
-        const int64_t r0 = (int64_t)(cx.pl.tile0 + tn % cx.pl.tiles) * kRows + 16 * lane;
+      if (tstart + units < cx.u1 && lane < kRowsOf<kMode> / 16) {
+        const int64_t r0 = (int64_t)(cx.pl.tile0 + tn % cx.pl.tiles) * kRowsOf<kMode> + 16 * lane;
         const int64_t live = min(rows - r0, (int64_t)16);
         if (live > 0)
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.Q + ((int64_t)(tn / cx.pl.tiles) * rows + r0) * kD),
@@ -1348,30 +1357,30 @@ __device__ __forceinline__ void role_prefetch(const Ctx<kWeights>& cx) {
   }
 }
 
-template <bool kWeights>
+template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, const __grid_constant__ CUtensorMap map, uint32_t* status) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  Smem<kWeights>& sm = *reinterpret_cast<Smem<kWeights>*>(smem_raw);
+  Smem<kMode>& sm = *reinterpret_cast<Smem<kMode>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5;
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      tc::mbar_init(&sm.kq_full[i], 4 * kSplit<kWeights>);
+      tc::mbar_init(&sm.kq_full[i], 4 * kSplit<kMode>);
       tc::mbar_init(&sm.kq_free[i], 1);
-      tc::mbar_init(&sm.v_full[i], 4 * kSplit<kWeights>);
+      tc::mbar_init(&sm.v_full[i], 4 * kSplit<kMode>);
       tc::mbar_init(&sm.v_free[i], 1);
     }
-    for (int i = 0; i < Stages<kWeights>::K; ++i) {
+    for (int i = 0; i < Stages<kMode>::K; ++i) {
       tc::mbar_init(&sm.kst_full[i], 1);
-      tc::mbar_init(&sm.kst_free[i], 4 * kSplit<kWeights>);
+      tc::mbar_init(&sm.kst_free[i], 4 * kSplit<kMode>);
     }
-    for (int i = 0; i < Stages<kWeights>::V; ++i) {
+    for (int i = 0; i < Stages<kMode>::V; ++i) {
       tc::mbar_init(&sm.vst_full[i], 1);
-      tc::mbar_init(&sm.vst_free[i], 4 * kSplit<kWeights>);
+      tc::mbar_init(&sm.vst_free[i], 4 * kSplit<kMode>);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
-      tc::mbar_init(&sm.s_free[i], kWeights ? kSoftWarps / 2 : kSoftWarps);
+      tc::mbar_init(&sm.s_free[i], kWeights<kMode> ? kSoftWarps / 2 : kSoftWarps);
     }
     tc::mbar_init(&sm.p_full, kSoftWarps);
     tc::mbar_init(&sm.p_free, 1);
@@ -1386,7 +1395,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
   const int tiles = a.B * pl.tiles;
   int mine = 0, total = 0;
 #pragma unroll 1
-  for (int t = tid; t < tiles; t += kThreads) mine += tile_units<kWeights>(a, pl, t);
+  for (int t = tid; t < tiles; t += kThreads) mine += tile_units<kMode>(a, pl, t);
   int inc = block_scan(mine, sm.scan, &total);
   const int ctas = min((int)gridDim.x, total), g = blockIdx.x;
   int u0 = g < ctas ? (int)((int64_t)total * g / ctas) : 0;
@@ -1398,7 +1407,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
 #pragma unroll 1
     for (int t0 = 0; t0 < tiles; t0 += kThreads) {
       if (tiles > kThreads) {          // (with one batch the first scan holds the answer)
-        v = t0 + tid < tiles ? tile_units<kWeights>(a, pl, t0 + tid) : 0;
+        v = t0 + tid < tiles ? tile_units<kMode>(a, pl, t0 + tid) : 0;
         inc = block_scan(v, sm.scan, &all);
       }
       const int start = base + inc - v;
@@ -1419,27 +1428,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_tc(DenseArgs a, Plan pl, 
     if (u0 - sm.found_start <= kTileUnits) u0 = sm.found_start;
     u1 = sm.found_end;
   }
-  Ctx<kWeights> cx{a, pl, sm, tm, u0, u1, sm.found_tile, sm.found_start, status, &map};
+  Ctx<kMode> cx{a, pl, sm, tm, u0, u1, sm.found_tile, sm.found_start, status, &map};
   if (u1 <= u0) cx.tile = 0;
-  if (!kWeights && tid == 0) pl.cont[g] = (u1 > u0 && cx.tstart < u0) ? cx.tile : -1;
+  if (!kWeights<kMode> && tid == 0) pl.cont[g] = (u1 > u0 && cx.tstart < u0) ? cx.tile : -1;
 
   // ---- roles, each with its own walk over the tiles (every walk meets the same barriers)
   if (warp < kValWarps + kKeyWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill<kWeights>));
-    role_fill<kWeights>(cx);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill<kMode>));
+    role_fill<kMode>(cx);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft<kWeights>));
-    role_softmax<kWeights>(cx);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft<kMode>));
+    role_softmax<kMode>(cx);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
     if (warp == kMmaWarp)
-      role_mma<kWeights>(cx);
+      role_mma<kMode>(cx);
     else if (warp == kMmaWarp + 1)
-      role_stage<kWeights, false>(cx);
+      role_stage<kMode, false>(cx);
     else if (warp == kMmaWarp + 2)
-      role_stage<kWeights, true>(cx);
+      role_stage<kMode, true>(cx);
     else
-      role_prefetch<kWeights>(cx);
+      role_prefetch<kMode>(cx);
   }
   tc::tc_fence_before();
   block_sync();
@@ -1560,13 +1569,13 @@ __global__ void __launch_bounds__(128) k_weights_ranges(DenseArgs a, Plan pl) {
   const int tile = blockIdx.x * 128 + threadIdx.x;
   if (tile >= a.B * pl.tiles) return;
   const int b = tile / pl.tiles;
-  const int r0 = (pl.tile0 + tile % pl.tiles) * kRows;
+  const int r0 = (pl.tile0 + tile % pl.tiles) * pl.rows;
   const int64_t rows = (int64_t)a.Tq * a.Hq;
   int lo = INT_MAX, hi = 0;
   if (r0 < rows) {
     const int n_ent = dense_entries(a, b);
     const int64_t shift = dense_shift(a, b);
-    const int i1 = (int)(min((int64_t)r0 + kRows, rows) - 1) / a.Hq;
+    const int i1 = (int)(min((int64_t)r0 + pl.rows, rows) - 1) / a.Hq;
 #pragma unroll 1
     for (int i = r0 / a.Hq; i <= i1; ++i) {
       const DenseRow r = dense_row(a, b, i, n_ent, shift, 0);
@@ -1580,7 +1589,8 @@ __global__ void __launch_bounds__(128) k_weights_ranges(DenseArgs a, Plan pl) {
   pl.ranges[tile] = hi > lo ? make_int2(lo / kChunk * kChunk, (hi + kChunk - 1) / kChunk * kChunk) : make_int2(0, 0);
 }
 
-int tiles_of(const csa2_dims* dm) { return (int)(((int64_t)dm->Tq * dm->Hq + kRows - 1) / kRows); }
+int tiles_of(const csa2_dims* dm, int rows) { return (int)(((int64_t)dm->Tq * dm->Hq + rows - 1) / rows); }
+int weights_rows(const csa2_dims* dm) { return (int64_t)dm->Tq * dm->Hq > 64 ? 128 : 64; }
 
 // Units that a sequence's tile can have.
 int64_t max_chunks(int max_entries, int W, int64_t tq) {
@@ -1596,15 +1606,15 @@ cudaError_t device_sms(int* sms) {
 
 // The register split adds up to what the block is launched with; a build whose
 // kernel has fewer registers per thread must not run it (its wait would not end).
-template <bool kWeights>
+template <int kMode>
 cudaError_t prepare_kernel() {
   cudaFuncAttributes at;
-  cudaError_t e = cudaFuncGetAttributes(&at, k_dense_tc<kWeights>);
+  cudaError_t e = cudaFuncGetAttributes(&at, k_dense_tc<kMode>);
   if (e != cudaSuccess) return e;
-  static_assert(4 * kRegsFill<kWeights> + 2 * kRegsSoft<kWeights> + kRegsMisc <= 7 * kRegsLaunch, "register split");
+  static_assert(4 * kRegsFill<kMode> + 2 * kRegsSoft<kMode> + kRegsMisc <= 7 * kRegsLaunch, "register split");
   if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(k_dense_tc<kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sizeof(Smem<kWeights>));
+  return cudaFuncSetAttribute(k_dense_tc<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(Smem<kMode>));
 }
 
 // Sums of the weights' tiles: at most this many bytes per slab of tiles.
@@ -1613,7 +1623,7 @@ constexpr size_t kSumBytes = (size_t)256 << 20;
 int slab_tiles(const csa2_dims* dm, int max_entries, int64_t* stride) {
   *stride = ((int64_t)max_entries + kChunk - 1) / kChunk * kChunk;
   const int64_t per = std::max<int64_t>(1, dm->B) * *stride * 4;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(tiles_of(dm), (int64_t)kSumBytes / std::max<int64_t>(1, per)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(tiles_of(dm, weights_rows(dm)), (int64_t)kSumBytes / std::max<int64_t>(1, per)));
 }
 
 // Tiles of every sequence that one launch takes: its units of work stay below 2^31.
@@ -1629,7 +1639,7 @@ bool dense_tc_supported(const csa2_dims* dm) { return dm->d == kD; }
 
 size_t dense_attn_workspace_bytes(const csa2_dims* dm, int max_entries) {
   // two slots per CTA, and never more CTAs than chunks
-  const int64_t units = (int64_t)dm->B * tiles_of(dm) * max_chunks(max_entries, dm->W, dm->swa_cap);
+  const int64_t units = (int64_t)dm->B * tiles_of(dm, kRows) * max_chunks(max_entries, dm->W, dm->swa_cap);
   const int64_t ctas = std::min<int64_t>(kMaxCtas, std::max<int64_t>(1, units));
   return up((size_t)kMaxCtas * 4) + (size_t)ctas * 2 * kPartFloats * sizeof(float);
 }
@@ -1649,12 +1659,13 @@ static bool codes_map(const DenseArgs& a, CUtensorMap* map) {
 cudaError_t launch_dense_attn_tc(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = device_sms(&sms);
-  if (e == cudaSuccess) e = prepare_kernel<false>();
+  if (e == cudaSuccess) e = prepare_kernel<0>();
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   if (!codes_map(a, &map)) return cudaErrorInvalidValue;
   Plan pl = {};
-  const int all = tiles_of(dm);
+  pl.rows = kRows;
+  const int all = tiles_of(dm, kRows);
   pl.cont = static_cast<int32_t*>(ws);
   pl.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + up((size_t)kMaxCtas * 4));
   const int64_t per_tile = (int64_t)a.B * max_chunks(a.max_entries, a.W, a.swa_cap);   // units of a tile of every sequence
@@ -1664,7 +1675,7 @@ cudaError_t launch_dense_attn_tc(const csa2_dims* dm, const DenseArgs& a, void* 
     pl.tile0 = t0;
     pl.tiles = std::min(slab, all - t0);
     pl.n_ctas = (int)std::min<int64_t>(std::min(sms, kMaxCtas), per_tile * pl.tiles);
-    e = launch_step(k_dense_tc<false>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<false>), s, a, pl, map, status_word());
+    e = launch_step(k_dense_tc<0>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<0>), s, a, pl, map, status_word());
     if (e != cudaSuccess) return e;
     if (pl.n_ctas == 1) continue;
     const unsigned shared = (unsigned)std::min<int64_t>((int64_t)a.B * pl.tiles, pl.n_ctas - 1);
@@ -1675,21 +1686,23 @@ cudaError_t launch_dense_attn_tc(const csa2_dims* dm, const DenseArgs& a, void* 
 }
 
 size_t entry_weights_workspace_bytes(const csa2_dims* dm, int max_entries) {
-  if (tiles_of(dm) <= 1) return 0;
+  if (tiles_of(dm, weights_rows(dm)) <= 1) return 0;
   int64_t stride;
   const int tiles = slab_tiles(dm, max_entries, &stride);
   return up((size_t)dm->B * tiles * sizeof(int2)) + (size_t)dm->B * tiles * stride * sizeof(float);
 }
 
-cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s) {
+template <int kMode>
+static cudaError_t launch_weights(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = device_sms(&sms);
-  if (e == cudaSuccess) e = prepare_kernel<true>();
+  if (e == cudaSuccess) e = prepare_kernel<kMode>();
   if (e != cudaSuccess) return e;
-  const int all = tiles_of(dm);
+  const int all = tiles_of(dm, kMode);
   CUtensorMap map;
   if (!codes_map(a, &map)) return cudaErrorInvalidValue;
   Plan pl = {};
+  pl.rows = kMode;
   const int64_t per_tile = (int64_t)a.B * max_chunks(a.max_entries, 0, 0);
   const int slab = std::min(launch_tiles(per_tile, all), all <= 1 ? 1 : slab_tiles(dm, a.max_entries, &pl.sum_stride));
   if (slab == 0) return cudaErrorInvalidConfiguration;
@@ -1703,7 +1716,7 @@ cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, voi
       e = launch_step(k_weights_ranges, dim3((unsigned)(((int64_t)a.B * pl.tiles + 127) / 128)), dim3(128), 0, s, a, pl);
       if (e != cudaSuccess) return e;
     }
-    e = launch_step(k_dense_tc<true>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<true>), s, a, pl, map, status_word());
+    e = launch_step(k_dense_tc<kMode>, dim3(pl.n_ctas), dim3(kThreads), sizeof(Smem<kMode>), s, a, pl, map, status_word());
     if (e != cudaSuccess) return e;
     if (all > 1) {
       e = launch_step(k_weights_sum, dim3((unsigned)((a.max_entries + 255) / 256), (unsigned)a.B), dim3(256), 0, s, a, pl,
@@ -1712,6 +1725,10 @@ cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, voi
     }
   }
   return cudaSuccess;
+}
+
+cudaError_t launch_entry_weights_tc(const csa2_dims* dm, const DenseArgs& a, void* ws, cudaStream_t s) {
+  return weights_rows(dm) == 64 ? launch_weights<64>(dm, a, ws, s) : launch_weights<128>(dm, a, ws, s);
 }
 
 }  // namespace csa2
