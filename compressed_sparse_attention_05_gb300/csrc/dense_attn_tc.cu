@@ -8,8 +8,8 @@
 //
 // One shared KV head, so the (token, head) pairs of a sequence are the rows of one
 // matrix whatever the number of heads: a tile is 64 consecutive rows (one token of
-// 64 heads, half a token of 128, several tokens of fewer heads), each row with its
-// own masks.  A tile's keys come in chunks of 128, nearest first (window rows, then
+// 64 heads, half a token of 128, several tokens of fewer heads; 128 rows for the weights
+// of more than 64), each row with its own masks.  A tile's keys come in chunks of 128, nearest first (window rows, then
 // entries from the newest to the oldest), so that a distance bias only lowers later
 // chunks and the reference maxima hardly move.  Per chunk
 //   S^T [128 keys x 64 rows]  = K [128 x 512] . Q^T        (32 MMAs, k = 16 channels)
