@@ -9,9 +9,9 @@
 // One shared KV head, so the (token, head) pairs of a sequence are the rows of one
 // matrix whatever the number of heads: a tile is 64 consecutive rows (one token of
 // 64 heads, half a token of 128, several tokens of fewer heads; 128 rows for the weights
-// of more than 64), each row with its own masks.  A tile's keys come in chunks of 128, nearest first (window rows, then
-// entries from the newest to the oldest), so that a distance bias only lowers later
-// chunks and the reference maxima hardly move.  Per chunk
+// of more than 64), each row with its own masks.  A tile's keys come in chunks of 128,
+// nearest first (window rows, then entries from the newest to the oldest), so that a
+// distance bias only lowers later chunks and the reference maxima hardly move.  Per chunk
 //   S^T [128 keys x 64 rows]  = K [128 x 512] . Q^T        (32 MMAs, k = 16 channels)
 //   O^T [512 dims x 64 rows] += V^T [512 x 128] . P^T      (4 M-tiles x 8 MMAs, k = 16 keys)
 //
@@ -297,23 +297,23 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// tanh below 0.55: an odd polynomial (least-squares fit of (tanh x / x - 1) / x^2 in x^2,
-// relative error 1.2 x 2^-24).
+// tanh up to 1/2: an odd polynomial (least-squares fit of (tanh x / x - 1) / x^2 in x^2, weighted to the
+// relative error, which is 1.1 x 2^-24).
 __device__ __forceinline__ float small_tanh(float x) {
   const float z = x * x;
-  float r = -0.0066150883f;
-  r = fmaf(r, z, 0.021312291f);
-  r = fmaf(r, z, -0.053909965f);
-  r = fmaf(r, z, 0.13333116f);
-  r = fmaf(r, z, -0.33333331f);
+  float r = -0.00666007306f;
+  r = fmaf(r, z, 0.02130601f);
+  r = fmaf(r, z, -0.0539009757f);
+  r = fmaf(r, z, 0.133329809f);
+  r = fmaf(r, z, -0.333333284f);
   return fmaf(x * z, r, x);
 }
-// Any x: above 0.55, 1 - 2 / (e^2x + 1) (relative error < 2^-21).
+// Any x: above 1/2, 1 - 2 / (e^2x + 1) (relative error < 2^-21).
 __device__ __forceinline__ float fast_tanh(float x) {
   const float a = fabsf(x);
   const float e = ex2(fminf(a, 10.f) * (2.f * kLog2e));   // tanh(10) rounds to 1
   const float big = copysignf(1.f - 2.f * rcp_approx(e + 1.f), x);
-  return a < 0.55f ? small_tanh(x) : big;
+  return a < 0.5f ? small_tanh(x) : big;
 }
 
 // ---- tiles and their chunks ----------------------------------------------------------
@@ -898,7 +898,7 @@ __device__ __forceinline__ void load_logits(const Ctx<kMode>& cx, const KeyView&
     float top = 0.f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(x[j]));
-    if (__all_sync(0xffffffffu, top * inv < 0.55f)) {
+    if (__all_sync(0xffffffffu, top * inv < 0.5f)) {
       // the usual case: every logit of the warp is well below the cap
 #pragma unroll
       for (int j = 0; j < 32; ++j) x[j] = cap2 * small_tanh(x[j] * inv);
