@@ -874,7 +874,7 @@ int csa2_evict(const csa2_dims* dm, const csa2_cache* c, const csa2_bounded* bou
     REQUIRE(dm->idx_dtype == CSA2_BF16 || dm->idx_dtype == CSA2_F32, "idx_dtype must be CSA2_BF16 or CSA2_F32");
   }
   REQUIRE(c->n_pages < (1ll << 31) / kPage, "cache.n_pages is too large");
-  if (max_entries <= keep) return CSA2_OK;   // no sequence can be over its budget
+  if (max_entries <= keep) return CSA2_OK;   // no sequence can have more than keep
   const size_t need = evict_workspace_bytes(dm->B, max_entries);
   if (!ws || ws_bytes < need) return fail(CSA2_ERR_WORKSPACE, "evict needs %zu workspace bytes (got %zu)", need, ws_bytes);
   REQUIRE(aligned16(ws), "ws must be 16-byte aligned");

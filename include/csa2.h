@@ -389,7 +389,7 @@ int csa2_sparse_attn(const csa2_dims* dims, const csa2_cache* cache, const csa2_
                      void* stream);
 
 /* ---- a bounded cache: attention over all of it, weights, eviction ------------
- * A cache that never grows past a budget needs no selection: every entry it
+ * A cache that never grows past a fixed size needs no selection: every entry it
  * holds is attended to, the weight each entry receives is added up, and when
  * the cache is full the entries of least weight leave.
  *
