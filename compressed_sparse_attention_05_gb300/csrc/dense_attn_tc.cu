@@ -1554,13 +1554,14 @@ __global__ void __launch_bounds__(256) k_weights_sum(DenseArgs a, Plan pl, int f
   if (j >= dense_entries(a, b)) return;
   const int64_t slot = entry_slot(a.page_table, a.max_pages, a.n_pages, b, j, first_slab ? status : nullptr);
   if (slot < 0) return;
-  float w = first_slab ? (a.weight_in ? a.decay * a.weight_in[slot] : 0.f) : a.weight_out[slot];
+  const float w = first_slab ? (a.weight_in ? a.decay * a.weight_in[slot] : 0.f) : a.weight_out[slot];
+  float sum = 0.f;                        // (by itself: the weight that was there may be much larger)
   for (int t = 0; t < pl.tiles; ++t) {
     const int64_t tile = (int64_t)b * pl.tiles + t;
     const int2 rg = pl.ranges[tile];
-    if (j >= rg.x && j < rg.y) w += pl.sums[tile * pl.sum_stride + j];
+    if (j >= rg.x && j < rg.y) sum += pl.sums[tile * pl.sum_stride + j];
   }
-  a.weight_out[slot] = w;
+  a.weight_out[slot] = w + sum;
 }
 // The entries whose sums a tile writes (whole chunks).
 __global__ void __launch_bounds__(128) k_weights_ranges(DenseArgs a, Plan pl) {

@@ -293,6 +293,20 @@ def test_weights_of_tiles_in_slabs():
     assert torch.equal(out[s], small[s])     # the tiles' sums are added in the same order
 
 
+def test_weights_of_more_tiles_than_a_slab_holds():
+    """32 tiles of 128 rows whose sums take more than twice the slab."""
+    c = Case(seed=42, Tq=64, lens=(300,), W=8, docs=[[(7 * i) % 900 for i in range(64)]])
+    c.attend()
+    c.max_entries = 5_000_000
+    assert 32 * c.max_entries * 4 > 2 * 256 << 20
+    assert abi.csa2_entry_weights_workspace_size(c.dims(), c.max_entries) < 300 << 20
+    w_in = torch.rand(c.n_pages * 64, device="cuda")
+    out = torch.zeros_like(w_in)
+    c.weigh(c.lse, w_in, out, decay=0.5)
+    assert status() == 0
+    c.check_weights(c.lse, w_in, out, decay=0.5)
+
+
 def test_one_slot_of_a_page_at_the_end_of_a_large_pool():
     """Byte offsets past 2^32: the last page of a pool whose codes take more than 4 GB."""
     n_pages = (1 << 32) // (64 * 256) + 3
