@@ -32,8 +32,8 @@
 // memory that the products keep busy (a barrier looked at: 180) and instruction issue (half of
 // all slots are taken, by 24 warps; no pipe is over 40%).  The products of a chunk interleaved with
 // the next scores, so that the last quarters have more time, changed nothing.  A batch of
-// 32 x 32,768 entries takes 217 us (635 TFLOP/s, 1.4 TB/s of packed entries), the weights of
-// the same batch 93 us, of which the products are 82.
+// 32 x 32,768 entries takes 215 us (642 TFLOP/s, 1.4 TB/s of packed entries), the weights of
+// the same batch 92 us, of which the products are 82.
 //
 // Work is split over the SMs by chunks, not by tiles: every CTA computes the chunk
 // count of all tiles (lengths live on the device), takes an equal contiguous share,
@@ -64,7 +64,7 @@ constexpr int kD = 512;
 // What a kernel does: 0 attention; else the weights, with tiles of that many rows (64 or 128).  Attention's
 // O^T takes tensor memory for 64 rows only.  An MMA with A in tensor memory takes 87 cycles for 64 rows as
 // for 128, so the weights take 128 where a sequence has more than 64: 2 x 257 tokens x 64 heads over 16,384
-// entries in 646 us instead of 861.
+// entries in 650 us instead of 861.
 template <int kMode> constexpr bool kWeights = kMode != 0;
 template <int kMode> constexpr int kRowsOf = kMode ? kMode : 64;
 constexpr int kRows = 64;                 // rows of an attention tile (N of both products)
@@ -326,10 +326,11 @@ __device__ __forceinline__ int range_chunks(const Range& r, bool weights) {
   return ne + nw;
 }
 // Units of work of a tile (tile = index among this launch's tiles): its chunks, and what beginning and
-// ending a tile takes (15 us, a chunk 4 us; without it an SM with 50 tiles of two chunks was still at work
-// when the SMs with tiles of 17 chunks had long finished).  A share never begins or ends in the first
+// ending a tile takes (17 us, a chunk 3.6 us; without it an SM with 50 tiles of two chunks was still at
+// work when the SMs with tiles of 17 chunks had long finished: 1,181 us for a prompt of 1,024 tokens with
+// documents; with 2, 3, 4, 5, 6 units 743, 649, 602, 573, 574).  A share never begins or ends in the first
 // kTileUnits units: such a bound moves to the tile's start.
-constexpr int kTileUnits = 4;
+constexpr int kTileUnits = 5;
 template <int kMode>
 __device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {
   const int b = tile / pl.tiles;
