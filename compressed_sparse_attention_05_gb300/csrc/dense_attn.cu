@@ -115,14 +115,16 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
       for (int c = 0; c < kPer; ++c) o[c] += pk * tile[k * kLd + 32 * c + lane];
     }
   };
-  for (int w0 = 0; w0 < r.w_n; w0 += kTile) {   // window rows (R5's operand: bf16 of code times scale)
+  // Window rows (R5's operand: bf16 of code times scale).  The conversion instruction keeps a NaN; rounding
+  // the bits as integers turns the one that arithmetic makes, 0x7FFFFFFF, into -0.
+  for (int w0 = 0; w0 < r.w_n; w0 += kTile) {
     __syncthreads();
     for (int u = threadIdx.x; u < kTile * D; u += blockDim.x) {
       const int k = u / D, c = u % D;
       float x = 0.f;
       if (w0 + k < r.w_n) {
         const int64_t wr = (int64_t)b * a.swa_cap + ((int64_t)r.w_lo + w0 + k - pos0);
-        x = bf16_bits_to_f32(f32_to_bf16_bits(fp8_to_f32(a.swa_codes[wr * D + c]) * a.swa_scales[wr]));
+        x = __uint_as_float(f32x2_bf16x2(fp8_to_f32(a.swa_codes[wr * D + c]) * a.swa_scales[wr], 0.f) << 16);
       }
       tile[k * kLd + c] = x;
     }
