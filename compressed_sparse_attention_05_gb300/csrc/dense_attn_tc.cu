@@ -308,10 +308,16 @@ __device__ __forceinline__ float small_tanh(float x) {
   r = fmaf(r, z, -0.333333284f);
   return fmaf(x * z, r, x);
 }
-// Any x: above 1/2, 1 - 2 / (e^2x + 1) (relative error < 2^-21).
+// min(a, b), NaN where one is NaN (fminf gives the other one).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Any x: above 1/2, 1 - 2 / (e^2x + 1) (relative error < 2^-21); a NaN stays one.
 __device__ __forceinline__ float fast_tanh(float x) {
   const float a = fabsf(x);
-  const float e = ex2(fminf(a, 10.f) * (2.f * kLog2e));   // tanh(10) rounds to 1
+  const float e = ex2(min_nan(a, 10.f) * (2.f * kLog2e));   // tanh(10) rounds to 1
   const float big = copysignf(1.f - 2.f * rcp_approx(e + 1.f), x);
   return a < 0.5f ? small_tanh(x) : big;
 }

@@ -26,6 +26,10 @@ def two_tokens(**kw):
     return Case(**{**dict(seed=11, Tq=2, Hq=8, lens=(300,), W=16, q_pos=[[1170, 1199]], docs=[[0, 1180]]), **kw})
 
 
+def poison_entry(c, j, group=1):
+    c.t["scales"][int(c.slots[0][j]), group] = 0x7F
+
+
 # ---- NaN window rows at d = 64 ---------------------------------------------------------
 @pytest.mark.parametrize("bad", ["scale", "code"])
 def test_nan_window_rows_of_the_small_kernel(bad):
@@ -38,4 +42,47 @@ def test_nan_window_rows_of_the_small_kernel(bad):
     c.attend()
     assert status() == 0
     assert c.lse[0, 0].isnan().all() and c.O[0, 0].isnan().all()
+    c.check_attention([(0, 1)])
+
+
+# ---- NaN under a cap ------------------------------------------------------------------
+@pytest.mark.parametrize("d", [512, 64])
+@pytest.mark.parametrize("bad", ["entry", "window"])
+def test_a_cap_lets_nan_keys_through(d, bad):
+    """Logits of a few times the cap, so that the cap's branch for large logits is taken."""
+    c = two_tokens(d=d, cap=2.0, q_scale=3.0)
+    if bad == "entry":
+        poison_entry(c, 200)
+    else:
+        c.t["wscales"][0, 1165 - int(c.pos0[0])] = float("nan")
+    c.attend()
+    assert status() == 0
+    assert c.lse[0, 0].isnan().all() and c.O[0, 0].isnan().all()
+    c.check_attention([(0, 1)])
+
+
+@pytest.mark.parametrize("d", [512, 64])
+def test_a_cap_lets_nan_keys_through_to_their_weight(d):
+    c = two_tokens(d=d, cap=2.0, q_scale=3.0)
+    c.attend()
+    lse = c.lse.clone()
+    want = c.weigh(lse, None, torch.zeros(c.n_pages * 64, device="cuda")).clone()
+    poison_entry(c, 200)
+    got = c.weigh(lse, None, torch.zeros(c.n_pages * 64, device="cuda"))
+    assert status() == 0
+    at = int(c.slots[0][200])
+    assert got[at].isnan()
+    got[at] = want[at]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("cap", [0.0, 2.0])
+def test_nan_in_a_query_stays_in_its_head(cap):
+    c = two_tokens(cap=cap, q_scale=3.0)
+    c.t["Q"][0, 0, 3, 77] = float("nan")
+    c.attend()
+    assert status() == 0
+    assert c.lse[0, 0, 3].isnan() and c.O[0, 0, 3].isnan().all()
+    rest = [h for h in range(8) if h != 3]
+    assert c.lse[0, 0, rest].isfinite().all() and c.O[0, 0, rest].isfinite().all()
     c.check_attention([(0, 1)])
