@@ -99,11 +99,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
   auto attend = [&](bool seen, float dist) {
     float dot = 0.f;
     for (int c = 0; c < D; ++c) dot += qs[warp * D + c] * tile[lane * kLd + c];
+    if (!__any_sync(0xffffffffu, seen)) return;
     const float x = seen ? dense_logit(a, dot, slope, dist) : -INFINITY;
-    const float mn = fmaxf(m, warp_max(x));
-    if (mn == -INFINITY) return;
+    const float mn = fmaxf(m, warp_max(x));             // -inf if all that was seen so far is NaN
     const float al = m == -INFINITY ? 0.f : expf(m - mn);
-    const float p = seen ? expf(x - mn) : 0.f;
+    const float p = seen ? expf(x - (mn == -INFINITY ? 0.f : mn)) : 0.f;
     m = mn;
     l = l * al + warp_sum(p);
 #pragma unroll

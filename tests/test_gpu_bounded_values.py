@@ -86,3 +86,26 @@ def test_nan_in_a_query_stays_in_its_head(cap):
     rest = [h for h in range(8) if h != 3]
     assert c.lse[0, 0, rest].isfinite().all() and c.O[0, 0, rest].isfinite().all()
     c.check_attention([(0, 1)])
+
+
+# ---- NaN where nothing finite came before ----------------------------------------------
+@pytest.mark.parametrize("d", [512, 64])
+def test_the_only_key_is_nan(d):
+    c = Case(seed=12, Hq=8, d=d, lens=(1,), window=False)
+    poison_entry(c, 0)
+    c.attend()
+    assert status() == 0
+    assert c.lse.isnan().all() and c.O.isnan().all()
+
+
+@pytest.mark.parametrize("d", [512, 64])
+def test_a_tile_of_nan_keys_before_good_ones(d):
+    """The first 32 entries (a whole tile of the d = 64 kernel) are NaN; the token of a later document sees none of
+    them."""
+    c = Case(seed=13, Tq=2, Hq=8, d=d, lens=(40,), window=False, q_pos=[[159, 159]], docs=[[0, 128]])
+    for j in range(32):
+        poison_entry(c, j, j % (d // 16))
+    c.attend()
+    assert status() == 0
+    assert c.lse[0, 0].isnan().all() and c.O[0, 0].isnan().all()
+    c.check_attention([(0, 1)])
