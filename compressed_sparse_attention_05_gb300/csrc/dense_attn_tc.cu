@@ -391,11 +391,16 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
 }
 
 // ---- dequantisation --------------------------------------------------------------------
-// min(a, b); the other one where one is NaN.  V takes a NaN as some finite value: a row that sees its key
-// gets the NaN through K and the weight, and a row that does not must not get 0 x NaN.
+// min(a, b) and max(a, b); the other one where one is NaN.  V takes NaN and infinity as some finite value: a
+// row that sees the key gets them through K and the weight, and a row that does not must not get 0 x NaN.
 __device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 // Half h (16 channels) of a piece with its two E4M3 scales (at most 448): 8 fp16 pairs.
@@ -460,6 +465,7 @@ __device__ __forceinline__ int page_of(const Ctx<kMode>& cx, int j, bool exists)
 template <bool kV>
 __device__ __forceinline__ void window_piece(const uint4& c, float wsc, uint32_t (&o)[8]) {
   if (kV && !isfinite(wsc)) wsc = 0.f;
+  const bool wide = kV && fabsf(wsc) > 128.f;   // a scale past 2^107: values may leave fp16's range at both ends
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t x = word_of(c, j);
@@ -468,6 +474,10 @@ __device__ __forceinline__ void window_piece(const uint4& c, float wsc, uint32_t
     if (kV) {
       o[2 * j] = min_f16x2(o[2 * j], 0x7BFF7BFFu);
       o[2 * j + 1] = min_f16x2(o[2 * j + 1], 0x7BFF7BFFu);
+      if (wide) {
+        o[2 * j] = max_f16x2(o[2 * j], 0xFBFFFBFFu);
+        o[2 * j + 1] = max_f16x2(o[2 * j + 1], 0xFBFFFBFFu);
+      }
     }
   }
 }

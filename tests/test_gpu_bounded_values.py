@@ -109,3 +109,16 @@ def test_a_tile_of_nan_keys_before_good_ones(d):
     assert status() == 0
     assert c.lse[0, 0].isnan().all() and c.O[0, 0].isnan().all()
     c.check_attention([(0, 1)])
+
+
+# ---- window rows of enormous scales --------------------------------------------------------
+@pytest.mark.parametrize("scale", [2.0 ** 112, 2.0 ** 125])
+def test_rows_past_the_operand_range_stay_with_the_tokens_that_see_them(scale):
+    c = two_tokens()
+    at = 1165 - int(c.pos0[0])
+    c.t["wscales"][0, at] = scale
+    c.t["wcodes"][0, at, 0::2] = 0x7E       # 448
+    c.t["wcodes"][0, at, 1::2] = 0xFE       # -448
+    c.attend()
+    assert status() == 0
+    c.check_attention([(0, 1)])
