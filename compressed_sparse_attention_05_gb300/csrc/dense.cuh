@@ -32,7 +32,8 @@ __device__ __forceinline__ int64_t dense_shift(const DenseArgs& a, int b) {
 // What one query token sees.
 struct DenseRow {
   int t;          // raw position
-  int nv;         // entries j < nv (and, with a document mask, first token >= doc)
+  int nv;         // entries j < nv whose last token is at or before `last` (without entry_pos: all of them)
+  int last;       // and, with a document mask, whose first token is at or after doc
   int doc;        // raw position at which the token's document starts
   int w_lo, w_n;  // window rows: raw positions w_lo .. w_lo + w_n - 1
 };
@@ -44,9 +45,14 @@ __device__ __forceinline__ DenseRow dense_row(const DenseArgs& a, int b, int i, 
   r.doc = a.doc_start ? max(0, a.doc_start[row]) : 0;
   int64_t last = (int64_t)r.t + 1;   // tokens the row may see
   if (a.prefix_len && r.t >= 0) last = max(last, (int64_t)a.prefix_len[b]);
-  const int64_t v = (last < 0 ? 0 : last >> 2) - shift;
+  // Evictions fill holes with newer entries, so that with entry_pos an index says nothing about the position.
+  const int64_t v = a.entry_pos ? n_ent : (last < 0 ? 0 : last >> 2) - shift;
   r.nv = (int)max((int64_t)0, min(v, (int64_t)n_ent));
-  if (r.t < 0) r.nv = 0;
+  r.last = (int)min(last - 1, (int64_t)INT_MAX);
+  if (r.t < 0) {
+    r.nv = 0;
+    r.last = INT_MIN;
+  }
   const int64_t lo = max(max((int64_t)r.doc, (int64_t)r.t - a.W + 1), (int64_t)max(pos0, 0));
   const int64_t hi = min((int64_t)r.t, (int64_t)pos0 + a.swa_cap - 1);
   r.w_lo = (int)lo;

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_dense_attn_plain(DenseArgs a, u
     __syncthreads();
     load_entries(a, b, e0, n_ent, shift, tile, pos, slots, status);
     const int64_t p = pos[lane];
-    attend(e0 + lane < r.nv && p != INT64_MIN && p - 3 >= r.doc, dense_distance(r.t, p));
+    attend(e0 + lane < r.nv && p != INT64_MIN && p <= r.last && p - 3 >= r.doc, dense_distance(r.t, p));
   }
   if (!live) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_entry_weights_plain(DenseArgs a
     float w = 0.f;
     for (int i = 0; i < a.Tq; ++i) {
       const DenseRow r = dense_row(a, b, i, n_ent, shift, 0);
-      const bool seen = e0 + lane < r.nv && p != INT64_MIN && p - 3 >= r.doc;
+      const bool seen = e0 + lane < r.nv && p != INT64_MIN && p <= r.last && p - 3 >= r.doc;
       for (int h = warp; h < a.Hq; h += kWarps) {
         const int64_t row = ((int64_t)b * a.Tq + i) * a.Hq + h;
         __syncwarp();

@@ -105,9 +105,9 @@ template <> struct Stages<0> { static constexpr int K = 3, V = 3; };
 struct Segment {            // what the roles need to know of the current tile
   int b, nw, c_hi;          // window chunks; entry chunks end at c_hi
   int n_chunks;
-  int e_lo, e_hi;           // entries any row of the tile sees
+  int e_lo, e_hi;           // entries any row of the tile may see
   int w_lo, w_hi;           // window rows any row sees (raw positions, inclusive)
-  int all_lo, all_hi;       // entries every row sees
+  int all_lim, all_doc;     // every row sees the entries that these would let through (as lim and doc of a row)
   int one_t;                // all rows belong to one token
   int one_tok;              // bit k: rows 32 k .. +31 do
   int next_t;               // first row of the tile's second token
@@ -123,9 +123,9 @@ struct Smem {
   float mult[kRowsOf<kMode>];        // logit multiplier: softmax scale * log2(e) * 2^e_r
   float nref[kRowsOf<kMode>];        // attention: -m_ref (kUnset before the row's first key); weights: -lse * log2(e)
   float slope2[kRowsOf<kMode>];      // slope * log2(e)
-  // a row sees entry j if j < nv and its first token is >= doc, and the window row at
-  // position p if 0 <= t - p < W and p >= doc
-  int nv[kRowsOf<kMode>], doc[kRowsOf<kMode>], t[kRowsOf<kMode>];
+  // a row sees an entry if its index (with entry_pos: its last token's position) is <= lim and
+  // its first token is >= doc, and the window row at position p if 0 <= t - p < W and p >= doc
+  int lim[kRowsOf<kMode>], doc[kRowsOf<kMode>], t[kRowsOf<kMode>];
   union {
     float red[4][kRowsOf<kMode>];            // per-lane-quarter maxima / sums of a row over the keys; [0] also: see below
     int qexp[4][kRowsOf<kMode>];             // [1]: largest exponent field of each row of Q, before the products
@@ -873,7 +873,7 @@ struct KeyView {
   bool masked;         // some row may not see the key, or its window row is rescaled (uniform over the warp)
   bool seen;           // a key that some row may see
   int win;             // 1: window row
-  int j, p;            // entry index; raw position (an entry's: of its last token)
+  int at, p;           // what an entry's rows compare with lim; raw position (an entry's: of its last token)
   float kf, ff;        // window row: 2^f and f
 };
 
@@ -885,7 +885,7 @@ template <int kMode>
 __device__ __forceinline__ bool row_sees(const Ctx<kMode>& cx, const KeyView& kv, int r) {
   const Smem<kMode>& sm = cx.sm;
   if (kv.win) return (uint32_t)(sm.t[r] - kv.p) < (uint32_t)cx.a.W && kv.p >= sm.doc[r];
-  return kv.j < sm.nv[r] && kv.p - 3 >= sm.doc[r];
+  return kv.at <= sm.lim[r] && kv.p - 3 >= sm.doc[r];
 }
 
 // Columns c0 .. c0+31 of this thread's key: the logits in the log2 domain as the value
@@ -973,7 +973,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
       sm.seg.b = b;
       sm.seg.pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
       sm.seg.e_lo = INT_MAX; sm.seg.e_hi = 0; sm.seg.w_lo = INT_MAX; sm.seg.w_hi = INT_MIN;
-      sm.seg.all_lo = 0; sm.seg.all_hi = INT_MAX;
+      sm.seg.all_lim = INT_MAX; sm.seg.all_doc = 0;
       sm.seg.next_t = a.Hq - r0 % a.Hq;
       sm.seg.one_tok = 0;
       for (int k = 0; k < kRowsOf<kMode> / 32; ++k)
@@ -984,7 +984,8 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
     soft_sync();
     if (st < kRowsOf<kMode>) {
       const bool live = r0 + st < rows;
-      DenseRow r{INT_MIN, 0, INT_MAX, 0, 0};   // no row: it sees nothing, wherever t - p wraps to
+      DenseRow r{INT_MIN, 0, INT_MIN, INT_MAX, 0, 0};   // no row: it sees nothing, wherever t - p wraps to
+      int lim = INT_MIN;
       float slope = 0.f, nref = kUnset;
       if (live) {
         const int i = (r0 + st) / a.Hq, h = (r0 + st) % a.Hq;
@@ -998,8 +999,9 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
           atomicMin(&sm.seg.w_lo, r.w_lo);
           atomicMax(&sm.seg.w_hi, r.w_lo + r.w_n - 1);
         }
-        atomicMax(&sm.seg.all_lo, a.entry_pos && r.doc > 0 ? INT_MAX : lo);   // by position: no chunk is free of masks
-        atomicMin(&sm.seg.all_hi, r.nv);
+        lim = a.entry_pos ? r.last : r.nv - 1;
+        atomicMin(&sm.seg.all_lim, lim);
+        atomicMax(&sm.seg.all_doc, r.doc);
         if (a.slopes) slope = a.slopes[h];
         if (kWeights<kMode>) {
           const float lse = a.lse_in[(int64_t)b * rows + r0 + st];
@@ -1008,7 +1010,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
       } else if (kWeights<kMode>) {
         nref = -INFINITY;
       }
-      sm.nv[st] = r.nv;
+      sm.lim[st] = lim;
       sm.doc[st] = r.doc;
       sm.t[st] = r.t;
       sm.slope2[st] = slope * kLog2e;
@@ -1044,7 +1046,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
       kv.win = k < sg.nw;
       kv.kf = 1.f;
       kv.ff = 0.f;
-      kv.j = 0;
+      kv.at = 0;
       *slot = -1;
       if (kv.win) {
         const int64_t p = (int64_t)sm.seg.w_lo + (int64_t)k * kChunk + key;
@@ -1059,13 +1061,13 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
           }
         }
       } else {
-        const int e0 = entry_of(i) - key;
-        kv.j = entry_of(i);
-        kv.seen = kv.j >= sg.e_lo && kv.j < sg.e_hi && page >= 0 && page < a.n_pages;
-        if (kv.seen) *slot = (int64_t)page * kPage + (kv.j & (kPage - 1));
+        const int j = entry_of(i);
+        kv.seen = j >= sg.e_lo && j < sg.e_hi && page >= 0 && page < a.n_pages;
+        if (kv.seen) *slot = (int64_t)page * kPage + (j & (kPage - 1));
         kv.p = a.entry_pos && kv.seen ? max(__ldg(a.entry_pos + *slot), INT_MIN + 3)
-                                      : kv.j + shift32 < (1 << 29) ? 4 * (kv.j + shift32) + 3 : INT_MAX;
-        kv.masked = e0 < sm.seg.all_lo || e0 + kChunk > sm.seg.all_hi || __any_sync(0xffffffffu, !kv.seen);
+                                      : j + shift32 < (1 << 29) ? 4 * (j + shift32) + 3 : INT_MAX;
+        kv.at = a.entry_pos ? kv.p : j;
+        kv.masked = __any_sync(0xffffffffu, !kv.seen || kv.at > sm.seg.all_lim || kv.p - 3 < sm.seg.all_doc);
       }
       page = page_ahead(i + kStep);
       return kv;

@@ -103,10 +103,11 @@
  *      l = cap * tanh(softmax_scale * q . k / cap) (cap = 0: no cap), minus
  *      slopes[h] * |t - p| with p the raw position of the key (an entry's: of
  *      its last token).  A key is visible to the token at raw position t if
- *        - entry j: j + shift completes by then, 4 (j + shift) + 3 <= t, where
- *          shift is the number of entries evicted so far (R16); tokens of the
- *          prefix (t < prefix_len) see every entry with 4 (j + shift) + 3 <
- *          prefix_len instead;
+ *        - entry: its last token lies at or before t; tokens of the prefix (t <
+ *          prefix_len) see every entry whose last token lies below prefix_len
+ *          instead.  The last token of entry j is at entry_pos where the call
+ *          gets it (an evicted cache's entries lie in any order, R16), else at
+ *          4 (j + shift) + 3, shift the number of entries evicted so far;
  *        - window row: raw position in max(0, t-W+1) .. t, held by the buffer
  *          (the window stays causal in the prefix too);
  *        - and, with a document mask, all of its tokens lie at or after
@@ -456,7 +457,11 @@ int csa2_entry_weights(const csa2_dims* dims, const csa2_cache* cache, const csa
  * After an eviction csa2_index_topk, csa2_sparse_attn and the other calls that
  * know nothing of shift take q_pos[b][i] - 4 shift[b] in the place of q_pos
  * (their visible count is then min(n_entries, floor((t+1)/4) - shift)) and
- * win->pos0[b] - 4 shift[b] in the place of pos0, with keep >= W / 4. */
+ * win->pos0[b] - 4 shift[b] in the place of pos0, with keep >= W / 4.  They go
+ * by index, so they are right for query tokens that see all that the eviction
+ * left, q_pos[b][i] >= 4 (keep + shift[b]) - 1 (evict, append, then ask); an
+ * older token would be shown entries of its future.  csa2_dense_attn and
+ * csa2_entry_weights go by entry_pos and take any token. */
 size_t csa2_evict_workspace_size(const csa2_dims* dims, int32_t max_entries);
 int csa2_evict(const csa2_dims* dims, const csa2_cache* cache, const csa2_bounded* bounded,
                int32_t* n_entries, int32_t keep, int32_t n_sink, int32_t n_recent,

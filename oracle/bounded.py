@@ -3,11 +3,11 @@
 Test infrastructure only (see ``oracle/__init__.py``).  No counterpart on the
 pages; the definitions are readings R14-R16 of include/csa2.h.
 
-* visible keys: entry j of a cache that ``shift`` entries left is complete at
-  raw position 4 (j + shift) + 3; a token sees the entries complete at its own
-  position (a token of the prefix: before the prefix ends), the window rows
+* visible keys: a token sees the entries whose last token is at or before its own
+  position (a token of the prefix: below the prefix's end), the window rows
   max(0, t-W+1) .. t, and with a document mask only keys whose tokens all lie
-  in its document;
+  in its document.  An eviction moves entries, so their positions say which they
+  are (``visible``); entries in order lie at 4 (j + shift) + 3 (``visible_count``);
 * logits: tau q.k, capped as cap * tanh(. / cap), minus slope_h |t - p|;
 * weights: decay * old + sum over tokens and heads of exp(logit - lse);
 * eviction: first n_sink and newest n_recent positions stay, then the highest
@@ -19,7 +19,7 @@ import numpy as np
 
 
 def visible_count(n_entries: int, shift: int, t: int, prefix_len: int = 0) -> int:
-    """Entries 0 .. count-1 that the token at raw position t may see (before a document mask)."""
+    """Entries in order: 0 .. count-1 are those that the token at raw position t may see (before a document mask)."""
     if t < 0:
         return 0
     sees = max(t + 1, prefix_len) if t < prefix_len else t + 1   # raw tokens 0 .. sees-1
@@ -28,6 +28,13 @@ def visible_count(n_entries: int, shift: int, t: int, prefix_len: int = 0) -> in
     if done > 0:
         count = min(done, n_entries)
     return count
+
+
+def visible(pos: np.ndarray, t: int, prefix_len: int = 0) -> np.ndarray:
+    """Indices of the entries, their last tokens at raw positions pos, that the token at raw position t may see."""
+    if t < 0:
+        return np.zeros(0, np.int64)
+    return np.flatnonzero(np.asarray(pos, np.int64) <= max(t, prefix_len - 1))
 
 
 def logits(q: np.ndarray, keys: np.ndarray, tau: float, t: int, pos: np.ndarray, cap: float = 0.0, slopes=None):
