@@ -109,7 +109,7 @@ struct Segment {            // what the roles need to know of the current tile
   int w_lo, w_hi;           // window rows any row sees (raw positions, inclusive)
   int all_lim, all_doc;     // every row sees the entries that these would let through (as lim and doc of a row)
   int one_t;                // all rows belong to one token
-  int one_tok;              // bit k: rows 32 k .. +31 do
+  int one_tok;              // bit k: rows 32 k .. +31 do, and none of the tile's adds nothing
   int next_t;               // first row of the tile's second token
   int pos0;
 };
@@ -1000,13 +1000,18 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
           atomicMax(&sm.seg.w_hi, r.w_lo + r.w_n - 1);
         }
         lim = a.entry_pos ? r.last : r.nv - 1;
+        if (kWeights<kMode>) {
+          const float lse = a.lse_in[(int64_t)b * rows + r0 + st];
+          nref = -lse * kLog2e;
+          if (isinf(lse)) {       // the row adds nothing: masks of its own, since a NaN key must not reach it either
+            nref = -INFINITY;
+            lim = INT_MIN;
+            sm.seg.one_tok = 0;
+          }
+        }
         atomicMin(&sm.seg.all_lim, lim);
         atomicMax(&sm.seg.all_doc, r.doc);
         if (a.slopes) slope = a.slopes[h];
-        if (kWeights<kMode>) {
-          const float lse = a.lse_in[(int64_t)b * rows + r0 + st];
-          nref = isinf(lse) ? -INFINITY : -lse * kLog2e;   // a row that saw nothing adds nothing
-        }
       } else if (kWeights<kMode>) {
         nref = -INFINITY;
       }

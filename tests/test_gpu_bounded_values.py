@@ -111,6 +111,45 @@ def test_a_tile_of_nan_keys_before_good_ones(d):
     c.check_attention([(0, 1)])
 
 
+# ---- infinite lse beside a NaN key -------------------------------------------------------
+@pytest.mark.parametrize("kw", [dict(), dict(d=64), dict(Hq=128), dict(Tq=4, Hq=64, q_pos=[[1170, 1180, 1190, 1199]],
+                                                                       docs=[[0, 1180, 1180, 1180]])],
+                         ids=["one_tile", "d64", "hq128", "tiles"])
+def test_rows_of_infinite_lse_add_nothing_beside_a_nan_key(kw):
+    """The first token sees the NaN entry, but its lse is infinite in every head."""
+    c = two_tokens(**kw)
+    c.attend()
+    lse = c.lse.clone()
+    poison_entry(c, 200)
+    lse[0, 0, 0::2] = float("inf")
+    lse[0, 0, 1::2] = float("-inf")
+    out = torch.zeros(c.n_pages * 64, device="cuda")
+    c.weigh(lse, None, out)
+    assert status() == 0
+    assert out.isfinite().all()
+    c.check_weights(lse, None, out)
+
+
+@pytest.mark.parametrize("d", [512, 64])
+def test_one_head_of_infinite_lse_beside_a_nan_key(d):
+    c = two_tokens(d=d)
+    c.attend()
+    lse = c.lse.clone()
+    lse[0, 0, 5] = float("inf")
+    lse[0, 1, 2] = float("-inf")
+    out = torch.zeros(c.n_pages * 64, device="cuda")
+    c.weigh(lse, None, out)
+    c.check_weights(lse, None, out)
+    poison_entry(c, 200)
+    again = torch.zeros(c.n_pages * 64, device="cuda")
+    c.weigh(lse, None, again)
+    assert status() == 0
+    at = int(c.slots[0][200])
+    assert again[at].isnan()            # the token's other heads see it
+    again[at] = out[at]
+    assert torch.equal(again, out)
+
+
 # ---- window rows of enormous scales --------------------------------------------------------
 @pytest.mark.parametrize("scale", [2.0 ** 112, 2.0 ** 125])
 def test_rows_past_the_operand_range_stay_with_the_tokens_that_see_them(scale):
