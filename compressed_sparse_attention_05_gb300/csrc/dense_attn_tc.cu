@@ -85,8 +85,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;
 template <int kMode> struct Cols { static constexpr uint32_t S = 0, K = 2 * kMode; static constexpr int ring = 4; };
 template <> struct Cols<0> { static constexpr uint32_t S = 256, K = 320; static constexpr int ring = 3; };
-constexpr float kRescaleLog2 = 8.f;       // a reference maximum moves only beyond this growth
-constexpr float kUnset = 3e38f;           // -m_ref of a row without keys: any finite logit outgrows it, -inf stays -inf
+// P = 2^(l - m_ref + kTopLog2): fp16 then holds a weight down to 2^-(24 + kTopLog2) of the reference, so that what
+// a long tail loses, at most 2^-32 of the reference per key, is far below O's bf16 step (2^-25 per key, without
+// the factor, took 0.6% of the mass of 262,144 keys at 2^-25.3 beside a peak).  O and l carry the same factor.
+constexpr float kTopLog2 = 7.f, kBottom = 1.f / 128;   // and 2^-kTopLog2
+constexpr float kRescaleLog2 = 8.f;       // a reference maximum moves only beyond this growth: P <= 2^15
+constexpr float kUnset = 3e38f;           // kTopLog2 - m_ref of a row without keys: any finite logit outgrows it, -inf stays -inf
 constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, then m and l
 
 constexpr int kQuarter = 128;                         // channels of a quarter
@@ -121,7 +125,7 @@ struct Smem {
   uint16_t v[kWeights<kMode> ? 8 : kVSlots * kChunk * kQuarter];
   uint16_t p[kWeights<kMode> ? 8 : kChunk * kRowsOf<kMode>];
   float mult[kRowsOf<kMode>];        // logit multiplier: softmax scale * log2(e) * 2^e_r
-  float nref[kRowsOf<kMode>];        // attention: -m_ref (kUnset before the row's first key); weights: -lse * log2(e)
+  float nref[kRowsOf<kMode>];        // attention: kTopLog2 - m_ref (kUnset before the row's first key); weights: -lse * log2(e)
   float slope2[kRowsOf<kMode>];      // slope * log2(e)
   // a row sees an entry if its index (with entry_pos: its last token's position) is <= lim and
   // its first token is >= doc, and the window row at position p if 0 <= t - p < W and p >= doc
@@ -1131,7 +1135,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
           top = fmaxf(top, fmaxf(fmaxf(x[4 * j4] + z.x, x[4 * j4 + 1] + z.y), fmaxf(x[4 * j4 + 2] + z.z, x[4 * j4 + 3] + z.w)));
         }
         const bool seen_abort = !ok || *abort != 0;
-        if (half_or(half, top > kRescaleLog2 || seen_abort)) {
+        if (half_or(half, top > kTopLog2 + kRescaleLog2 || seen_abort)) {
           if (half_or(half, seen_abort)) break;   // (a wait that fails below is met by the next vote)
           // maxima of the half's 32 rows over the 128 keys
           float mine = -INFINITY;
@@ -1148,12 +1152,13 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
             const float m = fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]), fmaxf(sm.red[2][r], sm.red[3][r]));
             const float no = sm.nref[r];
             float al = 1.f;
-            if (m + no > kRescaleLog2) {
+            if (m + no > kTopLog2 + kRescaleLog2) {
+              const float now = kTopLog2 - m;
               if (no != kUnset) {
-                al = ex2(-no - m);
+                al = ex2(now - no);
                 need = true;
               }
-              sm.nref[r] = -m;
+              sm.nref[r] = now;
             }
             sm.red[0][r] = al;
           }
@@ -1181,7 +1186,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
           }
           half_sync(half);                     // red is read; the next vote may come
         }
-        // ---- P = exp2(l - m_ref), rounded to fp16 for the value product
+        // ---- P, rounded to fp16 for the value product
         const float pf = pow2i(-(int)kv.ff);   // the normaliser adds p = 2^-f (2^f p)
         uint32_t pk[16];
 #pragma unroll
@@ -1219,11 +1224,11 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
       soft_sync();
       if (st < kRowsOf<kMode>) {
         const float l = (sm.red[0][st] + sm.red[1][st]) + (sm.red[2][st] + sm.red[3][st]);
-        const float m = sm.nref[st] == kUnset ? -INFINITY : -sm.nref[st];
+        const float m = sm.nref[st] == kUnset ? -INFINITY : -sm.nref[st];   // log2 of the unit of l and O
         sm.red[0][st] = l == 0.f ? 0.f : 1.f / l;   // the factor of O
         if (sp.first && sp.last) {
           if (a.lse && r0 + st < rows)
-            a.lse[(int64_t)b * rows + r0 + st] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            a.lse[(int64_t)b * rows + r0 + st] = l == 0.f ? -INFINITY : (m + kTopLog2 + log2f(l * kBottom)) * kLn2;
         } else {
           float* ml = cx.pl.parts + (int64_t)(2 * blockIdx.x + (sp.first ? 1 : 0)) * kPartFloats + kRowsOf<kMode> * kD;
           ml[st] = m;
@@ -1543,7 +1548,8 @@ __global__ void __launch_bounds__(128 * kMergeGroups) k_dense_merge(DenseArgs a,
     L = warp_sum(L);
     const float inv = L == 0.f ? 0.f : 1.f / L;
     for (int q = tid; q <= count; q += 32) s_fac[q] *= inv;
-    if (a.lse && tid == 0) a.lse[(int64_t)b * rows + row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (a.lse && tid == 0)
+      a.lse[(int64_t)b * rows + row] = L == 0.f ? -INFINITY : (M + kTopLog2 + log2f(L * kBottom)) * kLn2;
   }
   __syncthreads();
   const int n = s_count, grp = tid >> 7, c4 = tid & 127;

@@ -1,11 +1,15 @@
 """Values that the whole-cache kernels must carry through or keep apart: NaN, infinite lse, scales at the end of
 their range, a long tail beside a peak."""
+import math
 
+import numpy as np
 import pytest
 import torch
 
 from bounded_case import Case
 from compressed_sparse_attention_05_gb300 import abi, build
+from oracle import bounded as OB
+from oracle import formats as F
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +165,48 @@ def test_rows_past_the_operand_range_stay_with_the_tokens_that_see_them(scale):
     c.attend()
     assert status() == 0
     c.check_attention([(0, 1)])
+
+
+# ---- a peak and a long tail ---------------------------------------------------------------
+def test_a_long_tail_beside_a_peak():
+    """One window row, and 100,000 entries of about 2^-25.5 of its weight each, in tiles that one SM walks alone:
+    0.2% of the mass, and all of it in the channels where the window row is zero.
+
+    The error of O in such a channel, of a value of about 2e-3: its rounding, 2^-8 of it, and that of the tail's
+    weights.  Those are P = 2^7 w with w in units of the reference, above 2^-19 for a w above 2^-26, and fp16's
+    step there is 2^-24: at most 2^-25 / 2^-19 = 2^-6 of each weight, whatever their number.  Logit errors and the
+    rest of the kernel's bounds (2^-11 + 2 e + 2^-20) are below 2^-10."""
+    n, Tq = 100000, 160
+    c = Case(seed=14, Tq=Tq, Hq=64, lens=(64,), W=1, q_pos=[[4 * n - 1] * Tq], tau=25.5 * math.log(2) / 16)
+    g = torch.Generator().manual_seed(15)
+    x = torch.randn(n, 512, generator=g)
+    x[:, :16] = 1.5                                              # scale 1/4, code 6: exact
+    x[:, 32:] = x[:, 32:].abs()
+    codes, scales = F.mxfp4_pack(x.numpy().astype(np.float32))
+    pages = (n + 63) // 64
+    c.lens, c.n_pages, c.max_entries = [n], pages, n
+    c.table = np.random.RandomState(16).permutation(pages).astype(np.int32)[None, :]
+    c.slots = [c.table[0, np.arange(n) // 64].astype(np.int64) * 64 + np.arange(n) % 64]
+    c.codes, c.scales = torch.zeros(pages * 64, 256, dtype=torch.uint8), torch.zeros(pages * 64, 32, dtype=torch.uint8)
+    c.codes[c.slots[0]], c.scales[c.slots[0]] = torch.from_numpy(codes), torch.from_numpy(scales)
+    w = np.zeros((1, 512), np.float32)
+    w[0, :16] = 2.5
+    wc, ws = F.fp8_pack(w)
+    c.wcodes[0, 0], c.wscales[0, 0] = torch.from_numpy(wc[0]), float(ws[0])
+    c.Q = torch.zeros(1, Tq, 64, 512, dtype=torch.bfloat16)
+    c.Q[..., :16] = 1.0
+    c.Q[..., 16] = (torch.rand(1, Tq, 64, generator=g) * 0.05).bfloat16()  # the logits differ a little
+    c._device()
+    c.attend()
+    assert status() == 0
+    keys, pos = c.keys(0)
+    for i, h in ((0, 0), (77, 13), (159, 63)):
+        _, rows, xl, e = c.one(0, i, (keys, pos))
+        o, z = OB.attention(xl[h:h + 1], rows)
+        wt = np.exp(xl[h] - z[0])
+        assert wt[:-1].max() < 2.0 ** -25 and wt[:-1].min() > 2.0 ** -26 and wt[-1] > 0.99
+        got = c.O[0, i, h].double().cpu().numpy()
+        tail = o[0, 32:]                                         # the window row is zero here
+        assert tail.min() > 1e-3
+        assert np.max(np.abs(got[32:] - tail) / tail) < 2.0 ** -8 + 2.0 ** -6 + 2.0 ** -10
+        assert abs(float(c.lse[0, i, h]) - z[0]) < e[h].max() + 2.0 ** -20 + 2.0 ** -23 * abs(z[0])
