@@ -988,7 +988,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
     soft_sync();
     if (st < kRowsOf<kMode>) {
       const bool live = r0 + st < rows;
-      DenseRow r{INT_MIN, 0, INT_MIN, INT_MAX, 0, 0};   // no row: it sees nothing, wherever t - p wraps to
+      DenseRow r{-1, 0, INT_MIN, INT_MAX, 0, 0};        // no row: it sees nothing
       int lim = INT_MIN;
       float slope = 0.f, nref = kUnset;
       if (live) {
@@ -1021,7 +1021,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
       }
       sm.lim[st] = lim;
       sm.doc[st] = r.doc;
-      sm.t[st] = r.t;
+      sm.t[st] = max(r.t, -1);   // any t below 0 sees nothing, and from -1 no t - p wraps around into a window
       sm.slope2[st] = slope * kLog2e;
       sm.nref[st] = nref;
     }
