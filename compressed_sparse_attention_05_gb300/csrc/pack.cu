@@ -197,12 +197,17 @@ __device__ __forceinline__ void norm_rope_pack_entry(const LatentSource& src, in
   const int e = first_entry[b] + i;
   const int64_t slot = entry_slot(page_table, max_pages, n_pages, b, e, status);
   if (slot < 0) return;
+  // an entry of a bounded cache keeps the position it would have had without evictions
+  const int shift = bd.shift ? bd.shift[b] : 0;
+  const uint64_t pos = 4ull * ((uint64_t)e + (uint64_t)max(0, shift)) + 3ull;
+  if (bd.entry_pos && (shift < 0 || pos > INT_MAX)) {   // no such position (of the whole warp's entry)
+    if (lane == 0) raise_status(status, CSA2_STATUS_BAD_COUNT);
+    return;
+  }
 
   const bool has = lane < d / 16;
   float v[16];
   load_latent(src, m, has, lane, v);
-  // an entry of a bounded cache keeps the position it would have had without evictions
-  const uint64_t pos = 4ull * ((uint64_t)e + (bd.shift ? (uint64_t)max(0, bd.shift[b]) : 0ull)) + 3ull;
   if (lane == 0 && bd.entry_pos) bd.entry_pos[slot] = (int32_t)pos;
   if (lane == 0 && bd.weight) bd.weight[slot] = 0.f;
   norm_rope_row(v, has, d, r, gamma, eps, pos, rope, row, lane);

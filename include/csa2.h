@@ -469,7 +469,9 @@ int csa2_evict(const csa2_dims* dims, const csa2_cache* cache, const csa2_bounde
 
 /* csa2_compress_pack into a bounded cache: entry first_entry[b] + i (an index)
  * is rotated at position 4 (first_entry[b] + shift[b] + i) + 3, which entry_pos
- * receives, and starts with weight 0.  Workspace as for csa2_compress_pack. */
+ * receives, and starts with weight 0.  An entry whose shift is negative or whose
+ * position passes 2^31 - 1 is not written and raises CSA2_STATUS_BAD_COUNT.
+ * Workspace as for csa2_compress_pack. */
 int csa2_compress_pack_bounded(const uint16_t* hidden, int32_t B, int32_t T, int32_t H,
                                const uint16_t* W, const float* gamma, float eps, float rope_base,
                                const uint16_t* W_idx, const int32_t* first_entry,

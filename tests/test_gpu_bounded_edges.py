@@ -4,6 +4,7 @@ import torch
 
 from bounded_case import Case
 from compressed_sparse_attention_05_gb300 import abi, build
+from test_gpu_bounded_use import Cache
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +30,21 @@ def test_a_token_at_the_most_negative_position_sees_no_window():
     assert status() == 0
     assert not c.O[0, 0].any() and torch.all(c.lse[0, 0] == float("-inf"))
     c.check_attention([(0, 1)])
+
+
+def test_entries_whose_position_does_not_fit_are_not_written():
+    """Sequence 0's last 20 entries would lie past position 2^31 - 1; sequence 1's shift is negative."""
+    c = Cache(23)
+    c.t["shift"].copy_(torch.tensor([2 ** 29 - 40, -3], dtype=torch.int32))
+    c.t["n"].copy_(torch.tensor([10, 64], dtype=torch.int32))
+    names = ("codes", "scales", "pos")
+    before = [c.t[k].clone() for k in names] + [c.idx_k.clone(), c.weight.clone()]
+    c.compress(50)
+    assert status() == abi.STATUS_BAD_COUNT
+    wrote = torch.from_numpy(c.page_slots[0][10:40]).cuda()
+    assert c.t["pos"][wrote].tolist() == [4 * (2 ** 29 - 40 + e) + 3 for e in range(10, 40)]
+    assert not c.weight[wrote].any() and not torch.equal(c.t["codes"][wrote], before[0][wrote])
+    rest = torch.ones(c.n_pages * 64, dtype=torch.bool, device="cuda")
+    rest[wrote] = False
+    for now, old in zip([c.t[k] for k in names] + [c.idx_k, c.weight], before):
+        assert torch.equal(now[rest], old[rest])
