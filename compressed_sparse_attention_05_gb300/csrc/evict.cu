@@ -99,10 +99,12 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
   __shared__ uint32_t group[3][kWarps];  // sums of 64 bins
   __shared__ uint32_t sums[kWarps][2];
   __shared__ uint32_t pub[3];
-  __shared__ uint32_t found[3];
+  __shared__ uint32_t found[4];
+  __shared__ uint32_t no_page;           // an entry of this CTA's share lies behind a bad page (read by the others)
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
+  if (tid == 0) no_page = 0;
   pdl_wait();
   const int b = (int)blockIdx.x / n_cl;
   const int rank = n_cl > 1 ? (int)cl_rank() : 0;
@@ -143,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
     for (int i = 0; i < kAhead; ++i) {
       const int j = j0 + i * kThreads;
       if (j >= count) break;
+      if (slot[i] == kNone) no_page = 1;
       const uint32_t k = slot[i] == kNone ? 0u
                          : pos[i] < 4ll * a.n_sink || pos[i] >= first_recent ? 0xFFFFFFFFu
                                                                               : weight_key(w[i]);
@@ -197,7 +200,18 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
         found[2] = second ? c1 : c0;
       }
     }
+    // beside it: a survivor could not move to a hole without a page, so such a sequence stays as it is
+    if (pass == 0 && warp == 1) {
+      const bool none = n_cl == 1 ? no_page != 0 : lane < n_cl && cl_load(&no_page, lane) != 0;
+      const uint32_t any = __any_sync(0xffffffffu, none);
+      if (lane == 0) found[3] = any;
+    }
     __syncthreads();
+    if (pass == 0 && found[3]) {         // the same in every CTA of the cluster
+      if (n_cl > 1) cl_sync();           // none leaves while another reads its shared memory
+      if (rank == 0 && tid == 0) ws.n_moves[b] = 0;
+      return;
+    }
     prefix |= found[0] << sh;
     mask |= (uint32_t)(nb - 1) << sh;
     need = found[1];

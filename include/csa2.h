@@ -447,12 +447,15 @@ int csa2_entry_weights(const csa2_dims* dims, const csa2_cache* cache, const csa
  * inside the sequence's own pages, sets n_entries[b] = keep and adds the number
  * evicted to shift[b].  n_entries is the array that cache->n_entries points to,
  * writable.  Slots at index >= keep keep their bytes; pages that lie wholly
- * there are free for reuse once the call is done.  keep >= 1, n_sink + n_recent <= keep.  A
- * sequence whose n_entries is negative, above max_entries or past its page
- * table, or whose shift is negative, stays as it is and raises
- * CSA2_STATUS_BAD_COUNT (with max_entries <= keep the call returns at once and
- * looks at no count).  Sequences must not share pages.  NaN weights are not
- * supported.  dims: B, d, Di, idx_dtype, max_pages, kv_format are used.
+ * there are free for reuse once the call is done.  keep >= 1, n_sink +
+ * n_recent <= keep.  A sequence whose n_entries is negative, above max_entries
+ * or past its page table, or whose shift is negative, stays as it is and raises
+ * CSA2_STATUS_BAD_COUNT; one that would be cut but has a page-table entry out
+ * of range stays as it is and raises CSA2_STATUS_BAD_PAGE (with max_entries <=
+ * keep the call returns at once and looks at no count and no page).  Sequences
+ * must not share pages.  NaN weights are not supported.  dims: B, d, Di,
+ * idx_dtype, max_pages, kv_format are used.  Needs csa2_evict_workspace_size()
+ * bytes of workspace, which calls that can overlap must not share.
  *
  * After an eviction csa2_index_topk, csa2_sparse_attn and the other calls that
  * know nothing of shift take q_pos[b][i] - 4 shift[b] in the place of q_pos

@@ -5,6 +5,7 @@ import torch
 from bounded_case import Case
 from compressed_sparse_attention_05_gb300 import abi, build
 from test_gpu_bounded_use import Cache
+from test_gpu_evict import Pool
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,15 @@ def test_entries_whose_position_does_not_fit_are_not_written():
     rest[wrote] = False
     for now, old in zip([c.t[k] for k in names] + [c.idx_k, c.weight], before):
         assert torch.equal(now[rest], old[rest])
+
+
+@pytest.mark.parametrize("lens,keep,page", [([300, 280], 200, 0), ([300, 280], 200, 4), ([9000, 20000], 5000, 60)],
+                         ids=["below_keep", "above_keep", "cluster"])
+def test_a_bad_page_leaves_the_sequence_alone(lens, keep, page):
+    """No survivor may be lost to a hole that cannot be written."""
+    p = Pool(24, lens)
+    p.t["table"][0, page] = p.n_pages
+    p.evict(keep, 4, 10)
+    assert status() == abi.STATUS_BAD_PAGE
+    p.expect(keep, 4, 10, untouched=(0,))
+    assert p.lens == [lens[0], keep]
