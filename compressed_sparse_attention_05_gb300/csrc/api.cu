@@ -753,7 +753,9 @@ static int dense_args(const csa2_dims* dm, const csa2_cache* c, const csa2_bound
   REQUIRE((int64_t)dm->Tq * dm->Hq < (1ll << 30) && dm->B <= 65535, "too many query tokens or sequences");
   REQUIRE(softmax_scale == softmax_scale && softmax_scale - softmax_scale == 0.f, "softmax_scale must be finite");
   if (mods) {
-    REQUIRE(mods->logit_cap >= 0.f && mods->logit_cap - mods->logit_cap == 0.f, "logit_cap must be finite and >= 0");
+    // the kernels work with cap * log2(e) and its reciprocal: both must be finite
+    REQUIRE(mods->logit_cap == 0.f || (mods->logit_cap >= 0x1p-126f && mods->logit_cap <= 0x1p127f),
+            "logit_cap must be 0 or in 2^-126..2^127 (got %g)", (double)mods->logit_cap);
     if (mods->slopes) REQUIRE_IPTR(mods->slopes);
     if (mods->doc_start) REQUIRE_IPTR(mods->doc_start);
     if (mods->prefix_len) REQUIRE_IPTR(mods->prefix_len);

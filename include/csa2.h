@@ -406,7 +406,7 @@ typedef struct csa2_bounded {
 
 /* Changes to the logits and to what is visible (R14); NULL or zeros: none. */
 typedef struct csa2_score_mods {
-  float logit_cap;           /* > 0: l = cap * tanh(l / cap)                    */
+  float logit_cap;           /* 2^-126 .. 2^127: l = cap * tanh(l / cap); 0: none */
   const float* slopes;       /* fp32 [Hq]: l -= slopes[h] * |t - p|             */
   const int32_t* doc_start;  /* [B][Tq] raw position where the token's document starts */
   const int32_t* prefix_len; /* [B] tokens at positions below it see each other */

@@ -210,3 +210,17 @@ def test_a_long_tail_beside_a_peak():
         assert tail.min() > 1e-3
         assert np.max(np.abs(got[32:] - tail) / tail) < 2.0 ** -8 + 2.0 ** -6 + 2.0 ** -10
         assert abs(float(c.lse[0, i, h]) - z[0]) < e[h].max() + 2.0 ** -20 + 2.0 ** -23 * abs(z[0])
+
+
+# ---- the ends of the cap's range -------------------------------------------------------------
+@pytest.mark.parametrize("cap", [2.0 ** 127, 1e38, 2.0 ** -126])
+@pytest.mark.parametrize("d", [512, 64])
+def test_the_largest_and_smallest_caps(d, cap):
+    """The largest ones change no logit; under the smallest every logit is 0 to within 2^-125.  (x / cap may be
+    subnormal: steps of 2^-149, which cap makes 2^-21.4 of a logit in the log2 domain, well within the bound.)"""
+    c = two_tokens(d=d, cap=cap)
+    c.t["Q"][0, 1, 2] = 0                    # logits of exactly 0 too
+    c.Q[0, 1, 2] = 0
+    c.attend()
+    assert status() == 0
+    c.check_attention()
