@@ -335,7 +335,8 @@ def csa2_entry_weights_workspace_size(dims: Dims, max_entries: int) -> int:
 def csa2_entry_weights(dims: Dims, cache: Cache, Q, q_pos, lse, softmax_scale, decay, weight_in, weight_out,
                        max_entries, ws=None, mods: Optional[ScoreMods] = None, bounded: Optional[Bounded] = None,
                        stream=None):
-    """weight_out = decay * weight_in + the softmax weight of every entry, summed over tokens and heads."""
+    """weight_out = decay * weight_in + the softmax weight of every entry, summed over tokens and heads
+    (without tokens, Tq = 0, it stays as it was)."""
     _check(lib().csa2_entry_weights(C.byref(dims), C.byref(cache), _ref(bounded), _ref(mods), ptr(Q), ptr(q_pos),
                                     ptr(lse), softmax_scale, decay, ptr(weight_in), ptr(weight_out), max_entries,
                                     ptr(ws), _nbytes(ws), stream_handle(stream)))

@@ -431,8 +431,10 @@ int csa2_dense_attn(const csa2_dims* dims, const csa2_cache* cache, const csa2_b
  * Q, q_pos, softmax_scale and mods as given to csa2_dense_attn, lse as it wrote
  * them.  weight_in fp32 [n_pages][64] (NULL: zeros), weight_out fp32
  * [n_pages][64] (may be weight_in): written for the n_entries[b] entries of
- * every sequence, whether a token of the call saw them or not; other slots are
- * left as they were.  Sequences must not share pages.  decay in 0..1.  Sums run
+ * every sequence (but those behind a bad page), whether a token of the call saw
+ * them or not; other slots are left as they were.  A call without query tokens
+ * (Tq = 0) launches nothing and leaves weight_out as it was: no decay, and no
+ * copy of weight_in.  Sequences must not share pages.  decay in 0..1.  Sums run
  * in a fixed order.  Needs csa2_entry_weights_workspace_size() bytes of
  * workspace, which calls that can overlap must not share. */
 size_t csa2_entry_weights_workspace_size(const csa2_dims* dims, int32_t max_entries);

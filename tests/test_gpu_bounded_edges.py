@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from bounded_case import Case
+from bounded_case import SENTINEL, Case
 from compressed_sparse_attention_05_gb300 import abi, build
 from test_gpu_bounded_use import Cache
 from test_gpu_evict import Pool
@@ -19,6 +19,20 @@ def _lib():
 def status():
     torch.cuda.synchronize()
     return abi.csa2_get_status()
+
+
+@pytest.mark.parametrize("d", [512, 64])
+def test_no_query_tokens_leave_the_weights(d):
+    c = Case(seed=21, Tq=1, Hq=8, d=d, lens=(90,))
+    dm = c.dims()
+    dm.Tq = 0
+    cache, bounded, _, mods = c.structs()
+    w_in = torch.rand(c.n_pages * 64, device="cuda")
+    out = torch.full_like(w_in, SENTINEL)
+    launches = abi.lib().csa2_launch_count()
+    abi.csa2_entry_weights(dm, cache, None, None, None, c.tau, 0.5, w_in, out, 90, None, mods=mods, bounded=bounded)
+    assert status() == 0
+    assert abi.lib().csa2_launch_count() == launches and torch.all(out == SENTINEL)
 
 
 def test_a_token_at_the_most_negative_position_sees_no_window():
