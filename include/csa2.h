@@ -397,7 +397,13 @@ int csa2_sparse_attn(const csa2_dims* dims, const csa2_cache* cache, const csa2_
  * State of such a cache, beside csa2_cache (weight and entry_pos lie like the
  * pages, one value per slot; shift has one per sequence).  A cache that no
  * entry was evicted from may go without (NULL, or NULL members): entry j's
- * position is then 4 (j + shift) + 3 and shift is 0. */
+ * position is then 4 (j + shift) + 3 and shift is 0.
+ *
+ * Entries of such a cache are appended by csa2_compress_pack_bounded alone.
+ * csa2_compress_pack, csa2_compress_layers and csa2_layer with hidden != NULL
+ * rotate a new entry at 4 e + 3 with e its index, and write neither entry_pos
+ * nor weight: once entries were evicted they must not be used on it (csa2_cache
+ * does not show that, so they cannot refuse). */
 typedef struct csa2_bounded {
   int32_t* entry_pos;        /* [n_pages][64] raw position of the entry's last token */
   float* weight;             /* [n_pages][64] accumulated weight (R15)          */
@@ -409,7 +415,8 @@ typedef struct csa2_score_mods {
   float logit_cap;           /* 2^-126 .. 2^127: l = cap * tanh(l / cap); 0: none */
   const float* slopes;       /* fp32 [Hq]: l -= slopes[h] * |t - p|             */
   const int32_t* doc_start;  /* [B][Tq] raw position where the token's document starts */
-  const int32_t* prefix_len; /* [B] tokens at positions below it see each other */
+  const int32_t* prefix_len; /* [B] tokens below it see every entry that ends below it (R14); one that
+                                the prefix ends in the middle of, and the window, stay causal */
 } csa2_score_mods;
 
 /* Attention over every visible entry and the window (R14).  Q bf16
