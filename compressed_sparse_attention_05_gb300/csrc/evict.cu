@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
   __shared__ uint32_t group[3][kWarps];  // sums of 64 bins
   __shared__ uint32_t sums[kWarps][2];
   __shared__ uint32_t pub[3];
-  __shared__ uint32_t found[4];
-  __shared__ uint32_t no_page;           // an entry of this CTA's share lies behind a bad page (read by the others)
+  __shared__ uint32_t found[3];
+  __shared__ uint32_t no_page;           // an entry of this CTA's share lies behind a bad page (read by rank 0)
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
@@ -200,18 +200,7 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
         found[2] = second ? c1 : c0;
       }
     }
-    // beside it: a survivor could not move to a hole without a page, so such a sequence stays as it is
-    if (pass == 0 && warp == 1) {
-      const bool none = n_cl == 1 ? no_page != 0 : lane < n_cl && cl_load(&no_page, lane) != 0;
-      const uint32_t any = __any_sync(0xffffffffu, none);
-      if (lane == 0) found[3] = any;
-    }
     __syncthreads();
-    if (pass == 0 && found[3]) {         // the same in every CTA of the cluster
-      if (n_cl > 1) cl_sync();           // none leaves while another reads its shared memory
-      if (rank == 0 && tid == 0) ws.n_moves[b] = 0;
-      return;
-    }
     prefix |= found[0] << sh;
     mask |= (uint32_t)(nb - 1) << sh;
     need = found[1];
@@ -262,6 +251,7 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
   }
   warps_prefix(holes, movers, sums, before, all);
   uint32_t h = before[0], m = before[1], all_holes = all[0];
+  bool lost = no_page != 0;
   if (n_cl > 1) {
     if (tid == 0) {
       pub[1] = all[0];
@@ -271,6 +261,7 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
     uint32_t sum;
     h += ranks_prefix(&pub[1], &all_holes);
     m += ranks_prefix(&pub[2], &sum);
+    if (rank == 0 && warp == 0) lost = __any_sync(0xffffffffu, lane < n_cl && cl_load(&no_page, lane) != 0);
     // no CTA leaves while another still reads its shared memory, and every CTA has read the count
     // before it changes (waited for at the end)
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -291,9 +282,12 @@ __global__ void __launch_bounds__(kThreads) k_evict_select(EvictArgs a, EvictWs 
   if (n_cl > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   else __syncthreads();
   if (rank == 0 && tid == 0) {
-    ws.n_moves[b] = (int32_t)all_holes;
-    a.n_entries[b] = a.keep;
-    a.shift[b] = (int32_t)(shift + n - a.keep);
+    // a survivor cannot move to a hole without a page: a sequence with a bad one stays as it is
+    ws.n_moves[b] = lost ? 0 : (int32_t)all_holes;
+    if (!lost) {
+      a.n_entries[b] = a.keep;
+      a.shift[b] = (int32_t)(shift + n - a.keep);
+    }
   }
 }
 
