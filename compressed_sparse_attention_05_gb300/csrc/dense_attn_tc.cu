@@ -127,8 +127,8 @@ struct Smem {
   float mult[kRowsOf<kMode>];        // logit multiplier: softmax scale * log2(e) * 2^e_r
   float nref[kRowsOf<kMode>];        // attention: kTopLog2 - m_ref (kUnset before the row's first key); weights: -lse * log2(e)
   float slope2[kRowsOf<kMode>];      // slope * log2(e)
-  // a row sees an entry if its index (with entry_pos: its last token's position) is <= lim and
-  // its first token is >= doc, and the window row at position p if 0 <= t - p < W and p >= doc
+  // a row sees an entry if its last token is at or before lim and its first at or after doc, and
+  // the window row at position p if 0 <= t - p < W and p >= doc
   int lim[kRowsOf<kMode>], doc[kRowsOf<kMode>], t[kRowsOf<kMode>];
   union {
     float red[4][kRowsOf<kMode>];            // per-lane-quarter maxima / sums of a row over the keys; [0] also: see below
@@ -395,16 +395,11 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
 }
 
 // ---- dequantisation --------------------------------------------------------------------
-// min(a, b) and max(a, b); the other one where one is NaN.  V takes NaN and infinity as some finite value: a
-// row that sees the key gets them through K and the weight, and a row that does not must not get 0 x NaN.
+// min(a, b); the other one where one is NaN.  V takes NaN and infinity as some finite value: a row that sees
+// the key gets them through K and the weight, and a row that does not must not get 0 x NaN.
 __device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 // Half h (16 channels) of a piece with its two E4M3 scales (at most 448): 8 fp16 pairs.
@@ -469,19 +464,14 @@ __device__ __forceinline__ int page_of(const Ctx<kMode>& cx, int j, bool exists)
 template <bool kV>
 __device__ __forceinline__ void window_piece(const uint4& c, float wsc, uint32_t (&o)[8]) {
   if (kV && !isfinite(wsc)) wsc = 0.f;
-  const bool wide = kV && fabsf(wsc) > 128.f;   // a scale past 2^107: values may leave fp16's range at both ends
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t x = word_of(c, j);
-    o[2 * j] = win2_f16x2(x & 0xFFFFu, wsc);
-    o[2 * j + 1] = win2_f16x2(x >> 16, wsc);
+    o[2 * j] = win2_f16x2<kV>(x & 0xFFFFu, wsc);   // V: finite, but for NaN (scales past 2^107 leave fp16's range)
+    o[2 * j + 1] = win2_f16x2<kV>(x >> 16, wsc);
     if (kV) {
       o[2 * j] = min_f16x2(o[2 * j], 0x7BFF7BFFu);
       o[2 * j + 1] = min_f16x2(o[2 * j + 1], 0x7BFF7BFFu);
-      if (wide) {
-        o[2 * j] = max_f16x2(o[2 * j], 0xFBFFFBFFu);
-        o[2 * j + 1] = max_f16x2(o[2 * j + 1], 0xFBFFFBFFu);
-      }
     }
   }
 }
@@ -877,7 +867,7 @@ struct KeyView {
   bool masked;         // some row may not see the key, or its window row is rescaled (uniform over the warp)
   bool seen;           // a key that some row may see
   int win;             // 1: window row
-  int at, p;           // what an entry's rows compare with lim; raw position (an entry's: of its last token)
+  int p;               // raw position (an entry's: of its last token)
   float kf, ff;        // window row: 2^f and f
 };
 
@@ -889,7 +879,7 @@ template <int kMode>
 __device__ __forceinline__ bool row_sees(const Ctx<kMode>& cx, const KeyView& kv, int r) {
   const Smem<kMode>& sm = cx.sm;
   if (kv.win) return (uint32_t)(sm.t[r] - kv.p) < (uint32_t)cx.a.W && kv.p >= sm.doc[r];
-  return kv.at <= sm.lim[r] && kv.p - 3 >= sm.doc[r];
+  return kv.p <= sm.lim[r] && kv.p - 3 >= sm.doc[r];
 }
 
 // Columns c0 .. c0+31 of this thread's key: the logits in the log2 domain as the value
@@ -1003,7 +993,7 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
           atomicMin(&sm.seg.w_lo, r.w_lo);
           atomicMax(&sm.seg.w_hi, r.w_lo + r.w_n - 1);
         }
-        lim = a.entry_pos ? r.last : r.nv - 1;
+        lim = r.last;
         if (kWeights<kMode>) {
           const float lse = a.lse_in[(int64_t)b * rows + r0 + st];
           nref = -lse * kLog2e;
@@ -1055,7 +1045,6 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
       kv.win = k < sg.nw;
       kv.kf = 1.f;
       kv.ff = 0.f;
-      kv.at = 0;
       *slot = -1;
       if (kv.win) {
         const int64_t p = (int64_t)sm.seg.w_lo + (int64_t)k * kChunk + key;
@@ -1071,12 +1060,11 @@ __device__ __forceinline__ void role_softmax(const Ctx<kMode>& cx) {
         }
       } else {
         const int j = entry_of(i);
-        kv.seen = j >= sg.e_lo && j < sg.e_hi && page >= 0 && page < a.n_pages;
-        if (kv.seen) *slot = (int64_t)page * kPage + (j & (kPage - 1));
-        kv.p = a.entry_pos && kv.seen ? max(__ldg(a.entry_pos + *slot), INT_MIN + 3)
-                                      : j + shift32 < (1 << 29) ? 4 * (j + shift32) + 3 : INT_MAX;
-        kv.at = a.entry_pos ? kv.p : j;
-        kv.masked = __any_sync(0xffffffffu, !kv.seen || kv.at > sm.seg.all_lim || kv.p - 3 < sm.seg.all_doc);
+        const bool there = j >= sg.e_lo && j < sg.e_hi && page >= 0 && page < a.n_pages;
+        if (there) *slot = (int64_t)page * kPage + (j & (kPage - 1));
+        kv.seen = there && (a.entry_pos || j + shift32 < (1 << 29));   // no token is past 2^31 - 1
+        kv.p = a.entry_pos && there ? max(__ldg(a.entry_pos + *slot), INT_MIN + 3) : 4 * min(j + shift32, (1 << 29) - 1) + 3;
+        kv.masked = __any_sync(0xffffffffu, !kv.seen || kv.p > sm.seg.all_lim || kv.p - 3 < sm.seg.all_doc);
       }
       page = page_ahead(i + kStep);
       return kv;

@@ -48,6 +48,12 @@ __device__ __forceinline__ uint32_t f32x2_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The same, with the largest finite value in the place of infinity and of what would round to it.
+__device__ __forceinline__ uint32_t f32x2_f16x2_finite(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // (lo, hi) fp32 -> bf16x2 (round to nearest even), lo in the low half.
 __device__ __forceinline__ uint32_t f32x2_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -57,10 +63,12 @@ __device__ __forceinline__ uint32_t f32x2_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float f16_lo(uint32_t h2) { return __half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu))); }
 __device__ __forceinline__ float f16_hi(uint32_t h2) { return __half2float(__ushort_as_half((unsigned short)(h2 >> 16))); }
 // Two window codes -> f16x2 of bf16(fp32(e4m3 * scale)) (the window operand).
+template <bool kFinite = false>
 __device__ __forceinline__ uint32_t win2_f16x2(uint32_t pair, float sc) {
   const uint32_t e = e4m3x2_f16x2(pair);
   const uint32_t bf = f32x2_bf16x2(f16_lo(e) * sc, f16_hi(e) * sc);
-  return f32x2_f16x2(__uint_as_float(bf << 16), __uint_as_float(bf & 0xFFFF0000u));
+  const float lo = __uint_as_float(bf << 16), hi = __uint_as_float(bf & 0xFFFF0000u);
+  return kFinite ? f32x2_f16x2_finite(lo, hi) : f32x2_f16x2(lo, hi);
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
