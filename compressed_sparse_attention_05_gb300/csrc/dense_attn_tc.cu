@@ -21,24 +21,27 @@
 // Q (64 KB) and P, so with both products reading it the softmax would stand between them.  And
 // at N = 64 an MMA with both operands in shared memory reads 6 KB in 48 cycles, all that the
 // memory gives, while the dequantising warps' stores and every barrier wait: with the scores
-// of every second chunk from shared memory a batch of 32 x 32,768 entries took 281 us.)  An
-// MMA with A in tensor memory takes 87 cycles, so the tensor pipe's floor is 32 x 87 + 32 x 52
-// = 4,450 cycles per 128 keys x 64 rows.  S(c+1) is issued before PV(c), so that the softmax of
-// a chunk has a whole chunk's products to hide behind.
+// of every second chunk from shared memory a batch of 32 x 32,768 entries took 281 us.)  In
+// a probe of 32 MMAs back to back one takes 87 cycles with A in tensor memory and 52 with
+// both operands in shared memory, which would make 32 x 87 + 32 x 52 = 4,450 cycles per 128
+// keys x 64 rows; in the kernel they take somewhat less (next paragraph).  S(c+1) is issued
+// before PV(c), so that the softmax of a chunk has a whole chunk's products to hide behind.
 //
-// What bounds it: a chunk takes 3.6 us (6,400 cycles), the products 4,100 of them; the rest are
-// waits for the last quarters of K and V.  A fill warp's step (64 channels of 32 keys) takes
+// What bounds it: a chunk takes 3.6 us, 6,800 cycles at the 1.9 GHz of these runs.  In a copy
+// with clock stamps the MMA warp waits for 2,700 of them, for the last quarters of K and V,
+// and the products take the other 4,100.  A fill warp's step (64 channels of 32 keys) takes
 // 1,400 cycles, of which 400 are conversion and stores; the others are trips through a shared
 // memory that the products keep busy (a barrier looked at: 180) and instruction issue (half of
 // all slots are taken, by 24 warps; no pipe is over 40%).  The products of a chunk interleaved with
 // the next scores, so that the last quarters have more time, changed nothing.  A batch of
-// 32 x 32,768 entries takes 215 us (642 TFLOP/s, 1.4 TB/s of packed entries), the weights of
-// the same batch 92 us, of which the products are 82.
+// 32 x 32,768 entries takes 214 us (643 TFLOP/s, 1.4 TB/s of packed entries), the weights of
+// the same batch 92 us, of which the products are 82 at the probe's rate.
 //
 // Work is split over the SMs by chunks, not by tiles: every CTA computes the chunk
 // count of all tiles (lengths live on the device), takes an equal contiguous share,
-// and walks the tiles in it.  A tile counts kTileUnits chunks more than it has.  A tile that falls to several CTAs leaves partial
-// (m, l, O) in the workspace and k_dense_merge joins them in order.
+// and walks the tiles in it.  A tile counts kTileUnits chunks more than it has.  A
+// tile that falls to several CTAs leaves partial (m, l, O) in the workspace and
+// k_dense_merge joins them in order.
 //
 // Roles (896 threads): warps 0-7 dequantise V into shared memory, warps 8-15 K into tensor
 // memory (with the weights all sixteen do K); before a tile's products the same warps bring in
@@ -46,8 +49,8 @@
 // issues the MMAs, warps 25 and 26 copy the packed codes of K and V into staging slots (tensor
 // map copies: read by the dequantising warps themselves, lane = key, they throttled the L1),
 // warp 27 requests pages into L2 ahead.  Operand ranges as in attention_tc.cu (R11's powers of
-// two for Q rows and window rows); P is rounded to fp16, the normaliser sums the unrounded fp32
-// P, everything else is fp32.
+// two for Q rows and window rows); P is rounded to fp16 (kTopLog2), the normaliser sums the
+// unrounded fp32 P, everything else is fp32.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -64,7 +67,7 @@ constexpr int kD = 512;
 // What a kernel does: 0 attention; else the weights, with tiles of that many rows (64 or 128).  Attention's
 // O^T takes tensor memory for 64 rows only.  An MMA with A in tensor memory takes 87 cycles for 64 rows as
 // for 128, so the weights take 128 where a sequence has more than 64: 2 x 257 tokens x 64 heads over 16,384
-// entries in 650 us instead of 861.
+// entries took 649 us instead of 861 when this was changed, and take 651.
 template <int kMode> constexpr bool kWeights = kMode != 0;
 template <int kMode> constexpr int kRowsOf = kMode ? kMode : 64;
 constexpr int kRows = 64;                 // rows of an attention tile (N of both products)
@@ -338,8 +341,10 @@ __device__ __forceinline__ int range_chunks(const Range& r, bool weights) {
 // Units of work of a tile (tile = index among this launch's tiles): its chunks, and what beginning and
 // ending a tile takes (17 us, a chunk 3.6 us; without it an SM with 50 tiles of two chunks was still at
 // work when the SMs with tiles of 17 chunks had long finished: 1,181 us for a prompt of 1,024 tokens with
-// documents; with 2, 3, 4, 5, 6 units 743, 649, 602, 573, 574).  A share never begins or ends in the first
-// kTileUnits units: such a bound moves to the tile's start.
+// documents; with 2, 3, 4, 5, 6 units 743, 649, 602, 573, 574).  The figure is the attention kernel's; the
+// weights kernels, which have no O to write, use it too: from 4 to 5 units 257 tokens over 16,384 entries went
+// from 649 us to 658.  A share never begins or ends in the first kTileUnits units: such a bound moves to the
+// tile's start.
 constexpr int kTileUnits = 5;
 template <int kMode>
 __device__ int tile_units(const DenseArgs& a, const Plan& pl, int tile) {

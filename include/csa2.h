@@ -114,8 +114,9 @@
  *          doc_start.
  *      A token that sees nothing gets O = 0 and lse = -inf; a NaN in a key
  *      reaches the tokens that see the key, and no other.  Products run on
- *      fp16 tensor-core operands with R11's powers of two, P rounded to fp16,
- *      everything else in fp32; O is rounded once.
+ *      fp16 tensor-core operands with R11's powers of two, P rounded to fp16
+ *      (at d = 512, in units of 2^-7 of a reference that is the row's maximum
+ *      or up to 2^8 below it), everything else in fp32; O is rounded once.
  *   R15 accumulated weight: weight_out[j] = decay * weight_in[j] + the sum over
  *      the call's query tokens and heads of exp(l - lse), l as in R14, lse as
  *      csa2_dense_attn wrote it; rows whose lse is infinite add nothing.
