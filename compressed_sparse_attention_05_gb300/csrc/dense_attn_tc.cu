@@ -116,7 +116,7 @@ struct Segment {            // what the roles need to know of the current tile
   int w_lo, w_hi;           // window rows any row sees (raw positions, inclusive)
   int all_lim, all_doc;     // every row sees the entries that these would let through (as lim and doc of a row)
   int one_t;                // all rows belong to one token
-  int one_tok;              // bit k: rows 32 k .. +31 do, and none of the tile's adds nothing
+  int one_tok;              // bit k: rows 32 k .. +31 do (weights: 0 if a row of the tile has an infinite lse)
   int next_t;               // first row of the tile's second token
   int pos0;
 };
