@@ -20,6 +20,8 @@ CSA2_OK = 0
 CSA2_F32, CSA2_BF16 = 0, 1
 CSA2_KV_MXFP4, CSA2_KV_FP8 = 0, 1
 MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 STATUS_BAD_PAGE, STATUS_BAD_INDEX, STATUS_BAD_COUNT = 1, 2, 4
 
 ERRORS = {1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED", 3: "CSA2_ERR_CUDA",
@@ -53,6 +55,21 @@ class Bounded(C.Structure):
 class ScoreMods(C.Structure):
     _fields_ = [("logit_cap", C.c_float), ("slopes", C.c_void_p), ("doc_start", C.c_void_p),
                 ("prefix_len", C.c_void_p)]
+
+
+class PagePool(C.Structure):
+    _fields_ = [("page_table", C.c_void_p), ("held", C.c_void_p), ("free_pages", C.c_void_p), ("n_free", C.c_void_p),
+                ("n_pages", C.c_int64)]
+
+
+class RopeSpec(C.Structure):
+    _fields_ = [("scaling", C.c_int32), ("original_len", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+                ("beta_fast", C.c_float), ("beta_slow", C.c_float)]
+
+
+class Tree(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("ctx_len", C.c_void_p), ("path", C.c_void_p),
+                ("max_depth", C.c_int32)]
 
 
 class LayerArgs(C.Structure):
@@ -105,6 +122,18 @@ SIGNATURES = {
                                           _I32, _P]),
     "csa2_sparse_attn": (C.c_int, [C.POINTER(Dims), C.POINTER(Cache), C.POINTER(Window), _P, _P, _P, _P,
                                    _F, _P, _P, _P]),
+    "csa2_page_plan_workspace_size": (_SZ, [C.POINTER(Dims)]),
+    "csa2_page_plan": (C.c_int, [C.POINTER(Dims), C.POINTER(PagePool), _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ,
+                                 _P]),
+    "csa2_pack_fp8_blocks": (C.c_int, [_P, _I32, _I64, _I64, _I32, _P, _P, _P]),
+    "csa2_matmul_fp8_workspace_size": (_SZ, [_I32, _I32, _I32]),
+    "csa2_matmul_fp8": (C.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _SZ, _P]),
+    "csa2_rope_table": (C.c_int, [C.POINTER(RopeSpec), _I32, _P, _P]),
+    "csa2_rope": (C.c_int, [_P, _I32, _I64, _I64, _P, _I32, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _F, _P,
+                            _P, _P]),
+    "csa2_tree_plan": (C.c_int, [C.POINTER(Dims), _P, _P, _I32, _P, _P, _P]),
+    "csa2_tree_attn": (C.c_int, [C.POINTER(Dims), C.POINTER(Cache), C.POINTER(Window), C.POINTER(Tree), _P, _P, _P, _P, _F,
+                                 _P, _P, _P]),
     "csa2_dense_attn_workspace_size": (_SZ, [C.POINTER(Dims), _I32]),
     "csa2_dense_attn": (C.c_int, [C.POINTER(Dims), C.POINTER(Cache), C.POINTER(Bounded), C.POINTER(Window),
                                   C.POINTER(ScoreMods), _P, _P, _F, _I32, _P, _P, _P, _SZ, _P]),
@@ -313,6 +342,78 @@ def _ref(struct):
 
 def _nbytes(t) -> int:
     return t.numel() * t.element_size() if t is not None else 0
+
+
+def csa2_page_plan_workspace_size(dims: Dims) -> int:
+    return lib().csa2_page_plan_workspace_size(C.byref(dims))
+
+
+def csa2_page_plan(dims: Dims, pool: PagePool, seq_len, n_new, seq_len_out, n_entries, first_entry, ws, shift=None, q_pos=None,
+                   slots=None, granted=None, stream=None):
+    """Pages, positions and slots of a step's tokens; slots int64 [B][max_new], q_pos int32 [B][Tq]."""
+    _check(lib().csa2_page_plan(C.byref(dims), C.byref(pool), ptr(seq_len), ptr(n_new), ptr(shift),
+                                slots.shape[-1] if slots is not None else 0, ptr(seq_len_out), ptr(n_entries), ptr(first_entry),
+                                ptr(q_pos), ptr(slots), ptr(granted), ptr(ws), _nbytes(ws), stream_handle(stream)))
+
+
+def _strided(t: torch.Tensor):
+    """Address of a tensor whose last dimension is contiguous, whatever its other strides."""
+    if not t.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the tensor's last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _float_type(t: torch.Tensor) -> int:
+    kinds = {torch.float32: CSA2_F32, torch.bfloat16: CSA2_BF16}
+    if t.dtype not in kinds:
+        raise ValueError(f"tensor must be float32 or bfloat16, not {t.dtype}")
+    return kinds[t.dtype]
+
+
+def csa2_pack_fp8_blocks(x, codes, scales, stream=None):
+    """x [n][K] bf16 or fp32 (rows may be apart) -> codes [n][K] E4M3, scales fp32 [n][ceil(K/128)]."""
+    n, K = x.shape
+    _check(lib().csa2_pack_fp8_blocks(_strided(x), _float_type(x), x.stride(0), n, K, ptr(codes), ptr(scales),
+                                      stream_handle(stream)))
+
+
+def csa2_matmul_fp8_workspace_size(M: int, N: int, K: int) -> int:
+    return lib().csa2_matmul_fp8_workspace_size(M, N, K)
+
+
+def csa2_matmul_fp8(A, a_scales, Bw, b_scales, out, ws=None, stream=None):
+    """out [M][N] (bf16 or fp32) = A [M][K] Bw [N][K]^T, E4M3 codes with the scales of csa2_pack_fp8_blocks."""
+    (M, K), N = A.shape, Bw.shape[0]
+    _check(lib().csa2_matmul_fp8(ptr(A), ptr(a_scales), ptr(Bw), ptr(b_scales), M, N, K, ptr(out), _float_type(out), ptr(ws),
+                                 _nbytes(ws), stream_handle(stream)))
+
+
+def csa2_rope_table(spec: RopeSpec, r: int, table, stream=None):
+    """table: int64 [r/2], made once; csa2_rope reads it."""
+    _check(lib().csa2_rope_table(C.byref(spec), r, ptr(table), stream_handle(stream)))
+
+
+def csa2_rope(x, y, positions, table, start=0, layout=ROPE_HALF, inverse=False, amplitude=1.0, stream=None):
+    """y = x [tokens][heads][d] rotated by the positions [tokens]; table of r/2 pairs; y may be x."""
+    n, heads, d = x.shape
+    _check(lib().csa2_rope(_strided(x), _float_type(x), x.stride(0), x.stride(1), _strided(y), _float_type(y), y.stride(0),
+                           y.stride(1), n, heads, d, start, 2 * table.numel(), layout, int(inverse), amplitude, ptr(positions),
+                           ptr(table), stream_handle(stream)))
+
+
+def csa2_tree_plan(dims: Dims, parent, ctx_len, q_pos, path, stream=None):
+    """q_pos [B][Tq] and path [B][Tq][max_depth] of the trees that parent [B][Tq] describes."""
+    _check(lib().csa2_tree_plan(C.byref(dims), ptr(parent), ptr(ctx_len), path.shape[-1], ptr(q_pos), ptr(path),
+                                stream_handle(stream)))
+
+
+def csa2_tree_attn(dims: Dims, cache: Cache, window: Optional[Window], tree: Tree, Q, q_pos, idx, cnt, softmax_scale, O, lse=None,
+                   stream=None):
+    """csa2_sparse_attn for drafted trees; O [B][Tq][Hq][d] bf16."""
+    _check(lib().csa2_tree_attn(C.byref(dims), C.byref(cache), _ref(window), C.byref(tree), ptr(Q), ptr(q_pos), ptr(idx), ptr(cnt),
+                                softmax_scale, ptr(O), ptr(lse), stream_handle(stream)))
 
 
 def csa2_dense_attn_workspace_size(dims: Dims, max_entries: int) -> int:

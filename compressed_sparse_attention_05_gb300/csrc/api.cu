@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -716,7 +718,7 @@ static int attn_impl(const csa2_dims* dm, const csa2_cache* c, const csa2_window
   if (dm->swa_cap > 0 && dm->W > 0) {
     REQUIRE_PTR(win->codes); REQUIRE_PTR(win->scales); REQUIRE_IPTR(win->pos0);
   }
-  AttnArgs a;
+  AttnArgs a = {};
   a.Q = Q; a.kv_codes = c->kv_codes; a.kv_scales = c->kv_scales; a.page_table = c->page_table;
   a.n_pages = c->n_pages; a.max_pages = dm->max_pages; a.idx = idx; a.cnt = cnt; a.q_pos = q_pos;
   a.n_entries = c->n_entries; a.swa_codes = win->codes; a.swa_scales = win->scales; a.swa_pos0 = win->pos0;
@@ -733,6 +735,215 @@ int csa2_sparse_attn(const csa2_dims* dm, const csa2_cache* c, const csa2_window
   NvtxRange nvtx_("csa2_sparse_attn");
   g_err[0] = 0;
   return attn_impl(dm, c, win, Q, q_pos, idx, cnt, softmax_scale, O, lse, static_cast<cudaStream_t>(stream));
+}
+
+// ---- the query side of a step: pages, FP8 projections, rotary positions, drafted trees ----------
+size_t csa2_page_plan_workspace_size(const csa2_dims* dm) {
+  return dm && dm->B > 0 ? page_plan_workspace_bytes(dm->B) : 0;
+}
+
+int csa2_page_plan(const csa2_dims* dm, const csa2_page_pool* pool, const int32_t* seq_len, const int32_t* n_new,
+                   const int32_t* shift, int32_t max_new, int32_t* seq_len_out, int32_t* n_entries, int32_t* first_entry,
+                   int32_t* q_pos, int64_t* slots, int32_t* granted, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("csa2_page_plan");
+  g_err[0] = 0;
+  REQUIRE(dm, "dims must not be NULL");
+  REQUIRE(dm->B >= 0 && dm->Tq >= 0, "B and Tq must be >= 0");
+  REQUIRE(dm->max_pages >= 1, "max_pages must be >= 1");
+  REQUIRE(max_new >= 0, "max_new must be >= 0");
+  REQUIRE(pool, "pool must not be NULL");
+  REQUIRE(pool->n_pages >= 1 && pool->n_pages < (1ll << 31), "pool.n_pages must be in 1..2^31-1");
+  if (dm->B == 0) return CSA2_OK;
+  REQUIRE_IPTR(pool->page_table); REQUIRE_IPTR(pool->held); REQUIRE_IPTR(pool->free_pages); REQUIRE_IPTR(pool->n_free);
+  REQUIRE_IPTR(seq_len); REQUIRE_IPTR(n_new); REQUIRE_IPTR(seq_len_out); REQUIRE_IPTR(n_entries); REQUIRE_IPTR(first_entry);
+  if (shift) REQUIRE_IPTR(shift);
+  if (q_pos) REQUIRE_IPTR(q_pos);
+  if (granted) REQUIRE_IPTR(granted);
+  if (slots) REQUIRE((reinterpret_cast<uintptr_t>(slots) & 7u) == 0, "slots must be 8-byte aligned");
+  const size_t need = page_plan_workspace_bytes(dm->B);
+  if (!ws || ws_bytes < need) return fail(CSA2_ERR_WORKSPACE, "workspace: %zu bytes given, %zu needed", ws ? ws_bytes : 0, need);
+  REQUIRE(aligned16(ws), "workspace must be 16-byte aligned");
+  PagePlanArgs a = {};
+  a.page_table = pool->page_table; a.held = pool->held; a.free_pages = pool->free_pages; a.n_free = pool->n_free;
+  a.n_pages = pool->n_pages; a.seq_len = seq_len; a.n_new = n_new; a.shift = shift; a.seq_len_out = seq_len_out;
+  a.n_entries = n_entries; a.first_entry = first_entry; a.granted = granted;
+  a.q_pos = dm->Tq > 0 ? q_pos : nullptr; a.slots = max_new > 0 ? slots : nullptr;
+  a.B = dm->B; a.Tq = dm->Tq; a.max_pages = dm->max_pages; a.max_new = max_new;
+  LAUNCH(launch_page_plan(a, ws, static_cast<cudaStream_t>(stream)), "page_plan");
+  return CSA2_OK;
+}
+
+int csa2_pack_fp8_blocks(const void* x, int32_t dtype, int64_t row_stride, int64_t n_rows, int32_t K, uint8_t* codes,
+                         float* scales, void* stream) {
+  NvtxRange nvtx_("csa2_pack_fp8_blocks");
+  g_err[0] = 0;
+  REQUIRE(dtype == CSA2_BF16 || dtype == CSA2_F32, "dtype must be CSA2_BF16 or CSA2_F32");
+  REQUIRE(n_rows >= 0 && n_rows < (1ll << 31), "n_rows must be in 0..2^31-1");
+  REQUIRE(K > 0 && K % 16 == 0, "K must be a positive multiple of 16 (got %d)", K);
+  const int64_t size = dtype == CSA2_F32 ? 4 : 2;
+  REQUIRE(n_rows <= 1 || (row_stride >= K && row_stride * size % 16 == 0),
+          "row_stride must be at least K and a multiple of 16 bytes (got %lld elements)", (long long)row_stride);
+  if (n_rows == 0) return CSA2_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(codes); REQUIRE_PTR(scales);
+  LAUNCH(launch_pack_fp8_blocks(x, dtype, row_stride, n_rows, K, codes, scales, static_cast<cudaStream_t>(stream)), "pack_fp8_blocks");
+  return CSA2_OK;
+}
+
+static int check_matmul(int32_t M, int32_t N, int32_t K) {
+  REQUIRE(M >= 0 && N >= 0, "M and N must be >= 0");
+  REQUIRE(M <= (1 << 30) && N <= (1 << 30) && K <= (1 << 30), "M, N and K must be at most 2^30");
+  REQUIRE(K > 0 && K % 16 == 0, "K must be a positive multiple of 16 (got %d)", K);
+  return CSA2_OK;
+}
+
+size_t csa2_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return matmul_fp8_workspace_bytes(M, N, K);
+}
+
+int csa2_matmul_fp8(const uint8_t* A, const float* a_scales, const uint8_t* Bw, const float* b_scales, int32_t M, int32_t N,
+                    int32_t K, void* C, int32_t c_dtype, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("csa2_matmul_fp8");
+  g_err[0] = 0;
+  const int rc = check_matmul(M, N, K);
+  if (rc) return rc;
+  REQUIRE(c_dtype == CSA2_BF16 || c_dtype == CSA2_F32, "c_dtype must be CSA2_BF16 or CSA2_F32");
+  if (M == 0 || N == 0) return CSA2_OK;
+  REQUIRE_PTR(A); REQUIRE_PTR(a_scales); REQUIRE_PTR(Bw); REQUIRE_PTR(b_scales); REQUIRE_PTR(C);
+  const size_t need = matmul_fp8_workspace_bytes(M, N, K);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return fail(CSA2_ERR_WORKSPACE, "workspace: %zu bytes given, %zu needed", ws ? ws_bytes : 0, need);
+    REQUIRE(aligned16(ws), "workspace must be 16-byte aligned");
+  }
+  LAUNCH(launch_matmul_fp8(A, a_scales, Bw, b_scales, M, N, K, C, c_dtype == CSA2_F32, ws, static_cast<cudaStream_t>(stream)), "matmul_fp8");
+  return CSA2_OK;
+}
+
+int csa2_rope_table(const csa2_rope_spec* spec, int32_t r, uint64_t* table, void* stream) {
+  NvtxRange nvtx_("csa2_rope_table");
+  g_err[0] = 0;
+  REQUIRE(spec, "spec must not be NULL");
+  REQUIRE(r >= 0 && r % 2 == 0 && r <= 2 * kRopeMaxPairs, "r must be even and in 0..%d (got %d)", 2 * kRopeMaxPairs, r);
+  const int kind = spec->scaling;
+  REQUIRE(kind >= CSA2_ROPE_PLAIN && kind <= CSA2_ROPE_YARN, "scaling must be one of CSA2_ROPE_PLAIN .. CSA2_ROPE_YARN");
+  REQUIRE(spec->base > 1. && std::isfinite(spec->base), "base must be above 1 and finite");
+  const double base0 = spec->base, f = kind == CSA2_ROPE_PLAIN ? 1. : spec->factor;
+  REQUIRE(f >= 1. && std::isfinite(f), "factor must be at least 1 and finite");
+  REQUIRE(kind != CSA2_ROPE_NTK || r != 2, "CSA2_ROPE_NTK needs r > 2");
+  if (kind == CSA2_ROPE_YARN) {
+    REQUIRE(spec->original_len >= 1, "original_len must be at least 1");
+    REQUIRE(spec->beta_slow > 0.f && spec->beta_fast >= spec->beta_slow && std::isfinite(spec->beta_fast),
+            "beta_fast and beta_slow must be positive and finite, beta_fast the larger");
+  }
+  if (r == 0) return CSA2_OK;
+  REQUIRE(table && (reinterpret_cast<uintptr_t>(table) & 7u) == 0, "table must not be NULL and 8-byte aligned");
+  const double pi = 3.14159265358979323846;
+  const double base = kind == CSA2_ROPE_NTK ? base0 * pow(f, (double)r / (r - 2)) : base0;
+  REQUIRE(std::isfinite(base), "base and factor are too large");
+  double lo = 0., hi = 0.;
+  if (kind == CSA2_ROPE_YARN) {   // the pairs that turn beta_fast and beta_slow times in the original length
+    auto pair_of = [&](double turns) { return r * log(spec->original_len / (turns * 2. * pi)) / (2. * log(base)); };
+    lo = std::max(0., floor(pair_of(spec->beta_fast)));
+    hi = std::min(r - 1., ceil(pair_of(spec->beta_slow)));
+  }
+  RopeTable t = {};
+  for (int i = 0; i < r / 2; ++i) {
+    double theta = pow(base, -2. * i / r);
+    if (kind == CSA2_ROPE_LINEAR) theta /= f;
+    if (kind == CSA2_ROPE_YARN) {
+      const double ramp = std::min(1., std::max(0., (i - lo) / std::max(hi - lo, 0.001)));
+      theta = theta / f * ramp + theta * (1. - ramp);
+    }
+    t.g[i] = (uint64_t)ldexp(theta / (2. * pi), 64);   // theta <= 1: below 2^62
+  }
+  LAUNCH(launch_rope_table(t, r / 2, table, static_cast<cudaStream_t>(stream)), "rope_table");
+  return CSA2_OK;
+}
+
+int csa2_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, int64_t x_head_stride, void* y, int32_t y_dtype,
+              int64_t y_token_stride, int64_t y_head_stride, int64_t n_tokens, int32_t heads, int32_t d, int32_t start,
+              int32_t r, int32_t layout, int32_t inverse, float amplitude, const int32_t* positions, const uint64_t* table,
+              void* stream) {
+  NvtxRange nvtx_("csa2_rope");
+  g_err[0] = 0;
+  REQUIRE((x_dtype == CSA2_BF16 || x_dtype == CSA2_F32) && (y_dtype == CSA2_BF16 || y_dtype == CSA2_F32),
+          "x_dtype and y_dtype must be CSA2_BF16 or CSA2_F32");
+  REQUIRE(n_tokens >= 0 && n_tokens < (1ll << 31), "n_tokens must be in 0..2^31-1");
+  REQUIRE(heads >= 0 && heads <= 65535, "heads must be in 0..65535 (got %d)", heads);
+  REQUIRE(d >= 1 && d <= 65536, "d must be in 1..65536 (got %d)", d);
+  REQUIRE(r >= 0 && r % 2 == 0 && r <= 2 * kRopeMaxPairs, "r must be even and in 0..%d (got %d)", 2 * kRopeMaxPairs, r);
+  REQUIRE(start >= 0 && start <= d - r, "the rotated channels start .. start + r must lie in the head");
+  REQUIRE(layout == CSA2_ROPE_HALF || layout == CSA2_ROPE_INTERLEAVED, "layout must be CSA2_ROPE_HALF or CSA2_ROPE_INTERLEAVED");
+  REQUIRE(std::isfinite(amplitude), "amplitude must be finite");
+  REQUIRE(x_token_stride >= 0 && x_head_stride >= 0, "strides of x must be >= 0");
+  REQUIRE((n_tokens <= 1 || y_token_stride >= d) && (heads <= 1 || y_head_stride >= d), "strides of y must be at least d");
+  if (n_tokens == 0 || heads == 0) return CSA2_OK;
+  REQUIRE(x && y, "x and y must not be NULL");
+  REQUIRE(reinterpret_cast<uintptr_t>(x) % (x_dtype == CSA2_F32 ? 4 : 2) == 0 && reinterpret_cast<uintptr_t>(y) % (y_dtype == CSA2_F32 ? 4 : 2) == 0,
+          "x and y must be aligned to their elements");
+  REQUIRE_IPTR(positions);
+  if (r > 0) REQUIRE(table && (reinterpret_cast<uintptr_t>(table) & 7u) == 0, "table must not be NULL and 8-byte aligned");
+  if (x == y)
+    REQUIRE(x_dtype == y_dtype && (n_tokens <= 1 || x_token_stride == y_token_stride) && (heads <= 1 || x_head_stride == y_head_stride),
+            "in place (y == x) the types and strides must be the same");
+  RopeArgs a = {};
+  a.x = x; a.y = y; a.x_token = x_token_stride; a.x_head = x_head_stride; a.y_token = y_token_stride; a.y_head = y_head_stride;
+  a.rows = n_tokens; a.heads = heads; a.d = d; a.start = start; a.r = r; a.layout = layout; a.inverse = inverse != 0;
+  a.x_dtype = x_dtype; a.y_dtype = y_dtype; a.amplitude = amplitude; a.positions = positions; a.table = table;
+  LAUNCH(launch_rope(a, static_cast<cudaStream_t>(stream)), "rope");
+  return CSA2_OK;
+}
+
+int csa2_tree_plan(const csa2_dims* dm, const int32_t* parent, const int32_t* ctx_len, int32_t max_depth, int32_t* q_pos,
+                   int32_t* path, void* stream) {
+  NvtxRange nvtx_("csa2_tree_plan");
+  g_err[0] = 0;
+  REQUIRE(dm, "dims must not be NULL");
+  REQUIRE(dm->B >= 0 && dm->Tq >= 0, "B and Tq must be >= 0");
+  if (dm->Tq > tree_plan_max_nodes())
+    return fail(CSA2_ERR_UNSUPPORTED, "a tree has at most %d nodes (Tq = %d)", tree_plan_max_nodes(), dm->Tq);
+  REQUIRE(max_depth >= 1, "max_depth must be >= 1");
+  if ((int64_t)dm->B * dm->Tq == 0) return CSA2_OK;
+  REQUIRE_IPTR(parent); REQUIRE_IPTR(ctx_len); REQUIRE_IPTR(q_pos); REQUIRE_IPTR(path);
+  LAUNCH(launch_tree_plan(dm->B, dm->Tq, max_depth, parent, ctx_len, q_pos, path, static_cast<cudaStream_t>(stream)), "tree_plan");
+  return CSA2_OK;
+}
+
+int csa2_tree_attn(const csa2_dims* dm, const csa2_cache* c, const csa2_window* win, const csa2_tree* tree, const uint16_t* Q,
+                   const int32_t* q_pos, const int32_t* idx, const int32_t* cnt, float softmax_scale, uint16_t* O, float* lse,
+                   void* stream) {
+  NvtxRange nvtx_("csa2_tree_attn");
+  g_err[0] = 0;
+  int rc = check_dims(dm, false, true);
+  if (rc) return rc;
+  REQUIRE(std::isfinite(softmax_scale), "softmax_scale must be finite");
+  REQUIRE(tree, "tree must not be NULL");
+  REQUIRE(tree->max_depth >= 1, "tree.max_depth must be >= 1");
+  if ((int64_t)dm->B * dm->Tq == 0) return CSA2_OK;
+  rc = check_cache(c, true, false);
+  if (rc) return rc;
+  REQUIRE_PTR(Q); REQUIRE_IPTR(q_pos); REQUIRE_IPTR(idx); REQUIRE_IPTR(cnt); REQUIRE_PTR(O);
+  if (lse) REQUIRE(aligned16(lse), "lse must be 16-byte aligned");
+  REQUIRE_PTR(tree->codes); REQUIRE_PTR(tree->scales); REQUIRE_IPTR(tree->path); REQUIRE_IPTR(tree->ctx_len);
+  const bool window = dm->swa_cap > 0 && dm->W > 0;
+  if (window) {
+    REQUIRE(win, "window must not be NULL");
+    REQUIRE_PTR(win->codes); REQUIRE_PTR(win->scales); REQUIRE_IPTR(win->pos0);
+  }
+  REQUIRE(c->n_pages < (1ll << 31) / kPage, "cache.n_pages is too large");
+  REQUIRE((int64_t)dm->B * ((int64_t)dm->swa_cap + dm->Tq) < (1ll << 31) - 2, "too many window rows");
+  REQUIRE((int64_t)dm->B * dm->Tq < (1ll << 28) && (dm->d == 512 || (int64_t)dm->B * dm->Tq <= 65535), "too many query tokens");
+  AttnArgs a = {};
+  a.Q = Q; a.kv_codes = c->kv_codes; a.kv_scales = c->kv_scales; a.page_table = c->page_table;
+  a.n_pages = c->n_pages; a.max_pages = dm->max_pages; a.idx = idx; a.cnt = cnt; a.q_pos = q_pos;
+  a.n_entries = c->n_entries; a.B = dm->B; a.Tq = dm->Tq; a.Hq = dm->Hq; a.d = dm->d; a.K = dm->K; a.W = dm->W;
+  if (window) {
+    a.swa_codes = win->codes; a.swa_scales = win->scales; a.swa_pos0 = win->pos0; a.swa_cap = dm->swa_cap;
+  }
+  a.scale = softmax_scale; a.O16 = O; a.lse = lse; a.kv_fp8 = dm->kv_format == CSA2_KV_FP8;
+  a.path = tree->path; a.ctx_len = tree->ctx_len; a.tree_codes = tree->codes; a.tree_scales = tree->scales; a.max_depth = tree->max_depth;
+  LAUNCH(launch_sparse_attn(a, static_cast<cudaStream_t>(stream)), "tree_attn");
+  return CSA2_OK;
 }
 
 // ---- a bounded cache: attention over all of it, weights, eviction -----------------

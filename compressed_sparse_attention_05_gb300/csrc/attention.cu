@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "operands.cuh"
 #include "tc.cuh"
 
 namespace csa2 {
@@ -97,7 +98,7 @@ struct AttnSmem {
 };
 
 // Dequantise one 16-channel group of a key into 16 fp16 values in shared memory.
-template <int D>
+template <int D, bool kTree>
 __device__ __forceinline__ void dequant_group(const AttnArgs& a, int b, int64_t src, int grp,
                                               uint16_t* dst) {
   uint32_t w[8];
@@ -111,9 +112,10 @@ __device__ __forceinline__ void dequant_group(const AttnArgs& a, int b, int64_t 
       w[i] = hmul2_u32(e2m1x2_to_f16x2((word >> ((i & 3) * 8)) & 0xFFu), s2);  // exact
     }
   } else if (src <= -2) {
-    const int64_t wr = (int64_t)b * a.swa_cap + (-2 - src);
-    const uint4 c = *reinterpret_cast<const uint4*>(a.swa_codes + wr * D + grp * 16);
-    const float sw = a.swa_scales[wr];
+    const bool node = kTree && -2 - src >= a.swa_cap;   // a drafted token's row
+    const int64_t wr = node ? (int64_t)b * a.Tq + (-2 - src - a.swa_cap) : (int64_t)b * a.swa_cap + (-2 - src);
+    const uint4 c = *reinterpret_cast<const uint4*>((node ? a.tree_codes : a.swa_codes) + wr * D + grp * 16);
+    const float sw = (node ? a.tree_scales : a.swa_scales)[wr];
     const float sc = sw * pow2i(-window_exp(sw));
     const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -133,7 +135,7 @@ __device__ __forceinline__ void dequant_group(const AttnArgs& a, int b, int64_t 
   d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kAttnThreads)
 k_sparse_attn(AttnArgs a, uint32_t* status) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -147,16 +149,22 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
 
-  const int t = a.q_pos[row];
+  const int t = kTree ? max(a.q_pos[row], -1) : a.q_pos[row];   // (-1: no node of the tree)
   const int nv = n_visible(a.n_entries[b], t);  // bounds the indices checked below
-  int n_sel = a.cnt[row];
+  int n_sel = kTree && t < 0 ? 0 : a.cnt[row];
   if (n_sel < 0 || n_sel > a.K) {
     if (tid == 0) raise_status(status, CSA2_STATUS_BAD_COUNT);
     n_sel = n_sel < 0 ? 0 : a.K;
   }
   const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
-  const int w_lo = max(max(0, t - a.W + 1), pos0);
-  const int w_hi = min(t, pos0 + a.swa_cap - 1);
+  int w_lo = max(max(0, t - a.W + 1), pos0);
+  int w_hi = min(t, pos0 + a.swa_cap - 1);
+  int ctx = 0;
+  if (kTree) {   // from the first position that the buffer holds (or the first ancestor) to the token itself
+    ctx = max(0, a.ctx_len[b]);
+    w_lo = max(max(0, t - a.W + 1), min(a.swa_cap > 0 ? pos0 : INT_MAX, ctx));
+    w_hi = t;
+  }
   const int n_win = max(0, w_hi - w_lo + 1);
   const int n_keys = n_sel + n_win;
 
@@ -215,16 +223,28 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
         if (j >= 0 && j < nv) src = entry_slot(a.page_table, a.max_pages, a.n_pages, b, j, status);
         else raise_status(status, CSA2_STATUS_BAD_INDEX);
       } else if (i < n_keys) {
-        src = -2 - (int64_t)(w_lo + (i - n_sel) - pos0);
+        const int p = w_lo + (i - n_sel);
+        if (kTree && p >= ctx) {
+          const int node = p - ctx < a.max_depth ? a.path[row * a.max_depth + (p - ctx)] : -1;
+          if (node >= 0 && node < a.Tq) src = -2 - ((int64_t)a.swa_cap + node);
+          else raise_status(status, CSA2_STATUS_BAD_INDEX);
+        } else if (!kTree || (p >= pos0 && p - pos0 < a.swa_cap)) {
+          src = -2 - (int64_t)(p - pos0);
+        }
       }
       sm.key_src[tid] = src;
-      sm.kexp[tid] = src <= -2 ? window_exp(a.swa_scales[(int64_t)b * a.swa_cap + (-2 - src)]) : 0;
+      int f = 0;
+      if (src <= -2) {
+        if (kTree && -2 - src >= a.swa_cap) f = window_exp(a.tree_scales[(int64_t)b * a.Tq + (-2 - src - a.swa_cap)]);
+        else f = window_exp(a.swa_scales[(int64_t)b * a.swa_cap + (-2 - src)]);
+      }
+      sm.kexp[tid] = f;
     }
     __syncthreads();
     // ---- gather + dequantise
     for (int i = tid; i < kTK * (D / 16); i += kAttnThreads) {
       const int kr = i / (D / 16), grp = i % (D / 16);
-      dequant_group<D>(a, b, sm.key_src[kr], grp, &sm.k[kr * QS + grp * 16]);
+      dequant_group<D, kTree>(a, b, sm.key_src[kr], grp, &sm.k[kr * QS + grp * 16]);
     }
     __syncthreads();
     // ---- S = Q K^T : warp owns keys 8*warp .. +7
@@ -327,10 +347,13 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int ch = warp * DW + i * 8 + 2 * t4;
-    if (head0 < a.Hq)
-      *reinterpret_cast<float2*>(a.O + (row * a.Hq + head0) * D + ch) = make_float2(o[i][0] * inv0, o[i][1] * inv0);
-    if (head1 < a.Hq)
-      *reinterpret_cast<float2*>(a.O + (row * a.Hq + head1) * D + ch) = make_float2(o[i][2] * inv1, o[i][3] * inv1);
+    auto put = [&](int head, float v0, float v1) {
+      const int64_t at = (row * a.Hq + head) * D + ch;
+      if (kTree) *reinterpret_cast<uint32_t*>(a.O16 + at) = f32x2_bf16x2(v0, v1);
+      else *reinterpret_cast<float2*>(a.O + at) = make_float2(v0, v1);
+    };
+    if (head0 < a.Hq) put(head0, o[i][0] * inv0, o[i][1] * inv0);
+    if (head1 < a.Hq) put(head1, o[i][2] * inv1, o[i][3] * inv1);
   }
   if (a.lse && tid < kHG && hg * kHG + tid < a.Hq) {
     const float l = sm.l[tid];
@@ -338,13 +361,13 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
   }
 }
 
-template <int D>
+template <int D, bool kTree>
 static cudaError_t launch_attn_d(const AttnArgs& a, cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(k_sparse_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k_sparse_attn<D, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   dim3 grid((a.Hq + kHG - 1) / kHG, (unsigned)((int64_t)a.B * a.Tq));
-  k_sparse_attn<D><<<grid, kAttnThreads, smem, s>>>(a, status_word());
+  k_sparse_attn<D, kTree><<<grid, kAttnThreads, smem, s>>>(a, status_word());
   return counted(cudaGetLastError());
 }
 
@@ -352,7 +375,7 @@ cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t s) {
   if ((int64_t)a.B * a.Tq == 0) return cudaSuccess;
   if (sparse_attn_tc_supported(a)) return launch_sparse_attn_tc(a, s);
   if (a.d != 64) return cudaErrorInvalidValue;   // d = 512 always takes the tensor-memory kernel
-  return launch_attn_d<64>(a, s);
+  return a.path ? launch_attn_d<64, true>(a, s) : launch_attn_d<64, false>(a, s);
 }
 
 }  // namespace csa2

@@ -174,6 +174,17 @@ __device__ __forceinline__ float ld_gather4f(const float* p) {
 __device__ __forceinline__ uint2 load_scales(const AttnArgs& a, int32_t src, int qd) {
   return src >= 0 ? ld_gather8(a.kv_scales + (int64_t)src * (kD / 16) + 8 * qd) : make_uint2(0, 0);
 }
+// Codes and scale of window row w: the rows of the window buffer, then (with a tree of drafted tokens) the nodes'.
+template <bool kTree>
+__device__ __forceinline__ const uint8_t* window_codes(const AttnArgs& a, int64_t w) {
+  if (kTree && w >= (int64_t)a.B * a.swa_cap) return a.tree_codes + (w - (int64_t)a.B * a.swa_cap) * kD;
+  return a.swa_codes + w * kD;
+}
+template <bool kTree>
+__device__ __forceinline__ const float* window_scale(const AttnArgs& a, int64_t w) {
+  if (kTree && w >= (int64_t)a.B * a.swa_cap) return a.tree_scales + (w - (int64_t)a.B * a.swa_cap);
+  return a.swa_scales + w;
+}
 // A key stored as an FP8 row: a window row, or a main-KV entry in the FP8 format.
 template <bool kFp8>
 __device__ __forceinline__ bool fp8_row_key(int32_t src) {
@@ -184,11 +195,11 @@ __device__ __forceinline__ bool fp8_row_key(int32_t src) {
 // 16 bytes, in v[SL] (all four slices are requested together).  FP8 row: 32
 // bytes, in v[2 (SL & 1)] and the next (slices 0 and 1 are requested together,
 // slices 2 and 3 reuse their registers once 0 and 1 are stored).
-template <int SL, bool kFp8>
+template <int SL, bool kFp8, bool kTree>
 __device__ __forceinline__ void load_slice(const AttnArgs& a, int32_t src, int qd, KeyBytes& kb) {
   if (src == -1) return;
   if (fp8_row_key<kFp8>(src)) {
-    const uint8_t* p = (src <= -2 ? a.swa_codes + (-2 - (int64_t)src) * kD : a.kv_codes + (int64_t)src * kD) +
+    const uint8_t* p = (src <= -2 ? window_codes<kTree>(a, -2 - (int64_t)src) : a.kv_codes + (int64_t)src * kD) +
                        32 * qd + 128 * SL;
     kb.v[2 * (SL & 1)] = ld_gather16(p);
     kb.v[2 * (SL & 1) + 1] = ld_gather16(p + 16);
@@ -198,18 +209,18 @@ __device__ __forceinline__ void load_slice(const AttnArgs& a, int32_t src, int q
 }
 // Dequantisation scale of an FP8 row (a window row, or a main-KV entry in the FP8
 // format), times 2^-f (see window_exp); 0 for an MXFP4 entry or no key.
-template <bool kFp8>
+template <bool kFp8, bool kTree>
 __device__ __forceinline__ float load_wscale(const AttnArgs& a, int32_t src) {
   float sw;
-  if (src <= -2) sw = ld_gather4f(a.swa_scales + (-2 - (int64_t)src));
+  if (src <= -2) sw = ld_gather4f(window_scale<kTree>(a, -2 - (int64_t)src));
   else if (kFp8 && src >= 0) sw = ld_gather4f(reinterpret_cast<const float*>(a.kv_scales) + src);
   else return 0.f;
   return sw * pow2i(-window_exp(sw));
 }
 // Exponent f of a key's FP8 scale (0 for MXFP4 entries and missing keys).
-template <bool kFp8>
+template <bool kFp8, bool kTree>
 __device__ __forceinline__ int key_exp(const AttnArgs& a, int32_t src) {
-  if (src <= -2) return window_exp(__ldg(a.swa_scales + (-2 - (int64_t)src)));
+  if (src <= -2) return window_exp(__ldg(window_scale<kTree>(a, -2 - (int64_t)src)));
   if (kFp8 && src >= 0) return window_exp(__ldg(reinterpret_cast<const float*>(a.kv_scales) + src));
   return 0;
 }
@@ -262,8 +273,11 @@ __device__ __forceinline__ void store_slice(const AttnArgs& a, const KeyBytes& k
 // window rows from raw position w_first -- to a main-KV slot (page table) or a
 // window row, or -1 past the list [.., kk_end) or in an unused selection slot.
 // The index load does not wait for n_sel when sel_cap is fixed (the cluster path).
+// With a tree, window row w_first + i is the token's ancestor of that position from
+// position `ctx` on (and the window's rows end there).
+template <bool kTree>
 __device__ __forceinline__ int32_t key_source(const AttnArgs& a, int64_t row, int b, int kk, int n_sel, int sel_off,
-                                              int sel_cap, int kk_end, int nv, int w_first, int pos0, bool report,
+                                              int sel_cap, int kk_end, int nv, int w_first, int pos0, int ctx, bool report,
                                               uint32_t* status) {
   if (kk >= kk_end) return -1;
   if (kk < sel_cap) {
@@ -280,7 +294,17 @@ __device__ __forceinline__ int32_t key_source(const AttnArgs& a, int64_t row, in
     }
     return p * kPage + (j & (kPage - 1));
   }
-  return (int32_t)(-2 - ((int64_t)b * a.swa_cap + (w_first + (kk - sel_cap) - pos0)));
+  const int p = w_first + (kk - sel_cap);
+  if (kTree && p >= ctx) {
+    const int node = p - ctx < a.max_depth ? __ldg(a.path + row * a.max_depth + (p - ctx)) : -1;
+    if (node < 0 || node >= a.Tq) {
+      if (report) raise_status(status, CSA2_STATUS_BAD_INDEX);
+      return -1;
+    }
+    return (int32_t)(-2 - ((int64_t)a.B * a.swa_cap + (int64_t)b * a.Tq + node));
+  }
+  if (kTree && (p < pos0 || p - pos0 >= a.swa_cap)) return -1;   // not held by the buffer
+  return (int32_t)(-2 - ((int64_t)b * a.swa_cap + (p - pos0)));
 }
 
 // Scores of the thread's key for heads 16*hg .. +15 in the log2 domain, as
@@ -322,7 +346,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 
 
-template <bool kFp8>
+template <bool kFp8, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -343,7 +367,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   pdl_trigger();
   // ---- before the previous kernel of the step is done: the token's own inputs
   // (scalars, Q rows), barriers, tensor memory and the Q operand
-  const int t = a.q_pos[row];
+  const int t = kTree ? max(a.q_pos[row], -1) : a.q_pos[row];   // (-1: no node of the tree)
   const int n_ent = a.n_entries[b];
   const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
   uint4 qv[8];   // unit = (head, 8 dims); 8 heads of a unit group share a core matrix
@@ -413,12 +437,18 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     }
   }
   // the window rows of the token: raw positions max(0, t-W+1, pos0) .. min(t, last row held)
-  const int w_lo = max(max(0, t - a.W + 1), pos0);
-  const int w_hi = min(t, pos0 + a.swa_cap - 1);
+  int w_lo = max(max(0, t - a.W + 1), pos0);
+  int w_hi = min(t, pos0 + a.swa_cap - 1);
+  int ctx = 0;
+  if (kTree) {   // from the first position that the buffer holds (or the first ancestor) to the token itself
+    ctx = max(0, a.ctx_len[b]);
+    w_lo = max(max(0, t - a.W + 1), min(a.swa_cap > 0 ? pos0 : INT_MAX, ctx));
+    w_hi = t;
+  }
   const int n_win = max(0, w_hi - w_lo + 1);
   // ---- the selection (and the window rows) come from earlier kernels of the step
   pdl_wait();
-  int n_sel = a.cnt[row];
+  int n_sel = kTree && t < 0 ? 0 : a.cnt[row];
   const int nv = n_visible(n_ent, t);
   if (n_sel < 0 || n_sel > a.K) {
     if (tid == 0 && rank == 0) raise_status(status, CSA2_STATUS_BAD_COUNT);
@@ -443,17 +473,17 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   // key's later chunks are shared out among its four threads.
   int32_t cur_src = -1;
   if (!mma_warp && n_my > 0) {
-    cur_src = key_source(a, row, b, kb0 + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, qd == 0, status);
+    cur_src = key_source<kTree>(a, row, b, kb0 + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, ctx, qd == 0, status);
     if (qd == 0) {
       sm.slot[key] = cur_src;
-      sm.kexp[key] = (int8_t)key_exp<kFp8>(a, cur_src);
+      sm.kexp[key] = (int8_t)key_exp<kFp8, kTree>(a, cur_src);
     }
     for (int c = qd + 1; c < n_my; c += 4) {
       const int32_t src =
-          key_source(a, row, b, kb0 + c * kChunk + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, true,
-                     status);
+          key_source<kTree>(a, row, b, kb0 + c * kChunk + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, ctx, true,
+                            status);
       sm.slot[c * kChunk + key] = src;
-      sm.kexp[c * kChunk + key] = (int8_t)key_exp<kFp8>(a, src);
+      sm.kexp[c * kChunk + key] = (int8_t)key_exp<kFp8, kTree>(a, src);
     }
   }
   // ---- the first chunk's packed bytes
@@ -461,14 +491,14 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   uint2 cur_sc = make_uint2(0, 0);
   KeyBytes kb;
   if (!mma_warp && n_my > 0) {
-    load_slice<0, kFp8>(a, cur_src, qd, kb);
-    load_slice<1, kFp8>(a, cur_src, qd, kb);
+    load_slice<0, kFp8, kTree>(a, cur_src, qd, kb);
+    load_slice<1, kFp8, kTree>(a, cur_src, qd, kb);
     if (!fp8_row_key<kFp8>(cur_src)) {
-      load_slice<2, kFp8>(a, cur_src, qd, kb);
-      load_slice<3, kFp8>(a, cur_src, qd, kb);
+      load_slice<2, kFp8, kTree>(a, cur_src, qd, kb);
+      load_slice<3, kFp8, kTree>(a, cur_src, qd, kb);
       cur_sc = load_scales(a, cur_src, qd);
     }
-    cur_wsc = load_wscale<kFp8>(a, cur_src);
+    cur_wsc = load_wscale<kFp8, kTree>(a, cur_src);
   }
   tc::fence_async_smem();
   tc::tc_fence_before();
@@ -535,7 +565,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
       const uint32_t pr = ((qd >> 1) ? w1 : w0) >> (16 * (qd & 1));                      \
       if (wok) store_slice<SL, kFp8>(a, kb, pr & 0xFFFFu, cur_src, cur_wsc, key, qd, ktile); \
       /* FP8 rows: slices 2 and 3 of this chunk reuse the registers of 0 and 1 */        \
-      if (SL < 2 && fp8_row_key<kFp8>(cur_src)) load_slice<(SL + 2) & 3, kFp8>(a, cur_src, qd, kb); \
+      if (SL < 2 && fp8_row_key<kFp8>(cur_src)) load_slice<(SL + 2) & 3, kFp8, kTree>(a, cur_src, qd, kb); \
     }                                                                                    \
     tc::fence_async_smem();                                                              \
     __syncwarp();                                                                        \
@@ -548,17 +578,17 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
 #undef CSA2_SLICE
       // the next chunk's bytes, requested together once this chunk's tile is written
       if (it + 1 < n_my) {
-        load_slice<0, kFp8>(a, nxt_src, qd, kb);
-        load_slice<1, kFp8>(a, nxt_src, qd, kb);
+        load_slice<0, kFp8, kTree>(a, nxt_src, qd, kb);
+        load_slice<1, kFp8, kTree>(a, nxt_src, qd, kb);
         if (!fp8_row_key<kFp8>(nxt_src)) {
-          load_slice<2, kFp8>(a, nxt_src, qd, kb);
-          load_slice<3, kFp8>(a, nxt_src, qd, kb);
+          load_slice<2, kFp8, kTree>(a, nxt_src, qd, kb);
+          load_slice<3, kFp8, kTree>(a, nxt_src, qd, kb);
         }
       }
       const bool valid = sm.slot[it * kChunk + kc] != -1;   // the softmax thread's key
       const int fk = sm.kexp[it * kChunk + kc];
       cur_src = nxt_src;
-      cur_wsc = load_wscale<kFp8>(a, nxt_src);
+      cur_wsc = load_wscale<kFp8, kTree>(a, nxt_src);
       if (!kFp8) cur_sc = load_scales(a, nxt_src, qd);
 
       // ---- softmax of the chunk: this thread's key, heads 16*hg .. +15
@@ -677,7 +707,12 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int h = c + j;
-          if (hb + h < a.Hq) a.O[(row * a.Hq + hb + h) * kD + 128 * mt + 32 * q4 + lane] = have_o ? o[j] * sm.fac[h] : 0.f;
+          const float v = have_o ? o[j] * sm.fac[h] : 0.f;
+          const int64_t at = (row * a.Hq + hb + h) * kD + 128 * mt + 32 * q4 + lane;
+          if (hb + h < a.Hq) {
+            if (kTree) a.O16[at] = (uint16_t)(f32x2_bf16x2(v, 0.f) & 0xFFFFu);
+            else a.O[at] = v;
+          }
         }
       }
     }
@@ -752,7 +787,11 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
           const float f = facq[q * kHeads + h];
           acc.x += r[u][q].x * f; acc.y += r[u][q].y * f; acc.z += r[u][q].z * f; acc.w += r[u][q].w * f;
         }
-        if (hb + h < a.Hq) *reinterpret_cast<float4*>(a.O + (row * a.Hq + hb + h) * kD + (e % (kD / 4)) * 4) = acc;
+        const int64_t at = (row * a.Hq + hb + h) * kD + (e % (kD / 4)) * 4;
+        if (hb + h < a.Hq) {
+          if (kTree) *reinterpret_cast<uint2*>(a.O16 + at) = make_uint2(f32x2_bf16x2(acc.x, acc.y), f32x2_bf16x2(acc.z, acc.w));
+          else *reinterpret_cast<float4*>(a.O + at) = acc;
+        }
       }
     }
     cluster_sync();   // no CTA leaves while another still reads its shared memory
@@ -768,7 +807,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
 bool sparse_attn_tc_supported(const AttnArgs& a) {
   return a.d == kD && a.Hq >= 1 && a.Hq <= 2 * kHeads && a.K >= 0 && a.W >= 0 &&
          (int64_t)a.K + a.W <= (int64_t)kMaxChunks * kChunk && a.n_pages * kPage < ((int64_t)1 << 31) &&
-         (int64_t)a.B * a.swa_cap < ((int64_t)1 << 31) - 2;
+         (int64_t)a.B * ((int64_t)a.swa_cap + (a.path ? a.Tq : 0)) < ((int64_t)1 << 31) - 2;
 }
 
 cudaError_t launch_sparse_attn_tc(const AttnArgs& a, cudaStream_t s) {
@@ -783,7 +822,8 @@ cudaError_t launch_sparse_attn_tc(const AttnArgs& a, cudaStream_t s) {
   if (rows < sms && max_chunks > 1)
     n_split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(max_chunks, kMaxSplit), sms / rows));
   const size_t smem = sizeof(TcSmem);
-  auto kernel = a.kv_fp8 ? k_sparse_attn_tc<true> : k_sparse_attn_tc<false>;
+  auto kernel = a.path ? (a.kv_fp8 ? k_sparse_attn_tc<true, true> : k_sparse_attn_tc<false, true>)
+                       : (a.kv_fp8 ? k_sparse_attn_tc<true, false> : k_sparse_attn_tc<false, false>);
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   if (rows * n_split >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;

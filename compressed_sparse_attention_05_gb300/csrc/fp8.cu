@@ -1,0 +1,579 @@
+// FP8 rows with one scale per block of 128 columns (reading R18) and their matrix product (R19):
+//   C[m][n] = sum_kb sa[m][kb] sb[n/128][kb] sum_{k in block kb} a[m][k] b[n][k].
+//
+// A block's 128 products are summed by the tensor cores (tcgen05.mma, kind::f8f6f4, E4M3 x E4M3, fp32
+// accumulation) into a tensor-memory accumulator of their own; the accumulator is then read back, multiplied by the
+// block's two scales and added to the sum in registers, while the tensor cores work on the next block's.
+//
+// k_matmul_fp8_wide (more than 64 rows of A): tiles of 128 rows of A x 256 rows of B.  A row of A is a lane of the
+//   accumulator, so a thread has one scale per block: sa[its row] sb[its 128 columns].
+// k_matmul_fp8_few (up to 64 rows of A): the rows of B, the weights, are the MMA's M side, 128 at a time, and the
+//   few rows of A its N side, so that no part of the tensor cores' work and of shared memory goes to rows that are
+//   not there, and 128 B-rows x 128 columns (16 KB) per block stream through a deep ring.  A thread has a weight row
+//   and all rows of A; their scales come from the lanes of its warp.
+// Where the tiles do not fill the SMs, the blocks of K are split over several CTAs, which leave fp32 partial sums
+// that k_matmul_fp8_sum adds in order.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "operands.cuh"
+#include "tc.cuh"
+#include "tma.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kBlock = 128;                // columns that share a scale (and rows of B)
+
+// ---- packing --------------------------------------------------------------------------------------
+// amax of a block's 128 values, a = max(amax, 2^-100); scale a / 448, codes E4M3_rne_satfinite(x * (448 / a)).
+// Bytes bound it: a quarter warp's loads of 16 bytes a lane, four blocks in flight.
+constexpr int kPackThreads = 256;
+constexpr float kFloor = 0x1p-100f;
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{ .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n mov.b32 %0, {lo, hi}; }"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// kF32: 32 lanes share a block, 4 columns each; bf16: 16 lanes, 8 columns each.
+template <bool kF32>
+__global__ void __launch_bounds__(kPackThreads) k_pack_fp8_blocks(const void* x, int64_t stride, int64_t rows, int K, int kb_n, int64_t blocks,
+                                                                  uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int kLanes = kF32 ? 32 : 16, kCols = kBlock / kLanes, kMany = 4;
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes;
+  constexpr int kPer = 32 / kLanes;              // blocks of a warp
+  const int64_t step = (int64_t)gridDim.x * (kPackThreads / kLanes);
+  // (the loop runs on the warp's first block, so that its lanes stay together)
+  for (int64_t w0 = ((int64_t)blockIdx.x * kPackThreads + threadIdx.x) / 32 * kPer; w0 < blocks; w0 += kMany * step) {
+    uint4 v[kMany];
+    int64_t row[kMany];
+    int col[kMany];
+#pragma unroll
+    for (int i = 0; i < kMany; ++i) {
+      const int64_t b = w0 + i * step + sub;
+      row[i] = b / kb_n;
+      col[i] = b < blocks ? (int)(b - row[i] * kb_n) * kBlock + lane * kCols : K;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (col[i] < K) v[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(x) + (row[i] * stride + col[i]) * (kF32 ? 4 : 2));
+    }
+#pragma unroll
+    for (int i = 0; i < kMany; ++i) {
+      const int64_t b = w0 + i * step + sub;
+      float f[kCols];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = word_of(v[i], j);
+        if (kF32) {
+          f[j] = __uint_as_float(w);
+        } else {
+          f[(2 * j) % kCols] = __uint_as_float(w << 16);
+          f[(2 * j + 1) % kCols] = __uint_as_float(w & 0xFFFF0000u);
+        }
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) amax = fmaxf(amax, fabsf(f[j]));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const float a = fmaxf(amax, kFloor), inv = 448.f / a;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) f[j] *= inv;
+      uint8_t* out = codes + row[i] * K + col[i];
+      if (col[i] < K) {
+        if (kF32)
+          *reinterpret_cast<uint32_t*>(out) = e4m3x4(f[0], f[1], f[2], f[3]);
+        else
+          *reinterpret_cast<uint2*>(out) =
+              make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4 % kCols], f[5 % kCols], f[6 % kCols], f[7 % kCols]));
+      }
+      if (lane == 0 && b < blocks) scales[b] = a / 448.f;
+    }
+  }
+}
+
+// ---- the product ------------------------------------------------------------------------------------
+struct MatmulPlan {
+  const float* sa;          // [M][kb]
+  const float* sb;          // [ceil(N / 128)][kb]
+  void* C;                  // [M][N], or null: partial sums
+  float* partial;           // [n_split][M][ld]
+  int64_t ld;
+  int M, N, kb, n_split, f32;
+  int m_tiles, n_tiles;
+};
+
+constexpr uint32_t kIdFp8 = 1u << 4;   // instruction descriptor: fp32 accumulation, E4M3 x E4M3, both K-major
+__host__ __device__ constexpr uint32_t idesc_fp8(int M, int N) { return kIdFp8 | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
+
+__device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// K-major operand rows of 128 bytes as a tensor map writes them with the 128-byte swizzle.
+__device__ __forceinline__ uint64_t desc128(uint32_t saddr) { return tc::smem_desc(saddr, 16, 1024) | ((uint64_t)2 << 61); }
+
+// Bounded wait; on time-out the CTA's abort flag is raised.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 21); ++i) {   // <= 2^21 suspensions of <= 1 us
+    if (tc::mbar_try_wait_sleep(bar, parity, 1000)) return true;
+    if ((i & 63) == 63 && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// (a.x b.x + c.x, a.y b.y + c.y)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// The blocks [k0, k1) of split s.
+__device__ __forceinline__ void split_range(const MatmulPlan& p, int s, int* k0, int* k1) {
+  *k0 = (int)((int64_t)s * p.kb / p.n_split);
+  *k1 = (int)((int64_t)(s + 1) * p.kb / p.n_split);
+}
+
+// Shared by both kernels: the ring of operand stages and the accumulators' barriers.
+template <int kStages, int kStageBytes, int kBufs>
+struct Ring {
+  unsigned char stage[kStages][kStageBytes];   // 1024-aligned
+  uint64_t full[kStages], empty[kStages], acc_full[kBufs], acc_empty[kBufs];
+  uint32_t tmem;
+  int abort;
+};
+template <typename R, int kStages, int kBufs>
+__device__ __forceinline__ void ring_init(R& sm, uint32_t readers) {
+  for (int i = 0; i < kStages; ++i) {
+    tc::mbar_init(&sm.full[i], 1);
+    tc::mbar_init(&sm.empty[i], 1);
+  }
+  for (int i = 0; i < kBufs; ++i) {
+    tc::mbar_init(&sm.acc_full[i], 1);
+    tc::mbar_init(&sm.acc_empty[i], readers);
+  }
+  sm.abort = 0;
+  tc::mbar_fence_init();
+}
+
+// ---- many rows of A ----
+constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2;
+constexpr int kWStageBytes = (kWM + kWN) * kBlock;       // 48 KB
+constexpr int kWSumWarps = 8;
+constexpr int kWThreads = kWSumWarps * 32 + 128;
+constexpr int kWRegs = 168, kWRegsSum = 232, kWRegsMisc = 40;   // 2 x 232 + 40 = 3 x 168
+static_assert(2 * kWRegsSum + kWRegsMisc <= 3 * kWRegs, "register split");
+using WideSmem = Ring<kWStages, kWStageBytes, kWBufs>;
+
+template <typename T>
+__device__ __forceinline__ void store_row(T* out, const float2 (&acc)[64], int n_left, bool vec);
+template <>
+__device__ __forceinline__ void store_row<float>(float* out, const float2 (&acc)[64], int n_left, bool vec) {
+  if (vec && n_left >= 128) {
+#pragma unroll
+    for (int j = 0; j < 64; j += 2) *reinterpret_cast<float4*>(out + 2 * j) = make_float4(acc[j].x, acc[j].y, acc[j + 1].x, acc[j + 1].y);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+      if (2 * j < n_left) out[2 * j] = acc[j].x;
+      if (2 * j + 1 < n_left) out[2 * j + 1] = acc[j].y;
+    }
+  }
+}
+template <>
+__device__ __forceinline__ void store_row<uint16_t>(uint16_t* out, const float2 (&acc)[64], int n_left, bool vec) {
+  if (vec && n_left >= 128) {
+#pragma unroll
+    for (int j = 0; j < 64; j += 4)
+      *reinterpret_cast<uint4*>(out + 2 * j) = make_uint4(f32x2_bf16x2(acc[j].x, acc[j].y), f32x2_bf16x2(acc[j + 1].x, acc[j + 1].y),
+                                                          f32x2_bf16x2(acc[j + 2].x, acc[j + 2].y), f32x2_bf16x2(acc[j + 3].x, acc[j + 3].y));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+      const uint32_t v = f32x2_bf16x2(acc[j].x, acc[j].y);
+      if (2 * j < n_left) out[2 * j] = (uint16_t)(v & 0xFFFFu);
+      if (2 * j + 1 < n_left) out[2 * j + 1] = (uint16_t)(v >> 16);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kWThreads, 1)
+k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ MatmulPlan p,
+                  uint32_t* status) {
+  extern __shared__ unsigned char smem_raw[];
+  WideSmem& sm = *reinterpret_cast<WideSmem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (p.partial) pdl_trigger();   // k_matmul_fp8_sum waits for this kernel; C is not announced before it is complete
+  if (tid == 0) ring_init<WideSmem, kWStages, kWBufs>(sm, kWSumWarps);
+  if (warp == kWSumWarps) tc::tmem_alloc(&sm.tmem, kWBufs * kWN);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tm = sm.tmem;
+  volatile int* abort = &sm.abort;
+  pdl_wait();
+  const int64_t items = (int64_t)p.m_tiles * p.n_tiles * p.n_split;
+
+  if (warp >= kWSumWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsMisc));
+    if (warp == kWSumWarps && lane == 0) {
+      // ================= operand copies =================
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        const int s = (int)(it % p.n_split);
+        const int64_t tile = it / p.n_split;
+        const int m0 = (int)(tile % p.m_tiles) * kWM, n0 = (int)(tile / p.m_tiles) * kWN;
+        int k0, k1;
+        split_range(p, s, &k0, &k1);
+        for (int k = k0; k < k1; ++k, ++n) {
+          const uint32_t st = n % kWStages, use = n / kWStages;
+          if (use > 0 && !wait_bar(&sm.empty[st], (use - 1) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc::mbar_arrive_expect_tx(&sm.full[st], kWStageBytes);
+          tma::load_2d(sm.stage[st], &amap, k * kBlock, m0, &sm.full[st]);
+          tma::load_2d(sm.stage[st] + kWM * kBlock, &bmap, k * kBlock, n0, &sm.full[st]);
+        }
+      }
+      for (uint32_t i = n > kWStages ? n - kWStages : 0; i < n; ++i)   // every issued copy lands before exit
+        for (uint32_t w = 0; w < (1u << 22); ++w)
+          if (tc::mbar_try_wait(&sm.full[i % kWStages], (i / kWStages) & 1)) break;
+    } else if (warp == kWSumWarps + 1 && lane == 0) {
+      // ================= MMA issue =================
+      constexpr uint32_t idesc = idesc_fp8(kWM, kWN);
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        int k0, k1;
+        split_range(p, (int)(it % p.n_split), &k0, &k1);
+        for (int k = k0; k < k1; ++k, ++n) {
+          const uint32_t st = n % kWStages, buf = n % kWBufs, use = n / kWBufs;
+          if ((use > 0 && !wait_bar(&sm.acc_empty[buf], (use - 1) & 1, abort)) || !wait_bar(&sm.full[st], (n / kWStages) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t sa = tc::smem_addr(sm.stage[st]), sb = sa + kWM * kBlock;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_fp8(tm + buf * kWN, desc128(sa + 32 * ks), desc128(sb + 32 * ks), idesc, ks > 0);
+          tc::mma_commit(&sm.empty[st]);
+          tc::mma_commit(&sm.acc_full[buf]);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================= scales and sums: thread = row of A, 128 columns =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsSum));
+    const int lq = warp & 3, half = warp >> 2;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+      const int s = (int)(it % p.n_split);
+      const int64_t tile = it / p.n_split;
+      const int m = (int)(tile % p.m_tiles) * kWM + 32 * lq + lane, n0 = (int)(tile / p.m_tiles) * kWN + 128 * half;
+      int k0, k1;
+      split_range(p, s, &k0, &k1);
+      const bool live = m < p.M && n0 < p.N;
+      const float* sa = p.sa + (int64_t)(live ? m : 0) * p.kb;
+      const float* sb = p.sb + (int64_t)(live ? n0 / kBlock : 0) * p.kb;
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+      float next = k0 < k1 ? __ldg(sa + k0) * __ldg(sb + k0) : 0.f;
+      for (int k = k0; k < k1; ++k, ++n) {
+        const float sc = next;
+        const uint32_t buf = n % kWBufs;
+        if (k + 1 < k1) next = __ldg(sa + k + 1) * __ldg(sb + k + 1);
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.acc_full[buf], (n / kWBufs) & 1, abort));
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tm + ((uint32_t)(32 * lq) << 16) + buf * kWN + 128 * half + 32 * c, r);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            acc[16 * c + j] = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), make_float2(sc, sc), acc[16 * c + j]);
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.acc_empty[buf]);
+      }
+      if (!ok || !live) continue;
+      const int left = p.N - n0;
+      if (p.partial)
+        store_row<float>(p.partial + ((int64_t)s * p.M + m) * p.ld + n0, acc, left, true);
+      else if (p.f32)
+        store_row<float>(static_cast<float*>(p.C) + (int64_t)m * p.N + n0, acc, left, p.N % 4 == 0);
+      else
+        store_row<uint16_t>(static_cast<uint16_t*>(p.C) + (int64_t)m * p.N + n0, acc, left, p.N % 8 == 0);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kWSumWarps) tc::tmem_dealloc(tm, kWBufs * kWN);
+  if (tid == 0 && *abort) raise_status(status, CSA2_STATUS_TIMEOUT);
+}
+
+// ---- few rows of A ----
+constexpr int kFN = 128, kFBufs = 4;                // rows of B in a tile; accumulators
+constexpr int kFThreads = 192;                      // 4 warps of sums, copies, MMA
+template <int kRows> constexpr int kFStageBytes = (kFN + kRows) * kBlock;
+template <int kRows> constexpr int kFStages = 200 * 1024 / kFStageBytes<kRows>;
+template <int kRows> using FewSmem = Ring<kFStages<kRows>, kFStageBytes<kRows>, kFBufs>;
+
+template <int kRows>
+__global__ void __launch_bounds__(kFThreads, 1)
+k_matmul_fp8_few(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ MatmulPlan p,
+                 uint32_t* status) {
+  extern __shared__ unsigned char smem_raw[];
+  using Smem = FewSmem<kRows>;
+  constexpr int kStages = kFStages<kRows>, kBytes = kFStageBytes<kRows>;
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (p.partial) pdl_trigger();
+  constexpr uint32_t kCols = kFBufs * kRows;        // 64, 128 or 256 columns
+  if (tid == 0) ring_init<Smem, kStages, kFBufs>(sm, 4);
+  if (warp == 4) tc::tmem_alloc(&sm.tmem, kCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tm = sm.tmem;
+  volatile int* abort = &sm.abort;
+  pdl_wait();
+  const int64_t items = (int64_t)p.n_tiles * p.n_split;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        int k0, k1;
+        split_range(p, (int)(it % p.n_split), &k0, &k1);
+        const int n0 = (int)(it / p.n_split) * kFN;
+        for (int k = k0; k < k1; ++k, ++n) {
+          const uint32_t st = n % kStages, use = n / kStages;
+          if (use > 0 && !wait_bar(&sm.empty[st], (use - 1) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc::mbar_arrive_expect_tx(&sm.full[st], kBytes);
+          tma::load_2d(sm.stage[st], &bmap, k * kBlock, n0, &sm.full[st]);
+          tma::load_2d(sm.stage[st] + kFN * kBlock, &amap, k * kBlock, 0, &sm.full[st]);
+        }
+      }
+      for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+        for (uint32_t w = 0; w < (1u << 22); ++w)
+          if (tc::mbar_try_wait(&sm.full[i % kStages], (i / kStages) & 1)) break;
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_fp8(kFN, kRows);
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        int k0, k1;
+        split_range(p, (int)(it % p.n_split), &k0, &k1);
+        for (int k = k0; k < k1; ++k, ++n) {
+          const uint32_t st = n % kStages, buf = n % kFBufs, use = n / kFBufs;
+          if ((use > 0 && !wait_bar(&sm.acc_empty[buf], (use - 1) & 1, abort)) || !wait_bar(&sm.full[st], (n / kStages) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t sw = tc::smem_addr(sm.stage[st]), sx = sw + kFN * kBlock;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_fp8(tm + buf * kRows, desc128(sw + 32 * ks), desc128(sx + 32 * ks), idesc, ks > 0);
+          tc::mma_commit(&sm.empty[st]);
+          tc::mma_commit(&sm.acc_full[buf]);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================= scales and sums: thread = row of B, all rows of A =================
+    constexpr int kHeld = (kRows + 31) / 32;          // rows of A whose scales a lane holds
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+      const int s = (int)(it % p.n_split), n0 = (int)(it / p.n_split) * kFN;
+      int k0, k1;
+      split_range(p, s, &k0, &k1);
+      const float* sb = p.sb + (int64_t)(n0 / kBlock) * p.kb;
+      auto scale = [&](int k, int h) { return lane + 32 * h < p.M ? __ldg(p.sa + (int64_t)(lane + 32 * h) * p.kb + k) * __ldg(sb + k) : 0.f; };
+      float acc[kRows], next[kHeld];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) acc[j] = 0.f;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) next[h] = k0 < k1 ? scale(k0, h) : 0.f;
+      for (int k = k0; k < k1; ++k, ++n) {
+        float sc[kHeld];
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+          sc[h] = next[h];
+          if (k + 1 < k1) next[h] = scale(k + 1, h);
+        }
+        const uint32_t buf = n % kFBufs;
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.acc_full[buf], (n / kFBufs) & 1, abort));
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kRows; c += 16) {
+          float r[16];
+          tc::tmem_ld16(tm + ((uint32_t)(32 * warp) << 16) + buf * kRows + c, r);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(r[j], __shfl_sync(0xffffffffu, sc[(c + j) / 32], (c + j) & 31), acc[c + j]);
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.acc_empty[buf]);
+      }
+      const int col = n0 + 32 * warp + lane;
+      if (!ok || col >= p.N) continue;
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        if (j >= p.M) break;
+        if (p.partial) p.partial[((int64_t)s * p.M + j) * p.ld + col] = acc[j];
+        else if (p.f32) static_cast<float*>(p.C)[(int64_t)j * p.N + col] = acc[j];
+        else static_cast<uint16_t*>(p.C)[(int64_t)j * p.N + col] = (uint16_t)(f32x2_bf16x2(acc[j], 0.f) & 0xFFFFu);
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 4) tc::tmem_dealloc(tm, kCols);
+  if (tid == 0 && *abort) raise_status(status, CSA2_STATUS_TIMEOUT);
+}
+
+// The splits' partial sums, in order.
+__global__ void __launch_bounds__(256) k_matmul_fp8_sum(const __grid_constant__ MatmulPlan p) {
+  pdl_wait();
+  const int64_t m = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+  const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (m >= p.M || n >= p.N) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < p.n_split; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(p.partial + ((int64_t)s * p.M + m) * p.ld + n);
+    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+  }
+  const float f[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (n + j >= p.N) break;
+    if (p.f32) static_cast<float*>(p.C)[m * p.N + n + j] = f[j];
+    else static_cast<uint16_t*>(p.C)[m * p.N + n + j] = (uint16_t)(f32x2_bf16x2(f[j], 0.f) & 0xFFFFu);
+  }
+}
+constexpr int kSms = 152;
+constexpr int kFewRows = 64;
+
+int splits(int M, int N, int K) {
+  const int64_t kb = (K + kBlock - 1) / kBlock;
+  const int64_t tiles = M <= kFewRows ? (N + kFN - 1) / kFN : (int64_t)((M + kWM - 1) / kWM) * ((N + kWN - 1) / kWN);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kb, kSms / std::max<int64_t>(1, tiles)));
+}
+int64_t partial_ld(int N) { return ((int64_t)N + 127) / 128 * 128; }
+
+bool row_map(CUtensorMap* map, const uint8_t* p, int rows, int K, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)K};
+  const cuuint32_t box[2] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return tensor_map_encoder() &&
+         tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Kernel>
+cudaError_t launch_matmul(Kernel kernel, size_t smem, int threads, int64_t items, int sms, const CUtensorMap& am, const CUtensorMap& bm,
+                          const MatmulPlan& p, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_step(kernel, dim3((unsigned)std::min<int64_t>(items, sms)), dim3(threads), smem, s, am, bm, p, status_word());
+}
+
+}  // namespace
+
+cudaError_t launch_pack_fp8_blocks(const void* x, int dtype, int64_t stride, int64_t rows, int K, uint8_t* codes, float* scales, cudaStream_t s) {
+  const int kb = (K + kBlock - 1) / kBlock;
+  const int64_t blocks = rows * kb;
+  const int per = kPackThreads / (dtype == CSA2_F32 ? 32 : 16);
+  const int64_t grid = std::min<int64_t>((blocks + per - 1) / per, 152 * 8);
+  return dtype == CSA2_F32
+             ? launch_step(k_pack_fp8_blocks<true>, dim3((unsigned)grid), dim3(kPackThreads), 0, s, x, stride, rows, K, kb, blocks, codes, scales)
+             : launch_step(k_pack_fp8_blocks<false>, dim3((unsigned)grid), dim3(kPackThreads), 0, s, x, stride, rows, K, kb, blocks, codes, scales);
+}
+
+size_t matmul_fp8_workspace_bytes(int M, int N, int K) {
+  const int n = splits(M, N, K);
+  return n > 1 ? (size_t)n * M * partial_ld(N) * sizeof(float) : 0;
+}
+
+cudaError_t launch_matmul_fp8(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int M, int N, int K, void* C, int f32, void* ws,
+                              cudaStream_t s) {
+  MatmulPlan p = {};
+  p.sa = sa; p.sb = sb; p.C = C; p.M = M; p.N = N; p.kb = (K + kBlock - 1) / kBlock; p.f32 = f32;
+  p.n_split = splits(M, N, K);
+  p.ld = partial_ld(N);
+  p.partial = p.n_split > 1 ? static_cast<float*>(ws) : nullptr;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  CUtensorMap am, bm;
+  const bool few = M <= kFewRows;
+  const int rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  if (!row_map(&am, a, M, K, few ? rows : kWM) || !row_map(&bm, b, N, K, few ? kFN : kWN)) return cudaErrorInvalidValue;
+  if (few) {
+    p.m_tiles = 1;
+    p.n_tiles = (N + kFN - 1) / kFN;
+    const int64_t items = (int64_t)p.n_tiles * p.n_split;
+    if (rows == 16) e = launch_matmul(k_matmul_fp8_few<16>, sizeof(FewSmem<16>) + 1024, kFThreads, items, sms, am, bm, p, s);
+    else if (rows == 32) e = launch_matmul(k_matmul_fp8_few<32>, sizeof(FewSmem<32>) + 1024, kFThreads, items, sms, am, bm, p, s);
+    else e = launch_matmul(k_matmul_fp8_few<64>, sizeof(FewSmem<64>) + 1024, kFThreads, items, sms, am, bm, p, s);
+  } else {
+    p.m_tiles = (M + kWM - 1) / kWM;
+    p.n_tiles = (N + kWN - 1) / kWN;
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, k_matmul_fp8_wide);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < kWRegs) return cudaErrorInvalidConfiguration;   // the register split would wait forever
+    e = launch_matmul(k_matmul_fp8_wide, sizeof(WideSmem) + 1024, kWThreads, (int64_t)p.m_tiles * p.n_tiles * p.n_split, sms, am, bm, p, s);
+  }
+  if (e != cudaSuccess || p.n_split == 1) return e;
+  const unsigned gy = (unsigned)std::min(M, 32768);
+  return launch_step(k_matmul_fp8_sum, dim3((unsigned)((N + 1023) / 1024), gy, (unsigned)((M + gy - 1) / gy)), dim3(256), 0, s, p);
+}
+
+}  // namespace csa2

@@ -222,6 +222,13 @@ struct AttnArgs {
   float* O;                   // [rows][Hq][d]
   float* lse;                 // [rows][Hq] or null
   int kv_fp8;                 // main KV as FP8 rows (E4M3 [d] + fp32 scale per entry)
+  // a tree of drafted tokens (path != null): window positions from ctx_len[b] on are the token's own ancestors
+  const int32_t* path;        // [rows][max_depth] node of the token's path at every depth
+  const int32_t* ctx_len;     // [B] committed tokens
+  const uint8_t* tree_codes;  // [rows][d]
+  const float* tree_scales;   // [rows]
+  int max_depth;
+  uint16_t* O16;              // [rows][Hq][d] bf16, in the place of O
 };
 cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t s);
 // ---- attention_tc.cu: tcgen05 kernel for d = 512 (every Hq and K + W the ABI admits)
@@ -281,5 +288,54 @@ struct EvictArgs {
 };
 size_t evict_workspace_bytes(int B, int max_entries);
 cudaError_t launch_evict(const EvictArgs& a, void* ws, cudaStream_t s);
+
+// ---- plan.cu -----------------------------------------------------------------------
+struct PagePlanArgs {
+  int32_t* page_table;        // [B][max_pages]
+  int32_t* held;              // [B]
+  int32_t* free_pages;        // [n_pages]
+  int32_t* n_free;
+  int64_t n_pages;
+  const int32_t* seq_len;     // [B]
+  const int32_t* n_new;       // [B]
+  const int32_t* shift;       // [B] or null
+  int32_t* seq_len_out;       // [B], may be seq_len
+  int32_t* n_entries;         // [B]
+  int32_t* first_entry;       // [B]
+  int32_t* granted;           // [B] or null
+  int32_t* q_pos;             // [B][Tq] or null
+  int64_t* slots;             // [B][max_new] or null
+  int B, Tq, max_pages, max_new;
+};
+size_t page_plan_workspace_bytes(int B);
+cudaError_t launch_page_plan(const PagePlanArgs& a, void* ws, cudaStream_t s);
+int tree_plan_max_nodes();
+cudaError_t launch_tree_plan(int B, int Tq, int max_depth, const int32_t* parent, const int32_t* ctx_len, int32_t* q_pos,
+                             int32_t* path, cudaStream_t s);
+
+// ---- rope.cu -----------------------------------------------------------------------
+constexpr int kRopeMaxPairs = 256;
+struct RopeTable {
+  uint64_t g[kRopeMaxPairs];  // turns per position, 0.64 fixed point
+};
+cudaError_t launch_rope_table(const RopeTable& t, int pairs, uint64_t* out, cudaStream_t s);
+struct RopeArgs {
+  const void* x;
+  void* y;
+  int64_t x_token, x_head, y_token, y_head;   // strides in elements
+  int64_t rows;
+  int heads, d, start, r, layout, inverse, x_dtype, y_dtype;
+  float amplitude;
+  const int32_t* positions;   // [rows]
+  const uint64_t* table;      // [r / 2]
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
+// ---- fp8.cu ------------------------------------------------------------------------
+cudaError_t launch_pack_fp8_blocks(const void* x, int dtype, int64_t stride, int64_t rows, int K, uint8_t* codes, float* scales,
+                                   cudaStream_t s);
+size_t matmul_fp8_workspace_bytes(int M, int N, int K);
+cudaError_t launch_matmul_fp8(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int M, int N, int K, void* C,
+                              int f32, void* ws, cudaStream_t s);
 
 }  // namespace csa2

@@ -126,6 +126,36 @@
  *      all.  Survivors below index keep stay where they are; those above, in
  *      index order, fill the holes below keep, in index order.  So an entry's
  *      index no longer gives its position: entry_pos does.
+ *   R17 pages (csa2_page_plan): a sequence of L tokens of which `shift` entries
+ *      were evicted has e = floor(L/4) - shift entries and holds ceil(e/64) pages.
+ *      A step changes L by n_new (negative: drafts that were rejected, or the end
+ *      of the sequence).  The free list is a stack.  First every page that is no
+ *      longer needed goes onto it, in the order of sequences and then of pages;
+ *      then sequences that need more pop them, in the same order.  A sequence
+ *      waits (all of its state stays as it was) if its pages and those of all
+ *      sequences before it that need some are more than there are; who needs
+ *      none never waits.
+ *   R18 FP8 rows (csa2_pack_fp8_blocks): per 128 columns, a = max(amax, 2^-100),
+ *      scale = a / 448 and codes = E4M3_rne_satfinite(x * (448 / a)), each step
+ *      rounded to fp32.  The last block of a row may be shorter.  A block with an
+ *      infinity dequantises to NaN, a NaN stays one by itself.
+ *   R19 product (csa2_matmul_fp8): C[m][n] = sum over blocks kb of
+ *      a_scales[m][kb] * b_scales[n/128][kb] * (sum of the block's code products);
+ *      every block's sum and the sum over blocks are held in fp32, in an order
+ *      that M, N and K fix; C is rounded once.
+ *   R20 rotary positions (csa2_rope): pair i of the r rotated channels turns by
+ *      p * theta_i, theta_i = base^(-2i/r) as in R3; scaled for long contexts:
+ *      LINEAR theta_i / factor; NTK base * factor^(r/(r-2)) in the place of base;
+ *      YARN theta_i (1 - g_i) + theta_i / factor * g_i with g_i = clamp((i - lo) /
+ *      max(hi - lo, 0.001), 0, 1), lo = max(0, floor(c(beta_fast))), hi =
+ *      min(r - 1, ceil(c(beta_slow))), c(n) = r ln(original_len / (2 pi n)) /
+ *      (2 ln base).  HALF pairs channels (i, i + r/2), INTERLEAVED (2i, 2i + 1).
+ *   R21 drafted trees: node i of a sequence continues node parent[i] < i, or the
+ *      committed text (-1); -2 marks a place without a node.  It stands at raw
+ *      position ctx_len + depth.  csa2_tree_attn is R11 with the window rows of
+ *      positions from ctx_len on taken from the node's own ancestors (itself
+ *      among them), and O in bf16.  A place without a node gets O = 0, lse = -inf
+ *      (its selection is not looked at).
  * ---------------------------------------------------------------------------
  */
 #ifndef CSA2_H
@@ -389,6 +419,122 @@ int csa2_sparse_attn(const csa2_dims* dims, const csa2_cache* cache, const csa2_
                      const uint16_t* Q, const int32_t* q_pos, const int32_t* idx,
                      const int32_t* cnt, float softmax_scale, float* O, float* lse,
                      void* stream);
+
+/* ---- the query side of a step: pages, FP8 projections, rotary positions, trees ----
+ * What a step needs around csa2_layer: pages and positions for its tokens, the
+ * projections that give the queries, their rotation, and attention for tokens
+ * that were drafted as a tree. */
+
+/* Pages of a pool and who holds them; all arrays are read and written. */
+typedef struct csa2_page_pool {
+  int32_t* page_table;       /* [B][max_pages]: the array behind csa2_cache.page_table */
+  int32_t* held;             /* [B] pages that a sequence holds: its first `held` places */
+  int32_t* free_pages;       /* [n_pages]: a stack, its bottom first         */
+  int32_t* n_free;           /* [1] pages on the stack                       */
+  int64_t n_pages;           /* pages of the pool (below 2^31)               */
+} csa2_page_pool;
+
+/* Block tables, positions and slots of a step (R17).  seq_len int32 [B] raw tokens
+ * before the step, n_new int32 [B] tokens that it adds (negative: takes away),
+ * shift int32 [B] entries evicted so far or NULL.  Writes the pool, and per sequence
+ * seq_len_out [B] (may be seq_len), n_entries [B] and first_entry [B] (the first
+ * entry that the step writes; n_entries where it writes none), granted [B] (1, or 0
+ * where the sequence waits; NULL: not wanted), q_pos [B][Tq] (raw positions of the
+ * new tokens, -1 behind them; NULL: not wanted) and slots int64 [B][max_new] (64 page
+ * + place of every new entry in the pool, -1 behind them; NULL: not wanted).
+ * Table places at or behind a sequence's pages, and stack places at or behind
+ * n_free, keep whatever they held.  A sequence whose state is impossible (a
+ * negative length, fewer pages held than its entries need, more pages than
+ * max_pages, more new tokens than Tq where q_pos is wanted or new entries than
+ * max_new where slots are) waits and raises CSA2_STATUS_BAD_COUNT; a pool whose
+ * counts cannot be (n_free outside 0 .. n_pages, more released than it lacks)
+ * makes every sequence wait.  A page id outside the pool is passed on, gets no slot
+ * and raises CSA2_STATUS_BAD_PAGE.  After csa2_evict the pages behind the kept
+ * entries come back with the next call (shift says so).  dims: B, Tq, max_pages are
+ * used.  Needs csa2_page_plan_workspace_size() bytes of workspace, which calls that
+ * can overlap must not share. */
+size_t csa2_page_plan_workspace_size(const csa2_dims* dims);
+int csa2_page_plan(const csa2_dims* dims, const csa2_page_pool* pool, const int32_t* seq_len,
+                   const int32_t* n_new, const int32_t* shift, int32_t max_new, int32_t* seq_len_out,
+                   int32_t* n_entries, int32_t* first_entry, int32_t* q_pos, int64_t* slots,
+                   int32_t* granted, void* ws, size_t ws_bytes, void* stream);
+
+/* Rows to FP8 (R18): x bf16 or fp32 (dtype CSA2_BF16 or CSA2_F32) [n_rows][K], rows
+ * row_stride elements apart (a multiple of 16 bytes) -> codes uint8 [n_rows][K],
+ * scales fp32 [n_rows][ceil(K/128)].  K: a multiple of 16. */
+int csa2_pack_fp8_blocks(const void* x, int32_t dtype, int64_t row_stride, int64_t n_rows, int32_t K,
+                         uint8_t* codes, float* scales, void* stream);
+
+/* C = A Bw^T of FP8 rows (R19): A E4M3 [M][K] with a_scales fp32 [M][ceil(K/128)] as
+ * csa2_pack_fp8_blocks writes them, Bw E4M3 [N][K] (weights, one row per output) with
+ * b_scales fp32 [ceil(N/128)][ceil(K/128)], C [M][N] bf16 or fp32 (c_dtype).  K: a
+ * multiple of 16; M and N any.  Needs csa2_matmul_fp8_workspace_size() bytes of
+ * workspace (0: ws may be NULL), which calls that can overlap must not share. */
+size_t csa2_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K);
+int csa2_matmul_fp8(const uint8_t* A, const float* a_scales, const uint8_t* Bw, const float* b_scales,
+                    int32_t M, int32_t N, int32_t K, void* C, int32_t c_dtype, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/* frequencies of csa2_rope (R20) */
+#define CSA2_ROPE_PLAIN 0
+#define CSA2_ROPE_LINEAR 1
+#define CSA2_ROPE_NTK 2
+#define CSA2_ROPE_YARN 3
+/* pairs of csa2_rope */
+#define CSA2_ROPE_HALF 0
+#define CSA2_ROPE_INTERLEAVED 1
+
+typedef struct csa2_rope_spec {
+  int32_t scaling;           /* CSA2_ROPE_PLAIN .. CSA2_ROPE_YARN            */
+  int32_t original_len;      /* YARN: context length before the scaling      */
+  double base;               /* above 1 (10000 in R3)                        */
+  double factor;             /* all but PLAIN: how many times longer, >= 1   */
+  float beta_fast, beta_slow;/* YARN: turns (32 and 1 are usual)             */
+} csa2_rope_spec;
+
+/* The table that csa2_rope reads, made once for a model: table uint64 [r/2] (device)
+ * receives theta_i / 2 pi in turns per position, as 0.64 fixed point.  r: even, <= 512. */
+int csa2_rope_table(const csa2_rope_spec* spec, int32_t r, uint64_t* table, void* stream);
+
+/* y = x with channels start .. start + r - 1 of every head rotated to its token's
+ * position (R20) and multiplied by amplitude (1, or YARN's attention factor); the
+ * other channels are copied.  x and y: bf16 or fp32, [n_tokens][heads][d] with the
+ * given strides in elements, channels contiguous; 16-byte aligned rows and channel
+ * counts that 8 (HALF: r / 2 too) divides go 8 channels at a time.  y may be x (same
+ * type and strides: only the rotated channels are touched); otherwise they must not
+ * overlap.  positions int32 [n_tokens] (negative ones turn backwards).  inverse != 0
+ * turns by -p: back, and also the gradient (the transpose) of the rotation. */
+int csa2_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, int64_t x_head_stride, void* y,
+              int32_t y_dtype, int64_t y_token_stride, int64_t y_head_stride, int64_t n_tokens,
+              int32_t heads, int32_t d, int32_t start, int32_t r, int32_t layout, int32_t inverse,
+              float amplitude, const int32_t* positions, const uint64_t* table, void* stream);
+
+/* A tree of drafted tokens per sequence (R21). */
+typedef struct csa2_tree {
+  const uint8_t* codes;      /* [B][Tq][d] E4M3: the nodes' window rows (csa2_pack_swa_fp8) */
+  const float* scales;       /* [B][Tq]                                      */
+  const int32_t* ctx_len;    /* [B] committed raw tokens                     */
+  const int32_t* path;       /* [B][Tq][max_depth] as csa2_tree_plan writes it */
+  int32_t max_depth;         /* row length of path                           */
+} csa2_tree;
+
+/* Positions and paths of the trees: parent int32 [B][Tq], ctx_len int32 [B] ->
+ * q_pos [B][Tq] (-1 where there is no node) and path [B][Tq][max_depth] (the node's
+ * ancestor at every depth, itself last, -1 behind it).  A parent at or behind its
+ * child, or one that is no node, raises CSA2_STATUS_BAD_INDEX, a node deeper than
+ * max_depth or past position 2^31 - 1 and a negative ctx_len CSA2_STATUS_BAD_COUNT;
+ * these are no nodes then.  Tq <= 1024.  dims: B, Tq are used. */
+int csa2_tree_plan(const csa2_dims* dims, const int32_t* parent, const int32_t* ctx_len,
+                   int32_t max_depth, int32_t* q_pos, int32_t* path, void* stream);
+
+/* csa2_sparse_attn for drafted trees (R21): q_pos and tree->path as csa2_tree_plan
+ * wrote them, win the committed rows (unused, and may be NULL, where swa_cap or W is
+ * 0), idx and cnt the selection of every node, O bf16 [B][Tq][Hq][d], lse fp32
+ * [B][Tq][Hq] or NULL.  A path that does not reach the token's position raises
+ * CSA2_STATUS_BAD_INDEX, and that key is left out. */
+int csa2_tree_attn(const csa2_dims* dims, const csa2_cache* cache, const csa2_window* win,
+                   const csa2_tree* tree, const uint16_t* Q, const int32_t* q_pos, const int32_t* idx,
+                   const int32_t* cnt, float softmax_scale, uint16_t* O, float* lse, void* stream);
 
 /* ---- a bounded cache: attention over all of it, weights, eviction ------------
  * A cache that never grows past a fixed size needs no selection: every entry it
