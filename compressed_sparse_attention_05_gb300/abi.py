@@ -150,6 +150,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
 def lib():
@@ -183,8 +184,10 @@ def ptr(t: Optional[torch.Tensor]):
 
 
 def stream_handle(stream: Optional[torch.cuda.Stream] = None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle alone: making a Stream object takes longer than launching a kernel (3.0 us)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def bits16(t: torch.Tensor) -> torch.Tensor:
@@ -365,11 +368,14 @@ def _strided(t: torch.Tensor):
     return t.data_ptr()
 
 
+_FLOAT_TYPES = {torch.float32: CSA2_F32, torch.bfloat16: CSA2_BF16}
+
+
 def _float_type(t: torch.Tensor) -> int:
-    kinds = {torch.float32: CSA2_F32, torch.bfloat16: CSA2_BF16}
-    if t.dtype not in kinds:
+    kind = _FLOAT_TYPES.get(t.dtype)
+    if kind is None:
         raise ValueError(f"tensor must be float32 or bfloat16, not {t.dtype}")
-    return kinds[t.dtype]
+    return kind
 
 
 def csa2_pack_fp8_blocks(x, codes, scales, stream=None):

@@ -106,18 +106,59 @@ struct MatmulPlan {
   float* partial;           // [n_split][M][ld]
   int64_t ld;
   int M, N, kb, n_split, f32;
+  int c_map;                // C's rows start on 16 bytes: it is written by tensor-map copies
   int m_tiles, n_tiles;
 };
 
 constexpr uint32_t kIdFp8 = 1u << 4;   // instruction descriptor: fp32 accumulation, E4M3 x E4M3, both K-major
 __host__ __device__ constexpr uint32_t idesc_fp8(int M, int N) { return kIdFp8 | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 
-__device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// The MMA warp runs as a whole, so that the operands of its MMAs are uniform registers, and one lane (leader != 0)
+// issues: from a single thread's branch an MMA took 100 cycles to issue and a commit 84 (now 10 and 50), and a block's
+// four with its two commits then took longer to issue than the 513 cycles that they run.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_fp8(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, e;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
+}
+__device__ __forceinline__ void commit_fp8(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_addr(bar)),
+      "r"(leader)
+      : "memory");
+}
+// The same, arriving on the barrier at `bar`'s offset in every CTA of the cluster in `mask`.
+__device__ __forceinline__ void commit_fp8_mc(uint32_t leader, uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(tc::smem_addr(bar)),
+      "h"(mask), "r"(leader)
+      : "memory");
+}
+// The MMA warp's wait for up to three barriers with one look at a time: lane i looks at its own (bar, parity); `need`
+// has the bits of the lanes that count.  Never suspends; bounded.
+__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, uint32_t need, volatile int* abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 25); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if ((__ballot_sync(0xffffffffu, ok != 0) & need) == need) return true;
+    if ((i & 255) == 255 && __any_sync(0xffffffffu, *abort != 0)) return false;
+  }
+  *abort = 1;
+  return false;
 }
 // K-major operand rows of 128 bytes as a tensor map writes them with the 128-byte swizzle.
 __device__ __forceinline__ uint64_t desc128(uint32_t saddr) { return tc::smem_desc(saddr, 16, 1024) | ((uint64_t)2 << 61); }
@@ -141,6 +182,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+// The loads of this warp have arrived (r is named, so that nothing that uses it moves ahead of the wait).
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 // (a.x b.x + c.x, a.y b.y + c.y)
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -166,10 +217,10 @@ struct Ring {
   int abort;
 };
 template <typename R, int kStages, int kBufs>
-__device__ __forceinline__ void ring_init(R& sm, uint32_t readers) {
+__device__ __forceinline__ void ring_init(R& sm, uint32_t writers, uint32_t readers) {
   for (int i = 0; i < kStages; ++i) {
     tc::mbar_init(&sm.full[i], 1);
-    tc::mbar_init(&sm.empty[i], 1);
+    tc::mbar_init(&sm.empty[i], writers);
   }
   for (int i = 0; i < kBufs; ++i) {
     tc::mbar_init(&sm.acc_full[i], 1);
@@ -184,9 +235,33 @@ constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2;
 constexpr int kWStageBytes = (kWM + kWN) * kBlock;       // 48 KB
 constexpr int kWSumWarps = 8;
 constexpr int kWThreads = kWSumWarps * 32 + 128;
-constexpr int kWRegs = 168, kWRegsSum = 232, kWRegsMisc = 40;   // 2 x 232 + 40 = 3 x 168
-static_assert(2 * kWRegsSum + kWRegsMisc <= 3 * kWRegs, "register split");
-using WideSmem = Ring<kWStages, kWStageBytes, kWBufs>;
+// Registers: 2 x 232 + 40 = 2 x 224 + 56 = 3 x 168.  (Where a split makes the compiler spill in one role's loop, the
+// kernel takes up to twice as long: these two do not.)
+constexpr int kWRegs = 168;
+template <int kMc> constexpr int kWRegsSum = kMc == 1 ? 224 : 232;
+template <int kMc> constexpr int kWRegsMisc = 3 * kWRegs - 2 * kWRegsSum<kMc>;
+struct WideSmem : Ring<kWStages, kWStageBytes, kWBufs> {
+  alignas(1024) unsigned char out[kWSumWarps][4096];   // of each sum warp: 32 rows x 128 bytes of C on their way out
+};
+static_assert(sizeof(WideSmem) + 1024 <= 232448, "shared memory");
+
+// 32 rows x 128 bytes of C (lane = row, piece j of 16 bytes: get(j)) through the warp's staging rows.  Written by the
+// threads themselves, 16 bytes of 32 rows at a time, C took 75 of 520 us of a product of 4,096 x 32,768 x 4,096.
+template <typename Get>
+__device__ __forceinline__ void store_box(unsigned char* stage, const CUtensorMap* map, int x, int y, bool in, int lane, Get get) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the box before has left
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = get(j);   // 128-byte swizzle
+  tc::fence_async_smem();
+  __syncwarp();
+  if (lane == 0 && in)
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\tcp.async.bulk.commit_group;" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(tc::smem_addr(stage))
+                 : "memory");
+}
+
 
 template <typename T>
 __device__ __forceinline__ void store_row(T* out, const float2 (&acc)[64], int n_left, bool vec);
@@ -205,12 +280,7 @@ __device__ __forceinline__ void store_row<float>(float* out, const float2 (&acc)
 }
 template <>
 __device__ __forceinline__ void store_row<uint16_t>(uint16_t* out, const float2 (&acc)[64], int n_left, bool vec) {
-  if (vec && n_left >= 128) {
-#pragma unroll
-    for (int j = 0; j < 64; j += 4)
-      *reinterpret_cast<uint4*>(out + 2 * j) = make_uint4(f32x2_bf16x2(acc[j].x, acc[j].y), f32x2_bf16x2(acc[j + 1].x, acc[j + 1].y),
-                                                          f32x2_bf16x2(acc[j + 2].x, acc[j + 2].y), f32x2_bf16x2(acc[j + 3].x, acc[j + 3].y));
-  } else {
+  {
 #pragma unroll
     for (int j = 0; j < 64; ++j) {
       const uint32_t v = f32x2_bf16x2(acc[j].x, acc[j].y);
@@ -220,124 +290,184 @@ __device__ __forceinline__ void store_row<uint16_t>(uint16_t* out, const float2 
   }
 }
 
+// kMc CTAs of a cluster take tiles above one another and share the rows of B: each copies its part of them to all.
+template <int kMc>
 __global__ void __launch_bounds__(kWThreads, 1)
-k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ MatmulPlan p,
-                  uint32_t* status) {
+k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap,
+                  const __grid_constant__ MatmulPlan p, uint32_t* status) {
   extern __shared__ unsigned char smem_raw[];
   WideSmem& sm = *reinterpret_cast<WideSmem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (p.partial) pdl_trigger();   // k_matmul_fp8_sum waits for this kernel; C is not announced before it is complete
-  if (tid == 0) ring_init<WideSmem, kWStages, kWBufs>(sm, kWSumWarps);
+  if (tid == 0) ring_init<WideSmem, kWStages, kWBufs>(sm, kMc, kWSumWarps);
   if (warp == kWSumWarps) tc::tmem_alloc(&sm.tmem, kWBufs * kWN);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  if (kMc > 1) tc::cluster_barrier();   // every CTA's barriers exist before a peer copies or arrives into them
+  const int rank = kMc > 1 ? (int)tc::cluster_ctarank() : 0;
+  constexpr uint16_t kMask = (uint16_t)((1u << kMc) - 1);
+  constexpr int kBPart = kWN / kMc;
   const uint32_t tm = sm.tmem;
   volatile int* abort = &sm.abort;
   pdl_wait();
-  const int64_t items = (int64_t)p.m_tiles * p.n_tiles * p.n_split;
+  // work items: a cluster's tiles (kMc of them in M) times the splits of K
+  const int m_groups = (p.m_tiles + kMc - 1) / kMc;
+  const int items = m_groups * p.n_tiles * p.n_split, it0 = blockIdx.x / kMc, stride = gridDim.x / kMc;   // (below 2^31)
+  struct Item {
+    int s, m0, n0, k0, k1;   // split, this CTA's first row, the tile's first column, blocks of K
+  };
+  auto item = [&](int it) {
+    Item w;
+    const int tile = it / p.n_split;
+    w.s = it - tile * p.n_split;
+    w.n0 = tile / m_groups;
+    w.m0 = ((tile - w.n0 * m_groups) * kMc + rank) * kWM;
+    w.n0 *= kWN;
+    split_range(p, w.s, &w.k0, &w.k1);
+    return w;
+  };
 
   if (warp >= kWSumWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsMisc));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsMisc<kMc>));
     if (warp == kWSumWarps && lane == 0) {
       // ================= operand copies =================
       uint32_t n = 0;
       bool ok = true;
-      for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
-        const int s = (int)(it % p.n_split);
-        const int64_t tile = it / p.n_split;
-        const int m0 = (int)(tile % p.m_tiles) * kWM, n0 = (int)(tile / p.m_tiles) * kWN;
-        int k0, k1;
-        split_range(p, s, &k0, &k1);
-        for (int k = k0; k < k1; ++k, ++n) {
+      for (int it = it0; ok && it < items; it += stride) {
+        const Item w = item(it);
+        for (int k = w.k0; k < w.k1; ++k, ++n) {
           const uint32_t st = n % kWStages, use = n / kWStages;
           if (use > 0 && !wait_bar(&sm.empty[st], (use - 1) & 1, abort)) {
             ok = false;
             break;
           }
           tc::mbar_arrive_expect_tx(&sm.full[st], kWStageBytes);
-          tma::load_2d(sm.stage[st], &amap, k * kBlock, m0, &sm.full[st]);
-          tma::load_2d(sm.stage[st] + kWM * kBlock, &bmap, k * kBlock, n0, &sm.full[st]);
+          tma::load_2d(sm.stage[st], &amap, k * kBlock, w.m0, &sm.full[st]);
+          unsigned char* b = sm.stage[st] + kWM * kBlock + rank * (kBPart * kBlock);
+          if (kMc > 1) tma::load_2d_mc(b, &bmap, k * kBlock, w.n0 + rank * kBPart, &sm.full[st], kMask);
+          else tma::load_2d(b, &bmap, k * kBlock, w.n0, &sm.full[st]);
         }
       }
       for (uint32_t i = n > kWStages ? n - kWStages : 0; i < n; ++i)   // every issued copy lands before exit
-        for (uint32_t w = 0; w < (1u << 22); ++w)
+        for (uint32_t t = 0; t < (1u << 22); ++t)
           if (tc::mbar_try_wait(&sm.full[i % kWStages], (i / kWStages) & 1)) break;
-    } else if (warp == kWSumWarps + 1 && lane == 0) {
+    } else if (warp == kWSumWarps + 1) {
       // ================= MMA issue =================
       constexpr uint32_t idesc = idesc_fp8(kWM, kWN);
+      const uint32_t leader = elect_lane();
       uint32_t n = 0;
       bool ok = true;
-      for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
-        int k0, k1;
-        split_range(p, (int)(it % p.n_split), &k0, &k1);
-        for (int k = k0; k < k1; ++k, ++n) {
+      for (int it = it0; ok && it < items; it += stride) {
+        const Item w = item(it);
+        for (int k = w.k0; k < w.k1; ++k, ++n) {
           const uint32_t st = n % kWStages, buf = n % kWBufs, use = n / kWBufs;
-          if ((use > 0 && !wait_bar(&sm.acc_empty[buf], (use - 1) & 1, abort)) || !wait_bar(&sm.full[st], (n / kWStages) & 1, abort)) {
-            ok = false;
-            break;
-          }
+          ok = wait_lanes(tc::smem_addr(lane == 1 ? &sm.acc_empty[buf] : &sm.full[st]), lane == 1 ? (use - 1) & 1 : (n / kWStages) & 1,
+                          use > 0 ? 3u : 1u, abort);
+          if (!ok) break;
           tc::tc_fence_after();
           const uint32_t sa = tc::smem_addr(sm.stage[st]), sb = sa + kWM * kBlock;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) mma_fp8(tm + buf * kWN, desc128(sa + 32 * ks), desc128(sb + 32 * ks), idesc, ks > 0);
-          tc::mma_commit(&sm.empty[st]);
-          tc::mma_commit(&sm.acc_full[buf]);
+          for (int ks = 0; ks < 4; ++ks) mma_fp8(leader, tm + buf * kWN, desc128(sa + 32 * ks), desc128(sb + 32 * ks), idesc, ks > 0);
+          commit_fp8(leader, &sm.acc_full[buf]);
+          if (kMc > 1) commit_fp8_mc(leader, &sm.empty[st], kMask);
+          else commit_fp8(leader, &sm.empty[st]);
         }
       }
     }
     __syncwarp();
   } else {
     // ================= scales and sums: thread = row of A, 128 columns =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsSum));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsSum<kMc>));
     const int lq = warp & 3, half = warp >> 2;
+    const uint32_t t0 = tm + ((uint32_t)(32 * lq) << 16) + 128 * half;
+    const bool vec = p.kb % 4 == 0;   // (the scales' rows start on 16 bytes)
     uint32_t n = 0;
     bool ok = true;
-    for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
-      const int s = (int)(it % p.n_split);
-      const int64_t tile = it / p.n_split;
-      const int m = (int)(tile % p.m_tiles) * kWM + 32 * lq + lane, n0 = (int)(tile / p.m_tiles) * kWN + 128 * half;
-      int k0, k1;
-      split_range(p, s, &k0, &k1);
+    for (int it = it0; ok && it < items; it += stride) {
+      const Item w = item(it);
+      const int m = w.m0 + 32 * lq + lane, n0 = w.n0 + 128 * half;
       const bool live = m < p.M && n0 < p.N;
       const float* sa = p.sa + (int64_t)(live ? m : 0) * p.kb;
       const float* sb = p.sb + (int64_t)(live ? n0 / kBlock : 0) * p.kb;
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      float next = k0 < k1 ? __ldg(sa + k0) * __ldg(sb + k0) : 0.f;
-      for (int k = k0; k < k1; ++k, ++n) {
-        const float sc = next;
+      // Scales four blocks at a time: a row's lie behind one another, so that a warp's load touches 32 lines whether it
+      // takes 4 bytes of each or 16.
+      float4 sc;
+      auto block = [&](float both) {
         const uint32_t buf = n % kWBufs;
-        if (k + 1 < k1) next = __ldg(sa + k + 1) * __ldg(sb + k + 1);
         ok = __all_sync(0xffffffffu, wait_bar(&sm.acc_full[buf], (n / kWBufs) & 1, abort));
-        if (!ok) break;
+        if (!ok) return;
         tc::tc_fence_after();
+        ++n;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
-          tmem_ld32(tm + ((uint32_t)(32 * lq) << 16) + buf * kWN + 128 * half + 32 * c, r);
-          tc::tmem_wait_ld();
+          tmem_ld32(t0 + buf * kWN + 32 * c, r);
+          tmem_wait32(r);
+          if (c == 3) {       // the accumulator has been read
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.acc_empty[buf]);
+          }
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            acc[16 * c + j] = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), make_float2(sc, sc), acc[16 * c + j]);
+            acc[16 * c + j] = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), make_float2(both, both), acc[16 * c + j]);
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.acc_empty[buf]);
+      };
+#pragma unroll 1
+      for (int k = w.k0; ok && k < w.k1; ++k) {
+        const int i = k & 3;
+        if (k == w.k0 || i == 0) {
+          const int q = k & ~3;
+          if (vec) {
+            const float4 fa = __ldg(reinterpret_cast<const float4*>(sa + q)), fb = __ldg(reinterpret_cast<const float4*>(sb + q));
+            sc = make_float4(fa.x * fb.x, fa.y * fb.y, fa.z * fb.z, fa.w * fb.w);
+          } else {
+            auto at = [&](int j) { return q + j < p.kb ? __ldg(sa + q + j) * __ldg(sb + q + j) : 0.f; };
+            sc = make_float4(at(0), at(1), at(2), at(3));
+          }
+        }
+        block(i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w);
       }
-      if (!ok || !live) continue;
+      if (!ok) break;
+      if (p.c_map) {       // (copies leave out what lies outside of C)
+        const int y = w.m0 + 32 * lq;
+        unsigned char* stage = sm.out[warp];
+        if (p.f32) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            store_box(stage, &cmap, n0 + 32 * b, y, y < p.M && n0 + 32 * b < p.N, lane, [&](int j) {
+              const float2 u = acc[16 * b + 2 * j], v = acc[16 * b + 2 * j + 1];
+              return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y));
+            });
+        } else {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            store_box(stage, &cmap, n0 + 64 * b, y, y < p.M && n0 + 64 * b < p.N, lane, [&](int j) {
+              const float2* u = acc + 32 * b + 4 * j;
+              return make_uint4(f32x2_bf16x2(u[0].x, u[0].y), f32x2_bf16x2(u[1].x, u[1].y), f32x2_bf16x2(u[2].x, u[2].y), f32x2_bf16x2(u[3].x, u[3].y));
+            });
+        }
+        continue;
+      }
+      if (!live) continue;
       const int left = p.N - n0;
       if (p.partial)
-        store_row<float>(p.partial + ((int64_t)s * p.M + m) * p.ld + n0, acc, left, true);
+        store_row<float>(p.partial + ((int64_t)w.s * p.M + m) * p.ld + n0, acc, left, true);
       else if (p.f32)
-        store_row<float>(static_cast<float*>(p.C) + (int64_t)m * p.N + n0, acc, left, p.N % 4 == 0);
+        store_row<float>(static_cast<float*>(p.C) + (int64_t)m * p.N + n0, acc, left, false);
       else
-        store_row<uint16_t>(static_cast<uint16_t*>(p.C) + (int64_t)m * p.N + n0, acc, left, p.N % 8 == 0);
+        store_row<uint16_t>(static_cast<uint16_t*>(p.C) + (int64_t)m * p.N + n0, acc, left, false);
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (kMc > 1) tc::cluster_barrier();   // no copy or commit of a peer still targets this CTA
   if (warp == kWSumWarps) tc::tmem_dealloc(tm, kWBufs * kWN);
   if (tid == 0 && *abort) raise_status(status, CSA2_STATUS_TIMEOUT);
 }
@@ -360,7 +490,7 @@ k_matmul_fp8_few(const __grid_constant__ CUtensorMap amap, const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (p.partial) pdl_trigger();
   constexpr uint32_t kCols = kFBufs * kRows;        // 64, 128 or 256 columns
-  if (tid == 0) ring_init<Smem, kStages, kFBufs>(sm, 4);
+  if (tid == 0) ring_init<Smem, kStages, kFBufs>(sm, 1, 4);
   if (warp == 4) tc::tmem_alloc(&sm.tmem, kCols);
   tc::tc_fence_before();
   __syncthreads();
@@ -395,26 +525,25 @@ k_matmul_fp8_few(const __grid_constant__ CUtensorMap amap, const __grid_constant
     }
     __syncwarp();
   } else if (warp == 5) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_fp8(kFN, kRows);
-      uint32_t n = 0;
-      bool ok = true;
-      for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
-        int k0, k1;
-        split_range(p, (int)(it % p.n_split), &k0, &k1);
-        for (int k = k0; k < k1; ++k, ++n) {
-          const uint32_t st = n % kStages, buf = n % kFBufs, use = n / kFBufs;
-          if ((use > 0 && !wait_bar(&sm.acc_empty[buf], (use - 1) & 1, abort)) || !wait_bar(&sm.full[st], (n / kStages) & 1, abort)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t sw = tc::smem_addr(sm.stage[st]), sx = sw + kFN * kBlock;
+    constexpr uint32_t idesc = idesc_fp8(kFN, kRows);
+    const uint32_t leader = elect_lane();
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+      int k0, k1;
+      split_range(p, (int)(it % p.n_split), &k0, &k1);
+      for (int k = k0; k < k1; ++k, ++n) {
+        const uint32_t st = n % kStages, buf = n % kFBufs, use = n / kFBufs;
+        ok = wait_lanes(tc::smem_addr(lane == 2 ? &sm.acc_empty[buf] : &sm.full[st]), lane == 2 ? (use - 1) & 1 : (n / kStages) & 1,
+                        use > 0 ? 5u : 1u, abort);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t sw = tc::smem_addr(sm.stage[st]), sx = sw + kFN * kBlock;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) mma_fp8(tm + buf * kRows, desc128(sw + 32 * ks), desc128(sx + 32 * ks), idesc, ks > 0);
-          tc::mma_commit(&sm.empty[st]);
-          tc::mma_commit(&sm.acc_full[buf]);
-        }
+        for (int ks = 0; ks < 4; ++ks)
+          mma_fp8(leader, tm + buf * kRows, desc128(sw + 32 * ks), desc128(sx + 32 * ks), idesc, ks > 0);
+        commit_fp8(leader, &sm.empty[st]);
+        commit_fp8(leader, &sm.acc_full[buf]);
       }
     }
     __syncwarp();
@@ -497,10 +626,22 @@ __global__ void __launch_bounds__(256) k_matmul_fp8_sum(const __grid_constant__ 
 constexpr int kSms = 152;
 constexpr int kFewRows = 64;
 
-int splits(int M, int N, int K) {
-  const int64_t kb = (K + kBlock - 1) / kBlock;
-  const int64_t tiles = M <= kFewRows ? (N + kFN - 1) / kFN : (int64_t)((M + kWM - 1) / kWM) * ((N + kWN - 1) / kWN);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(kb, kSms / std::max<int64_t>(1, tiles)));
+// How a product is cut: the rows and columns of a tile, the CTAs that share B, and the splits of K that fill the SMs
+// where the tiles do not.
+struct Cut {
+  int m, n, ctas, n_split;
+  bool few;
+};
+Cut cut_of(int M, int N, int K) {
+  Cut c;
+  c.few = M <= kFewRows;
+  c.m = c.few ? kFewRows : kWM;
+  c.n = c.few ? kFN : kWN;
+  c.ctas = !c.few && M > kWM ? 2 : 1;
+  const int64_t groups = ((M + c.m - 1) / c.m + c.ctas - 1) / c.ctas;
+  const int64_t kb = (K + kBlock - 1) / kBlock, tiles = groups * ((N + c.n - 1) / c.n);
+  c.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(kb, kSms / c.ctas / std::max<int64_t>(1, tiles)));
+  return c;
 }
 int64_t partial_ld(int N) { return ((int64_t)N + 127) / 128 * 128; }
 
@@ -515,12 +656,46 @@ bool row_map(CUtensorMap* map, const uint8_t* p, int rows, int K, int box_rows) 
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Kernel>
-cudaError_t launch_matmul(Kernel kernel, size_t smem, int threads, int64_t items, int sms, const CUtensorMap& am, const CUtensorMap& bm,
-                          const MatmulPlan& p, cudaStream_t s) {
+template <typename Kernel, typename... Rest>
+cudaError_t launch_matmul(Kernel kernel, size_t smem, int threads, int64_t items, int sms, int ctas, cudaStream_t s, const CUtensorMap& am,
+                          const CUtensorMap& bm, const Rest&... rest) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_step(kernel, dim3((unsigned)std::min<int64_t>(items, sms)), dim3(threads), smem, s, am, bm, p, status_word());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(items, std::max(1, sms / ctas)) * ctas));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)ctas;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return counted(cudaLaunchKernelEx(&cfg, kernel, am, bm, rest..., status_word()));
+}
+template <int kMc>
+cudaError_t launch_wide(int64_t items, int sms, const CUtensorMap& am, const CUtensorMap& bm, MatmulPlan p, cudaStream_t s) {
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, k_matmul_fp8_wide<kMc>);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs < kWRegs) return cudaErrorInvalidConfiguration;   // the register split would wait forever
+  CUtensorMap cm = am;
+  const int size = p.f32 ? 4 : 2;
+  p.c_map = !p.partial && (int64_t)p.N * size % 16 == 0;
+  if (p.c_map) {
+    const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.N * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32}, estr[2] = {1, 1};
+    if (tensor_map_encoder()(&cm, p.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.C, dims, strides, box, estr,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  return launch_matmul(k_matmul_fp8_wide<kMc>, sizeof(WideSmem) + 1024, kWThreads, items, sms, kMc, s, am, bm, cm, p);
 }
 
 }  // namespace
@@ -536,40 +711,35 @@ cudaError_t launch_pack_fp8_blocks(const void* x, int dtype, int64_t stride, int
 }
 
 size_t matmul_fp8_workspace_bytes(int M, int N, int K) {
-  const int n = splits(M, N, K);
+  const int n = cut_of(M, N, K).n_split;
   return n > 1 ? (size_t)n * M * partial_ld(N) * sizeof(float) : 0;
 }
 
 cudaError_t launch_matmul_fp8(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int M, int N, int K, void* C, int f32, void* ws,
                               cudaStream_t s) {
+  const Cut cut = cut_of(M, N, K);
   MatmulPlan p = {};
   p.sa = sa; p.sb = sb; p.C = C; p.M = M; p.N = N; p.kb = (K + kBlock - 1) / kBlock; p.f32 = f32;
-  p.n_split = splits(M, N, K);
+  p.n_split = cut.n_split;
   p.ld = partial_ld(N);
   p.partial = p.n_split > 1 ? static_cast<float*>(ws) : nullptr;
+  p.m_tiles = (M + cut.m - 1) / cut.m;
+  p.n_tiles = (N + cut.n - 1) / cut.n;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   CUtensorMap am, bm;
-  const bool few = M <= kFewRows;
   const int rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  if (!row_map(&am, a, M, K, few ? rows : kWM) || !row_map(&bm, b, N, K, few ? kFN : kWN)) return cudaErrorInvalidValue;
-  if (few) {
-    p.m_tiles = 1;
-    p.n_tiles = (N + kFN - 1) / kFN;
-    const int64_t items = (int64_t)p.n_tiles * p.n_split;
-    if (rows == 16) e = launch_matmul(k_matmul_fp8_few<16>, sizeof(FewSmem<16>) + 1024, kFThreads, items, sms, am, bm, p, s);
-    else if (rows == 32) e = launch_matmul(k_matmul_fp8_few<32>, sizeof(FewSmem<32>) + 1024, kFThreads, items, sms, am, bm, p, s);
-    else e = launch_matmul(k_matmul_fp8_few<64>, sizeof(FewSmem<64>) + 1024, kFThreads, items, sms, am, bm, p, s);
+  if (!row_map(&am, a, M, K, cut.few ? rows : kWM) || !row_map(&bm, b, N, K, cut.few ? kFN : kWN / cut.ctas))
+    return cudaErrorInvalidValue;
+  const int64_t items = (int64_t)((p.m_tiles + cut.ctas - 1) / cut.ctas) * p.n_tiles * p.n_split;
+  if (cut.few) {
+    if (rows == 16) e = launch_matmul(k_matmul_fp8_few<16>, sizeof(FewSmem<16>) + 1024, kFThreads, items, sms, 1, s, am, bm, p);
+    else if (rows == 32) e = launch_matmul(k_matmul_fp8_few<32>, sizeof(FewSmem<32>) + 1024, kFThreads, items, sms, 1, s, am, bm, p);
+    else e = launch_matmul(k_matmul_fp8_few<64>, sizeof(FewSmem<64>) + 1024, kFThreads, items, sms, 1, s, am, bm, p);
   } else {
-    p.m_tiles = (M + kWM - 1) / kWM;
-    p.n_tiles = (N + kWN - 1) / kWN;
-    cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, k_matmul_fp8_wide);
-    if (e != cudaSuccess) return e;
-    if (at.numRegs < kWRegs) return cudaErrorInvalidConfiguration;   // the register split would wait forever
-    e = launch_matmul(k_matmul_fp8_wide, sizeof(WideSmem) + 1024, kWThreads, (int64_t)p.m_tiles * p.n_tiles * p.n_split, sms, am, bm, p, s);
+    e = cut.ctas == 2 ? launch_wide<2>(items, sms, am, bm, p, s) : launch_wide<1>(items, sms, am, bm, p, s);
   }
   if (e != cudaSuccess || p.n_split == 1) return e;
   const unsigned gy = (unsigned)std::min(M, 32768);
