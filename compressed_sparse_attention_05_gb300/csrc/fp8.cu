@@ -5,14 +5,20 @@
 // accumulation) into a tensor-memory accumulator of their own; the accumulator is then read back, multiplied by the
 // block's two scales and added to the sum in registers, while the tensor cores work on the next block's.
 //
-// k_matmul_fp8_wide (more than 64 rows of A): tiles of 128 rows of A x 256 rows of B.  A row of A is a lane of the
-//   accumulator, so a thread has one scale per block: sa[its row] sb[its 128 columns].
-// k_matmul_fp8_few (up to 64 rows of A): the rows of B, the weights, are the MMA's M side, 128 at a time, and the
-//   few rows of A its N side, so that no part of the tensor cores' work and of shared memory goes to rows that are
-//   not there, and 128 B-rows x 128 columns (16 KB) per block stream through a deep ring.  A thread has a weight row
-//   and all rows of A; their scales come from the lanes of its warp.
-// Where the tiles do not fill the SMs, the blocks of K are split over several CTAs, which leave fp32 partial sums
-// that k_matmul_fp8_sum adds in order.
+// k_matmul_fp8_wide (many rows of A): tiles of 128 rows of A x 256 rows of B.  A row of A is a lane of the accumulator,
+//   so a thread has one scale per block: sa[its row] sb[its 128 columns].  Two CTAs with tiles above one another copy B's
+//   rows for each other (32 KB out of L2 for each instead of 48).
+//   4,096 x 32,768 x 4,096 takes 440 us (2.5 PFLOP/s of fp8).  What bounds it: a block's MMAs run 513 cycles, and the
+//   way MMA -> sums (200 cycles after the last product) -> accumulator read (300) -> next MMAs (200) about as long again,
+//   with two accumulators (all of tensor memory) to hide it; the sums themselves take 310 cycles of every scheduler.
+//   Tried: a pair of CTAs with one MMA for both (cta_group::2; its arrivals from SM to SM are too slow for this way:
+//   480 us), 16 sum warps (570, registers), named barriers in the place of shared-memory ones (530).
+// k_matmul_fp8_thin (few rows of A, or few tiles): the rows of B, the weights, are the MMA's M side, 128 at a time, and
+//   16 to 128 rows of A its N side, so that no part of the tensor cores' work and of shared memory goes to rows that are
+//   not there, and 128 B-rows x 128 columns (16 KB) per block stream through a deep ring.  A thread has a weight row and
+//   up to 64 rows of A; their scales go through shared memory.  32 x 32,768 x 4,096: 27.6 us, 4.9 TB/s.
+//   Where its tiles do not fill the SMs, the blocks of K are split over several CTAs, which leave fp32 partial sums that
+//   k_matmul_fp8_sum adds in order.
 #include <algorithm>
 
 #include "common.cuh"
@@ -193,6 +199,20 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 // (a.x b.x + c.x, a.y b.y + c.y)
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -231,15 +251,14 @@ __device__ __forceinline__ void ring_init(R& sm, uint32_t writers, uint32_t read
 }
 
 // ---- many rows of A ----
-constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2;
+constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2, kMc = 2;   // kMc: CTAs of a cluster
 constexpr int kWStageBytes = (kWM + kWN) * kBlock;       // 48 KB
 constexpr int kWSumWarps = 8;
 constexpr int kWThreads = kWSumWarps * 32 + 128;
-// Registers: 2 x 232 + 40 = 2 x 224 + 56 = 3 x 168.  (Where a split makes the compiler spill in one role's loop, the
-// kernel takes up to twice as long: these two do not.)
+// Registers: 2 x 224 + 56 = 3 x 168.  (Where a split makes the compiler spill in one role's loop, the kernel takes up
+// to twice as long; this one does not.)
 constexpr int kWRegs = 168;
-template <int kMc> constexpr int kWRegsSum = kMc == 1 ? 224 : 232;
-template <int kMc> constexpr int kWRegsMisc = 3 * kWRegs - 2 * kWRegsSum<kMc>;
+constexpr int kWRegsSum = 224, kWRegsMisc = 56;
 struct WideSmem : Ring<kWStages, kWStageBytes, kWBufs> {
   alignas(1024) unsigned char out[kWSumWarps][4096];   // of each sum warp: 32 rows x 128 bytes of C on their way out
 };
@@ -263,80 +282,65 @@ __device__ __forceinline__ void store_box(unsigned char* stage, const CUtensorMa
 }
 
 
-template <typename T>
-__device__ __forceinline__ void store_row(T* out, const float2 (&acc)[64], int n_left, bool vec);
-template <>
-__device__ __forceinline__ void store_row<float>(float* out, const float2 (&acc)[64], int n_left, bool vec) {
-  if (vec && n_left >= 128) {
+// A thread's 128 columns of a row of C whose rows do not start on 16 bytes.
+__device__ __forceinline__ void store_row(float* out, const float2 (&acc)[64], int n_left) {
 #pragma unroll
-    for (int j = 0; j < 64; j += 2) *reinterpret_cast<float4*>(out + 2 * j) = make_float4(acc[j].x, acc[j].y, acc[j + 1].x, acc[j + 1].y);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 64; ++j) {
-      if (2 * j < n_left) out[2 * j] = acc[j].x;
-      if (2 * j + 1 < n_left) out[2 * j + 1] = acc[j].y;
-    }
+  for (int j = 0; j < 64; ++j) {
+    if (2 * j < n_left) out[2 * j] = acc[j].x;
+    if (2 * j + 1 < n_left) out[2 * j + 1] = acc[j].y;
   }
 }
-template <>
-__device__ __forceinline__ void store_row<uint16_t>(uint16_t* out, const float2 (&acc)[64], int n_left, bool vec) {
-  {
+__device__ __forceinline__ void store_row(uint16_t* out, const float2 (&acc)[64], int n_left) {
 #pragma unroll
-    for (int j = 0; j < 64; ++j) {
-      const uint32_t v = f32x2_bf16x2(acc[j].x, acc[j].y);
-      if (2 * j < n_left) out[2 * j] = (uint16_t)(v & 0xFFFFu);
-      if (2 * j + 1 < n_left) out[2 * j + 1] = (uint16_t)(v >> 16);
-    }
+  for (int j = 0; j < 64; ++j) {
+    const uint32_t v = f32x2_bf16x2(acc[j].x, acc[j].y);
+    if (2 * j < n_left) out[2 * j] = (uint16_t)(v & 0xFFFFu);
+    if (2 * j + 1 < n_left) out[2 * j + 1] = (uint16_t)(v >> 16);
   }
 }
 
-// kMc CTAs of a cluster take tiles above one another and share the rows of B: each copies its part of them to all.
-template <int kMc>
+// The CTAs of a cluster take tiles above one another and share the rows of B: each copies its part of them to all.
 __global__ void __launch_bounds__(kWThreads, 1)
 k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap,
                   const __grid_constant__ MatmulPlan p, uint32_t* status) {
   extern __shared__ unsigned char smem_raw[];
   WideSmem& sm = *reinterpret_cast<WideSmem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (p.partial) pdl_trigger();   // k_matmul_fp8_sum waits for this kernel; C is not announced before it is complete
   if (tid == 0) ring_init<WideSmem, kWStages, kWBufs>(sm, kMc, kWSumWarps);
   if (warp == kWSumWarps) tc::tmem_alloc(&sm.tmem, kWBufs * kWN);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (kMc > 1) tc::cluster_barrier();   // every CTA's barriers exist before a peer copies or arrives into them
-  const int rank = kMc > 1 ? (int)tc::cluster_ctarank() : 0;
+  tc::cluster_barrier();   // every CTA's barriers exist before a peer copies or arrives into them
+  const int rank = (int)tc::cluster_ctarank();
   constexpr uint16_t kMask = (uint16_t)((1u << kMc) - 1);
   constexpr int kBPart = kWN / kMc;
   const uint32_t tm = sm.tmem;
   volatile int* abort = &sm.abort;
   pdl_wait();
-  // work items: a cluster's tiles (kMc of them in M) times the splits of K
+  // work items: kMc tiles above one another, one for each CTA
   const int m_groups = (p.m_tiles + kMc - 1) / kMc;
-  const int items = m_groups * p.n_tiles * p.n_split, it0 = blockIdx.x / kMc, stride = gridDim.x / kMc;   // (below 2^31)
+  const int items = m_groups * p.n_tiles, it0 = blockIdx.x / kMc, stride = gridDim.x / kMc;   // (below 2^31)
   struct Item {
-    int s, m0, n0, k0, k1;   // split, this CTA's first row, the tile's first column, blocks of K
+    int m0, n0;   // this CTA's first row, the tile's first column
   };
   auto item = [&](int it) {
     Item w;
-    const int tile = it / p.n_split;
-    w.s = it - tile * p.n_split;
-    w.n0 = tile / m_groups;
-    w.m0 = ((tile - w.n0 * m_groups) * kMc + rank) * kWM;
+    w.n0 = it / m_groups;
+    w.m0 = ((it - w.n0 * m_groups) * kMc + rank) * kWM;
     w.n0 *= kWN;
-    split_range(p, w.s, &w.k0, &w.k1);
     return w;
   };
 
   if (warp >= kWSumWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsMisc<kMc>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsMisc));
     if (warp == kWSumWarps && lane == 0) {
       // ================= operand copies =================
       uint32_t n = 0;
       bool ok = true;
       for (int it = it0; ok && it < items; it += stride) {
         const Item w = item(it);
-        for (int k = w.k0; k < w.k1; ++k, ++n) {
+        for (int k = 0; k < p.kb; ++k, ++n) {
           const uint32_t st = n % kWStages, use = n / kWStages;
           if (use > 0 && !wait_bar(&sm.empty[st], (use - 1) & 1, abort)) {
             ok = false;
@@ -345,8 +349,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
           tc::mbar_arrive_expect_tx(&sm.full[st], kWStageBytes);
           tma::load_2d(sm.stage[st], &amap, k * kBlock, w.m0, &sm.full[st]);
           unsigned char* b = sm.stage[st] + kWM * kBlock + rank * (kBPart * kBlock);
-          if (kMc > 1) tma::load_2d_mc(b, &bmap, k * kBlock, w.n0 + rank * kBPart, &sm.full[st], kMask);
-          else tma::load_2d(b, &bmap, k * kBlock, w.n0, &sm.full[st]);
+          tma::load_2d_mc(b, &bmap, k * kBlock, w.n0 + rank * kBPart, &sm.full[st], kMask);
         }
       }
       for (uint32_t i = n > kWStages ? n - kWStages : 0; i < n; ++i)   // every issued copy lands before exit
@@ -360,7 +363,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
       bool ok = true;
       for (int it = it0; ok && it < items; it += stride) {
         const Item w = item(it);
-        for (int k = w.k0; k < w.k1; ++k, ++n) {
+        for (int k = 0; k < p.kb; ++k, ++n) {
           const uint32_t st = n % kWStages, buf = n % kWBufs, use = n / kWBufs;
           ok = wait_lanes(tc::smem_addr(lane == 1 ? &sm.acc_empty[buf] : &sm.full[st]), lane == 1 ? (use - 1) & 1 : (n / kWStages) & 1,
                           use > 0 ? 3u : 1u, abort);
@@ -370,15 +373,14 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) mma_fp8(leader, tm + buf * kWN, desc128(sa + 32 * ks), desc128(sb + 32 * ks), idesc, ks > 0);
           commit_fp8(leader, &sm.acc_full[buf]);
-          if (kMc > 1) commit_fp8_mc(leader, &sm.empty[st], kMask);
-          else commit_fp8(leader, &sm.empty[st]);
+          commit_fp8_mc(leader, &sm.empty[st], kMask);
         }
       }
     }
     __syncwarp();
   } else {
     // ================= scales and sums: thread = row of A, 128 columns =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsSum<kMc>));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsSum));
     const int lq = warp & 3, half = warp >> 2;
     const uint32_t t0 = tm + ((uint32_t)(32 * lq) << 16) + 128 * half;
     const bool vec = p.kb % 4 == 0;   // (the scales' rows start on 16 bytes)
@@ -418,9 +420,9 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
         }
       };
 #pragma unroll 1
-      for (int k = w.k0; ok && k < w.k1; ++k) {
+      for (int k = 0; ok && k < p.kb; ++k) {
         const int i = k & 3;
-        if (k == w.k0 || i == 0) {
+        if (i == 0) {
           const int q = k & ~3;
           if (vec) {
             const float4 fa = __ldg(reinterpret_cast<const float4*>(sa + q)), fb = __ldg(reinterpret_cast<const float4*>(sb + q));
@@ -455,151 +457,186 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
       }
       if (!live) continue;
       const int left = p.N - n0;
-      if (p.partial)
-        store_row<float>(p.partial + ((int64_t)w.s * p.M + m) * p.ld + n0, acc, left, true);
-      else if (p.f32)
-        store_row<float>(static_cast<float*>(p.C) + (int64_t)m * p.N + n0, acc, left, false);
+      if (p.f32)
+        store_row(static_cast<float*>(p.C) + (int64_t)m * p.N + n0, acc, left);
       else
-        store_row<uint16_t>(static_cast<uint16_t*>(p.C) + (int64_t)m * p.N + n0, acc, left, false);
+        store_row(static_cast<uint16_t*>(p.C) + (int64_t)m * p.N + n0, acc, left);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (kMc > 1) tc::cluster_barrier();   // no copy or commit of a peer still targets this CTA
+  tc::cluster_barrier();   // no copy or commit of a peer still targets this CTA
   if (warp == kWSumWarps) tc::tmem_dealloc(tm, kWBufs * kWN);
   if (tid == 0 && *abort) raise_status(status, CSA2_STATUS_TIMEOUT);
 }
 
-// ---- few rows of A ----
-constexpr int kFN = 128, kFBufs = 4;                // rows of B in a tile; accumulators
-constexpr int kFThreads = 192;                      // 4 warps of sums, copies, MMA
-template <int kRows> constexpr int kFStageBytes = (kFN + kRows) * kBlock;
-template <int kRows> constexpr int kFStages = 200 * 1024 / kFStageBytes<kRows>;
-template <int kRows> using FewSmem = Ring<kFStages<kRows>, kFStageBytes<kRows>, kFBufs>;
+// ---- few rows of A, or few tiles ----
+// A tile is 128 rows of B x kRows (16 to 128) rows of A.
+constexpr int kTN = 128, kTBufs = 4;                // rows of B; accumulators
+template <int kRows> constexpr int kTSumWarps = kRows > 16 ? 8 : 4;      // two groups share the rows of A
+template <int kRows> constexpr int kTThreads = (kTSumWarps<kRows> + 2) * 32;
+template <int kRows> constexpr int kTOwn = kRows / (kTSumWarps<kRows> / 4);   // rows of A of a sum warp: 16, 16, 32, 64
+template <int kRows> constexpr int kTStageBytes = (kTN + kRows) * kBlock;
+template <int kRows> constexpr int kTStages = 200 * 1024 / kTStageBytes<kRows>;
+template <int kRows>
+struct ThinSmem : Ring<kTStages<kRows>, kTStageBytes<kRows>, kTBufs> {
+  alignas(16) float scale[kTSumWarps<kRows>][2][kTOwn<kRows>];   // of a block, for all lanes of a warp
+};
 
 template <int kRows>
-__global__ void __launch_bounds__(kFThreads, 1)
-k_matmul_fp8_few(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ MatmulPlan p,
-                 uint32_t* status) {
+__global__ void __launch_bounds__(kTThreads<kRows>, 1)
+k_matmul_fp8_thin(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ MatmulPlan p,
+                  uint32_t* status) {
   extern __shared__ unsigned char smem_raw[];
-  using Smem = FewSmem<kRows>;
-  constexpr int kStages = kFStages<kRows>, kBytes = kFStageBytes<kRows>;
+  using Smem = ThinSmem<kRows>;
+  constexpr int kStages = kTStages<kRows>, kBytes = kTStageBytes<kRows>, kSumWarps = kTSumWarps<kRows>, kOwn = kTOwn<kRows>;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (p.partial) pdl_trigger();
-  constexpr uint32_t kCols = kFBufs * kRows;        // 64, 128 or 256 columns
-  if (tid == 0) ring_init<Smem, kStages, kFBufs>(sm, 1, 4);
-  if (warp == 4) tc::tmem_alloc(&sm.tmem, kCols);
+  constexpr uint32_t kCols = kTBufs * kRows;        // 64 to 512 columns
+  if (tid == 0) ring_init<Smem, kStages, kTBufs>(sm, 1, kSumWarps);
+  if (warp == kSumWarps) tc::tmem_alloc(&sm.tmem, kCols);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tm = sm.tmem;
   volatile int* abort = &sm.abort;
   pdl_wait();
-  const int64_t items = (int64_t)p.n_tiles * p.n_split;
+  const int items = p.m_tiles * p.n_tiles * p.n_split;   // (below 2^31)
+  struct Item {
+    int s, m0, n0, k0, k1;   // split, first rows of A and of B, blocks of K
+  };
+  auto item = [&](int it) {
+    Item w;
+    const int tile = it / p.n_split;
+    w.s = it - tile * p.n_split;
+    w.n0 = tile / p.m_tiles;
+    w.m0 = (tile - w.n0 * p.m_tiles) * kRows;
+    w.n0 *= kTN;
+    split_range(p, w.s, &w.k0, &w.k1);
+    return w;
+  };
 
-  if (warp == 4) {
+  if (warp == kSumWarps) {
+    // ================= operand copies =================
     if (lane == 0) {
       uint32_t n = 0;
       bool ok = true;
-      for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
-        int k0, k1;
-        split_range(p, (int)(it % p.n_split), &k0, &k1);
-        const int n0 = (int)(it / p.n_split) * kFN;
-        for (int k = k0; k < k1; ++k, ++n) {
+      for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        const Item w = item(it);
+        for (int k = w.k0; k < w.k1; ++k, ++n) {
           const uint32_t st = n % kStages, use = n / kStages;
           if (use > 0 && !wait_bar(&sm.empty[st], (use - 1) & 1, abort)) {
             ok = false;
             break;
           }
           tc::mbar_arrive_expect_tx(&sm.full[st], kBytes);
-          tma::load_2d(sm.stage[st], &bmap, k * kBlock, n0, &sm.full[st]);
-          tma::load_2d(sm.stage[st] + kFN * kBlock, &amap, k * kBlock, 0, &sm.full[st]);
+          tma::load_2d(sm.stage[st], &bmap, k * kBlock, w.n0, &sm.full[st]);
+          tma::load_2d(sm.stage[st] + kTN * kBlock, &amap, k * kBlock, w.m0, &sm.full[st]);
         }
       }
-      for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+      for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)   // every issued copy lands before exit
         for (uint32_t w = 0; w < (1u << 22); ++w)
           if (tc::mbar_try_wait(&sm.full[i % kStages], (i / kStages) & 1)) break;
     }
     __syncwarp();
-  } else if (warp == 5) {
-    constexpr uint32_t idesc = idesc_fp8(kFN, kRows);
+  } else if (warp == kSumWarps + 1) {
+    // ================= MMA issue =================
+    constexpr uint32_t idesc = idesc_fp8(kTN, kRows);
     const uint32_t leader = elect_lane();
     uint32_t n = 0;
     bool ok = true;
-    for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
-      int k0, k1;
-      split_range(p, (int)(it % p.n_split), &k0, &k1);
-      for (int k = k0; k < k1; ++k, ++n) {
-        const uint32_t st = n % kStages, buf = n % kFBufs, use = n / kFBufs;
-        ok = wait_lanes(tc::smem_addr(lane == 2 ? &sm.acc_empty[buf] : &sm.full[st]), lane == 2 ? (use - 1) & 1 : (n / kStages) & 1,
-                        use > 0 ? 5u : 1u, abort);
+    for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+      const Item w = item(it);
+      for (int k = w.k0; k < w.k1; ++k, ++n) {
+        const uint32_t st = n % kStages, buf = n % kTBufs, use = n / kTBufs;
+        ok = wait_lanes(tc::smem_addr(lane == 1 ? &sm.acc_empty[buf] : &sm.full[st]), lane == 1 ? (use - 1) & 1 : (n / kStages) & 1,
+                        use > 0 ? 3u : 1u, abort);
         if (!ok) break;
         tc::tc_fence_after();
-        const uint32_t sw = tc::smem_addr(sm.stage[st]), sx = sw + kFN * kBlock;
+        const uint32_t sw = tc::smem_addr(sm.stage[st]), sx = sw + kTN * kBlock;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_fp8(leader, tm + buf * kRows, desc128(sw + 32 * ks), desc128(sx + 32 * ks), idesc, ks > 0);
+        for (int ks = 0; ks < 4; ++ks) mma_fp8(leader, tm + buf * kRows, desc128(sw + 32 * ks), desc128(sx + 32 * ks), idesc, ks > 0);
         commit_fp8(leader, &sm.empty[st]);
         commit_fp8(leader, &sm.acc_full[buf]);
       }
     }
     __syncwarp();
   } else {
-    // ================= scales and sums: thread = row of B, all rows of A =================
-    constexpr int kHeld = (kRows + 31) / 32;          // rows of A whose scales a lane holds
+    // ================= scales and sums: thread = row of B, kOwn rows of A =================
+    constexpr int kHeld = (kOwn + 31) / 32;          // rows of A whose scales a lane reads
+    const int lq = warp & 3, own0 = (warp >> 2) * kOwn;
+    const bool vec = p.kb % 4 == 0;                  // (the scales' rows start on 16 bytes)
     uint32_t n = 0;
     bool ok = true;
-    for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
-      const int s = (int)(it % p.n_split), n0 = (int)(it / p.n_split) * kFN;
-      int k0, k1;
-      split_range(p, s, &k0, &k1);
-      const float* sb = p.sb + (int64_t)(n0 / kBlock) * p.kb;
-      auto scale = [&](int k, int h) { return lane + 32 * h < p.M ? __ldg(p.sa + (int64_t)(lane + 32 * h) * p.kb + k) * __ldg(sb + k) : 0.f; };
-      float acc[kRows], next[kHeld];
+    for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+      const Item w = item(it);
+      const int m0 = w.m0 + own0;
+      const float* sb = p.sb + (int64_t)(w.n0 / kBlock) * p.kb;
+      float2 acc[kOwn / 2];
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) acc[j] = 0.f;
+      for (int j = 0; j < kOwn / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      float4 sc[kHeld];
+#pragma unroll 1
+      for (int k = w.k0; k < w.k1; ++k, ++n) {
+        const int i = k & 3, q = k & ~3;
+        if (k == w.k0 || i == 0) {                   // the scales of four blocks
 #pragma unroll
-      for (int h = 0; h < kHeld; ++h) next[h] = k0 < k1 ? scale(k0, h) : 0.f;
-      for (int k = k0; k < k1; ++k, ++n) {
-        float sc[kHeld];
-#pragma unroll
-        for (int h = 0; h < kHeld; ++h) {
-          sc[h] = next[h];
-          if (k + 1 < k1) next[h] = scale(k + 1, h);
+          for (int h = 0; h < kHeld; ++h) {
+            const int m = m0 + lane + 32 * h;
+            const float* sa = p.sa + (int64_t)(m < p.M ? m : 0) * p.kb;
+            if (vec) {
+              const float4 a = __ldg(reinterpret_cast<const float4*>(sa + q)), b = __ldg(reinterpret_cast<const float4*>(sb + q));
+              sc[h] = make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+            } else {
+              auto at = [&](int j) { return q + j < p.kb ? __ldg(sa + q + j) * __ldg(sb + q + j) : 0.f; };
+              sc[h] = make_float4(at(0), at(1), at(2), at(3));
+            }
+          }
         }
-        const uint32_t buf = n % kFBufs;
-        ok = __all_sync(0xffffffffu, wait_bar(&sm.acc_full[buf], (n / kFBufs) & 1, abort));
+        float* shared = sm.scale[warp][n & 1];
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+          if (lane + 32 * h < kOwn) shared[lane + 32 * h] = i == 0 ? sc[h].x : i == 1 ? sc[h].y : i == 2 ? sc[h].z : sc[h].w;
+        const uint32_t buf = n % kTBufs;
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.acc_full[buf], (n / kTBufs) & 1, abort));   // (and the scales are there)
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < kRows; c += 16) {
-          float r[16];
-          tc::tmem_ld16(tm + ((uint32_t)(32 * warp) << 16) + buf * kRows + c, r);
-          tc::tmem_wait_ld();
+        for (int c = 0; c < kOwn; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(tm + ((uint32_t)(32 * lq) << 16) + buf * kRows + own0 + c, r);
+          tmem_wait16(r);
+          if (c + 16 == kOwn) {   // the accumulator has been read
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.acc_empty[buf]);
+          }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(r[j], __shfl_sync(0xffffffffu, sc[(c + j) / 32], (c + j) & 31), acc[c + j]);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(shared + c + j);
+            acc[(c + j) / 2] = fma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), make_float2(f.x, f.y), acc[(c + j) / 2]);
+            acc[(c + j) / 2 + 1] = fma2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), make_float2(f.z, f.w), acc[(c + j) / 2 + 1]);
+          }
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.acc_empty[buf]);
       }
-      const int col = n0 + 32 * warp + lane;
+      const int col = w.n0 + 32 * lq + lane;
       if (!ok || col >= p.N) continue;
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        if (j >= p.M) break;
-        if (p.partial) p.partial[((int64_t)s * p.M + j) * p.ld + col] = acc[j];
-        else if (p.f32) static_cast<float*>(p.C)[(int64_t)j * p.N + col] = acc[j];
-        else static_cast<uint16_t*>(p.C)[(int64_t)j * p.N + col] = (uint16_t)(f32x2_bf16x2(acc[j], 0.f) & 0xFFFFu);
+      for (int j = 0; j < kOwn; ++j) {
+        if (m0 + j >= p.M) break;
+        const float v = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+        if (p.partial) p.partial[((int64_t)w.s * p.M + m0 + j) * p.ld + col] = v;
+        else if (p.f32) static_cast<float*>(p.C)[(int64_t)(m0 + j) * p.N + col] = v;
+        else static_cast<uint16_t*>(p.C)[(int64_t)(m0 + j) * p.N + col] = (uint16_t)(f32x2_bf16x2(v, 0.f) & 0xFFFFu);
       }
     }
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 4) tc::tmem_dealloc(tm, kCols);
+  if (warp == kSumWarps) tc::tmem_dealloc(tm, kCols);
   if (tid == 0 && *abort) raise_status(status, CSA2_STATUS_TIMEOUT);
 }
 
@@ -624,24 +661,35 @@ __global__ void __launch_bounds__(256) k_matmul_fp8_sum(const __grid_constant__ 
   }
 }
 constexpr int kSms = 152;
-constexpr int kFewRows = 64;
-
-// How a product is cut: the rows and columns of a tile, the CTAs that share B, and the splits of K that fill the SMs
-// where the tiles do not.
+// How a product is cut: the rows of A and of B of a tile, the CTAs that share B, and the splits of K.
 struct Cut {
   int m, n, ctas, n_split;
-  bool few;
+  bool thin;
 };
+// Estimated times in us, from measurements of shapes around the borders: a block of K takes 0.47 us in the wide kernel
+// and 0.45 (128 rows of A) or 0.3 in the thin one, the end of a tile 1.2 and 2 or 0.5, a launch that adds the partial sums 2.5, and these go to L2 and back
+// at 5 TB/s.  200 x 16,384 x 4,096: wide 20 us, thin 33; 161 x 1,001 x 1,552: wide (split) 18, thin 10.
+struct Estimate {
+  int n_split;
+  double us;
+};
+Estimate thin_time(int64_t tiles, int64_t kb, double block, double end, double bytes) {
+  Estimate best{1, (double)((tiles + kSms - 1) / kSms) * (kb * block + end)};
+  for (int n = 2; n <= std::min<int64_t>(kb, kSms / tiles); ++n) {
+    const double us = (double)((kb + n - 1) / n) * block + end + 2.5 + n * 2 * bytes / 5e6;
+    if (us < best.us) best = Estimate{n, us};
+  }
+  return best;
+}
 Cut cut_of(int M, int N, int K) {
-  Cut c;
-  c.few = M <= kFewRows;
-  c.m = c.few ? kFewRows : kWM;
-  c.n = c.few ? kFN : kWN;
-  c.ctas = !c.few && M > kWM ? 2 : 1;
-  const int64_t groups = ((M + c.m - 1) / c.m + c.ctas - 1) / c.ctas;
-  const int64_t kb = (K + kBlock - 1) / kBlock, tiles = groups * ((N + c.n - 1) / c.n);
-  c.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(kb, kSms / c.ctas / std::max<int64_t>(1, tiles)));
-  return c;
+  const int64_t kb = (K + kBlock - 1) / kBlock;
+  auto tiles = [&](int m, int n) { return (int64_t)((M + m - 1) / m) * ((N + n - 1) / n); };
+  const int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const Estimate thin = thin_time(std::max<int64_t>(1, tiles(rows, kTN)), kb, rows == 128 ? 0.45 : 0.3, rows == 128 ? 2. : 0.5, 4. * M * N);
+  const int64_t groups = tiles(kMc * kWM, kWN);
+  const double wide = (double)((groups + kSms / kMc - 1) / (kSms / kMc)) * (kb * 0.47 + 1.2);
+  if (M <= 128 || thin.us <= wide) return Cut{rows, kTN, 1, thin.n_split, true};
+  return Cut{kWM, kWN, kMc, 1, false};
 }
 int64_t partial_ld(int N) { return ((int64_t)N + 127) / 128 * 128; }
 
@@ -677,15 +725,14 @@ cudaError_t launch_matmul(Kernel kernel, size_t smem, int threads, int64_t items
   cfg.numAttrs = ctas > 1 ? 2 : 1;
   return counted(cudaLaunchKernelEx(&cfg, kernel, am, bm, rest..., status_word()));
 }
-template <int kMc>
 cudaError_t launch_wide(int64_t items, int sms, const CUtensorMap& am, const CUtensorMap& bm, MatmulPlan p, cudaStream_t s) {
   cudaFuncAttributes at;
-  const cudaError_t e = cudaFuncGetAttributes(&at, k_matmul_fp8_wide<kMc>);
+  const cudaError_t e = cudaFuncGetAttributes(&at, k_matmul_fp8_wide);
   if (e != cudaSuccess) return e;
   if (at.numRegs < kWRegs) return cudaErrorInvalidConfiguration;   // the register split would wait forever
   CUtensorMap cm = am;
   const int size = p.f32 ? 4 : 2;
-  p.c_map = !p.partial && (int64_t)p.N * size % 16 == 0;
+  p.c_map = (int64_t)p.N * size % 16 == 0;
   if (p.c_map) {
     const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
     const cuuint64_t strides[1] = {(cuuint64_t)p.N * size};
@@ -695,7 +742,13 @@ cudaError_t launch_wide(int64_t items, int sms, const CUtensorMap& am, const CUt
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  return launch_matmul(k_matmul_fp8_wide<kMc>, sizeof(WideSmem) + 1024, kWThreads, items, sms, kMc, s, am, bm, cm, p);
+  return launch_matmul(k_matmul_fp8_wide, sizeof(WideSmem) + 1024, kWThreads, items, sms, kMc, s, am, bm, cm, p);
+}
+
+template <int kRows>
+cudaError_t launch_thin(int64_t items, int sms, const CUtensorMap& am, const CUtensorMap& bm, const MatmulPlan& p, cudaStream_t s) {
+  static_assert(sizeof(ThinSmem<kRows>) + 1024 <= 232448, "shared memory");
+  return launch_matmul(k_matmul_fp8_thin<kRows>, sizeof(ThinSmem<kRows>) + 1024, kTThreads<kRows>, items, sms, 1, s, am, bm, p);
 }
 
 }  // namespace
@@ -730,17 +783,14 @@ cudaError_t launch_matmul_fp8(const uint8_t* a, const float* sa, const uint8_t* 
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   CUtensorMap am, bm;
-  const int rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  if (!row_map(&am, a, M, K, cut.few ? rows : kWM) || !row_map(&bm, b, N, K, cut.few ? kFN : kWN / cut.ctas))
-    return cudaErrorInvalidValue;
+  if (!row_map(&am, a, M, K, cut.m) || !row_map(&bm, b, N, K, cut.n / cut.ctas)) return cudaErrorInvalidValue;
   const int64_t items = (int64_t)((p.m_tiles + cut.ctas - 1) / cut.ctas) * p.n_tiles * p.n_split;
-  if (cut.few) {
-    if (rows == 16) e = launch_matmul(k_matmul_fp8_few<16>, sizeof(FewSmem<16>) + 1024, kFThreads, items, sms, 1, s, am, bm, p);
-    else if (rows == 32) e = launch_matmul(k_matmul_fp8_few<32>, sizeof(FewSmem<32>) + 1024, kFThreads, items, sms, 1, s, am, bm, p);
-    else e = launch_matmul(k_matmul_fp8_few<64>, sizeof(FewSmem<64>) + 1024, kFThreads, items, sms, 1, s, am, bm, p);
-  } else {
-    e = cut.ctas == 2 ? launch_wide<2>(items, sms, am, bm, p, s) : launch_wide<1>(items, sms, am, bm, p, s);
-  }
+  if (items > INT_MAX) return cudaErrorInvalidConfiguration;
+  if (!cut.thin) e = launch_wide(items, sms, am, bm, p, s);
+  else if (cut.m == 16) e = launch_thin<16>(items, sms, am, bm, p, s);
+  else if (cut.m == 32) e = launch_thin<32>(items, sms, am, bm, p, s);
+  else if (cut.m == 64) e = launch_thin<64>(items, sms, am, bm, p, s);
+  else e = launch_thin<128>(items, sms, am, bm, p, s);
   if (e != cudaSuccess || p.n_split == 1) return e;
   const unsigned gy = (unsigned)std::min(M, 32768);
   return launch_step(k_matmul_fp8_sum, dim3((unsigned)((N + 1023) / 1024), gy, (unsigned)((M + gy - 1) / gy)), dim3(256), 0, s, p);
