@@ -34,8 +34,11 @@ constexpr int kBlock = 128;                // columns that share a scale (and ro
 
 // ---- packing --------------------------------------------------------------------------------------
 // amax of a block's 128 values, a = max(amax, 2^-100); scale a / 448, codes E4M3_rne_satfinite(x * (448 / a)).
-// Bytes bound it: a quarter warp's loads of 16 bytes a lane, four blocks in flight.
-constexpr int kPackThreads = 256;
+// Bytes bound it, and instructions not far behind (a block of fp32 leaves 108 issue slots per SM): a warp takes two
+// blocks that lie behind one another, both loads in flight (4 columns a lane), one reduction instruction a block, and
+// their divisions at once, in a lane each.  16,411 x 4,240 of fp32 in a wider tensor: 55 us, 6.4 TB/s.  (Four blocks a
+// warp and fewer warps 58, eight 74: many small blocks of threads load and store at different times.)
+constexpr int kPackThreads = 256, kPackMany = 2;
 constexpr float kFloor = 0x1p-100f;
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -46,60 +49,70 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return r;
 }
 
-// kF32: 32 lanes share a block, 4 columns each; bf16: 16 lanes, 8 columns each.
+// many: blocks of a warp (at most kPackMany).
 template <bool kF32>
-__global__ void __launch_bounds__(kPackThreads) k_pack_fp8_blocks(const void* x, int64_t stride, int64_t rows, int K, int kb_n, int64_t blocks,
+__global__ void __launch_bounds__(kPackThreads, 8) k_pack_fp8_blocks(const void* x, int64_t stride, int K, int kb_n, int64_t blocks, int many,
                                                                   uint8_t* __restrict__ codes, float* __restrict__ scales) {
-  constexpr int kLanes = kF32 ? 32 : 16, kCols = kBlock / kLanes, kMany = 4;
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes;
-  constexpr int kPer = 32 / kLanes;              // blocks of a warp
-  const int64_t step = (int64_t)gridDim.x * (kPackThreads / kLanes);
-  // (the loop runs on the warp's first block, so that its lanes stay together)
-  for (int64_t w0 = ((int64_t)blockIdx.x * kPackThreads + threadIdx.x) / 32 * kPer; w0 < blocks; w0 += kMany * step) {
-    uint4 v[kMany];
-    int64_t row[kMany];
-    int col[kMany];
+  const int lane = threadIdx.x & 31;
+  const int64_t b0 = ((int64_t)blockIdx.x * (kPackThreads / 32) + (threadIdx.x >> 5)) * many;
+  if (b0 >= blocks) return;
+  const int n = (int)min((int64_t)many, blocks - b0);
+  const int64_t row0 = b0 / kb_n;
+  const int kb0 = (int)(b0 - row0 * kb_n);
+  uint4 v[kPackMany];            // (bf16: two words)
+  int64_t row = row0;
+  int kb = kb0;
 #pragma unroll
-    for (int i = 0; i < kMany; ++i) {
-      const int64_t b = w0 + i * step + sub;
-      row[i] = b / kb_n;
-      col[i] = b < blocks ? (int)(b - row[i] * kb_n) * kBlock + lane * kCols : K;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (col[i] < K) v[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(x) + (row[i] * stride + col[i]) * (kF32 ? 4 : 2));
+  for (int i = 0; i < kPackMany; ++i) {
+    v[i] = make_uint4(0, 0, 0, 0);
+    const int col = kb * kBlock + lane * 4;
+    if (i < n && col < K) {
+      if (kF32) {
+        v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(x) + row * stride + col));
+      } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + row * stride + col));
+        v[i].x = w.x;
+        v[i].y = w.y;
+      }
     }
+    if (++kb == kb_n) {
+      kb = 0;
+      ++row;
+    }
+  }
+  auto values = [&](int i, float (&f)[4]) {
+    f[0] = __uint_as_float(kF32 ? v[i].x : v[i].x << 16);
+    f[1] = __uint_as_float(kF32 ? v[i].y : v[i].x & 0xFFFF0000u);
+    f[2] = __uint_as_float(kF32 ? v[i].z : v[i].y << 16);
+    f[3] = __uint_as_float(kF32 ? v[i].w : v[i].y & 0xFFFF0000u);
+  };
+  float amax = 0.f;              // of block `lane`
 #pragma unroll
-    for (int i = 0; i < kMany; ++i) {
-      const int64_t b = w0 + i * step + sub;
-      float f[kCols];
+  for (int i = 0; i < kPackMany; ++i) {
+    float f[4];
+    values(i, f);
+    // (fmaxf drops a NaN; the bits of what is left order like the values)
+    const float m = fmaxf(fmaxf(fmaxf(0.f, fabsf(f[0])), fabsf(f[1])), fmaxf(fmaxf(0.f, fabsf(f[2])), fabsf(f[3])));
+    const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    if (lane == i) amax = all;
+  }
+  const float a = fmaxf(amax, kFloor), inv = 448.f / a;
+  if (lane < n) scales[b0 + lane] = a / 448.f;
+  row = row0;
+  kb = kb0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = word_of(v[i], j);
-        if (kF32) {
-          f[j] = __uint_as_float(w);
-        } else {
-          f[(2 * j) % kCols] = __uint_as_float(w << 16);
-          f[(2 * j + 1) % kCols] = __uint_as_float(w & 0xFFFF0000u);
-        }
-      }
-      float amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) amax = fmaxf(amax, fabsf(f[j]));
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float a = fmaxf(amax, kFloor), inv = 448.f / a;
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) f[j] *= inv;
-      uint8_t* out = codes + row[i] * K + col[i];
-      if (col[i] < K) {
-        if (kF32)
-          *reinterpret_cast<uint32_t*>(out) = e4m3x4(f[0], f[1], f[2], f[3]);
-        else
-          *reinterpret_cast<uint2*>(out) =
-              make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4 % kCols], f[5 % kCols], f[6 % kCols], f[7 % kCols]));
-      }
-      if (lane == 0 && b < blocks) scales[b] = a / 448.f;
+  for (int i = 0; i < kPackMany; ++i) {
+    float f[4];
+    values(i, f);
+    const float q = __shfl_sync(0xffffffffu, inv, i);
+    const int col = kb * kBlock + lane * 4;
+    if (i < n && col < K)
+      *reinterpret_cast<uint32_t*>(codes + row * K + col) = e4m3x4(f[0] * q, f[1] * q, f[2] * q, f[3] * q);
+    if (++kb == kb_n) {
+      kb = 0;
+      ++row;
     }
   }
 }
@@ -756,11 +769,12 @@ cudaError_t launch_thin(int64_t items, int sms, const CUtensorMap& am, const CUt
 cudaError_t launch_pack_fp8_blocks(const void* x, int dtype, int64_t stride, int64_t rows, int K, uint8_t* codes, float* scales, cudaStream_t s) {
   const int kb = (K + kBlock - 1) / kBlock;
   const int64_t blocks = rows * kb;
-  const int per = kPackThreads / (dtype == CSA2_F32 ? 32 : 16);
-  const int64_t grid = std::min<int64_t>((blocks + per - 1) / per, 152 * 8);
-  return dtype == CSA2_F32
-             ? launch_step(k_pack_fp8_blocks<true>, dim3((unsigned)grid), dim3(kPackThreads), 0, s, x, stride, rows, K, kb, blocks, codes, scales)
-             : launch_step(k_pack_fp8_blocks<false>, dim3((unsigned)grid), dim3(kPackThreads), 0, s, x, stride, rows, K, kb, blocks, codes, scales);
+  // one block a warp where there are not enough of them for two blocks of threads on every SM
+  const int many = (int)std::max<int64_t>(1, std::min<int64_t>(kPackMany, blocks / (152 * 2 * (kPackThreads / 32))));
+  const int64_t per = (int64_t)many * (kPackThreads / 32), grid = (blocks + per - 1) / per;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  return launch_step(dtype == CSA2_F32 ? k_pack_fp8_blocks<true> : k_pack_fp8_blocks<false>, dim3((unsigned)grid), dim3(kPackThreads), 0, s, x, stride,
+                     K, kb, blocks, many, codes, scales);
 }
 
 size_t matmul_fp8_workspace_bytes(int M, int N, int K) {
