@@ -507,38 +507,39 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   const uint32_t tm = sm.tmem;
 
   if (mma_warp) {
-    // ================= MMA issue (one thread; an MMA issue blocks while the tensor pipe is busy) ====
-    if (lane == 0) {
-      constexpr uint32_t kIdS = tc::idesc_f16(128, kHeads, 0, 0, 0);   // K-major A and B
-      constexpr uint32_t kIdO = tc::idesc_f16(128, kHeads, 0, 1, 1);   // MN-major A and B
-      const uint64_t dk_s = tc::smem_desc(tc::smem_addr(sm.k), 128, 8192);
-      const uint64_t dq_s = tc::smem_desc(tc::smem_addr(sm.q), 128, 8192);
-      const uint64_t dk_o = tc::smem_desc(tc::smem_addr(sm.k), 8192, 128);
-      const uint64_t dp_o = tc::smem_desc(tc::smem_addr(sm.p), 1024, 128);
-      for (int it = 0; it < n_my; ++it) {
-        bool ok = true;
+    // ================= MMA issue (a warp of its own: an MMA issue blocks while the tensor pipe is busy) ====
+    constexpr uint32_t kIdS = tc::idesc_f16(128, kHeads, 0, 0, 0);   // K-major A and B
+    constexpr uint32_t kIdO = tc::idesc_f16(128, kHeads, 0, 1, 1);   // MN-major A and B
+    const uint64_t dk_s = tc::smem_desc(tc::smem_addr(sm.k), 128, 8192);
+    const uint64_t dq_s = tc::smem_desc(tc::smem_addr(sm.q), 128, 8192);
+    const uint64_t dk_o = tc::smem_desc(tc::smem_addr(sm.k), 8192, 128);
+    const uint64_t dp_o = tc::smem_desc(tc::smem_addr(sm.p), 1024, 128);
+    const uint32_t leader = tc::elect_lane();
+    for (int it = 0; it < n_my; ++it) {
+      bool ok = true;
 #pragma unroll
-        for (int sl = 0; sl < 4; ++sl) {
-          ok = ok && tc::mbar_wait(&sm.k_ready[sl], it & 1, 1u << 22);
-          if (!ok) break;
-          tc::tc_fence_after();
-#pragma unroll
-          for (int ks = 8 * sl; ks < 8 * sl + 8; ++ks)   // descriptor addresses advance in 16-byte units
-            tc::mma_f16(tm + kColS, dk_s + (uint64_t)(ks * 16), dq_s + (uint64_t)(ks * 16), kIdS, ks > 0);
-        }
-        if (!ok) { *abort = 1; break; }
-        tc::mma_commit(&sm.bar_s);
-        if (!tc::mbar_wait(&sm.p_ready, it & 1, 1u << 22)) { *abort = 1; break; }
+      for (int sl = 0; sl < 4; ++sl) {
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.k_ready[sl], it & 1, 1u << 22));
+        if (!ok) break;
         tc::tc_fence_after();
-        // PV over the chunk's keys only (a short last chunk skips its empty 16-key steps)
-        const int ksteps = (min(kChunk, kb1 - kb0 - kChunk * it) + 15) / 16;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {   // tile by tile: a finished tile frees its K slice for the next chunk
-          for (int kk = 0; kk < ksteps; ++kk)
-            tc::mma_f16(tm + kColO + 64 * mt, dk_o + (uint64_t)(mt * 128 + kk * 1024), dp_o + (uint64_t)(kk * 128),
-                        kIdO, (it > 0 || kk > 0) ? 1u : 0u);
-          tc::mma_commit(&sm.bar_pv[mt]);
-        }
+        for (int ks = 8 * sl; ks < 8 * sl + 8; ++ks)   // descriptor addresses advance in 16-byte units
+          tc::mma_f16_by(leader, tm + kColS, dk_s + (uint64_t)(ks * 16), dq_s + (uint64_t)(ks * 16), kIdS, ks > 0);
+      }
+      if (!ok) { *abort = 1; break; }
+      tc::mma_commit_by(leader, &sm.bar_s);
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.p_ready, it & 1, 1u << 22))) { *abort = 1; break; }
+      tc::tc_fence_after();
+      // PV over the chunk's keys only (a short last chunk skips its empty 16-key steps)
+      const int ksteps = (min(kChunk, kb1 - kb0 - kChunk * it) + 15) / 16;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {   // tile by tile: a finished tile frees its K slice for the next chunk
+#pragma unroll
+        for (int kk = 0; kk < kChunk / 16; ++kk)
+          if (kk < ksteps)
+            tc::mma_f16_by(leader, tm + kColO + 64 * mt, dk_o + (uint64_t)(mt * 128 + kk * 1024), dp_o + (uint64_t)(kk * 128),
+                           kIdO, (it > 0 || kk > 0) ? 1u : 0u);
+        tc::mma_commit_by(leader, &sm.bar_pv[mt]);
       }
     }
     __syncwarp();

@@ -132,14 +132,8 @@ struct MatmulPlan {
 constexpr uint32_t kIdFp8 = 1u << 4;   // instruction descriptor: fp32 accumulation, E4M3 x E4M3, both K-major
 __host__ __device__ constexpr uint32_t idesc_fp8(int M, int N) { return kIdFp8 | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 
-// The MMA warp runs as a whole, so that the operands of its MMAs are uniform registers, and one lane (leader != 0)
-// issues: from a single thread's branch an MMA took 100 cycles to issue and a commit 84 (now 10 and 50), and a block's
-// four with its two commits then took longer to issue than the 513 cycles that they run.
-__device__ __forceinline__ uint32_t elect_lane() {
-  uint32_t e;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
-  return e;
-}
+// D[tmem] (+)= A . B^T of E4M3, issued by one lane of a warp that runs as a whole (tc::elect_lane): from a single thread's
+// branch a block's four MMAs with their two commits took longer to issue than the 513 cycles that they run.
 __device__ __forceinline__ void mma_fp8(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p, e;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
@@ -147,14 +141,7 @@ __device__ __forceinline__ void mma_fp8(uint32_t leader, uint32_t d_tmem, uint64
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void commit_fp8(uint32_t leader, uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_addr(bar)),
-      "r"(leader)
-      : "memory");
-}
-// The same, arriving on the barrier at `bar`'s offset in every CTA of the cluster in `mask`.
+// tc::mma_commit_by arriving on the barrier at `bar`'s offset in every CTA of the cluster in `mask`.
 __device__ __forceinline__ void commit_fp8_mc(uint32_t leader, uint64_t* bar, uint16_t mask) {
   asm volatile(
       "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
@@ -371,7 +358,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
     } else if (warp == kWSumWarps + 1) {
       // ================= MMA issue =================
       constexpr uint32_t idesc = idesc_fp8(kWM, kWN);
-      const uint32_t leader = elect_lane();
+      const uint32_t leader = tc::elect_lane();
       uint32_t n = 0;
       bool ok = true;
       for (int it = it0; ok && it < items; it += stride) {
@@ -385,7 +372,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
           const uint32_t sa = tc::smem_addr(sm.stage[st]), sb = sa + kWM * kBlock;
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) mma_fp8(leader, tm + buf * kWN, desc128(sa + 32 * ks), desc128(sb + 32 * ks), idesc, ks > 0);
-          commit_fp8(leader, &sm.acc_full[buf]);
+          tc::mma_commit_by(leader, &sm.acc_full[buf]);
           commit_fp8_mc(leader, &sm.empty[st], kMask);
         }
       }
@@ -558,7 +545,7 @@ k_matmul_fp8_thin(const __grid_constant__ CUtensorMap amap, const __grid_constan
   } else if (warp == kSumWarps + 1) {
     // ================= MMA issue =================
     constexpr uint32_t idesc = idesc_fp8(kTN, kRows);
-    const uint32_t leader = elect_lane();
+    const uint32_t leader = tc::elect_lane();
     uint32_t n = 0;
     bool ok = true;
     for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
@@ -572,8 +559,8 @@ k_matmul_fp8_thin(const __grid_constant__ CUtensorMap amap, const __grid_constan
         const uint32_t sw = tc::smem_addr(sm.stage[st]), sx = sw + kTN * kBlock;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_fp8(leader, tm + buf * kRows, desc128(sw + 32 * ks), desc128(sx + 32 * ks), idesc, ks > 0);
-        commit_fp8(leader, &sm.empty[st]);
-        commit_fp8(leader, &sm.acc_full[buf]);
+        tc::mma_commit_by(leader, &sm.empty[st]);
+        tc::mma_commit_by(leader, &sm.acc_full[buf]);
       }
     }
     __syncwarp();
