@@ -360,12 +360,13 @@ def csa2_page_plan(dims: Dims, pool: PagePool, seq_len, n_new, seq_len_out, n_en
 
 
 def _strided(t: torch.Tensor):
-    """Address of a tensor whose last dimension is contiguous, whatever its other strides."""
+    """Address and strides of a tensor whose last dimension is contiguous, whatever its other strides."""
     if not t.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if strides[-1] != 1 and t.shape[-1] > 1:
         raise ValueError("the tensor's last dimension must be contiguous")
-    return t.data_ptr()
+    return t.data_ptr(), strides
 
 
 _FLOAT_TYPES = {torch.float32: CSA2_F32, torch.bfloat16: CSA2_BF16}
@@ -381,8 +382,8 @@ def _float_type(t: torch.Tensor) -> int:
 def csa2_pack_fp8_blocks(x, codes, scales, stream=None):
     """x [n][K] bf16 or fp32 (rows may be apart) -> codes [n][K] E4M3, scales fp32 [n][ceil(K/128)]."""
     n, K = x.shape
-    _check(lib().csa2_pack_fp8_blocks(_strided(x), _float_type(x), x.stride(0), n, K, ptr(codes), ptr(scales),
-                                      stream_handle(stream)))
+    address, strides = _strided(x)
+    _check(lib().csa2_pack_fp8_blocks(address, _float_type(x), strides[0], n, K, ptr(codes), ptr(scales), stream_handle(stream)))
 
 
 def csa2_matmul_fp8_workspace_size(M: int, N: int, K: int) -> int:
@@ -404,9 +405,13 @@ def csa2_rope_table(spec: RopeSpec, r: int, table, stream=None):
 def csa2_rope(x, y, positions, table, start=0, layout=ROPE_HALF, inverse=False, amplitude=1.0, stream=None):
     """y = x [tokens][heads][d] rotated by the positions [tokens]; table of r/2 pairs; y may be x."""
     n, heads, d = x.shape
-    _check(lib().csa2_rope(_strided(x), _float_type(x), x.stride(0), x.stride(1), _strided(y), _float_type(y), y.stride(0),
-                           y.stride(1), n, heads, d, start, 2 * table.numel(), layout, int(inverse), amplitude, ptr(positions),
-                           ptr(table), stream_handle(stream)))
+    if y.shape != x.shape:
+        raise ValueError(f"x and y must have the same shape (got {tuple(x.shape)} and {tuple(y.shape)})")
+    px, sx = _strided(x)
+    py, sy = _strided(y)
+    _check(lib().csa2_rope(px, _float_type(x), sx[0], sx[1], py, _float_type(y), sy[0], sy[1], n, heads, d, start,
+                           2 * table.numel(), layout, int(inverse), amplitude, ptr(positions), ptr(table),
+                           stream_handle(stream)))
 
 
 def csa2_tree_plan(dims: Dims, parent, ctx_len, q_pos, path, stream=None):

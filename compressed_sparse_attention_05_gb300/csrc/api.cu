@@ -769,6 +769,7 @@ int csa2_page_plan(const csa2_dims* dm, const csa2_page_pool* pool, const int32_
   a.n_entries = n_entries; a.first_entry = first_entry; a.granted = granted;
   a.q_pos = dm->Tq > 0 ? q_pos : nullptr; a.slots = max_new > 0 ? slots : nullptr;
   a.B = dm->B; a.Tq = dm->Tq; a.max_pages = dm->max_pages; a.max_new = max_new;
+  a.q_pos4 = dm->Tq % 4 == 0 && aligned16(q_pos);
   LAUNCH(launch_page_plan(a, ws, static_cast<cudaStream_t>(stream)), "page_plan");
   return CSA2_OK;
 }

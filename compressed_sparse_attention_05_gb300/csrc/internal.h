@@ -306,6 +306,7 @@ struct PagePlanArgs {
   int32_t* q_pos;             // [B][Tq] or null
   int64_t* slots;             // [B][max_new] or null
   int B, Tq, max_pages, max_new;
+  bool q_pos4;                // rows of q_pos start on 16 bytes and have a multiple of 4
 };
 size_t page_plan_workspace_bytes(int B);
 cudaError_t launch_page_plan(const PagePlanArgs& a, void* ws, cudaStream_t s);

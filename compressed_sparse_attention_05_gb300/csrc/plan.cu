@@ -38,21 +38,9 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {
   }
   return v;
 }
-// Inclusive prefix sum over the block and its total (all threads call; two barriers).
-__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* sums, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  v = warp_scan64(v, lane);
-  __syncthreads();
-  if (lane == 31) sums[warp] = v;
-  __syncthreads();
-  const int64_t w = warp_scan64(lane < warps ? sums[lane] : 0, lane);
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-  return v + (warp ? before : 0);
-}
-
 // The page at place i of the stack: the free list, then the released pages in the order of their sequences.
 __device__ __forceinline__ int32_t stack_page(const PagePlanArgs& a, const PageHead& h, const PageRow* rows, int64_t i) {
+  if (i < 0 || i >= (int64_t)h.n_free + h.released) return -1;
   if (i < h.n_free) return a.free_pages[i];
   const int32_t j = (int32_t)(i - h.n_free);
   int lo = 0, hi = a.B - 1;                 // the last sequence whose released pages begin at or before j
@@ -65,31 +53,51 @@ __device__ __forceinline__ int32_t stack_page(const PagePlanArgs& a, const PageH
   return a.page_table[(int64_t)lo * a.max_pages + r.need + (j - r.back)];
 }
 
-// Columns first, first + step, ... of sequence b.
+// What thread `t` of `threads` writes of sequence b: new places in the table, positions, slots.  A warp takes the slots of
+// a page, which is looked up once for all of them.
 __device__ __forceinline__ void fill_row(const PagePlanArgs& a, const PageHead& h, const PageRow* rows, const PageRow& r, int b,
-                                         int64_t first, int64_t step, uint32_t* status) {
+                                         int64_t t, int64_t threads, uint32_t* status) {
   auto new_page = [&](int p) { return stack_page(a, h, rows, (int64_t)h.n_free + h.released - 1 - (r.take + (p - r.held))); };
   int32_t* table = a.page_table + (int64_t)b * a.max_pages;
-  for (int64_t k = first; k < (int64_t)r.need - r.held; k += step) {
+  for (int64_t k = t; k < (int64_t)r.need - r.held; k += threads) {
     const int32_t page = new_page(r.held + (int)k);
     if (page < 0 || page >= a.n_pages) raise_status(status, CSA2_STATUS_BAD_PAGE);
     table[r.held + k] = page;
   }
-  if (a.q_pos)
-    for (int64_t i = first; i < a.Tq; i += step) a.q_pos[(int64_t)b * a.Tq + i] = i < r.n_new ? r.len + (int32_t)i : -1;
-  if (a.slots)
-    for (int64_t i = first; i < a.max_new; i += step) {
-      const int64_t e = r.e0 + i;
-      int64_t slot = -1;
-      if (e < r.e1) {
-        const int p = (int)(e >> 6);
-        // (a page behind `held` may not be in the table yet: another thread writes it)
-        const int32_t page = p < r.held ? table[p] : new_page(p);
-        if (page >= 0 && page < a.n_pages) slot = (int64_t)page * kPage + (e & (kPage - 1));
-        else raise_status(status, CSA2_STATUS_BAD_PAGE);
-      }
-      a.slots[(int64_t)b * a.max_new + i] = slot;
+  if (a.q_pos) {
+    int32_t* out = a.q_pos + (int64_t)b * a.Tq;
+    auto at = [&](int64_t i) { return i < r.n_new ? r.len + (int32_t)i : -1; };
+    if (a.q_pos4) {        // four at a time: rows start on 16 bytes
+      for (int64_t i = 4 * t; i < a.Tq; i += 4 * threads)
+        *reinterpret_cast<int4*>(out + i) = make_int4(at(i), at(i + 1), at(i + 2), at(i + 3));
+    } else {
+      for (int64_t i = t; i < a.Tq; i += threads) out[i] = at(i);
     }
+  }
+  if (a.slots) {
+    int64_t* out = a.slots + (int64_t)b * a.max_new;
+    const int lane = threadIdx.x & 31;
+    const int p0 = r.e0 >> 6;                                // column i is place (e0 + i) % 64 of page p0 + ...
+    const int64_t groups = ((r.e0 & (kPage - 1)) + (int64_t)a.max_new + kPage - 1) / kPage;
+    for (int64_t g = t >> 5; g < groups; g += threads >> 5) {
+      const int64_t p = p0 + g;
+      int32_t page = -1;
+      if (r.e1 > r.e0 && p * kPage < r.e1) {                 // (so p is below `need`)
+        // (a page behind `held` may not be in the table yet: another thread writes it)
+        page = p < r.held ? table[p] : new_page((int)p);
+        if (page < 0 || page >= a.n_pages) {
+          if (lane == 0) raise_status(status, CSA2_STATUS_BAD_PAGE);
+          page = -1;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int place = lane + 32 * u;
+        const int64_t e = p * kPage + place, i = e - r.e0;
+        if (i >= 0 && i < a.max_new) out[i] = page >= 0 && e < r.e1 ? (int64_t)page * kPage + place : -1;
+      }
+    }
+  }
 }
 
 // Released pages that nobody took go back on the free list.
@@ -102,12 +110,16 @@ __device__ __forceinline__ void push_released(const PagePlanArgs& a, const PageH
   }
 }
 
+// fill_here: the columns too (then the rows stay in shared memory, as far as they fit).
+constexpr int kSharedRows = 256;
 __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PagePlanArgs a, PageHead* head, PageRow* rows, int fill_here, uint32_t* status) {
-  __shared__ int64_t s_sums[32];
+  __shared__ int64_t s_sums[2][32];
   __shared__ PageHead s_head;
+  __shared__ PageRow s_rows[kSharedRows];
   if (!fill_here) pdl_trigger();   // k_page_fill waits for this kernel; what follows it must not start before both are done
   pdl_wait();
-  const int tid = threadIdx.x, threads = blockDim.x;
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
+  if (fill_here && a.B <= kSharedRows) rows = s_rows;
   // one sequence's counts, or a change of nothing where its state is impossible
   auto read = [&](int b, bool report) {
     PageRow r;
@@ -128,76 +140,104 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PagePlanArgs a, Page
     if (!ok && report) raise_status(status, CSA2_STATUS_BAD_COUNT);
     return r;
   };
-  // pages given back by all sequences (they are there to be handed out to any)
-  int64_t mine = 0, released = 0;
-  for (int b = tid; b < a.B; b += threads) {
-    const PageRow r = read(b, false);
-    mine += max(0, r.held - r.need);
-  }
-  block_scan64(mine, s_sums, &released);
+  // Inclusive prefix sums over the block of two values, and their totals.  (A warp's worth of sequences takes no barrier.)
+  auto scan2 = [&](int64_t& x, int64_t& y, int64_t* all_x, int64_t* all_y) {
+    x = warp_scan64(x, lane);
+    y = warp_scan64(y, lane);
+    __syncthreads();
+    if (lane == 31) {
+      s_sums[0][warp] = x;
+      s_sums[1][warp] = y;
+    }
+    __syncthreads();
+    const int64_t wx = warp_scan64(lane < warps ? s_sums[0][lane] : 0, lane), wy = warp_scan64(lane < warps ? s_sums[1][lane] : 0, lane);
+    *all_x = __shfl_sync(0xffffffffu, wx, 31);
+    *all_y = __shfl_sync(0xffffffffu, wy, 31);
+    const int64_t bx = __shfl_sync(0xffffffffu, wx, warp > 0 ? warp - 1 : 0), by = __shfl_sync(0xffffffffu, wy, warp > 0 ? warp - 1 : 0);
+    if (warp) {
+      x += bx;
+      y += by;
+    }
+  };
   const int32_t n_free = *a.n_free;
+  // The first batch of sequences stays in registers; with more, the pages that all of them give back (they are there to
+  // be handed out to any) are counted before.
+  PageRow r = {};
+  if (tid < a.B) r = read(tid, true);
+  int64_t back_inc = tid < a.B ? max(0, r.held - r.need) : 0, want_inc = tid < a.B ? max(0, r.need - r.held) : 0;
+  int64_t back_all, want_all;
+  scan2(back_inc, want_inc, &back_all, &want_all);
+  int64_t released = back_all;
+  if (a.B > threads) {
+    int64_t mine = 0, none = 0, total;
+    for (int b = threads + tid; b < a.B; b += threads) {
+      const PageRow q = read(b, true);
+      mine += max(0, q.held - q.need);
+    }
+    scan2(mine, none, &total, &none);
+    released += total;
+  }
   const int64_t avail = (int64_t)n_free + released;
   const bool sane = n_free >= 0 && avail <= a.n_pages;
   if (!sane && tid == 0) raise_status(status, CSA2_STATUS_BAD_COUNT);
-  int64_t back0 = 0, want0 = 0, taken = 0;
-  for (int b0 = 0; b0 < a.B; b0 += threads) {
+  if (tid == 0) s_head = PageHead{n_free, sane ? (int32_t)released : 0, 0, 0};
+  __syncthreads();
+  int64_t back0 = 0, want0 = 0;
+  for (int b0 = 0;;) {
     const int b = b0 + tid;
-    const bool live = b < a.B;
-    PageRow r = {};
-    if (live) r = read(b, true);
-    const int64_t back = live ? max(0, r.held - r.need) : 0, want = live ? max(0, r.need - r.held) : 0;
-    int64_t back_all, want_all;
-    const int64_t back_inc = block_scan64(back, s_sums, &back_all);
-    const int64_t want_inc = block_scan64(want, s_sums, &want_all);
-    // in order: a sequence gets its pages if they and all that was asked for before it are there
-    const bool granted = live && r.e1 >= 0 && sane && (want == 0 || want0 + want_inc <= avail);
-    if (live) {
-      const int32_t len0 = r.len, e_last = granted ? r.e1 : r.e0;
-      a.seq_len_out[b] = granted ? len0 + r.n_new : len0;
+    if (b < a.B) {
+      const int64_t back = max(0, r.held - r.need), want = max(0, r.need - r.held);
+      // in order: a sequence gets its pages if they and all that was asked for before it are there
+      const bool granted = r.e1 >= 0 && sane && (want == 0 || want0 + want_inc <= avail);
+      const int32_t e_last = granted ? r.e1 : r.e0;
+      a.seq_len_out[b] = granted ? r.len + r.n_new : r.len;
       a.n_entries[b] = e_last;
       a.first_entry[b] = min(r.e0, e_last);
       if (a.granted) a.granted[b] = granted ? 1 : 0;
       a.held[b] = granted ? r.need : r.held;
+      if (granted && want > 0) atomicMax(&s_head.taken, (int32_t)(want0 + want_inc));   // the last one granted has the sum
       if (!granted) r.need = r.held;
       r.n_new = granted ? max(0, r.n_new) : 0;
-      r.e1 = granted ? r.e1 : r.e0;
+      r.e1 = e_last;
       r.back = (int32_t)(back0 + back_inc - back);
       r.take = (int32_t)min((int64_t)INT_MAX, want0 + want_inc - want);
       rows[b] = r;
-      if (granted && want > 0) taken = want0 + want_inc;   // (grows with b: the last one granted has the sum)
     }
     back0 += back_all;
     want0 += want_all;
+    b0 += threads;
+    if (b0 >= a.B) break;
+    r = PageRow{};
+    const bool live = b0 + tid < a.B;
+    if (live) r = read(b0 + tid, false);
+    back_inc = live ? max(0, r.held - r.need) : 0;
+    want_inc = live ? max(0, r.need - r.held) : 0;
+    scan2(back_inc, want_inc, &back_all, &want_all);
   }
-  // the largest sum that was granted
   __syncthreads();
-  if (tid == 0) s_head = PageHead{n_free, sane ? (int32_t)released : 0, 0, 0};
-  __syncthreads();
-  if (taken > 0) atomicMax(&s_head.taken, (int32_t)taken);
-  __syncthreads();
+  const PageHead h = s_head;
   if (tid == 0) {
-    *head = s_head;
-    if (sane) *a.n_free = s_head.n_free + s_head.released - s_head.taken;
+    if (!fill_here) *head = h;
+    if (sane) *a.n_free = h.n_free + h.released - h.taken;
   }
   if (!fill_here) return;
-  // ---- few columns: written here (rows[] of this block are visible after the barrier)
-  const PageHead h = s_head;
-  const int64_t cols = max(max((int64_t)(a.q_pos ? a.Tq : 0), a.slots ? (int64_t)a.max_new : 0), (int64_t)32);
-  const int per = cols >= threads ? threads : (int)((cols + 31) / 32) * 32;   // threads to a sequence
-  const int lanes = threads / per * per;
-  if (tid < lanes)
-    for (int b = tid / per; b < a.B; b += threads / per) fill_row(a, h, rows, rows[b], b, tid % per, per, status);
+  // ---- few columns: written here, a power of two of warps to a sequence
+  int per = 32;
+  while (per < threads && per * min(a.B, threads / per) < threads && per * 2 <= threads) per *= 2;
+  const int teams = threads / per;
+  if (tid < teams * per)
+    for (int b = tid / per; b < a.B; b += teams) fill_row(a, h, rows, rows[b], b, tid % per, per, status);
   push_released(a, h, rows, tid, threads, status);
 }
 
-constexpr int kFillThreads = 256, kFillPer = 8;   // threads of a block, columns of a thread
+constexpr int kFillThreads = 256, kFillPer = 16;   // threads of a block, columns of a thread
 
 __global__ void __launch_bounds__(kFillThreads) k_page_fill(PagePlanArgs a, const PageHead* head, const PageRow* rows, uint32_t* status) {
   pdl_wait();
   const PageHead h = *head;
-  const int64_t first = (int64_t)blockIdx.x * kFillThreads + threadIdx.x, step = (int64_t)gridDim.x * kFillThreads;
-  for (int b = blockIdx.y; b < a.B; b += gridDim.y) fill_row(a, h, rows, rows[b], b, first, step, status);
-  push_released(a, h, rows, first + step * blockIdx.y, step * gridDim.y, status);
+  const int64_t t = (int64_t)blockIdx.x * kFillThreads + threadIdx.x, threads = (int64_t)gridDim.x * kFillThreads;
+  for (int b = blockIdx.y; b < a.B; b += gridDim.y) fill_row(a, h, rows, rows[b], b, t, threads, status);
+  push_released(a, h, rows, t + threads * blockIdx.y, threads * gridDim.y, status);
 }
 
 // ---- a tree of drafted tokens -----------------------------------------------------------------
@@ -258,7 +298,9 @@ cudaError_t launch_page_plan(const PagePlanArgs& a, void* ws, cudaStream_t s) {
   PageRow* rows = reinterpret_cast<PageRow*>(static_cast<char*>(ws) + head_bytes());
   const int64_t cols = std::max<int64_t>(std::max<int64_t>(a.q_pos ? a.Tq : 0, a.slots ? a.max_new : 0), 1);
   const bool here = cols * a.B <= kFillHere;
-  const int threads = here ? kPlanThreads : std::min(kPlanThreads, (a.B + 31) / 32 * 32);
+  // as many threads as there are sequences, and for the columns up to eight warps to a sequence
+  const int64_t warps = (a.B + 31) / 32, want = here ? std::max<int64_t>(warps, a.B * std::min<int64_t>((cols + 63) / 64, 8)) : warps;
+  const int threads = (int)std::min<int64_t>(kPlanThreads / 32, want) * 32;
   cudaError_t e = launch_step(k_page_plan, dim3(1), dim3(threads), 0, s, a, head, rows, (int)here, status_word());
   if (e != cudaSuccess || here) return e;
   const unsigned gx = (unsigned)std::min<int64_t>((cols + kFillThreads * kFillPer - 1) / (kFillThreads * kFillPer), 65535);
