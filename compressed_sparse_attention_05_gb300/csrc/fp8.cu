@@ -8,15 +8,17 @@
 // k_matmul_fp8_wide (many rows of A): tiles of 128 rows of A x 256 rows of B.  A row of A is a lane of the accumulator,
 //   so a thread has one scale per block: sa[its row] sb[its 128 columns].  Two CTAs with tiles above one another copy B's
 //   rows for each other (32 KB out of L2 for each instead of 48).
-//   4,096 x 32,768 x 4,096 takes 440 us (2.5 PFLOP/s of fp8).  What bounds it: a block's MMAs run 513 cycles, and the
-//   way MMA -> sums (200 cycles after the last product) -> accumulator read (300) -> next MMAs (200) about as long again,
-//   with two accumulators (all of tensor memory) to hide it; the sums themselves take 310 cycles of every scheduler.
+//   4,096 x 32,768 x 4,096 takes 417 us (2.6 PFLOP/s) from a cool start and 447 (2.5) in a row, at the card's 1,400 W:
+//   the power cap holds the clock at 1.88 GHz, and operands of zeros take 405.  Below that: a block's MMAs run 513 cycles,
+//   and the way MMA -> sums (200 cycles after the last product) -> accumulator read (300) -> next MMAs (200) about as long
+//   again, with two accumulators (all of tensor memory) to hide it; the tensor pipe is active for 53% of the cycles.
 //   Tried: a pair of CTAs with one MMA for both (cta_group::2; its arrivals from SM to SM are too slow for this way:
-//   480 us), 16 sum warps (570, registers), named barriers in the place of shared-memory ones (530).
+//   480 us), 16 sum warps (570, registers), halves of the accumulator on their own (478), named barriers in the place of
+//   shared-memory ones, loads and looks ahead in the sums (no difference).
 // k_matmul_fp8_thin (few rows of A, or few tiles): the rows of B, the weights, are the MMA's M side, 128 at a time, and
 //   16 to 128 rows of A its N side, so that no part of the tensor cores' work and of shared memory goes to rows that are
 //   not there, and 128 B-rows x 128 columns (16 KB) per block stream through a deep ring.  A thread has a weight row and
-//   up to 64 rows of A; their scales go through shared memory.  32 x 32,768 x 4,096: 27.6 us, 4.9 TB/s.
+//   up to 64 rows of A; their scales go through shared memory.  32 x 32,768 x 4,096: 24.8 us, 5.5 TB/s.
 //   Where its tiles do not fill the SMs, the blocks of K are split over several CTAs, which leave fp32 partial sums that
 //   k_matmul_fp8_sum adds in order.
 #include <algorithm>
@@ -228,21 +230,14 @@ __device__ __forceinline__ void split_range(const MatmulPlan& p, int s, int* k0,
   *k1 = (int)((int64_t)(s + 1) * p.kb / p.n_split);
 }
 
-// Shared by both kernels: the ring of operand stages and the accumulators' barriers.
-template <int kStages, int kStageBytes, int kBufs>
-struct Ring {
-  unsigned char stage[kStages][kStageBytes];   // 1024-aligned
-  uint64_t full[kStages], empty[kStages], acc_full[kBufs], acc_empty[kBufs];
-  uint32_t tmem;
-  int abort;
-};
-template <typename R, int kStages, int kBufs>
-__device__ __forceinline__ void ring_init(R& sm, uint32_t writers, uint32_t readers) {
-  for (int i = 0; i < kStages; ++i) {
+// The barriers of a ring of operand stages (writers: arrivals that free one) and of the accumulators.
+template <typename Smem>
+__device__ __forceinline__ void ring_init(Smem& sm, int stages, int bufs, uint32_t writers, uint32_t readers) {
+  for (int i = 0; i < stages; ++i) {
     tc::mbar_init(&sm.full[i], 1);
     tc::mbar_init(&sm.empty[i], writers);
   }
-  for (int i = 0; i < kBufs; ++i) {
+  for (int i = 0; i < bufs; ++i) {
     tc::mbar_init(&sm.acc_full[i], 1);
     tc::mbar_init(&sm.acc_empty[i], readers);
   }
@@ -259,8 +254,12 @@ constexpr int kWThreads = kWSumWarps * 32 + 128;
 // to twice as long; this one does not.)
 constexpr int kWRegs = 168;
 constexpr int kWRegsSum = 224, kWRegsMisc = 56;
-struct WideSmem : Ring<kWStages, kWStageBytes, kWBufs> {
-  alignas(1024) unsigned char out[kWSumWarps][4096];   // of each sum warp: 32 rows x 128 bytes of C on their way out
+struct WideSmem {
+  unsigned char stage[kWStages][kWStageBytes];   // 1024-aligned
+  unsigned char out[kWSumWarps][4096];           // of each sum warp: 32 rows x 128 bytes of C on their way out
+  uint64_t full[kWStages], empty[kWStages], acc_full[kWBufs], acc_empty[kWBufs];
+  uint32_t tmem;
+  int abort;
 };
 static_assert(sizeof(WideSmem) + 1024 <= 232448, "shared memory");
 
@@ -306,7 +305,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
   extern __shared__ unsigned char smem_raw[];
   WideSmem& sm = *reinterpret_cast<WideSmem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) ring_init<WideSmem, kWStages, kWBufs>(sm, kMc, kWSumWarps);
+  if (tid == 0) ring_init(sm, kWStages, kWBufs, kMc, kWSumWarps);
   if (warp == kWSumWarps) tc::tmem_alloc(&sm.tmem, kWBufs * kWN);
   tc::tc_fence_before();
   __syncthreads();
@@ -479,24 +478,33 @@ template <int kRows> constexpr int kTSumWarps = kRows > 16 ? 8 : 4;      // two 
 template <int kRows> constexpr int kTThreads = (kTSumWarps<kRows> + 2) * 32;
 template <int kRows> constexpr int kTOwn = kRows / (kTSumWarps<kRows> / 4);   // rows of A of a sum warp: 16, 16, 32, 64
 template <int kRows> constexpr int kTStageBytes = (kTN + kRows) * kBlock;
-template <int kRows> constexpr int kTStages = 200 * 1024 / kTStageBytes<kRows>;
+// CTAs that an SM can hold.  With more tiles than SMs two of them, with half the ring each, read at the same time, and
+// no second wave of tiles leaves SMs idle: 32 x 32,768 x 4,096 takes 25.1 us instead of 27.5.
+template <int kRows> constexpr int kTCtas = kRows <= 64 ? 2 : 1;
+constexpr int kTRingBytes = 200 * 1024, kTMaxStages = kTRingBytes / kTStageBytes<16>;
 template <int kRows>
-struct ThinSmem : Ring<kTStages<kRows>, kTStageBytes<kRows>, kTBufs> {
+struct ThinSmem {              // the ring's stages follow, 1024-aligned
+  uint64_t full[kTMaxStages], empty[kTMaxStages], acc_full[kTBufs], acc_empty[kTBufs];
   alignas(16) float scale[kTSumWarps<kRows>][2][kTOwn<kRows>];   // of a block, for all lanes of a warp
+  uint32_t tmem;
+  int abort;
 };
+template <int kRows> constexpr size_t kTSmemBytes(int stages) { return 1024 + (sizeof(ThinSmem<kRows>) + 1023) / 1024 * 1024 + (size_t)stages * kTStageBytes<kRows>; }
 
 template <int kRows>
-__global__ void __launch_bounds__(kTThreads<kRows>, 1)
+__global__ void __launch_bounds__(kTThreads<kRows>, kTCtas<kRows>)
 k_matmul_fp8_thin(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ MatmulPlan p,
-                  uint32_t* status) {
+                  int n_stages, uint32_t* status) {
   extern __shared__ unsigned char smem_raw[];
   using Smem = ThinSmem<kRows>;
-  constexpr int kStages = kTStages<kRows>, kBytes = kTStageBytes<kRows>, kSumWarps = kTSumWarps<kRows>, kOwn = kTOwn<kRows>;
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
+  constexpr int kBytes = kTStageBytes<kRows>, kSumWarps = kTSumWarps<kRows>, kOwn = kTOwn<kRows>;
+  unsigned char* base = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
+  Smem& sm = *reinterpret_cast<Smem*>(base);
+  unsigned char* ring = base + (sizeof(Smem) + 1023) / 1024 * 1024;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (p.partial) pdl_trigger();
   constexpr uint32_t kCols = kTBufs * kRows;        // 64 to 512 columns
-  if (tid == 0) ring_init<Smem, kStages, kTBufs>(sm, 1, kSumWarps);
+  if (tid == 0) ring_init(sm, n_stages, kTBufs, 1, kSumWarps);
   if (warp == kSumWarps) tc::tmem_alloc(&sm.tmem, kCols);
   tc::tc_fence_before();
   __syncthreads();
@@ -522,45 +530,58 @@ k_matmul_fp8_thin(const __grid_constant__ CUtensorMap amap, const __grid_constan
   if (warp == kSumWarps) {
     // ================= operand copies =================
     if (lane == 0) {
-      uint32_t n = 0;
+      int st = 0;
+      uint32_t round = 0;                 // uses of the stage before this one
       bool ok = true;
       for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
         const Item w = item(it);
-        for (int k = w.k0; k < w.k1; ++k, ++n) {
-          const uint32_t st = n % kStages, use = n / kStages;
-          if (use > 0 && !wait_bar(&sm.empty[st], (use - 1) & 1, abort)) {
+        for (int k = w.k0; k < w.k1; ++k) {
+          if (round > 0 && !wait_bar(&sm.empty[st], (round - 1) & 1, abort)) {
             ok = false;
             break;
           }
+          unsigned char* stage = ring + st * kBytes;
           tc::mbar_arrive_expect_tx(&sm.full[st], kBytes);
-          tma::load_2d(sm.stage[st], &bmap, k * kBlock, w.n0, &sm.full[st]);
-          tma::load_2d(sm.stage[st] + kTN * kBlock, &amap, k * kBlock, w.m0, &sm.full[st]);
+          tma::load_2d(stage, &bmap, k * kBlock, w.n0, &sm.full[st]);
+          tma::load_2d(stage + kTN * kBlock, &amap, k * kBlock, w.m0, &sm.full[st]);
+          if (++st == n_stages) {
+            st = 0;
+            ++round;
+          }
         }
       }
-      for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)   // every issued copy lands before exit
+      // every issued copy lands before exit: the last use of stage i is `round` where i < st, else the one before
+      for (int i = 0; i < n_stages; ++i) {
+        if (i >= st && round == 0) break;
         for (uint32_t w = 0; w < (1u << 22); ++w)
-          if (tc::mbar_try_wait(&sm.full[i % kStages], (i / kStages) & 1)) break;
+          if (tc::mbar_try_wait(&sm.full[i], (i < st ? round : round - 1) & 1)) break;
+      }
     }
     __syncwarp();
   } else if (warp == kSumWarps + 1) {
     // ================= MMA issue =================
     constexpr uint32_t idesc = idesc_fp8(kTN, kRows);
     const uint32_t leader = tc::elect_lane();
-    uint32_t n = 0;
+    uint32_t n = 0, phase = 0;
+    int st = 0;
     bool ok = true;
     for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
       const Item w = item(it);
       for (int k = w.k0; k < w.k1; ++k, ++n) {
-        const uint32_t st = n % kStages, buf = n % kTBufs, use = n / kTBufs;
-        ok = wait_lanes(tc::smem_addr(lane == 1 ? &sm.acc_empty[buf] : &sm.full[st]), lane == 1 ? (use - 1) & 1 : (n / kStages) & 1,
+        const uint32_t buf = n % kTBufs, use = n / kTBufs;
+        ok = wait_lanes(tc::smem_addr(lane == 1 ? &sm.acc_empty[buf] : &sm.full[st]), lane == 1 ? (use - 1) & 1 : phase,
                         use > 0 ? 3u : 1u, abort);
         if (!ok) break;
         tc::tc_fence_after();
-        const uint32_t sw = tc::smem_addr(sm.stage[st]), sx = sw + kTN * kBlock;
+        const uint32_t sw = tc::smem_addr(ring) + st * kBytes, sx = sw + kTN * kBlock;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_fp8(leader, tm + buf * kRows, desc128(sw + 32 * ks), desc128(sx + 32 * ks), idesc, ks > 0);
         tc::mma_commit_by(leader, &sm.empty[st]);
         tc::mma_commit_by(leader, &sm.acc_full[buf]);
+        if (++st == n_stages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
     }
     __syncwarp();
@@ -747,8 +768,10 @@ cudaError_t launch_wide(int64_t items, int sms, const CUtensorMap& am, const CUt
 
 template <int kRows>
 cudaError_t launch_thin(int64_t items, int sms, const CUtensorMap& am, const CUtensorMap& bm, const MatmulPlan& p, cudaStream_t s) {
-  static_assert(sizeof(ThinSmem<kRows>) + 1024 <= 232448, "shared memory");
-  return launch_matmul(k_matmul_fp8_thin<kRows>, sizeof(ThinSmem<kRows>) + 1024, kTThreads<kRows>, items, sms, 1, s, am, bm, p);
+  const int ctas = items > sms ? kTCtas<kRows> : 1, stages = kTRingBytes / ctas / kTStageBytes<kRows>;
+  static_assert(kTSmemBytes<kRows>(kTRingBytes / kTStageBytes<kRows>) <= 232448, "shared memory of a block");
+  static_assert(kTCtas<kRows> * (kTSmemBytes<kRows>(kTRingBytes / kTCtas<kRows> / kTStageBytes<kRows>) + 1024) <= 233472, "shared memory of an SM");
+  return launch_matmul(k_matmul_fp8_thin<kRows>, kTSmemBytes<kRows>(stages), kTThreads<kRows>, items, ctas * sms, 1, s, am, bm, p, stages);
 }
 
 }  // namespace
