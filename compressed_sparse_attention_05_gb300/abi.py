@@ -382,6 +382,8 @@ def _float_type(t: torch.Tensor) -> int:
 def csa2_pack_fp8_blocks(x, codes, scales, stream=None):
     """x [n][K] bf16 or fp32 (rows may be apart) -> codes [n][K] E4M3, scales fp32 [n][ceil(K/128)]."""
     n, K = x.shape
+    if codes.shape != x.shape:
+        raise ValueError(f"x and codes must have the same shape (got {tuple(x.shape)} and {tuple(codes.shape)})")
     address, strides = _strided(x)
     _check(lib().csa2_pack_fp8_blocks(address, _float_type(x), strides[0], n, K, ptr(codes), ptr(scales), stream_handle(stream)))
 
@@ -393,6 +395,8 @@ def csa2_matmul_fp8_workspace_size(M: int, N: int, K: int) -> int:
 def csa2_matmul_fp8(A, a_scales, Bw, b_scales, out, ws=None, stream=None):
     """out [M][N] (bf16 or fp32) = A [M][K] Bw [N][K]^T, E4M3 codes with the scales of csa2_pack_fp8_blocks."""
     (M, K), N = A.shape, Bw.shape[0]
+    if Bw.shape[1] != K or out.shape != (M, N):
+        raise ValueError(f"A {tuple(A.shape)}, Bw {tuple(Bw.shape)} and out {tuple(out.shape)} do not fit together")
     _check(lib().csa2_matmul_fp8(ptr(A), ptr(a_scales), ptr(Bw), ptr(b_scales), M, N, K, ptr(out), _float_type(out), ptr(ws),
                                  _nbytes(ws), stream_handle(stream)))
 

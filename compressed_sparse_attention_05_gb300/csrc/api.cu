@@ -780,7 +780,7 @@ int csa2_pack_fp8_blocks(const void* x, int32_t dtype, int64_t row_stride, int64
   g_err[0] = 0;
   REQUIRE(dtype == CSA2_BF16 || dtype == CSA2_F32, "dtype must be CSA2_BF16 or CSA2_F32");
   REQUIRE(n_rows >= 0 && n_rows < (1ll << 31), "n_rows must be in 0..2^31-1");
-  REQUIRE(K > 0 && K % 16 == 0, "K must be a positive multiple of 16 (got %d)", K);
+  REQUIRE(K > 0 && K % 16 == 0 && K <= (1 << 30), "K must be a positive multiple of 16 up to 2^30 (got %d)", K);
   const int64_t size = dtype == CSA2_F32 ? 4 : 2;
   REQUIRE(n_rows <= 1 || (row_stride >= K && row_stride * size % 16 == 0),
           "row_stride must be at least K and a multiple of 16 bytes (got %lld elements)", (long long)row_stride);

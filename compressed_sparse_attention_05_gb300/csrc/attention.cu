@@ -228,7 +228,7 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
           const int node = p - ctx < a.max_depth ? a.path[row * a.max_depth + (p - ctx)] : -1;
           if (node >= 0 && node < a.Tq) src = -2 - ((int64_t)a.swa_cap + node);
           else raise_status(status, CSA2_STATUS_BAD_INDEX);
-        } else if (!kTree || (p >= pos0 && p - pos0 < a.swa_cap)) {
+        } else if (!kTree || (p >= pos0 && (uint32_t)p - (uint32_t)pos0 < (uint32_t)a.swa_cap)) {
           src = -2 - (int64_t)(p - pos0);
         }
       }

@@ -303,7 +303,7 @@ __device__ __forceinline__ int32_t key_source(const AttnArgs& a, int64_t row, in
     }
     return (int32_t)(-2 - ((int64_t)a.B * a.swa_cap + (int64_t)b * a.Tq + node));
   }
-  if (kTree && (p < pos0 || p - pos0 >= a.swa_cap)) return -1;   // not held by the buffer
+  if (kTree && (p < pos0 || (uint32_t)p - (uint32_t)pos0 >= (uint32_t)a.swa_cap)) return -1;   // not held by the buffer
   return (int32_t)(-2 - ((int64_t)b * a.swa_cap + (p - pos0)));
 }
 

@@ -131,7 +131,7 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // Visible entries of the token at raw position t: j < min(n_entries, (t+1)/4).
 __device__ __forceinline__ int n_visible(int n_entries, int t) {
-  int v = (t + 1) >> 2;
+  int v = (int)(((uint32_t)t + 1u) >> 2);   // (unsigned: t may be the largest position)
   if (t < 0) v = 0;
   return v < n_entries ? v : n_entries;
 }

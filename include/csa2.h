@@ -450,8 +450,9 @@ typedef struct csa2_page_pool {
  * counts cannot be (n_free outside 0 .. n_pages, more released than it lacks)
  * makes every sequence wait.  A page id outside the pool is passed on, gets no slot
  * and raises CSA2_STATUS_BAD_PAGE.  After csa2_evict the pages behind the kept
- * entries come back with the next call (shift says so).  dims: B, Tq, max_pages are
- * used.  Needs csa2_page_plan_workspace_size() bytes of workspace, which calls that
+ * entries come back with the next call (shift says so).  A page belongs to one
+ * sequence or to the free list.  Counts and tables may be the ones that csa2_cache
+ * points to.  dims: B, Tq, max_pages are used.  Needs csa2_page_plan_workspace_size() bytes of workspace, which calls that
  * can overlap must not share. */
 size_t csa2_page_plan_workspace_size(const csa2_dims* dims);
 int csa2_page_plan(const csa2_dims* dims, const csa2_page_pool* pool, const int32_t* seq_len,

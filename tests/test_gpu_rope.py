@@ -181,6 +181,31 @@ def test_captured():
         assert torch.equal(y, z)
 
 
+def test_a_head_for_many_tokens():
+    """A stride of zero in x: one head's channels rotated for every token."""
+    x = torch.randn(1, 4, 64, generator=torch.Generator().manual_seed(5)).cuda()
+    pos = torch.arange(300, dtype=torch.int32).cuda()
+    y = torch.empty(300, 4, 64, device="cuda")
+    abi.csa2_rope(x.expand(300, 4, 64), y, pos, table_of(64))
+    z = torch.empty_like(y)
+    abi.csa2_rope(x.expand(300, 4, 64).contiguous(), z, pos, table_of(64))
+    torch.cuda.synchronize()
+    assert torch.equal(y, z)
+
+
+def test_past_4_gb():
+    """Rows of x and y whose offsets pass 2^32 bytes."""
+    n, h, d = 70000, 64, 512
+    x = torch.empty(n, h, d, dtype=torch.bfloat16, device="cuda")
+    x.copy_((torch.arange(n, device="cuda") % 251).view(n, 1, 1).expand(n, h, d))
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+    y = torch.zeros_like(x)
+    abi.csa2_rope(x, y, pos, table_of(64), start=448, layout=abi.ROPE_INTERLEAVED)
+    torch.cuda.synchronize()
+    for i in (0, 1, 65535, 65536, 69999):
+        assert torch.equal(x[i], y[i])
+
+
 def test_no_tokens():
     x = torch.empty(0, 4, 64, device="cuda")
     abi.csa2_rope(x, x, torch.empty(0, dtype=torch.int32, device="cuda"), table_of(64))

@@ -228,6 +228,31 @@ def test_attention_d64(kw):
     c.check()
 
 
+@pytest.mark.parametrize("d", [512, 64])
+def test_the_last_positions(d):
+    """Trees that end at position 2^31 - 1, the buffer's rows in front of them."""
+    c = Case(19, lens=[50, 70], T=5, K=20, W=30, d=d, chain=True)
+    c.ctx = np.array([2 ** 31 - 5, 2 ** 31 - 40])
+    c.pos0 = c.ctx - c.cap
+    c.upload()
+    c.run()
+    assert status() == 0
+    c.check()
+
+
+def test_two_streams_at_once():
+    cs = [Case(20 + k, lens=[300 + k, 40], T=6, K=64).upload() for k in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(3):
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                c.run()
+    assert status() == 0
+    for c in cs:
+        c.check()
+
+
 def test_many_tokens():
     """More tokens than SMs: one CTA per token."""
     c = Case(11, lens=[1000 + 37 * b for b in range(24)], T=8, K=512).upload()

@@ -178,5 +178,13 @@ def test_binding_refuses_tensors_it_cannot_describe():
     with pytest.raises(ValueError, match="CUDA"):
         abi.csa2_pack_fp8_blocks(torch.zeros(4, 64), torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 1))
     assert abi._float_type(x) == abi.CSA2_F32
+    with pytest.raises(ValueError, match="same shape"):
+        abi.csa2_rope(x, x[:3], torch.zeros(4, dtype=torch.int32), torch.zeros(32, dtype=torch.int64))
+    with pytest.raises(ValueError, match="same shape"):
+        abi.csa2_pack_fp8_blocks(torch.zeros(4, 64), torch.zeros(4, 80, dtype=torch.uint8), torch.zeros(4, 1))
+    u8 = lambda *n: torch.zeros(*n, dtype=torch.uint8)  # noqa: E731
+    for b, c in ((u8(5, 48), torch.zeros(4, 5)), (u8(5, 32), torch.zeros(5, 4)), (u8(5, 32), torch.zeros(20))):
+        with pytest.raises(ValueError, match="fit together"):
+            abi.csa2_matmul_fp8(u8(4, 32), torch.zeros(4, 1), b, torch.zeros(1, 1), c)
     with pytest.raises(ValueError, match="bfloat16"):
         abi._float_type(x.half())
