@@ -263,39 +263,39 @@ struct WideSmem {
 };
 static_assert(sizeof(WideSmem) + 1024 <= 232448, "shared memory");
 
-// 32 rows x 128 bytes of C (lane = row, piece j of 16 bytes: get(j)) through the warp's staging rows.  Written by the
-// threads themselves, 16 bytes of 32 rows at a time, C took 75 of 520 us of a product of 4,096 x 32,768 x 4,096.
-template <typename Get>
-__device__ __forceinline__ void store_box(unsigned char* stage, const CUtensorMap* map, int x, int y, bool in, int lane, Get get) {
+// 32 rows x 128 bytes of C (lane = row, piece j of 16 bytes: get(j)) from row y, column x on, through the warp's staging
+// rows: by a tensor-map copy where C's rows start on 16 bytes, else row by row with a lane to an element.  (Written by the
+// threads themselves, each along its own row, C took 75 of 520 us of a product of 4,096 x 32,768 x 4,096 with 16 bytes
+// at a time, and 119 us for 351 x 27,102 element by element.)
+template <typename T, typename Get>
+__device__ __forceinline__ void store_box(unsigned char* stage, const CUtensorMap* map, const MatmulPlan& p, int x, int y, int lane, Get get) {
+  constexpr int kCols = 128 / (int)sizeof(T);
   if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the box before has left
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = get(j);   // 128-byte swizzle
-  tc::fence_async_smem();
+  if (p.c_map) {
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0 && y < p.M && x < p.N)     // (the copy leaves out what lies outside of C)
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\tcp.async.bulk.commit_group;" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(x), "r"(y), "r"(tc::smem_addr(stage))
+                   : "memory");
+    return;
+  }
   __syncwarp();
-  if (lane == 0 && in)
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\tcp.async.bulk.commit_group;" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(tc::smem_addr(stage))
-                 : "memory");
-}
-
-
-// A thread's 128 columns of a row of C whose rows do not start on 16 bytes.
-__device__ __forceinline__ void store_row(float* out, const float2 (&acc)[64], int n_left) {
+  T* out = static_cast<T*>(p.C) + (int64_t)y * p.N + x;
+  const int rows = min(32, p.M - y), cols = min(kCols, p.N - x);
+#pragma unroll 2
+  for (int r = 0; r < rows; ++r)
 #pragma unroll
-  for (int j = 0; j < 64; ++j) {
-    if (2 * j < n_left) out[2 * j] = acc[j].x;
-    if (2 * j + 1 < n_left) out[2 * j + 1] = acc[j].y;
-  }
-}
-__device__ __forceinline__ void store_row(uint16_t* out, const float2 (&acc)[64], int n_left) {
-#pragma unroll
-  for (int j = 0; j < 64; ++j) {
-    const uint32_t v = f32x2_bf16x2(acc[j].x, acc[j].y);
-    if (2 * j < n_left) out[2 * j] = (uint16_t)(v & 0xFFFFu);
-    if (2 * j + 1 < n_left) out[2 * j + 1] = (uint16_t)(v >> 16);
-  }
+    for (int c = lane; c < kCols; c += 32)
+      if (c < cols) {
+        const int at = c * (int)sizeof(T);
+        out[(int64_t)r * p.N + c] = *reinterpret_cast<const T*>(stage + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
+      }
+  __syncwarp();
 }
 
 // The CTAs of a cluster take tiles above one another and share the rows of B: each copies its part of them to all.
@@ -434,32 +434,23 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
         block(i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w);
       }
       if (!ok) break;
-      if (p.c_map) {       // (copies leave out what lies outside of C)
-        const int y = w.m0 + 32 * lq;
-        unsigned char* stage = sm.out[warp];
-        if (p.f32) {
+      const int y = w.m0 + 32 * lq;
+      unsigned char* stage = sm.out[warp];
+      if (p.f32) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            store_box(stage, &cmap, n0 + 32 * b, y, y < p.M && n0 + 32 * b < p.N, lane, [&](int j) {
-              const float2 u = acc[16 * b + 2 * j], v = acc[16 * b + 2 * j + 1];
-              return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y));
-            });
-        } else {
+        for (int b = 0; b < 4; ++b)
+          store_box<float>(stage, &cmap, p, n0 + 32 * b, y, lane, [&](int j) {
+            const float2 u = acc[16 * b + 2 * j], v = acc[16 * b + 2 * j + 1];
+            return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y));
+          });
+      } else {
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-            store_box(stage, &cmap, n0 + 64 * b, y, y < p.M && n0 + 64 * b < p.N, lane, [&](int j) {
-              const float2* u = acc + 32 * b + 4 * j;
-              return make_uint4(f32x2_bf16x2(u[0].x, u[0].y), f32x2_bf16x2(u[1].x, u[1].y), f32x2_bf16x2(u[2].x, u[2].y), f32x2_bf16x2(u[3].x, u[3].y));
-            });
-        }
-        continue;
+        for (int b = 0; b < 2; ++b)
+          store_box<uint16_t>(stage, &cmap, p, n0 + 64 * b, y, lane, [&](int j) {
+            const float2* u = acc + 32 * b + 4 * j;
+            return make_uint4(f32x2_bf16x2(u[0].x, u[0].y), f32x2_bf16x2(u[1].x, u[1].y), f32x2_bf16x2(u[2].x, u[2].y), f32x2_bf16x2(u[3].x, u[3].y));
+          });
       }
-      if (!live) continue;
-      const int left = p.N - n0;
-      if (p.f32)
-        store_row(static_cast<float*>(p.C) + (int64_t)m * p.N + n0, acc, left);
-      else
-        store_row(static_cast<uint16_t*>(p.C) + (int64_t)m * p.N + n0, acc, left);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
