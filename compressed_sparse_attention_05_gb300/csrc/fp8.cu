@@ -250,10 +250,10 @@ constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2, kMc = 2;   // kMc:
 constexpr int kWStageBytes = (kWM + kWN) * kBlock;       // 48 KB
 constexpr int kWSumWarps = 8;
 constexpr int kWThreads = kWSumWarps * 32 + 128;
-// Registers: 2 x 224 + 56 = 3 x 168.  (Where a split makes the compiler spill in one role's loop, the kernel takes up
+// Registers: 2 x 216 + 72 = 3 x 168.  (Where a split makes the compiler spill in one role's loop, the kernel takes up
 // to twice as long; this one does not.)
 constexpr int kWRegs = 168;
-constexpr int kWRegsSum = 224, kWRegsMisc = 56;
+constexpr int kWRegsSum = 216, kWRegsMisc = 72;
 struct WideSmem {
   unsigned char stage[kWStages][kWStageBytes];   // 1024-aligned
   unsigned char out[kWSumWarps][4096];           // of each sum warp: 32 rows x 128 bytes of C on their way out
@@ -387,10 +387,8 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
     bool ok = true;
     for (int it = it0; ok && it < items; it += stride) {
       const Item w = item(it);
-      const int m = w.m0 + 32 * lq + lane, n0 = w.n0 + 128 * half;
-      const bool live = m < p.M && n0 < p.N;
-      const float* sa = p.sa + (int64_t)(live ? m : 0) * p.kb;
-      const float* sb = p.sb + (int64_t)(live ? n0 / kBlock : 0) * p.kb;
+      const int y = w.m0 + 32 * lq, n0 = w.n0 + 128 * half;
+      const int m = y + lane < p.M ? y + lane : 0, nb = n0 < p.N ? n0 / kBlock : 0;   // rows of the scales
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
@@ -422,19 +420,19 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
       for (int k = 0; ok && k < p.kb; ++k) {
         const int i = k & 3;
         if (i == 0) {
-          const int q = k & ~3;
+          const float* sa = p.sa + (int64_t)m * p.kb + k;
+          const float* sb = p.sb + (int64_t)nb * p.kb + k;
           if (vec) {
-            const float4 fa = __ldg(reinterpret_cast<const float4*>(sa + q)), fb = __ldg(reinterpret_cast<const float4*>(sb + q));
+            const float4 fa = __ldg(reinterpret_cast<const float4*>(sa)), fb = __ldg(reinterpret_cast<const float4*>(sb));
             sc = make_float4(fa.x * fb.x, fa.y * fb.y, fa.z * fb.z, fa.w * fb.w);
           } else {
-            auto at = [&](int j) { return q + j < p.kb ? __ldg(sa + q + j) * __ldg(sb + q + j) : 0.f; };
+            auto at = [&](int j) { return k + j < p.kb ? __ldg(sa + j) * __ldg(sb + j) : 0.f; };
             sc = make_float4(at(0), at(1), at(2), at(3));
           }
         }
         block(i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w);
       }
       if (!ok) break;
-      const int y = w.m0 + 32 * lq;
       unsigned char* stage = sm.out[warp];
       if (p.f32) {
 #pragma unroll
