@@ -847,7 +847,7 @@ int csa2_rope_table(const csa2_rope_spec* spec, int32_t r, uint64_t* table, void
     lo = std::max(0., floor(pair_of(spec->beta_fast)));
     hi = std::min(r - 1., ceil(pair_of(spec->beta_slow)));
   }
-  RopeTable t = {};
+  uint64_t turns[kRopeMaxPairs];          // per position, 0.64 fixed point
   for (int i = 0; i < r / 2; ++i) {
     double theta = pow(base, -2. * i / r);
     if (kind == CSA2_ROPE_LINEAR) theta /= f;
@@ -855,9 +855,9 @@ int csa2_rope_table(const csa2_rope_spec* spec, int32_t r, uint64_t* table, void
       const double ramp = std::min(1., std::max(0., (i - lo) / std::max(hi - lo, 0.001)));
       theta = theta / f * ramp + theta * (1. - ramp);
     }
-    t.g[i] = (uint64_t)ldexp(theta / (2. * pi), 64);   // theta <= 1: below 2^62
+    turns[i] = (uint64_t)ldexp(theta / (2. * pi), 64);   // theta <= 1: below 2^62
   }
-  LAUNCH(launch_rope_table(t, r / 2, table, static_cast<cudaStream_t>(stream)), "rope_table");
+  LAUNCH(launch_rope_table(turns, r / 2, table, static_cast<cudaStream_t>(stream)), "rope_table");
   return CSA2_OK;
 }
 

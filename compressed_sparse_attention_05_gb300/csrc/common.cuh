@@ -129,6 +129,21 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// n / d and n % d for n < 2^31 by a multiplication (d >= 1): m = ceil(2^(31 + l) / d), l = ceil(log2 d), is below
+// 2^32 and its excess over 2^(31 + l) / d below 2^l / 2^(31 + l), so that floor(n m / 2^(31 + l)) is exact there.
+struct Divisor {
+  uint32_t d, m, shift;
+  static Divisor of(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return {d, (uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+  }
+  __device__ __forceinline__ void split(uint32_t n, uint32_t* q, uint32_t* r) const {
+    *q = (uint32_t)(((uint64_t)n * m) >> shift);
+    *r = n - *q * d;
+  }
+};
+
 // Visible entries of the token at raw position t: j < min(n_entries, (t+1)/4).
 __device__ __forceinline__ int n_visible(int n_entries, int t) {
   int v = (int)(((uint32_t)t + 1u) >> 2);   // (unsigned: t may be the largest position)

@@ -36,10 +36,11 @@ constexpr int kBlock = 128;                // columns that share a scale (and ro
 
 // ---- packing --------------------------------------------------------------------------------------
 // amax of a block's 128 values, a = max(amax, 2^-100); scale a / 448, codes E4M3_rne_satfinite(x * (448 / a)).
-// Bytes bound it, and instructions not far behind (a block of fp32 leaves 108 issue slots per SM): a warp takes two
-// blocks that lie behind one another, both loads in flight (4 columns a lane), one reduction instruction a block, and
-// their divisions at once, in a lane each.  16,411 x 4,240 of fp32 in a wider tensor: 55 us, 6.4 TB/s.  (Four blocks a
-// warp and fewer warps 58, eight 74: many small blocks of threads load and store at different times.)
+// Bytes bound it, and instructions not far behind (a block of bf16 leaves 66 issue slots per SM): a lane loads 16 bytes,
+// so a block is 16 lanes of bf16 or 32 of fp32, and 2, 4 .. lanes where rows are shorter than half a block; every group
+// of lanes takes two blocks, both loads in flight, and divides for both at once, in an even and an odd lane.
+// 16,411 x 4,240 of fp32 in a wider tensor: 53 us, 6.6 TB/s.  460,166 x 96 of bf16: 26.5 us (a warp a block, 8-byte
+// loads: 44); 2,368,205 x 16 of fp32: 33 us (204).
 constexpr int kPackThreads = 256, kPackMany = 2;
 constexpr float kFloor = 0x1p-100f;
 
@@ -50,71 +51,92 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
       : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
+// The larger of each half (bf16); a NaN only where both are.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
-// many: blocks of a warp (at most kPackMany).
-template <bool kF32>
-__global__ void __launch_bounds__(kPackThreads, 8) k_pack_fp8_blocks(const void* x, int64_t stride, int K, int kb_n, int64_t blocks, int many,
-                                                                  uint8_t* __restrict__ codes, float* __restrict__ scales) {
+// kLanes = 2^lanes_log: lanes of a block; kLanes 0: fewer than a whole block has, at least 2.  many: blocks of a group of lanes (at most
+// kPackMany).
+template <bool kF32, int kLanes>
+__global__ void __launch_bounds__(kPackThreads, 8) k_pack_fp8_blocks(const void* x, int64_t stride, int K, Divisor per_row, uint32_t blocks,
+                                                                     int many, int lanes_log, uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int kCols = kF32 ? 4 : 8;               // of a lane: 16 bytes
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t b0 = ((int64_t)blockIdx.x * (kPackThreads / 32) + (threadIdx.x >> 5)) * many;
+  const int lane = threadIdx.x & 31, n_lanes = kLanes ? kLanes : 1 << lanes_log, groups = 32 >> lanes_log;
+  const uint32_t b0 = (blockIdx.x * (kPackThreads / 32) + (threadIdx.x >> 5)) * (uint32_t)(many * groups);
   if (b0 >= blocks) return;
-  const int n = (int)min((int64_t)many, blocks - b0);
-  const int64_t row0 = b0 / kb_n;
-  const int kb0 = (int)(b0 - row0 * kb_n);
-  uint4 v[kPackMany];            // (bf16: two words)
-  int64_t row = row0;
-  int kb = kb0;
+  const int col0 = (lane & (n_lanes - 1)) * kCols;
+  uint32_t b[kPackMany];
+  int64_t at[kPackMany];                            // in codes; -1: nothing
+  uint4 v[kPackMany];
 #pragma unroll
   for (int i = 0; i < kPackMany; ++i) {
+    b[i] = b0 + i * groups + (kLanes == 32 ? 0 : lane >> lanes_log);
     v[i] = make_uint4(0, 0, 0, 0);
-    const int col = kb * kBlock + lane * 4;
-    if (i < n && col < K) {
-      if (kF32) {
-        v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(x) + row * stride + col));
+    at[i] = -1;
+    if (i >= many || b[i] >= blocks) {
+      b[i] = blocks;
+      continue;
+    }
+    uint32_t row, kb;
+    per_row.split(b[i], &row, &kb);
+    const int col = (int)kb * kBlock + col0;
+    if (col >= K) continue;
+    const int64_t from = row * stride + col;
+    v[i] = __ldg(reinterpret_cast<const uint4*>(kF32 ? static_cast<const void*>(static_cast<const float*>(x) + from)
+                                                     : static_cast<const void*>(static_cast<const uint16_t*>(x) + from)));
+    at[i] = (int64_t)row * K + col;
+  }
+  // The blocks' largest magnitudes, in every lane of the group.  (The maxima drop a NaN.)
+  float amax[kPackMany];
+  if (kF32) {
+#pragma unroll
+    for (int i = 0; i < kPackMany; ++i) {
+      const float m = fmaxf(fmaxf(fmaxf(0.f, fabsf(__uint_as_float(v[i].x))), fabsf(__uint_as_float(v[i].y))),
+                            fmaxf(fmaxf(0.f, fabsf(__uint_as_float(v[i].z))), fabsf(__uint_as_float(v[i].w))));
+      uint32_t w = __float_as_uint(m);              // (orders like the values)
+      if (kLanes == 32) {
+        w = __reduce_max_sync(0xffffffffu, w);
       } else {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + row * stride + col));
-        v[i].x = w.x;
-        v[i].y = w.y;
+#pragma unroll 1
+        for (int o = n_lanes / 2; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
       }
+      amax[i] = __uint_as_float(w);
     }
-    if (++kb == kb_n) {
-      kb = 0;
-      ++row;
-    }
+  } else {
+    uint32_t m[kPackMany];
+#pragma unroll
+    for (int i = 0; i < kPackMany; ++i)
+      m[i] = max_bf16x2(max_bf16x2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu), max_bf16x2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+    static_assert(kPackMany == 2, "a half-word for each");
+    uint32_t w = max_bf16x2(prmt(m[0], m[1], 0x5410), prmt(m[0], m[1], 0x7632));
+#pragma unroll
+    for (int o = kLanes ? kLanes / 2 : 8; o > 0; o >>= 1)
+      if (kLanes || o < n_lanes) w = max_bf16x2(w, __shfl_xor_sync(0xffffffffu, w, o));
+    amax[0] = __uint_as_float(w << 16);
+    amax[1] = __uint_as_float(w & 0xFFFF0000u);
   }
-  auto values = [&](int i, float (&f)[4]) {
-    f[0] = __uint_as_float(kF32 ? v[i].x : v[i].x << 16);
-    f[1] = __uint_as_float(kF32 ? v[i].y : v[i].x & 0xFFFF0000u);
-    f[2] = __uint_as_float(kF32 ? v[i].z : v[i].y << 16);
-    f[3] = __uint_as_float(kF32 ? v[i].w : v[i].y & 0xFFFF0000u);
-  };
-  float amax = 0.f;              // of block `lane`
+  // The divisions: an even lane block 0's, an odd lane block 1's.
+  const int mine = lane & 1;
+  const float a = fmaxf(mine ? amax[1] : amax[0], kFloor), inv = 448.f / a;
+  const uint32_t b_mine = mine ? b[1] : b[0];
+  if ((lane & (n_lanes - 1)) < kPackMany && b_mine < blocks) scales[b_mine] = a / 448.f;
 #pragma unroll
   for (int i = 0; i < kPackMany; ++i) {
-    float f[4];
-    values(i, f);
-    // (fmaxf drops a NaN; the bits of what is left order like the values)
-    const float m = fmaxf(fmaxf(fmaxf(0.f, fabsf(f[0])), fabsf(f[1])), fmaxf(fmaxf(0.f, fabsf(f[2])), fabsf(f[3])));
-    const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-    if (lane == i) amax = all;
-  }
-  const float a = fmaxf(amax, kFloor), inv = 448.f / a;
-  if (lane < n) scales[b0 + lane] = a / 448.f;
-  row = row0;
-  kb = kb0;
-#pragma unroll
-  for (int i = 0; i < kPackMany; ++i) {
-    float f[4];
-    values(i, f);
-    const float q = __shfl_sync(0xffffffffu, inv, i);
-    const int col = kb * kBlock + lane * 4;
-    if (i < n && col < K)
-      *reinterpret_cast<uint32_t*>(codes + row * K + col) = e4m3x4(f[0] * q, f[1] * q, f[2] * q, f[3] * q);
-    if (++kb == kb_n) {
-      kb = 0;
-      ++row;
+    const float q = __shfl_sync(0xffffffffu, inv, (lane & ~1) | i);
+    if (at[i] < 0) continue;
+    if (kF32) {
+      *reinterpret_cast<uint32_t*>(codes + at[i]) = e4m3x4(__uint_as_float(v[i].x) * q, __uint_as_float(v[i].y) * q, __uint_as_float(v[i].z) * q,
+                                                           __uint_as_float(v[i].w) * q);
+    } else {
+      auto lo = [&](uint32_t w) { return __uint_as_float(w << 16) * q; };
+      auto hi = [&](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u) * q; };
+      *reinterpret_cast<uint2*>(codes + at[i]) =
+          make_uint2(e4m3x4(lo(v[i].x), hi(v[i].x), lo(v[i].y), hi(v[i].y)), e4m3x4(lo(v[i].z), hi(v[i].z), lo(v[i].w), hi(v[i].w)));
     }
   }
 }
@@ -766,14 +788,20 @@ cudaError_t launch_thin(int64_t items, int sms, const CUtensorMap& am, const CUt
 }  // namespace
 
 cudaError_t launch_pack_fp8_blocks(const void* x, int dtype, int64_t stride, int64_t rows, int K, uint8_t* codes, float* scales, cudaStream_t s) {
-  const int kb = (K + kBlock - 1) / kBlock;
+  const bool f32 = dtype == CSA2_F32;
+  const int kb = (K + kBlock - 1) / kBlock, whole = f32 ? 32 : 16;
   const int64_t blocks = rows * kb;
-  // one block a warp where there are not enough of them for two blocks of threads on every SM
-  const int many = (int)std::max<int64_t>(1, std::min<int64_t>(kPackMany, blocks / (152 * 2 * (kPackThreads / 32))));
-  const int64_t per = (int64_t)many * (kPackThreads / 32), grid = (blocks + per - 1) / per;
-  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  return launch_step(dtype == CSA2_F32 ? k_pack_fp8_blocks<true> : k_pack_fp8_blocks<false>, dim3((unsigned)grid), dim3(kPackThreads), 0, s, x, stride,
-                     K, kb, blocks, many, codes, scales);
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  int lanes_log = f32 ? 5 : 4;                       // short rows leave no lane without work
+  while (K <= kBlock / 2 && (kBlock / whole << (lanes_log - 1)) >= K) --lanes_log;
+  const int groups = 32 >> lanes_log;
+  // one block a group of lanes where there are not enough of them for two blocks of threads on every SM
+  const int many = (int)std::max<int64_t>(1, std::min<int64_t>(kPackMany, blocks / (152 * 2 * (kPackThreads / 32) * groups)));
+  const int64_t per = (int64_t)many * groups * (kPackThreads / 32), grid = (blocks + per - 1) / per;
+  const auto kernel = f32 ? (K > kBlock / 2 ? k_pack_fp8_blocks<true, 32> : k_pack_fp8_blocks<true, 0>)
+                          : (K > kBlock / 2 ? k_pack_fp8_blocks<false, 16> : k_pack_fp8_blocks<false, 0>);
+  return launch_step(kernel, dim3((unsigned)grid), dim3(kPackThreads), 0, s, x, stride, K, Divisor::of(kb), (uint32_t)blocks, many, lanes_log, codes,
+                     scales);
 }
 
 size_t matmul_fp8_workspace_bytes(int M, int N, int K) {

@@ -315,11 +315,8 @@ cudaError_t launch_tree_plan(int B, int Tq, int max_depth, const int32_t* parent
                              int32_t* path, cudaStream_t s);
 
 // ---- rope.cu -----------------------------------------------------------------------
-constexpr int kRopeMaxPairs = 256;
-struct RopeTable {
-  uint64_t g[kRopeMaxPairs];  // turns per position, 0.64 fixed point
-};
-cudaError_t launch_rope_table(const RopeTable& t, int pairs, uint64_t* out, cudaStream_t s);
+constexpr int kRopeMaxPairs = 1024;
+cudaError_t launch_rope_table(const uint64_t* turns, int pairs, uint64_t* out, cudaStream_t s);   // (turns: of the host)
 struct RopeArgs {
   const void* x;
   void* y;

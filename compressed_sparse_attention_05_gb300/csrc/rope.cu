@@ -7,9 +7,13 @@
 // rest in integers before it becomes fp32: the rest is below 1/8 of a turn, so its rounding is at most 2^-27
 // turns and sinpi / cospi of it lose nothing to a large argument.
 //
-// Bound: bytes.  A block takes a few tokens: its threads compute the tokens' sines and cosines into shared memory
-// once for all heads while the copied channels are on their way, then rotate 8 channels (two halves of 8) at a time
-// with 16-byte loads and stores.  Shapes that 8 channels at a time do not divide go channel pair by channel pair.
+// Bound: bytes.  A block takes about 2,048 units of work of 16-byte loads (8 channels; two halves of 8) that lie behind
+// one another, over tokens and heads: its threads compute their tokens' sines and cosines into shared memory once for
+// all heads, then rotate and copy with 2 or 4 units' loads in flight each.  4,096 tokens x 64 heads x 512 channels, 64
+// rotated, bf16: 85 us, 6.3 TB/s (whole heads a block: 90; 79 at the rate of a copy).  With one head there is nothing to
+// share a rotation with: 109,307 x 512 takes 47 us (4.7 TB/s), 338,137 x 64 with 32 rotated 35 (2.4).
+// Half pairs that 8 channels do not divide, odd starts and unaligned rows go pair by pair (445 x 40 x 512, 62 rotated,
+// half: 11 us, at 3.3 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -23,25 +27,13 @@ constexpr int kThreads = 256;
 constexpr int kMaxAngles = 2048;    // (token, pair) angles of a block in shared memory
 constexpr int kUnit = 8;            // channels of a load
 
-// n / d and n % d for n < 2^31 by a multiplication (d >= 1): m = ceil(2^(31 + l) / d), l = ceil(log2 d), is below
-// 2^32 and its excess over 2^(31 + l) / d below 2^l / 2^(31 + l), so that floor(n m / 2^(31 + l)) is exact there.
-struct Divisor {
-  uint32_t d, m, shift;
-  static Divisor of(uint32_t d) {
-    uint32_t l = 0;
-    while ((1ull << l) < d) ++l;
-    return {d, (uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
-  }
-  __device__ __forceinline__ void split(uint32_t n, uint32_t* q, uint32_t* r) const {
-    *q = (uint32_t)(((uint64_t)n * m) >> shift);
-    *r = n - *q * d;
-  }
-};
-
+// The units of work in a row, token after token, head after head; a block takes `span` of them.
 struct RopePlan {
   RopeArgs a;
-  int tokens, heads;                // of a block
-  Divisor units, head_div;          // work units of a head, heads of a block
+  int64_t total;                    // units of all tokens
+  int span, tokens;                 // of a block: units, tokens that they can touch
+  int far;                          // total >= 2^31
+  Divisor per_token, units;         // units of a token, of a head
 };
 
 // cos and sin of p turns-per-position g, times the amplitude.
@@ -92,6 +84,19 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = (uint16_t)(f32x2_bf16x2(x, 0.f) & 0xFFFFu); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 
+// A block's first token and the units of it that lie before the block's.
+__device__ __forceinline__ void first_unit(const RopePlan& pl, int64_t* t0, uint32_t* before) {
+  const int64_t u = (int64_t)blockIdx.x * pl.span;
+  if (pl.far) {
+    *t0 = u / pl.per_token.d;
+    *before = (uint32_t)(u - *t0 * pl.per_token.d);
+  } else {
+    uint32_t t;
+    pl.per_token.split((uint32_t)u, &t, before);
+    *t0 = t;
+  }
+}
+
 // The block's tokens' rotations into shared memory: cs[token][pair].
 __device__ __forceinline__ void rotations(const RopeArgs& a, int64_t t0, int tokens, float2* cs) {
   const int pairs = a.r / 2;
@@ -102,20 +107,31 @@ __device__ __forceinline__ void rotations(const RopeArgs& a, int64_t t0, int tok
 }
 
 // 8 channels at a time.  Units of a head: with half pairs r / 16 pairs of 8 + 8 channels, with interleaved ones
-// r / 8 of 8; then, unless y is x, (d - r) / 8 copied ones.
-template <typename In, typename Out, bool kHalf>
+// r / 8 of 8; then, unless y is x, (d - r) / 8 copied ones.  kRagged: interleaved pairs from any even channel on, so
+// that the rotated units' first and last may have pairs that are copied.
+enum Mode { kInterleaved, kHalves, kRagged, kOnes, kOnesWhole };
+// 8-channel loads of a head that have a rotated channel.
+__host__ __device__ inline int touched_units(const RopeArgs& a) { return a.r ? (a.start + a.r + kUnit - 1) / kUnit - a.start / kUnit : 0; }
+__host__ __device__ inline int rotated_units(const RopeArgs& a, Mode mode) {
+  return mode == kHalves ? a.r / 16 : mode == kInterleaved ? a.r / 8 : touched_units(a);
+}
+
+template <typename In, typename Out, Mode kMode>
 __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
   __shared__ float2 cs[kMaxAngles];
+  constexpr bool kHalf = kMode == kHalves;
   const RopeArgs& a = pl.a;
   pdl_wait();
-  const int64_t t0 = (int64_t)blockIdx.x * pl.tokens;
-  const int h0 = blockIdx.y * pl.heads;
+  int64_t t0;
+  uint32_t before;
+  first_unit(pl, &t0, &before);
   rotations(a, t0, pl.tokens, cs);
   __syncthreads();
   const In* x = static_cast<const In*>(a.x);
   Out* y = static_cast<Out*>(a.y);
-  const int rot = kHalf ? a.r / 16 : a.r / 8;      // rotated units of a head come first
-  const int total = pl.tokens * pl.heads * (int)pl.units.d;
+  const int rot = rotated_units(a, kMode);         // of a head; they come first
+  const int first = kMode == kRagged ? a.start & ~(kUnit - 1) : a.start, width = kMode == kRagged ? rot * kUnit : a.r;
+  const int total = (int)min((int64_t)pl.span, pl.total - (int64_t)blockIdx.x * pl.span);
   constexpr int kMany = sizeof(In) == 4 ? 2 : 4;   // units in flight
   for (int u0 = threadIdx.x; u0 < total; u0 += kMany * kThreads) {
     Eight<In> v[kMany], w[kMany];
@@ -127,23 +143,22 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
       at[k] = -2;
       to[k] = 0;
       if (u >= (uint32_t)total) continue;
-      uint32_t th, unit, t, h;
-      pl.units.split(u, &th, &unit);
-      pl.head_div.split(th, &t, &h);
-      if (t0 + t >= a.rows || h0 + (int)h >= a.heads) continue;
+      uint32_t t, h, unit;
+      pl.per_token.split(before + u, &t, &unit);
+      pl.units.split(unit, &h, &unit);
       int c;
       if ((int)unit < rot) {
-        c = a.start + unit * kUnit;
-        at[k] = t * (a.r / 2) + unit * (kHalf ? kUnit : kUnit / 2);
+        c = first + unit * kUnit;
+        at[k] = kMode == kRagged ? (int)(t << 16 | unit) : t * (a.r / 2) + unit * (kHalf ? kUnit : kUnit / 2);
       } else {
         c = (unit - rot) * kUnit;
-        if (c >= a.start) c += a.r;
+        if (c >= first) c += width;
         at[k] = -1;
       }
-      const In* p = x + (t0 + t) * a.x_token + (int64_t)(h0 + h) * a.x_head + c;
+      const In* p = x + (t0 + t) * a.x_token + (int64_t)h * a.x_head + c;
       v[k].load(p);
       if (kHalf && at[k] >= 0) w[k].load(p + a.r / 2);
-      to[k] = (t0 + t) * a.y_token + (int64_t)(h0 + h) * a.y_head + c;
+      to[k] = (t0 + t) * a.y_token + (int64_t)h * a.y_head + c;
     }
 #pragma unroll
     for (int k = 0; k < kMany; ++k) {
@@ -163,9 +178,11 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
           }
           store8(y + to[k] + a.r / 2, g);
         } else {
+          const int t = at[k] >> 16, i0 = kMode == kRagged ? (first - a.start) / 2 + (at[k] & 0xFFFF) * (kUnit / 2) : 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 q = cs[at[k] + j];
+            if (kMode == kRagged && (uint32_t)(i0 + j) >= (uint32_t)a.r / 2) continue;
+            const float2 q = kMode == kRagged ? cs[t * (a.r / 2) + i0 + j] : cs[at[k] + j];
             const float f1 = f[2 * j] * q.x - f[2 * j + 1] * q.y;
             f[2 * j + 1] = f[2 * j] * q.y + f[2 * j + 1] * q.x;
             f[2 * j] = f1;
@@ -177,87 +194,157 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
   }
 }
 
-// Any shape: a unit is a pair, or a copied channel.
-template <typename In, typename Out>
+// Any shape.  Units of a head: r / 2 pairs; then, unless y is x, copied channels one by one and, kWhole, where rows are
+// of whole 16 bytes, 8 by 8 those of loads without a rotated channel.
+template <typename In, typename Out, bool kWhole>
 __global__ void __launch_bounds__(kThreads) k_rope_any(RopePlan pl) {
   __shared__ float2 cs[kMaxAngles];
   const RopeArgs& a = pl.a;
   pdl_wait();
-  const int64_t t0 = (int64_t)blockIdx.x * pl.tokens;
-  const int h0 = blockIdx.y * pl.heads;
+  int64_t t0;
+  uint32_t before;
+  first_unit(pl, &t0, &before);
   rotations(a, t0, pl.tokens, cs);
   __syncthreads();
   const In* x = static_cast<const In*>(a.x);
   Out* y = static_cast<Out*>(a.y);
-  const int total = pl.tokens * pl.heads * (int)pl.units.d, pairs = a.r / 2;
-  for (int u = threadIdx.x; u < total; u += kThreads) {
-    uint32_t th, unit, t, h;
-    pl.units.split(u, &th, &unit);
-    pl.head_div.split(th, &t, &h);
-    if (t0 + t >= a.rows || h0 + (int)h >= a.heads) continue;
-    const In* p = x + (t0 + t) * a.x_token + (int64_t)(h0 + h) * a.x_head;
-    Out* q = y + (t0 + t) * a.y_token + (int64_t)(h0 + h) * a.y_head;
-    if ((int)unit < pairs) {
-      const int c1 = a.start + (a.layout == CSA2_ROPE_HALF ? (int)unit : 2 * (int)unit);
-      const int c2 = a.layout == CSA2_ROPE_HALF ? c1 + pairs : c1 + 1;
-      const float x1 = to_f32(p[c1]), x2 = to_f32(p[c2]);
-      const float2 z = cs[t * pairs + unit];
-      store1(q + c1, x1 * z.x - x2 * z.y);
-      store1(q + c2, x1 * z.y + x2 * z.x);
-    } else {
-      int c = unit - pairs;
-      if (c >= a.start) c += a.r;
-      store1(q + c, to_f32(p[c]));
+  const int total = (int)min((int64_t)pl.span, pl.total - (int64_t)blockIdx.x * pl.span), pairs = a.r / 2;
+  const int first = kWhole ? a.start & ~(kUnit - 1) : 0, width = kWhole ? touched_units(a) * kUnit : a.d;
+  const int ones = pairs + width - a.r;             // units below: a pair or a channel
+  constexpr int kMany = sizeof(In) == 4 ? 2 : 4;    // units in flight
+  for (int u0 = threadIdx.x; u0 < total; u0 += kMany * kThreads) {
+    Eight<In> v[kMany];
+    float x1[kMany], x2[kMany];
+    int64_t to[kMany];
+    int c2[kMany], at[kMany];                       // second channel, angle; at -1: copied; -2: nothing; -3: copied 8
+#pragma unroll
+    for (int k = 0; k < kMany; ++k) {
+      const uint32_t u = u0 + k * kThreads;
+      at[k] = -2;
+      to[k] = c2[k] = 0;
+      if (u >= (uint32_t)total) continue;
+      uint32_t t, h, unit;
+      pl.per_token.split(before + u, &t, &unit);
+      pl.units.split(unit, &h, &unit);
+      int c;
+      if ((int)unit < pairs) {
+        c = a.start + (a.layout == CSA2_ROPE_HALF ? (int)unit : 2 * (int)unit);
+        c2[k] = a.layout == CSA2_ROPE_HALF ? pairs : 1;
+        at[k] = t * pairs + unit;
+      } else if (!kWhole || (int)unit < ones) {
+        c = first + unit - pairs;
+        if (c >= a.start) c += a.r;
+        at[k] = -1;
+      } else {
+        c = (unit - ones) * kUnit;
+        if (c >= first) c += width;
+        at[k] = -3;
+      }
+      const In* p = x + (t0 + t) * a.x_token + (int64_t)h * a.x_head + c;
+      to[k] = (t0 + t) * a.y_token + (int64_t)h * a.y_head + c;
+      if (kWhole && at[k] == -3) v[k].load(p);
+      else x1[k] = to_f32(*p);
+      if (at[k] >= 0) x2[k] = to_f32(p[c2[k]]);
+    }
+#pragma unroll
+    for (int k = 0; k < kMany; ++k) {
+      if (at[k] == -2) continue;
+      if (kWhole && at[k] == -3) {
+        float f[8];
+        v[k].get(f);
+        store8(y + to[k], f);
+        continue;
+      }
+      if (at[k] >= 0) {
+        const float2 z = cs[at[k]];
+        const float f1 = x1[k] * z.x - x2[k] * z.y;
+        store1(y + to[k] + c2[k], x1[k] * z.y + x2[k] * z.x);
+        x1[k] = f1;
+      }
+      store1(y + to[k], x1[k]);
     }
   }
 }
 
-__global__ void k_rope_table(const __grid_constant__ RopeTable t, int n, uint64_t* out) {
+// The table comes from the host with the launch, 256 pairs at a time.
+struct RopeTable {
+  uint64_t g[256];
+};
+__global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ RopeTable t, int n, uint64_t* out) {
   pdl_wait();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) out[i] = t.g[i];
+  if (threadIdx.x < n) out[threadIdx.x] = t.g[threadIdx.x];
 }
 
 template <typename In, typename Out>
-cudaError_t launch_typed(const RopePlan& pl, dim3 grid, bool eight, cudaStream_t s) {
-  if (!eight) return launch_step(k_rope_any<In, Out>, grid, dim3(kThreads), 0, s, pl);
-  return pl.a.layout == CSA2_ROPE_HALF ? launch_step(k_rope<In, Out, true>, grid, dim3(kThreads), 0, s, pl)
-                                       : launch_step(k_rope<In, Out, false>, grid, dim3(kThreads), 0, s, pl);
+cudaError_t launch_typed(const RopePlan& pl, int64_t grid, Mode mode, cudaStream_t s) {
+  const auto kernel = mode == kHalves    ? k_rope<In, Out, kHalves>
+                      : mode == kRagged  ? k_rope<In, Out, kRagged>
+                      : mode == kOnes    ? k_rope_any<In, Out, false>
+                      : mode == kOnesWhole ? k_rope_any<In, Out, true>
+                                         : k_rope<In, Out, kInterleaved>;
+  return launch_step(kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, pl);
 }
 
 }  // namespace
 
-cudaError_t launch_rope_table(const RopeTable& t, int pairs, uint64_t* out, cudaStream_t s) {
-  return launch_step(k_rope_table, dim3(1), dim3(256), 0, s, t, pairs, out);
+cudaError_t launch_rope_table(const uint64_t* turns, int pairs, uint64_t* out, cudaStream_t s) {
+  for (int i = 0; i < pairs; i += 256) {
+    RopeTable t = {};
+    const int n = std::min(256, pairs - i);
+    std::copy(turns + i, turns + i + n, t.g);
+    const cudaError_t e = launch_step(k_rope_table, dim3(1), dim3(256), 0, s, t, n, out + i);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
-  const bool in_place = a.x == a.y;
+  const bool in_place = a.x == a.y, half = a.layout == CSA2_ROPE_HALF;
   const int in = a.x_dtype == CSA2_F32 ? 4 : 2, out = a.y_dtype == CSA2_F32 ? 4 : 2;
   auto whole = [](const void* p, int64_t token, int64_t head, int size) {   // rows start on 16 bytes
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && token * size % 16 == 0 && head * size % 16 == 0;
   };
-  const bool eight = a.d % kUnit == 0 && a.start % kUnit == 0 && a.r % (a.layout == CSA2_ROPE_HALF ? 2 * kUnit : kUnit) == 0 &&
-                     whole(a.x, a.x_token, a.x_head, in) && whole(a.y, a.y_token, a.y_head, out);
-  const int copied = in_place ? 0 : a.d - a.r;
+  const bool eight = a.d % kUnit == 0 && whole(a.x, a.x_token, a.x_head, in) && whole(a.y, a.y_token, a.y_head, out);
+  const Mode mode = !eight ? kOnes
+                    : half ? (a.start % kUnit == 0 && a.r % (2 * kUnit) == 0 ? kHalves : kOnesWhole)
+                           : (a.start % 2 != 0 ? kOnesWhole : a.start % kUnit == 0 && a.r % kUnit == 0 ? kInterleaved : kRagged);
+  int units, copied;                        // of a head: in all, copied ones of them
+  switch (mode) {
+    case kOnes: units = a.d - a.r / 2, copied = a.d - a.r; break;
+    case kOnesWhole: copied = 7 * touched_units(a) + a.d / kUnit - a.r, units = a.r / 2 + copied; break;
+    default: units = a.d / kUnit - (half ? a.r / 16 : 0), copied = units - rotated_units(a, mode);
+  }
+  if (in_place) units -= copied;
+  if (units == 0) return cudaSuccess;       // (nothing rotated)
   RopePlan pl;
   pl.a = a;
-  const int units = eight ? (a.layout == CSA2_ROPE_HALF ? a.r / 16 : a.r / 8) + copied / kUnit : a.r / 2 + copied;
-  if (units == 0) return cudaSuccess;       // (in place, nothing rotated)
-  // A block: about 2,048 units, whole tokens while their angles fit; fewer heads of one token where there are
-  // few tokens, so that every SM has a block (one token of 64 heads x 512 channels in 32 blocks).
+  // A block: 2,048 units (8 a thread), fewer where there are few, so
+  // that every SM has work (one token of 64 heads x 512 channels goes to 64 blocks), and no more tokens than there is
+  // shared memory for their angles.
   const int64_t per_token = (int64_t)a.heads * units;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(2048, a.rows * per_token / (2 * 152) + 1));
-  pl.heads = (int)std::min<int64_t>(a.heads, std::max<int64_t>(1, (want + units - 1) / units));
-  pl.tokens = 1;
-  if (pl.heads == a.heads) pl.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(want / per_token, kMaxAngles / std::max(1, a.r / 2)));
+  if (per_token > 1 << 30) {                // (positions in a token, with a block's units behind them, fit 31 bits)
+    RopeArgs b = a;
+    b.heads = a.heads / 2;
+    const cudaError_t e = launch_rope(b, s);
+    if (e != cudaSuccess) return e;
+    b.heads = a.heads - b.heads;
+    b.x = static_cast<const uint8_t*>(a.x) + (a.heads - b.heads) * a.x_head * in;
+    b.y = static_cast<uint8_t*>(a.y) + (a.heads - b.heads) * a.y_head * out;
+    return launch_rope(b, s);
+  }
+  const int pairs = std::max(1, a.r / 2);
+  pl.total = a.rows * per_token;
+  pl.far = pl.total > INT_MAX;
+  pl.span = (int)std::min<int64_t>(std::max<int64_t>(64, std::min<int64_t>(2048, pl.total / (2 * 152))), (kMaxAngles / pairs - 1) * per_token);
+  pl.tokens = (int)((pl.span - 2) / per_token) + 2;
+  if (pl.span % per_token == 0) pl.tokens = (int)(pl.span / per_token);
+  pl.per_token = Divisor::of((uint32_t)per_token);
   pl.units = Divisor::of(units);
-  pl.head_div = Divisor::of(pl.heads);
-  const int64_t gx = (a.rows + pl.tokens - 1) / pl.tokens;
-  if (gx > INT_MAX) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)gx, (unsigned)((a.heads + pl.heads - 1) / pl.heads));
+  const int64_t grid = (pl.total + pl.span - 1) / pl.span;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   if (a.x_dtype == CSA2_F32)
-    return a.y_dtype == CSA2_F32 ? launch_typed<float, float>(pl, grid, eight, s) : launch_typed<float, uint16_t>(pl, grid, eight, s);
-  return a.y_dtype == CSA2_F32 ? launch_typed<uint16_t, float>(pl, grid, eight, s) : launch_typed<uint16_t, uint16_t>(pl, grid, eight, s);
+    return a.y_dtype == CSA2_F32 ? launch_typed<float, float>(pl, grid, mode, s) : launch_typed<float, uint16_t>(pl, grid, mode, s);
+  return a.y_dtype == CSA2_F32 ? launch_typed<uint16_t, float>(pl, grid, mode, s) : launch_typed<uint16_t, uint16_t>(pl, grid, mode, s);
 }
 
 }  // namespace csa2

@@ -494,14 +494,14 @@ typedef struct csa2_rope_spec {
 } csa2_rope_spec;
 
 /* The table that csa2_rope reads, made once for a model: table uint64 [r/2] (device)
- * receives theta_i / 2 pi in turns per position, as 0.64 fixed point.  r: even, <= 512. */
+ * receives theta_i / 2 pi in turns per position, as 0.64 fixed point.  r: even, <= 2048. */
 int csa2_rope_table(const csa2_rope_spec* spec, int32_t r, uint64_t* table, void* stream);
 
 /* y = x with channels start .. start + r - 1 of every head rotated to its token's
  * position (R20) and multiplied by amplitude (1, or YARN's attention factor); the
  * other channels are copied.  x and y: bf16 or fp32, [n_tokens][heads][d] with the
- * given strides in elements, channels contiguous; 16-byte aligned rows and channel
- * counts that 8 (HALF: r / 2 too) divides go 8 channels at a time.  y may be x (same
+ * given strides in elements, channels contiguous; fastest where rows are 16-byte
+ * aligned and 8 divides d (HALF: start and r / 2 too).  y may be x (same
  * type and strides: only the rotated channels are touched); otherwise they must not
  * overlap.  positions int32 [n_tokens] (negative ones turn backwards).  inverse != 0
  * turns by -p: back, and also the gradient (the transpose) of the rotation. */

@@ -53,6 +53,33 @@ def test_pack_bit_exact(n, K, extra, dtype):
     np.testing.assert_array_equal(codes.cpu().numpy(), rc)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [16, 32, 48, 64, 80, 96, 112, 128, 208])
+def test_pack_short_rows(K, dtype):
+    """Rows of one short block (several share a warp's lanes), with infinities and NaN that stay in their rows."""
+    for n in (1, 2, 37, 6001):
+        g = torch.Generator().manual_seed(n + K)
+        x = torch.randn(n, K + 16, generator=g) * torch.exp(3 * torch.randn(n, 1, generator=g))
+        x[:, K:] = 1e20                                    # (not of the rows)
+        nan = torch.rand(n, generator=g) < 0.2
+        inf = (torch.rand(n, generator=g) < 0.2) & ~nan
+        x = x.to(dtype).cuda()[:, :K]
+        x[nan.cuda(), K // 3] = float("nan")
+        clean = x.nan_to_num(nan=0.0).float().cpu().numpy()
+        x[inf.cuda(), K - 1] = -float("inf")
+        codes, scales = pack(x)
+        rc, rs = O.pack_fp8_blocks(clean)
+        codes, scales, nan, inf = codes.cpu().numpy(), scales.cpu().numpy(), nan.numpy(), inf.numpy()
+        assert np.all(codes[nan, K // 3] & 0x7F == 0x7F)
+        rc[nan, K // 3] = codes[nan, K // 3]
+        last = (K - 1) // 128 * 128
+        assert np.all(np.isinf(scales[inf, -1]))
+        np.testing.assert_array_equal(scales[~inf], rs[~inf])
+        np.testing.assert_array_equal(scales[:, :-1], rs[:, :-1])
+        np.testing.assert_array_equal(codes[~inf], rc[~inf])
+        np.testing.assert_array_equal(codes[:, :last], rc[:, :last])
+
+
 def test_pack_every_bf16_value():
     """All finite bf16 patterns, each beside a maximum that puts it somewhere in the codes' range."""
     bits = np.arange(1 << 16, dtype=np.uint16)

@@ -32,7 +32,8 @@ def table_of(r, scaling="none", factor=1.0, base=10000.0, original=4096):
 @pytest.mark.parametrize("r,base,scaling,factor,original", [
     (2, 10000.0, "none", 1.0, 0), (64, 10000.0, "none", 1.0, 0), (512, 1e6, "none", 1.0, 0), (64, 10000.0, "linear", 8.0, 0),
     (64, 10000.0, "ntk", 8.0, 0), (128, 500000.0, "yarn", 32.0, 8192), (64, 10000.0, "yarn", 40.0, 4096), (64, 10000.0, "yarn", 4.0, 1),
-    (6, 100.0, "yarn", 2.0, 100), (64, 1.5, "none", 1.0, 0)])
+    (6, 100.0, "yarn", 2.0, 100), (64, 1.5, "none", 1.0, 0),
+    (514, 10000.0, "ntk", 4.0, 0), (576, 10000.0, "yarn", 40.0, 4096), (2048, 10000.0, "none", 1.0, 0)])
 def test_table(r, base, scaling, factor, original):
     """Turns per position to 2^-50 of themselves (the libraries' powers and logarithms) and one unit of 2^-64."""
     t = table_of(r, scaling, factor, base, original).cpu().numpy().astype(np.uint64)
@@ -104,6 +105,43 @@ def test_odd_shapes(n, heads, d, start, r, layout):
 def test_places(place, layout):
     for dtype in (torch.bfloat16, torch.float32):
         check(50, 6, 128, 64, 64, layout, dtype, place=place)
+
+
+@pytest.mark.parametrize("place", ["apart", "in_place", "slice"])
+@pytest.mark.parametrize("n,heads,d,start,r", [(7, 5, 128, 0, 62), (300, 8, 128, 66, 62), (40, 3, 64, 2, 4), (11, 2, 64, 6, 4), (9, 1, 24, 2, 20),
+                                               (2, 4, 16, 4, 8)])
+def test_pairs_that_share_a_load_with_copied_channels(n, heads, d, start, r, place):
+    """Interleaved pairs from any even channel on, in rows of whole 16 bytes."""
+    for x_dtype in (torch.bfloat16, torch.float32):
+        check(n, heads, d, start, r, "interleaved", x_dtype, place=place)
+        if place != "in_place":
+            check(n, heads, d, start, r, "interleaved", x_dtype, torch.float32 if x_dtype == torch.bfloat16 else torch.bfloat16, place=place)
+
+
+@pytest.mark.parametrize("place", ["apart", "in_place", "slice"])
+@pytest.mark.parametrize("n,heads,d,start,r,layout", [(7, 5, 128, 1, 62, "interleaved"), (21, 8, 128, 66, 62, "half"), (5, 40, 512, 450, 62, "half"),
+                                                      (9, 1, 24, 3, 20, "interleaved"), (3, 2, 16, 5, 2, "half"), (2, 70, 64, 4, 56, "half")])
+def test_any_channels_of_whole_rows(n, heads, d, start, r, layout, place):
+    for x_dtype in (torch.bfloat16, torch.float32):
+        check(n, heads, d, start, r, layout, x_dtype, place=place)
+        if place != "in_place":
+            check(n, heads, d, start, r, layout, x_dtype, torch.float32 if x_dtype == torch.bfloat16 else torch.bfloat16, place=place)
+
+
+@pytest.mark.parametrize("n,heads,d,r", [(4000, 1, 16, 16), (700, 3, 512, 512), (2049, 1, 2, 2), (650, 1, 512, 512), (61, 37, 72, 16), (301, 3, 576, 576), (5, 2, 2048, 2048),
+                                         (6, 1, 1990, 1986)])
+def test_blocks_that_begin_inside_a_token(n, heads, d, r):
+    for place in ("apart", "in_place"):
+        for layout in ("half", "interleaved"):
+            check(n, heads, d, 0, r, layout, place=place)
+
+
+def test_tokens_of_more_than_2_31_channels():
+    heads, d = 40000, 65535
+    x = torch.arange(d, device="cuda").remainder(251).to(torch.bfloat16).expand(heads, d)
+    y = torch.full((heads, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    abi.csa2_rope(x[None], y[None], torch.zeros(1, dtype=torch.int32, device="cuda"), table_of(2), start=0, layout=abi.ROPE_HALF)
+    assert all(bool((part == x[:1]).all()) for part in y.split(1000))
 
 
 @pytest.mark.parametrize("scaling,factor", [("linear", 8.0), ("ntk", 8.0), ("yarn", 40.0)])

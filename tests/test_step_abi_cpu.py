@@ -98,7 +98,7 @@ def spec(**kw):
 def test_rope_table(lib):
     call = lambda r=64, t=FAKE, **kw: lib.csa2_rope_table(ref(spec(**kw)), r, t, None)  # noqa: E731
     assert lib.csa2_rope_table(None, 64, FAKE, None) == 1
-    for r in (-2, 3, 514):
+    for r in (-2, 3, 2050):
         assert call(r) == 1 and "even" in err()
     for bad in (dict(scaling=4), dict(scaling=-1), dict(base=1.0), dict(base=math.inf), dict(base=math.nan), dict(factor=0.5),
                 dict(factor=math.inf), dict(factor=math.nan), dict(original_len=0), dict(beta_slow=0.0), dict(beta_fast=0.5),
@@ -117,7 +117,7 @@ def test_rope(lib):
         return lib.csa2_rope(a["x"], a["xt"], a["xts"], a["xhs"], a["y"], a["yt"], a["yts"], a["yhs"], a["n"], a["heads"], a["d"], a["start"],
                              a["r"], a["layout"], a["inv"], a["amp"], a["pos"], a["table"], None)
     for bad in (dict(xt=2), dict(yt=-1), dict(n=-1), dict(n=1 << 31), dict(heads=-1), dict(heads=65536), dict(d=0), dict(d=65537),
-                dict(r=31), dict(r=-2), dict(r=514, d=600), dict(start=-1), dict(start=33), dict(layout=2), dict(amp=math.nan),
+                dict(r=31), dict(r=-2), dict(r=2050, d=2200), dict(start=-1), dict(start=33), dict(layout=2), dict(amp=math.nan),
                 dict(amp=math.inf), dict(xts=-1), dict(xhs=-64), dict(yts=63), dict(yhs=63), dict(x=None), dict(y=None), dict(x=FAKE + 1),
                 dict(yt=0, y=FAKE + 2), dict(pos=None), dict(pos=FAKE + 2), dict(table=None), dict(table=FAKE + 4)):
         assert call(**bad) == 1, bad
