@@ -131,6 +131,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Barrier / vote among the worker warps only (the MMA warp never joins).
 __device__ __forceinline__ void workers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
@@ -256,10 +262,11 @@ __device__ __forceinline__ void store_slice(const AttnArgs& a, const KeyBytes& k
       const uint32_t w = word_of(kb.v[SL], j);
       const uint32_t s2 = j < 2 ? g0 : g1;
       uint4 o;
-      o.x = hmul2(e2m1x2_f16x2(w & 0xFFu), s2);   // exact: <= 6 significant bits
-      o.y = hmul2(e2m1x2_f16x2((w >> 8) & 0xFFu), s2);
-      o.z = hmul2(e2m1x2_f16x2((w >> 16) & 0xFFu), s2);
-      o.w = hmul2(e2m1x2_f16x2(w >> 24), s2);
+      e2m1x8_f16x8(w, o.x, o.y, o.z, o.w);
+      o.x = hmul2(o.x, s2);   // exact: <= 6 significant bits
+      o.y = hmul2(o.y, s2);
+      o.z = hmul2(o.z, s2);
+      o.w = hmul2(o.w, s2);
       *reinterpret_cast<uint4*>(dst + j * 128) = o;
     }
   } else {
@@ -378,6 +385,81 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     qv[r] = (!mma_warp && hb + h < a.Hq) ? __ldg(reinterpret_cast<const uint4*>(a.Q + (row * a.Hq + hb + h) * kD + c8 * 8))
                                     : make_uint4(0, 0, 0, 0);
   }
+  // the window rows of the token: raw positions max(0, t-W+1, pos0) .. min(t, last row held)
+  int w_lo = max(max(0, t - a.W + 1), pos0);
+  int w_hi = min(t, pos0 + a.swa_cap - 1);
+  int ctx = 0;
+  if (kTree) {   // from the first position that the buffer holds (or the first ancestor) to the token itself
+    ctx = max(0, a.ctx_len[b]);
+    w_lo = max(max(0, t - a.W + 1), min(a.swa_cap > 0 ? pos0 : INT_MAX, ctx));
+    w_hi = t;
+  }
+  const int n_win = max(0, w_hi - w_lo + 1);
+  int n_sel = 0, n_mine = 0, n_my = 0;
+  int32_t cur_src = -1;
+  float cur_wsc = 0.f;
+  uint2 cur_sc = make_uint2(0, 0);
+  KeyBytes kb;
+  auto resolve = [&] {
+    // ---- the selection (and the window rows) come from earlier kernels of the step
+    pdl_wait();
+    n_sel = kTree && t < 0 ? 0 : a.cnt[row];
+    const int nv = n_visible(n_ent, t);
+    if (n_sel < 0 || n_sel > a.K) {
+      if (tid == 0 && rank == 0) raise_status(status, CSA2_STATUS_BAD_COUNT);
+      n_sel = n_sel < 0 ? 0 : a.K;
+    }
+    // the key list.  One CTA per token: its n_sel selected entries, then its window
+    // rows.  A cluster: rank r takes an equal share of the K selection slots (unused
+    // ones empty, so that the index loads need not wait for the count) and an equal
+    // share of the window rows.
+    int sel_off = 0, sel_cap = n_sel, w_first = w_lo;
+    n_mine = n_sel + n_win;
+    if (n_split > 1) {
+      sel_off = (int)((int64_t)a.K * rank / n_split);
+      sel_cap = (int)((int64_t)a.K * (rank + 1) / n_split) - sel_off;
+      // (a tree's window bounds round up where the selection's round down, so that K + W = 640 keys over five ranks are
+      // 128 for each of them, one chunk, and not 129 for one)
+      const int up = kTree ? n_split - 1 : 0;
+      const int u0 = (int)(((int64_t)n_win * rank + up) / n_split), u1 = (int)(((int64_t)n_win * (rank + 1) + up) / n_split);
+      w_first = w_lo + u0;
+      n_mine = sel_cap + (u1 - u0);
+    }
+    const int kb0 = 0, kb1 = n_mine;
+    n_my = (kb1 - kb0 + kChunk - 1) / kChunk;   // chunks of kChunk keys, <= kMaxChunks
+
+    // ---- key sources.  Every worker resolves its key in the first chunk; the
+    // key's later chunks are shared out among its four threads.
+    if (!mma_warp && n_my > 0) {
+      cur_src = key_source<kTree>(a, row, b, kb0 + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, ctx, qd == 0, status);
+      if (qd == 0) {
+        sm.slot[key] = cur_src;
+        sm.kexp[key] = (int8_t)key_exp<kFp8, kTree>(a, cur_src);
+      }
+      for (int c = qd + 1; c < n_my; c += 4) {
+        const int32_t src =
+            key_source<kTree>(a, row, b, kb0 + c * kChunk + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, ctx, true,
+                              status);
+        sm.slot[c * kChunk + key] = src;
+        sm.kexp[c * kChunk + key] = (int8_t)key_exp<kFp8, kTree>(a, src);
+      }
+    }
+    // ---- the first chunk's packed bytes
+    if (!mma_warp && n_my > 0) {
+      load_slice<0, kFp8, kTree>(a, cur_src, qd, kb);
+      load_slice<1, kFp8, kTree>(a, cur_src, qd, kb);
+      if (!fp8_row_key<kFp8>(cur_src)) {
+        load_slice<2, kFp8, kTree>(a, cur_src, qd, kb);
+        load_slice<3, kFp8, kTree>(a, cur_src, qd, kb);
+        cur_sc = load_scales(a, cur_src, qd);
+      }
+      cur_wsc = load_wscale<kFp8, kTree>(a, cur_src);
+    }
+  };
+  // The keys' chain of loads (index, page, bytes) runs while Q is on its way.  A cluster of the layer step does the
+  // work on Q first, which needs none of the previous kernel's results and hides behind its end.
+  const bool early = kTree || n_split == 1;
+  if (early) resolve();
   if (tid == 0) {
     tc::mbar_init(&sm.bar_s, 1);
     tc::mbar_init(&sm.p_ready, kWorkers / 32);
@@ -396,20 +478,26 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     sm.qexp[tid] = 0;
   }
   __syncthreads();
-  // largest bf16 exponent field of each head (lanes L, L^8, L^16, L^24 share a head)
+  // largest bf16 exponent field of each head (lanes L, L^8, L^16, L^24 share a head), of heads r and r + 32 at once
   if (!mma_warp) {
+    uint32_t e[4];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      uint32_t e = 0;
+      uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = word_of(qv[r], j);
-        e = max(e, max((w >> 7) & 0xFFu, (w >> 23) & 0xFFu));
-      }
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 8));
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 16));
-      if (lane < 8 && e) atomicMax(&sm.qexp[8 * r + lane], (int)e);
+      for (int j = 0; j < 4; ++j) m = max_u16x2(m, word_of(qv[r], j) & 0x7FFF7FFFu);
+      m = max(m >> 23, (m >> 7) & 0xFFu);
+      if (r < 4) e[r] = m;
+      else e[r - 4] |= m << 16;
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      e[r] = max_u16x2(e[r], __shfl_xor_sync(0xffffffffu, e[r], 8));
+      e[r] = max_u16x2(e[r], __shfl_xor_sync(0xffffffffu, e[r], 16));
+    }
+    const uint32_t m = qd == 0 ? e[0] : qd == 1 ? e[1] : qd == 2 ? e[2] : e[3];
+    atomicMax(&sm.qexp[lane], (int)(m & 0xFFFFu));
+    atomicMax(&sm.qexp[32 + lane], (int)(m >> 16));
   }
   __syncthreads();
   // per head: 2^-e_h brings the largest magnitude into [2^14, 2^15) (e_h in [-110, 110])
@@ -436,70 +524,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
           make_uint4(ov[0], ov[1], ov[2], ov[3]);
     }
   }
-  // the window rows of the token: raw positions max(0, t-W+1, pos0) .. min(t, last row held)
-  int w_lo = max(max(0, t - a.W + 1), pos0);
-  int w_hi = min(t, pos0 + a.swa_cap - 1);
-  int ctx = 0;
-  if (kTree) {   // from the first position that the buffer holds (or the first ancestor) to the token itself
-    ctx = max(0, a.ctx_len[b]);
-    w_lo = max(max(0, t - a.W + 1), min(a.swa_cap > 0 ? pos0 : INT_MAX, ctx));
-    w_hi = t;
-  }
-  const int n_win = max(0, w_hi - w_lo + 1);
-  // ---- the selection (and the window rows) come from earlier kernels of the step
-  pdl_wait();
-  int n_sel = kTree && t < 0 ? 0 : a.cnt[row];
-  const int nv = n_visible(n_ent, t);
-  if (n_sel < 0 || n_sel > a.K) {
-    if (tid == 0 && rank == 0) raise_status(status, CSA2_STATUS_BAD_COUNT);
-    n_sel = n_sel < 0 ? 0 : a.K;
-  }
-  // the key list.  One CTA per token: its n_sel selected entries, then its window
-  // rows.  A cluster: rank r takes an equal share of the K selection slots (unused
-  // ones empty, so that the index loads need not wait for the count) and an equal
-  // share of the window rows.
-  int sel_off = 0, sel_cap = n_sel, w_first = w_lo, n_mine = n_sel + n_win;
-  if (n_split > 1) {
-    sel_off = (int)((int64_t)a.K * rank / n_split);
-    sel_cap = (int)((int64_t)a.K * (rank + 1) / n_split) - sel_off;
-    const int u0 = (int)((int64_t)n_win * rank / n_split), u1 = (int)((int64_t)n_win * (rank + 1) / n_split);
-    w_first = w_lo + u0;
-    n_mine = sel_cap + (u1 - u0);
-  }
-  const int kb0 = 0, kb1 = n_mine;
-  const int n_my = (kb1 - kb0 + kChunk - 1) / kChunk;   // chunks of kChunk keys, <= kMaxChunks
-
-  // ---- key sources.  Every worker resolves its key in the first chunk; the
-  // key's later chunks are shared out among its four threads.
-  int32_t cur_src = -1;
-  if (!mma_warp && n_my > 0) {
-    cur_src = key_source<kTree>(a, row, b, kb0 + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, ctx, qd == 0, status);
-    if (qd == 0) {
-      sm.slot[key] = cur_src;
-      sm.kexp[key] = (int8_t)key_exp<kFp8, kTree>(a, cur_src);
-    }
-    for (int c = qd + 1; c < n_my; c += 4) {
-      const int32_t src =
-          key_source<kTree>(a, row, b, kb0 + c * kChunk + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, ctx, true,
-                            status);
-      sm.slot[c * kChunk + key] = src;
-      sm.kexp[c * kChunk + key] = (int8_t)key_exp<kFp8, kTree>(a, src);
-    }
-  }
-  // ---- the first chunk's packed bytes
-  float cur_wsc = 0.f;
-  uint2 cur_sc = make_uint2(0, 0);
-  KeyBytes kb;
-  if (!mma_warp && n_my > 0) {
-    load_slice<0, kFp8, kTree>(a, cur_src, qd, kb);
-    load_slice<1, kFp8, kTree>(a, cur_src, qd, kb);
-    if (!fp8_row_key<kFp8>(cur_src)) {
-      load_slice<2, kFp8, kTree>(a, cur_src, qd, kb);
-      load_slice<3, kFp8, kTree>(a, cur_src, qd, kb);
-      cur_sc = load_scales(a, cur_src, qd);
-    }
-    cur_wsc = load_wscale<kFp8, kTree>(a, cur_src);
-  }
+  if (!early) resolve();
   tc::fence_async_smem();
   tc::tc_fence_before();
   __syncthreads();
@@ -531,7 +556,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
       if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.p_ready, it & 1, 1u << 22))) { *abort = 1; break; }
       tc::tc_fence_after();
       // PV over the chunk's keys only (a short last chunk skips its empty 16-key steps)
-      const int ksteps = (min(kChunk, kb1 - kb0 - kChunk * it) + 15) / 16;
+      const int ksteps = (min(kChunk, n_mine - kChunk * it) + 15) / 16;
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {   // tile by tile: a finished tile frees its K slice for the next chunk
 #pragma unroll
@@ -739,6 +764,23 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     }
     cluster_sync();   // every rank's (m, l) and partial O are published
     const int h0 = kHeads * crank / n_split, h1 = kHeads * (crank + 1) / n_split;
+    // this rank's heads, 4 dims per element; every rank's value of two elements in flight, the first two while the
+    // factors are computed
+    const uint32_t pbase = tc::smem_addr(part);
+    const int n4 = (h1 - h0) * (kD / 4);
+    float4 r[2][kMaxSplit];
+    auto request = [&](int e0) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int e = e0 + u * kThreads, at = h0 * (kD / 4) + e;
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q)
+          r[u][q] = q >= n_split || e >= n4 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                    : q == crank            ? reinterpret_cast<const float4*>(part)[at]
+                                            : ld_cluster4(map_to_rank(pbase + 16u * (uint32_t)at, q));
+      }
+    };
+    request(tid);
     float* facq = reinterpret_cast<float*>(sm.q);    // [rank][head]: the Q tile is no longer read
     if (tid < kHeads) {
       // every rank's (m, l) of this head; the loads are independent (unrolled, predicated)
@@ -763,19 +805,8 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
         a.lse[row * a.Hq + hb + tid] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
     }
     __syncthreads();
-    // this rank's heads, 4 dims per element; every rank's value of two elements in flight
-    const uint32_t pbase = tc::smem_addr(part);
-    const int n4 = (h1 - h0) * (kD / 4);
     for (int e0 = tid; e0 < n4; e0 += 2 * kThreads) {
-      float4 r[2][kMaxSplit];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int e = e0 + u * kThreads;
-#pragma unroll
-        for (int q = 0; q < kMaxSplit; ++q)
-          r[u][q] = (q < n_split && e < n4) ? ld_cluster4(map_to_rank(pbase + 16u * (uint32_t)(h0 * (kD / 4) + e), q))
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      if (e0 != tid) request(e0);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int e = e0 + u * kThreads;
