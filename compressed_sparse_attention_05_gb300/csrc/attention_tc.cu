@@ -97,6 +97,7 @@ struct TcSmem {
   float alpha[kHeads], l_run[kHeads], fac[kHeads];
   uint64_t k_ready[4];   // workers -> MMA warp: slice of the K tile written (one arrival per warp)
   uint64_t p_ready;      // workers -> MMA warp: P written, O^T rescaled
+  uint64_t bar_q;        // Q's rows have arrived in the K tile
   uint64_t bar_s;        // MMA commit: S^T complete
   uint64_t bar_pv[4];    // MMA commit: PV M-tile complete (its K slice is free again)
   uint32_t tmem;
@@ -377,13 +378,27 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   const int t = kTree ? max(a.q_pos[row], -1) : a.q_pos[row];   // (-1: no node of the tree)
   const int n_ent = a.n_entries[b];
   const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
-  uint4 qv[8];   // unit = (head, 8 dims); 8 heads of a unit group share a core matrix
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int u = tid + kWorkers * r;
-    const int h = ((u >> 9) << 3) | (u & 7), c8 = (u >> 3) & 63;
-    qv[r] = (!mma_warp && hb + h < a.Hq) ? __ldg(reinterpret_cast<const uint4*>(a.Q + (row * a.Hq + hb + h) * kD + c8 * 8))
-                                    : make_uint4(0, 0, 0, 0);
+  if (tid == 0) {
+    tc::mbar_init(&sm.bar_q, 1);
+    tc::mbar_init(&sm.bar_s, 1);
+    tc::mbar_init(&sm.p_ready, kWorkers / 32);
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sm.bar_pv[i], 1);
+      tc::mbar_init(&sm.k_ready[i], kWorkers / 32);
+    }
+    sm.abort = 0;
+    tc::mbar_fence_init();
+    // Q's rows into the K tile, which is free until the first chunk is dequantised
+    const uint32_t bytes = (uint32_t)min(kHeads, a.Hq - hb) * kD * sizeof(uint16_t);
+    tc::mbar_arrive_expect_tx(&sm.bar_q, bytes);
+    tc::bulk_g2s(sm.k, a.Q + (row * a.Hq + hb) * kD, bytes, &sm.bar_q);
+  }
+  if (mma_warp) tc::tmem_alloc(&sm.tmem, kTmemCols);
+  if (tid < kHeads) {
+    sm.m_ref[tid] = -INFINITY;
+    sm.m_thr[tid] = -INFINITY;
+    sm.m_exp[tid] = 0.f;
+    sm.qexp[tid] = 0;
   }
   // the window rows of the token: raw positions max(0, t-W+1, pos0) .. min(t, last row held)
   int w_lo = max(max(0, t - a.W + 1), pos0);
@@ -460,24 +475,19 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   // work on Q first, which needs none of the previous kernel's results and hides behind its end.
   const bool early = kTree || n_split == 1;
   if (early) resolve();
-  if (tid == 0) {
-    tc::mbar_init(&sm.bar_s, 1);
-    tc::mbar_init(&sm.p_ready, kWorkers / 32);
-    for (int i = 0; i < 4; ++i) {
-      tc::mbar_init(&sm.bar_pv[i], 1);
-      tc::mbar_init(&sm.k_ready[i], kWorkers / 32);
-    }
-    sm.abort = 0;
-    tc::mbar_fence_init();
-  }
-  if (mma_warp) tc::tmem_alloc(&sm.tmem, kTmemCols);
-  if (tid < kHeads) {
-    sm.m_ref[tid] = -INFINITY;
-    sm.m_thr[tid] = -INFINITY;
-    sm.m_exp[tid] = 0.f;
-    sm.qexp[tid] = 0;
-  }
   __syncthreads();
+  // units of (head 8 r + lane % 8, 8 dims): eight lanes have eight dim groups too, so that neither the reads of rows nor
+  // the writes of core matrices meet in a bank
+  uint4 qv[8];
+  const int c8 = (tid >> 3 & ~7) | (((tid >> 3) + lane) & 7);
+  if (!mma_warp) {
+    const bool here = warp_wait(&sm.bar_q, 0, abort);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int h = 8 * r + (lane & 7);
+      qv[r] = here && hb + h < a.Hq ? *reinterpret_cast<const uint4*>(sm.k + h * kD + c8 * 8) : make_uint4(0, 0, 0, 0);
+    }
+  }
   // largest bf16 exponent field of each head (lanes L, L^8, L^16, L^24 share a head), of heads r and r + 32 at once
   if (!mma_warp) {
     uint32_t e[4];
@@ -511,8 +521,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   if (!mma_warp) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const int u = tid + kWorkers * r;
-      const int h = ((u >> 9) << 3) | (u & 7), c8 = (u >> 3) & 63;
+      const int h = 8 * r + (lane & 7);
       const float qs = pow2i(-sm.qexp[h]);
       uint32_t ov[4];
 #pragma unroll
