@@ -15,18 +15,21 @@
 // K = V, so one dequantised shared-memory tile serves as the K-major A
 // operand of the first product and as the MN-major A operand of the second.
 // S^T takes 64 tensor-memory columns and O^T four M-tiles of 64.  PV runs
-// tile by tile with a commit per tile, so that the next chunk's slice of the
-// K tile is rewritten as soon as the tile that read it is done.
+// tile by tile with a commit per two tiles, so that the next chunk's half of
+// the K tile is rewritten as soon as the tiles that read it are done.
 //
 // A CTA (16 worker warps and one MMA warp) owns one token (all heads) and a contiguous run of its
-// chunks.  Per chunk: the threads dequantise the tile in four 128-dim slices
-// (thread = one key x 32 dims of every slice, a warp = 8 whole keys); each
-// warp announces a written slice on an mbarrier and
-// the MMA warp issues the slice's eight S MMAs once all warps have, so
+// chunks.  Per chunk: the threads dequantise the tile in two halves of 256 dims
+// (thread = one key x 64 dims of each half, a warp = 8 whole keys); each
+// warp announces a written half on an mbarrier and
+// the MMA warp issues the half's sixteen S MMAs once all warps have, so
 // dequantisation overlaps the tensor core.  (An MMA issue blocks the issuing
 // thread while the tensor pipe is full, hence a warp of its own.)  The next
-// chunk's bytes are requested together once the tile is written (loads spread
-// over the slices stall the slices that follow them).  Softmax (thread = one key x 16 heads): the reference maximum of a
+// chunk's bytes are requested together once the tile is written.  The load
+// units bound a chunk as much as the tensor cores do: they take a request of
+// a warp line by line, so a key's four threads read whole lines, 32 bytes each
+// (256 tokens of 640 keys: 61 us; 16 bytes each, twice the requests, 69; four
+// slices of 128 dims instead of two halves made no difference).  Softmax (thread = one key x 16 heads): the reference maximum of a
 // head only moves when a score exceeds it by more than 2^8 (then O^T is
 // rescaled in tensor memory), so P = exp2(s - m) <= 256 fits fp16 and most
 // chunks need no maximum reduction at all; row sums stay per thread until
@@ -48,7 +51,7 @@
 // PV product (the reference maximum then follows the largest 2^f p, and the
 // normaliser adds p itself).  Main-KV entries in the FP8 format (the V4-style
 // layout kept for the A/B against MXFP4: E4M3 row + fp32 scale, one 32-byte
-// run of codes per thread and slice) go through the window rows' path: code x
+// run of codes per thread and 128 dims) go through the window rows' path: code x
 // scale rounded to bf16, the same power-of-two treatment; the kernel is
 // instantiated once per format.  P is rounded to fp16 for the PV product; the
 // normaliser sums the unrounded fp32 P (relative difference <= 2^-11).
@@ -95,11 +98,11 @@ struct TcSmem {
   float m_thr[kHeads];                 // m_ref + 2^8 growth allowance
   float m_exp[kHeads];                 // m_ref, or 0 while the head has seen no key
   float alpha[kHeads], l_run[kHeads], fac[kHeads];
-  uint64_t k_ready[4];   // workers -> MMA warp: slice of the K tile written (one arrival per warp)
+  uint64_t k_ready[2];   // workers -> MMA warp: half of the K tile (256 dims) written (one arrival per warp)
   uint64_t p_ready;      // workers -> MMA warp: P written, O^T rescaled
   uint64_t bar_q;        // Q's rows have arrived in the K tile
   uint64_t bar_s;        // MMA commit: S^T complete
-  uint64_t bar_pv[4];    // MMA commit: PV M-tile complete (its K slice is free again)
+  uint64_t bar_pv[2];    // MMA commit: two PV M-tiles complete (their half of the K tile is free again)
   uint32_t tmem;
   int abort;
 };
@@ -152,20 +155,24 @@ __device__ __forceinline__ bool workers_or(bool v) {
   return r != 0;
 }
 
-// Packed bytes of one key for the thread's 32 dims (128*sl + 32*qd ..) of each
-// slice sl, held in registers from the moment they are requested until the slice
-// is stored, so that the gather of the next chunk overlaps this chunk's products.
+// Packed bytes of one key, held in registers from the moment they are requested until the
+// half of the dims that they belong to is stored, so that the gather of the next chunk
+// overlaps this chunk's products.
 struct KeyBytes {
   uint4 v[4];
 };
 // Loads that the compiler keeps where they are written (volatile): a plain load
 // may be moved down to its first use, which would turn the prefetch into a stall.
-__device__ __forceinline__ uint4 ld_gather16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 32 bytes (rows of 256 or 512 bytes: aligned as the tensor is, at least to 16).
+__device__ __forceinline__ void ld_gather32(const uint8_t* p, uint4& lo, uint4& hi) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+                 : "l"(p));
+  } else {
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w) : "l"(p));
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w) : "l"(p + 16));
+  }
 }
 __device__ __forceinline__ uint2 ld_gather8(const void* p) {
   uint2 v;
@@ -177,7 +184,7 @@ __device__ __forceinline__ float ld_gather4f(const float* p) {
   asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
-// MXFP4 scales of a key: quarter qd loads bytes 8*qd .. +7 (the groups of slice qd)
+// MXFP4 scales of a key: quarter qd loads bytes 8*qd .. +7 (the groups of dims 128 qd ..)
 __device__ __forceinline__ uint2 load_scales(const AttnArgs& a, int32_t src, int qd) {
   return src >= 0 ? ld_gather8(a.kv_scales + (int64_t)src * (kD / 16) + 8 * qd) : make_uint2(0, 0);
 }
@@ -198,20 +205,20 @@ __device__ __forceinline__ bool fp8_row_key(int32_t src) {
   return src <= -2 || (kFp8 && src >= 0);
 }
 
-// Packed bytes of slice SL of a key for the thread's 32 dims.  MXFP4 entry:
-// 16 bytes, in v[SL] (all four slices are requested together).  FP8 row: 32
-// bytes, in v[2 (SL & 1)] and the next (slices 0 and 1 are requested together,
-// slices 2 and 3 reuse their registers once 0 and 1 are stored).
-template <int SL, bool kFp8, bool kTree>
-__device__ __forceinline__ void load_slice(const AttnArgs& a, int32_t src, int qd, KeyBytes& kb) {
+// Packed bytes of a key for the thread's 64 dims of half P (256 P ..).  MXFP4 entry: dims 64 qd .. +63, 32 bytes, in
+// v[2 P] and the next (both halves are requested together).  FP8 row: dims 32 qd .. +31 and 128 + 32 qd .. +31, in all
+// four (the second half reuses the registers once the first is stored).  Either way the quarters of a key read whole
+// 128-byte lines, half as many requests as 16 bytes a lane.
+template <int P, bool kFp8, bool kTree>
+__device__ __forceinline__ void load_half(const AttnArgs& a, int32_t src, int qd, KeyBytes& kb) {
   if (src == -1) return;
   if (fp8_row_key<kFp8>(src)) {
     const uint8_t* p = (src <= -2 ? window_codes<kTree>(a, -2 - (int64_t)src) : a.kv_codes + (int64_t)src * kD) +
-                       32 * qd + 128 * SL;
-    kb.v[2 * (SL & 1)] = ld_gather16(p);
-    kb.v[2 * (SL & 1) + 1] = ld_gather16(p + 16);
+                       256 * P + 32 * qd;
+    ld_gather32(p, kb.v[0], kb.v[1]);
+    ld_gather32(p + 128, kb.v[2], kb.v[3]);
   } else {
-    kb.v[SL] = ld_gather16(a.kv_codes + (int64_t)src * (kD / 2) + 16 * qd + 64 * SL);
+    ld_gather32(a.kv_codes + (int64_t)src * (kD / 2) + 128 * P + 32 * qd, kb.v[2 * P], kb.v[2 * P + 1]);
   }
 }
 // Dequantisation scale of an FP8 row (a window row, or a main-KV entry in the FP8
@@ -248,31 +255,34 @@ __device__ __forceinline__ void store_fp8_dims(uint4 c0, uint4 c1, float sc, uns
   }
 }
 
-// Dequantise the thread's 32 dims of slice SL into the K tile (4 core-matrix rows).
-template <int SL, bool kFp8>
-__device__ __forceinline__ void store_slice(const AttnArgs& a, const KeyBytes& kb, uint32_t sc_pair, int32_t src,
-                                            float wsc, int key, int qd, unsigned char* ktile) {
-  unsigned char* dst = ktile + (key >> 3) * 8192 + (16 * SL + 4 * qd) * 128 + (key & 7) * 16;
+// Dequantise the thread's 64 dims of half P into the K tile (8 core-matrix rows); scales: of its four groups of 16 dims.
+template <int P, bool kFp8>
+__device__ __forceinline__ void store_half(const KeyBytes& kb, uint32_t scales, int32_t src, float wsc, int key, int qd,
+                                           unsigned char* ktile) {
+  unsigned char* dst = ktile + (key >> 3) * 8192 + 32 * P * 128 + (key & 7) * 16;
   if (fp8_row_key<kFp8>(src)) {
-    store_fp8_dims(kb.v[2 * (SL & 1)], kb.v[2 * (SL & 1) + 1], wsc, dst);
-  } else if (src >= 0) {
-    const uint32_t s = e4m3x2_f16x2(sc_pair);
-    const uint32_t g0 = prmt(s, s, 0x1010u), g1 = prmt(s, s, 0x3232u);   // (scale, scale) of each group
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = word_of(kb.v[SL], j);
-      const uint32_t s2 = j < 2 ? g0 : g1;
-      uint4 o;
-      e2m1x8_f16x8(w, o.x, o.y, o.z, o.w);
-      o.x = hmul2(o.x, s2);   // exact: <= 6 significant bits
-      o.y = hmul2(o.y, s2);
-      o.z = hmul2(o.z, s2);
-      o.w = hmul2(o.w, s2);
-      *reinterpret_cast<uint4*>(dst + j * 128) = o;
-    }
+    store_fp8_dims(kb.v[0], kb.v[1], wsc, dst + 4 * qd * 128);
+    store_fp8_dims(kb.v[2], kb.v[3], wsc, dst + (16 + 4 * qd) * 128);
   } else {
+    dst += 8 * qd * 128;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + j * 128) = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t s = e4m3x2_f16x2(scales >> (16 * i) & 0xFFFFu);
+      const uint32_t g0 = prmt(s, s, 0x1010u), g1 = prmt(s, s, 0x3232u);   // (scale, scale) of each group
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (src >= 0) {
+          const uint32_t s2 = j < 2 ? g0 : g1;
+          e2m1x8_f16x8(word_of(kb.v[2 * P + i], j), o.x, o.y, o.z, o.w);
+          o.x = hmul2(o.x, s2);   // exact: <= 6 significant bits
+          o.y = hmul2(o.y, s2);
+          o.z = hmul2(o.z, s2);
+          o.w = hmul2(o.w, s2);
+        }
+        *reinterpret_cast<uint4*>(dst + (4 * i + j) * 128) = o;
+      }
+    }
   }
 }
 
@@ -365,7 +375,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   const int rank = (int)(blockIdx.x % n_split);
   const int b = (int)(row / a.Tq);
   const int hb = kHeads * (int)blockIdx.y;   // first head of this CTA's group of 64
-  // dequantisation: one key, 32 dims of each slice.  A warp holds 8 whole keys
+  // dequantisation: one key, 64 dims of each half.  A warp holds 8 whole keys
   // (coalesced loads); lanes 8q .. 8q+7 hold quarter q of the 8 keys, so each
   // 8-lane phase of a 16-byte store covers 8 distinct bank groups.
   const int key = ((warp & 15) << 3) | (lane & 7), qd = (lane >> 3) & 3;
@@ -382,7 +392,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     tc::mbar_init(&sm.bar_q, 1);
     tc::mbar_init(&sm.bar_s, 1);
     tc::mbar_init(&sm.p_ready, kWorkers / 32);
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.bar_pv[i], 1);
       tc::mbar_init(&sm.k_ready[i], kWorkers / 32);
     }
@@ -415,6 +425,14 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   float cur_wsc = 0.f;
   uint2 cur_sc = make_uint2(0, 0);
   KeyBytes kb;
+  auto load_first = [&] {   // the first chunk's packed bytes
+    load_half<0, kFp8, kTree>(a, cur_src, qd, kb);
+    if (!fp8_row_key<kFp8>(cur_src)) {
+      load_half<1, kFp8, kTree>(a, cur_src, qd, kb);
+      cur_sc = load_scales(a, cur_src, qd);
+    }
+    cur_wsc = load_wscale<kFp8, kTree>(a, cur_src);
+  };
   auto resolve = [&] {
     // ---- the selection (and the window rows) come from earlier kernels of the step
     pdl_wait();
@@ -443,32 +461,20 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     const int kb0 = 0, kb1 = n_mine;
     n_my = (kb1 - kb0 + kChunk - 1) / kChunk;   // chunks of kChunk keys, <= kMaxChunks
 
-    // ---- key sources.  Every worker resolves its key in the first chunk; the
-    // key's later chunks are shared out among its four threads.
+    // ---- key sources: a key's chunks are shared out among its four threads, the first four chunks before the first
+    // chunk's packed bytes are requested
     if (!mma_warp && n_my > 0) {
-      cur_src = key_source<kTree>(a, row, b, kb0 + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, ctx, qd == 0, status);
-      if (qd == 0) {
-        sm.slot[key] = cur_src;
-        sm.kexp[key] = (int8_t)key_exp<kFp8, kTree>(a, cur_src);
-      }
-      for (int c = qd + 1; c < n_my; c += 4) {
-        const int32_t src =
-            key_source<kTree>(a, row, b, kb0 + c * kChunk + key, n_sel, sel_off, sel_cap, kb1, nv, w_first, pos0, ctx, true,
-                              status);
+      auto resolve_chunk = [&](int c) {
+        const int32_t src = key_source<kTree>(a, row, b, kb0 + c * kChunk + key, n_sel, sel_off, sel_cap, kb1, nv, w_first,
+                                              pos0, ctx, true, status);
         sm.slot[c * kChunk + key] = src;
         sm.kexp[c * kChunk + key] = (int8_t)key_exp<kFp8, kTree>(a, src);
-      }
-    }
-    // ---- the first chunk's packed bytes
-    if (!mma_warp && n_my > 0) {
-      load_slice<0, kFp8, kTree>(a, cur_src, qd, kb);
-      load_slice<1, kFp8, kTree>(a, cur_src, qd, kb);
-      if (!fp8_row_key<kFp8>(cur_src)) {
-        load_slice<2, kFp8, kTree>(a, cur_src, qd, kb);
-        load_slice<3, kFp8, kTree>(a, cur_src, qd, kb);
-        cur_sc = load_scales(a, cur_src, qd);
-      }
-      cur_wsc = load_wscale<kFp8, kTree>(a, cur_src);
+        return src;
+      };
+      const int32_t src = qd < n_my ? resolve_chunk(qd) : -1;
+      cur_src = __shfl_sync(0xffffffffu, src, lane & 7);
+      load_first();
+      for (int c = qd + 4; c < n_my; c += 4) resolve_chunk(c);
     }
   };
   // The keys' chain of loads (index, page, bytes) runs while Q is on its way.  A cluster of the layer step does the
@@ -552,12 +558,12 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     for (int it = 0; it < n_my; ++it) {
       bool ok = true;
 #pragma unroll
-      for (int sl = 0; sl < 4; ++sl) {
+      for (int sl = 0; sl < 2; ++sl) {
         ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.k_ready[sl], it & 1, 1u << 22));
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
-        for (int ks = 8 * sl; ks < 8 * sl + 8; ++ks)   // descriptor addresses advance in 16-byte units
+        for (int ks = 16 * sl; ks < 16 * sl + 16; ++ks)   // descriptor addresses advance in 16-byte units
           tc::mma_f16_by(leader, tm + kColS, dk_s + (uint64_t)(ks * 16), dq_s + (uint64_t)(ks * 16), kIdS, ks > 0);
       }
       if (!ok) { *abort = 1; break; }
@@ -567,13 +573,13 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
       // PV over the chunk's keys only (a short last chunk skips its empty 16-key steps)
       const int ksteps = (min(kChunk, n_mine - kChunk * it) + 15) / 16;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {   // tile by tile: a finished tile frees its K slice for the next chunk
+      for (int mt = 0; mt < 4; ++mt) {   // tile by tile: two finished ones free their half of the K tile for the next chunk
 #pragma unroll
         for (int kk = 0; kk < kChunk / 16; ++kk)
           if (kk < ksteps)
             tc::mma_f16_by(leader, tm + kColO + 64 * mt, dk_o + (uint64_t)(mt * 128 + kk * 1024), dp_o + (uint64_t)(kk * 128),
                            kIdO, (it > 0 || kk > 0) ? 1u : 0u);
-        tc::mma_commit_by(leader, &sm.bar_pv[mt]);
+        if (mt & 1) tc::mma_commit_by(leader, &sm.bar_pv[mt >> 1]);
       }
     }
     __syncwarp();
@@ -589,35 +595,28 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     for (int it = 0; it < n_my; ++it) {
       const int32_t nxt_src = it + 1 < n_my ? sm.slot[(it + 1) * kChunk + key] : -1;
       bool wok = true;
-      // ---- dequantise slice by slice; refill each slice's registers with the next chunk
-#define CSA2_SLICE(SL)                                                                   \
+      // ---- dequantise in two halves of the dims
+#define CSA2_HALF(P)                                                                     \
   {                                                                                      \
-    if (it > 0) wok = wok && warp_wait(&sm.bar_pv[SL], (it - 1) & 1, abort);             \
-    {                                                                                    \
-      /* the slice's two group scales were loaded by quarter SL of the key */            \
-      const uint32_t w0 = __shfl_sync(0xffffffffu, cur_sc.x, (lane & 7) | (SL << 3));    \
-      const uint32_t w1 = __shfl_sync(0xffffffffu, cur_sc.y, (lane & 7) | (SL << 3));    \
-      const uint32_t pr = ((qd >> 1) ? w1 : w0) >> (16 * (qd & 1));                      \
-      if (wok) store_slice<SL, kFp8>(a, kb, pr & 0xFFFFu, cur_src, cur_wsc, key, qd, ktile); \
-      /* FP8 rows: slices 2 and 3 of this chunk reuse the registers of 0 and 1 */        \
-      if (SL < 2 && fp8_row_key<kFp8>(cur_src)) load_slice<(SL + 2) & 3, kFp8, kTree>(a, cur_src, qd, kb); \
-    }                                                                                    \
+    if (it > 0) wok = wok && warp_wait(&sm.bar_pv[P], (it - 1) & 1, abort);              \
+    /* the four group scales of the thread's 64 dims were loaded by quarter 2 P + qd / 2 of the key */ \
+    const uint32_t w0 = __shfl_sync(0xffffffffu, cur_sc.x, (lane & 7) | ((2 * P + (qd >> 1)) << 3)); \
+    const uint32_t w1 = __shfl_sync(0xffffffffu, cur_sc.y, (lane & 7) | ((2 * P + (qd >> 1)) << 3)); \
+    if (wok) store_half<P, kFp8>(kb, (qd & 1) ? w1 : w0, cur_src, cur_wsc, key, qd, ktile); \
+    /* FP8 rows: the second half reuses the registers of the first */                    \
+    if (P == 0 && fp8_row_key<kFp8>(cur_src)) load_half<1, kFp8, kTree>(a, cur_src, qd, kb); \
     tc::fence_async_smem();                                                              \
     __syncwarp();                                                                        \
-    if (lane == 0) tc::mbar_arrive(&sm.k_ready[SL]);                                     \
+    if (lane == 0) tc::mbar_arrive(&sm.k_ready[P]);                                      \
   }
-      CSA2_SLICE(0)
-      CSA2_SLICE(1)
-      CSA2_SLICE(2)
-      CSA2_SLICE(3)
-#undef CSA2_SLICE
+      CSA2_HALF(0)
+      CSA2_HALF(1)
+#undef CSA2_HALF
       // the next chunk's bytes, requested together once this chunk's tile is written
       if (it + 1 < n_my) {
-        load_slice<0, kFp8, kTree>(a, nxt_src, qd, kb);
-        load_slice<1, kFp8, kTree>(a, nxt_src, qd, kb);
+        load_half<0, kFp8, kTree>(a, nxt_src, qd, kb);
         if (!fp8_row_key<kFp8>(nxt_src)) {
-          load_slice<2, kFp8, kTree>(a, nxt_src, qd, kb);
-          load_slice<3, kFp8, kTree>(a, nxt_src, qd, kb);
+          load_half<1, kFp8, kTree>(a, nxt_src, qd, kb);
         }
       }
       const bool valid = sm.slot[it * kChunk + kc] != -1;   // the softmax thread's key
@@ -711,12 +710,12 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.p_ready);
     }
-    // all PV products of the CTA are complete once the last commit has arrived
-    if (!*abort && n_my > 0) warp_wait(&sm.bar_pv[3], (n_my - 1) & 1, abort);
-    tc::tc_fence_after();
     // row sums over the 128 keys: warp, then lane quarters
     const float s = reduce16<false>(lsum, lane);
     if (lane < 16) sm.red[q4][16 * hg + lane] = s;
+    // all PV products of the CTA are complete once the last commit has arrived
+    if (!*abort && n_my > 0) warp_wait(&sm.bar_pv[1], (n_my - 1) & 1, abort);
+    tc::tc_fence_after();
   }
   __syncthreads();
   const bool ok = *abort == 0;
