@@ -878,6 +878,9 @@ int csa2_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, int64_t x_
   REQUIRE(std::isfinite(amplitude), "amplitude must be finite");
   REQUIRE(x_token_stride >= 0 && x_head_stride >= 0, "strides of x must be >= 0");
   REQUIRE((n_tokens <= 1 || y_token_stride >= d) && (heads <= 1 || y_head_stride >= d), "strides of y must be at least d");
+  if (n_tokens > 1 && heads > 1)
+    REQUIRE((__int128)y_token_stride >= (__int128)(heads - 1) * y_head_stride + d || (__int128)y_head_stride >= (__int128)(n_tokens - 1) * y_token_stride + d,
+            "rows of y must not overlap");
   if (n_tokens == 0 || heads == 0) return CSA2_OK;
   REQUIRE(x && y, "x and y must not be NULL");
   REQUIRE(reinterpret_cast<uintptr_t>(x) % (x_dtype == CSA2_F32 ? 4 : 2) == 0 && reinterpret_cast<uintptr_t>(y) % (y_dtype == CSA2_F32 ? 4 : 2) == 0,

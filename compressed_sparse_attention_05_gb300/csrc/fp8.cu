@@ -173,7 +173,7 @@ __device__ __forceinline__ void commit_fp8_mc(uint32_t leader, uint64_t* bar, ui
       "h"(mask), "r"(leader)
       : "memory");
 }
-// The MMA warp's wait for up to three barriers with one look at a time: lane i looks at its own (bar, parity); `need`
+// The MMA warp's wait for two barriers with one look at a time: lane i looks at its own (bar, parity); `need`
 // has the bits of the lanes that count.  Never suspends; bounded.
 __device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, uint32_t need, volatile int* abort) {
 #pragma unroll 1

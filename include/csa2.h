@@ -503,7 +503,7 @@ int csa2_rope_table(const csa2_rope_spec* spec, int32_t r, uint64_t* table, void
  * given strides in elements, channels contiguous; fastest where rows are 16-byte
  * aligned and 8 divides d (HALF: start and r / 2 too).  y may be x (same
  * type and strides: only the rotated channels are touched); otherwise they must not
- * overlap.  positions int32 [n_tokens] (negative ones turn backwards).  inverse != 0
+ * overlap, and no two rows of y either.  positions int32 [n_tokens] (negative ones turn backwards).  inverse != 0
  * turns by -p: back, and also the gradient (the transpose) of the rotation. */
 int csa2_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, int64_t x_head_stride, void* y,
               int32_t y_dtype, int64_t y_token_stride, int64_t y_head_stride, int64_t n_tokens,

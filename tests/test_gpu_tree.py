@@ -343,3 +343,26 @@ def test_same_bits_and_replayed():
     graph.replay()
     assert status() == 0
     c.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[700, 90], [300 + b for b in range(40)]])
+def test_rows_that_start_on_16_bytes_only(lens, fp8):
+    """Codes 16 bytes behind a 32-byte boundary give the same bits."""
+    c = Case(23, lens=lens, T=5, K=256, fp8=fp8, Hq=8).upload()
+    c.run()
+    first, lse = c.O.clone(), c.lse.clone()
+    moved = {}
+    for k in ("codes", "wc", "nc"):
+        t = c.t[k].view(-1)
+        buffer = torch.full((t.numel() + 48,), 0x55, dtype=torch.uint8, device="cuda")
+        at = (16 - buffer.data_ptr()) % 32
+        moved[k] = buffer[at:at + t.numel()]
+        moved[k].copy_(t)
+        assert moved[k].data_ptr() % 32 == 16
+        c.t[k].fill_(0)
+    c.cache.kv_codes, c.window.codes, c.tree.codes = (moved[k].data_ptr() for k in ("codes", "wc", "nc"))
+    c.O.fill_(0)
+    c.run()
+    assert status() == 0
+    assert torch.equal(first, c.O) and torch.equal(lse, c.lse)

@@ -121,6 +121,8 @@ def test_rope(lib):
                 dict(amp=math.inf), dict(xts=-1), dict(xhs=-64), dict(yts=63), dict(yhs=63), dict(x=None), dict(y=None), dict(x=FAKE + 1),
                 dict(yt=0, y=FAKE + 2), dict(pos=None), dict(pos=FAKE + 2), dict(table=None), dict(table=FAKE + 4)):
         assert call(**bad) == 1, bad
+    for bad in (dict(yts=64), dict(yts=127), dict(heads=3), dict(yts=64, yhs=255), dict(yts=1 << 62, yhs=1 << 62, n=(1 << 31) - 1, heads=65535)):
+        assert call(**bad) == 1 and "overlap" in err(), bad                   # tokens and heads that share rows of y
     for bad in (dict(xts=256), dict(xhs=128, xts=256, yhs=64), dict(yt=0)):   # in place, but not the same layout or type
         assert call(**{**bad, "y": FAKE}) == 1 and "in place" in err()
     assert call(n=0, x=None) == 0 and call(heads=0, y=None) == 0
