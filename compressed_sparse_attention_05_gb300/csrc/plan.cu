@@ -8,7 +8,8 @@
 // pages; the k-th page handed out is S[n_free + R - 1 - k], so every page of the result follows from the sums alone
 // and no thread waits for another's pop.  k_page_plan (one block) makes the sums; the columns (slots, positions,
 // page-table entries) are written by the same block where they are few and by k_page_fill where they are many.
-// Bound: latency of a chain of dependent loads in the small case, the bytes written in the large one.
+// Bound: latency of a chain of dependent loads in the small case (32 sequences of 8 tokens: 5.7 us), the bytes written in
+// the large one (160 sequences of up to 32,768 tokens, 31.5 MB of columns: 10.4 us, of which the sums are 5).
 #include <algorithm>
 
 #include "common.cuh"
@@ -110,16 +111,16 @@ __device__ __forceinline__ void push_released(const PagePlanArgs& a, const PageH
   }
 }
 
-// fill_here: the columns too (then the rows stay in shared memory, as far as they fit).
-constexpr int kSharedRows = 256;
+// fill_here: the columns too (then the rows stay in shared memory).
+constexpr int kFillSeqs = 64;
 __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PagePlanArgs a, PageHead* head, PageRow* rows, int fill_here, uint32_t* status) {
   __shared__ int64_t s_sums[2][32];
   __shared__ PageHead s_head;
-  __shared__ PageRow s_rows[kSharedRows];
+  __shared__ PageRow s_rows[kFillSeqs];
   if (!fill_here) pdl_trigger();   // k_page_fill waits for this kernel; what follows it must not start before both are done
   pdl_wait();
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
-  if (fill_here && a.B <= kSharedRows) rows = s_rows;
+  if (fill_here) rows = s_rows;      // (at most kFillSeqs sequences)
   // one sequence's counts, or a change of nothing where its state is impossible
   auto read = [&](int b, bool report) {
     PageRow r;
@@ -230,7 +231,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PagePlanArgs a, Page
   push_released(a, h, rows, tid, threads, status);
 }
 
-constexpr int kFillThreads = 256, kFillPer = 16;   // threads of a block, columns of a thread
+// Threads of a block, columns of a thread (16 x 8,192 and 160 x 32,768 columns: with 4 columns 5.9 and 17.4 us, 8 6.3 and
+// 12.4, 16 6.6 and 10.4, 32 7.6 and 11.1).
+constexpr int kFillThreads = 256, kFillPer = 16;
 
 __global__ void __launch_bounds__(kFillThreads) k_page_fill(PagePlanArgs a, const PageHead* head, const PageRow* rows, uint32_t* status) {
   pdl_wait();
@@ -290,14 +293,17 @@ size_t head_bytes() { return 256; }
 
 size_t page_plan_workspace_bytes(int B) { return head_bytes() + (size_t)B * sizeof(PageRow); }
 
-// Columns that one block writes itself: the second launch costs about as long as they take.
-constexpr int64_t kFillHere = 16384;
+// One block writes the columns itself up to kFillSeqs sequences and kFillHere columns of all together: that saves the
+// second launch, 2 us of the host's time, where it takes about as long (one launch, two launches, in us on the GPU:
+// 8 x 8 3.3 and 4.7, 32 x 8 5.7 and 5.5, 64 x 8 6.6 and 5.9, 4 x 1,024 4.7 and 4.1).  Beyond that the block is the slower
+// one: 32 x 512 7.0 and 5.4, 128 x 8 10.0 and 7.0, 256 x 64 16.8 and 7.6, 600 x 8 35.1 and 10.2.
+constexpr int64_t kFillHere = 4096;
 
 cudaError_t launch_page_plan(const PagePlanArgs& a, void* ws, cudaStream_t s) {
   PageHead* head = static_cast<PageHead*>(ws);
   PageRow* rows = reinterpret_cast<PageRow*>(static_cast<char*>(ws) + head_bytes());
   const int64_t cols = std::max<int64_t>(std::max<int64_t>(a.q_pos ? a.Tq : 0, a.slots ? a.max_new : 0), 1);
-  const bool here = cols * a.B <= kFillHere;
+  const bool here = a.B <= kFillSeqs && cols * a.B <= kFillHere;
   // as many threads as there are sequences, and for the columns up to eight warps to a sequence
   const int64_t warps = (a.B + 31) / 32, want = here ? std::max<int64_t>(warps, a.B * std::min<int64_t>((cols + 63) / 64, 8)) : warps;
   const int threads = (int)std::min<int64_t>(kPlanThreads / 32, want) * 32;
