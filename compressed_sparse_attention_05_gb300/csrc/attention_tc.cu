@@ -383,9 +383,12 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   volatile int* abort = &sm.abort;
 
   pdl_trigger();
+  if (kTree) pdl_wait();
   // ---- before the previous kernel of the step is done: the token's own inputs
-  // (scalars, Q rows), barriers, tensor memory and the Q operand
+  // (scalars, Q rows), barriers, tensor memory and the Q operand (a tree's positions come from its plan, which lets
+  // nothing start before it is done)
   const int t = kTree ? max(a.q_pos[row], -1) : a.q_pos[row];   // (-1: no node of the tree)
+  int n_sel = kTree ? a.cnt[row] : 0;
   const int n_ent = a.n_entries[b];
   const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
   if (tid == 0) {
@@ -420,7 +423,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     w_hi = t;
   }
   const int n_win = max(0, w_hi - w_lo + 1);
-  int n_sel = 0, n_mine = 0, n_my = 0;
+  int n_mine = 0, n_my = 0;
   int32_t cur_src = -1;
   float cur_wsc = 0.f;
   uint2 cur_sc = make_uint2(0, 0);
@@ -435,8 +438,12 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   };
   auto resolve = [&] {
     // ---- the selection (and the window rows) come from earlier kernels of the step
-    pdl_wait();
-    n_sel = kTree && t < 0 ? 0 : a.cnt[row];
+    if (!kTree) {
+      pdl_wait();
+      n_sel = a.cnt[row];
+    } else if (t < 0) {
+      n_sel = 0;
+    }
     const int nv = n_visible(n_ent, t);
     if (n_sel < 0 || n_sel > a.K) {
       if (tid == 0 && rank == 0) raise_status(status, CSA2_STATUS_BAD_COUNT);
@@ -445,16 +452,25 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     // the key list.  One CTA per token: its n_sel selected entries, then its window
     // rows.  A cluster: rank r takes an equal share of the K selection slots (unused
     // ones empty, so that the index loads need not wait for the count) and an equal
-    // share of the window rows.
+    // share of the window rows.  With a tree the count is there as early as the
+    // position, and rank r takes an equal share of the keys that there are: none has a
+    // chunk more than it must (640 keys over five ranks are 128 for each, where two
+    // shares rounded by themselves are 129 for one), and short contexts no empty ones.
     int sel_off = 0, sel_cap = n_sel, w_first = w_lo;
     n_mine = n_sel + n_win;
     if (n_split > 1) {
-      sel_off = (int)((int64_t)a.K * rank / n_split);
-      sel_cap = (int)((int64_t)a.K * (rank + 1) / n_split) - sel_off;
-      // (a tree's window bounds round up where the selection's round down, so that K + W = 640 keys over five ranks are
-      // 128 for each of them, one chunk, and not 129 for one)
-      const int up = kTree ? n_split - 1 : 0;
-      const int u0 = (int)(((int64_t)n_win * rank + up) / n_split), u1 = (int)(((int64_t)n_win * (rank + 1) + up) / n_split);
+      auto cut = [&](int r, int* win) {   // the first selected entry and window row of rank r
+        const int sel = (int)((int64_t)(kTree ? n_sel : a.K) * r / n_split);
+        *win = (int)((int64_t)n_win * r / n_split);
+        if (!kTree) return sel;
+        const int all = (int)((int64_t)(n_sel + n_win) * r / n_split);
+        const int mine = n_win >= n_split ? sel : min(all, n_sel);   // (so that the rest never goes back)
+        *win = all - mine;
+        return mine;
+      };
+      int u0, u1;
+      sel_off = cut(rank, &u0);
+      sel_cap = cut(rank + 1, &u1) - sel_off;
       w_first = w_lo + u0;
       n_mine = sel_cap + (u1 - u0);
     }

@@ -8,8 +8,8 @@
 // pages; the k-th page handed out is S[n_free + R - 1 - k], so every page of the result follows from the sums alone
 // and no thread waits for another's pop.  k_page_plan (one block) makes the sums; the columns (slots, positions,
 // page-table entries) are written by the same block where they are few and by k_page_fill where they are many.
-// Bound: latency of a chain of dependent loads in the small case (32 sequences of 8 tokens: 5.7 us), the bytes written in
-// the large one (160 sequences of up to 32,768 tokens, 31.5 MB of columns: 10.4 us, of which the sums are 5).
+// Bound: latency of a chain of dependent loads in the small case (32 sequences of 8 tokens: 5.1 us), the bytes written in
+// the large one (160 sequences of up to 32,768 tokens, 31.5 MB of columns: 8.0 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -54,10 +54,11 @@ __device__ __forceinline__ int32_t stack_page(const PagePlanArgs& a, const PageH
   return a.page_table[(int64_t)lo * a.max_pages + r.need + (j - r.back)];
 }
 
-// What thread `t` of `threads` writes of sequence b: new places in the table, positions, slots.  A warp takes the slots of
-// a page, which is looked up once for all of them.
+// What thread `t` of `threads` (at most 2^24) writes of sequence b: new places in the table, positions, slots.  A warp takes
+// the slots of a page, which is looked up once for all of them.  Columns are below 2^31 and entries below 2^29, so that
+// their sums fit 32 bits without a sign; with 64 the fill's instructions took longer than its bytes.
 __device__ __forceinline__ void fill_row(const PagePlanArgs& a, const PageHead& h, const PageRow* rows, const PageRow& r, int b,
-                                         int64_t t, int64_t threads, uint32_t* status) {
+                                         uint32_t t, uint32_t threads, uint32_t* status) {
   auto new_page = [&](int p) { return stack_page(a, h, rows, (int64_t)h.n_free + h.released - 1 - (r.take + (p - r.held))); };
   int32_t* table = a.page_table + (int64_t)b * a.max_pages;
   for (int64_t k = t; k < (int64_t)r.need - r.held; k += threads) {
@@ -67,35 +68,34 @@ __device__ __forceinline__ void fill_row(const PagePlanArgs& a, const PageHead& 
   }
   if (a.q_pos) {
     int32_t* out = a.q_pos + (int64_t)b * a.Tq;
-    auto at = [&](int64_t i) { return i < r.n_new ? r.len + (int32_t)i : -1; };
+    const uint32_t cols = (uint32_t)a.Tq, n = (uint32_t)r.n_new;
+    auto at = [&](uint32_t i) { return i < n ? r.len + (int32_t)i : -1; };
     if (a.q_pos4) {        // four at a time: rows start on 16 bytes
-      for (int64_t i = 4 * t; i < a.Tq; i += 4 * threads)
+      for (uint32_t i = 4 * t; i < cols; i += 4 * threads)
         *reinterpret_cast<int4*>(out + i) = make_int4(at(i), at(i + 1), at(i + 2), at(i + 3));
     } else {
-      for (int64_t i = t; i < a.Tq; i += threads) out[i] = at(i);
+      for (uint32_t i = t; i < cols; i += threads) out[i] = at(i);
     }
   }
   if (a.slots) {
     int64_t* out = a.slots + (int64_t)b * a.max_new;
-    const int lane = threadIdx.x & 31;
-    const int p0 = r.e0 >> 6;                                // column i is place (e0 + i) % 64 of page p0 + ...
-    const int64_t groups = ((r.e0 & (kPage - 1)) + (int64_t)a.max_new + kPage - 1) / kPage;
-    for (int64_t g = t >> 5; g < groups; g += threads >> 5) {
-      const int64_t p = p0 + g;
+    const uint32_t lane = threadIdx.x & 31, cols = (uint32_t)a.max_new, e0 = (uint32_t)r.e0, e1 = (uint32_t)r.e1;
+    const uint32_t p0 = e0 / kPage, groups = (e0 % kPage + cols + kPage - 1) / kPage;   // column i is place (e0 + i) % 64
+    for (uint32_t g = t >> 5; g < groups; g += threads >> 5) {
+      const uint32_t p = p0 + g, e = p * kPage + lane;
       int32_t page = -1;
-      if (r.e1 > r.e0 && p * kPage < r.e1) {                 // (so p is below `need`)
+      if (e1 > e0 && p * kPage < e1) {                       // (so p is below `need`)
         // (a page behind `held` may not be in the table yet: another thread writes it)
-        page = p < r.held ? table[p] : new_page((int)p);
+        page = (int32_t)p < r.held ? table[p] : new_page((int)p);
         if (page < 0 || page >= a.n_pages) {
           if (lane == 0) raise_status(status, CSA2_STATUS_BAD_PAGE);
           page = -1;
         }
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int place = lane + 32 * u;
-        const int64_t e = p * kPage + place, i = e - r.e0;
-        if (i >= 0 && i < a.max_new) out[i] = page >= 0 && e < r.e1 ? (int64_t)page * kPage + place : -1;
+      for (uint32_t u = 0; u < kPage; u += 32) {
+        const uint32_t i = e + u - e0;                       // (before e0 it wraps past every column)
+        if (i < cols) out[i] = page >= 0 && e + u < e1 ? (int64_t)page * kPage + lane + u : -1;
       }
     }
   }
@@ -231,16 +231,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PagePlanArgs a, Page
   push_released(a, h, rows, tid, threads, status);
 }
 
-// Threads of a block, columns of a thread (16 x 8,192 and 160 x 32,768 columns: with 4 columns 5.9 and 17.4 us, 8 6.3 and
-// 12.4, 16 6.6 and 10.4, 32 7.6 and 11.1).
-constexpr int kFillThreads = 256, kFillPer = 16;
+// Threads of a block, columns of a thread (16 x 8,192 and 160 x 32,768 columns: with 8 columns 5.7 and 8.0 us, 16 6.4 and
+// 9.6, 32 6.8 and 10.2).
+constexpr int kFillThreads = 256, kFillPer = 8;
 
 __global__ void __launch_bounds__(kFillThreads) k_page_fill(PagePlanArgs a, const PageHead* head, const PageRow* rows, uint32_t* status) {
   pdl_wait();
   const PageHead h = *head;
-  const int64_t t = (int64_t)blockIdx.x * kFillThreads + threadIdx.x, threads = (int64_t)gridDim.x * kFillThreads;
+  const uint32_t t = blockIdx.x * kFillThreads + threadIdx.x, threads = gridDim.x * kFillThreads;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) fill_row(a, h, rows, rows[b], b, t, threads, status);
-  push_released(a, h, rows, t + threads * blockIdx.y, threads * gridDim.y, status);
+  push_released(a, h, rows, t + (int64_t)threads * blockIdx.y, (int64_t)threads * gridDim.y, status);
 }
 
 // ---- a tree of drafted tokens -----------------------------------------------------------------

@@ -218,6 +218,17 @@ def test_attention(kw):
     c.check()
 
 
+@pytest.mark.parametrize("kw", [dict(lens=[15, 200], T=2, K=2048, W=5), dict(lens=[700], T=3, K=1024, W=3), dict(lens=[2000, 0], T=1, K=2048, W=9),
+                                dict(lens=[512], T=8, K=512), dict(lens=[511], T=4, K=512), dict(lens=[900, 33], T=5, K=1000, W=100, few=True),
+                                dict(lens=[600], T=2, K=600, W=1, fp8=True)])
+def test_shares_of_a_split_token(kw):
+    """Few tokens: the keys that are there go over several CTAs, whatever K and W would allow."""
+    c = Case(24, **kw).upload()
+    c.run()
+    assert status() == 0
+    c.check()
+
+
 @pytest.mark.parametrize("kw", [dict(lens=[300, 20], T=9, K=64, Hq=7), dict(lens=[60], T=20, K=16, W=5, Hq=4, chain=True),
                                 dict(lens=[100, 3], T=6, W=64, cap=40, late=-10, K=64, Hq=17), dict(lens=[90], T=6, K=20, W=0),
                                 dict(lens=[90, 4], T=6, K=20, cap=0, live=[6, 2]), dict(lens=[90], T=6, K=20, big=True)])
