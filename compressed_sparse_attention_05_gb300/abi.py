@@ -151,6 +151,7 @@ SIGNATURES = {
 
 _lib = None
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def lib():
@@ -187,7 +188,7 @@ def stream_handle(stream: Optional[torch.cuda.Stream] = None):
     if stream is not None:
         return stream.cuda_stream
     # the current stream's handle alone: making a Stream object takes longer than launching a kernel (3.0 us)
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_current_device())
 
 
 def bits16(t: torch.Tensor) -> torch.Tensor:

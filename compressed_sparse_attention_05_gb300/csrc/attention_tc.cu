@@ -295,19 +295,19 @@ __device__ __forceinline__ void store_half(const KeyBytes& kb, uint32_t scales, 
 // position `ctx` on (and the window's rows end there).
 template <bool kTree>
 __device__ __forceinline__ int32_t key_source(const AttnArgs& a, int64_t row, int b, int kk, int n_sel, int sel_off,
-                                              int sel_cap, int kk_end, int nv, int w_first, int pos0, int ctx, bool report,
+                                              int sel_cap, int kk_end, int nv, int w_first, int pos0, int ctx,
                                               uint32_t* status) {
   if (kk >= kk_end) return -1;
   if (kk < sel_cap) {
     const int j = __ldg(a.idx + row * a.K + sel_off + kk);
     if (sel_off + kk >= n_sel) return -1;
     if (j < 0 || j >= nv || (j >> 6) >= a.max_pages) {
-      if (report) raise_status(status, CSA2_STATUS_BAD_INDEX);
+      raise_status(status, CSA2_STATUS_BAD_INDEX);
       return -1;
     }
     const int p = __ldg(a.page_table + (int64_t)b * a.max_pages + (j >> 6));
     if (p < 0 || p >= a.n_pages) {
-      if (report) raise_status(status, CSA2_STATUS_BAD_PAGE);
+      raise_status(status, CSA2_STATUS_BAD_PAGE);
       return -1;
     }
     return p * kPage + (j & (kPage - 1));
@@ -316,7 +316,7 @@ __device__ __forceinline__ int32_t key_source(const AttnArgs& a, int64_t row, in
   if (kTree && p >= ctx) {
     const int node = p - ctx < a.max_depth ? __ldg(a.path + row * a.max_depth + (p - ctx)) : -1;
     if (node < 0 || node >= a.Tq) {
-      if (report) raise_status(status, CSA2_STATUS_BAD_INDEX);
+      raise_status(status, CSA2_STATUS_BAD_INDEX);
       return -1;
     }
     return (int32_t)(-2 - ((int64_t)a.B * a.swa_cap + (int64_t)b * a.Tq + node));
@@ -361,8 +361,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   if (!ok) *abort = 1;
   return ok;
 }
-
-
 
 template <bool kFp8, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -474,15 +472,14 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
       w_first = w_lo + u0;
       n_mine = sel_cap + (u1 - u0);
     }
-    const int kb0 = 0, kb1 = n_mine;
-    n_my = (kb1 - kb0 + kChunk - 1) / kChunk;   // chunks of kChunk keys, <= kMaxChunks
+    n_my = (n_mine + kChunk - 1) / kChunk;   // chunks of kChunk keys, <= kMaxChunks
 
     // ---- key sources: a key's chunks are shared out among its four threads, the first four chunks before the first
     // chunk's packed bytes are requested
     if (!mma_warp && n_my > 0) {
       auto resolve_chunk = [&](int c) {
-        const int32_t src = key_source<kTree>(a, row, b, kb0 + c * kChunk + key, n_sel, sel_off, sel_cap, kb1, nv, w_first,
-                                              pos0, ctx, true, status);
+        const int32_t src = key_source<kTree>(a, row, b, c * kChunk + key, n_sel, sel_off, sel_cap, n_mine, nv, w_first, pos0, ctx,
+                                              status);
         sm.slot[c * kChunk + key] = src;
         sm.kexp[c * kChunk + key] = (int8_t)key_exp<kFp8, kTree>(a, src);
         return src;
@@ -509,9 +506,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
       const int h = 8 * r + (lane & 7);
       qv[r] = here && hb + h < a.Hq ? *reinterpret_cast<const uint4*>(sm.k + h * kD + c8 * 8) : make_uint4(0, 0, 0, 0);
     }
-  }
-  // largest bf16 exponent field of each head (lanes L, L^8, L^16, L^24 share a head), of heads r and r + 32 at once
-  if (!mma_warp) {
+    // largest bf16 exponent field of each head (lanes L, L^8, L^16, L^24 share a head), of heads h and h + 32 at once
     uint32_t e[4];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
