@@ -632,8 +632,9 @@ k_matmul_fp8_thin(const __grid_constant__ CUtensorMap amap, const __grid_constan
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
           if (lane + 32 * h < kOwn) shared[lane + 32 * h] = i == 0 ? sc[h].x : i == 1 ? sc[h].y : i == 2 ? sc[h].z : sc[h].w;
+        __syncwarp();
         const uint32_t buf = n % kTBufs;
-        ok = __all_sync(0xffffffffu, wait_bar(&sm.acc_full[buf], (n / kTBufs) & 1, abort));   // (and the scales are there)
+        ok = __all_sync(0xffffffffu, wait_bar(&sm.acc_full[buf], (n / kTBufs) & 1, abort));
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
