@@ -5,9 +5,10 @@
 // accumulation) into a tensor-memory accumulator of their own; the accumulator is then read back, multiplied by the
 // block's two scales and added to the sum in registers, while the tensor cores work on the next block's.
 //
-// k_matmul_fp8_wide (many rows of A): tiles of 128 rows of A x 256 rows of B.  A row of A is a lane of the accumulator,
-//   so a thread has one scale per block: sa[its row] sb[its 128 columns].  Two CTAs with tiles above one another copy B's
-//   rows for each other (32 KB out of L2 for each instead of 48).
+// k_matmul_fp8_wide (many rows of A, or more rows of B than the SMs take 128 at a time): tiles of 128 rows of A x 256 rows
+//   of B.  A row of A is a lane of the accumulator, so a thread has one scale per block: sa[its row] sb[its 128 columns].
+//   In long products two CTAs with tiles above one another copy B's rows for each other (32 KB out of L2 for each instead
+//   of 48).
 //   4,096 x 32,768 x 4,096 takes 417 us (2.6 PFLOP/s) from a cool start and 447 (2.5) in a row, at the card's 1,400 W:
 //   the power cap holds the clock at 1.88 GHz, and operands of zeros take 405.  Below that: a block's MMAs run 513 cycles,
 //   and the way MMA -> sums (200 cycles after the last product) -> accumulator read (300) -> next MMAs (200) about as long
@@ -18,7 +19,7 @@
 // k_matmul_fp8_thin (few rows of A, or few tiles): the rows of B, the weights, are the MMA's M side, 128 at a time, and
 //   16 to 128 rows of A its N side, so that no part of the tensor cores' work and of shared memory goes to rows that are
 //   not there, and 128 B-rows x 128 columns (16 KB) per block stream through a deep ring.  A thread has a weight row and
-//   up to 64 rows of A; their scales go through shared memory.  32 x 32,768 x 4,096: 24.8 us, 5.5 TB/s.
+//   up to 32 rows of A; their scales go through shared memory.  32 x 32,768 x 4,096: 24.8 us, 5.5 TB/s.
 //   Where its tiles do not fill the SMs, the blocks of K are split over several CTAs, which leave fp32 partial sums that
 //   k_matmul_fp8_sum adds in order.
 #include <algorithm>
@@ -149,6 +150,7 @@ struct MatmulPlan {
   float* partial;           // [n_split][M][ld]
   int64_t ld;
   int M, N, kb, n_split, f32;
+  int ctas;                 // of a cluster (wide)
   int c_map;                // C's rows start on 16 bytes: it is written by tensor-map copies
   int m_tiles, n_tiles;
 };
@@ -268,7 +270,7 @@ __device__ __forceinline__ void ring_init(Smem& sm, int stages, int bufs, uint32
 }
 
 // ---- many rows of A ----
-constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2, kMc = 2;   // kMc: CTAs of a cluster
+constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2, kMc = 2;   // kMc: most CTAs of a cluster
 constexpr int kWStageBytes = (kWM + kWN) * kBlock;       // 48 KB
 constexpr int kWSumWarps = 8;
 constexpr int kWThreads = kWSumWarps * 32 + 128;
@@ -320,35 +322,36 @@ __device__ __forceinline__ void store_box(unsigned char* stage, const CUtensorMa
   __syncwarp();
 }
 
-// The CTAs of a cluster take tiles above one another and share the rows of B: each copies its part of them to all.
+// The CTAs of a cluster (one or two) take tiles above one another and share the rows of B: each copies its part of them to
+// all.
 __global__ void __launch_bounds__(kWThreads, 1)
 k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap,
                   const __grid_constant__ MatmulPlan p, uint32_t* status) {
   extern __shared__ unsigned char smem_raw[];
   WideSmem& sm = *reinterpret_cast<WideSmem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) ring_init(sm, kWStages, kWBufs, kMc, kWSumWarps);
+  if (tid == 0) ring_init(sm, kWStages, kWBufs, p.ctas, kWSumWarps);
   if (warp == kWSumWarps) tc::tmem_alloc(&sm.tmem, kWBufs * kWN);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   tc::cluster_barrier();   // every CTA's barriers exist before a peer copies or arrives into them
   const int rank = (int)tc::cluster_ctarank();
-  constexpr uint16_t kMask = (uint16_t)((1u << kMc) - 1);
-  constexpr int kBPart = kWN / kMc;
+  const int mc = p.ctas, b_part = kWN / mc;
+  const uint16_t mask = (uint16_t)((1u << mc) - 1);
   const uint32_t tm = sm.tmem;
   volatile int* abort = &sm.abort;
   pdl_wait();
-  // work items: kMc tiles above one another, one for each CTA
-  const int m_groups = (p.m_tiles + kMc - 1) / kMc;
-  const int items = m_groups * p.n_tiles, it0 = blockIdx.x / kMc, stride = gridDim.x / kMc;   // (below 2^31)
+  // work items: mc tiles above one another, one for each CTA
+  const int m_groups = (p.m_tiles + mc - 1) / mc;
+  const int items = m_groups * p.n_tiles, it0 = blockIdx.x / mc, stride = gridDim.x / mc;   // (below 2^31)
   struct Item {
     int m0, n0;   // this CTA's first row, the tile's first column
   };
   auto item = [&](int it) {
     Item w;
     w.n0 = it / m_groups;
-    w.m0 = ((it - w.n0 * m_groups) * kMc + rank) * kWM;
+    w.m0 = ((it - w.n0 * m_groups) * mc + rank) * kWM;
     w.n0 *= kWN;
     return w;
   };
@@ -369,8 +372,9 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
           }
           tc::mbar_arrive_expect_tx(&sm.full[st], kWStageBytes);
           tma::load_2d(sm.stage[st], &amap, k * kBlock, w.m0, &sm.full[st]);
-          unsigned char* b = sm.stage[st] + kWM * kBlock + rank * (kBPart * kBlock);
-          tma::load_2d_mc(b, &bmap, k * kBlock, w.n0 + rank * kBPart, &sm.full[st], kMask);
+          unsigned char* b = sm.stage[st] + kWM * kBlock + rank * (b_part * kBlock);
+          if (mc > 1) tma::load_2d_mc(b, &bmap, k * kBlock, w.n0 + rank * b_part, &sm.full[st], mask);
+          else tma::load_2d(b, &bmap, k * kBlock, w.n0, &sm.full[st]);
         }
       }
       for (uint32_t i = n > kWStages ? n - kWStages : 0; i < n; ++i)   // every issued copy lands before exit
@@ -394,7 +398,8 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) mma_fp8(leader, tm + buf * kWN, desc128(sa + 32 * ks), desc128(sb + 32 * ks), idesc, ks > 0);
           tc::mma_commit_by(leader, &sm.acc_full[buf]);
-          commit_fp8_mc(leader, &sm.empty[st], kMask);
+          if (mc > 1) commit_fp8_mc(leader, &sm.empty[st], mask);
+          else tc::mma_commit_by(leader, &sm.empty[st]);
         }
       }
     }
@@ -485,9 +490,9 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
 // ---- few rows of A, or few tiles ----
 // A tile is 128 rows of B x kRows (16 to 128) rows of A.
 constexpr int kTN = 128, kTBufs = 4;                // rows of B; accumulators
-template <int kRows> constexpr int kTSumWarps = kRows > 16 ? 8 : 4;      // two groups share the rows of A
+template <int kRows> constexpr int kTSumWarps = kRows > 64 ? 16 : kRows > 16 ? 8 : 4;   // groups of four share the rows of A
 template <int kRows> constexpr int kTThreads = (kTSumWarps<kRows> + 2) * 32;
-template <int kRows> constexpr int kTOwn = kRows / (kTSumWarps<kRows> / 4);   // rows of A of a sum warp: 16, 16, 32, 64
+template <int kRows> constexpr int kTOwn = kRows / (kTSumWarps<kRows> / 4);   // rows of A of a sum warp: 16, 16, 32, 32
 template <int kRows> constexpr int kTStageBytes = (kTN + kRows) * kBlock;
 // CTAs that an SM can hold.  With more tiles than SMs two of them, with half the ring each, read at the same time, and
 // no second wave of tiles leaves SMs idle: 32 x 32,768 x 4,096 takes 25.1 us instead of 27.5.
@@ -699,9 +704,14 @@ struct Cut {
   int m, n, ctas, n_split;
   bool thin;
 };
-// Estimated times in us, from measurements of shapes around the borders: a block of K takes 0.47 us in the wide kernel
-// and 0.45 (128 rows of A) or 0.3 in the thin one, the end of a tile 1.2 and 2 or 0.5, a launch that adds the partial sums 2.5, and these go to L2 and back
-// at 5 TB/s.  200 x 16,384 x 4,096: wide 20 us, thin 33; 161 x 1,001 x 1,552: wide (split) 18, thin 10.
+// Estimated times in us without the launch, fitted to measurements of shapes around the borders.  A block of K takes 0.42
+// us in the wide kernel, the end of a tile 1.2; pairs of CTAs start 1 us later, but copy half of B, which counts where there
+// is more than one tile for an SM (a block alone 0.45; 1,741 x 9,547 x 1,456: 37.7 us in pairs, 40.8 alone, 4,096 x 32,768 x
+// 4,096 at the power limit 450 and 457, 512 x 8,192 x 8,192 32.3 and 31.0), and weights that come from memory for one row of
+// tiles take 0.47 a block.  In the thin kernel a block takes 0.45 (128 rows of A) or 0.3, the end of a tile 1 or 0.5, a
+// launch that adds the partial sums 2.5, and these go to L2 and back at 5 TB/s.
+// 128 x 32,768 x 4,096: thin 34.6 us, wide 26.8; 128 x 8,192 x 8,192: 20.6 (split) and 30.4; 200 x 16,384 x 4,096: 33 and
+// 17.3; 161 x 1,001 x 1,552: 7.6 (split) and 18.
 struct Estimate {
   int n_split;
   double us;
@@ -718,11 +728,14 @@ Cut cut_of(int M, int N, int K) {
   const int64_t kb = (K + kBlock - 1) / kBlock;
   auto tiles = [&](int m, int n) { return (int64_t)((M + m - 1) / m) * ((N + n - 1) / n); };
   const int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  const Estimate thin = thin_time(std::max<int64_t>(1, tiles(rows, kTN)), kb, rows == 128 ? 0.45 : 0.3, rows == 128 ? 2. : 0.5, 4. * M * N);
-  const int64_t groups = tiles(kMc * kWM, kWN);
-  const double wide = (double)((groups + kSms / kMc - 1) / (kSms / kMc)) * (kb * 0.47 + 1.2);
-  if (M <= 128 || thin.us <= wide) return Cut{rows, kTN, 1, thin.n_split, true};
-  return Cut{kWM, kWN, kMc, 1, false};
+  const Estimate thin = thin_time(std::max<int64_t>(1, tiles(rows, kTN)), kb, rows == 128 ? 0.45 : 0.3, rows == 128 ? 1. : 0.5, 4. * M * N);
+  auto wide = [&](int ctas, double block) {
+    const int64_t groups = tiles(ctas * kWM, kWN), at_once = kSms / ctas;
+    return (double)((groups + at_once - 1) / at_once) * (kb * block + 1.2);
+  };
+  const double two = wide(kMc, 0.42) + 1., one = wide(1, M <= kWM ? 0.47 : tiles(kWM, kWN) <= kSms ? 0.42 : 0.45);
+  if (M <= 64 || thin.us <= std::min(one, two)) return Cut{rows, kTN, 1, thin.n_split, true};
+  return Cut{kWM, kWN, one < two ? 1 : kMc, 1, false};
 }
 int64_t partial_ld(int N) { return ((int64_t)N + 127) / 128 * 128; }
 
@@ -775,7 +788,7 @@ cudaError_t launch_wide(int64_t items, int sms, const CUtensorMap& am, const CUt
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  return launch_matmul(k_matmul_fp8_wide, sizeof(WideSmem) + 1024, kWThreads, items, sms, kMc, s, am, bm, cm, p);
+  return launch_matmul(k_matmul_fp8_wide, sizeof(WideSmem) + 1024, kWThreads, items, sms, p.ctas, s, am, bm, cm, p);
 }
 
 template <int kRows>
@@ -816,6 +829,7 @@ cudaError_t launch_matmul_fp8(const uint8_t* a, const float* sa, const uint8_t* 
   MatmulPlan p = {};
   p.sa = sa; p.sb = sb; p.C = C; p.M = M; p.N = N; p.kb = (K + kBlock - 1) / kBlock; p.f32 = f32;
   p.n_split = cut.n_split;
+  p.ctas = cut.ctas;
   p.ld = partial_ld(N);
   p.partial = p.n_split > 1 ? static_cast<float*>(ws) : nullptr;
   p.m_tiles = (M + cut.m - 1) / cut.m;

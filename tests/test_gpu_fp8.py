@@ -150,6 +150,13 @@ def test_product_many_tiles_per_sm(M, N):
     check_product(M, N, 768)
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(100, 30001, 272), (128, 20480, 1024), (300, 9001, 528), (257, 12288, 640), (1500, 9547, 400), (2100, 58, 992)])
+def test_product_of_wide_tiles(M, N, K, out):
+    """One row of tiles, odd numbers of them, one wave and several, rows of C on 16 bytes and not."""
+    check_product(M, N, K, out)
+
+
 def test_scales_belong_to_their_rows_and_blocks():
     """Powers of two in every scale and ones in every code: C counts what each block contributes, exactly."""
     for M in (40, 130):
