@@ -9,7 +9,7 @@
 //   of B.  A row of A is a lane of the accumulator, so a thread has one scale per block: sa[its row] sb[its 128 columns].
 //   In long products two CTAs with tiles above one another copy B's rows for each other (32 KB out of L2 for each instead
 //   of 48).
-//   4,096 x 32,768 x 4,096 takes 417 us (2.6 PFLOP/s) from a cool start and 447 (2.5) in a row, at the card's 1,400 W:
+//   4,096 x 32,768 x 4,096 takes 417 us (2.6 PFLOP/s) from a cool start and 450 to 460 (2.4) in a row, at the card's 1,400 W:
 //   the power cap holds the clock at 1.88 GHz, and operands of zeros take 405.  Below that: a block's MMAs run 513 cycles,
 //   and the way MMA -> sums (200 cycles after the last product) -> accumulator read (300) -> next MMAs (200) about as long
 //   again, with two accumulators (all of tensor memory) to hide it; the tensor pipe is active for 53% of the cycles.
