@@ -79,6 +79,17 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
+// Those of the four pairs whose bit of `which` is set.
+__device__ __forceinline__ void store_pairs(uint16_t* p, const float (&f)[8], uint32_t which) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (which >> j & 1) *reinterpret_cast<uint32_t*>(p + 2 * j) = f32x2_bf16x2(f[2 * j], f[2 * j + 1]);
+}
+__device__ __forceinline__ void store_pairs(float* p, const float (&f)[8], uint32_t which) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (which >> j & 1) *reinterpret_cast<float2*>(p + 2 * j) = make_float2(f[2 * j], f[2 * j + 1]);
+}
 __device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = (uint16_t)(f32x2_bf16x2(x, 0.f) & 0xFFFFu); }
@@ -108,7 +119,7 @@ __device__ __forceinline__ void rotations(const RopeArgs& a, int64_t t0, int tok
 
 // 8 channels at a time.  Units of a head: with half pairs r / 16 pairs of 8 + 8 channels, with interleaved ones
 // r / 8 of 8; then, unless y is x, (d - r) / 8 copied ones.  kRagged: interleaved pairs from any even channel on, so
-// that the rotated units' first and last may have pairs that are copied.
+// that the rotated units' first and last may have pairs that are copied (in place: left alone).
 enum Mode { kInterleaved, kHalves, kRagged, kOnes, kOnesWhole };
 // 8-channel loads of a head that have a rotated channel.
 __host__ __device__ inline int touched_units(const RopeArgs& a) { return a.r ? (a.start + a.r + kUnit - 1) / kUnit - a.start / kUnit : 0; }
@@ -132,6 +143,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
   const int rot = rotated_units(a, kMode);         // of a head; they come first
   const int first = kMode == kRagged ? a.start & ~(kUnit - 1) : a.start, width = kMode == kRagged ? rot * kUnit : a.r;
   const int total = (int)min((int64_t)pl.span, pl.total - (int64_t)blockIdx.x * pl.span);
+  const bool in_place = a.x == a.y;
   constexpr int kMany = sizeof(In) == 4 ? 2 : 4;   // units in flight
   for (int u0 = threadIdx.x; u0 < total; u0 += kMany * kThreads) {
     Eight<In> v[kMany], w[kMany];
@@ -165,6 +177,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
       if (at[k] == -2) continue;
       float f[8];
       v[k].get(f);
+      uint32_t turned = 15;                         // pairs of the unit that turn
       if (at[k] >= 0) {
         if (kHalf) {
           float g[8];
@@ -181,7 +194,10 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
           const int t = at[k] >> 16, i0 = kMode == kRagged ? (first - a.start) / 2 + (at[k] & 0xFFFF) * (kUnit / 2) : 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (kMode == kRagged && (uint32_t)(i0 + j) >= (uint32_t)a.r / 2) continue;
+            if (kMode == kRagged && (uint32_t)(i0 + j) >= (uint32_t)a.r / 2) {
+              turned &= ~(1u << j);
+              continue;
+            }
             const float2 q = kMode == kRagged ? cs[t * (a.r / 2) + i0 + j] : cs[at[k] + j];
             const float f1 = f[2 * j] * q.x - f[2 * j + 1] * q.y;
             f[2 * j + 1] = f[2 * j] * q.y + f[2 * j + 1] * q.x;
@@ -189,7 +205,9 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
           }
         }
       }
-      store8(y + to[k], f);
+      // In place the other pairs of a ragged unit are left alone: somebody else may be writing them.
+      if (kMode == kRagged && turned != 15 && in_place) store_pairs(y + to[k], f, turned);
+      else store8(y + to[k], f);
     }
   }
 }
