@@ -10,8 +10,8 @@
 // Bound: bytes.  A block takes about 2,048 units of work of 16-byte loads (8 channels; two halves of 8) that lie behind
 // one another, over tokens and heads: its threads compute their tokens' sines and cosines into shared memory once for
 // all heads, then rotate and copy with 2 or 4 units' loads in flight each.  4,096 tokens x 64 heads x 512 channels, 64
-// rotated, bf16: 85 us, 6.3 TB/s (whole heads a block: 90; 79 at the rate of a copy).  With one head there is nothing to
-// share a rotation with: 109,307 x 512 takes 47 us (4.7 TB/s), 338,137 x 64 with 32 rotated 35 (2.4).
+// rotated, bf16: 79 us, 6.8 TB/s (whole heads a block: 90; four blocks an SM: 85).  With one head there is nothing to
+// share a rotation with: 109,307 x 512 takes 42 us (5.3 TB/s), 338,137 x 64 with 32 rotated 32.5 (2.7; half pairs 44).
 // Half pairs that 8 channels do not divide, odd starts and unaligned rows go pair by pair (445 x 40 x 512, 62 rotated,
 // half: 11 us, at 3.3 TB/s).
 #include <algorithm>
@@ -72,28 +72,41 @@ template <> struct Eight<float> {
     f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w; f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
   }
 };
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(f32x2_bf16x2(f[0], f[1]), f32x2_bf16x2(f[2], f[3]), f32x2_bf16x2(f[4], f[5]), f32x2_bf16x2(f[6], f[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-// Those of the four pairs whose bit of `which` is set.
-__device__ __forceinline__ void store_pairs(uint16_t* p, const float (&f)[8], uint32_t which) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (which >> j & 1) *reinterpret_cast<uint32_t*>(p + 2 * j) = f32x2_bf16x2(f[2 * j], f[2 * j + 1]);
-}
-__device__ __forceinline__ void store_pairs(float* p, const float (&f)[8], uint32_t which) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (which >> j & 1) *reinterpret_cast<float2*>(p + 2 * j) = make_float2(f[2 * j], f[2 * j + 1]);
-}
+// 8 channels on their way out.  Copied ones of the same type keep their bits: a NaN's payload would not come through a
+// conversion.
+template <typename T> struct Result;
+template <> struct Result<uint16_t> {
+  uint32_t w[4];
+  __device__ __forceinline__ void copy(const Eight<uint16_t>& e) { w[0] = e.v.x; w[1] = e.v.y; w[2] = e.v.z; w[3] = e.v.w; }
+  __device__ __forceinline__ void copy(const Eight<float>& e) {
+    set(0, e.lo.x, e.lo.y); set(1, e.lo.z, e.lo.w); set(2, e.hi.x, e.hi.y); set(3, e.hi.z, e.hi.w);
+  }
+  __device__ __forceinline__ void set(int pair, float a, float b) { w[pair] = f32x2_bf16x2(a, b); }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
+  __device__ __forceinline__ void store_pair(uint16_t* p, int pair) const { *reinterpret_cast<uint32_t*>(p + 2 * pair) = w[pair]; }
+};
+template <> struct Result<float> {
+  float f[8];
+  template <typename In> __device__ __forceinline__ void copy(const Eight<In>& e) { e.get(f); }
+  __device__ __forceinline__ void set(int pair, float a, float b) { f[2 * pair] = a; f[2 * pair + 1] = b; }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  __device__ __forceinline__ void store_pair(float* p, int pair) const { *reinterpret_cast<float2*>(p + 2 * pair) = make_float2(f[2 * pair], f[2 * pair + 1]); }
+};
 __device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = (uint16_t)(f32x2_bf16x2(x, 0.f) & 0xFFFFu); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+// A copied channel, its bits too.
+template <typename In>
+__device__ __forceinline__ void copy1(uint16_t* p, float x) {
+  if (sizeof(In) == 2) *p = (uint16_t)(__float_as_uint(x) >> 16);
+  else store1(p, x);
+}
+template <typename In>
+__device__ __forceinline__ void copy1(float* p, float x) { *p = x; }
 
 // A block's first token and the units of it that lie before the block's.
 __device__ __forceinline__ void first_unit(const RopePlan& pl, int64_t* t0, uint32_t* before) {
@@ -119,18 +132,24 @@ __device__ __forceinline__ void rotations(const RopeArgs& a, int64_t t0, int tok
 
 // 8 channels at a time.  Units of a head: with half pairs r / 16 pairs of 8 + 8 channels, with interleaved ones
 // r / 8 of 8; then, unless y is x, (d - r) / 8 copied ones.  kRagged: interleaved pairs from any even channel on, so
-// that the rotated units' first and last may have pairs that are copied (in place: left alone).
-enum Mode { kInterleaved, kHalves, kRagged, kOnes, kOnesWhole };
+// that the rotated units' first and last may have pairs that are copied; kRaggedInPlace: that are left alone (somebody else
+// may be writing them).
+enum Mode { kInterleaved, kHalves, kRagged, kRaggedInPlace, kOnes, kOnesWhole };
 // 8-channel loads of a head that have a rotated channel.
 __host__ __device__ inline int touched_units(const RopeArgs& a) { return a.r ? (a.start + a.r + kUnit - 1) / kUnit - a.start / kUnit : 0; }
 __host__ __device__ inline int rotated_units(const RopeArgs& a, Mode mode) {
   return mode == kHalves ? a.r / 16 : mode == kInterleaved ? a.r / 8 : touched_units(a);
 }
 
+// Blocks of an SM: as many as take no spills (4,096 x 64 x 512 of bf16: interleaved 78.6 us with 5, 83.5 with 4; ragged 79.4
+// with 6, 83.3 with 5); 0 leaves it to the compiler.
 template <typename In, typename Out, Mode kMode>
-__global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
+constexpr int kBlocks = kMode == kHalves ? 3 : kMode == kRaggedInPlace ? 0 : kMode == kRagged && sizeof(In) + sizeof(Out) == 4 ? 6 : 5;
+
+template <typename In, typename Out, Mode kMode>
+__global__ void __launch_bounds__(kThreads, kBlocks<In, Out, kMode>) k_rope(RopePlan pl) {
   __shared__ float2 cs[kMaxAngles];
-  constexpr bool kHalf = kMode == kHalves;
+  constexpr bool kHalf = kMode == kHalves, kAnyPair = kMode == kRagged || kMode == kRaggedInPlace;
   const RopeArgs& a = pl.a;
   pdl_wait();
   int64_t t0;
@@ -141,9 +160,8 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
   const In* x = static_cast<const In*>(a.x);
   Out* y = static_cast<Out*>(a.y);
   const int rot = rotated_units(a, kMode);         // of a head; they come first
-  const int first = kMode == kRagged ? a.start & ~(kUnit - 1) : a.start, width = kMode == kRagged ? rot * kUnit : a.r;
+  const int first = kAnyPair ? a.start & ~(kUnit - 1) : a.start, width = kAnyPair ? rot * kUnit : a.r;
   const int total = (int)min((int64_t)pl.span, pl.total - (int64_t)blockIdx.x * pl.span);
-  const bool in_place = a.x == a.y;
   constexpr int kMany = sizeof(In) == 4 ? 2 : 4;   // units in flight
   for (int u0 = threadIdx.x; u0 < total; u0 += kMany * kThreads) {
     Eight<In> v[kMany], w[kMany];
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
       int c;
       if ((int)unit < rot) {
         c = first + unit * kUnit;
-        at[k] = kMode == kRagged ? (int)(t << 16 | unit) : t * (a.r / 2) + unit * (kHalf ? kUnit : kUnit / 2);
+        at[k] = kAnyPair ? (int)(t << 16 | unit) : t * (a.r / 2) + unit * (kHalf ? kUnit : kUnit / 2);
       } else {
         c = (unit - rot) * kUnit;
         if (c >= first) c += width;
@@ -175,39 +193,52 @@ __global__ void __launch_bounds__(kThreads) k_rope(RopePlan pl) {
 #pragma unroll
     for (int k = 0; k < kMany; ++k) {
       if (at[k] == -2) continue;
+      Result<Out> out;
+      if (!kAnyPair && at[k] < 0) {
+        out.copy(v[k]);
+        out.store(y + to[k]);
+        continue;
+      }
       float f[8];
       v[k].get(f);
-      uint32_t turned = 15;                         // pairs of the unit that turn
-      if (at[k] >= 0) {
-        if (kHalf) {
-          float g[8];
-          w[k].get(g);
+      if (kHalf) {
+        float g[8];
+        w[k].get(g);
+        Result<Out> second;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 q = cs[at[k] + j];
-            const float f1 = f[j] * q.x - g[j] * q.y;
-            g[j] = f[j] * q.y + g[j] * q.x;
-            f[j] = f1;
-          }
-          store8(y + to[k] + a.r / 2, g);
-        } else {
-          const int t = at[k] >> 16, i0 = kMode == kRagged ? (first - a.start) / 2 + (at[k] & 0xFFFF) * (kUnit / 2) : 0;
+        for (int j = 0; j < 8; j += 2) {
+          const float2 q = cs[at[k] + j], z = cs[at[k] + j + 1];
+          out.set(j / 2, f[j] * q.x - g[j] * q.y, f[j + 1] * z.x - g[j + 1] * z.y);
+          second.set(j / 2, f[j] * q.y + g[j] * q.x, f[j + 1] * z.y + g[j + 1] * z.x);
+        }
+        second.store(y + to[k] + a.r / 2);
+        out.store(y + to[k]);
+        continue;
+      }
+      // pair j of the unit, the i-th angle of its token on
+      auto turn = [&](int j, int i) {
+        const float2 q = cs[i + j];
+        out.set(j, f[2 * j] * q.x - f[2 * j + 1] * q.y, f[2 * j] * q.y + f[2 * j + 1] * q.x);
+      };
+      if (kAnyPair) {
+        out.copy(v[k]);
+        if (at[k] >= 0) {
+          const int pairs = a.r / 2, i0 = (first - a.start) / 2 + (at[k] & 0xFFFF) * (kUnit / 2);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (kMode == kRagged && (uint32_t)(i0 + j) >= (uint32_t)a.r / 2) {
-              turned &= ~(1u << j);
-              continue;
-            }
-            const float2 q = kMode == kRagged ? cs[t * (a.r / 2) + i0 + j] : cs[at[k] + j];
-            const float f1 = f[2 * j] * q.x - f[2 * j + 1] * q.y;
-            f[2 * j + 1] = f[2 * j] * q.y + f[2 * j + 1] * q.x;
-            f[2 * j] = f1;
+          for (int j = 0; j < 4; ++j)
+            if ((uint32_t)(i0 + j) < (uint32_t)pairs) turn(j, (at[k] >> 16) * pairs + i0);
+          if (kMode == kRaggedInPlace && (i0 < 0 || i0 + 4 > pairs)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if ((uint32_t)(i0 + j) < (uint32_t)pairs) out.store_pair(y + to[k], j);
+            continue;
           }
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) turn(j, at[k]);
       }
-      // In place the other pairs of a ragged unit are left alone: somebody else may be writing them.
-      if (kMode == kRagged && turned != 15 && in_place) store_pairs(y + to[k], f, turned);
-      else store8(y + to[k], f);
+      out.store(y + to[k]);
     }
   }
 }
@@ -268,18 +299,19 @@ __global__ void __launch_bounds__(kThreads) k_rope_any(RopePlan pl) {
     for (int k = 0; k < kMany; ++k) {
       if (at[k] == -2) continue;
       if (kWhole && at[k] == -3) {
-        float f[8];
-        v[k].get(f);
-        store8(y + to[k], f);
+        Result<Out> out;
+        out.copy(v[k]);
+        out.store(y + to[k]);
         continue;
       }
       if (at[k] >= 0) {
         const float2 z = cs[at[k]];
         const float f1 = x1[k] * z.x - x2[k] * z.y;
         store1(y + to[k] + c2[k], x1[k] * z.y + x2[k] * z.x);
-        x1[k] = f1;
+        store1(y + to[k], f1);
+      } else {
+        copy1<In>(y + to[k], x1[k]);
       }
-      store1(y + to[k], x1[k]);
     }
   }
 }
@@ -297,6 +329,7 @@ template <typename In, typename Out>
 cudaError_t launch_typed(const RopePlan& pl, int64_t grid, Mode mode, cudaStream_t s) {
   const auto kernel = mode == kHalves    ? k_rope<In, Out, kHalves>
                       : mode == kRagged  ? k_rope<In, Out, kRagged>
+                      : mode == kRaggedInPlace ? k_rope<In, In, kRaggedInPlace>
                       : mode == kOnes    ? k_rope_any<In, Out, false>
                       : mode == kOnesWhole ? k_rope_any<In, Out, true>
                                          : k_rope<In, Out, kInterleaved>;
@@ -325,7 +358,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   const bool eight = a.d % kUnit == 0 && whole(a.x, a.x_token, a.x_head, in) && whole(a.y, a.y_token, a.y_head, out);
   const Mode mode = !eight ? kOnes
                     : half ? (a.start % kUnit == 0 && a.r % (2 * kUnit) == 0 ? kHalves : kOnesWhole)
-                           : (a.start % 2 != 0 ? kOnesWhole : a.start % kUnit == 0 && a.r % kUnit == 0 ? kInterleaved : kRagged);
+                           : (a.start % 2 != 0 ? kOnesWhole : a.start % kUnit == 0 && a.r % kUnit == 0 ? kInterleaved : in_place ? kRaggedInPlace : kRagged);
   int units, copied;                        // of a head: in all, copied ones of them
   switch (mode) {
     case kOnes: units = a.d - a.r / 2, copied = a.d - a.r; break;
