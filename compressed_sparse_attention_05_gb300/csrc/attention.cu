@@ -149,7 +149,7 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
 
-  const int t = kTree ? max(a.q_pos[row], -1) : a.q_pos[row];   // (-1: no node of the tree)
+  const int t = max(a.q_pos[row], -1);   // (before the first position, or no node of a tree: -1, which sees nothing)
   const int nv = n_visible(a.n_entries[b], t);  // bounds the indices checked below
   int n_sel = kTree && t < 0 ? 0 : a.cnt[row];
   if (n_sel < 0 || n_sel > a.K) {
@@ -157,15 +157,17 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
     n_sel = n_sel < 0 ? 0 : a.K;
   }
   const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
-  int w_lo = max(max(0, t - a.W + 1), pos0);
-  int w_hi = min(t, pos0 + a.swa_cap - 1);
+  // (neither the first position of a window of no rows nor the buffer's last row need be a position)
+  const int first = max(0, t - max(a.W - 1, 0));
+  int w_lo = max(first, pos0);
+  int w_hi = (int)min((int64_t)t, (int64_t)pos0 + a.swa_cap - 1);
   int ctx = 0;
   if (kTree) {   // from the first position that the buffer holds (or the first ancestor) to the token itself
     ctx = max(0, a.ctx_len[b]);
-    w_lo = max(max(0, t - a.W + 1), min(a.swa_cap > 0 ? pos0 : INT_MAX, ctx));
+    w_lo = max(first, min(a.swa_cap > 0 ? pos0 : INT_MAX, ctx));
     w_hi = t;
   }
-  const int n_win = max(0, w_hi - w_lo + 1);
+  const int n_win = a.W > 0 && w_hi >= w_lo ? w_hi - w_lo + 1 : 0;
   const int n_keys = n_sel + n_win;
 
   // Q rows of this head group: bf16 bits first, with each head's largest exponent field

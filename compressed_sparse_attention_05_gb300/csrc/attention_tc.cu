@@ -385,7 +385,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   // ---- before the previous kernel of the step is done: the token's own inputs
   // (scalars, Q rows), barriers, tensor memory and the Q operand (a tree's positions come from its plan, which lets
   // nothing start before it is done)
-  const int t = kTree ? max(a.q_pos[row], -1) : a.q_pos[row];   // (-1: no node of the tree)
+  const int t = max(a.q_pos[row], -1);   // (before the first position, or no node of a tree: -1, which sees nothing)
   int n_sel = kTree ? a.cnt[row] : 0;
   const int n_ent = a.n_entries[b];
   const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
@@ -412,15 +412,17 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     sm.qexp[tid] = 0;
   }
   // the window rows of the token: raw positions max(0, t-W+1, pos0) .. min(t, last row held)
-  int w_lo = max(max(0, t - a.W + 1), pos0);
-  int w_hi = min(t, pos0 + a.swa_cap - 1);
+  // (neither the first position of a window of no rows nor the buffer's last row need be a position)
+  const int first = max(0, t - max(a.W - 1, 0));
+  int w_lo = max(first, pos0);
+  int w_hi = (int)min((int64_t)t, (int64_t)pos0 + a.swa_cap - 1);
   int ctx = 0;
   if (kTree) {   // from the first position that the buffer holds (or the first ancestor) to the token itself
     ctx = max(0, a.ctx_len[b]);
-    w_lo = max(max(0, t - a.W + 1), min(a.swa_cap > 0 ? pos0 : INT_MAX, ctx));
+    w_lo = max(first, min(a.swa_cap > 0 ? pos0 : INT_MAX, ctx));
     w_hi = t;
   }
-  const int n_win = max(0, w_hi - w_lo + 1);
+  const int n_win = a.W > 0 && w_hi >= w_lo ? w_hi - w_lo + 1 : 0;
   int n_mine = 0, n_my = 0;
   int32_t cur_src = -1;
   float cur_wsc = 0.f;
