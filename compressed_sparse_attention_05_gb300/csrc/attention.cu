@@ -122,8 +122,8 @@ __device__ __forceinline__ void dequant_group(const AttnArgs& a, int b, int64_t 
     for (int i = 0; i < 8; ++i) {
       const uint32_t word = cw[i >> 1];
       const int sh = (i & 1) * 16;
-      const float lo = bf16_bits_to_f32(f32_to_bf16_bits(e4m3_to_f32((word >> sh) & 0xFFu) * sc));
-      const float hi = bf16_bits_to_f32(f32_to_bf16_bits(e4m3_to_f32((word >> (sh + 8)) & 0xFFu) * sc));
+      const uint32_t bf = f32x2_bf16x2(e4m3_to_f32((word >> sh) & 0xFFu) * sc, e4m3_to_f32((word >> (sh + 8)) & 0xFFu) * sc);
+      const float lo = __uint_as_float(bf << 16), hi = __uint_as_float(bf & 0xFFFF0000u);
       w[i] = f32_to_f16_bits(lo) | (f32_to_f16_bits(hi) << 16);
     }
   } else {
@@ -287,8 +287,9 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
       const float m_old = sm.m[h];
       const float m_new = fmaxf(m_old, mx);
       const bool none = m_new == -INFINITY;
-      const float e0 = none ? 0.f : exp2f(sv.x - m_new), e1 = none ? 0.f : exp2f(sv.y - m_new);
-      const float e2 = none ? 0.f : exp2f(sv.z - m_new), e3 = none ? 0.f : exp2f(sv.w - m_new);
+      const float ref = none ? 0.f : m_new;      // (none: no key so far, or logits of NaN alone, which stay NaN)
+      const float e0 = exp2f(sv.x - ref), e1 = exp2f(sv.y - ref);
+      const float e2 = exp2f(sv.z - ref), e3 = exp2f(sv.w - ref);
       const __half p0 = __float2half_rn(e0), p1 = __float2half_rn(e1);
       const __half p2 = __float2half_rn(e2), p3 = __float2half_rn(e3);
       // the normaliser sums the fp32 weights (2^f p of a rescaled window row counts as
@@ -359,7 +360,7 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
   }
   if (a.lse && tid < kHG && hg * kHG + tid < a.Hq) {
     const float l = sm.l[tid];
-    a.lse[row * a.Hq + hg * kHG + tid] = l > 0.f ? (sm.m[tid] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    a.lse[row * a.Hq + hg * kHG + tid] = l > 0.f ? (sm.m[tid] + log2f(l)) * 0.6931471805599453f : lse_of_nothing(l);
   }
 }
 

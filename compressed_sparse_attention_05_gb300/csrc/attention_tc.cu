@@ -741,7 +741,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     if (tid < kHeads) sm.fac[tid] = sm.l_run[tid] > 0.f ? 1.f / sm.l_run[tid] : 0.f;
     if (a.lse && tid < kHeads && hb + tid < a.Hq) {
       const float l = sm.l_run[tid];
-      a.lse[row * a.Hq + hb + tid] = l > 0.f ? (sm.m_ref[tid] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      a.lse[row * a.Hq + hb + tid] = l > 0.f ? (sm.m_ref[tid] + log2f(l)) * 0.6931471805599453f : lse_of_nothing(l);
     }
     __syncthreads();
     if (!mma_warp) {
@@ -819,11 +819,12 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
 #pragma unroll
       for (int q = 0; q < kMaxSplit; ++q)
         if (mq[q] != -INFINITY) L += lq[q] * ex2(mq[q] - M);
+        else L += lq[q];   // (0, or NaN where NaN is all that the rank's keys gave)
 #pragma unroll
       for (int q = 0; q < kMaxSplit; ++q)
         if (q < n_split) facq[q * kHeads + tid] = (mq[q] == -INFINITY || L <= 0.f) ? 0.f : ex2(mq[q] - M) / L;
       if (crank == 0 && a.lse && hb + tid < a.Hq)
-        a.lse[row * a.Hq + hb + tid] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        a.lse[row * a.Hq + hb + tid] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : lse_of_nothing(L);
     }
     __syncthreads();
     for (int e0 = tid; e0 < n4; e0 += 2 * kThreads) {
