@@ -355,9 +355,12 @@ def csa2_page_plan_workspace_size(dims: Dims) -> int:
 def csa2_page_plan(dims: Dims, pool: PagePool, seq_len, n_new, seq_len_out, n_entries, first_entry, ws, shift=None, q_pos=None,
                    slots=None, granted=None, stream=None):
     """Pages, positions and slots of a step's tokens; slots int64 [B][max_new], q_pos int32 [B][Tq]."""
+    def wanted(t):     # a tensor without columns has no address of its own: any other says that it is there
+        return ptr(ws) if t is not None and t.numel() == 0 else ptr(t)
+
     _check(lib().csa2_page_plan(C.byref(dims), C.byref(pool), ptr(seq_len), ptr(n_new), ptr(shift),
                                 slots.shape[-1] if slots is not None else 0, ptr(seq_len_out), ptr(n_entries), ptr(first_entry),
-                                ptr(q_pos), ptr(slots), ptr(granted), ptr(ws), _nbytes(ws), stream_handle(stream)))
+                                wanted(q_pos), wanted(slots), ptr(granted), ptr(ws), _nbytes(ws), stream_handle(stream)))
 
 
 def _strided(t: torch.Tensor):

@@ -767,7 +767,7 @@ int csa2_page_plan(const csa2_dims* dm, const csa2_page_pool* pool, const int32_
   a.page_table = pool->page_table; a.held = pool->held; a.free_pages = pool->free_pages; a.n_free = pool->n_free;
   a.n_pages = pool->n_pages; a.seq_len = seq_len; a.n_new = n_new; a.shift = shift; a.seq_len_out = seq_len_out;
   a.n_entries = n_entries; a.first_entry = first_entry; a.granted = granted;
-  a.q_pos = dm->Tq > 0 ? q_pos : nullptr; a.slots = max_new > 0 ? slots : nullptr;
+  a.q_pos = q_pos; a.slots = slots;   // (wanted, if without a column: then who has new ones waits)
   a.B = dm->B; a.Tq = dm->Tq; a.max_pages = dm->max_pages; a.max_new = max_new;
   a.q_pos4 = dm->Tq % 4 == 0 && aligned16(q_pos);
   LAUNCH(launch_page_plan(a, ws, static_cast<cudaStream_t>(stream)), "page_plan");
