@@ -7,8 +7,6 @@
 //
 // k_matmul_fp8_wide (many rows of A, or more rows of B than the SMs take 128 at a time): tiles of 128 rows of A x 256 rows
 //   of B.  A row of A is a lane of the accumulator, so a thread has one scale per block: sa[its row] sb[its 128 columns].
-//   In long products two CTAs with tiles above one another copy B's rows for each other (32 KB out of L2 for each instead
-//   of 48).
 //   4,096 x 32,768 x 4,096 takes 417 us (2.6 PFLOP/s) from a cool start and 450 to 460 (2.4) in a row, at the card's 1,400 W:
 //   the power cap holds the clock at 1.88 GHz, and operands of zeros take 405.  Below that: a block's MMAs run 513 cycles,
 //   and the way MMA -> sums (200 cycles after the last product) -> accumulator read (300) -> next MMAs (200) about as long
@@ -150,7 +148,6 @@ struct MatmulPlan {
   float* partial;           // [n_split][M][ld]
   int64_t ld;
   int M, N, kb, n_split, f32;
-  int ctas;                 // of a cluster (wide)
   int c_map;                // C's rows start on 16 bytes: it is written by tensor-map copies
   int m_tiles, n_tiles;
 };
@@ -165,14 +162,6 @@ __device__ __forceinline__ void mma_fp8(uint32_t leader, uint32_t d_tmem, uint64
       "{\n .reg .pred p, e;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
       " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
-}
-// tc::mma_commit_by arriving on the barrier at `bar`'s offset in every CTA of the cluster in `mask`.
-__device__ __forceinline__ void commit_fp8_mc(uint32_t leader, uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(tc::smem_addr(bar)),
-      "h"(mask), "r"(leader)
       : "memory");
 }
 // The MMA warp's wait for two barriers with one look at a time: lane i looks at its own (bar, parity); `need`
@@ -254,12 +243,12 @@ __device__ __forceinline__ void split_range(const MatmulPlan& p, int s, int* k0,
   *k1 = (int)((int64_t)(s + 1) * p.kb / p.n_split);
 }
 
-// The barriers of a ring of operand stages (writers: arrivals that free one) and of the accumulators.
+// The barriers of a ring of operand stages and of the accumulators.
 template <typename Smem>
-__device__ __forceinline__ void ring_init(Smem& sm, int stages, int bufs, uint32_t writers, uint32_t readers) {
+__device__ __forceinline__ void ring_init(Smem& sm, int stages, int bufs, uint32_t readers) {
   for (int i = 0; i < stages; ++i) {
     tc::mbar_init(&sm.full[i], 1);
-    tc::mbar_init(&sm.empty[i], writers);
+    tc::mbar_init(&sm.empty[i], 1);
   }
   for (int i = 0; i < bufs; ++i) {
     tc::mbar_init(&sm.acc_full[i], 1);
@@ -270,7 +259,7 @@ __device__ __forceinline__ void ring_init(Smem& sm, int stages, int bufs, uint32
 }
 
 // ---- many rows of A ----
-constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2, kMc = 2;   // kMc: most CTAs of a cluster
+constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2;
 constexpr int kWStageBytes = (kWM + kWN) * kBlock;       // 48 KB
 constexpr int kWSumWarps = 8;
 constexpr int kWThreads = kWSumWarps * 32 + 128;
@@ -322,38 +311,28 @@ __device__ __forceinline__ void store_box(unsigned char* stage, const CUtensorMa
   __syncwarp();
 }
 
-// The CTAs of a cluster (one or two) take tiles above one another and share the rows of B: each copies its part of them to
-// all.
 __global__ void __launch_bounds__(kWThreads, 1)
 k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap,
                   const __grid_constant__ MatmulPlan p, uint32_t* status) {
   extern __shared__ unsigned char smem_raw[];
   WideSmem& sm = *reinterpret_cast<WideSmem*>(smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) ring_init(sm, kWStages, kWBufs, p.ctas, kWSumWarps);
+  if (tid == 0) ring_init(sm, kWStages, kWBufs, kWSumWarps);
   if (warp == kWSumWarps) tc::tmem_alloc(&sm.tmem, kWBufs * kWN);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  tc::cluster_barrier();   // every CTA's barriers exist before a peer copies or arrives into them
-  const int rank = (int)tc::cluster_ctarank();
-  const int mc = p.ctas, b_part = kWN / mc;
-  const uint16_t mask = (uint16_t)((1u << mc) - 1);
   const uint32_t tm = sm.tmem;
   volatile int* abort = &sm.abort;
   pdl_wait();
-  // work items: mc tiles above one another, one for each CTA
-  const int m_groups = (p.m_tiles + mc - 1) / mc;
-  const int items = m_groups * p.n_tiles, it0 = blockIdx.x / mc, stride = gridDim.x / mc;   // (below 2^31)
+  // the tiles of a column after one another
+  const int items = p.m_tiles * p.n_tiles;   // (below 2^31)
   struct Item {
-    int m0, n0;   // this CTA's first row, the tile's first column
+    int m0, n0;   // first row and column
   };
   auto item = [&](int it) {
-    Item w;
-    w.n0 = it / m_groups;
-    w.m0 = ((it - w.n0 * m_groups) * mc + rank) * kWM;
-    w.n0 *= kWN;
-    return w;
+    const int n = it / p.m_tiles;
+    return Item{(it - n * p.m_tiles) * kWM, n * kWN};
   };
 
   if (warp >= kWSumWarps) {
@@ -362,7 +341,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
       // ================= operand copies =================
       uint32_t n = 0;
       bool ok = true;
-      for (int it = it0; ok && it < items; it += stride) {
+      for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
         const Item w = item(it);
         for (int k = 0; k < p.kb; ++k, ++n) {
           const uint32_t st = n % kWStages, use = n / kWStages;
@@ -372,9 +351,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
           }
           tc::mbar_arrive_expect_tx(&sm.full[st], kWStageBytes);
           tma::load_2d(sm.stage[st], &amap, k * kBlock, w.m0, &sm.full[st]);
-          unsigned char* b = sm.stage[st] + kWM * kBlock + rank * (b_part * kBlock);
-          if (mc > 1) tma::load_2d_mc(b, &bmap, k * kBlock, w.n0 + rank * b_part, &sm.full[st], mask);
-          else tma::load_2d(b, &bmap, k * kBlock, w.n0, &sm.full[st]);
+          tma::load_2d(sm.stage[st] + kWM * kBlock, &bmap, k * kBlock, w.n0, &sm.full[st]);
         }
       }
       for (uint32_t i = n > kWStages ? n - kWStages : 0; i < n; ++i)   // every issued copy lands before exit
@@ -386,7 +363,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
       const uint32_t leader = tc::elect_lane();
       uint32_t n = 0;
       bool ok = true;
-      for (int it = it0; ok && it < items; it += stride) {
+      for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
         const Item w = item(it);
         for (int k = 0; k < p.kb; ++k, ++n) {
           const uint32_t st = n % kWStages, buf = n % kWBufs, use = n / kWBufs;
@@ -398,8 +375,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) mma_fp8(leader, tm + buf * kWN, desc128(sa + 32 * ks), desc128(sb + 32 * ks), idesc, ks > 0);
           tc::mma_commit_by(leader, &sm.acc_full[buf]);
-          if (mc > 1) commit_fp8_mc(leader, &sm.empty[st], mask);
-          else tc::mma_commit_by(leader, &sm.empty[st]);
+          tc::mma_commit_by(leader, &sm.empty[st]);
         }
       }
     }
@@ -412,7 +388,7 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
     const bool vec = p.kb % 4 == 0;   // (the scales' rows start on 16 bytes)
     uint32_t n = 0;
     bool ok = true;
-    for (int it = it0; ok && it < items; it += stride) {
+    for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
       const Item w = item(it);
       const int y = w.m0 + 32 * lq, n0 = w.n0 + 128 * half;
       const int m = y + lane < p.M ? y + lane : 0, nb = n0 < p.N ? n0 / kBlock : 0;   // rows of the scales
@@ -482,7 +458,6 @@ k_matmul_fp8_wide(const __grid_constant__ CUtensorMap amap, const __grid_constan
   }
   tc::tc_fence_before();
   __syncthreads();
-  tc::cluster_barrier();   // no copy or commit of a peer still targets this CTA
   if (warp == kWSumWarps) tc::tmem_dealloc(tm, kWBufs * kWN);
   if (tid == 0 && *abort) raise_status(status, CSA2_STATUS_TIMEOUT);
 }
@@ -520,7 +495,7 @@ k_matmul_fp8_thin(const __grid_constant__ CUtensorMap amap, const __grid_constan
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (p.partial) pdl_trigger();
   constexpr uint32_t kCols = kTBufs * kRows;        // 64 to 512 columns
-  if (tid == 0) ring_init(sm, n_stages, kTBufs, 1, kSumWarps);
+  if (tid == 0) ring_init(sm, n_stages, kTBufs, kSumWarps);
   if (warp == kSumWarps) tc::tmem_alloc(&sm.tmem, kCols);
   tc::tc_fence_before();
   __syncthreads();
@@ -699,17 +674,15 @@ __global__ void __launch_bounds__(256) k_matmul_fp8_sum(const __grid_constant__ 
   }
 }
 constexpr int kSms = 152;
-// How a product is cut: the rows of A and of B of a tile, the CTAs that share B, and the splits of K.
+// How a product is cut: the rows of A and of B of a tile, and the splits of K.
 struct Cut {
-  int m, n, ctas, n_split;
+  int m, n, n_split;
   bool thin;
 };
 // Estimated times in us without the launch, fitted to measurements of shapes around the borders.  A block of K takes 0.42
-// us in the wide kernel, the end of a tile 1.2; pairs of CTAs start 1 us later, but copy half of B, which counts where there
-// is more than one tile for an SM (a block alone 0.45; 1,741 x 9,547 x 1,456: 37.7 us in pairs, 40.8 alone, 4,096 x 32,768 x
-// 4,096 at the power limit 450 and 457, 512 x 8,192 x 8,192 32.3 and 31.0), and weights that come from memory for one row of
-// tiles take 0.47 a block.  In the thin kernel a block takes 0.45 (128 rows of A) or 0.3, the end of a tile 1 or 0.5, a
-// launch that adds the partial sums 2.5, and these go to L2 and back at 5 TB/s.
+// us in the wide kernel, 0.45 where there is more than one tile for an SM, 0.47 where the weights come from memory for one
+// row of tiles; the end of a tile 1.2.  In the thin kernel a block takes 0.45 (128 rows of A) or 0.3, the end of a tile 1 or
+// 0.5, a launch that adds the partial sums 2.5, and these go to L2 and back at 5 TB/s.
 // 128 x 32,768 x 4,096: thin 34.6 us, wide 26.8; 128 x 8,192 x 8,192: 20.6 (split) and 30.4; 200 x 16,384 x 4,096: 33 and
 // 17.3; 161 x 1,001 x 1,552: 7.6 (split) and 18.
 struct Estimate {
@@ -729,13 +702,10 @@ Cut cut_of(int M, int N, int K) {
   auto tiles = [&](int m, int n) { return (int64_t)((M + m - 1) / m) * ((N + n - 1) / n); };
   const int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const Estimate thin = thin_time(std::max<int64_t>(1, tiles(rows, kTN)), kb, rows == 128 ? 0.45 : 0.3, rows == 128 ? 1. : 0.5, 4. * M * N);
-  auto wide = [&](int ctas, double block) {
-    const int64_t groups = tiles(ctas * kWM, kWN), at_once = kSms / ctas;
-    return (double)((groups + at_once - 1) / at_once) * (kb * block + 1.2);
-  };
-  const double two = wide(kMc, 0.42) + 1., one = wide(1, M <= kWM ? 0.47 : tiles(kWM, kWN) <= kSms ? 0.42 : 0.45);
-  if (M <= 64 || thin.us <= std::min(one, two)) return Cut{rows, kTN, 1, thin.n_split, true};
-  return Cut{kWM, kWN, one < two ? 1 : kMc, 1, false};
+  const int64_t wide_tiles = tiles(kWM, kWN);
+  const double wide = (double)((wide_tiles + kSms - 1) / kSms) * (kb * (M <= kWM ? 0.47 : wide_tiles <= kSms ? 0.42 : 0.45) + 1.2);
+  if (M <= 64 || thin.us <= wide) return Cut{rows, kTN, thin.n_split, true};
+  return Cut{kWM, kWN, 1, false};
 }
 int64_t partial_ld(int N) { return ((int64_t)N + 127) / 128 * 128; }
 
@@ -751,25 +721,11 @@ bool row_map(CUtensorMap* map, const uint8_t* p, int rows, int K, int box_rows) 
 }
 
 template <typename Kernel, typename... Rest>
-cudaError_t launch_matmul(Kernel kernel, size_t smem, int threads, int64_t items, int sms, int ctas, cudaStream_t s, const CUtensorMap& am,
+cudaError_t launch_matmul(Kernel kernel, size_t smem, int threads, int64_t items, int ctas, cudaStream_t s, const CUtensorMap& am,
                           const CUtensorMap& bm, const Rest&... rest) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(items, std::max(1, sms / ctas)) * ctas));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)ctas;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = ctas > 1 ? 2 : 1;
-  return counted(cudaLaunchKernelEx(&cfg, kernel, am, bm, rest..., status_word()));
+  return launch_step(kernel, dim3((unsigned)std::min<int64_t>(items, ctas)), dim3(threads), smem, s, am, bm, rest..., status_word());
 }
 cudaError_t launch_wide(int64_t items, int sms, const CUtensorMap& am, const CUtensorMap& bm, MatmulPlan p, cudaStream_t s) {
   cudaFuncAttributes at;
@@ -788,7 +744,7 @@ cudaError_t launch_wide(int64_t items, int sms, const CUtensorMap& am, const CUt
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  return launch_matmul(k_matmul_fp8_wide, sizeof(WideSmem) + 1024, kWThreads, items, sms, p.ctas, s, am, bm, cm, p);
+  return launch_matmul(k_matmul_fp8_wide, sizeof(WideSmem) + 1024, kWThreads, items, sms, s, am, bm, cm, p);
 }
 
 template <int kRows>
@@ -796,7 +752,7 @@ cudaError_t launch_thin(int64_t items, int sms, const CUtensorMap& am, const CUt
   const int ctas = items > sms ? kTCtas<kRows> : 1, stages = kTRingBytes / ctas / kTStageBytes<kRows>;
   static_assert(kTSmemBytes<kRows>(kTRingBytes / kTStageBytes<kRows>) <= 232448, "shared memory of a block");
   static_assert(kTCtas<kRows> * (kTSmemBytes<kRows>(kTRingBytes / kTCtas<kRows> / kTStageBytes<kRows>) + 1024) <= 233472, "shared memory of an SM");
-  return launch_matmul(k_matmul_fp8_thin<kRows>, kTSmemBytes<kRows>(stages), kTThreads<kRows>, items, ctas * sms, 1, s, am, bm, p, stages);
+  return launch_matmul(k_matmul_fp8_thin<kRows>, kTSmemBytes<kRows>(stages), kTThreads<kRows>, items, ctas * sms, s, am, bm, p, stages);
 }
 
 }  // namespace
@@ -829,7 +785,6 @@ cudaError_t launch_matmul_fp8(const uint8_t* a, const float* sa, const uint8_t* 
   MatmulPlan p = {};
   p.sa = sa; p.sb = sb; p.C = C; p.M = M; p.N = N; p.kb = (K + kBlock - 1) / kBlock; p.f32 = f32;
   p.n_split = cut.n_split;
-  p.ctas = cut.ctas;
   p.ld = partial_ld(N);
   p.partial = p.n_split > 1 ? static_cast<float*>(ws) : nullptr;
   p.m_tiles = (M + cut.m - 1) / cut.m;
@@ -839,8 +794,8 @@ cudaError_t launch_matmul_fp8(const uint8_t* a, const float* sa, const uint8_t* 
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   CUtensorMap am, bm;
-  if (!row_map(&am, a, M, K, cut.m) || !row_map(&bm, b, N, K, cut.n / cut.ctas)) return cudaErrorInvalidValue;
-  const int64_t items = (int64_t)((p.m_tiles + cut.ctas - 1) / cut.ctas) * p.n_tiles * p.n_split;
+  if (!row_map(&am, a, M, K, cut.m) || !row_map(&bm, b, N, K, cut.n)) return cudaErrorInvalidValue;
+  const int64_t items = (int64_t)p.m_tiles * p.n_tiles * p.n_split;
   if (items > INT_MAX) return cudaErrorInvalidConfiguration;
   if (!cut.thin) e = launch_wide(items, sms, am, bm, p, s);
   else if (cut.m == 16) e = launch_thin<16>(items, sms, am, bm, p, s);
