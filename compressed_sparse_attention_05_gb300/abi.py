@@ -22,6 +22,7 @@ CSA2_KV_MXFP4, CSA2_KV_FP8 = 0, 1
 MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+MATMUL_FP8_WORKSPACE_MAX = 9961472
 STATUS_BAD_PAGE, STATUS_BAD_INDEX, STATUS_BAD_COUNT = 1, 2, 4
 
 ERRORS = {1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED", 3: "CSA2_ERR_CUDA",
@@ -393,6 +394,7 @@ def csa2_pack_fp8_blocks(x, codes, scales, stream=None):
 
 
 def csa2_matmul_fp8_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes for this very shape (fewer rows can need more); MATMUL_FP8_WORKSPACE_MAX is enough for every shape."""
     return lib().csa2_matmul_fp8_workspace_size(M, N, K)
 
 

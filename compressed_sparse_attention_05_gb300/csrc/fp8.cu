@@ -774,6 +774,8 @@ cudaError_t launch_pack_fp8_blocks(const void* x, int dtype, int64_t stride, int
                      scales);
 }
 
+// Tiles times splits are at most kSms where K is split, and a tile's partial sums at most 128 x 128.
+static_assert((size_t)kSms * 128 * kTN * sizeof(float) == CSA2_MATMUL_FP8_WORKSPACE_MAX, "workspace of any product");
 size_t matmul_fp8_workspace_bytes(int M, int N, int K) {
   const int n = cut_of(M, N, K).n_split;
   return n > 1 ? (size_t)n * M * partial_ld(N) * sizeof(float) : 0;

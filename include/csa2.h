@@ -471,7 +471,12 @@ int csa2_pack_fp8_blocks(const void* x, int32_t dtype, int64_t row_stride, int64
  * csa2_pack_fp8_blocks writes them, Bw E4M3 [N][K] (weights, one row per output) with
  * b_scales fp32 [ceil(N/128)][ceil(K/128)], C [M][N] bf16 or fp32 (c_dtype).  K: a
  * multiple of 16; M and N any.  Needs csa2_matmul_fp8_workspace_size() bytes of
- * workspace (0: ws may be NULL), which calls that can overlap must not share. */
+ * workspace (0: ws may be NULL), which calls that can overlap must not share.  A size
+ * belongs to its very shape: fewer rows of A can need more of it (4,096 x 4,096 x 7,168
+ * needs none, 32 x 4,096 x 7,168 some), as K is split where there are few tiles.
+ * CSA2_MATMUL_FP8_WORKSPACE_MAX bytes are enough for every shape, so that a program
+ * with several can keep one workspace of that size. */
+#define CSA2_MATMUL_FP8_WORKSPACE_MAX 9961472
 size_t csa2_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K);
 int csa2_matmul_fp8(const uint8_t* A, const float* a_scales, const uint8_t* Bw, const float* b_scales,
                     int32_t M, int32_t N, int32_t K, void* C, int32_t c_dtype, void* ws, size_t ws_bytes,
