@@ -8,6 +8,7 @@ library is missing, loading raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 from typing import Optional
 
@@ -374,6 +375,18 @@ def _strided(t: torch.Tensor):
     return t.data_ptr(), strides
 
 
+def _expect(name: str, t: torch.Tensor, shape: tuple, *dtypes):
+    """A tensor of that shape (or flat, with as many values) and of one of the types."""
+    if t.dtype not in dtypes or (t.shape != shape and t.shape != (math.prod(shape),)):
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)} {list(shape)}, not {t.dtype} {list(t.shape)}")
+
+
+def _expect_codes(name: str, t: torch.Tensor):
+    if t.element_size() != 1:
+        raise ValueError(f"{name} must hold one byte per value, not {t.dtype}")
+
+
+_TABLE_TYPES = (torch.int64, torch.uint64)
 _FLOAT_TYPES = {torch.float32: CSA2_F32, torch.bfloat16: CSA2_BF16}
 
 
@@ -389,6 +402,8 @@ def csa2_pack_fp8_blocks(x, codes, scales, stream=None):
     n, K = x.shape
     if codes.shape != x.shape:
         raise ValueError(f"x and codes must have the same shape (got {tuple(x.shape)} and {tuple(codes.shape)})")
+    _expect_codes("codes", codes)
+    _expect("scales", scales, (n, (K + 127) // 128), torch.float32)
     address, strides = _strided(x)
     _check(lib().csa2_pack_fp8_blocks(address, _float_type(x), strides[0], n, K, ptr(codes), ptr(scales), stream_handle(stream)))
 
@@ -403,20 +418,31 @@ def csa2_matmul_fp8(A, a_scales, Bw, b_scales, out, ws=None, stream=None):
     (M, K), N = A.shape, Bw.shape[0]
     if Bw.shape[1] != K or out.shape != (M, N):
         raise ValueError(f"A {tuple(A.shape)}, Bw {tuple(Bw.shape)} and out {tuple(out.shape)} do not fit together")
+    _expect_codes("A", A)
+    _expect_codes("Bw", Bw)
+    blocks = (K + 127) // 128
+    _expect("a_scales", a_scales, (M, blocks), torch.float32)
+    _expect("b_scales", b_scales, ((N + 127) // 128, blocks), torch.float32)
     _check(lib().csa2_matmul_fp8(ptr(A), ptr(a_scales), ptr(Bw), ptr(b_scales), M, N, K, ptr(out), _float_type(out), ptr(ws),
                                  _nbytes(ws), stream_handle(stream)))
 
 
 def csa2_rope_table(spec: RopeSpec, r: int, table, stream=None):
     """table: int64 [r/2], made once; csa2_rope reads it."""
+    if r >= 0 and r % 2 == 0:      # (the library refuses others)
+        _expect("table", table, (r // 2,), *_TABLE_TYPES)
     _check(lib().csa2_rope_table(C.byref(spec), r, ptr(table), stream_handle(stream)))
 
 
 def csa2_rope(x, y, positions, table, start=0, layout=ROPE_HALF, inverse=False, amplitude=1.0, stream=None):
-    """y = x [tokens][heads][d] rotated by the positions [tokens]; table of r/2 pairs; y may be x."""
+    """y = x [tokens][heads][d] rotated by the positions (int32, one per token); table of r/2 pairs; y may be x."""
     n, heads, d = x.shape
     if y.shape != x.shape:
         raise ValueError(f"x and y must have the same shape (got {tuple(x.shape)} and {tuple(y.shape)})")
+    if positions.dtype != torch.int32 or positions.numel() != n:
+        raise ValueError(f"positions must be int32, one for each of the {n} tokens, not {positions.dtype} {list(positions.shape)}")
+    if table.dtype not in _TABLE_TYPES:
+        raise ValueError(f"table must be as csa2_rope_table wrote it, int64, not {table.dtype}")
     px, sx = _strided(x)
     py, sy = _strided(y)
     _check(lib().csa2_rope(px, _float_type(x), sx[0], sx[1], py, _float_type(y), sy[0], sy[1], n, heads, d, start,
