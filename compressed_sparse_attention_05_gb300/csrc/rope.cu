@@ -5,7 +5,9 @@
 // Angles: the table holds theta_i / 2 pi in 0.64 fixed point, p times that mod 2^64 is the angle's fraction of a
 // turn (as in pack.cu, so that queries and cached keys agree), and the fraction is cut to a quarter turn and its
 // rest in integers before it becomes fp32: the rest is below 1/8 of a turn, so its rounding is at most 2^-27
-// turns and sinpi / cospi of it lose nothing to a large argument.
+// turns and sinpi / cospi of it lose nothing to a large argument.  The table's words come from fp64 and are off by a few
+// 2^-53 of themselves, which p multiplies: an angle is known to p 2^-50 radians, 2^-19 at the last position, and the same
+// angle for queries and keys.
 //
 // Bound: bytes.  A block takes about 2,048 units of work of 16-byte loads (8 channels; two halves of 8) that lie behind
 // one another, over tokens and heads: its threads compute their tokens' sines and cosines into shared memory once for

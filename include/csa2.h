@@ -141,16 +141,19 @@
  *      rounded to fp32.  The last block of a row may be shorter.  A block with an
  *      infinity dequantises to NaN, a NaN stays one by itself.
  *   R19 product (csa2_matmul_fp8): C[m][n] = sum over blocks kb of
- *      a_scales[m][kb] * b_scales[n/128][kb] * (sum of the block's code products);
- *      every block's sum and the sum over blocks are held in fp32, in an order
- *      that M, N and K fix; C is rounded once.
+ *      (a_scales[m][kb] * b_scales[n/128][kb]) * (sum of the block's code products);
+ *      the product of the scales (so it has to be a normal fp32 value, or 0), every
+ *      block's sum and the sum over blocks are held in fp32, in an order that M, N
+ *      and K fix; C is rounded once.
  *   R20 rotary positions (csa2_rope): pair i of the r rotated channels turns by
  *      p * theta_i, theta_i = base^(-2i/r) as in R3; scaled for long contexts:
  *      LINEAR theta_i / factor; NTK base * factor^(r/(r-2)) in the place of base;
  *      YARN theta_i (1 - g_i) + theta_i / factor * g_i with g_i = clamp((i - lo) /
  *      max(hi - lo, 0.001), 0, 1), lo = max(0, floor(c(beta_fast))), hi =
  *      min(r - 1, ceil(c(beta_slow))), c(n) = r ln(original_len / (2 pi n)) /
- *      (2 ln base).  HALF pairs channels (i, i + r/2), INTERLEAVED (2i, 2i + 1).
+ *      (2 ln base).  HALF pairs channels (i, i + r/2), INTERLEAVED (2i, 2i + 1).  The
+ *      frequencies are fp64: the angle at position p is known to p 2^-50 radians
+ *      (below fp32's own rounding up to p = 2^26).
  *   R21 drafted trees: node i of a sequence continues node parent[i] < i, or the
  *      committed text (-1); -2 marks a place without a node.  It stands at raw
  *      position ctx_len + depth.  csa2_tree_attn is R11 with the window rows of
