@@ -91,8 +91,10 @@
  *      the scale times 2^-f (f = floor(log2 scale), clamped to [-100, 100]),
  *      its logits and softmax weights corrected by the same power.  MXFP4
  *      values (<= 2688 in magnitude, >= 2^-10) need none.  Logits must stay
- *      finite in fp32.  A NaN in a head of Q or in a key that the token sees makes
- *      O and lse NaN there, and nowhere else.
+ *      finite in fp32.  Softmax weights are rounded to fp16 for the product with
+ *      the values (2^-11 of each at most, and 2^-25 of the largest below its normal
+ *      range); their sum takes them unrounded.  A NaN in a head of Q or in a key that
+ *      the token sees makes O and lse NaN there, and nowhere else.
  *   R12 the indexer key of a new entry (Full layer with compression) is
  *      W_idx * [h_4j; ..; h_4j+3], rounded to the indexer dtype.
  *   R13 SWA Bounded Replay (csa2_swa_replay): a rebuilt window row is the
