@@ -157,7 +157,7 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
     n_sel = n_sel < 0 ? 0 : a.K;
   }
   const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
-  // (neither the first position of a window of no rows nor the buffer's last row need be a position)
+  // (the buffer's last row may lie behind the last position)
   const int first = max(0, t - max(a.W - 1, 0));
   int w_lo = max(first, pos0);
   int w_hi = (int)min((int64_t)t, (int64_t)pos0 + a.swa_cap - 1);
@@ -360,7 +360,7 @@ k_sparse_attn(AttnArgs a, uint32_t* status) {
   }
   if (a.lse && tid < kHG && hg * kHG + tid < a.Hq) {
     const float l = sm.l[tid];
-    a.lse[row * a.Hq + hg * kHG + tid] = l > 0.f ? (sm.m[tid] + log2f(l)) * 0.6931471805599453f : lse_of_nothing(l);
+    a.lse[row * a.Hq + hg * kHG + tid] = (sm.m[tid] + log2f(l)) * 0.6931471805599453f;   // (no key: -inf twice)
   }
 }
 

@@ -385,7 +385,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   // ---- before the previous kernel of the step is done: the token's own inputs
   // (scalars, Q rows), barriers, tensor memory and the Q operand (a tree's positions come from its plan, which lets
   // nothing start before it is done)
-  const int t = max(a.q_pos[row], -1);   // (before the first position, or no node of a tree: -1, which sees nothing)
+  const int t = kTree ? max(a.q_pos[row], -1) : a.q_pos[row];   // (-1: no node of the tree)
   int n_sel = kTree ? a.cnt[row] : 0;
   const int n_ent = a.n_entries[b];
   const int pos0 = a.swa_cap > 0 ? a.swa_pos0[b] : 0;
@@ -412,10 +412,10 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     sm.qexp[tid] = 0;
   }
   // the window rows of the token: raw positions max(0, t-W+1, pos0) .. min(t, last row held)
-  // (neither the first position of a window of no rows nor the buffer's last row need be a position)
-  const int first = max(0, t - max(a.W - 1, 0));
+  // (t may lie before the first position, and the buffer's last row behind the last)
+  const int first = max(0, max(t, 0) - max(a.W - 1, 0));
   int w_lo = max(first, pos0);
-  int w_hi = (int)min((int64_t)t, (int64_t)pos0 + a.swa_cap - 1);
+  int w_hi = pos0 <= t && (uint32_t)t - (uint32_t)pos0 >= (uint32_t)a.swa_cap ? pos0 + a.swa_cap - 1 : t;
   int ctx = 0;
   if (kTree) {   // from the first position that the buffer holds (or the first ancestor) to the token itself
     ctx = max(0, a.ctx_len[b]);
@@ -733,7 +733,11 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
   __syncthreads();
   const bool ok = *abort == 0;
   const bool have_o = ok && n_my > 0;
-  if (tid < kHeads) sm.l_run[tid] = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
+  if (tid < kHeads) {
+    const float l = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
+    sm.l_run[tid] = l;
+    if (n_split > 1 && l != l) sm.m_ref[tid] = 0.f;   // (-inf where all logits were NaN: the merge would leave the rank out)
+  }
   __syncthreads();
   const int mt = (warp >> 2) & 3;   // epilogue (workers): warp takes M-tile mt, dims 128*mt + 32*q4 + lane
 
@@ -741,7 +745,7 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
     if (tid < kHeads) sm.fac[tid] = sm.l_run[tid] > 0.f ? 1.f / sm.l_run[tid] : 0.f;
     if (a.lse && tid < kHeads && hb + tid < a.Hq) {
       const float l = sm.l_run[tid];
-      a.lse[row * a.Hq + hb + tid] = l > 0.f ? (sm.m_ref[tid] + log2f(l)) * 0.6931471805599453f : lse_of_nothing(l);
+      a.lse[row * a.Hq + hb + tid] = (sm.m_ref[tid] + log2f(l)) * 0.6931471805599453f;   // (no key: -inf twice)
     }
     __syncthreads();
     if (!mma_warp) {
@@ -819,12 +823,11 @@ k_sparse_attn_tc(AttnArgs a, uint32_t* status, int n_split) {
 #pragma unroll
       for (int q = 0; q < kMaxSplit; ++q)
         if (mq[q] != -INFINITY) L += lq[q] * ex2(mq[q] - M);
-        else L += lq[q];   // (0, or NaN where NaN is all that the rank's keys gave)
 #pragma unroll
       for (int q = 0; q < kMaxSplit; ++q)
         if (q < n_split) facq[q * kHeads + tid] = (mq[q] == -INFINITY || L <= 0.f) ? 0.f : ex2(mq[q] - M) / L;
       if (crank == 0 && a.lse && hb + tid < a.Hq)
-        a.lse[row * a.Hq + hb + tid] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : lse_of_nothing(L);
+        a.lse[row * a.Hq + hb + tid] = (M + log2f(L)) * 0.6931471805599453f;
     }
     __syncthreads();
     for (int e0 = tid; e0 < n4; e0 += 2 * kThreads) {

@@ -75,8 +75,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// The lse of a sum of weights that is not above 0: -inf without a key, NaN where a logit was NaN.
-__device__ __forceinline__ float lse_of_nothing(float l) { return l != l ? l : -INFINITY; }
 
 // Reduction (max or sum) over the 32 lanes of each of 16 columns; lane L
 // ends with column L & 15.  v is consumed.
