@@ -7,10 +7,11 @@
 //
 // k_matmul_fp8_wide (many rows of A, or more rows of B than the SMs take 128 at a time): tiles of 128 rows of A x 256 rows
 //   of B.  A row of A is a lane of the accumulator, so a thread has one scale per block: sa[its row] sb[its 128 columns].
-//   4,096 x 32,768 x 4,096 takes 417 us (2.6 PFLOP/s) from a cool start and 450 to 460 (2.4) in a row, at the card's 1,400 W:
-//   the power cap holds the clock at 1.88 GHz, and operands of zeros take 405.  Below that: a block's MMAs run 513 cycles,
-//   and the way MMA -> sums (200 cycles after the last product) -> accumulator read (300) -> next MMAs (200) about as long
-//   again, with two accumulators (all of tensor memory) to hide it; the tensor pipe is active for 53% of the cycles.
+//   4,096 x 32,768 x 4,096 takes 440 us (2.5 PFLOP/s) at first and 458 to 466 (2.4) in a row, at the card's 1,400 W, which
+//   sets the clock (1.91 GHz, with zeros 1.96) but not the cycles: a block takes 963 of them, its MMAs 513 (the tensor pipe
+//   is active for 52%).  The sums and their hand-over set the pace: a warp waits 200 cycles for an accumulator, releases it 400 after that (four
+//   loads of 32 columns with their additions) and adds the rest, while the MMA warp waits 430 for a free one of the two (all
+//   of tensor memory); operands are always ahead (the copy warp waits 720 for a free stage).
 //   Tried: a pair of CTAs with one MMA for both (cta_group::2; its arrivals from SM to SM are too slow for this way:
 //   480 us), 16 sum warps (570, registers), halves of the accumulator on their own (478), named barriers in the place of
 //   shared-memory ones, loads and looks ahead in the sums (no difference).
@@ -263,8 +264,8 @@ constexpr int kWM = 128, kWN = 256, kWStages = 4, kWBufs = 2;
 constexpr int kWStageBytes = (kWM + kWN) * kBlock;       // 48 KB
 constexpr int kWSumWarps = 8;
 constexpr int kWThreads = kWSumWarps * 32 + 128;
-// Registers: 2 x 216 + 72 = 3 x 168.  (Where a split makes the compiler spill in one role's loop, the kernel takes up
-// to twice as long; this one does not.)
+// Registers: 2 x 216 + 72 = 3 x 168, without spills.  (Splits that make the compiler spill in one role's loop take up to
+// twice as long.)
 constexpr int kWRegs = 168;
 constexpr int kWRegsSum = 216, kWRegsMisc = 72;
 struct WideSmem {

@@ -12,8 +12,9 @@
 // Bound: bytes.  A block takes about 2,048 units of work of 16-byte loads (8 channels; two halves of 8) that lie behind
 // one another, over tokens and heads: its threads compute their tokens' sines and cosines into shared memory once for
 // all heads, then rotate and copy with 2 or 4 units' loads in flight each.  4,096 tokens x 64 heads x 512 channels, 64
-// rotated, bf16: 79 us, 6.8 TB/s (whole heads a block: 90; four blocks an SM: 85).  With one head there is nothing to
-// share a rotation with: 109,307 x 512 takes 42 us (5.3 TB/s), 338,137 x 64 with 32 rotated 32.5 (2.7; half pairs 44).
+// rotated, bf16: 79 us, 6.8 TB/s (whole heads a block: 90; four blocks an SM: 85).  With one head, whose
+// rotations serve no other, nothing lies under a block's start (positions, sines, barrier): 109,307 x 512 takes 42 us (5.3
+// TB/s), 338,137 x 64 with 32 rotated 32.5 (2.7; half pairs 44).
 // Half pairs that 8 channels do not divide, odd starts and unaligned rows go pair by pair (445 x 40 x 512, 62 rotated,
 // half: 11 us, at 3.3 TB/s).
 #include <algorithm>
